@@ -30,6 +30,7 @@ constexpr uint32_t kChkGStore = 1u << 4;         // a store of G outside [T, ld_
 constexpr uint32_t kChkOutBox = 1u << 5;         // a product's output box outside C
 constexpr uint32_t kChkSplitIndex = 1u << 6;     // a split-sum read or write outside its buffer
 constexpr uint32_t kChkCopyIndex = 1u << 7;      // a padding / row-copy access outside its buffer
+constexpr uint32_t kChkPlan = 1u << 8;           // an optimizer plan's tensor index outside the plan
 
 // One check word per translation unit (each .cu file is its own module).
 static __device__ uint32_t g_check_word;

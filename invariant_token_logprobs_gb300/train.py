@@ -1,0 +1,540 @@
+"""The operators of a training step on either side of the log-probabilities:
+ctypes binding of the entry points declared in include/lp_train.h.
+
+    out  = residual_norm(residual, branch, weight=..., branch_weight=..., gate=...)
+    grad = residual_norm_backward(grad_normed, grad_residual, out.residual, out.rstd, ...)
+    loss = policy_loss(logp, old_logp, advantages, mask=..., cu_seqlens=..., ...)
+    optimizer = AdamW(params, grads, copies=..., state_bits=8); optimizer.step(max_norm=1.0)
+
+Argument marshalling only, as in lp.py: every step of the computation runs in
+liblp's kernels on the current stream, and there is no fallback.  A call given
+another stream runs there, its outputs and workspace are allocated for that
+stream, and ordering it after the work that made its inputs is the caller's.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import os
+import re
+from typing import NamedTuple, Optional, Sequence, Union
+
+import torch
+
+from . import lp
+from .lp import LpError  # noqa: F401  (raised by every call here)
+
+__all__ = [
+    "ResidualNorm",
+    "ResidualNormGrad",
+    "PolicyLoss",
+    "AdamW",
+    "ADAMW_ALIGN",
+    "ADAMW_BLOCK",
+    "declared_symbols",
+    "load",
+    "residual_norm",
+    "residual_norm_backward",
+    "residual_norm_backward_workspace_size",
+    "policy_loss",
+    "policy_loss_workspace_size",
+]
+
+HEADER = os.path.join(os.path.dirname(lp.HEADER), "lp_train.h")
+
+FLOAT32, BFLOAT16 = 0, 1
+REDUCE_TOKEN, REDUCE_SEQUENCE = 0, 1
+ADAMW_ALIGN = 2048  # LP_ADAMW_ALIGN
+ADAMW_BLOCK = 256   # LP_ADAMW_BLOCK
+
+_i64 = ctypes.c_int64
+_int = ctypes.c_int
+_vp = ctypes.c_void_p
+_sz = ctypes.c_size_t
+_f32 = ctypes.c_float
+_f64 = ctypes.c_double
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", _vp), ("copy", _vp), ("grad", _vp), ("n", _i64), ("lr_scale", _f32),
+                ("weight_decay", _f32), ("grad_dtype", _int), ("reserved", _int)]
+
+
+_tensors = ctypes.POINTER(_AdamwTensor)
+
+_SIGNATURES = {
+    "lp_residual_norm": (
+        _int, [_vp, _i64, _int, _vp, _i64, _vp, _i64, _int, _vp, _vp, _int, _i64, _i64, _f32, _f32,
+               _f32, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "lp_residual_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "lp_residual_norm_backward": (
+        _int, [_vp, _i64, _int, _vp, _i64, _vp, _i64, _int, _vp, _vp, _int, _i64, _i64, _f32, _f32,
+               _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz,
+               _vp]),
+    "lp_policy_loss_workspace_size": (_sz, [_i64, _i64]),
+    "lp_policy_loss": (
+        _int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _int, _f64, _f64, _f64, _f64,
+               _vp, _vp, _vp, _vp, _sz, _vp]),
+    "lp_adamw_state_elements": (_i64, [_tensors, _i64]),
+    "lp_adamw_plan_size": (_sz, [_tensors, _i64]),
+    "lp_adamw_plan": (_int, [_tensors, _i64, _vp, _sz]),
+    "lp_adamw_grad_norm_workspace_size": (_sz, [_i64]),
+    "lp_adamw_grad_norm": (_int, [_vp, _i64, _i64, _f32, _vp, _vp, _sz, _vp]),
+    "lp_adamw_step": (
+        _int, [_vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _f64, _f64, _f64, _f64, _i64,
+               ctypes.c_uint64, _vp, _vp]),
+    "lp_adamw_state_values": (_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+}
+
+_lib: Optional[ctypes.CDLL] = None
+
+
+def declared_symbols() -> list[str]:
+    """Names of the entry points include/lp_train.h declares."""
+    with open(HEADER) as f:
+        text = f.read()
+    return re.findall(r"^LP_API\s+[\w\s\*]+?\b(lp_\w+)\s*\(", text, flags=re.M)
+
+
+def load() -> ctypes.CDLL:
+    """lp.load() with the signatures of this module's entry points."""
+    global _lib
+    lib = lp.load()
+    if _lib is not lib:
+        for name, (res, args) in _SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = lib
+    return lib
+
+
+def _dtype_code(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return BFLOAT16
+    if t.dtype == torch.float32:
+        return FLOAT32
+    raise TypeError(f"{what} must be float32 or bfloat16")
+
+
+def _on_device(*tensors: Optional[torch.Tensor]) -> None:
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError("expected tensors of one device")
+
+
+def _ld(t: Optional[torch.Tensor], shape, what: str) -> int:
+    """Row stride of a 2-D operand of `shape`; a single row may have any stride."""
+    if t is None:
+        return 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have the shape {tuple(shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t: Optional[torch.Tensor], n: int, what: str, dtype=torch.float32) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {str(dtype)[6:]}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {n}")
+
+
+def _same_dtype(t: Optional[torch.Tensor], dtype, what: str) -> None:
+    if t is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {str(dtype)[6:]}")
+
+
+@contextlib.contextmanager
+def _other_stream(stream):
+    handle = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(handle):
+        yield
+
+
+def _within(stream):
+    """Allocations inside belong to `stream` (the current one for None)."""
+    return contextlib.nullcontext() if stream is None else _other_stream(stream)
+
+
+# ---------------------------------------------------------------- residual norm
+
+class ResidualNorm(NamedTuple):
+    normed: Optional[torch.Tensor]       # [T, d], the branch's dtype; None without weight
+    residual: torch.Tensor               # [T, d], the new residual stream
+    rstd: Optional[torch.Tensor]         # [T] float32; None without weight
+    branch_rstd: Optional[torch.Tensor]  # [T] float32; None without branch_weight
+
+
+class ResidualNormGrad(NamedTuple):
+    residual: torch.Tensor
+    branch: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]         # [d] float32
+    branch_weight: Optional[torch.Tensor]  # [d] float32
+    gate: Optional[torch.Tensor]           # [T, d] in the gate's dtype, or [d] float32
+
+
+class _Operands(NamedTuple):
+    T: int
+    d: int
+    residual_dtype: int
+    act_dtype: int
+    weight_dtype: int
+    ld_branch: int
+    ld_gate: int
+
+
+def _norm_operands(residual, branch, gate, branch_weight, weight, act) -> _Operands:
+    """Checks what forward and backward share; `act` has the activations' dtype."""
+    if residual.dim() != 2:
+        raise ValueError("expected a 2-D residual")
+    T, d = residual.shape
+    act_dtype = _dtype_code(act, "activations")
+    _same_dtype(gate, act.dtype, "gate")
+    if gate is not None and gate.dim() == 1:
+        if tuple(gate.shape) != (d,) or not gate.is_contiguous():
+            raise ValueError(f"gate must be a contiguous row of {d} or have the residual's shape")
+        ld_gate = 0
+    else:
+        ld_gate = _ld(gate, (T, d), "gate")
+        if gate is not None and ld_gate < d:
+            raise ValueError("gate rows overlap: pass one row [d] for all")
+    weight_dtype = FLOAT32
+    for w, what in ((weight, "weight"), (branch_weight, "branch_weight")):
+        if w is not None:
+            weight_dtype = _dtype_code(w, what)
+            _vector(w, d, what, w.dtype)
+    if weight is not None and branch_weight is not None and weight.dtype != branch_weight.dtype:
+        raise TypeError("weight and branch_weight must have one dtype")
+    return _Operands(T, d, _dtype_code(residual, "residual"), act_dtype, weight_dtype,
+                     _ld(branch, (T, d), "branch"), ld_gate)
+
+
+def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None, *,
+                  weight: Optional[torch.Tensor] = None,
+                  branch_weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                  branch_scale: float = 1.0, eps: float = 1e-6, in_place: bool = False,
+                  stream=None) -> ResidualNorm:
+    """The residual stream r' = residual_scale * residual + branch_scale * gate * n and its
+    norm h = rms_norm(r') * weight, where n = rms_norm(branch) * branch_weight (branch itself
+    without branch_weight).
+
+    residual [T, d] and branch [T, d] are float32 or bfloat16 each; gate has the branch's dtype
+    and is [T, d] or one row [d]; the weights [d] share a dtype; h comes in the branch's dtype
+    (the residual's without branch).  Without branch the residual is normed as it stands.
+    in_place=True writes r' over the residual."""
+    act = branch if branch is not None else residual
+    _on_device(residual, branch, gate, branch_weight, weight)
+    o = _norm_operands(residual, branch, gate, branch_weight, weight, act)
+    fn = load().lp_residual_norm
+    with _within(stream):
+        new = residual
+        if branch is not None and not in_place:
+            new = torch.empty((o.T, o.d), dtype=residual.dtype, device=residual.device)
+        normed = rstd = branch_rstd = None
+        if weight is not None:
+            normed = torch.empty((o.T, o.d), dtype=act.dtype, device=residual.device)
+            rstd = torch.empty(o.T, dtype=torch.float32, device=residual.device)
+        if branch_weight is not None:
+            branch_rstd = torch.empty(o.T, dtype=torch.float32, device=residual.device)
+        lp._check("lp_residual_norm", fn(
+            lp._ptr(residual), _ld(residual, (o.T, o.d), "residual"), o.residual_dtype,
+            lp._ptr(branch), o.ld_branch, lp._ptr(gate), o.ld_gate, o.act_dtype,
+            lp._ptr(branch_weight), lp._ptr(weight), o.weight_dtype, o.T, o.d, residual_scale,
+            branch_scale, eps, lp._ptr(new) if branch is not None else None,
+            _ld(new, (o.T, o.d), "residual"), lp._ptr(normed), o.d, lp._ptr(branch_rstd),
+            lp._ptr(rstd), lp._stream(stream)))
+    return ResidualNorm(normed, new, rstd, branch_rstd)
+
+
+def residual_norm_backward_workspace_size(T: int, d: int) -> int:
+    return int(load().lp_residual_norm_backward_workspace_size(T, d))
+
+
+def residual_norm_backward(grad_normed: Optional[torch.Tensor],
+                           grad_residual: Optional[torch.Tensor], residual: torch.Tensor,
+                           rstd: Optional[torch.Tensor], *,
+                           branch: Optional[torch.Tensor] = None,
+                           weight: Optional[torch.Tensor] = None,
+                           branch_weight: Optional[torch.Tensor] = None,
+                           branch_rstd: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                           branch_scale: float = 1.0, weight_grads: bool = True,
+                           workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> ResidualNormGrad:
+    """The gradients of residual_norm: grad_normed and grad_residual are those of its normed and
+    residual outputs (grad_residual may be None when there is a weight; grad_normed is None
+    without weight), residual, rstd and branch_rstd its outputs, the rest its inputs.
+    weight_grads=False leaves out the gradients that are sums over the rows (weight,
+    branch_weight and a one-row gate)."""
+    act = branch if branch is not None else residual
+    _on_device(residual, grad_normed, grad_residual, branch, gate, branch_weight, weight, rstd,
+               branch_rstd, workspace)
+    o = _norm_operands(residual, branch, gate, branch_weight, weight, act)
+    shape = (o.T, o.d)
+    _same_dtype(grad_normed, act.dtype, "grad_normed")
+    _same_dtype(grad_residual, residual.dtype, "grad_residual")
+    _vector(rstd, o.T, "rstd")
+    _vector(branch_rstd, o.T, "branch_rstd")
+    fn = load().lp_residual_norm_backward
+    device = residual.device
+    with _within(stream):
+        out = torch.empty(shape, dtype=residual.dtype, device=device)
+        grad_branch = torch.empty(shape, dtype=act.dtype, device=device) \
+            if branch is not None else None
+        grad_gate = grad_weight = grad_branch_weight = None
+        if gate is not None and o.ld_gate != 0:
+            grad_gate = torch.empty(shape, dtype=gate.dtype, device=device)
+        elif gate is not None and weight_grads:
+            grad_gate = torch.empty(o.d, dtype=torch.float32, device=device)
+        if weight is not None and weight_grads:
+            grad_weight = torch.empty(o.d, dtype=torch.float32, device=device)
+        if branch_weight is not None and weight_grads:
+            grad_branch_weight = torch.empty(o.d, dtype=torch.float32, device=device)
+        if workspace is None and weight_grads:
+            workspace = lp._workspace(residual_norm_backward_workspace_size(o.T, o.d), device)
+        lp._check("lp_residual_norm_backward", fn(
+            lp._ptr(residual) if weight is not None else None,
+            _ld(residual, shape, "residual"), o.residual_dtype, lp._ptr(branch), o.ld_branch,
+            lp._ptr(gate), o.ld_gate, o.act_dtype, lp._ptr(branch_weight), lp._ptr(weight),
+            o.weight_dtype, o.T, o.d, residual_scale, branch_scale, lp._ptr(branch_rstd),
+            lp._ptr(rstd), lp._ptr(grad_normed), _ld(grad_normed, shape, "grad_normed"),
+            lp._ptr(grad_residual), _ld(grad_residual, shape, "grad_residual"), lp._ptr(out), o.d,
+            lp._ptr(grad_branch), o.d, lp._ptr(grad_gate), o.d, lp._ptr(grad_branch_weight),
+            lp._ptr(grad_weight), lp._ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            lp._stream(stream)))
+    return ResidualNormGrad(out, grad_branch, grad_weight, grad_branch_weight, grad_gate)
+
+
+# ------------------------------------------------------------------ policy loss
+
+class PolicyLoss(NamedTuple):
+    stats: torch.Tensor                   # [5]: loss, policy, kl, entropy, clipped share
+    grad_logp: torch.Tensor               # [T]
+    grad_entropy: Optional[torch.Tensor]  # [T]; None without entropy
+
+
+def policy_loss_workspace_size(T: int, n_sequences: int) -> int:
+    return int(load().lp_policy_loss_workspace_size(T, n_sequences))
+
+
+def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
+                mask: Optional[torch.Tensor] = None, ref_logp: Optional[torch.Tensor] = None,
+                entropy: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                reduction: str = "token", per_sequence: bool = False, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_coef: float = 0.0, entropy_coef: float = 0.0,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> PolicyLoss:
+    """The clipped policy-gradient loss of T rows and its gradients with respect to logp and
+    entropy.
+
+    advantages are [T], or one for each sequence with per_sequence=True; mask [T] (bool or
+    uint8) says which rows count; cu_seqlens [n + 1] int64 are the sequences' row offsets, needed
+    for reduction="sequence" (the mean over sequences of their rows' means; "token" is the mean
+    over all counted rows) and for per_sequence.  ref_logp adds kl_coef times the estimate
+    exp(r) - r - 1 of the divergence from the reference, entropy subtracts entropy_coef times the
+    entropy."""
+    if logp.dim() != 1:
+        raise ValueError("expected a 1-D logp")
+    if reduction not in ("token", "sequence"):
+        raise ValueError("reduction must be 'token' or 'sequence'")
+    _on_device(logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens, workspace)
+    T = logp.shape[0]
+    for t, what in ((logp, "logp"), (old_logp, "old_logp"), (ref_logp, "ref_logp"),
+                    (entropy, "entropy")):
+        _vector(t, T, what)
+    n = 0
+    if reduction == "sequence" or per_sequence:
+        if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens [n + 1] is needed")
+        n = cu_seqlens.shape[0] - 1
+        _vector(cu_seqlens, n + 1, "cu_seqlens", torch.int64)
+    else:
+        cu_seqlens = None
+    _vector(advantages, n if per_sequence else T, "advantages")
+    if mask is not None:
+        _vector(mask, T, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool)
+    fn = load().lp_policy_loss
+    device = logp.device
+    with _within(stream):
+        stats = torch.empty(5, dtype=torch.float32, device=device)
+        grad_logp = torch.empty(T, dtype=torch.float32, device=device)
+        grad_entropy = torch.empty(T, dtype=torch.float32, device=device) \
+            if entropy is not None else None
+        if workspace is None:
+            workspace = lp._workspace(policy_loss_workspace_size(T, n), device)
+        lp._check("lp_policy_loss", fn(
+            lp._ptr(logp), lp._ptr(old_logp), lp._ptr(ref_logp), lp._ptr(entropy),
+            lp._ptr(advantages), int(per_sequence), lp._ptr(mask), lp._ptr(cu_seqlens), T, n,
+            REDUCE_SEQUENCE if reduction == "sequence" else REDUCE_TOKEN, clip_low, clip_high,
+            kl_coef, entropy_coef, lp._ptr(stats), lp._ptr(grad_logp), lp._ptr(grad_entropy),
+            lp._ptr(workspace), workspace.numel() * workspace.element_size(),
+            lp._stream(stream)))
+    return PolicyLoss(stats, grad_logp, grad_entropy)
+
+
+# ------------------------------------------------------------------------ AdamW
+
+def _per_tensor(value: Union[float, Sequence[float]], n: int, what: str) -> list[float]:
+    values = [float(value)] * n if isinstance(value, (int, float)) else [float(v) for v in value]
+    if len(values) != n:
+        raise ValueError(f"{what} must be a number or one for each tensor")
+    return values
+
+
+def _disjoint(tensors: Sequence[torch.Tensor]) -> bool:
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                   for t in tensors if t.numel() > 0)
+    return all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+
+
+class AdamW:
+    """AdamW with decoupled weight decay over a list of tensors, one launch a step.
+
+    params are contiguous float32 tensors of any shapes, updated in place; grads their
+    gradients (float32 or bfloat16), read at every step from the same memory, such as the main
+    gradients that lp.linear_logprob_backward(accumulate_into=...) adds to; copies, where given,
+    bfloat16 tensors (or None) that receive the updated params.  weight_decay and lr_scale are
+    numbers or one for each tensor.
+
+    state_bits=8 holds both moments in a byte an element and one scale for 256 elements, rounded
+    without bias under `seed`; 32 holds them in float32.  `state`, as state_dict() gives it,
+    continues from it with its buffers.  set_grads() names other gradient tensors."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], *,
+                 copies: Optional[Sequence[Optional[torch.Tensor]]] = None, lr: float = 1e-3,
+                 betas: tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: Union[float, Sequence[float]] = 0.01,
+                 lr_scale: Union[float, Sequence[float]] = 1.0, state_bits: int = 32,
+                 seed: int = 0, state: Optional[dict] = None):
+        self.params = list(params)
+        n = len(self.params)
+        if n == 0:
+            raise ValueError("no tensors")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(self.copies) != n:
+            raise ValueError("copies must have one tensor or None for each param")
+        self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
+        self.weight_decay = _per_tensor(weight_decay, n, "weight_decay")
+        self.lr_scale = _per_tensor(lr_scale, n, "lr_scale")
+        self.state_bits, self.seed = state_bits, int(seed) & (2**64 - 1)
+        for p, c in zip(self.params, self.copies):
+            if p.dtype != torch.float32 or not p.is_contiguous():
+                raise TypeError("params must be contiguous float32 tensors")
+            if c is not None and (c.dtype != torch.bfloat16 or c.shape != p.shape or
+                                  not c.is_contiguous()):
+                raise TypeError("copies must be contiguous bfloat16 tensors of the params' shapes")
+        self.set_grads(grads)
+        self._allocate(state)
+
+    def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
+        """Lays the plan of the step out for these gradient tensors."""
+        self.grads = list(grads)
+        if len(self.grads) != len(self.params):
+            raise ValueError("grads must have one tensor for each param")
+        written = self.params + [c for c in self.copies if c is not None]
+        _on_device(*written, *self.grads)
+        for p, g in zip(self.params, self.grads):
+            _dtype_code(g, "gradients")
+            if g.shape != p.shape or not g.is_contiguous():
+                raise ValueError("gradients must be contiguous and of the params' shapes")
+        if not _disjoint(written):
+            raise ValueError("params and copies must not share memory")
+        lib = load()
+        n = len(self.params)
+        records = (_AdamwTensor * n)(*[
+            _AdamwTensor(p.data_ptr(), lp._ptr(c), g.data_ptr(), p.numel(), s, w,
+                         _dtype_code(g, "gradients"), 0)
+            for p, c, g, s, w in zip(self.params, self.copies, self.grads, self.lr_scale,
+                                     self.weight_decay)])
+        self.state_elements = int(lib.lp_adamw_state_elements(records, n))
+        size = int(lib.lp_adamw_plan_size(records, n))
+        host = torch.empty(max(size, 1), dtype=torch.uint8)
+        lp._check("lp_adamw_plan", lib.lp_adamw_plan(records, n, host.data_ptr(), size))
+        self._plan = host.to(self.params[0].device)
+
+    def _allocate(self, state: Optional[dict]) -> None:
+        n, device = self.state_elements, self.params[0].device
+        small = self.state_bits == 8
+        kind = torch.uint8 if small else torch.float32
+        self.step_count = 0 if state is None else int(state["step"])
+        wanted = {"exp_avg": (n, kind), "exp_avg_sq": (n, kind)}
+        if small:
+            wanted["exp_avg_scale"] = wanted["exp_avg_sq_scale"] = (n // ADAMW_BLOCK, torch.float32)
+        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        for name, (count, dtype) in wanted.items():
+            if state is None:
+                t = torch.zeros(count, dtype=dtype, device=device)
+            else:
+                t = state[name]
+                _vector(t, count, name, dtype)
+                _on_device(self.params[0], t)
+            setattr(self, name, t)
+
+    def state_dict(self) -> dict:
+        """The step count and the moments' buffers (not copied)."""
+        return {"step": self.step_count, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
+                "exp_avg_scale": self.exp_avg_scale, "exp_avg_sq_scale": self.exp_avg_sq_scale}
+
+    def step(self, lr: Optional[float] = None, max_norm: Optional[float] = None,
+             stream=None) -> Optional[torch.Tensor]:
+        """One step.  With max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))
+        of their global 2-norm, which is returned as a float32 scalar on the device; a norm that
+        is not finite leaves every param and moment as it was (the step is counted)."""
+        lib = load()
+        n = len(self.params)
+        with _within(stream):
+            s = lp._stream(stream)
+            norm = scale = None
+            if max_norm is not None:
+                norm = torch.empty(2, dtype=torch.float32, device=self._plan.device)
+                work = lp._workspace(
+                    int(lib.lp_adamw_grad_norm_workspace_size(self.state_elements)), norm.device)
+                lp._check("lp_adamw_grad_norm", lib.lp_adamw_grad_norm(
+                    self._plan.data_ptr(), n, self.state_elements, max_norm, norm.data_ptr(),
+                    work.data_ptr(), work.numel(), s))
+                scale = norm.data_ptr() + 4
+            lp._check("lp_adamw_step", lib.lp_adamw_step(
+                self._plan.data_ptr(), n, self.state_elements, self.state_bits,
+                self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), lp._ptr(self.exp_avg_scale),
+                lp._ptr(self.exp_avg_sq_scale), self.lr if lr is None else lr, self.betas[0],
+                self.betas[1], self.eps, self.step_count + 1, self.seed, scale, s))
+        self.step_count += 1
+        return None if norm is None else norm[0]
+
+    def state_values(self, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(first moment, second moment) as flat float32: the buffers themselves for 32-bit
+        moments, what the bytes stand for for 8-bit ones.  views() cuts them by tensor."""
+        if self.state_bits == 32:
+            return self.exp_avg, self.exp_avg_sq
+        with _within(stream):
+            m = torch.empty(self.state_elements, dtype=torch.float32, device=self.exp_avg.device)
+            v = torch.empty_like(m)
+            lp._check("lp_adamw_state_values", load().lp_adamw_state_values(
+                self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), self.exp_avg_scale.data_ptr(),
+                self.exp_avg_sq_scale.data_ptr(), self.state_elements, m.data_ptr(), v.data_ptr(),
+                lp._stream(stream)))
+        return m, v
+
+    def views(self, flat: torch.Tensor) -> list[torch.Tensor]:
+        """The part of a flat moment buffer that belongs to each param, in its shape."""
+        out, at = [], 0
+        for p in self.params:
+            out.append(flat[at:at + p.numel()].view(p.shape))
+            at += -(-p.numel() // ADAMW_ALIGN) * ADAMW_ALIGN
+        return out
