@@ -14,7 +14,6 @@ stream, and ordering it after the work that made its inputs is the caller's.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -23,7 +22,7 @@ from typing import NamedTuple, Optional, Sequence, Union
 import torch
 
 from . import lp
-from .lp import LpError  # noqa: F401  (raised by every call here)
+from .lp import LpError
 
 __all__ = [
     "ResidualNorm",
@@ -100,46 +99,48 @@ def declared_symbols() -> list[str]:
 def load() -> ctypes.CDLL:
     """lp.load() with the signatures of this module's entry points."""
     global _lib
-    lib = lp.load()
-    if _lib is not lib:
+    if _lib is None:
+        lib = lp.load()
         for name, (res, args) in _SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
         _lib = lib
-    return lib
+    return _lib
+
+
+_CODES = {torch.float32: FLOAT32, torch.bfloat16: BFLOAT16}
+_current_stream = torch._C._cuda_getCurrentRawStream  # what current_stream().cuda_stream is
 
 
 def _dtype_code(t: torch.Tensor, what: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return BFLOAT16
-    if t.dtype == torch.float32:
-        return FLOAT32
-    raise TypeError(f"{what} must be float32 or bfloat16")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    return code
 
 
-def _on_device(*tensors: Optional[torch.Tensor]) -> None:
-    device = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError("expected tensors of one device")
+def _device_of(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The index of the CUDA device that holds all of them."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("expected CUDA tensors of one device")
+    return index
 
 
 def _ld(t: Optional[torch.Tensor], shape, what: str) -> int:
     """Row stride of a 2-D operand of `shape`; a single row may have any stride."""
     if t is None:
         return 0
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have the shape {tuple(shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
         raise ValueError(f"{what} must have contiguous rows")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _vector(t: Optional[torch.Tensor], n: int, what: str, dtype=torch.float32) -> None:
@@ -147,7 +148,7 @@ def _vector(t: Optional[torch.Tensor], n: int, what: str, dtype=torch.float32) -
         return
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {str(dtype)[6:]}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n}")
 
 
@@ -156,17 +157,16 @@ def _same_dtype(t: Optional[torch.Tensor], dtype, what: str) -> None:
         raise TypeError(f"{what} must be {str(dtype)[6:]}")
 
 
-@contextlib.contextmanager
-def _other_stream(stream):
-    handle = stream if isinstance(stream, torch.cuda.Stream) else \
-        torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(handle):
-        yield
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _within(stream):
-    """Allocations inside belong to `stream` (the current one for None)."""
-    return contextlib.nullcontext() if stream is None else _other_stream(stream)
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` (a torch stream or a handle) as the current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 # ---------------------------------------------------------------- residual norm
@@ -186,40 +186,33 @@ class ResidualNormGrad(NamedTuple):
     gate: Optional[torch.Tensor]           # [T, d] in the gate's dtype, or [d] float32
 
 
-class _Operands(NamedTuple):
-    T: int
-    d: int
-    residual_dtype: int
-    act_dtype: int
-    weight_dtype: int
-    ld_branch: int
-    ld_gate: int
-
-
-def _norm_operands(residual, branch, gate, branch_weight, weight, act) -> _Operands:
-    """Checks what forward and backward share; `act` has the activations' dtype."""
-    if residual.dim() != 2:
+def _norm_operands(residual, branch, gate, branch_weight, weight, act):
+    """(residual_dtype, act_dtype, weight_dtype, ld_residual, ld_branch, ld_gate) of the operands
+    that forward and backward share, checked; `act` has the activations' dtype."""
+    shape = residual.shape
+    if len(shape) != 2:
         raise ValueError("expected a 2-D residual")
-    T, d = residual.shape
-    act_dtype = _dtype_code(act, "activations")
-    _same_dtype(gate, act.dtype, "gate")
-    if gate is not None and gate.dim() == 1:
-        if tuple(gate.shape) != (d,) or not gate.is_contiguous():
-            raise ValueError(f"gate must be a contiguous row of {d} or have the residual's shape")
-        ld_gate = 0
-    else:
-        ld_gate = _ld(gate, (T, d), "gate")
-        if gate is not None and ld_gate < d:
-            raise ValueError("gate rows overlap: pass one row [d] for all")
+    ld_gate = 0
+    if gate is not None:
+        if gate.dtype != act.dtype:
+            raise TypeError(f"gate must be {str(act.dtype)[6:]}")
+        if gate.dim() == 1:
+            _vector(gate, shape[1], "gate", act.dtype)
+        else:
+            ld_gate = _ld(gate, shape, "gate")
+            if ld_gate < shape[1]:
+                raise ValueError("gate rows overlap: pass one row [d] for all")
     weight_dtype = FLOAT32
-    for w, what in ((weight, "weight"), (branch_weight, "branch_weight")):
-        if w is not None:
-            weight_dtype = _dtype_code(w, what)
-            _vector(w, d, what, w.dtype)
-    if weight is not None and branch_weight is not None and weight.dtype != branch_weight.dtype:
-        raise TypeError("weight and branch_weight must have one dtype")
-    return _Operands(T, d, _dtype_code(residual, "residual"), act_dtype, weight_dtype,
-                     _ld(branch, (T, d), "branch"), ld_gate)
+    if weight is not None:
+        weight_dtype = _dtype_code(weight, "weight")
+        _vector(weight, shape[1], "weight", weight.dtype)
+    if branch_weight is not None:
+        weight_dtype = _dtype_code(branch_weight, "branch_weight")
+        _vector(branch_weight, shape[1], "branch_weight", branch_weight.dtype)
+        if weight is not None and weight.dtype != branch_weight.dtype:
+            raise TypeError("weight and branch_weight must have one dtype")
+    return (_dtype_code(residual, "residual"), _dtype_code(act, "activations"), weight_dtype,
+            _ld(residual, shape, "residual"), _ld(branch, shape, "branch"), ld_gate)
 
 
 def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None, *,
@@ -236,27 +229,34 @@ def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
     and is [T, d] or one row [d]; the weights [d] share a dtype; h comes in the branch's dtype
     (the residual's without branch).  Without branch the residual is normed as it stands.
     in_place=True writes r' over the residual."""
-    act = branch if branch is not None else residual
-    _on_device(residual, branch, gate, branch_weight, weight)
-    o = _norm_operands(residual, branch, gate, branch_weight, weight, act)
-    fn = load().lp_residual_norm
-    with _within(stream):
-        new = residual
-        if branch is not None and not in_place:
-            new = torch.empty((o.T, o.d), dtype=residual.dtype, device=residual.device)
-        normed = rstd = branch_rstd = None
-        if weight is not None:
-            normed = torch.empty((o.T, o.d), dtype=act.dtype, device=residual.device)
-            rstd = torch.empty(o.T, dtype=torch.float32, device=residual.device)
-        if branch_weight is not None:
-            branch_rstd = torch.empty(o.T, dtype=torch.float32, device=residual.device)
-        lp._check("lp_residual_norm", fn(
-            lp._ptr(residual), _ld(residual, (o.T, o.d), "residual"), o.residual_dtype,
-            lp._ptr(branch), o.ld_branch, lp._ptr(gate), o.ld_gate, o.act_dtype,
-            lp._ptr(branch_weight), lp._ptr(weight), o.weight_dtype, o.T, o.d, residual_scale,
-            branch_scale, eps, lp._ptr(new) if branch is not None else None,
-            _ld(new, (o.T, o.d), "residual"), lp._ptr(normed), o.d, lp._ptr(branch_rstd),
-            lp._ptr(rstd), lp._stream(stream)))
+    if stream is not None:
+        return _on_stream(stream, residual_norm, residual, branch, weight=weight,
+                          branch_weight=branch_weight, gate=gate, residual_scale=residual_scale,
+                          branch_scale=branch_scale, eps=eps, in_place=in_place)
+    act = residual if branch is None else branch
+    index = _device_of(residual, branch, gate, branch_weight, weight)
+    residual_dtype, act_dtype, weight_dtype, ld, ld_branch, ld_gate = _norm_operands(
+        residual, branch, gate, branch_weight, weight, act)
+    T, d = residual.shape
+    device = residual.device
+    new, out, ld_out = residual, None, ld
+    if branch is not None:
+        if not in_place:
+            new, ld_out = torch.empty((T, d), dtype=residual.dtype, device=device), d
+        out = new.data_ptr()
+    normed = rstd = branch_rstd = None
+    if weight is not None:
+        normed = torch.empty((T, d), dtype=act.dtype, device=device)
+        rstd = torch.empty(T, dtype=torch.float32, device=device)
+    if branch_weight is not None:
+        branch_rstd = torch.empty(T, dtype=torch.float32, device=device)
+    status = load().lp_residual_norm(
+        residual.data_ptr(), ld, residual_dtype, _ptr(branch), ld_branch, _ptr(gate), ld_gate,
+        act_dtype, _ptr(branch_weight), _ptr(weight), weight_dtype, T, d, residual_scale,
+        branch_scale, eps, out, ld_out, _ptr(normed), d, _ptr(branch_rstd), _ptr(rstd),
+        _current_stream(index))
+    if status != 0:
+        raise LpError("lp_residual_norm", status)
     return ResidualNorm(normed, new, rstd, branch_rstd)
 
 
@@ -280,43 +280,53 @@ def residual_norm_backward(grad_normed: Optional[torch.Tensor],
     without weight), residual, rstd and branch_rstd its outputs, the rest its inputs.
     weight_grads=False leaves out the gradients that are sums over the rows (weight,
     branch_weight and a one-row gate)."""
-    act = branch if branch is not None else residual
-    _on_device(residual, grad_normed, grad_residual, branch, gate, branch_weight, weight, rstd,
-               branch_rstd, workspace)
-    o = _norm_operands(residual, branch, gate, branch_weight, weight, act)
-    shape = (o.T, o.d)
+    if stream is not None:
+        return _on_stream(stream, residual_norm_backward, grad_normed, grad_residual, residual,
+                          rstd, branch=branch, weight=weight, branch_weight=branch_weight,
+                          branch_rstd=branch_rstd, gate=gate, residual_scale=residual_scale,
+                          branch_scale=branch_scale, weight_grads=weight_grads,
+                          workspace=workspace)
+    act = residual if branch is None else branch
+    index = _device_of(residual, grad_normed, grad_residual, branch, gate, branch_weight, weight,
+                       rstd, branch_rstd, workspace)
+    residual_dtype, act_dtype, weight_dtype, ld, ld_branch, ld_gate = _norm_operands(
+        residual, branch, gate, branch_weight, weight, act)
+    shape = residual.shape
+    T, d = shape
     _same_dtype(grad_normed, act.dtype, "grad_normed")
     _same_dtype(grad_residual, residual.dtype, "grad_residual")
-    _vector(rstd, o.T, "rstd")
-    _vector(branch_rstd, o.T, "branch_rstd")
-    fn = load().lp_residual_norm_backward
-    device = residual.device
-    with _within(stream):
-        out = torch.empty(shape, dtype=residual.dtype, device=device)
-        grad_branch = torch.empty(shape, dtype=act.dtype, device=device) \
-            if branch is not None else None
-        grad_gate = grad_weight = grad_branch_weight = None
-        if gate is not None and o.ld_gate != 0:
-            grad_gate = torch.empty(shape, dtype=gate.dtype, device=device)
-        elif gate is not None and weight_grads:
-            grad_gate = torch.empty(o.d, dtype=torch.float32, device=device)
-        if weight is not None and weight_grads:
-            grad_weight = torch.empty(o.d, dtype=torch.float32, device=device)
-        if branch_weight is not None and weight_grads:
-            grad_branch_weight = torch.empty(o.d, dtype=torch.float32, device=device)
-        if workspace is None and weight_grads:
-            workspace = lp._workspace(residual_norm_backward_workspace_size(o.T, o.d), device)
-        lp._check("lp_residual_norm_backward", fn(
-            lp._ptr(residual) if weight is not None else None,
-            _ld(residual, shape, "residual"), o.residual_dtype, lp._ptr(branch), o.ld_branch,
-            lp._ptr(gate), o.ld_gate, o.act_dtype, lp._ptr(branch_weight), lp._ptr(weight),
-            o.weight_dtype, o.T, o.d, residual_scale, branch_scale, lp._ptr(branch_rstd),
-            lp._ptr(rstd), lp._ptr(grad_normed), _ld(grad_normed, shape, "grad_normed"),
-            lp._ptr(grad_residual), _ld(grad_residual, shape, "grad_residual"), lp._ptr(out), o.d,
-            lp._ptr(grad_branch), o.d, lp._ptr(grad_gate), o.d, lp._ptr(grad_branch_weight),
-            lp._ptr(grad_weight), lp._ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            lp._stream(stream)))
+    _vector(rstd, T, "rstd")
+    _vector(branch_rstd, T, "branch_rstd")
+    lib, device = load(), residual.device
+    out = torch.empty((T, d), dtype=residual.dtype, device=device)
+    grad_branch = grad_gate = grad_weight = grad_branch_weight = None
+    if branch is not None:
+        grad_branch = torch.empty((T, d), dtype=act.dtype, device=device)
+    if gate is not None and ld_gate != 0:
+        grad_gate = torch.empty((T, d), dtype=gate.dtype, device=device)
+    size = 0
+    if weight_grads:
+        if gate is not None and ld_gate == 0:
+            grad_gate = torch.empty(d, dtype=torch.float32, device=device)
+        if weight is not None:
+            grad_weight = torch.empty(d, dtype=torch.float32, device=device)
+        if branch_weight is not None:
+            grad_branch_weight = torch.empty(d, dtype=torch.float32, device=device)
+        if workspace is None:
+            size = lib.lp_residual_norm_backward_workspace_size(T, d)
+            workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+        else:
+            size = workspace.numel() * workspace.element_size()
+    status = lib.lp_residual_norm_backward(
+        residual.data_ptr() if weight is not None else None, ld, residual_dtype, _ptr(branch),
+        ld_branch, _ptr(gate), ld_gate, act_dtype, _ptr(branch_weight), _ptr(weight), weight_dtype,
+        T, d, residual_scale, branch_scale, _ptr(branch_rstd), _ptr(rstd), _ptr(grad_normed),
+        _ld(grad_normed, shape, "grad_normed"), _ptr(grad_residual),
+        _ld(grad_residual, shape, "grad_residual"), out.data_ptr(), d, _ptr(grad_branch), d,
+        _ptr(grad_gate), d, _ptr(grad_branch_weight), _ptr(grad_weight), _ptr(workspace), size,
+        _current_stream(index))
+    if status != 0:
+        raise LpError("lp_residual_norm_backward", status)
     return ResidualNormGrad(out, grad_branch, grad_weight, grad_branch_weight, grad_gate)
 
 
@@ -347,17 +357,25 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     over all counted rows) and for per_sequence.  ref_logp adds kl_coef times the estimate
     exp(r) - r - 1 of the divergence from the reference, entropy subtracts entropy_coef times the
     entropy."""
+    if stream is not None:
+        return _on_stream(stream, policy_loss, logp, old_logp, advantages, mask=mask,
+                          ref_logp=ref_logp, entropy=entropy, cu_seqlens=cu_seqlens,
+                          reduction=reduction, per_sequence=per_sequence, clip_low=clip_low,
+                          clip_high=clip_high, kl_coef=kl_coef, entropy_coef=entropy_coef,
+                          workspace=workspace)
     if logp.dim() != 1:
         raise ValueError("expected a 1-D logp")
     if reduction not in ("token", "sequence"):
         raise ValueError("reduction must be 'token' or 'sequence'")
-    _on_device(logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens, workspace)
+    index = _device_of(logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens, workspace)
     T = logp.shape[0]
-    for t, what in ((logp, "logp"), (old_logp, "old_logp"), (ref_logp, "ref_logp"),
-                    (entropy, "entropy")):
-        _vector(t, T, what)
+    _vector(logp, T, "logp")
+    _vector(old_logp, T, "old_logp")
+    _vector(ref_logp, T, "ref_logp")
+    _vector(entropy, T, "entropy")
     n = 0
-    if reduction == "sequence" or per_sequence:
+    by_sequence = reduction == "sequence"
+    if by_sequence or per_sequence:
         if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens [n + 1] is needed")
         n = cu_seqlens.shape[0] - 1
@@ -367,22 +385,25 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     _vector(advantages, n if per_sequence else T, "advantages")
     if mask is not None:
         _vector(mask, T, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool)
-    fn = load().lp_policy_loss
-    device = logp.device
-    with _within(stream):
-        stats = torch.empty(5, dtype=torch.float32, device=device)
-        grad_logp = torch.empty(T, dtype=torch.float32, device=device)
-        grad_entropy = torch.empty(T, dtype=torch.float32, device=device) \
-            if entropy is not None else None
-        if workspace is None:
-            workspace = lp._workspace(policy_loss_workspace_size(T, n), device)
-        lp._check("lp_policy_loss", fn(
-            lp._ptr(logp), lp._ptr(old_logp), lp._ptr(ref_logp), lp._ptr(entropy),
-            lp._ptr(advantages), int(per_sequence), lp._ptr(mask), lp._ptr(cu_seqlens), T, n,
-            REDUCE_SEQUENCE if reduction == "sequence" else REDUCE_TOKEN, clip_low, clip_high,
-            kl_coef, entropy_coef, lp._ptr(stats), lp._ptr(grad_logp), lp._ptr(grad_entropy),
-            lp._ptr(workspace), workspace.numel() * workspace.element_size(),
-            lp._stream(stream)))
+    lib, device = load(), logp.device
+    stats = torch.empty(5, dtype=torch.float32, device=device)
+    grad_logp = torch.empty(T, dtype=torch.float32, device=device)
+    grad_entropy = None
+    if entropy is not None:
+        grad_entropy = torch.empty(T, dtype=torch.float32, device=device)
+    if workspace is None:
+        size = lib.lp_policy_loss_workspace_size(T, n)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    status = lib.lp_policy_loss(
+        logp.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp), _ptr(entropy), _ptr(advantages),
+        int(per_sequence), _ptr(mask), _ptr(cu_seqlens), T, n,
+        REDUCE_SEQUENCE if by_sequence else REDUCE_TOKEN, clip_low, clip_high, kl_coef,
+        entropy_coef, stats.data_ptr(), grad_logp.data_ptr(), _ptr(grad_entropy),
+        workspace.data_ptr(), size, _current_stream(index))
+    if status != 0:
+        raise LpError("lp_policy_loss", status)
     return PolicyLoss(stats, grad_logp, grad_entropy)
 
 
@@ -448,7 +469,7 @@ class AdamW:
         if len(self.grads) != len(self.params):
             raise ValueError("grads must have one tensor for each param")
         written = self.params + [c for c in self.copies if c is not None]
-        _on_device(*written, *self.grads)
+        self._index = _device_of(*written, *self.grads)
         for p, g in zip(self.params, self.grads):
             _dtype_code(g, "gradients")
             if g.shape != p.shape or not g.is_contiguous():
@@ -458,7 +479,7 @@ class AdamW:
         lib = load()
         n = len(self.params)
         records = (_AdamwTensor * n)(*[
-            _AdamwTensor(p.data_ptr(), lp._ptr(c), g.data_ptr(), p.numel(), s, w,
+            _AdamwTensor(p.data_ptr(), _ptr(c), g.data_ptr(), p.numel(), s, w,
                          _dtype_code(g, "gradients"), 0)
             for p, c, g, s, w in zip(self.params, self.copies, self.grads, self.lr_scale,
                                      self.weight_decay)])
@@ -483,7 +504,7 @@ class AdamW:
             else:
                 t = state[name]
                 _vector(t, count, name, dtype)
-                _on_device(self.params[0], t)
+                _device_of(self.params[0], t)
             setattr(self, name, t)
 
     def state_dict(self) -> dict:
@@ -496,24 +517,27 @@ class AdamW:
         """One step.  With max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))
         of their global 2-norm, which is returned as a float32 scalar on the device; a norm that
         is not finite leaves every param and moment as it was (the step is counted)."""
-        lib = load()
-        n = len(self.params)
-        with _within(stream):
-            s = lp._stream(stream)
-            norm = scale = None
-            if max_norm is not None:
-                norm = torch.empty(2, dtype=torch.float32, device=self._plan.device)
-                work = lp._workspace(
-                    int(lib.lp_adamw_grad_norm_workspace_size(self.state_elements)), norm.device)
-                lp._check("lp_adamw_grad_norm", lib.lp_adamw_grad_norm(
-                    self._plan.data_ptr(), n, self.state_elements, max_norm, norm.data_ptr(),
-                    work.data_ptr(), work.numel(), s))
-                scale = norm.data_ptr() + 4
-            lp._check("lp_adamw_step", lib.lp_adamw_step(
-                self._plan.data_ptr(), n, self.state_elements, self.state_bits,
-                self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), lp._ptr(self.exp_avg_scale),
-                lp._ptr(self.exp_avg_sq_scale), self.lr if lr is None else lr, self.betas[0],
-                self.betas[1], self.eps, self.step_count + 1, self.seed, scale, s))
+        if stream is not None:
+            return _on_stream(stream, self.step, lr, max_norm)
+        lib, plan, n = load(), self._plan.data_ptr(), len(self.params)
+        elements, current = self.state_elements, _current_stream(self._index)
+        norm = scale = None
+        if max_norm is not None:
+            norm = torch.empty(2, dtype=torch.float32, device=self._plan.device)
+            size = lib.lp_adamw_grad_norm_workspace_size(elements)
+            work = torch.empty(size, dtype=torch.uint8, device=self._plan.device)
+            status = lib.lp_adamw_grad_norm(plan, n, elements, max_norm, norm.data_ptr(),
+                                            work.data_ptr(), size, current)
+            if status != 0:
+                raise LpError("lp_adamw_grad_norm", status)
+            scale = norm.data_ptr() + 4
+        status = lib.lp_adamw_step(
+            plan, n, elements, self.state_bits, self.exp_avg.data_ptr(),
+            self.exp_avg_sq.data_ptr(), _ptr(self.exp_avg_scale), _ptr(self.exp_avg_sq_scale),
+            self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
+            self.step_count + 1, self.seed, scale, current)
+        if status != 0:
+            raise LpError("lp_adamw_step", status)
         self.step_count += 1
         return None if norm is None else norm[0]
 
@@ -522,13 +546,17 @@ class AdamW:
         moments, what the bytes stand for for 8-bit ones.  views() cuts them by tensor."""
         if self.state_bits == 32:
             return self.exp_avg, self.exp_avg_sq
-        with _within(stream):
-            m = torch.empty(self.state_elements, dtype=torch.float32, device=self.exp_avg.device)
-            v = torch.empty_like(m)
-            lp._check("lp_adamw_state_values", load().lp_adamw_state_values(
-                self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), self.exp_avg_scale.data_ptr(),
-                self.exp_avg_sq_scale.data_ptr(), self.state_elements, m.data_ptr(), v.data_ptr(),
-                lp._stream(stream)))
+        if stream is not None:
+            return _on_stream(stream, self.state_values)
+        n, device = self.state_elements, self.exp_avg.device
+        m = torch.empty(n, dtype=torch.float32, device=device)
+        v = torch.empty(n, dtype=torch.float32, device=device)
+        status = load().lp_adamw_state_values(
+            self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), self.exp_avg_scale.data_ptr(),
+            self.exp_avg_sq_scale.data_ptr(), n, m.data_ptr(), v.data_ptr(),
+            _current_stream(self._index))
+        if status != 0:
+            raise LpError("lp_adamw_state_values", status)
         return m, v
 
     def views(self, flat: torch.Tensor) -> list[torch.Tensor]:
