@@ -1,4 +1,13 @@
 // lp_policy.cu: the clipped policy-gradient loss and its gradients (include/lp_train.h).
+//
+// A row's weight needs the number of counted rows of its sequence, or of all, before any
+// gradient can be written, so the call has two passes: over the masks (a byte a row) and over
+// the rest.  Up to kSmallRows rows one CTA does both from registers in one launch; beyond
+// that they are two grids over chunks of rows, launched as programmatic dependents.
+//
+// Counts are integers added by atomics, whose order does not show.  The loss's sums are
+// taken in a fixed order: a thread's rows, the CTA's tree, then the CTAs' sums by whichever
+// CTA finishes last.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -9,122 +18,437 @@
 namespace lp {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kStats = 4;  // w policy, w kl, w entropy, the clipped rows' w
 
-// The sequence of row t: the number of sequences that end at or before it; B when
-// there is none, also for the rows before the first.
-__device__ __forceinline__ int64_t sequence_of(const int64_t* cu, int64_t B, int64_t t) {
-  if (t < cu[0]) return B;
-  int64_t lo = 0, hi = B;
+// ---- one CTA
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallRounds = 2;  // groups of 4 rows a thread
+constexpr int64_t kSmallRows = int64_t(kSmallThreads) * 4 * kSmallRounds;
+constexpr int64_t kSmallSequences = 2048;
+
+// ---- two grids
+constexpr int kThreads = 256;
+constexpr int kRounds = 4;                    // groups of 4 rows a thread
+constexpr int kChunk = kThreads * 4 * kRounds;  // rows of a CTA
+constexpr int kStaged = 512;                  // sequence offsets of a chunk held in shared memory
+
+struct Header {
+  unsigned counted;    // rows that count, in all
+  unsigned sequences;  // sequences with a row that counts
+  unsigned finished;   // CTAs of the second pass that have written their sums
+};
+constexpr size_t kHeaderBytes = 256;
+size_t counts_bytes(int64_t n_sequences) {
+  return static_cast<size_t>((n_sequences * 4 + 255) / 256 * 256);
+}
+
+// The first of n ascending offsets that is above t, in [0, n].
+template <class Int>
+__device__ __forceinline__ int64_t upper_bound(const Int* offsets, int64_t n, int64_t t) {
+  int64_t lo = 0, hi = n;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
-    if (cu[mid + 1] <= t)
+    if (offsets[mid] <= t)
       lo = mid + 1;
     else
       hi = mid;
   }
   return lo;
 }
-
-// One row's terms and gradients before the weight.
-struct RowTerms {
-  float policy, kl, entropy, clipped, grad;
-};
-__device__ __forceinline__ RowTerms row_terms(const PolicyArgs& a, int64_t t, float A) {
-  RowTerms r{0.f, 0.f, 0.f, 0.f, 0.f};
-  const float logp = a.logp[t];
-  const float delta = logp - a.old_logp[t];
-  const float ratio = expf(delta);
-  const bool over = A > 0.f && delta > a.high, under = A < 0.f && delta < a.low;
-  r.clipped = over || under ? 1.f : 0.f;
-  r.policy = -A * (over ? a.ratio_high : under ? a.ratio_low : ratio);
-  r.grad = over || under ? 0.f : -A * ratio;
-  if (a.ref_logp != nullptr) {
-    const float x = a.ref_logp[t] - logp;
-    const float up = expm1f(x);
-    r.kl = up - x;
-    r.grad -= a.kl_coef * up;
+// The same by a whole warp, 32 probes a step: for offsets in global memory.
+__device__ __forceinline__ int64_t warp_upper_bound(const int64_t* offsets, int64_t n, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = n;  // the answer is in [lo, hi]
+  while (lo < hi) {
+    const int64_t stride = (hi - lo + 31) / 32;
+    const int64_t at = lo + lane * stride;
+    const bool below = at < hi && offsets[at] <= t;
+    const int k = __popc(__ballot_sync(0xffffffffu, below));  // the probes below t come first
+    if (k == 0) return lo;
+    hi = min(hi, lo + k * stride);
+    lo += (k - 1) * stride + 1;
   }
-  if (a.entropy != nullptr) r.entropy = a.entropy[t];
-  return r;
+  return lo;
 }
 
-// One CTA: counts, then terms, then the sums in a fixed order.
-__global__ void __launch_bounds__(kThreads) lp_policy_kernel(PolicyArgs a) {
-  __shared__ unsigned total;
-  __shared__ float slots[kThreads][kStats];
-  unsigned* counts = static_cast<unsigned*>(a.workspace);
-  const int64_t B = a.n_sequences;
-  if (threadIdx.x == 0) total = 0;
-  if (a.by_sequence)
-    for (int64_t i = threadIdx.x; i < B; i += kThreads) counts[i] = 0;
-  __syncthreads();
-  for (int64_t t = threadIdx.x; t < a.T; t += kThreads) {
-    if (a.mask != nullptr && a.mask[t] == 0) continue;
-    const int64_t s = a.cu_seqlens != nullptr ? sequence_of(a.cu_seqlens, B, t) : 0;
-    if (a.cu_seqlens != nullptr && s == B) continue;
-    if (a.by_sequence)
-      atomicAdd(&counts[s], 1u);
-    else
-      atomicAdd(&total, 1u);
+// Four values of an operand; rows past T read as zero.
+__device__ __forceinline__ void load4(const float* p, int64_t t, int64_t T, bool wide,
+                                      float (&v)[4]) {
+  if (wide && t + 4 <= T) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p + t));
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    return;
   }
-  __threadfence_block();
-  __syncthreads();
-  if (a.by_sequence) {
-    unsigned some = 0;
-    for (int64_t i = threadIdx.x; i < B; i += kThreads) some += __ldcg(&counts[i]) > 0 ? 1u : 0u;
-    atomicAdd(&total, some);
-    __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = t + j < T ? p[t + j] : 0.f;
+}
+__device__ __forceinline__ void store4(float* p, int64_t t, int64_t T, bool wide,
+                                       const float (&v)[4]) {
+  if (wide && t + 4 <= T) {
+    *reinterpret_cast<float4*>(p + t) = make_float4(v[0], v[1], v[2], v[3]);
+    return;
   }
-  const float whole = static_cast<float>(max(total, 1u));
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (t + j < T) p[t + j] = v[j];
+}
+// Bit j: row t + j counts by the mask.
+__device__ __forceinline__ unsigned load_mask4(const uint8_t* mask, int64_t t, int64_t T, bool wide) {
+  const unsigned inside = t + 4 <= T ? 0xfu : t < T ? (1u << (T - t)) - 1u : 0u;
+  if (mask == nullptr) return inside;
+  unsigned kept = 0;
+  if (wide && inside == 0xfu) {
+    const uchar4 m = __ldg(reinterpret_cast<const uchar4*>(mask + t));
+    kept = (m.x ? 1u : 0u) | (m.y ? 2u : 0u) | (m.z ? 4u : 0u) | (m.w ? 8u : 0u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (inside >> j & 1u) kept |= mask[t + j] != 0 ? 1u << j : 0u;
+  }
+  return kept;
+}
+
+// Four rows in registers.
+struct Four {
+  float logp[4], old[4], ref[4], entropy[4], advantage[4];
+};
+__device__ __forceinline__ void load_rows(const PolicyArgs& a, int64_t t, Four& f) {
+  load4(a.logp, t, a.T, a.wide, f.logp);
+  load4(a.old_logp, t, a.T, a.wide, f.old);
+  if (a.ref_logp != nullptr) load4(a.ref_logp, t, a.T, a.wide, f.ref);
+  if (a.entropy != nullptr) load4(a.entropy, t, a.T, a.wide, f.entropy);
+  if (!a.per_sequence) load4(a.advantages, t, a.T, a.wide, f.advantage);
+}
+// Their gradients, and their terms added to `sum`.  kept: the rows that count; w: weights.
+__device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, const Four& f,
+                                            unsigned kept, const float (&w)[4],
+                                            float (&sum)[kStats]) {
+  float grad[4], grad_entropy[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    grad[j] = grad_entropy[j] = 0.f;
+    if (!(kept >> j & 1u)) continue;  // whatever it holds
+    const float A = f.advantage[j], delta = f.logp[j] - f.old[j];
+    const float ratio = expf(delta);
+    const bool over = A > 0.f && delta > a.high, under = A < 0.f && delta < a.low;
+    const bool clipped = over || under;
+    float g = clipped ? 0.f : -A * ratio;
+    sum[0] += w[j] * (-A * (over ? a.ratio_high : under ? a.ratio_low : ratio));
+    if (a.ref_logp != nullptr) {
+      const float r = f.ref[j] - f.logp[j], up = expm1f(r);
+      sum[1] += w[j] * (up - r);
+      g -= a.kl_coef * up;
+    }
+    if (a.entropy != nullptr) {
+      sum[2] += w[j] * f.entropy[j];
+      grad_entropy[j] = -a.entropy_coef * w[j];
+    }
+    if (clipped) sum[3] += w[j];
+    grad[j] = w[j] * g;
+  }
+  store4(a.grad_logp, t, a.T, a.wide, grad);
+  if (a.grad_entropy != nullptr) store4(a.grad_entropy, t, a.T, a.wide, grad_entropy);
+}
+
+// The sums of a CTA's threads, in thread 0: shuffles, then the warps' sums in order.
+template <int kCtaThreads>
+__device__ __forceinline__ void cta_sum(float (&sum)[kStats], float (*slots)[kStats]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < kStats; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < kStats; ++k) slots[threadIdx.x / 32][k] = sum[k];
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int warp = 1; warp < int(blockDim.x) / 32; ++warp)
+#pragma unroll
+    for (int k = 0; k < kStats; ++k) sum[k] += slots[warp][k];
+}
+
+__device__ __forceinline__ void write_stats(const PolicyArgs& a, const float (&sum)[kStats]) {
+  a.stats[0] = sum[0] + a.kl_coef * sum[1] - a.entropy_coef * sum[2];
+#pragma unroll
+  for (int k = 0; k < kStats; ++k) a.stats[k + 1] = sum[k];
+}
+
+__device__ __forceinline__ float weight_of(bool by_sequence, unsigned in_sequence, unsigned whole) {
+  return by_sequence
+             ? 1.f / (static_cast<float>(max(in_sequence, 1u)) * static_cast<float>(max(whole, 1u)))
+             : 1.f / static_cast<float>(max(whole, 1u));
+}
+
+__global__ void __launch_bounds__(kSmallThreads) lp_policy_small_kernel(const __grid_constant__ PolicyArgs a) {
+  __shared__ int offsets[kSmallSequences + 1];
+  __shared__ unsigned counts[kSmallSequences];
+  __shared__ unsigned whole;
+  __shared__ float slots[kSmallThreads / 32][kStats];
+  const int B = int(a.n_sequences), threads = int(blockDim.x);
+  const bool sequences = a.cu_seqlens != nullptr;
+  if (threadIdx.x == 0) whole = 0;
+  if (sequences)
+    for (int i = threadIdx.x; i <= B; i += threads) {
+      const int64_t c = a.cu_seqlens[i];
+      offsets[i] = int(min(max(c, int64_t(0)), a.T));
+      if (i < B) counts[i] = 0;
+    }
+  // all rows are on their way before the counts are needed
+  Four rows[kSmallRounds];
+  unsigned kept[kSmallRounds];
+#pragma unroll
+  for (int k = 0; k < kSmallRounds; ++k) {
+    const int64_t t = 4 * (int64_t(threadIdx.x) + k * threads);
+    kept[k] = load_mask4(a.mask, t, a.T, a.wide);
+    load_rows(a, t, rows[k]);
+  }
+  __syncthreads();
+  int sequence[kSmallRounds][4];
+  unsigned mine = 0;
+#pragma unroll
+  for (int k = 0; k < kSmallRounds; ++k) {
+    const int64_t t = 4 * (int64_t(threadIdx.x) + k * threads);
+    if (sequences) {
+      int s = t < a.T ? int(upper_bound(offsets + 1, B, t)) : B;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        while (s < B && offsets[s + 1] <= t + j) ++s;
+        sequence[k][j] = s;
+        if (s == B || t + j < offsets[0]) kept[k] &= ~(1u << j);
+        if (a.by_sequence && kept[k] >> j & 1u) mine += atomicAdd(&counts[s], 1u) == 0 ? 1u : 0u;
+      }
+    }
+    if (!a.by_sequence) mine += __popc(kept[k]);
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0 && mine > 0) atomicAdd(&whole, mine);
+  __syncthreads();
   float sum[kStats] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t t = threadIdx.x; t < a.T; t += kThreads) {
-    float w = 0.f, A = 0.f;
-    bool counted = a.mask == nullptr || a.mask[t] != 0;
-    int64_t s = 0;
-    if (counted && a.cu_seqlens != nullptr) {
-      s = sequence_of(a.cu_seqlens, B, t);
-      counted = s < B;
+#pragma unroll
+  for (int k = 0; k < kSmallRounds; ++k) {
+    const int64_t t = 4 * (int64_t(threadIdx.x) + k * threads);
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!(kept[k] >> j & 1u)) continue;
+      w[j] = weight_of(a.by_sequence, a.by_sequence ? counts[sequence[k][j]] : 0u, whole);
+      if (a.per_sequence) rows[k].advantage[j] = a.advantages[sequence[k][j]];
     }
-    float grad = 0.f;
-    if (counted) {
-      w = a.by_sequence ? 1.f / (static_cast<float>(__ldcg(&counts[s])) * whole) : 1.f / whole;
-      A = a.advantages[a.per_sequence ? s : t];
-      const RowTerms r = row_terms(a, t, A);
-      sum[0] += w * r.policy;
-      sum[1] += w * r.kl;
-      sum[2] += w * r.entropy;
-      sum[3] += w * r.clipped;
-      grad = w * r.grad;
-    }
-    a.grad_logp[t] = grad;
-    if (a.grad_entropy != nullptr) a.grad_entropy[t] = -a.entropy_coef * w;
+    finish_rows(a, t, rows[k], kept[k], w, sum);
   }
-  for (int k = 0; k < kStats; ++k) slots[threadIdx.x][k] = sum[k];
-  for (int n = kThreads / 2; n > 0; n >>= 1) {
+  cta_sum<kSmallThreads>(sum, slots);
+  if (threadIdx.x == 0) write_stats(a, sum);
+}
+
+// The sequences that a chunk of rows touches.
+struct Span {
+  int64_t first, last;  // of its first and of its last row; n_sequences: none
+  bool staged;          // the offsets from cu_seqlens[first + 1] on are in shared memory
+};
+__device__ __forceinline__ Span find_span(const PolicyArgs& a, int64_t t0, int64_t t1,
+                                          int64_t* staged, int64_t* ends) {
+  const int warp = threadIdx.x / 32;
+  if (warp < 2) {
+    const int64_t s =
+        warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, warp == 0 ? t0 : t1 - 1);
+    if ((threadIdx.x & 31) == 0) ends[warp] = s;
+  }
+  __syncthreads();
+  Span span{ends[0], ends[1], false};
+  span.staged = span.last >= span.first && span.last - span.first < kStaged;
+  if (span.staged) {
+    for (int64_t i = threadIdx.x; i <= span.last - span.first; i += kThreads)
+      if (span.first + i < a.n_sequences) staged[i] = a.cu_seqlens[span.first + 1 + i];
     __syncthreads();
-    if (threadIdx.x < n)
-      for (int k = 0; k < kStats; ++k) slots[threadIdx.x][k] += slots[threadIdx.x + n][k];
   }
+  return span;
+}
+// The sequence of row t of the chunk.
+__device__ __forceinline__ int64_t sequence_of(const PolicyArgs& a, const Span& span,
+                                               const int64_t* staged, int64_t t) {
+  if (span.staged)
+    return span.first +
+           upper_bound(staged, min(span.last + 1, a.n_sequences) - span.first, t);
+  return upper_bound(a.cu_seqlens + 1, a.n_sequences, t);
+}
+__device__ __forceinline__ int64_t offset_after(const PolicyArgs& a, const Span& span,
+                                                const int64_t* staged, int64_t s) {
+  const int64_t i = s - span.first;
+  return span.staged && i >= 0 && i <= span.last - span.first ? staged[i] : a.cu_seqlens[s + 1];
+}
+
+__global__ void __launch_bounds__(kThreads) lp_policy_clear_kernel(Header* header, unsigned* counts, int64_t n) {
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (i == 0) header->counted = header->sequences = header->finished = 0;
+  if (i < n) counts[i] = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// First pass: the rows that count, in all or by sequence.
+__global__ void __launch_bounds__(kThreads)
+    lp_policy_count_kernel(const __grid_constant__ PolicyArgs a, Header* header, unsigned* counts) {
+  __shared__ int64_t staged[kStaged], ends[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t t0 = int64_t(blockIdx.x) * kChunk, t1 = min(t0 + kChunk, a.T);
+  if (!LP_CHECK(t0 < a.T, kChkRowIndex)) return;
+  unsigned kept[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k)
+    kept[k] = load_mask4(a.mask, t0 + 4 * (threadIdx.x + k * kThreads), a.T, a.wide);
+  Span span{0, 0, false};
+  if (a.cu_seqlens != nullptr) span = find_span(a, t0, t1, staged, ends);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+  unsigned mine = 0, started = 0;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int64_t t = t0 + 4 * (threadIdx.x + k * kThreads);
+    int64_t s = a.n_sequences;
+    unsigned in_s = 0;
+    if (a.cu_seqlens != nullptr && kept[k] != 0) {
+      s = sequence_of(a, span, staged, t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        while (s < a.n_sequences && offset_after(a, span, staged, s) <= t + j) {
+          if (a.by_sequence && in_s > 0) started += atomicAdd(&counts[s], in_s) == 0 ? 1u : 0u;
+          in_s = 0;
+          ++s;
+        }
+        if (s == a.n_sequences || t + j < a.cu_seqlens[0]) kept[k] &= ~(1u << j);
+        in_s += kept[k] >> j & 1u;
+      }
+    }
+    mine += __popc(kept[k]);
+    if (!a.by_sequence) continue;
+    // a warp's 128 rows mostly lie in one sequence
+    int same;
+    __match_all_sync(0xffffffffu, static_cast<unsigned long long>(s), &same);
+    if (same) in_s = __reduce_add_sync(0xffffffffu, in_s);
+    if (in_s > 0 && (!same || (threadIdx.x & 31) == 0))
+      started += atomicAdd(&counts[s], in_s) == 0 ? 1u : 0u;
+  }
+  mine = __reduce_add_sync(0xffffffffu, a.by_sequence ? started : mine);
+  if ((threadIdx.x & 31) == 0 && mine > 0)
+    atomicAdd(a.by_sequence ? &header->sequences : &header->counted, mine);
+}
+
+// Second pass: weights, terms, gradients, and the sums by the CTA that finishes last.
+__global__ void __launch_bounds__(kThreads)
+    lp_policy_rows_kernel(const __grid_constant__ PolicyArgs a, Header* header, const unsigned* counts,
+                          float4* partials) {
+  __shared__ int64_t staged[kStaged], ends[2];
+  __shared__ float slots[kThreads / 32][kStats];
+  __shared__ bool last;
+  const int64_t t0 = int64_t(blockIdx.x) * kChunk, t1 = min(t0 + kChunk, a.T);
+  if (!LP_CHECK(t0 < a.T, kChkRowIndex)) return;
+  Span span{0, 0, false};
+  if (a.cu_seqlens != nullptr) span = find_span(a, t0, t1, staged, ends);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are done
+  const unsigned whole = __ldcg(a.by_sequence ? &header->sequences : &header->counted);
+  float sum[kStats] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int k = 0; k < kRounds; ++k) {
+    const int64_t t = t0 + 4 * (threadIdx.x + k * kThreads);
+    if (t >= a.T) break;
+    Four f;
+    unsigned kept = load_mask4(a.mask, t, a.T, a.wide);
+    load_rows(a, t, f);
+    float w[4];
+    int64_t s = a.cu_seqlens != nullptr && kept != 0 ? sequence_of(a, span, staged, t) : 0;
+    int64_t known = -1;
+    float weight = weight_of(false, 0u, whole), advantage = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!(kept >> j & 1u)) continue;
+      if (a.cu_seqlens != nullptr) {
+        while (s < a.n_sequences && offset_after(a, span, staged, s) <= t + j) ++s;
+        if (s == a.n_sequences || t + j < a.cu_seqlens[0]) {
+          kept &= ~(1u << j);
+          continue;
+        }
+        if (s != known) {
+          known = s;
+          if (a.by_sequence) weight = weight_of(true, __ldcg(counts + s), whole);
+          if (a.per_sequence) advantage = __ldg(a.advantages + s);
+        }
+        if (a.per_sequence) f.advantage[j] = advantage;
+      }
+      w[j] = weight;
+    }
+    finish_rows(a, t, f, kept, w, sum);
+  }
+  cta_sum<kThreads>(sum, slots);
   if (threadIdx.x == 0) {
-    const float policy = slots[0][0], kl = slots[0][1], entropy = slots[0][2];
-    a.stats[0] = policy + a.kl_coef * kl - a.entropy_coef * entropy;
-    a.stats[1] = policy;
-    a.stats[2] = kl;
-    a.stats[3] = entropy;
-    a.stats[4] = slots[0][3];
+    partials[blockIdx.x] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    __threadfence();
+    last = atomicAdd(&header->finished, 1u) == gridDim.x - 1;
   }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+#pragma unroll
+  for (int k = 0; k < kStats; ++k) sum[k] = 0.f;
+  for (int64_t i = threadIdx.x; i < gridDim.x; i += kThreads) {
+    const float4 p = __ldcg(partials + i);
+    sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
+  }
+  cta_sum<kThreads>(sum, slots);
+  if (threadIdx.x == 0) write_stats(a, sum);
+}
+
+bool one_cta(int64_t T, int64_t n_sequences) {
+  return T <= kSmallRows && n_sequences <= kSmallSequences;
+}
+int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
+
+template <class... Params, class... Args>
+bool launch_dependent(void (*kernel)(Params...), int64_t blocks, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 }  // namespace
 
-size_t policy_loss_workspace(int64_t, int64_t n_sequences) {
-  return static_cast<size_t>(std::max<int64_t>(1, n_sequences)) * 4;
+size_t policy_loss_workspace(int64_t T, int64_t n_sequences) {
+  if (one_cta(T, n_sequences)) return kHeaderBytes;
+  return kHeaderBytes + counts_bytes(n_sequences) + static_cast<size_t>(chunks_of(T)) * sizeof(float4);
 }
 
-lp_status launch_policy_loss(const PolicyArgs& a, cudaStream_t stream) {
-  lp_policy_kernel<<<1, kThreads, 0, stream>>>(a);
+lp_status launch_policy_loss(const PolicyArgs& args, cudaStream_t stream) {
+  PolicyArgs a = args;
+  const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  a.wide = at16(a.logp) && at16(a.old_logp) && at16(a.ref_logp) && at16(a.entropy) &&
+           (a.per_sequence || at16(a.advantages)) && at16(a.grad_logp) && at16(a.grad_entropy) &&
+           reinterpret_cast<uintptr_t>(a.mask) % 4 == 0;
+  if (a.T == 0) {  // nothing counts
+    a.cu_seqlens = nullptr;
+    a.n_sequences = 0;
+  }
+  if (one_cta(a.T, a.n_sequences)) {
+    const int64_t groups = (a.T + 3) / 4;
+    const int threads = int(std::min<int64_t>(kSmallThreads, std::max<int64_t>(1, (groups + 31) / 32) * 32));
+    lp_policy_small_kernel<<<1, threads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  }
+  char* p = static_cast<char*>(a.workspace);
+  Header* header = reinterpret_cast<Header*>(p);
+  unsigned* counts = reinterpret_cast<unsigned*>(p + kHeaderBytes);
+  float4* partials = reinterpret_cast<float4*>(p + kHeaderBytes + counts_bytes(a.n_sequences));
+  const int64_t cleared = a.by_sequence ? a.n_sequences : 0;
+  const int64_t chunks = chunks_of(a.T);
+  lp_policy_clear_kernel<<<unsigned(cleared / kThreads + 1), kThreads, 0, stream>>>(header, counts, cleared);
+  if (cudaGetLastError() != cudaSuccess) return LP_ERR_CUDA;
+  if (!launch_dependent(lp_policy_count_kernel, chunks, stream, a, header, counts) ||
+      !launch_dependent(lp_policy_rows_kernel, chunks, stream, a, header,
+                        static_cast<const unsigned*>(counts), partials))
+    return LP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 

@@ -64,6 +64,7 @@ struct PolicyArgs {
   float low, high;            // the clip's limits on delta
   float ratio_low, ratio_high;
   float kl_coef, entropy_coef;
+  bool wide;                  // set by the launcher: rows may go 16 bytes at a time
   float *stats, *grad_logp, *grad_entropy;
   void* workspace;
 };
