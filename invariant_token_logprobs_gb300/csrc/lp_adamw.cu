@@ -71,119 +71,233 @@ __device__ __forceinline__ float scale_of(float largest, bool finite) {
   return largest < 0x1p-100f ? 0.f : largest;
 }
 
-__global__ void __launch_bounds__(kThreads) lp_adamw_kernel(AdamwArgs a) {
+// A lane's 8 elements of a block: 4 lane + {0..3} and 128 + 4 lane + {0..3}, 16 bytes of
+// float32 or 8 of bfloat16 an access.  Where the tensor is not aligned for that, or the block
+// is its ragged end, they go through a warp's stretch of shared memory, 32 neighbours an access.
+__device__ __forceinline__ void load8(const float* p, int count, bool wide, float* stretch,
+                                      float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  if (wide && count >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
+                   : "l"(p + 128 * h + 4 * lane)
+                   : "memory");
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = 32 * k + lane;
+    stretch[e] = e < count ? p[e] : 0.f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = stretch[(k >> 2) * 128 + lane * 4 + (k & 3)];
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int count, bool wide, float* stretch,
+                                      float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  if (wide && count >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a, b;
+      asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(a), "=r"(b)
+                   : "l"(p + 128 * h + 4 * lane)
+                   : "memory");
+      v[4 * h] = __uint_as_float(a << 16), v[4 * h + 1] = __uint_as_float(a & 0xffff0000u);
+      v[4 * h + 2] = __uint_as_float(b << 16), v[4 * h + 3] = __uint_as_float(b & 0xffff0000u);
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = 32 * k + lane;
+    stretch[e] = e < count ? __bfloat162float(p[e]) : 0.f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = stretch[(k >> 2) * 128 + lane * 4 + (k & 3)];
+}
+__device__ __forceinline__ void store8(float* p, __nv_bfloat16* copy, int count, bool wide,
+                                       float* stretch, const float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  if (wide && count >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = 128 * h + 4 * lane;
+      *reinterpret_cast<float4*>(p + e) =
+          make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      if (copy == nullptr) continue;
+      __nv_bfloat162 two[2] = {__floats2bfloat162_rn(v[4 * h], v[4 * h + 1]),
+                               __floats2bfloat162_rn(v[4 * h + 2], v[4 * h + 3])};
+      *reinterpret_cast<uint2*>(copy + e) = *reinterpret_cast<const uint2*>(two);
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) stretch[(k >> 2) * 128 + lane * 4 + (k & 3)] = v[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = 32 * k + lane;
+    if (e >= count) continue;
+    p[e] = stretch[e];
+    if (copy != nullptr) copy[e] = __float2bfloat16_rn(stretch[e]);
+  }
+}
+
+// One block of a tensor a warp.  The moments' buffers are padded to whole blocks, and what lies
+// past a tensor's end in them stays zero.
+template <bool kSmall>
+__global__ void __launch_bounds__(kThreads) lp_adamw_kernel(const __grid_constant__ AdamwArgs a) {
+  __shared__ __align__(16) float stretches[kThreads / 32][kBlock];
   const int64_t row = blockIdx.x;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int32_t index = a.table[row];
   if (!LP_CHECK(index >= 0 && index < a.n_tensors, kChkPlan)) return;
   const AdamwRecord rec = a.records[index];
-  const float clip = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
-  if (clip != clip) return;
+  // this warp's block: its first element in the tensor and in the flat buffers
+  const int64_t first = (row - rec.first_row) * kRow + warp * kBlock;
+  const int64_t flat = row * kRow + warp * kBlock, block = flat / kBlock;
+  if (first >= rec.n) return;
+  const int count = int(min(rec.n - first, int64_t(kBlock)));
+  const bool is_wide = rec.wide != 0;
+  float* stretch = stretches[warp];
+  float p[8], g[8], m[8], v[8];
+  uint32_t old_m[2], old_u[2];
+  float old_scale_m = 0.f, old_scale_u = 0.f;
+  load8(rec.param + first, count, is_wide, stretch, p);
+  if (rec.grad_bf16)
+    load8(static_cast<const __nv_bfloat16*>(rec.grad) + first, count, is_wide, stretch, g);
+  else
+    load8(static_cast<const float*>(rec.grad) + first, count, is_wide, stretch, g);
+  if (kSmall) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      old_m[h] = static_cast<const uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane];
+      old_u[h] = static_cast<const uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane];
+    }
+    old_scale_m = a.exp_avg_scale[block];
+    old_scale_u = a.exp_avg_sq_scale[block];
+  } else {
+    load8(static_cast<const float*>(a.exp_avg) + flat, kBlock, true, stretch, m);
+    load8(static_cast<const float*>(a.exp_avg_sq) + flat, kBlock, true, stretch, v);
+  }
+  float clip = 1.f;
+  if (a.grad_scale != nullptr) {
+    clip = *a.grad_scale;
+    if (clip != clip) return;
+  }
   const float lr = a.lr * rec.lr_scale;
   const float kept = 1.f - lr * rec.weight_decay, step_size = a.step_size * rec.lr_scale;
-  const int lane = threadIdx.x & 31;
-  const bool small = a.exp_avg_scale != nullptr;
-  // this warp's block: its first element in the tensor and in the flat buffers
-  const int64_t first = (row - rec.first_row) * kRow + (threadIdx.x >> 5) * kBlock;
-  const int64_t flat = row * kRow + (threadIdx.x >> 5) * kBlock;
-  if (first >= rec.n) return;
-  const int64_t block = flat / kBlock;
-  float m[8], u[8];
-  float top_m = 0.f, top_u = 0.f;
+  float u[8], top_m = 0.f, top_u = 0.f;
   bool finite = true;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int e = (k >> 2) * 128 + lane * 4 + (k & 3);
-    m[k] = u[k] = 0.f;
-    if (first + e >= rec.n) continue;
-    float g = rec.grad_bf16
-                  ? __bfloat162float(static_cast<const __nv_bfloat16*>(rec.grad)[first + e])
-                  : static_cast<const float*>(rec.grad)[first + e];
-    if (a.grad_scale != nullptr) g *= clip;
-    float m0, v0;
-    if (small) {
-      m0 = Code<true>::decode(static_cast<uint8_t*>(a.exp_avg)[flat + e], a.exp_avg_scale[block]);
-      v0 = Code<false>::decode(static_cast<uint8_t*>(a.exp_avg_sq)[flat + e],
-                               a.exp_avg_sq_scale[block]);
-      v0 *= v0;
-    } else {
-      m0 = static_cast<float*>(a.exp_avg)[flat + e];
-      v0 = static_cast<float*>(a.exp_avg_sq)[flat + e];
+    if (kSmall) {
+      m[k] = Code<true>::decode(old_m[k >> 2] >> 8 * (k & 3) & 255u, old_scale_m);
+      v[k] = Code<false>::decode(old_u[k >> 2] >> 8 * (k & 3) & 255u, old_scale_u);
+      v[k] *= v[k];
     }
-    m[k] = a.beta1 * m0 + a.rest1 * g;
-    const float v = a.beta2 * v0 + a.rest2 * (g * g);
-    u[k] = sqrtf(v);
+    const float gk = a.grad_scale != nullptr ? g[k] * clip : g[k];
+    m[k] = a.beta1 * m[k] + a.rest1 * gk;
+    v[k] = a.beta2 * v[k] + a.rest2 * (gk * gk);
+    u[k] = sqrtf(v[k]);
     const float change = m[k] / (u[k] * a.root_scale + a.eps);
-    const float p = rec.param[first + e] * kept - step_size * change;
-    rec.param[first + e] = p;
-    if (rec.copy != nullptr) rec.copy[first + e] = __float2bfloat16_rn(p);
-    if (!small) {
-      static_cast<float*>(a.exp_avg)[flat + e] = m[k];
-      static_cast<float*>(a.exp_avg_sq)[flat + e] = v;
+    p[k] = p[k] * kept - step_size * change;
+    if (kSmall) {
+      top_m = fmaxf(top_m, fabsf(m[k]));
+      top_u = fmaxf(top_u, u[k]);
+      finite = finite && fabsf(m[k]) <= 0x1.fffffep127f && u[k] <= 0x1.fffffep127f;
     }
-    top_m = fmaxf(top_m, fabsf(m[k]));
-    top_u = fmaxf(top_u, u[k]);
-    finite = finite && fabsf(m[k]) <= 0x1.fffffep127f && u[k] <= 0x1.fffffep127f;
   }
-  if (!small) return;
+  store8(rec.param + first, rec.copy != nullptr ? rec.copy + first : nullptr, count, is_wide, stretch,
+         p);
+  if (!kSmall) {
+    store8(static_cast<float*>(a.exp_avg) + flat, nullptr, kBlock, true, stretch, m);
+    store8(static_cast<float*>(a.exp_avg_sq) + flat, nullptr, kBlock, true, stretch, v);
+    return;
+  }
   finite = __all_sync(0xffffffffu, finite);
   const float scale_m = scale_of(warp_max(top_m), finite);
   const float scale_u = scale_of(warp_max(top_u), finite);
   const float inv_m = scale_m > 0.f ? 1.f / scale_m : 0.f;
   const float inv_u = scale_u > 0.f ? 1.f / scale_u : 0.f;
-  __syncwarp();  // every lane has read the old scales
   if (lane == 0) {
     a.exp_avg_scale[block] = scale_m;
     a.exp_avg_sq_scale[block] = scale_u;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w[4];
+    uint32_t w[4], new_m = 0, new_u = 0;
     random_words(uint64_t(flat / 4 + h * 32 + lane), a.step, a.seed, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int e = h * 128 + lane * 4 + j;
-      static_cast<uint8_t*>(a.exp_avg)[flat + e] =
-          uint8_t(Code<true>::encode(m[h * 4 + j], inv_m, w[j] & 0xffffu));
-      static_cast<uint8_t*>(a.exp_avg_sq)[flat + e] =
-          uint8_t(Code<false>::encode(u[h * 4 + j], inv_u, w[j] >> 16));
+      new_m |= Code<true>::encode(m[h * 4 + j], inv_m, w[j] & 0xffffu) << 8 * j;
+      new_u |= Code<false>::encode(u[h * 4 + j], inv_u, w[j] >> 16) << 8 * j;
     }
+    static_cast<uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane] = new_m;
+    static_cast<uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane] = new_u;
   }
 }
 
+// One row of a tensor a warp, whose squares are summed by lane in order and then by shuffles.
 __global__ void __launch_bounds__(kThreads)
     lp_adamw_square_sum_kernel(const AdamwRecord* records, const int32_t* table, int64_t n_tensors,
-                               float* sums) {
-  __shared__ float slots[kThreads / 32];
-  const int64_t row = blockIdx.x;
+                               int64_t rows, float* sums) {
+  __shared__ __align__(16) float stretches[kThreads / 32][kBlock];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x / 32;
+  const int64_t row = int64_t(blockIdx.x) * (kThreads / 32) + warp;
+  if (row >= rows) return;
   const int32_t index = table[row];
   if (!LP_CHECK(index >= 0 && index < n_tensors, kChkPlan)) return;
   const AdamwRecord rec = records[index];
   const int64_t first = (row - rec.first_row) * kRow;
+  const int count = int(min(rec.n - first, int64_t(kRow)));
   float s = 0.f;
-  for (int e = threadIdx.x; e < kRow && first + e < rec.n; e += kThreads) {
-    const float g = rec.grad_bf16
-                        ? __bfloat162float(static_cast<const __nv_bfloat16*>(rec.grad)[first + e])
-                        : static_cast<const float*>(rec.grad)[first + e];
-    s += g * g;
+#pragma unroll 8
+  for (int b = 0; b < kRow; b += kBlock) {
+    if (b >= count) break;
+    float g[8];
+    if (rec.grad_bf16)
+      load8(static_cast<const __nv_bfloat16*>(rec.grad) + first + b, count - b, rec.wide != 0,
+            stretches[warp], g);
+    else
+      load8(static_cast<const float*>(rec.grad) + first + b, count - b, rec.wide != 0,
+            stretches[warp], g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += g[k] * g[k];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int w = 1; w < kThreads / 32; ++w) s += slots[w];
-  sums[row] = s;
+  if ((threadIdx.x & 31) == 0) sums[row] = s;
 }
 
-__global__ void __launch_bounds__(kThreads)
+constexpr int kNormThreads = 1024;
+__global__ void __launch_bounds__(kNormThreads)
     lp_adamw_norm_kernel(const float* sums, int64_t rows, float max_norm, float* norm_out) {
-  __shared__ double slots[kThreads];
+  __shared__ double slots[kNormThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < rows; i += kThreads) s += sums[i];
-  slots[threadIdx.x] = s;
+  const int64_t quads = rows / 4;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < quads; i += kNormThreads) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(sums) + i);
+    s += (double(x.x) + double(x.y)) + (double(x.z) + double(x.w));
+  }
+  if (threadIdx.x < rows % 4) s += __ldcg(sums + quads * 4 + threadIdx.x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = s;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int i = 1; i < kThreads; ++i) s += slots[i];
+  for (int i = 1; i < kNormThreads / 32; ++i) s += slots[i];
   const float norm = static_cast<float>(sqrt(s));
   norm_out[0] = norm;
   norm_out[1] = norm <= 0x1.fffffep127f ? fminf(max_norm / (norm + 1e-6f), 1.f)
@@ -191,20 +305,45 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 __global__ void __launch_bounds__(kThreads)
-    lp_adamw_values_kernel(const uint8_t* m, const uint8_t* u, const float* m_scale,
-                           const float* u_scale, float* m_out, float* v_out) {
-  for (int e = threadIdx.x; e < kRow; e += kThreads) {
-    const int64_t i = int64_t(blockIdx.x) * kRow + e;
-    m_out[i] = Code<true>::decode(m[i], m_scale[i / kBlock]);
-    const float root = Code<false>::decode(u[i], u_scale[i / kBlock]);
-    v_out[i] = root * root;
+    lp_adamw_values_kernel(const uint32_t* m, const uint32_t* u, const float* m_scale,
+                           const float* u_scale, float4* m_out, float4* v_out) {
+#pragma unroll
+  for (int k = 0; k < kRow / 4 / kThreads; ++k) {
+    const int64_t i = int64_t(blockIdx.x) * (kRow / 4) + k * kThreads + threadIdx.x;
+    const uint32_t cm = __ldg(m + i), cu = __ldg(u + i);
+    const float sm = __ldg(m_scale + i / (kBlock / 4)), su = __ldg(u_scale + i / (kBlock / 4));
+    float a[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = Code<true>::decode(cm >> 8 * j & 255u, sm);
+      const float root = Code<false>::decode(cu >> 8 * j & 255u, su);
+      b[j] = root * root;
+    }
+    m_out[i] = make_float4(a[0], a[1], a[2], a[3]);
+    v_out[i] = make_float4(b[0], b[1], b[2], b[3]);
   }
+}
+
+template <class... Params, class... Args>
+bool launch_dependent(void (*kernel)(Params...), int64_t blocks, int threads, cudaStream_t stream,
+                      Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 }  // namespace
 
 lp_status launch_adamw_step(const AdamwArgs& a, cudaStream_t stream) {
-  lp_adamw_kernel<<<unsigned(a.rows), kThreads, 0, stream>>>(a);
+  auto* kernel = a.exp_avg_scale != nullptr ? lp_adamw_kernel<true> : lp_adamw_kernel<false>;
+  kernel<<<unsigned(a.rows), kThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 
@@ -216,10 +355,15 @@ lp_status launch_adamw_grad_norm(const AdamwRecord* records, const int32_t* tabl
                                  int64_t n_tensors, int64_t rows, float max_norm, float* norm_out,
                                  void* workspace, cudaStream_t stream) {
   float* sums = static_cast<float*>(workspace);
-  if (rows > 0)
-    lp_adamw_square_sum_kernel<<<unsigned(rows), kThreads, 0, stream>>>(records, table, n_tensors,
-                                                                        sums);
-  lp_adamw_norm_kernel<<<1, kThreads, 0, stream>>>(sums, rows, max_norm, norm_out);
+  constexpr int kRowsOfCta = kThreads / 32;
+  if (rows > 0) {
+    lp_adamw_square_sum_kernel<<<unsigned((rows + kRowsOfCta - 1) / kRowsOfCta), kThreads, 0,
+                                 stream>>>(records, table, n_tensors, rows, sums);
+    if (cudaGetLastError() != cudaSuccess) return LP_ERR_CUDA;
+  }
+  if (!launch_dependent(lp_adamw_norm_kernel, 1, kNormThreads, stream,
+                        static_cast<const float*>(sums), rows, max_norm, norm_out))
+    return LP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 
@@ -228,8 +372,9 @@ lp_status launch_adamw_state_values(const void* exp_avg, const void* exp_avg_sq,
                                     int64_t rows, float* m_out, float* v_out,
                                     cudaStream_t stream) {
   lp_adamw_values_kernel<<<unsigned(rows), kThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(exp_avg), static_cast<const uint8_t*>(exp_avg_sq), exp_avg_scale,
-      exp_avg_sq_scale, m_out, v_out);
+      static_cast<const uint32_t*>(exp_avg), static_cast<const uint32_t*>(exp_avg_sq),
+      exp_avg_scale, exp_avg_sq_scale, reinterpret_cast<float4*>(m_out),
+      reinterpret_cast<float4*>(v_out));
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 
