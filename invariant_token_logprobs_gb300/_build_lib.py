@@ -24,10 +24,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liblp.so")
 SOURCES = ["lp_api.cu", "lp_logits.cu", "lp_linear.cu", "lp_backward.cu", "lp_train_api.cu",
-           "lp_norm.cu", "lp_policy.cu", "lp_adamw.cu"]
+           "lp_norm.cu", "lp_norm_backward.cu", "lp_policy.cu", "lp_adamw.cu"]
 HEADERS = [os.path.join(ROOT, "include", f) for f in ("lp.h", "lp_train.h")] + [
     os.path.join(CSRC, f) for f in ("lp_device.cuh", "lp_internal.h", "lp_tcgen05.cuh",
-                                    "lp_check.cuh", "lp_train_internal.h")
+                                    "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh")
 ]
 # the checked build (-DLP_CHECKED: index and coordinate tests in every kernel)
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")

@@ -164,17 +164,18 @@ lp_status lp_get_check_word(uint32_t* word_out) {
   const lp_status st = lp::current_device(&dev);
   if (st != LP_OK) return st;
   if (cudaDeviceSynchronize() != cudaSuccess) return LP_ERR_CUDA;
-  uint32_t a = 0, b = 0, c = 0, n = 0, p = 0, w = 0;
+  uint32_t a = 0, b = 0, c = 0, n = 0, nb = 0, p = 0, w = 0;
   if (lp::take_check_word_logits(&a) != cudaSuccess ||
       lp::take_check_word_linear(&b) != cudaSuccess ||
       lp::take_check_word_backward(&c) != cudaSuccess ||
       lp::take_check_word_norm(&n) != cudaSuccess ||
+      lp::take_check_word_norm_backward(&nb) != cudaSuccess ||
       lp::take_check_word_policy(&p) != cudaSuccess ||
       lp::take_check_word_adamw(&w) != cudaSuccess) {
     cudaGetLastError();
     return LP_ERR_CUDA;
   }
-  *word_out = a | b | c | n | p | w;
+  *word_out = a | b | c | n | nb | p | w;
   return LP_OK;
 }
 

@@ -1,0 +1,369 @@
+// lp_norm.cuh: what the residual norm's forward and backward kernels share.
+//
+// Both are bound by the bytes of their row operands, so a row is read once and held
+// on chip.  A row belongs to a team of whole warps; thread i of a team of n owns the
+// groups of 8 columns i, i + n, i + 2n, ... of the row, which is 16 bytes of bfloat16
+// or 32 of float32.  The team's size and the groups a thread holds depend on d alone,
+// so a row's sums are taken in the same order whatever the batch.
+//
+// A CTA takes rows in turn.  The operands of the next rows are on their way into a ring
+// of shared memory (cp.async) while the current one is computed, so that the two
+// sums of a row, each a wait for all its threads, do not leave the memory idle.  A thread
+// copies its own groups where every row is aligned for it (the kernels' kFast); else its
+// warp copies its stretch of the row, 32 neighbours an access.  The arithmetic and its
+// order are the same.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "lp_check.cuh"
+#include "lp_train_internal.h"
+
+namespace lp {
+namespace {
+
+constexpr int kMaxTeam = 512;  // threads of a row, and of a CTA
+constexpr int kMaxWarps = kMaxTeam / 32;
+// Row slots: one for each SM of a GB300.  Fixed, so that the order in which the backward
+// sums rows does not depend on the device's partition.
+constexpr int64_t kSlots = 152;
+
+// 8 columns as they lie in memory.
+template <class T>
+struct __align__(8 * sizeof(T)) Group {
+  uint32_t w[2 * sizeof(T)];
+};
+using Group16 = Group<__nv_bfloat16>;
+using Group32 = Group<float>;
+
+__device__ __forceinline__ void store_group(__nv_bfloat16* p, const Group16& g) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(g.w[0]), "r"(g.w[1]),
+               "r"(g.w[2]), "r"(g.w[3])
+               : "memory");
+}
+__device__ __forceinline__ void store_group(float* p, const Group32& g) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(g.w[0]),
+               "r"(g.w[1]), "r"(g.w[2]), "r"(g.w[3]), "r"(g.w[4]), "r"(g.w[5]), "r"(g.w[6]),
+               "r"(g.w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float element(const Group32& g, int i) { return __uint_as_float(g.w[i]); }
+__device__ __forceinline__ float element(const Group16& g, int i) {
+  return __uint_as_float(i & 1 ? g.w[i / 2] & 0xffff0000u : g.w[i / 2] << 16);
+}
+// Element i as it is stored.
+template <class T>
+__device__ __forceinline__ T item(const Group<T>& g, int i);
+template <>
+__device__ __forceinline__ float item(const Group32& g, int i) { return element(g, i); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 item(const Group16& g, int i) {
+  return __ushort_as_bfloat16(
+      static_cast<unsigned short>(i & 1 ? g.w[i / 2] >> 16 : g.w[i / 2] & 0xffffu));
+}
+__device__ __forceinline__ Group32 pack(const float (&v)[8], float) {
+  Group32 g;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g.w[i] = __float_as_uint(v[i]);
+  return g;
+}
+__device__ __forceinline__ Group16 pack(const float (&v)[8], __nv_bfloat16) {
+  Group16 g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    g.w[i] = *reinterpret_cast<const uint32_t*>(&two);
+  }
+  return g;
+}
+
+// How an operand's rows can be reached: whole groups, 4 bytes at a time, or only element by
+// element (bfloat16 at odd places).  2 bits an operand.
+enum Access : uint32_t { kPlain = 0, kWords = 1, kWide = 2 };
+enum Operand : int {
+  kResidual, kBranch, kGate, kOut, kNormed, kGradNormed, kGradOut, kGradResidual, kGradBranch,
+  kGradGate, kBranchWeight, kWeight,
+};
+__host__ __device__ __forceinline__ uint32_t access_of(uint32_t accesses, int operand) {
+  return accesses >> 2 * operand & 3u;
+}
+
+// How rows of d columns are laid over threads.
+struct Shape {
+  int team;   // threads of a row
+  int teams;  // rows of a CTA at once
+};
+
+// What the kernels need to know besides the operands.
+struct Plan {
+  Shape shape;
+  uint32_t accesses;
+  int stages;       // of the ring
+  int stage_bytes;
+};
+
+// A thread's place in its CTA.
+struct Place {
+  int d;           // the row's columns
+  int i, team;     // which thread of its team
+  int lane, warp;
+  int in_cta;      // which team of the CTA
+  int first_warp;  // of the team
+  __device__ __forceinline__ Place(int64_t columns, const Shape& s)
+      : d(int(columns)),
+        i(int(threadIdx.x)),
+        team(s.team),
+        lane(int(threadIdx.x & 31)),
+        warp(int(threadIdx.x / 32)),
+        in_cta(0),
+        first_warp(0) {
+    if (s.teams > 1) {
+      in_cta = int(threadIdx.x) / s.team;
+      i -= in_cta * s.team;
+      first_warp = in_cta * (s.team / 32);
+    }
+  }
+};
+
+// A row operand on its way through the ring: this thread's place in the rows and in a stage.
+template <class T>
+struct Stream {
+  const T* row;     // the row that is fetched next, from the thread's first group on; from its
+                    // first column on where it is not kFast
+  int64_t advance;  // elements from one turn's row to the next
+  uint32_t slot;    // the thread's first group in stage 0, as a shared address
+  T* ring;          // the same as a pointer
+
+  // `offset` is the operand's first byte in a stage, moved past it.
+  template <bool kFast, int G>
+  __device__ __forceinline__ void start(const Rows& r, int64_t t, int64_t step, const Place& p,
+                                        unsigned char* stage0, int* offset) {
+    row = static_cast<const T*>(r.p) + t * r.ld + (kFast ? 8 * p.i : 0);
+    advance = step * r.ld;
+    ring = reinterpret_cast<T*>(stage0 + *offset) + 8 * threadIdx.x;
+    slot = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    *offset += int(blockDim.x) * G * 8 * int(sizeof(T));
+  }
+  // Starts the copy of the next row's groups into the stage `at` bytes on; zeros where the team
+  // has no row (or past its columns), as a row of zeros adds nothing to any sum.
+  template <bool kFast, int G>
+  __device__ __forceinline__ void fetch(uint32_t at, bool mine, uint32_t access, const Place& p) {
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const uint32_t to = slot + at + k * int(blockDim.x) * 8 * int(sizeof(T));
+      if (kFast) {
+        const int c = 8 * (p.i + k * p.team);
+        const uint32_t bytes = mine && c < p.d ? 16u : 0u;
+#pragma unroll
+        for (int q = 0; q < int(sizeof(T)) / 2; ++q)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * q),
+                       "l"(bytes ? row + k * p.team * 8 + q * (16 / int(sizeof(T))) : row), "r"(bytes)
+                       : "memory");
+        continue;
+      }
+      // the warp's stretch, 32 neighbours an access
+      const int first = 8 * (p.i - p.lane + k * p.team);
+      const uint32_t stretch = to - 8 * p.lane * int(sizeof(T));
+      const int d = mine ? p.d : 0;
+      if (access != kPlain) {
+        constexpr int kOf4 = 4 / sizeof(T);
+#pragma unroll
+        for (int q = 0; q < 2 * int(sizeof(T)); ++q) {
+          const int e = (32 * q + p.lane) * kOf4, left = d - first - e;
+          const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                           stretch + e * int(sizeof(T))),
+                       "l"(bytes ? row + first + e : row), "r"(bytes)
+                       : "memory");
+        }
+      } else {
+        T* s = reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(ring) + at) +
+               k * int(blockDim.x) * 8 - 8 * p.lane;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int e = 32 * q + p.lane;
+          s[e] = first + e < d ? row[first + e] : T(0.f);
+        }
+      }
+    }
+    row += advance;
+  }
+  // The thread's group k in the stage `at` bytes on.
+  __device__ __forceinline__ void get(uint32_t at, int k, float (&v)[8]) const {
+    const uint4* from = reinterpret_cast<const uint4*>(
+        reinterpret_cast<const unsigned char*>(ring) + at + k * int(blockDim.x) * 8 * int(sizeof(T)));
+    Group<T> g;
+#pragma unroll
+    for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
+      const uint4 x = from[q];
+      g.w[4 * q] = x.x, g.w[4 * q + 1] = x.y, g.w[4 * q + 2] = x.z, g.w[4 * q + 3] = x.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = element(g, e);
+  }
+};
+
+// Waits for all but the newest `ahead` commits of this thread's copies.
+__device__ __forceinline__ void wait_copies(int ahead) {
+  if (ahead >= 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (ahead == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (ahead == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Writes the thread's group k of row t, through a warp's stretch of 256 elements where rows are
+// not aligned.  All threads of a warp call it together; `mine`: the team has a row.
+template <bool kFast, class T>
+__device__ __forceinline__ void write_group(const Rows& r, int64_t t, int k, bool mine,
+                                            uint32_t access, const Place& p, void* stretch,
+                                            const float (&v)[8]) {
+  const Group<T> g = pack(v, T());
+  const int c = 8 * (p.i + k * p.team);
+  T* row = static_cast<T*>(r.p) + t * r.ld;
+  if (kFast) {
+    if (mine && c < p.d) store_group(row + c, g);
+    return;
+  }
+  const int d = mine ? p.d : 0;
+  if (access == kWide) {
+    if (c + 8 <= d) return store_group(row + c, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < d) row[c + e] = item<T>(g, e);
+    return;
+  }
+  T* s = static_cast<T*>(stretch);
+  const int first = c - 8 * p.lane;
+  __syncwarp();
+  reinterpret_cast<Group<T>*>(s)[p.lane] = g;
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int e = 32 * q + p.lane;
+    if (first + e < d) row[first + e] = s[e];
+  }
+}
+
+// Group k of a weight vector, of a type known at run time.  It is read again by every row, so it
+// may stay in L1.
+__device__ __forceinline__ void read_weight(const void* w, bool bf16, int k, bool wide,
+                                            const Place& p, float (&v)[8]) {
+  const int index = p.i + k * p.team, c = 8 * index;
+  if (wide && c + 8 <= p.d) {
+    if (bf16) {
+      const uint4 x = __ldg(static_cast<const uint4*>(w) + index);
+      const Group16 g{{x.x, x.y, x.z, x.w}};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = element(g, e);
+    } else {
+      const float4 a = __ldg(static_cast<const float4*>(w) + 2 * index);
+      const float4 b = __ldg(static_cast<const float4*>(w) + 2 * index + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = c + e >= p.d ? 0.f
+           : bf16       ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c + e])
+                        : static_cast<const float*>(w)[c + e];
+}
+
+// N sums over a team at once, the same bits for all its threads: shuffles within the warps, then
+// over the warps' sums, of which there are at most 16.  `slots` is written again only after
+// another barrier.
+template <int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*slots)[N], const Place& p) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (p.team == 32) return;
+  if (p.lane == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) slots[p.warp][k] = v[k];
+  __syncthreads();
+  const int w = p.lane & (kMaxWarps - 1);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 32 * w < p.team ? slots[p.first_warp + w][k] : 0.f;
+#pragma unroll
+  for (int o = kMaxWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
+
+// ------------------------------------------------------------------------- host
+
+Shape shape_of(int64_t d, int groups_per_thread, int64_t T) {
+  const int64_t groups = (d + 7) / 8;
+  Shape s;
+  s.team = int((groups + 32 * groups_per_thread - 1) / (32 * groups_per_thread)) * 32;
+  s.teams = int(std::max<int64_t>(1, std::min<int64_t>(256 / s.team, T)));
+  return s;
+}
+
+// The access that a row operand allows, in its place among the others'.
+uint32_t access_bits(int operand, const void* p, int64_t ld, bool bf16) {
+  const uintptr_t size = bf16 ? 2 : 4;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld) * size;
+  return (at % (8 * size) == 0 ? kWide : at % 4 == 0 ? kWords : kPlain) << 2 * operand;
+}
+uint32_t access_bits(int operand, const Rows& r, bool bf16) {
+  return access_bits(operand, r.p, r.p != nullptr ? r.ld : 0, bf16);
+}
+// Whether every operand allows whole groups and rows are made of them (an absent operand does).
+bool all_wide(uint32_t accesses, std::initializer_list<int> operands, int64_t d) {
+  for (int o : operands)
+    if (access_of(accesses, o) != kWide) return false;
+  return d % 8 == 0;
+}
+
+// The ring and, where an output is not aligned, the warps' stretches.
+constexpr int kRingBytes = 200 << 10;
+constexpr int kMaxStages = 4;
+constexpr int kStretch = 256 * int(sizeof(float));
+// Sets the stages that fit `budget` bytes and returns the dynamic shared bytes.
+int plan_ring(Plan* plan, int column_bytes, int groups, bool stretches, int64_t turns, int budget) {
+  const int threads = plan->shape.team * plan->shape.teams;
+  plan->stage_bytes = threads * groups * 8 * column_bytes;
+  const int extra = stretches ? threads / 32 * kStretch : 0;
+  plan->stages = std::max(1, std::min({kMaxStages, (budget - extra) / plan->stage_bytes,
+                                       int(std::min<int64_t>(turns, kMaxStages))}));
+  return plan->stages * plan->stage_bytes + extra;
+}
+
+template <class K>
+bool allow_ring(K* kernel, const Device& dev, PerContextOnce* once) {
+  return once->run(dev.ctx_id, [&] {
+           return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kRingBytes + (20 << 10));
+         }) == cudaSuccess;
+}
+
+// The types of the residual stream and of the activations, as template arguments.
+template <class F>
+lp_status with_types(bool residual_bf16, bool act_bf16, F&& f) {
+  if (residual_bf16) {
+    if (act_bf16) return f(__nv_bfloat16(), __nv_bfloat16());
+    return f(__nv_bfloat16(), float());
+  }
+  if (act_bf16) return f(float(), __nv_bfloat16());
+  return f(float(), float());
+}
+
+lp_status launched() { return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA; }
+
+}  // namespace
+}  // namespace lp

@@ -1,0 +1,444 @@
+// lp_norm_backward.cu: the backward pass of the residual norm (include/lp_train.h).  Bound by
+// HBM: 12 bytes a column in bfloat16.  lp_norm.cuh says how rows lie over threads and
+// come on chip.
+#include "lp_norm.cuh"
+
+namespace lp {
+namespace {
+
+// d up to kTeamDim: a CTA takes rows in turn and keeps its share of the sums over rows
+// (grad_weight, grad_branch_weight, a one-row gate's gradient) in registers.
+//
+// One round of sums a row: with e = b g w_b yh the second mean is linear in the first,
+//   mean(e D) = mean(e (dr' + rstd dx)) - mean(dx x) mean(e rstd x),
+// so the three sums are taken together.
+template <class R, class A, int G, bool kPost, bool kFast>
+__global__ void __launch_bounds__(kMaxTeam)
+    lp_residual_norm_grad_kernel(const __grid_constant__ NormGradArgs a, const Plan plan) {
+  constexpr int kSums = kPost ? 3 : 1;
+  __shared__ float slots[2][kMaxWarps][kSums];
+  extern __shared__ __align__(32) unsigned char ring[];
+  const Place p(a.d, plan.shape);
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  const bool norm = a.weight != nullptr, branch = a.branch.p != nullptr, gate = a.gate.p != nullptr;
+  const bool has_dr = a.grad_residual_out.p != nullptr, gate_sum = gate && a.gate.ld == 0;
+  float sum_w[G][8] = {}, sum_b[G][8] = {}, sum_g[G][8] = {};
+  const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
+  int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
+  if (!LP_CHECK(a.d <= a.grad_residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
+  // a stage: the rows of the stream, its gradient, the norm's gradient, the branch, the gate
+  Stream<R> s, dr;
+  Stream<A> dh, y, g;
+  int offset = 0;
+  if (norm) s.template start<kFast, G>(a.residual_out, t, step, p, ring, &offset);
+  if (has_dr) dr.template start<kFast, G>(a.grad_residual_out, t, step, p, ring, &offset);
+  if (norm) dh.template start<kFast, G>(a.grad_normed, t, step, p, ring, &offset);
+  if (branch) y.template start<kFast, G>(a.branch, t, step, p, ring, &offset);
+  if (gate) g.template start<kFast, G>(a.gate, t, step, p, ring, &offset);
+  void* stretch = ring + plan.stages * plan.stage_bytes + p.warp * kStretch;
+  const uint32_t accesses = plan.accesses;
+  int64_t next = t;  // the row that is fetched next
+  const auto fetch = [&](int stage) {
+    if (next - p.in_cta < a.T) {  // the CTA has a turn for it
+      const uint32_t at = stage * plan.stage_bytes;
+      const bool mine = next < a.T;
+      if (norm) s.template fetch<kFast, G>(at, mine, access_of(accesses, kOut), p);
+      if (has_dr) dr.template fetch<kFast, G>(at, mine, access_of(accesses, kGradOut), p);
+      if (norm) dh.template fetch<kFast, G>(at, mine, access_of(accesses, kGradNormed), p);
+      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p);
+      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p);
+    }
+    next += step;
+    commit_copies();
+  };
+  for (int n = 0; n + 1 < plan.stages; ++n) fetch(n);
+  const bool wide_w = access_of(accesses, kWeight) == kWide;
+  const bool wide_b = access_of(accesses, kBranchWeight) == kWide;
+  // with one group a thread the weights stay in registers
+  float w0[8], wb0[8];
+  if (G == 1 && norm) read_weight(a.weight, a.weight_bf16, 0, wide_w, p, w0);
+  if (G == 1 && kPost) read_weight(a.branch_weight, a.weight_bf16, 0, wide_b, p, wb0);
+  int stage = 0, turn = 0;
+  // every team runs as many turns as the CTA's first, so that all meet at the barriers
+  for (; t - p.in_cta < a.T; t += step, turn ^= 1) {
+    const int ahead = plan.stages - 1;
+    __syncwarp();  // the stage that is copied into has been read by the warp
+    fetch(stage == 0 ? ahead : stage - 1);
+    const bool mine = t < a.T;
+    const float root = norm && mine ? a.rstd[t] : 0.f;
+    const float root_y = kPost && mine ? a.branch_rstd[t] : 1.f;
+    wait_copies(ahead);
+    __syncwarp();
+    const uint32_t at = stage * plan.stage_bytes;
+    float x[G][8], D[G][8], m[kSums] = {};
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      if (has_dr) {
+        dr.get(at, k, D[k]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) D[k][e] = 0.f;
+      }
+      if (norm) {
+        float h[8], w[8];
+        s.get(at, k, x[k]);
+        dh.get(at, k, h);
+        if (G == 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = w0[e];
+        } else {
+          read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float dx = h[e] * w[e];
+          x[k][e] *= root;
+          m[0] = __fmaf_rn(dx, x[k][e], m[0]);
+          sum_w[k][e] = __fmaf_rn(h[e], x[k][e], sum_w[k][e]);
+          D[k][e] = __fmaf_rn(root, dx, D[k][e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+      }
+      if (kPost) {
+        float f[8], wb[8];
+        y.get(at, k, f);
+        if (G == 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
+        } else {
+          read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = a.branch_scale * (f[e] * root_y) * wb[e];
+        if (gate) {
+          g.get(at, k, wb);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= wb[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          m[1 % kSums] = __fmaf_rn(f[e], D[k][e], m[1 % kSums]);
+          m[2 % kSums] = __fmaf_rn(f[e], x[k][e], m[2 % kSums]);
+        }
+      }
+    }
+    if (norm || kPost) team_sum(m, slots[turn], p);
+    const float m1 = root * (m[0] * inv_d);  // rstd mean(dx x)
+    // mean(e D)
+    const float m2 = kPost ? __fmaf_rn(-m1, m[2 % kSums], m[1 % kSums]) * inv_d : 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      float out[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        D[k][e] = __fmaf_rn(-m1, x[k][e], D[k][e]);
+        out[e] = a.residual_scale * D[k][e];
+      }
+      write_group<kFast, R>(a.grad_residual, t, k, mine, access_of(accesses, kGradResidual), p, stretch, out);
+      if (!branch) continue;
+      float yh[8], wb[8];
+      if (kPost || gate) {
+        y.get(at, k, yh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) yh[e] *= root_y;
+      }
+      if (kPost) {
+        if (G == 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
+        } else {
+          read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = a.branch_scale * D[k][e];
+      if (gate) {
+        float f[8], dg[8];
+        g.get(at, k, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dg[e] = out[e] * (kPost ? yh[e] * wb[e] : yh[e]);
+          if (gate_sum) sum_g[k][e] += dg[e];
+          out[e] *= f[e];
+        }
+        if (!gate_sum && a.grad_gate.p != nullptr)
+          write_group<kFast, A>(a.grad_gate, t, k, mine, access_of(accesses, kGradGate), p, stretch, dg);
+      }
+      if (kPost) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum_b[k][e] = __fmaf_rn(out[e], yh[e], sum_b[k][e]);
+          out[e] = root_y * __fmaf_rn(out[e], wb[e], -(yh[e] * m2));
+        }
+      }
+      write_group<kFast, A>(a.grad_branch, t, k, mine, access_of(accesses, kGradBranch), p, stretch, out);
+    }
+    stage = stage + 1 == plan.stages ? 0 : stage + 1;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.partials == nullptr) return;
+  // the teams' sums in order, then the CTA's [3][d]
+  float* shared = reinterpret_cast<float*>(ring);  // all copies have been waited for
+  float* part = a.partials + int64_t(blockIdx.x) * 3 * a.d;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    float(&sum)[G][8] = q == 0 ? sum_w : q == 1 ? sum_b : sum_g;
+    if (q == 0 ? a.grad_weight == nullptr : q == 1 ? a.grad_branch_weight == nullptr : !gate_sum)
+      continue;
+    for (int from = 1; from < plan.shape.teams; ++from) {
+      __syncthreads();
+      if (p.in_cta == from)
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) shared[(k * p.team + p.i) * 8 + e] = sum[k][e];
+      __syncthreads();
+      if (p.in_cta == 0)
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[k][e] += shared[(k * p.team + p.i) * 8 + e];
+    }
+    if (p.in_cta == 0)
+#pragma unroll
+      for (int k = 0; k < G; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = 8 * int64_t(p.i + k * p.team) + e;
+          if (c < a.d) part[q * a.d + c] = sum[k][e];
+        }
+  }
+}
+
+// Backward of rows wider than that: the row is read twice (the second time from L2) and the
+// sums over rows lie in shared memory, where each column has one owner.
+constexpr int kWideThreads = 1024;
+
+template <class T>
+__device__ __forceinline__ T* row_of(const Rows& r, int64_t t) {
+  return static_cast<T*>(r.p) + t * r.ld;
+}
+__device__ __forceinline__ float get(const float* p, int64_t i) { return p[i]; }
+__device__ __forceinline__ float get(const __nv_bfloat16* p, int64_t i) {
+  return __bfloat162float(p[i]);
+}
+__device__ __forceinline__ void put(float* p, int64_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, int64_t i, float v) {
+  p[i] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ float weight_at(const void* w, bool bf16, int64_t i) {
+  return bf16 ? get(static_cast<const __nv_bfloat16*>(w), i) : get(static_cast<const float*>(w), i);
+}
+
+// Three sums over the CTA, the same bits for all threads.
+__device__ __forceinline__ void wide_sum(float (&v)[3], float (*slots)[3]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) slots[threadIdx.x / 32][k] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) v[k] = slots[threadIdx.x & 31][k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
+
+template <class R, class A>
+__global__ void __launch_bounds__(kWideThreads)
+    lp_residual_norm_grad_wide_kernel(const __grid_constant__ NormGradArgs a) {
+  extern __shared__ float sums[];
+  __shared__ float slots[2][kWideThreads / 32][3];
+  const int64_t d = a.d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const bool post = a.branch_weight != nullptr, norm = a.weight != nullptr;
+  for (int64_t c = threadIdx.x; c < d; c += kWideThreads)
+    sums[c] = sums[d + c] = sums[2 * d + c] = 0.f;
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    const R* s = norm ? row_of<const R>(a.residual_out, t) : nullptr;
+    const A* y = a.branch.p ? row_of<const A>(a.branch, t) : nullptr;
+    const A* g = a.gate.p ? row_of<const A>(a.gate, t) : nullptr;
+    const A* dh = norm ? row_of<const A>(a.grad_normed, t) : nullptr;
+    const R* dr = a.grad_residual_out.p ? row_of<const R>(a.grad_residual_out, t) : nullptr;
+    const float root = norm ? a.rstd[t] : 0.f, root_y = post ? a.branch_rstd[t] : 1.f;
+    float m[3] = {0.f, 0.f, 0.f};
+    for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
+      const float x = norm ? get(s, c) * root : 0.f;
+      const float dx = norm ? get(dh, c) * weight_at(a.weight, a.weight_bf16, c) : 0.f;
+      m[0] += dx * x;
+      if (post) {
+        float f = a.branch_scale * weight_at(a.branch_weight, a.weight_bf16, c);
+        if (g != nullptr) f *= get(g, c);
+        f *= get(y, c) * root_y;
+        m[1] += f * ((dr != nullptr ? get(dr, c) : 0.f) + root * dx);
+        m[2] += f * (root * x);
+      }
+    }
+    if (norm || post) wide_sum(m, slots[turn]);
+    const float m1 = m[0] * inv_d, m2 = (m[1] - m1 * m[2]) * inv_d;
+    for (int64_t c = threadIdx.x; c < d; c += kWideThreads) {
+      float D = dr != nullptr ? get(dr, c) : 0.f;
+      if (norm) {
+        const float x = get(s, c) * root, h = get(dh, c);
+        D += root * (h * weight_at(a.weight, a.weight_bf16, c) - x * m1);
+        sums[c] += h * x;
+      }
+      put(row_of<R>(a.grad_residual, t), c, a.residual_scale * D);
+      if (y == nullptr) continue;
+      const float yh = get(y, c) * root_y;
+      const float wb = post ? weight_at(a.branch_weight, a.weight_bf16, c) : 1.f;
+      float dn = a.branch_scale * D;
+      if (g != nullptr) {
+        const float dg = dn * (yh * wb);
+        if (a.gate.ld == 0)
+          sums[2 * d + c] += dg;
+        else if (a.grad_gate.p != nullptr)
+          put(row_of<A>(a.grad_gate, t), c, dg);
+        dn *= get(g, c);
+      }
+      if (post) {
+        sums[d + c] += dn * yh;
+        dn = root_y * (dn * wb - yh * m2);
+      }
+      put(row_of<A>(a.grad_branch, t), c, dn);
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.partials == nullptr) return;
+  float* part = a.partials + int64_t(blockIdx.x) * 3 * d;
+  for (int64_t c = threadIdx.x; c < d; c += kWideThreads)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) part[q * d + c] = sums[q * d + c];
+}
+
+// The CTAs' partial sums: 8 threads a column take every eighth part in order, and their
+// sums are added in order.
+constexpr int kSumLanes = 8;
+__global__ void __launch_bounds__(32 * kSumLanes)
+    lp_norm_sum_kernel(const float* partials, int64_t parts, int64_t d, float* grad_weight,
+                       float* grad_branch_weight, float* grad_gate) {
+  __shared__ float slots[kSumLanes][32];
+  float* const out = blockIdx.y == 0 ? grad_weight : blockIdx.y == 1 ? grad_branch_weight : grad_gate;
+  if (out == nullptr) return;
+  const int lane = threadIdx.x & 31, from = threadIdx.x / 32;
+  const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  // launched as a programmatic dependent of the row kernel: wait for its partial sums
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float s = 0.f;
+  if (c < d)
+    for (int64_t p = from; p < parts; p += kSumLanes) s += partials[(p * 3 + blockIdx.y) * d + c];
+  slots[from][lane] = s;
+  __syncthreads();
+  if (from != 0 || c >= d) return;
+  for (int k = 1; k < kSumLanes; ++k) s += slots[k][lane];
+  out[c] = s;
+}
+
+// The rows that the CTAs take at once, and how many CTAs there are.
+constexpr int64_t kTeamDim = kMaxTeam * 8 * 2;  // the widest row of the team kernel
+int groups_of(int64_t d) { return d <= kTeamDim / 2 ? 1 : 2; }
+int64_t backward_blocks(int64_t T, int64_t d) {
+  const int64_t at_once = d <= kTeamDim ? shape_of(d, groups_of(d), T).teams : 1;
+  return std::min((T + at_once - 1) / at_once, kSlots);
+}
+
+template <int G>
+lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t accesses, bool fast,
+                          int64_t blocks, cudaStream_t stream) {
+  return with_types(a.residual_bf16, a.act_bf16, [&](auto r, auto x) {
+    using R = decltype(r);
+    using A = decltype(x);
+    const auto launch = [&](auto* kernel, PerContextOnce* once) {
+      if (!allow_ring(kernel, dev, once)) return LP_ERR_CUDA;
+      Plan plan{shape_of(a.d, G, a.T), accesses, 1, 0};
+      const int columns = (a.weight ? int(sizeof(R) + sizeof(A)) : 0) +
+                          (a.grad_residual_out.p ? int(sizeof(R)) : 0) +
+                          (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
+      const int64_t at_once = blocks * plan.shape.teams;
+      int smem = plan_ring(&plan, columns, G, !fast, (a.T + at_once - 1) / at_once, kRingBytes);
+      if (plan.shape.teams > 1) smem = std::max(smem, plan.shape.team * G * 8 * int(sizeof(float)));
+      kernel<<<unsigned(blocks), plan.shape.team * plan.shape.teams, smem, stream>>>(a, plan);
+      return launched();
+    };
+    static PerContextOnce once[4];
+    if (a.branch_weight != nullptr)
+      return fast ? launch(lp_residual_norm_grad_kernel<R, A, G, true, true>, &once[0])
+                  : launch(lp_residual_norm_grad_kernel<R, A, G, true, false>, &once[1]);
+    return fast ? launch(lp_residual_norm_grad_kernel<R, A, G, false, true>, &once[2])
+                : launch(lp_residual_norm_grad_kernel<R, A, G, false, false>, &once[3]);
+  });
+}
+
+lp_status launch_backward_wide(const Device& dev, const NormGradArgs& a, int64_t blocks,
+                               cudaStream_t stream) {
+  return with_types(a.residual_bf16, a.act_bf16, [&](auto r, auto x) {
+    auto* kernel = lp_residual_norm_grad_wide_kernel<decltype(r), decltype(x)>;
+    static PerContextOnce once;
+    if (once.run(dev.ctx_id, [&] {
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      int(kNormMaxDim * 12));
+        }) != cudaSuccess)
+      return LP_ERR_CUDA;
+    kernel<<<unsigned(blocks), kWideThreads, size_t(a.d) * 12, stream>>>(a);
+    return launched();
+  });
+}
+
+}  // namespace
+
+size_t residual_norm_backward_workspace(int64_t T, int64_t d) {
+  return static_cast<size_t>(std::max<int64_t>(1, backward_blocks(std::max<int64_t>(T, 1), d)) * 3 *
+                             d * 4);
+}
+
+lp_status launch_residual_norm_backward(const Device& dev, const NormGradArgs& a,
+                                        cudaStream_t stream) {
+  const int64_t blocks = a.T > 0 ? backward_blocks(a.T, a.d) : 0;
+  if (blocks > 0) {
+    const uint32_t accesses = access_bits(kOut, a.residual_out, a.residual_bf16) |
+                              access_bits(kBranch, a.branch, a.act_bf16) |
+                              access_bits(kGate, a.gate, a.act_bf16) |
+                              access_bits(kBranchWeight, a.branch_weight, 0, a.weight_bf16) |
+                              access_bits(kWeight, a.weight, 0, a.weight_bf16) |
+                              access_bits(kGradNormed, a.grad_normed, a.act_bf16) |
+                              access_bits(kGradOut, a.grad_residual_out, a.residual_bf16) |
+                              access_bits(kGradResidual, a.grad_residual, a.residual_bf16) |
+                              access_bits(kGradBranch, a.grad_branch, a.act_bf16) |
+                              access_bits(kGradGate, a.grad_gate, a.act_bf16);
+    const bool fast = all_wide(accesses,
+                               {kOut, kBranch, kGate, kGradNormed, kGradOut, kGradResidual, kGradBranch,
+                                kGradGate},
+                               a.d);
+    const lp_status st = a.d > kTeamDim        ? launch_backward_wide(dev, a, blocks, stream)
+                         : groups_of(a.d) == 1 ? launch_backward<1>(dev, a, accesses, fast, blocks, stream)
+                                               : launch_backward<2>(dev, a, accesses, fast, blocks, stream);
+    if (st != LP_OK) return st;
+  }
+  float* gate_sum = a.gate.ld == 0 ? static_cast<float*>(a.grad_gate.p) : nullptr;
+  if (a.grad_weight == nullptr && a.grad_branch_weight == nullptr && gate_sum == nullptr)
+    return LP_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((a.d + 31) / 32), 3);
+  cfg.blockDim = dim3(32 * kSumLanes);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = blocks > 0 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, lp_norm_sum_kernel, static_cast<const float*>(a.partials), blocks, a.d,
+                         a.grad_weight, a.grad_branch_weight, gate_sum) != cudaSuccess)
+    return LP_ERR_CUDA;
+  return launched();
+}
+
+cudaError_t take_check_word_norm_backward(uint32_t* out) { return take_check_word(out); }
+
+}  // namespace lp

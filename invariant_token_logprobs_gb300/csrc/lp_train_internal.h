@@ -113,6 +113,7 @@ lp_status launch_adamw_state_values(const void* exp_avg, const void* exp_avg_sq,
 
 // Read and clear the check words of these translation units (lp_check.cuh).
 cudaError_t take_check_word_norm(uint32_t* out);
+cudaError_t take_check_word_norm_backward(uint32_t* out);
 cudaError_t take_check_word_policy(uint32_t* out);
 cudaError_t take_check_word_adamw(uint32_t* out);
 
