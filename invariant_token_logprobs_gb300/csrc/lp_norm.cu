@@ -30,9 +30,9 @@ __global__ void __launch_bounds__(kMaxTeam)
     if (next - p.in_cta < a.T) {  // the CTA has a turn for it
       const uint32_t at = stage * plan.stage_bytes;
       const bool mine = next < a.T;
-      residual.template fetch<kFast, G>(at, mine, access_of(accesses, kResidual), p);
-      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p);
-      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p);
+      residual.template fetch<kFast, G>(at, mine, access_of(accesses, kResidual), p, a.residual.p);
+      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p, a.branch.p);
+      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p, a.gate.p);
     }
     next += step;
     commit_copies();
@@ -120,7 +120,7 @@ lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses
       const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
       const int64_t blocks = std::min<int64_t>(all, kSlots * (1024 / threads));
       const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
-      const int smem = plan_ring(&plan, columns, G, !fast, (all + blocks - 1) / blocks,
+      const int smem = plan_ring(&plan, columns, G, !fast, (all + blocks - 1) / blocks, 1,
                                  std::max(kForwardBudget * threads / 256, threads * G * 8 * columns));
       kernel<<<unsigned(blocks), threads, smem, stream>>>(a, plan);
       return launched();

@@ -151,7 +151,10 @@ struct Stream {
   // Starts the copy of the next row's groups into the stage `at` bytes on; zeros where the team
   // has no row (or past its columns), as a row of zeros adds nothing to any sum.
   template <bool kFast, int G>
-  __device__ __forceinline__ void fetch(uint32_t at, bool mine, uint32_t access, const Place& p) {
+  // `base`: an address in the operand, for copies of no bytes.
+  __device__ __forceinline__ void fetch(uint32_t at, bool mine, uint32_t access, const Place& p,
+                                        const void* base) {
+    const T* none = static_cast<const T*>(base);
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       const uint32_t to = slot + at + k * int(blockDim.x) * 8 * int(sizeof(T));
@@ -161,7 +164,7 @@ struct Stream {
 #pragma unroll
         for (int q = 0; q < int(sizeof(T)) / 2; ++q)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * q),
-                       "l"(bytes ? row + k * p.team * 8 + q * (16 / int(sizeof(T))) : row), "r"(bytes)
+                       "l"(bytes ? row + k * p.team * 8 + q * (16 / int(sizeof(T))) : none), "r"(bytes)
                        : "memory");
         continue;
       }
@@ -177,7 +180,7 @@ struct Stream {
           const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                            stretch + e * int(sizeof(T))),
-                       "l"(bytes ? row + first + e : row), "r"(bytes)
+                       "l"(bytes ? row + first + e : none), "r"(bytes)
                        : "memory");
         }
       } else {
@@ -334,13 +337,15 @@ bool all_wide(uint32_t accesses, std::initializer_list<int> operands, int64_t d)
 constexpr int kRingBytes = 200 << 10;
 constexpr int kMaxStages = 4;
 constexpr int kStretch = 256 * int(sizeof(float));
-// Sets the stages that fit `budget` bytes and returns the dynamic shared bytes.
-int plan_ring(Plan* plan, int column_bytes, int groups, bool stretches, int64_t turns, int budget) {
+// Sets the stages, of one row a team, that fit `budget` bytes, at least `least`, and returns the
+// dynamic shared bytes.  `rows`: that a team takes in all.
+int plan_ring(Plan* plan, int column_bytes, int groups, bool stretches, int64_t rows, int least,
+              int budget) {
   const int threads = plan->shape.team * plan->shape.teams;
   plan->stage_bytes = threads * groups * 8 * column_bytes;
   const int extra = stretches ? threads / 32 * kStretch : 0;
-  plan->stages = std::max(1, std::min({kMaxStages, (budget - extra) / plan->stage_bytes,
-                                       int(std::min<int64_t>(turns, kMaxStages))}));
+  plan->stages = std::max(least, std::min({kMaxStages, (budget - extra) / plan->stage_bytes,
+                                           int(std::min<int64_t>(rows, kMaxStages))}));
   return plan->stages * plan->stage_bytes + extra;
 }
 

@@ -6,17 +6,27 @@
 namespace lp {
 namespace {
 
+// Floats from one sum of a CTA to the next in the workspace: whole groups.
+__host__ __device__ __forceinline__ int64_t pitch_of(int64_t d) { return (d + 7) / 8 * 8; }
+
 // d up to kTeamDim: a CTA takes rows in turn and keeps its share of the sums over rows
 // (grad_weight, grad_branch_weight, a one-row gate's gradient) in registers.
 //
 // One round of sums a row: with e = b g w_b yh the second mean is linear in the first,
 //   mean(e D) = mean(e (dr' + rstd dx)) - mean(dx x) mean(e rstd x),
 // so the three sums are taken together.
+//
+// Where the registers and the ring allow, a team takes two rows a turn: their waits for the
+// team are one, and the work of one hides the latencies of the other.
+template <class R, class A, int G>
+constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) <= 6 ? 2 : 1;
+
 template <class R, class A, int G, bool kPost, bool kFast>
 __global__ void __launch_bounds__(kMaxTeam)
     lp_residual_norm_grad_kernel(const __grid_constant__ NormGradArgs a, const Plan plan) {
   constexpr int kSums = kPost ? 3 : 1;
-  __shared__ float slots[2][kMaxWarps][kSums];
+  constexpr int kRows = kRowsATurn<R, A, G>;
+  __shared__ float slots[2][kMaxWarps][kRows * kSums];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
@@ -42,146 +52,188 @@ __global__ void __launch_bounds__(kMaxTeam)
     if (next - p.in_cta < a.T) {  // the CTA has a turn for it
       const uint32_t at = stage * plan.stage_bytes;
       const bool mine = next < a.T;
-      if (norm) s.template fetch<kFast, G>(at, mine, access_of(accesses, kOut), p);
-      if (has_dr) dr.template fetch<kFast, G>(at, mine, access_of(accesses, kGradOut), p);
-      if (norm) dh.template fetch<kFast, G>(at, mine, access_of(accesses, kGradNormed), p);
-      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p);
-      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p);
+      if (norm) s.template fetch<kFast, G>(at, mine, access_of(accesses, kOut), p, a.residual_out.p);
+      if (has_dr) dr.template fetch<kFast, G>(at, mine, access_of(accesses, kGradOut), p, a.grad_residual_out.p);
+      if (norm) dh.template fetch<kFast, G>(at, mine, access_of(accesses, kGradNormed), p, a.grad_normed.p);
+      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p, a.branch.p);
+      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p, a.gate.p);
     }
     next += step;
     commit_copies();
   };
-  for (int n = 0; n + 1 < plan.stages; ++n) fetch(n);
+  for (int n = 0; n + kRows < plan.stages; ++n) fetch(n);
   const bool wide_w = access_of(accesses, kWeight) == kWide;
   const bool wide_b = access_of(accesses, kBranchWeight) == kWide;
   // with one group a thread the weights stay in registers
   float w0[8], wb0[8];
   if (G == 1 && norm) read_weight(a.weight, a.weight_bf16, 0, wide_w, p, w0);
   if (G == 1 && kPost) read_weight(a.branch_weight, a.weight_bf16, 0, wide_b, p, wb0);
+  // the rows' roots, loaded a turn ahead
+  float root[kRows], root_y[kRows];
+  const auto load_roots = [&](int64_t first) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const bool mine = first + j * step < a.T;
+      root[j] = norm && mine ? a.rstd[first + j * step] : 0.f;
+      root_y[j] = kPost && mine ? a.branch_rstd[first + j * step] : 1.f;
+    }
+  };
+  load_roots(t);
   int stage = 0, turn = 0;
   // every team runs as many turns as the CTA's first, so that all meet at the barriers
-  for (; t - p.in_cta < a.T; t += step, turn ^= 1) {
-    const int ahead = plan.stages - 1;
-    __syncwarp();  // the stage that is copied into has been read by the warp
-    fetch(stage == 0 ? ahead : stage - 1);
-    const bool mine = t < a.T;
-    const float root = norm && mine ? a.rstd[t] : 0.f;
-    const float root_y = kPost && mine ? a.branch_rstd[t] : 1.f;
-    wait_copies(ahead);
+  for (; t - p.in_cta < a.T; t += kRows * step, turn ^= 1) {
+    __syncwarp();  // the stages that are copied into have been read by the warp
+    int to = stage - kRows;
+    if (to < 0) to += plan.stages;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      fetch(to);
+      if (++to == plan.stages) to = 0;
+    }
+    wait_copies(plan.stages - kRows);
     __syncwarp();
-    const uint32_t at = stage * plan.stage_bytes;
-    float x[G][8], D[G][8], m[kSums] = {};
+    uint32_t at[kRows];
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-      if (has_dr) {
-        dr.get(at, k, D[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) D[k][e] = 0.f;
-      }
-      if (norm) {
-        float h[8], w[8];
-        s.get(at, k, x[k]);
-        dh.get(at, k, h);
-        if (G == 1) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = w0[e];
-        } else {
-          read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float dx = h[e] * w[e];
-          x[k][e] *= root;
-          m[0] = __fmaf_rn(dx, x[k][e], m[0]);
-          sum_w[k][e] = __fmaf_rn(h[e], x[k][e], sum_w[k][e]);
-          D[k][e] = __fmaf_rn(root, dx, D[k][e]);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-      }
-      if (kPost) {
-        float f[8], wb[8];
-        y.get(at, k, f);
-        if (G == 1) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
-        } else {
-          read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = a.branch_scale * (f[e] * root_y) * wb[e];
-        if (gate) {
-          g.get(at, k, wb);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= wb[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          m[1 % kSums] = __fmaf_rn(f[e], D[k][e], m[1 % kSums]);
-          m[2 % kSums] = __fmaf_rn(f[e], x[k][e], m[2 % kSums]);
-        }
-      }
+    for (int j = 0; j < kRows; ++j) {
+      at[j] = stage * plan.stage_bytes;
+      if (++stage == plan.stages) stage = 0;
     }
+    float x[kRows][G][8], D[kRows][G][8], m[kRows * kSums] = {};
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        float(&xk)[8] = x[j][k];
+        float(&Dk)[8] = D[j][k];
+        if (j > 0 && t + j * step - p.in_cta >= a.T) {  // no team has the row: nothing was copied
+#pragma unroll
+          for (int e = 0; e < 8; ++e) Dk[e] = xk[e] = 0.f;
+          continue;
+        }
+        if (has_dr) {
+          dr.get(at[j], k, Dk);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) Dk[e] = 0.f;
+        }
+        if (norm) {
+          float h[8], w[8];
+          s.get(at[j], k, xk);
+          dh.get(at[j], k, h);
+          if (G == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = w0[e];
+          } else {
+            read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float dx = h[e] * w[e];
+            xk[e] *= root[j];
+            m[j * kSums] = __fmaf_rn(dx, xk[e], m[j * kSums]);
+            sum_w[k][e] = __fmaf_rn(h[e], xk[e], sum_w[k][e]);
+            Dk[e] = __fmaf_rn(root[j], dx, Dk[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xk[e] = 0.f;
+        }
+        if (kPost) {
+          float f[8], wb[8];
+          y.get(at[j], k, f);
+          if (G == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
+          } else {
+            read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = a.branch_scale * (f[e] * root_y[j]) * wb[e];
+          if (gate) {
+            g.get(at[j], k, wb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= wb[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            m[j * kSums + 1 % kSums] = __fmaf_rn(f[e], Dk[e], m[j * kSums + 1 % kSums]);
+            m[j * kSums + 2 % kSums] = __fmaf_rn(f[e], xk[e], m[j * kSums + 2 % kSums]);
+          }
+        }
+      }
     if (norm || kPost) team_sum(m, slots[turn], p);
-    const float m1 = root * (m[0] * inv_d);  // rstd mean(dx x)
-    // mean(e D)
-    const float m2 = kPost ? __fmaf_rn(-m1, m[2 % kSums], m[1 % kSums]) * inv_d : 0.f;
+    float m1[kRows], m2[kRows], scale_y[kRows];
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-      float out[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        D[k][e] = __fmaf_rn(-m1, x[k][e], D[k][e]);
-        out[e] = a.residual_scale * D[k][e];
-      }
-      write_group<kFast, R>(a.grad_residual, t, k, mine, access_of(accesses, kGradResidual), p, stretch, out);
-      if (!branch) continue;
-      float yh[8], wb[8];
-      if (kPost || gate) {
-        y.get(at, k, yh);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) yh[e] *= root_y;
-      }
-      if (kPost) {
-        if (G == 1) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
-        } else {
-          read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = a.branch_scale * D[k][e];
-      if (gate) {
-        float f[8], dg[8];
-        g.get(at, k, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dg[e] = out[e] * (kPost ? yh[e] * wb[e] : yh[e]);
-          if (gate_sum) sum_g[k][e] += dg[e];
-          out[e] *= f[e];
-        }
-        if (!gate_sum && a.grad_gate.p != nullptr)
-          write_group<kFast, A>(a.grad_gate, t, k, mine, access_of(accesses, kGradGate), p, stretch, dg);
-      }
-      if (kPost) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum_b[k][e] = __fmaf_rn(out[e], yh[e], sum_b[k][e]);
-          out[e] = root_y * __fmaf_rn(out[e], wb[e], -(yh[e] * m2));
-        }
-      }
-      write_group<kFast, A>(a.grad_branch, t, k, mine, access_of(accesses, kGradBranch), p, stretch, out);
+    for (int j = 0; j < kRows; ++j) {
+      m1[j] = root[j] * (m[j * kSums] * inv_d);  // rstd mean(dx x)
+      // mean(e D)
+      m2[j] = kPost ? __fmaf_rn(-m1[j], m[j * kSums + 2 % kSums], m[j * kSums + 1 % kSums]) * inv_d : 0.f;
+      scale_y[j] = root_y[j];
     }
-    stage = stage + 1 == plan.stages ? 0 : stage + 1;
+    load_roots(t + kRows * step);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t row = t + j * step;
+      const bool mine = row < a.T;
+      if (j > 0 && row - p.in_cta >= a.T) continue;  // no team has it
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        float(&Dk)[8] = D[j][k];
+        float out[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          Dk[e] = __fmaf_rn(-m1[j], x[j][k][e], Dk[e]);
+          out[e] = a.residual_scale * Dk[e];
+        }
+        write_group<kFast, R>(a.grad_residual, row, k, mine, access_of(accesses, kGradResidual), p,
+                              stretch, out);
+        if (!branch) continue;
+        float yh[8], wb[8];
+        if (kPost || gate) {
+          y.get(at[j], k, yh);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) yh[e] *= scale_y[j];
+        }
+        if (kPost) {
+          if (G == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
+          } else {
+            read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = a.branch_scale * Dk[e];
+        if (gate) {
+          float f[8], dg[8];
+          g.get(at[j], k, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dg[e] = out[e] * (kPost ? yh[e] * wb[e] : yh[e]);
+            if (gate_sum) sum_g[k][e] += dg[e];
+            out[e] *= f[e];
+          }
+          if (!gate_sum && a.grad_gate.p != nullptr)
+            write_group<kFast, A>(a.grad_gate, row, k, mine, access_of(accesses, kGradGate), p,
+                                  stretch, dg);
+        }
+        if (kPost) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum_b[k][e] = __fmaf_rn(out[e], yh[e], sum_b[k][e]);
+            out[e] = scale_y[j] * __fmaf_rn(out[e], wb[e], -(yh[e] * m2[j]));
+          }
+        }
+        write_group<kFast, A>(a.grad_branch, row, k, mine, access_of(accesses, kGradBranch), p,
+                              stretch, out);
+      }
+    }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partials == nullptr) return;
-  // the teams' sums in order, then the CTA's [3][d]
+  // the teams' sums in order, then the CTA's, three rows of whole groups
   float* shared = reinterpret_cast<float*>(ring);  // all copies have been waited for
-  float* part = a.partials + int64_t(blockIdx.x) * 3 * a.d;
+  float* part = a.partials + int64_t(blockIdx.x) * 3 * pitch_of(a.d);
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
     float(&sum)[G][8] = q == 0 ? sum_w : q == 1 ? sum_b : sum_g;
@@ -203,12 +255,10 @@ __global__ void __launch_bounds__(kMaxTeam)
     }
     if (p.in_cta == 0)
 #pragma unroll
-      for (int k = 0; k < G; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = 8 * int64_t(p.i + k * p.team) + e;
-          if (c < a.d) part[q * a.d + c] = sum[k][e];
-        }
+      for (int k = 0; k < G; ++k) {
+        const int c = 8 * (p.i + k * p.team);
+        if (c < p.d) store_group(part + q * pitch_of(a.d) + c, pack(sum[k], float()));
+      }
   }
 }
 
@@ -312,15 +362,15 @@ __global__ void __launch_bounds__(kWideThreads)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partials == nullptr) return;
-  float* part = a.partials + int64_t(blockIdx.x) * 3 * d;
+  float* part = a.partials + int64_t(blockIdx.x) * 3 * pitch_of(d);
   for (int64_t c = threadIdx.x; c < d; c += kWideThreads)
 #pragma unroll
-    for (int q = 0; q < 3; ++q) part[q * d + c] = sums[q * d + c];
+    for (int q = 0; q < 3; ++q) part[q * pitch_of(d) + c] = sums[q * d + c];
 }
 
-// The CTAs' partial sums: 8 threads a column take every eighth part in order, and their
+// The CTAs' partial sums: 16 threads a column take every sixteenth part in order, and their
 // sums are added in order.
-constexpr int kSumLanes = 8;
+constexpr int kSumLanes = 16;
 __global__ void __launch_bounds__(32 * kSumLanes)
     lp_norm_sum_kernel(const float* partials, int64_t parts, int64_t d, float* grad_weight,
                        float* grad_branch_weight, float* grad_gate) {
@@ -328,15 +378,19 @@ __global__ void __launch_bounds__(32 * kSumLanes)
   float* const out = blockIdx.y == 0 ? grad_weight : blockIdx.y == 1 ? grad_branch_weight : grad_gate;
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, from = threadIdx.x / 32;
-  const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+  const int64_t c = int64_t(blockIdx.x) * 32 + lane, pitch = pitch_of(d);
   // launched as a programmatic dependent of the row kernel: wait for its partial sums
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.f;
-  if (c < d)
-    for (int64_t p = from; p < parts; p += kSumLanes) s += partials[(p * 3 + blockIdx.y) * d + c];
+  if (c < d) {
+    const float* p = partials + (int64_t(from) * 3 + blockIdx.y) * pitch + c;
+#pragma unroll 4
+    for (int64_t k = from; k < parts; k += kSumLanes, p += 3 * kSumLanes * pitch) s += __ldcg(p);
+  }
   slots[from][lane] = s;
   __syncthreads();
   if (from != 0 || c >= d) return;
+#pragma unroll
   for (int k = 1; k < kSumLanes; ++k) s += slots[k][lane];
   out[c] = s;
 }
@@ -344,9 +398,12 @@ __global__ void __launch_bounds__(32 * kSumLanes)
 // The rows that the CTAs take at once, and how many CTAs there are.
 constexpr int64_t kTeamDim = kMaxTeam * 8 * 2;  // the widest row of the team kernel
 int groups_of(int64_t d) { return d <= kTeamDim / 2 ? 1 : 2; }
+// CTAs of an SM: two where a row takes no more than half of its threads.
+int ctas_of_sm(int threads) { return threads <= kMaxTeam / 2 ? 2 : 1; }
 int64_t backward_blocks(int64_t T, int64_t d) {
-  const int64_t at_once = d <= kTeamDim ? shape_of(d, groups_of(d), T).teams : 1;
-  return std::min((T + at_once - 1) / at_once, kSlots);
+  if (d > kTeamDim) return std::min(T, kSlots);
+  const Shape s = shape_of(d, groups_of(d), T);
+  return std::min((T + s.teams - 1) / s.teams, kSlots * ctas_of_sm(s.team * s.teams));
 }
 
 template <int G>
@@ -362,7 +419,9 @@ lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t acc
                           (a.grad_residual_out.p ? int(sizeof(R)) : 0) +
                           (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
       const int64_t at_once = blocks * plan.shape.teams;
-      int smem = plan_ring(&plan, columns, G, !fast, (a.T + at_once - 1) / at_once, kRingBytes);
+      int smem = plan_ring(&plan, columns, G, !fast, (a.T + at_once - 1) / at_once,
+                           kRowsATurn<R, A, G>,
+                           kRingBytes / ctas_of_sm(plan.shape.team * plan.shape.teams));
       if (plan.shape.teams > 1) smem = std::max(smem, plan.shape.team * G * 8 * int(sizeof(float)));
       kernel<<<unsigned(blocks), plan.shape.team * plan.shape.teams, smem, stream>>>(a, plan);
       return launched();
@@ -395,7 +454,7 @@ lp_status launch_backward_wide(const Device& dev, const NormGradArgs& a, int64_t
 
 size_t residual_norm_backward_workspace(int64_t T, int64_t d) {
   return static_cast<size_t>(std::max<int64_t>(1, backward_blocks(std::max<int64_t>(T, 1), d)) * 3 *
-                             d * 4);
+                             pitch_of(d) * 4);
 }
 
 lp_status launch_residual_norm_backward(const Device& dev, const NormGradArgs& a,
