@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include "lp_check.cuh"
+#include "lp_device.cuh"
 #include "lp_train_internal.h"
 
 namespace lp {
@@ -14,29 +15,65 @@ constexpr int kRow = LP_ADAMW_ALIGN;    // state elements of a CTA
 constexpr int kBlock = LP_ADAMW_BLOCK;  // elements of a warp, with one scale
 static_assert(kRow == kBlock * kThreads / 32, "one block of elements a warp");
 
+template <int j>
+struct Byte {
+  static constexpr int value = j;
+};
+
 // The magnitude codes of 8-bit moments: code c > 0 is the float of bits (c + kFirst) << kShift.
+// The code of a float is its own leading bits, so both ways are a few integer operations on
+// bytes where they lie in a word of four.
 template <bool kSigned>
 struct Code {
   static constexpr int kShift = kSigned ? 20 : 19;
-  static constexpr int kFirst = kSigned ? 889 : 1777;
-  // the lowest code's value over 2^kShift: what a random number below 2^kShift is scaled
-  // by to round a magnitude below that value to it or to zero
+  static constexpr uint32_t kFirst = kSigned ? 889 : 1777;
+  static constexpr uint32_t kMask = kSigned ? 127 : 255;
+  static constexpr uint32_t kLowest = (kFirst + 1) << kShift;  // bits of the value of code 1
+  // that value over 2^kShift: what a random number below 2^kShift is scaled by to round a
+  // magnitude below that value to it or to zero
   static constexpr float kLow = kSigned ? 0x1.4p-36f : 0x1.2p-35f;
 
-  static __device__ __forceinline__ float decode(uint32_t byte, float scale) {
-    const uint32_t c = kSigned ? byte & 127u : byte;
-    float v = c > 0 ? __uint_as_float((c + kFirst) << kShift) : 0.f;
-    if (kSigned && byte >= 128u) v = -v;
-    return v * scale;
+  // byte j of the word
+  template <int j>
+  static __device__ __forceinline__ float decode(uint32_t word, float scale) {
+    constexpr int left = kShift - 8 * j;
+    const uint32_t moved = left >= 0 ? word << (left >= 0 ? left : 0) : word >> (left < 0 ? -left : 0);
+    uint32_t bits = (moved & kMask << kShift) + (kFirst << kShift);
+    if (kSigned) bits |= word << (24 - 8 * j) & 0x80000000u;
+    return (word & kMask << 8 * j) != 0 ? __uint_as_float(bits) * scale : 0.f * scale;
   }
-  // x over the block's largest magnitude, as a byte; half: 16 random bits
-  static __device__ __forceinline__ uint32_t encode(float x, float inverse, uint32_t half) {
-    const float part = fminf(fabsf(x) * inverse, 1.f);
-    const uint32_t bits = __float_as_uint(part), r = half << (kShift - 16);
-    uint32_t c = ((bits + r) >> kShift) - kFirst;
-    if (bits < uint32_t(kFirst + 1) << kShift) c = part > static_cast<float>(r) * kLow ? 1u : 0u;
-    if (kSigned && x < 0.f && c > 0) c += 128u;
-    return c;
+  // The random bits that a word's half rounds with, in place for the code.
+  static __device__ __forceinline__ uint32_t random(uint32_t word) {
+    return kSigned ? word << 4 & 0xffff0u : word >> 13 & 0x7fff8u;
+  }
+  // |x| over the block's largest magnitude, at most 1
+  static __device__ __forceinline__ float part(float x, float inverse) {
+    return fminf(fabsf(x) * inverse, 1.f);
+  }
+  // Puts the code of x, whose part is given, into byte j.  Parts between zero and the lowest
+  // code become zero here: `between` says that there is one.
+  template <int j>
+  static __device__ __forceinline__ void encode(float x, float part, uint32_t random, uint32_t* word,
+                                                bool* between) {
+    const uint32_t bits = __float_as_uint(part);
+    *between = *between || bits - 1u < kLowest - 1u;
+    const bool whole = bits >= kLowest;
+    const uint32_t code = whole ? bits + random - (kFirst << kShift) : 0u;
+    constexpr int right = kShift - 8 * j;
+    const uint32_t moved = right >= 0 ? code >> (right >= 0 ? right : 0) : code << (right < 0 ? -right : 0);
+    *word |= moved & kMask << 8 * j;
+    if (kSigned) {
+      const uint32_t sign = whole ? __float_as_uint(x) : 0u;
+      *word |= sign >> (24 - 8 * j) & 0x80u << 8 * j;
+    }
+  }
+  // The same for those parts, and nothing for others.
+  template <int j>
+  static __device__ __forceinline__ void encode_between(float x, float part, uint32_t random,
+                                                        uint32_t* word) {
+    if (__float_as_uint(part) - 1u >= kLowest - 1u) return;
+    if (part > static_cast<float>(random) * kLow)
+      *word |= (1u | (kSigned && x < 0.f ? 128u : 0u)) << 8 * j;
   }
 };
 
@@ -59,16 +96,27 @@ __device__ __forceinline__ void random_words(uint64_t group, uint64_t step, uint
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
 
+// The largest of a warp's values, NaN when one is.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // A block's scale from its largest magnitude: 0 below 2^-100, NaN when not finite.
-__device__ __forceinline__ float scale_of(float largest, bool finite) {
-  if (!finite) return __int_as_float(0x7fffffff);
+__device__ __forceinline__ float scale_of(float largest) {
+  if (!(largest <= 0x1.fffffep127f)) return __int_as_float(0x7fffffff);
   return largest < 0x1p-100f ? 0.f : largest;
+}
+
+// One element: the moments from m, v and the gradient, the root of v, and the new param.
+__device__ __forceinline__ void update(const AdamwArgs& a, float g, float kept, float step_size,
+                                       float* p, float* m, float* v, float* u) {
+  *m = a.beta1 * *m + a.rest1 * g;
+  *v = a.beta2 * *v + a.rest2 * (g * g);
+  *u = sqrtf(*v);
+  // the quotient within 2 units in the last place: it is far below the param it changes
+  *p = *p * kept - step_size * __fdividef(*m, *u * a.root_scale + a.eps);
 }
 
 // A lane's 8 elements of a block: 4 lane + {0..3} and 128 + 4 lane + {0..3}, 16 bytes of
@@ -195,37 +243,41 @@ __global__ void __launch_bounds__(kThreads) lp_adamw_kernel(const __grid_constan
   }
   const float lr = a.lr * rec.lr_scale;
   const float kept = 1.f - lr * rec.weight_decay, step_size = a.step_size * rec.lr_scale;
-  float u[8], top_m = 0.f, top_u = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (kSmall) {
-      m[k] = Code<true>::decode(old_m[k >> 2] >> 8 * (k & 3) & 255u, old_scale_m);
-      v[k] = Code<false>::decode(old_u[k >> 2] >> 8 * (k & 3) & 255u, old_scale_u);
-      v[k] *= v[k];
-    }
-    const float gk = a.grad_scale != nullptr ? g[k] * clip : g[k];
-    m[k] = a.beta1 * m[k] + a.rest1 * gk;
-    v[k] = a.beta2 * v[k] + a.rest2 * (gk * gk);
-    u[k] = sqrtf(v[k]);
-    const float change = m[k] / (u[k] * a.root_scale + a.eps);
-    p[k] = p[k] * kept - step_size * change;
-    if (kSmall) {
-      top_m = fmaxf(top_m, fabsf(m[k]));
-      top_u = fmaxf(top_u, u[k]);
-      finite = finite && fabsf(m[k]) <= 0x1.fffffep127f && u[k] <= 0x1.fffffep127f;
-    }
-  }
-  store8(rec.param + first, rec.copy != nullptr ? rec.copy + first : nullptr, count, is_wide, stretch,
-         p);
   if (!kSmall) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float u;
+      update(a, a.grad_scale != nullptr ? g[k] * clip : g[k], kept, step_size, &p[k], &m[k], &v[k], &u);
+    }
+    store8(rec.param + first, rec.copy != nullptr ? rec.copy + first : nullptr, count, is_wide,
+           stretch, p);
     store8(static_cast<float*>(a.exp_avg) + flat, nullptr, kBlock, true, stretch, m);
     store8(static_cast<float*>(a.exp_avg_sq) + flat, nullptr, kBlock, true, stretch, v);
     return;
   }
-  finite = __all_sync(0xffffffffu, finite);
-  const float scale_m = scale_of(warp_max(top_m), finite);
-  const float scale_u = scale_of(warp_max(top_u), finite);
+  float u[8], top_m = 0.f, top_u = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    m[4 * h] = Code<true>::decode<0>(old_m[h], old_scale_m);
+    m[4 * h + 1] = Code<true>::decode<1>(old_m[h], old_scale_m);
+    m[4 * h + 2] = Code<true>::decode<2>(old_m[h], old_scale_m);
+    m[4 * h + 3] = Code<true>::decode<3>(old_m[h], old_scale_m);
+    v[4 * h] = Code<false>::decode<0>(old_u[h], old_scale_u);
+    v[4 * h + 1] = Code<false>::decode<1>(old_u[h], old_scale_u);
+    v[4 * h + 2] = Code<false>::decode<2>(old_u[h], old_scale_u);
+    v[4 * h + 3] = Code<false>::decode<3>(old_u[h], old_scale_u);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] *= v[k];
+    update(a, a.grad_scale != nullptr ? g[k] * clip : g[k], kept, step_size, &p[k], &m[k], &v[k],
+           &u[k]);
+    top_m = fmax_nan(top_m, fabsf(m[k]));
+    top_u = fmax_nan(top_u, u[k]);
+  }
+  store8(rec.param + first, rec.copy != nullptr ? rec.copy + first : nullptr, count, is_wide, stretch,
+         p);
+  const float scale_m = scale_of(warp_max(top_m)), scale_u = scale_of(warp_max(top_u));
   const float inv_m = scale_m > 0.f ? 1.f / scale_m : 0.f;
   const float inv_u = scale_u > 0.f ? 1.f / scale_u : 0.f;
   if (lane == 0) {
@@ -236,10 +288,26 @@ __global__ void __launch_bounds__(kThreads) lp_adamw_kernel(const __grid_constan
   for (int h = 0; h < 2; ++h) {
     uint32_t w[4], new_m = 0, new_u = 0;
     random_words(uint64_t(flat / 4 + h * 32 + lane), a.step, a.seed, w);
+    float part_m[4], part_u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      new_m |= Code<true>::encode(m[h * 4 + j], inv_m, w[j] & 0xffffu) << 8 * j;
-      new_u |= Code<false>::encode(u[h * 4 + j], inv_u, w[j] >> 16) << 8 * j;
+      part_m[j] = Code<true>::part(m[4 * h + j], inv_m);
+      part_u[j] = Code<false>::part(u[4 * h + j], inv_u);
+    }
+    bool between = false;
+    const auto each = [&](auto byte) {
+      constexpr int j = decltype(byte)::value;
+      Code<true>::encode<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m, &between);
+      Code<false>::encode<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u, &between);
+    };
+    each(Byte<0>()), each(Byte<1>()), each(Byte<2>()), each(Byte<3>());
+    if (between) {  // rare: a magnitude below 2^-16 of its block's largest
+      const auto rest = [&](auto byte) {
+        constexpr int j = decltype(byte)::value;
+        Code<true>::encode_between<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m);
+        Code<false>::encode_between<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u);
+      };
+      rest(Byte<0>()), rest(Byte<1>()), rest(Byte<2>()), rest(Byte<3>());
     }
     static_cast<uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane] = new_m;
     static_cast<uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane] = new_u;
@@ -280,25 +348,42 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 constexpr int kNormThreads = 1024;
+// A sum and what its roundings lost (the error of a sum of two floats is a float: Knuth's two-sum).
+// float64 additions would take longer than the loads.
+struct Pair {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float sum = hi + x, back = sum - hi;
+    lo += (hi - (sum - back)) + (x - back);
+    hi = sum;
+  }
+};
 __global__ void __launch_bounds__(kNormThreads)
     lp_adamw_norm_kernel(const float* sums, int64_t rows, float max_norm, float* norm_out) {
-  __shared__ double slots[kNormThreads / 32];
+  __shared__ Pair slots[kNormThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  double s = 0.0;
+  Pair s{0.f, 0.f};
   const int64_t quads = rows / 4;
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < quads; i += kNormThreads) {
     const float4 x = __ldcg(reinterpret_cast<const float4*>(sums) + i);
-    s += (double(x.x) + double(x.y)) + (double(x.z) + double(x.w));
+    s.add(x.x), s.add(x.y), s.add(x.z), s.add(x.w);
   }
-  if (threadIdx.x < rows % 4) s += __ldcg(sums + quads * 4 + threadIdx.x);
+  if (threadIdx.x < rows % 4) s.add(__ldcg(sums + quads * 4 + threadIdx.x));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+    s.add(hi);
+    s.lo += lo;
+  }
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = s;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int i = 1; i < kNormThreads / 32; ++i) s += slots[i];
-  const float norm = static_cast<float>(sqrt(s));
+  for (int i = 1; i < kNormThreads / 32; ++i) {
+    s.add(slots[i].hi);
+    s.lo += slots[i].lo;
+  }
+  const float norm = sqrtf(s.hi + s.lo);
   norm_out[0] = norm;
   norm_out[1] = norm <= 0x1.fffffep127f ? fminf(max_norm / (norm + 1e-6f), 1.f)
                                         : __int_as_float(0x7fffffff);
@@ -312,15 +397,11 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t i = int64_t(blockIdx.x) * (kRow / 4) + k * kThreads + threadIdx.x;
     const uint32_t cm = __ldg(m + i), cu = __ldg(u + i);
     const float sm = __ldg(m_scale + i / (kBlock / 4)), su = __ldg(u_scale + i / (kBlock / 4));
-    float a[4], b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = Code<true>::decode(cm >> 8 * j & 255u, sm);
-      const float root = Code<false>::decode(cu >> 8 * j & 255u, su);
-      b[j] = root * root;
-    }
-    m_out[i] = make_float4(a[0], a[1], a[2], a[3]);
-    v_out[i] = make_float4(b[0], b[1], b[2], b[3]);
+    m_out[i] = make_float4(Code<true>::decode<0>(cm, sm), Code<true>::decode<1>(cm, sm),
+                           Code<true>::decode<2>(cm, sm), Code<true>::decode<3>(cm, sm));
+    const float4 u4 = make_float4(Code<false>::decode<0>(cu, su), Code<false>::decode<1>(cu, su),
+                                  Code<false>::decode<2>(cu, su), Code<false>::decode<3>(cu, su));
+    v_out[i] = make_float4(u4.x * u4.x, u4.y * u4.y, u4.z * u4.z, u4.w * u4.w);
   }
 }
 
