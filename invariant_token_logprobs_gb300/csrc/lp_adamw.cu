@@ -78,20 +78,18 @@ struct Code {
 };
 
 // Philox 4x32 with 7 rounds (Salmon, Moraes, Dror and Shaw, "Parallel random numbers:
-// as easy as 1, 2, 3", SC11) at counter (group, step) under `seed`.
-__device__ __forceinline__ void random_words(uint64_t group, uint64_t step, uint64_t seed,
-                                             uint32_t (&w)[4]) {
+// as easy as 1, 2, 3", SC11) at counter (group, step), with the rounds' keys at hand.
+__device__ __forceinline__ void random_words(uint64_t group, uint64_t step,
+                                             const uint32_t (&keys)[7][2], uint32_t (&w)[4]) {
   uint32_t c0 = uint32_t(group), c1 = uint32_t(group >> 32), c2 = uint32_t(step),
-           c3 = uint32_t(step >> 32), k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+           c3 = uint32_t(step >> 32);
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
     const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
-    c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+    c0 = uint32_t(b >> 32) ^ c1 ^ keys[i][0];
     c1 = uint32_t(b);
-    c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c2 = uint32_t(a >> 32) ^ c3 ^ keys[i][1];
     c3 = uint32_t(a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
@@ -109,14 +107,37 @@ __device__ __forceinline__ float scale_of(float largest) {
   return largest < 0x1p-100f ? 0.f : largest;
 }
 
-// One element: the moments from m, v and the gradient, the root of v, and the new param.
-__device__ __forceinline__ void update(const AdamwArgs& a, float g, float kept, float step_size,
-                                       float* p, float* m, float* v, float* u) {
-  *m = a.beta1 * *m + a.rest1 * g;
-  *v = a.beta2 * *v + a.rest2 * (g * g);
-  *u = sqrtf(*v);
+// Two products or sums an instruction, each rounded as by itself.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; "
+      "mov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; "
+      "mov.b64 {%0, %1}, z;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Two elements: the moments from m, v and the gradient, the new param, and the roots of v.
+__device__ __forceinline__ float2 update(const AdamwArgs& a, float2 g, float kept, float step_size,
+                                         float2* p, float2* m, float2* v) {
+  // element by element: the moments' products are each rounded, and a pair's may be fused
+  m->x = a.beta1 * m->x + a.rest1 * g.x, m->y = a.beta1 * m->y + a.rest1 * g.y;
+  v->x = a.beta2 * v->x + a.rest2 * (g.x * g.x), v->y = a.beta2 * v->y + a.rest2 * (g.y * g.y);
+  const float2 u = make_float2(sqrtf(v->x), sqrtf(v->y));
+  const float2 below = add2(mul2(u, both(a.root_scale)), both(a.eps));
   // the quotient within 2 units in the last place: it is far below the param it changes
-  *p = *p * kept - step_size * __fdividef(*m, *u * a.root_scale + a.eps);
+  const float2 change = make_float2(__fdividef(m->x, below.x), __fdividef(m->y, below.y));
+  *p = add2(mul2(*p, both(kept)), mul2(both(-step_size), change));
+  return u;
 }
 
 // A lane's 8 elements of a block: 4 lane + {0..3} and 128 + 4 lane + {0..3}, 16 bytes of
@@ -199,118 +220,124 @@ __device__ __forceinline__ void store8(float* p, __nv_bfloat16* copy, int count,
   }
 }
 
-// One block of a tensor a warp.  The moments' buffers are padded to whole blocks, and what lies
-// past a tensor's end in them stays zero.
+// One row of a tensor a CTA, its blocks in turn a warp.  The moments' buffers are padded to whole
+// blocks, and what lies past a tensor's end in them stays zero.
 template <bool kSmall>
-__global__ void __launch_bounds__(kThreads) lp_adamw_kernel(const __grid_constant__ AdamwArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) lp_adamw_kernel(const __grid_constant__ AdamwArgs a) {
   __shared__ __align__(16) float stretches[kThreads / 32][kBlock];
   const int64_t row = blockIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int32_t index = a.table[row];
   if (!LP_CHECK(index >= 0 && index < a.n_tensors, kChkPlan)) return;
   const AdamwRecord rec = a.records[index];
-  // this warp's block: its first element in the tensor and in the flat buffers
-  const int64_t first = (row - rec.first_row) * kRow + warp * kBlock;
-  const int64_t flat = row * kRow + warp * kBlock, block = flat / kBlock;
-  if (first >= rec.n) return;
-  const int count = int(min(rec.n - first, int64_t(kBlock)));
-  const bool is_wide = rec.wide != 0;
-  float* stretch = stretches[warp];
-  float p[8], g[8], m[8], v[8];
-  uint32_t old_m[2], old_u[2];
-  float old_scale_m = 0.f, old_scale_u = 0.f;
-  load8(rec.param + first, count, is_wide, stretch, p);
-  if (rec.grad_bf16)
-    load8(static_cast<const __nv_bfloat16*>(rec.grad) + first, count, is_wide, stretch, g);
-  else
-    load8(static_cast<const float*>(rec.grad) + first, count, is_wide, stretch, g);
-  if (kSmall) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      old_m[h] = static_cast<const uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane];
-      old_u[h] = static_cast<const uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane];
-    }
-    old_scale_m = a.exp_avg_scale[block];
-    old_scale_u = a.exp_avg_sq_scale[block];
-  } else {
-    load8(static_cast<const float*>(a.exp_avg) + flat, kBlock, true, stretch, m);
-    load8(static_cast<const float*>(a.exp_avg_sq) + flat, kBlock, true, stretch, v);
-  }
-  float clip = 1.f;
-  if (a.grad_scale != nullptr) {
-    clip = *a.grad_scale;
-    if (clip != clip) return;
-  }
+  const float clip = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
+  if (clip != clip) return;
   const float lr = a.lr * rec.lr_scale;
   const float kept = 1.f - lr * rec.weight_decay, step_size = a.step_size * rec.lr_scale;
-  if (!kSmall) {
+  float* stretch = stretches[warp];
+  const int64_t first = (row - rec.first_row) * kRow;  // of the row in the tensor
+  const int left = int(min(rec.n - first, int64_t(kRow)));
+  const bool is_wide = rec.wide != 0;
+  float* const params = rec.param + first;
+  __nv_bfloat16* const copies = rec.copy != nullptr ? rec.copy + first : nullptr;
+  for (int at = warp * kBlock; at < left; at += int(blockDim.x) * 8) {
+    const int count = min(left - at, kBlock);
+    const int64_t flat = row * kRow + at;
+    float p[8], g[8], m[8], v[8];
+    uint32_t old_m[2], old_u[2];
+    float old_scale_m = 0.f, old_scale_u = 0.f;
+    load8(params + at, count, is_wide, stretch, p);
+    if (rec.grad_bf16)
+      load8(static_cast<const __nv_bfloat16*>(rec.grad) + first + at, count, is_wide, stretch, g);
+    else
+      load8(static_cast<const float*>(rec.grad) + first + at, count, is_wide, stretch, g);
+    uint32_t* const codes_m = static_cast<uint32_t*>(a.exp_avg) + flat / 4 + lane;
+    uint32_t* const codes_u = static_cast<uint32_t*>(a.exp_avg_sq) + flat / 4 + lane;
+    if (kSmall) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        old_m[h] = codes_m[32 * h];
+        old_u[h] = codes_u[32 * h];
+      }
+      old_scale_m = a.exp_avg_scale[flat / kBlock];
+      old_scale_u = a.exp_avg_sq_scale[flat / kBlock];
+    } else {
+      load8(static_cast<const float*>(a.exp_avg) + flat, kBlock, true, stretch, m);
+      load8(static_cast<const float*>(a.exp_avg_sq) + flat, kBlock, true, stretch, v);
+    }
+    if (a.grad_scale != nullptr)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] *= clip;
+    if (kSmall) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m[4 * h] = Code<true>::decode<0>(old_m[h], old_scale_m);
+        m[4 * h + 1] = Code<true>::decode<1>(old_m[h], old_scale_m);
+        m[4 * h + 2] = Code<true>::decode<2>(old_m[h], old_scale_m);
+        m[4 * h + 3] = Code<true>::decode<3>(old_m[h], old_scale_m);
+        v[4 * h] = Code<false>::decode<0>(old_u[h], old_scale_u);
+        v[4 * h + 1] = Code<false>::decode<1>(old_u[h], old_scale_u);
+        v[4 * h + 2] = Code<false>::decode<2>(old_u[h], old_scale_u);
+        v[4 * h + 3] = Code<false>::decode<3>(old_u[h], old_scale_u);
+      }
+    }
+    float u[8];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      float2 mk = make_float2(m[k], m[k + 1]), vk = make_float2(v[k], v[k + 1]),
+             pk = make_float2(p[k], p[k + 1]);
+      if (kSmall) vk = mul2(vk, vk);
+      const float2 uk = update(a, make_float2(g[k], g[k + 1]), kept, step_size, &pk, &mk, &vk);
+      m[k] = mk.x, m[k + 1] = mk.y, v[k] = vk.x, v[k + 1] = vk.y, p[k] = pk.x, p[k + 1] = pk.y;
+      u[k] = uk.x, u[k + 1] = uk.y;
+    }
+    store8(params + at, copies != nullptr ? copies + at : nullptr, count, is_wide, stretch, p);
+    if (!kSmall) {
+      store8(static_cast<float*>(a.exp_avg) + flat, nullptr, kBlock, true, stretch, m);
+      store8(static_cast<float*>(a.exp_avg_sq) + flat, nullptr, kBlock, true, stretch, v);
+      continue;
+    }
+    float top_m = 0.f, top_u = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float u;
-      update(a, a.grad_scale != nullptr ? g[k] * clip : g[k], kept, step_size, &p[k], &m[k], &v[k], &u);
+      top_m = fmax_nan(top_m, fabsf(m[k]));
+      top_u = fmax_nan(top_u, u[k]);
     }
-    store8(rec.param + first, rec.copy != nullptr ? rec.copy + first : nullptr, count, is_wide,
-           stretch, p);
-    store8(static_cast<float*>(a.exp_avg) + flat, nullptr, kBlock, true, stretch, m);
-    store8(static_cast<float*>(a.exp_avg_sq) + flat, nullptr, kBlock, true, stretch, v);
-    return;
-  }
-  float u[8], top_m = 0.f, top_u = 0.f;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    m[4 * h] = Code<true>::decode<0>(old_m[h], old_scale_m);
-    m[4 * h + 1] = Code<true>::decode<1>(old_m[h], old_scale_m);
-    m[4 * h + 2] = Code<true>::decode<2>(old_m[h], old_scale_m);
-    m[4 * h + 3] = Code<true>::decode<3>(old_m[h], old_scale_m);
-    v[4 * h] = Code<false>::decode<0>(old_u[h], old_scale_u);
-    v[4 * h + 1] = Code<false>::decode<1>(old_u[h], old_scale_u);
-    v[4 * h + 2] = Code<false>::decode<2>(old_u[h], old_scale_u);
-    v[4 * h + 3] = Code<false>::decode<3>(old_u[h], old_scale_u);
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    v[k] *= v[k];
-    update(a, a.grad_scale != nullptr ? g[k] * clip : g[k], kept, step_size, &p[k], &m[k], &v[k],
-           &u[k]);
-    top_m = fmax_nan(top_m, fabsf(m[k]));
-    top_u = fmax_nan(top_u, u[k]);
-  }
-  store8(rec.param + first, rec.copy != nullptr ? rec.copy + first : nullptr, count, is_wide, stretch,
-         p);
-  const float scale_m = scale_of(warp_max(top_m)), scale_u = scale_of(warp_max(top_u));
-  const float inv_m = scale_m > 0.f ? 1.f / scale_m : 0.f;
-  const float inv_u = scale_u > 0.f ? 1.f / scale_u : 0.f;
-  if (lane == 0) {
-    a.exp_avg_scale[block] = scale_m;
-    a.exp_avg_sq_scale[block] = scale_u;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[4], new_m = 0, new_u = 0;
-    random_words(uint64_t(flat / 4 + h * 32 + lane), a.step, a.seed, w);
-    float part_m[4], part_u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      part_m[j] = Code<true>::part(m[4 * h + j], inv_m);
-      part_u[j] = Code<false>::part(u[4 * h + j], inv_u);
+    const float scale_m = scale_of(warp_max(top_m)), scale_u = scale_of(warp_max(top_u));
+    const float inv_m = scale_m > 0.f ? 1.f / scale_m : 0.f;
+    const float inv_u = scale_u > 0.f ? 1.f / scale_u : 0.f;
+    if (lane == 0) {
+      a.exp_avg_scale[flat / kBlock] = scale_m;
+      a.exp_avg_sq_scale[flat / kBlock] = scale_u;
     }
-    bool between = false;
-    const auto each = [&](auto byte) {
-      constexpr int j = decltype(byte)::value;
-      Code<true>::encode<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m, &between);
-      Code<false>::encode<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u, &between);
-    };
-    each(Byte<0>()), each(Byte<1>()), each(Byte<2>()), each(Byte<3>());
-    if (between) {  // rare: a magnitude below 2^-16 of its block's largest
-      const auto rest = [&](auto byte) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4], new_m = 0, new_u = 0;
+      random_words(uint64_t(flat / 4 + h * 32 + lane), a.step, a.round_keys, w);
+      float part_m[4], part_u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        part_m[j] = Code<true>::part(m[4 * h + j], inv_m);
+        part_u[j] = Code<false>::part(u[4 * h + j], inv_u);
+      }
+      bool between = false;
+      const auto each = [&](auto byte) {
         constexpr int j = decltype(byte)::value;
-        Code<true>::encode_between<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m);
-        Code<false>::encode_between<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u);
+        Code<true>::encode<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m, &between);
+        Code<false>::encode<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u, &between);
       };
-      rest(Byte<0>()), rest(Byte<1>()), rest(Byte<2>()), rest(Byte<3>());
+      each(Byte<0>()), each(Byte<1>()), each(Byte<2>()), each(Byte<3>());
+      if (between) {  // rare: a magnitude below 2^-16 of its block's largest
+        const auto rest = [&](auto byte) {
+          constexpr int j = decltype(byte)::value;
+          Code<true>::encode_between<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m);
+          Code<false>::encode_between<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u);
+        };
+        rest(Byte<0>()), rest(Byte<1>()), rest(Byte<2>()), rest(Byte<3>());
+      }
+      codes_m[32 * h] = new_m;
+      codes_u[32 * h] = new_u;
     }
-    static_cast<uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane] = new_m;
-    static_cast<uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane] = new_u;
   }
 }
 
@@ -405,6 +432,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// From this many rows on a warp takes four blocks in turn instead of one, which spreads what it
+// costs to find them.
+constexpr int64_t kManyRows = 152 * 32;
+
 template <class... Params, class... Args>
 bool launch_dependent(void (*kernel)(Params...), int64_t blocks, int threads, cudaStream_t stream,
                       Args... args) {
@@ -422,9 +453,15 @@ bool launch_dependent(void (*kernel)(Params...), int64_t blocks, int threads, cu
 
 }  // namespace
 
-lp_status launch_adamw_step(const AdamwArgs& a, cudaStream_t stream) {
+lp_status launch_adamw_step(const AdamwArgs& args, cudaStream_t stream) {
+  AdamwArgs a = args;
+  for (int i = 0; i < 7; ++i) {
+    a.round_keys[i][0] = uint32_t(a.seed) + uint32_t(i) * 0x9E3779B9u;
+    a.round_keys[i][1] = uint32_t(a.seed >> 32) + uint32_t(i) * 0xBB67AE85u;
+  }
   auto* kernel = a.exp_avg_scale != nullptr ? lp_adamw_kernel<true> : lp_adamw_kernel<false>;
-  kernel<<<unsigned(a.rows), kThreads, 0, stream>>>(a);
+  const int threads = a.rows >= kManyRows ? kThreads / 4 : kThreads;
+  kernel<<<unsigned(a.rows), threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 

@@ -100,6 +100,7 @@ struct AdamwArgs {
   float *exp_avg_scale, *exp_avg_sq_scale;  // null: 32-bit moments
   float lr, step_size, beta1, beta2, rest1, rest2, root_scale, eps;
   uint64_t step, seed;
+  uint32_t round_keys[7][2];  // of the random words, set by the launcher from seed
   const float* grad_scale;
 };
 lp_status launch_adamw_step(const AdamwArgs& a, cudaStream_t stream);
