@@ -33,14 +33,15 @@ struct Code {
   // magnitude below that value to it or to zero
   static constexpr float kLow = kSigned ? 0x1.4p-36f : 0x1.2p-35f;
 
-  // byte j of the word
+  // byte j of the word.  For the first moment the sign's bit, multiplied up with the code, adds
+  // 16 to the exponent, which the factor of a negative value takes back.
   template <int j>
   static __device__ __forceinline__ float decode(uint32_t word, float scale) {
-    constexpr int left = kShift - 8 * j;
-    const uint32_t moved = left >= 0 ? word << (left >= 0 ? left : 0) : word >> (left < 0 ? -left : 0);
-    uint32_t bits = (moved & kMask << kShift) + (kFirst << kShift);
-    if (kSigned) bits |= word << (24 - 8 * j) & 0x80000000u;
-    return (word & kMask << 8 * j) != 0 ? __uint_as_float(bits) * scale : 0.f * scale;
+    const uint32_t byte = __byte_perm(word, 0u, 0x4440u + j);
+    const float value = __uint_as_float(byte * (1u << kShift) + (kFirst << kShift));
+    float factor = kSigned && byte >= 128u ? scale * -0x1p-16f : scale;
+    if ((byte & kMask) == 0u) factor = 0.f * scale;
+    return value * factor;
   }
   // The random bits that a word's half rounds with, in place for the code.
   static __device__ __forceinline__ uint32_t random(uint32_t word) {
@@ -51,12 +52,12 @@ struct Code {
     return fminf(fabsf(x) * inverse, 1.f);
   }
   // Puts the code of x, whose part is given, into byte j.  Parts between zero and the lowest
-  // code become zero here: `between` says that there is one.
+  // code become zero here; `least`, the smallest of all parts' bits less one, tells of them.
   template <int j>
   static __device__ __forceinline__ void encode(float x, float part, uint32_t random, uint32_t* word,
-                                                bool* between) {
+                                                uint32_t* least) {
     const uint32_t bits = __float_as_uint(part);
-    *between = *between || bits - 1u < kLowest - 1u;
+    *least = min(*least, bits - 1u);
     const bool whole = bits >= kLowest;
     const uint32_t code = whole ? bits + random - (kFirst << kShift) : 0u;
     constexpr int right = kShift - 8 * j;
@@ -126,6 +127,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Two elements: the moments from m, v and the gradient, the new param, and the roots of v.
 __device__ __forceinline__ float2 update(const AdamwArgs& a, float2 g, float kept, float step_size,
                                          float2* p, float2* m, float2* v) {
@@ -134,8 +141,9 @@ __device__ __forceinline__ float2 update(const AdamwArgs& a, float2 g, float kep
   v->x = a.beta2 * v->x + a.rest2 * (g.x * g.x), v->y = a.beta2 * v->y + a.rest2 * (g.y * g.y);
   const float2 u = make_float2(sqrtf(v->x), sqrtf(v->y));
   const float2 below = add2(mul2(u, both(a.root_scale)), both(a.eps));
-  // the quotient within 2 units in the last place: it is far below the param it changes
-  const float2 change = make_float2(__fdividef(m->x, below.x), __fdividef(m->y, below.y));
+  // the quotient by an approximate reciprocal, within 3 units in the last place: it is far below
+  // the param that it changes
+  const float2 change = mul2(*m, make_float2(reciprocal(below.x), reciprocal(below.y)));
   *p = add2(mul2(*p, both(kept)), mul2(both(-step_size), change));
   return u;
 }
@@ -220,11 +228,37 @@ __device__ __forceinline__ void store8(float* p, __nv_bfloat16* copy, int count,
   }
 }
 
+// A block on its way into shared memory; a lane copies what it reads.
+struct Stage {
+  float p[kBlock];
+  float g[kBlock];  // float32 or bfloat16
+  uint32_t m[kBlock / 4], u[kBlock / 4];
+};
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from)
+               : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_few(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+               "l"(from), "n"(kBytes)
+               : "memory");
+}
+
 // One row of a tensor a CTA, its blocks in turn a warp.  The moments' buffers are padded to whole
 // blocks, and what lies past a tensor's end in them stays zero.
-template <bool kSmall>
-__global__ void __launch_bounds__(kThreads, 4) lp_adamw_kernel(const __grid_constant__ AdamwArgs a) {
-  __shared__ __align__(16) float stretches[kThreads / 32][kBlock];
+//
+// With 32-bit moments a block is 7 KB of traffic and 32 warps an SM keep the memory busy.  With
+// 8-bit ones it is half of that and some 90 instructions an element, so the next block is
+// copied while one is computed.
+template <bool kSmall, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
+    lp_adamw_kernel(const __grid_constant__ AdamwArgs a) {
+  constexpr int kStretch = (kSmall ? 2 * sizeof(Stage) : kBlock * sizeof(float)) / sizeof(float);
+  __shared__ __align__(16) float stretches[kWarps][kStretch];
   const int64_t row = blockIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int32_t index = a.table[row];
@@ -240,30 +274,75 @@ __global__ void __launch_bounds__(kThreads, 4) lp_adamw_kernel(const __grid_cons
   const bool is_wide = rec.wide != 0;
   float* const params = rec.param + first;
   __nv_bfloat16* const copies = rec.copy != nullptr ? rec.copy + first : nullptr;
-  for (int at = warp * kBlock; at < left; at += int(blockDim.x) * 8) {
+  constexpr int step = kWarps * kBlock;
+  // starts the copy of the block at `at`, where it is whole and aligned
+  const auto fetch = [&](int at, Stage* to) {
+    if (is_wide && left - at >= kBlock) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = 128 * h + 4 * lane;
+        copy16(to->p + e, params + at + e);
+        if (rec.grad_bf16)
+          copy_few<8>(reinterpret_cast<__nv_bfloat16*>(to->g) + e,
+                      static_cast<const __nv_bfloat16*>(rec.grad) + first + at + e);
+        else
+          copy16(to->g + e, static_cast<const float*>(rec.grad) + first + at + e);
+        copy_few<4>(to->m + e / 4, static_cast<const uint32_t*>(a.exp_avg) + (row * kRow + at + e) / 4);
+        copy_few<4>(to->u + e / 4, static_cast<const uint32_t*>(a.exp_avg_sq) + (row * kRow + at + e) / 4);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Stage* stage = reinterpret_cast<Stage*>(stretch);
+  Stage* other = stage + 1;
+  if (kSmall) fetch(warp * kBlock, stage);
+  for (int at = warp * kBlock; at < left; at += step) {
     const int count = min(left - at, kBlock);
     const int64_t flat = row * kRow + at;
     float p[8], g[8], m[8], v[8];
     uint32_t old_m[2], old_u[2];
     float old_scale_m = 0.f, old_scale_u = 0.f;
-    load8(params + at, count, is_wide, stretch, p);
-    if (rec.grad_bf16)
-      load8(static_cast<const __nv_bfloat16*>(rec.grad) + first + at, count, is_wide, stretch, g);
-    else
-      load8(static_cast<const float*>(rec.grad) + first + at, count, is_wide, stretch, g);
-    uint32_t* const codes_m = static_cast<uint32_t*>(a.exp_avg) + flat / 4 + lane;
-    uint32_t* const codes_u = static_cast<uint32_t*>(a.exp_avg_sq) + flat / 4 + lane;
     if (kSmall) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        old_m[h] = codes_m[32 * h];
-        old_u[h] = codes_u[32 * h];
-      }
       old_scale_m = a.exp_avg_scale[flat / kBlock];
       old_scale_u = a.exp_avg_sq_scale[flat / kBlock];
+      fetch(at + step, other);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    }
+    if (kSmall && is_wide && count == kBlock) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = 128 * h + 4 * lane;
+        const float4 x = *reinterpret_cast<const float4*>(stage->p + e);
+        p[4 * h] = x.x, p[4 * h + 1] = x.y, p[4 * h + 2] = x.z, p[4 * h + 3] = x.w;
+        if (rec.grad_bf16) {
+          const uint2 y = *reinterpret_cast<const uint2*>(
+              reinterpret_cast<const __nv_bfloat16*>(stage->g) + e);
+          g[4 * h] = __uint_as_float(y.x << 16), g[4 * h + 1] = __uint_as_float(y.x & 0xffff0000u);
+          g[4 * h + 2] = __uint_as_float(y.y << 16);
+          g[4 * h + 3] = __uint_as_float(y.y & 0xffff0000u);
+        } else {
+          const float4 y = *reinterpret_cast<const float4*>(stage->g + e);
+          g[4 * h] = y.x, g[4 * h + 1] = y.y, g[4 * h + 2] = y.z, g[4 * h + 3] = y.w;
+        }
+        old_m[h] = stage->m[e / 4];
+        old_u[h] = stage->u[e / 4];
+      }
     } else {
-      load8(static_cast<const float*>(a.exp_avg) + flat, kBlock, true, stretch, m);
-      load8(static_cast<const float*>(a.exp_avg_sq) + flat, kBlock, true, stretch, v);
+      load8(params + at, count, is_wide, stretch, p);
+      if (rec.grad_bf16)
+        load8(static_cast<const __nv_bfloat16*>(rec.grad) + first + at, count, is_wide, stretch, g);
+      else
+        load8(static_cast<const float*>(rec.grad) + first + at, count, is_wide, stretch, g);
+      if (kSmall) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          old_m[h] = static_cast<const uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane];
+          old_u[h] = static_cast<const uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane];
+        }
+      } else {
+        load8(static_cast<const float*>(a.exp_avg) + flat, kBlock, true, stretch, m);
+        load8(static_cast<const float*>(a.exp_avg_sq) + flat, kBlock, true, stretch, v);
+      }
     }
     if (a.grad_scale != nullptr)
 #pragma unroll
@@ -320,14 +399,14 @@ __global__ void __launch_bounds__(kThreads, 4) lp_adamw_kernel(const __grid_cons
         part_m[j] = Code<true>::part(m[4 * h + j], inv_m);
         part_u[j] = Code<false>::part(u[4 * h + j], inv_u);
       }
-      bool between = false;
+      uint32_t least_m = ~0u, least_u = ~0u;
       const auto each = [&](auto byte) {
         constexpr int j = decltype(byte)::value;
-        Code<true>::encode<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m, &between);
-        Code<false>::encode<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u, &between);
+        Code<true>::encode<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m, &least_m);
+        Code<false>::encode<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u, &least_u);
       };
       each(Byte<0>()), each(Byte<1>()), each(Byte<2>()), each(Byte<3>());
-      if (between) {  // rare: a magnitude below 2^-16 of its block's largest
+      if (least_m < Code<true>::kLowest - 1u || least_u < Code<false>::kLowest - 1u) {  // rare: a magnitude below 2^-16 of its block's largest
         const auto rest = [&](auto byte) {
           constexpr int j = decltype(byte)::value;
           Code<true>::encode_between<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m);
@@ -335,9 +414,12 @@ __global__ void __launch_bounds__(kThreads, 4) lp_adamw_kernel(const __grid_cons
         };
         rest(Byte<0>()), rest(Byte<1>()), rest(Byte<2>()), rest(Byte<3>());
       }
-      codes_m[32 * h] = new_m;
-      codes_u[32 * h] = new_u;
+      static_cast<uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane] = new_m;
+      static_cast<uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane] = new_u;
     }
+    Stage* const next = other;
+    other = stage;
+    stage = next;
   }
 }
 
@@ -459,9 +541,14 @@ lp_status launch_adamw_step(const AdamwArgs& args, cudaStream_t stream) {
     a.round_keys[i][0] = uint32_t(a.seed) + uint32_t(i) * 0x9E3779B9u;
     a.round_keys[i][1] = uint32_t(a.seed >> 32) + uint32_t(i) * 0xBB67AE85u;
   }
-  auto* kernel = a.exp_avg_scale != nullptr ? lp_adamw_kernel<true> : lp_adamw_kernel<false>;
-  const int threads = a.rows >= kManyRows ? kThreads / 4 : kThreads;
-  kernel<<<unsigned(a.rows), threads, 0, stream>>>(a);
+  const bool small = a.exp_avg_scale != nullptr;
+  if (a.rows >= kManyRows) {
+    auto* kernel = small ? lp_adamw_kernel<true, 2> : lp_adamw_kernel<false, 2>;
+    kernel<<<unsigned(a.rows), 64, 0, stream>>>(a);
+  } else {
+    auto* kernel = small ? lp_adamw_kernel<true, 8> : lp_adamw_kernel<false, 8>;
+    kernel<<<unsigned(a.rows), 256, 0, stream>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }
 
