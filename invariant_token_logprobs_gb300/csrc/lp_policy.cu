@@ -28,9 +28,16 @@ constexpr int64_t kSmallSequences = 2048;
 
 // ---- two grids
 constexpr int kThreads = 256;
-constexpr int kRounds = 4;                    // groups of 4 rows a thread
-constexpr int kChunk = kThreads * 4 * kRounds;  // rows of a CTA
-constexpr int kStaged = 512;                  // sequence offsets of a chunk held in shared memory
+constexpr int kTurn = kThreads * 4;              // rows of a CTA at once in the second pass
+constexpr int64_t kMostChunks = 152 * 4;         // its CTAs: four to an SM of a GB300
+constexpr int kCountRun = 16;                    // neighbouring rows a thread of the first
+constexpr int kCountChunk = kThreads * kCountRun;
+constexpr int kStaged = 1024;                    // sequences of a chunk held in shared memory
+// Rows of a CTA of the second pass: whole turns, as many as it takes.
+int64_t chunk_of(int64_t T) {
+  const int64_t turns = (T + kTurn - 1) / kTurn;
+  return (turns + kMostChunks - 1) / kMostChunks * kTurn;
+}
 
 struct Header {
   unsigned counted;    // rows that count, in all
@@ -71,7 +78,7 @@ __device__ __forceinline__ int64_t warp_upper_bound(const int64_t* offsets, int6
   return lo;
 }
 
-// Four values of an operand; rows past T read as zero.
+// Four values of an operand; rows from T on read as zero.
 __device__ __forceinline__ void load4(const float* p, int64_t t, int64_t T, bool wide,
                                       float (&v)[4]) {
   if (wide && t + 4 <= T) {
@@ -112,16 +119,16 @@ __device__ __forceinline__ unsigned load_mask4(const uint8_t* mask, int64_t t, i
 struct Four {
   float logp[4], old[4], ref[4], entropy[4], advantage[4];
 };
-__device__ __forceinline__ void load_rows(const PolicyArgs& a, int64_t t, Four& f) {
-  load4(a.logp, t, a.T, a.wide, f.logp);
-  load4(a.old_logp, t, a.T, a.wide, f.old);
-  if (a.ref_logp != nullptr) load4(a.ref_logp, t, a.T, a.wide, f.ref);
-  if (a.entropy != nullptr) load4(a.entropy, t, a.T, a.wide, f.entropy);
-  if (!a.per_sequence) load4(a.advantages, t, a.T, a.wide, f.advantage);
+__device__ __forceinline__ void load_rows(const PolicyArgs& a, int64_t t, int64_t T, Four& f) {
+  load4(a.logp, t, T, a.wide, f.logp);
+  load4(a.old_logp, t, T, a.wide, f.old);
+  if (a.ref_logp != nullptr) load4(a.ref_logp, t, T, a.wide, f.ref);
+  if (a.entropy != nullptr) load4(a.entropy, t, T, a.wide, f.entropy);
+  if (!a.per_sequence) load4(a.advantages, t, T, a.wide, f.advantage);
 }
 // Their gradients, and their terms added to `sum`.  kept: the rows that count; w: weights.
-__device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, const Four& f,
-                                            unsigned kept, const float (&w)[4],
+__device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int64_t T,
+                                            const Four& f, unsigned kept, const float (&w)[4],
                                             float (&sum)[kStats]) {
   float grad[4], grad_entropy[4];
 #pragma unroll
@@ -129,7 +136,7 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, cons
     grad[j] = grad_entropy[j] = 0.f;
     if (!(kept >> j & 1u)) continue;  // whatever it holds
     const float A = f.advantage[j], delta = f.logp[j] - f.old[j];
-    const float ratio = expf(delta);
+    const float ratio = __expf(delta);  // within 2 + |1.2 delta| units in the last place
     const bool over = A > 0.f && delta > a.high, under = A < 0.f && delta < a.low;
     const bool clipped = over || under;
     float g = clipped ? 0.f : -A * ratio;
@@ -146,8 +153,8 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, cons
     if (clipped) sum[3] += w[j];
     grad[j] = w[j] * g;
   }
-  store4(a.grad_logp, t, a.T, a.wide, grad);
-  if (a.grad_entropy != nullptr) store4(a.grad_entropy, t, a.T, a.wide, grad_entropy);
+  store4(a.grad_logp, t, T, a.wide, grad);
+  if (a.grad_entropy != nullptr) store4(a.grad_entropy, t, T, a.wide, grad_entropy);
 }
 
 // The sums of a CTA's threads, in thread 0: shuffles, then the warps' sums in order.
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kSmallThreads) lp_policy_small_kernel(const __
   for (int k = 0; k < kSmallRounds; ++k) {
     const int64_t t = 4 * (int64_t(threadIdx.x) + k * threads);
     kept[k] = load_mask4(a.mask, t, a.T, a.wide);
-    load_rows(a, t, rows[k]);
+    load_rows(a, t, a.T, rows[k]);
   }
   __syncthreads();
   int sequence[kSmallRounds][4];
@@ -234,147 +241,197 @@ __global__ void __launch_bounds__(kSmallThreads) lp_policy_small_kernel(const __
       w[j] = weight_of(a.by_sequence, a.by_sequence ? counts[sequence[k][j]] : 0u, whole);
       if (a.per_sequence) rows[k].advantage[j] = a.advantages[sequence[k][j]];
     }
-    finish_rows(a, t, rows[k], kept[k], w, sum);
+    finish_rows(a, t, a.T, rows[k], kept[k], w, sum);
   }
   cta_sum<kSmallThreads>(sum, slots);
   if (threadIdx.x == 0) write_stats(a, sum);
 }
 
-// The sequences that a chunk of rows touches.
+// The sequences that a chunk of rows [t0, t1) touches, with offsets counted from t0.
 struct Span {
-  int64_t first, last;  // of its first and of its last row; n_sequences: none
-  bool staged;          // the offsets from cu_seqlens[first + 1] on are in shared memory
+  int64_t first;  // of row t0
+  int sequences;  // that the chunk's rows may lie in, from `first` on; 0: the rows lie in none
+  int begin;      // where the first sequence of all begins
+  bool staged;    // their ends are in shared memory
 };
-__device__ __forceinline__ Span find_span(const PolicyArgs& a, int64_t t0, int64_t t1,
-                                          int64_t* staged, int64_t* ends) {
+__device__ __forceinline__ int from_chunk(int64_t offset, int64_t t0) {
+  return int(min(max(offset - t0, int64_t(0)), int64_t(1) << 30));
+}
+__device__ __forceinline__ Span find_span(const PolicyArgs& a, int64_t t0, int64_t t1, int* ends,
+                                          int64_t* found) {
   const int warp = threadIdx.x / 32;
   if (warp < 2) {
-    const int64_t s =
-        warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, warp == 0 ? t0 : t1 - 1);
-    if ((threadIdx.x & 31) == 0) ends[warp] = s;
+    const int64_t s = warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, warp == 0 ? t0 : t1 - 1);
+    if ((threadIdx.x & 31) == 0) found[warp] = s;
   }
+  Span span{};
+  span.begin = from_chunk(__ldg(a.cu_seqlens), t0);
   __syncthreads();
-  Span span{ends[0], ends[1], false};
-  span.staged = span.last >= span.first && span.last - span.first < kStaged;
+  span.first = found[0];
+  const int64_t sequences = max(min(found[1] + 1, a.n_sequences) - span.first, int64_t(0));
+  span.staged = sequences <= kStaged;
+  span.sequences = int(min(sequences, a.n_sequences));
   if (span.staged) {
-    for (int64_t i = threadIdx.x; i <= span.last - span.first; i += kThreads)
-      if (span.first + i < a.n_sequences) staged[i] = a.cu_seqlens[span.first + 1 + i];
+    for (int i = threadIdx.x; i < span.sequences; i += kThreads)
+      ends[i] = from_chunk(a.cu_seqlens[span.first + 1 + i], t0);
     __syncthreads();
   }
   return span;
 }
-// The sequence of row t of the chunk.
-__device__ __forceinline__ int64_t sequence_of(const PolicyArgs& a, const Span& span,
-                                               const int64_t* staged, int64_t t) {
-  if (span.staged)
-    return span.first +
-           upper_bound(staged, min(span.last + 1, a.n_sequences) - span.first, t);
-  return upper_bound(a.cu_seqlens + 1, a.n_sequences, t);
+// Which of the span's sequences the chunk's row `r` lies in; span.sequences: in none.
+// It is `lo` or a later one.
+__device__ __forceinline__ int local_sequence(const PolicyArgs& a, const Span& span, const int* ends,
+                                              int64_t t0, int r, int lo) {
+  int hi = span.sequences;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    const int end = span.staged ? ends[mid] : from_chunk(a.cu_seqlens[span.first + 1 + mid], t0);
+    if (end <= r)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
 }
-__device__ __forceinline__ int64_t offset_after(const PolicyArgs& a, const Span& span,
-                                                const int64_t* staged, int64_t s) {
-  const int64_t i = s - span.first;
-  return span.staged && i >= 0 && i <= span.last - span.first ? staged[i] : a.cu_seqlens[s + 1];
+__device__ __forceinline__ int local_end(const PolicyArgs& a, const Span& span, const int* ends,
+                                         int64_t t0, int i) {
+  return span.staged ? ends[i] : from_chunk(a.cu_seqlens[span.first + 1 + i], t0);
 }
 
-__global__ void __launch_bounds__(kThreads) lp_policy_clear_kernel(Header* header, unsigned* counts, int64_t n) {
+__global__ void __launch_bounds__(kThreads)
+    lp_policy_clear_kernel(Header* header, unsigned* counts, int64_t n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (i == 0) header->counted = header->sequences = header->finished = 0;
   if (i < n) counts[i] = 0;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Bit j: byte j of the word is not zero.
+__device__ __forceinline__ unsigned nonzero_bytes(unsigned x) {
+  const unsigned y = __vcmpne4(x, 0u) & 0x01010101u;
+  return (y * 0x10204080u) >> 28;
 }
 
 // First pass: the rows that count, in all or by sequence.
 __global__ void __launch_bounds__(kThreads)
     lp_policy_count_kernel(const __grid_constant__ PolicyArgs a, Header* header, unsigned* counts) {
-  __shared__ int64_t staged[kStaged], ends[2];
+  __shared__ int ends[kStaged];
+  __shared__ int64_t found[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t t0 = int64_t(blockIdx.x) * kChunk, t1 = min(t0 + kChunk, a.T);
+  const int64_t t0 = int64_t(blockIdx.x) * kCountChunk, t1 = min(t0 + kCountChunk, a.T);
   if (!LP_CHECK(t0 < a.T, kChkRowIndex)) return;
-  unsigned kept[kRounds];
+  const int r = int(threadIdx.x) * kCountRun, rows = int(t1 - t0);
+  // bit j: row r + j counts by the mask
+  unsigned kept = r + kCountRun <= rows ? 0xffffu : r < rows ? (1u << (rows - r)) - 1u : 0u;
+  if (a.mask != nullptr && kept != 0) {
+    const uint8_t* mask = a.mask + t0 + r;
+    if (kept == 0xffffu && reinterpret_cast<uintptr_t>(mask) % 16 == 0) {
+      const uint4 m = __ldg(reinterpret_cast<const uint4*>(mask));
+      kept = nonzero_bytes(m.x) | nonzero_bytes(m.y) << 4 | nonzero_bytes(m.z) << 8 |
+             nonzero_bytes(m.w) << 12;
+    } else {
+      unsigned some = 0;
 #pragma unroll
-  for (int k = 0; k < kRounds; ++k)
-    kept[k] = load_mask4(a.mask, t0 + 4 * (threadIdx.x + k * kThreads), a.T, a.wide);
-  Span span{0, 0, false};
-  if (a.cu_seqlens != nullptr) span = find_span(a, t0, t1, staged, ends);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-  unsigned mine = 0, started = 0;
-#pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    const int64_t t = t0 + 4 * (threadIdx.x + k * kThreads);
-    int64_t s = a.n_sequences;
-    unsigned in_s = 0;
-    if (a.cu_seqlens != nullptr && kept[k] != 0) {
-      s = sequence_of(a, span, staged, t);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        while (s < a.n_sequences && offset_after(a, span, staged, s) <= t + j) {
-          if (a.by_sequence && in_s > 0) started += atomicAdd(&counts[s], in_s) == 0 ? 1u : 0u;
-          in_s = 0;
-          ++s;
-        }
-        if (s == a.n_sequences || t + j < a.cu_seqlens[0]) kept[k] &= ~(1u << j);
-        in_s += kept[k] >> j & 1u;
-      }
+      for (int j = 0; j < kCountRun; ++j)
+        if (kept >> j & 1u) some |= mask[j] != 0 ? 1u << j : 0u;
+      kept = some;
     }
-    mine += __popc(kept[k]);
-    if (!a.by_sequence) continue;
-    // a warp's 128 rows mostly lie in one sequence
-    int same;
-    __match_all_sync(0xffffffffu, static_cast<unsigned long long>(s), &same);
-    if (same) in_s = __reduce_add_sync(0xffffffffu, in_s);
-    if (in_s > 0 && (!same || (threadIdx.x & 31) == 0))
-      started += atomicAdd(&counts[s], in_s) == 0 ? 1u : 0u;
   }
-  mine = __reduce_add_sync(0xffffffffu, a.by_sequence ? started : mine);
+  Span span{};
+  if (a.cu_seqlens != nullptr) span = find_span(a, t0, t1, ends, found);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+  unsigned mine = 0, in_last = 0;
+  int last = -1;  // the sequence of the thread's last row
+  if (a.cu_seqlens == nullptr) {
+    mine = __popc(kept);
+  } else {
+    if (r < span.begin) kept &= span.begin - r >= 32 ? 0u : ~0u << (span.begin - r);
+    int i = kept != 0 ? local_sequence(a, span, ends, t0, r, 0) : span.sequences;
+    unsigned left = kept;
+    while (left != 0 && i < span.sequences) {
+      const int run = local_end(a, span, ends, t0, i) - r;  // rows up to the sequence's end
+      const unsigned here = run >= 32 ? left : left & ((1u << max(run, 0)) - 1u);
+      left &= ~here;
+      const unsigned n = __popc(here);
+      if (!a.by_sequence) {
+        mine += n;
+      } else if (left == 0) {
+        in_last = n;
+        last = i;
+      } else if (n > 0) {
+        mine += atomicAdd(&counts[span.first + i], n) == 0 ? 1u : 0u;
+      }
+      ++i;
+    }
+  }
+  if (a.by_sequence) {
+    // a warp's 512 rows mostly end in one sequence
+    int same;
+    __match_all_sync(0xffffffffu, last, &same);
+    if (same) in_last = __reduce_add_sync(0xffffffffu, in_last);
+    if (in_last > 0 && (!same || (threadIdx.x & 31) == 0))
+      mine += atomicAdd(&counts[span.first + last], in_last) == 0 ? 1u : 0u;
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
   if ((threadIdx.x & 31) == 0 && mine > 0)
     atomicAdd(a.by_sequence ? &header->sequences : &header->counted, mine);
 }
 
-// Second pass: weights, terms, gradients, and the sums by the CTA that finishes last.
-__global__ void __launch_bounds__(kThreads)
-    lp_policy_rows_kernel(const __grid_constant__ PolicyArgs a, Header* header, const unsigned* counts,
-                          float4* partials) {
-  __shared__ int64_t staged[kStaged], ends[2];
+// Second pass: weights, terms, gradients, and the sums by the CTA that finishes last.  A CTA has a
+// stretch of neighbouring rows, so that it looks for its sequences once; the rows of its next turn
+// (of its first, before the first pass is waited for) are on their way while it computes.
+__global__ void __launch_bounds__(kThreads, 4)
+    lp_policy_rows_kernel(const __grid_constant__ PolicyArgs a, int64_t chunk, Header* header,
+                          const unsigned* counts, float4* partials) {
+  __shared__ int ends[kStaged];
+  __shared__ float weights[kStaged], advantages[kStaged];
+  __shared__ int64_t found[2];
   __shared__ float slots[kThreads / 32][kStats];
   __shared__ bool last;
-  const int64_t t0 = int64_t(blockIdx.x) * kChunk, t1 = min(t0 + kChunk, a.T);
+  const int64_t t0 = int64_t(blockIdx.x) * chunk, t1 = min(t0 + chunk, a.T);
   if (!LP_CHECK(t0 < a.T, kChkRowIndex)) return;
-  Span span{0, 0, false};
-  if (a.cu_seqlens != nullptr) span = find_span(a, t0, t1, staged, ends);
+  const int rows = int(t1 - t0);
+  int r = 4 * int(threadIdx.x);
+  Four next;
+  unsigned next_kept = load_mask4(a.mask, t0 + r, t1, a.wide);
+  load_rows(a, t0 + r, t1, next);
+  Span span{};
+  if (a.cu_seqlens != nullptr) span = find_span(a, t0, t1, ends, found);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are done
   const unsigned whole = __ldcg(a.by_sequence ? &header->sequences : &header->counted);
-  float sum[kStats] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int k = 0; k < kRounds; ++k) {
-    const int64_t t = t0 + 4 * (threadIdx.x + k * kThreads);
-    if (t >= a.T) break;
-    Four f;
-    unsigned kept = load_mask4(a.mask, t, a.T, a.wide);
-    load_rows(a, t, f);
-    float w[4];
-    int64_t s = a.cu_seqlens != nullptr && kept != 0 ? sequence_of(a, span, staged, t) : 0;
-    int64_t known = -1;
-    float weight = weight_of(false, 0u, whole), advantage = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!(kept >> j & 1u)) continue;
-      if (a.cu_seqlens != nullptr) {
-        while (s < a.n_sequences && offset_after(a, span, staged, s) <= t + j) ++s;
-        if (s == a.n_sequences || t + j < a.cu_seqlens[0]) {
-          kept &= ~(1u << j);
-          continue;
-        }
-        if (s != known) {
-          known = s;
-          if (a.by_sequence) weight = weight_of(true, __ldcg(counts + s), whole);
-          if (a.per_sequence) advantage = __ldg(a.advantages + s);
-        }
-        if (a.per_sequence) f.advantage[j] = advantage;
-      }
-      w[j] = weight;
+  if (a.cu_seqlens != nullptr && span.staged) {
+    for (int i = threadIdx.x; i < span.sequences; i += kThreads) {
+      weights[i] = weight_of(a.by_sequence, a.by_sequence ? __ldcg(counts + span.first + i) : 0u, whole);
+      if (a.per_sequence) advantages[i] = __ldg(a.advantages + span.first + i);
     }
-    finish_rows(a, t, f, kept, w, sum);
+    __syncthreads();
+  }
+  const float of_all = weight_of(false, 0u, whole);
+  float sum[kStats] = {0.f, 0.f, 0.f, 0.f};
+  int i = 0;  // the sequence of the thread's next row, or one before it
+  for (; r < rows; r += kTurn) {
+    Four four = next;
+    unsigned kept = next_kept;
+    next_kept = load_mask4(a.mask, t0 + r + kTurn, t1, a.wide);
+    load_rows(a, t0 + r + kTurn, t1, next);
+    float w[4] = {of_all, of_all, of_all, of_all};
+    if (a.cu_seqlens != nullptr && kept != 0) {
+      i = local_sequence(a, span, ends, t0, r, i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        while (i < span.sequences && local_end(a, span, ends, t0, i) <= r + j) ++i;
+        if (i == span.sequences || r + j < span.begin) {
+          kept &= ~(1u << j);
+        } else if (span.staged) {
+          w[j] = weights[i];
+          if (a.per_sequence) four.advantage[j] = advantages[i];
+        } else {
+          if (a.by_sequence) w[j] = weight_of(true, __ldcg(counts + span.first + i), whole);
+          if (a.per_sequence) four.advantage[j] = __ldg(a.advantages + span.first + i);
+        }
+      }
+    }
+    finish_rows(a, t0 + r, t1, four, kept, w, sum);
   }
   cta_sum<kThreads>(sum, slots);
   if (threadIdx.x == 0) {
@@ -387,6 +444,7 @@ __global__ void __launch_bounds__(kThreads)
   __threadfence();
 #pragma unroll
   for (int k = 0; k < kStats; ++k) sum[k] = 0.f;
+#pragma unroll 4
   for (int64_t i = threadIdx.x; i < gridDim.x; i += kThreads) {
     const float4 p = __ldcg(partials + i);
     sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
@@ -398,7 +456,7 @@ __global__ void __launch_bounds__(kThreads)
 bool one_cta(int64_t T, int64_t n_sequences) {
   return T <= kSmallRows && n_sequences <= kSmallSequences;
 }
-int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
+int64_t chunks_of(int64_t T) { return T > 0 ? (T + chunk_of(T) - 1) / chunk_of(T) : 0; }
 
 template <class... Params, class... Args>
 bool launch_dependent(void (*kernel)(Params...), int64_t blocks, cudaStream_t stream, Args... args) {
@@ -445,8 +503,9 @@ lp_status launch_policy_loss(const PolicyArgs& args, cudaStream_t stream) {
   const int64_t chunks = chunks_of(a.T);
   lp_policy_clear_kernel<<<unsigned(cleared / kThreads + 1), kThreads, 0, stream>>>(header, counts, cleared);
   if (cudaGetLastError() != cudaSuccess) return LP_ERR_CUDA;
-  if (!launch_dependent(lp_policy_count_kernel, chunks, stream, a, header, counts) ||
-      !launch_dependent(lp_policy_rows_kernel, chunks, stream, a, header,
+  if (!launch_dependent(lp_policy_count_kernel, (a.T + kCountChunk - 1) / kCountChunk, stream, a, header,
+                        counts) ||
+      !launch_dependent(lp_policy_rows_kernel, chunks, stream, a, chunk_of(a.T), header,
                         static_cast<const unsigned*>(counts), partials))
     return LP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
