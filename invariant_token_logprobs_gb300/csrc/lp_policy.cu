@@ -416,18 +416,29 @@ __global__ void __launch_bounds__(kThreads, 4)
     load_rows(a, t0 + r + kTurn, t1, next);
     float w[4] = {of_all, of_all, of_all, of_all};
     if (a.cu_seqlens != nullptr && kept != 0) {
-      i = local_sequence(a, span, ends, t0, r, i);
+      if (i < span.sequences && local_end(a, span, ends, t0, i) <= r)
+        i = local_sequence(a, span, ends, t0, r, i + 1);
+      if (span.staged && i < span.sequences && r >= span.begin && r + 4 <= ends[i]) {
+        const float weight = weights[i];  // mostly all four rows lie in one sequence
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        while (i < span.sequences && local_end(a, span, ends, t0, i) <= r + j) ++i;
-        if (i == span.sequences || r + j < span.begin) {
-          kept &= ~(1u << j);
-        } else if (span.staged) {
-          w[j] = weights[i];
-          if (a.per_sequence) four.advantage[j] = advantages[i];
-        } else {
-          if (a.by_sequence) w[j] = weight_of(true, __ldcg(counts + span.first + i), whole);
-          if (a.per_sequence) four.advantage[j] = __ldg(a.advantages + span.first + i);
+        for (int j = 0; j < 4; ++j) w[j] = weight;
+        if (a.per_sequence) {
+          const float advantage = advantages[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) four.advantage[j] = advantage;
+        }
+      } else {
+        int s = i;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          while (s < span.sequences && local_end(a, span, ends, t0, s) <= r + j) ++s;
+          if (s == span.sequences || r + j < span.begin) {
+            kept &= ~(1u << j);
+          } else {
+            const int64_t at = span.first + s;
+            if (a.by_sequence) w[j] = weight_of(true, __ldcg(counts + at), whole);
+            if (a.per_sequence) four.advantage[j] = __ldg(a.advantages + at);
+          }
         }
       }
     }
