@@ -17,6 +17,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,6 +31,9 @@ HEADERS = [os.path.join(ROOT, "include", f) for f in ("lp.h", "lp_train.h")] + [
     os.path.join(CSRC, f) for f in ("lp_device.cuh", "lp_internal.h", "lp_tcgen05.cuh",
                                     "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh")
 ]
+# the Python calls of train.py: host code against torch's headers, no part of liblp
+CALLS_SOURCE = os.path.join(CSRC, "train_calls.cpp")
+CALLS = os.path.join(BUILD, "_train_calls.so")
 # the checked build (-DLP_CHECKED: index and coordinate tests in every kernel)
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "liblp.so")
@@ -85,6 +90,53 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{res.stdout}\n{res.stderr}")
     return obj
+
+
+def _calls_command(out: str) -> list[str]:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = os.path.join(root, "include")
+    libs = os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", sysconfig.get_paths()["include"], "-I", include,
+            "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", cuda,
+            CALLS_SOURCE, "-o", out, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+
+
+def calls_hash() -> str:
+    """SHA-256 over train.py's compiled calls: their source, the header, the command (which names
+    the flags and torch) and the versions of torch and Python."""
+    import torch
+    h = hashlib.sha256()
+    for path in (CALLS_SOURCE, HEADERS[0], HEADERS[1]):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    h.update(" ".join(_calls_command(CALLS)).encode())
+    h.update(f"{torch.__version__} {sys.version}".encode())
+    return h.hexdigest()
+
+
+def build_calls(force: bool = False, quiet: bool = False) -> str:
+    """Compile _train_calls.so unless it was built from exactly this source; return its path."""
+    digest, stamp = calls_hash(), CALLS + ".sha256"
+    if not force and os.path.exists(CALLS) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == digest:
+                return CALLS
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = f"{CALLS}.{os.getpid()}.tmp"
+    res = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for train_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS)
+    with open(stamp, "w") as f:
+        f.write(digest + "\n")
+    if not quiet:
+        print("train calls: compiled", flush=True)
+    return CALLS
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False,

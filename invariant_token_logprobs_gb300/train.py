@@ -7,7 +7,9 @@ ctypes binding of the entry points declared in include/lp_train.h.
     optimizer = AdamW(params, grads, copies=..., state_bits=8); optimizer.step(max_norm=1.0)
 
 Argument marshalling only, as in lp.py: every step of the computation runs in
-liblp's kernels on the current stream, and there is no fallback.  A call given
+liblp's kernels on the current stream, and there is no fallback.  The calls'
+checks and allocations are compiled (csrc/train_calls.cpp, built next to liblp),
+since the smallest ones take 3 us on the GPU.  A call given
 another stream runs there, its outputs and workspace are allocated for that
 stream, and ordering it after the work that made its inputs is the caller's.
 """
@@ -15,13 +17,15 @@ stream, and ordering it after the work that made its inputs is the caller's.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
-from . import lp
+from . import _build_lib, lp
 from .lp import LpError
 
 __all__ = [
@@ -33,6 +37,7 @@ __all__ = [
     "ADAMW_BLOCK",
     "declared_symbols",
     "load",
+    "load_calls",
     "residual_norm",
     "residual_norm_backward",
     "residual_norm_backward_workspace_size",
@@ -87,6 +92,13 @@ _SIGNATURES = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
+_calls = None
+
+# what train_calls.cpp calls, in the order of its table
+_BOUND = ("lp_residual_norm", "lp_residual_norm_backward_workspace_size",
+          "lp_residual_norm_backward", "lp_policy_loss_workspace_size", "lp_policy_loss",
+          "lp_adamw_grad_norm_workspace_size", "lp_adamw_grad_norm", "lp_adamw_step",
+          "lp_adamw_state_values")
 
 
 def declared_symbols() -> list[str]:
@@ -109,56 +121,31 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-_CODES = {torch.float32: FLOAT32, torch.bfloat16: BFLOAT16}
-_current_stream = torch._C._cuda_getCurrentRawStream  # what current_stream().cuda_stream is
+def load_calls():
+    """The compiled calls, bound to the loaded library's entry points."""
+    global _calls
+    if _calls is None:
+        lib, path = load(), _build_lib.build_calls(quiet=True)
+        loader = importlib.machinery.ExtensionFileLoader("_train_calls", path)
+        spec = importlib.util.spec_from_file_location("_train_calls", path, loader=loader)
+        calls = importlib.util.module_from_spec(spec)
+        loader.exec_module(calls)
+        calls.bind(LpError, tuple(ctypes.cast(getattr(lib, f), _vp).value for f in _BOUND))
+        _calls = calls
+    return _calls
 
 
 def _dtype_code(t: torch.Tensor, what: str) -> int:
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{what} must be float32 or bfloat16")
-    return code
+    if t.dtype == torch.bfloat16:
+        return BFLOAT16
+    if t.dtype == torch.float32:
+        return FLOAT32
+    raise TypeError(f"{what} must be float32 or bfloat16")
 
 
-def _device_of(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """The index of the CUDA device that holds all of them."""
-    index = first.get_device()
-    if index < 0:
-        raise ValueError("expected CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError("expected CUDA tensors of one device")
-    return index
-
-
-def _ld(t: Optional[torch.Tensor], shape, what: str) -> int:
-    """Row stride of a 2-D operand of `shape`; a single row may have any stride."""
-    if t is None:
-        return 0
-    if t.shape != shape:
-        raise ValueError(f"{what} must have the shape {tuple(shape)}")
-    ld, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
-        raise ValueError(f"{what} must have contiguous rows")
-    return ld if shape[0] > 1 else shape[1]
-
-
-def _vector(t: Optional[torch.Tensor], n: int, what: str, dtype=torch.float32) -> None:
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {str(dtype)[6:]}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous vector of {n}")
-
-
-def _same_dtype(t: Optional[torch.Tensor], dtype, what: str) -> None:
-    if t is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {str(dtype)[6:]}")
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _on_one_device(tensors: Sequence[torch.Tensor]) -> None:
+    if not all(t.is_cuda and t.device == tensors[0].device for t in tensors):
+        raise ValueError("expected CUDA tensors of one device")
 
 
 def _on_stream(stream, call, *args, **kw):
@@ -186,35 +173,6 @@ class ResidualNormGrad(NamedTuple):
     gate: Optional[torch.Tensor]           # [T, d] in the gate's dtype, or [d] float32
 
 
-def _norm_operands(residual, branch, gate, branch_weight, weight, act):
-    """(residual_dtype, act_dtype, weight_dtype, ld_residual, ld_branch, ld_gate) of the operands
-    that forward and backward share, checked; `act` has the activations' dtype."""
-    shape = residual.shape
-    if len(shape) != 2:
-        raise ValueError("expected a 2-D residual")
-    ld_gate = 0
-    if gate is not None:
-        if gate.dtype != act.dtype:
-            raise TypeError(f"gate must be {str(act.dtype)[6:]}")
-        if gate.dim() == 1:
-            _vector(gate, shape[1], "gate", act.dtype)
-        else:
-            ld_gate = _ld(gate, shape, "gate")
-            if ld_gate < shape[1]:
-                raise ValueError("gate rows overlap: pass one row [d] for all")
-    weight_dtype = FLOAT32
-    if weight is not None:
-        weight_dtype = _dtype_code(weight, "weight")
-        _vector(weight, shape[1], "weight", weight.dtype)
-    if branch_weight is not None:
-        weight_dtype = _dtype_code(branch_weight, "branch_weight")
-        _vector(branch_weight, shape[1], "branch_weight", branch_weight.dtype)
-        if weight is not None and weight.dtype != branch_weight.dtype:
-            raise TypeError("weight and branch_weight must have one dtype")
-    return (_dtype_code(residual, "residual"), _dtype_code(act, "activations"), weight_dtype,
-            _ld(residual, shape, "residual"), _ld(branch, shape, "branch"), ld_gate)
-
-
 def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None, *,
                   weight: Optional[torch.Tensor] = None,
                   branch_weight: Optional[torch.Tensor] = None,
@@ -233,31 +191,8 @@ def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
         return _on_stream(stream, residual_norm, residual, branch, weight=weight,
                           branch_weight=branch_weight, gate=gate, residual_scale=residual_scale,
                           branch_scale=branch_scale, eps=eps, in_place=in_place)
-    act = residual if branch is None else branch
-    index = _device_of(residual, branch, gate, branch_weight, weight)
-    residual_dtype, act_dtype, weight_dtype, ld, ld_branch, ld_gate = _norm_operands(
-        residual, branch, gate, branch_weight, weight, act)
-    T, d = residual.shape
-    device = residual.device
-    new, out, ld_out = residual, None, ld
-    if branch is not None:
-        if not in_place:
-            new, ld_out = torch.empty((T, d), dtype=residual.dtype, device=device), d
-        out = new.data_ptr()
-    normed = rstd = branch_rstd = None
-    if weight is not None:
-        normed = torch.empty((T, d), dtype=act.dtype, device=device)
-        rstd = torch.empty(T, dtype=torch.float32, device=device)
-    if branch_weight is not None:
-        branch_rstd = torch.empty(T, dtype=torch.float32, device=device)
-    status = load().lp_residual_norm(
-        residual.data_ptr(), ld, residual_dtype, _ptr(branch), ld_branch, _ptr(gate), ld_gate,
-        act_dtype, _ptr(branch_weight), _ptr(weight), weight_dtype, T, d, residual_scale,
-        branch_scale, eps, out, ld_out, _ptr(normed), d, _ptr(branch_rstd), _ptr(rstd),
-        _current_stream(index))
-    if status != 0:
-        raise LpError("lp_residual_norm", status)
-    return ResidualNorm(normed, new, rstd, branch_rstd)
+    return ResidualNorm._make((_calls or load_calls()).residual_norm(
+        residual, branch, weight, branch_weight, gate, residual_scale, branch_scale, eps, in_place))
 
 
 def residual_norm_backward_workspace_size(T: int, d: int) -> int:
@@ -286,48 +221,9 @@ def residual_norm_backward(grad_normed: Optional[torch.Tensor],
                           branch_rstd=branch_rstd, gate=gate, residual_scale=residual_scale,
                           branch_scale=branch_scale, weight_grads=weight_grads,
                           workspace=workspace)
-    act = residual if branch is None else branch
-    index = _device_of(residual, grad_normed, grad_residual, branch, gate, branch_weight, weight,
-                       rstd, branch_rstd, workspace)
-    residual_dtype, act_dtype, weight_dtype, ld, ld_branch, ld_gate = _norm_operands(
-        residual, branch, gate, branch_weight, weight, act)
-    shape = residual.shape
-    T, d = shape
-    _same_dtype(grad_normed, act.dtype, "grad_normed")
-    _same_dtype(grad_residual, residual.dtype, "grad_residual")
-    _vector(rstd, T, "rstd")
-    _vector(branch_rstd, T, "branch_rstd")
-    lib, device = load(), residual.device
-    out = torch.empty((T, d), dtype=residual.dtype, device=device)
-    grad_branch = grad_gate = grad_weight = grad_branch_weight = None
-    if branch is not None:
-        grad_branch = torch.empty((T, d), dtype=act.dtype, device=device)
-    if gate is not None and ld_gate != 0:
-        grad_gate = torch.empty((T, d), dtype=gate.dtype, device=device)
-    size = 0
-    if weight_grads:
-        if gate is not None and ld_gate == 0:
-            grad_gate = torch.empty(d, dtype=torch.float32, device=device)
-        if weight is not None:
-            grad_weight = torch.empty(d, dtype=torch.float32, device=device)
-        if branch_weight is not None:
-            grad_branch_weight = torch.empty(d, dtype=torch.float32, device=device)
-        if workspace is None:
-            size = lib.lp_residual_norm_backward_workspace_size(T, d)
-            workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=device)
-        else:
-            size = workspace.numel() * workspace.element_size()
-    status = lib.lp_residual_norm_backward(
-        residual.data_ptr() if weight is not None else None, ld, residual_dtype, _ptr(branch),
-        ld_branch, _ptr(gate), ld_gate, act_dtype, _ptr(branch_weight), _ptr(weight), weight_dtype,
-        T, d, residual_scale, branch_scale, _ptr(branch_rstd), _ptr(rstd), _ptr(grad_normed),
-        _ld(grad_normed, shape, "grad_normed"), _ptr(grad_residual),
-        _ld(grad_residual, shape, "grad_residual"), out.data_ptr(), d, _ptr(grad_branch), d,
-        _ptr(grad_gate), d, _ptr(grad_branch_weight), _ptr(grad_weight), _ptr(workspace), size,
-        _current_stream(index))
-    if status != 0:
-        raise LpError("lp_residual_norm_backward", status)
-    return ResidualNormGrad(out, grad_branch, grad_weight, grad_branch_weight, grad_gate)
+    return ResidualNormGrad._make((_calls or load_calls()).residual_norm_backward(
+        grad_normed, grad_residual, residual, rstd, branch, weight, branch_weight, branch_rstd, gate,
+        residual_scale, branch_scale, weight_grads, workspace))
 
 
 # ------------------------------------------------------------------ policy loss
@@ -363,48 +259,11 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
                           reduction=reduction, per_sequence=per_sequence, clip_low=clip_low,
                           clip_high=clip_high, kl_coef=kl_coef, entropy_coef=entropy_coef,
                           workspace=workspace)
-    if logp.dim() != 1:
-        raise ValueError("expected a 1-D logp")
     if reduction not in ("token", "sequence"):
         raise ValueError("reduction must be 'token' or 'sequence'")
-    index = _device_of(logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens, workspace)
-    T = logp.shape[0]
-    _vector(logp, T, "logp")
-    _vector(old_logp, T, "old_logp")
-    _vector(ref_logp, T, "ref_logp")
-    _vector(entropy, T, "entropy")
-    n = 0
-    by_sequence = reduction == "sequence"
-    if by_sequence or per_sequence:
-        if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-            raise ValueError("cu_seqlens [n + 1] is needed")
-        n = cu_seqlens.shape[0] - 1
-        _vector(cu_seqlens, n + 1, "cu_seqlens", torch.int64)
-    else:
-        cu_seqlens = None
-    _vector(advantages, n if per_sequence else T, "advantages")
-    if mask is not None:
-        _vector(mask, T, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool)
-    lib, device = load(), logp.device
-    stats = torch.empty(5, dtype=torch.float32, device=device)
-    grad_logp = torch.empty(T, dtype=torch.float32, device=device)
-    grad_entropy = None
-    if entropy is not None:
-        grad_entropy = torch.empty(T, dtype=torch.float32, device=device)
-    if workspace is None:
-        size = lib.lp_policy_loss_workspace_size(T, n)
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    else:
-        size = workspace.numel() * workspace.element_size()
-    status = lib.lp_policy_loss(
-        logp.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp), _ptr(entropy), _ptr(advantages),
-        int(per_sequence), _ptr(mask), _ptr(cu_seqlens), T, n,
-        REDUCE_SEQUENCE if by_sequence else REDUCE_TOKEN, clip_low, clip_high, kl_coef,
-        entropy_coef, stats.data_ptr(), grad_logp.data_ptr(), _ptr(grad_entropy),
-        workspace.data_ptr(), size, _current_stream(index))
-    if status != 0:
-        raise LpError("lp_policy_loss", status)
-    return PolicyLoss(stats, grad_logp, grad_entropy)
+    return PolicyLoss._make((_calls or load_calls()).policy_loss(
+        logp, old_logp, advantages, mask, ref_logp, entropy, cu_seqlens, reduction == "sequence",
+        per_sequence, clip_low, clip_high, kl_coef, entropy_coef, workspace))
 
 
 # ------------------------------------------------------------------------ AdamW
@@ -469,7 +328,7 @@ class AdamW:
         if len(self.grads) != len(self.params):
             raise ValueError("grads must have one tensor for each param")
         written = self.params + [c for c in self.copies if c is not None]
-        self._index = _device_of(*written, *self.grads)
+        _on_one_device(written + self.grads)
         for p, g in zip(self.params, self.grads):
             _dtype_code(g, "gradients")
             if g.shape != p.shape or not g.is_contiguous():
@@ -479,7 +338,7 @@ class AdamW:
         lib = load()
         n = len(self.params)
         records = (_AdamwTensor * n)(*[
-            _AdamwTensor(p.data_ptr(), _ptr(c), g.data_ptr(), p.numel(), s, w,
+            _AdamwTensor(p.data_ptr(), None if c is None else c.data_ptr(), g.data_ptr(), p.numel(), s, w,
                          _dtype_code(g, "gradients"), 0)
             for p, c, g, s, w in zip(self.params, self.copies, self.grads, self.lr_scale,
                                      self.weight_decay)])
@@ -503,8 +362,9 @@ class AdamW:
                 t = torch.zeros(count, dtype=dtype, device=device)
             else:
                 t = state[name]
-                _vector(t, count, name, dtype)
-                _device_of(self.params[0], t)
+                if t.dtype != dtype or t.shape != (count,) or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector of {count}")
+                _on_one_device([self.params[0], t])
             setattr(self, name, t)
 
     def state_dict(self) -> dict:
@@ -519,27 +379,12 @@ class AdamW:
         is not finite leaves every param and moment as it was (the step is counted)."""
         if stream is not None:
             return _on_stream(stream, self.step, lr, max_norm)
-        lib, plan, n = load(), self._plan.data_ptr(), len(self.params)
-        elements, current = self.state_elements, _current_stream(self._index)
-        norm = scale = None
-        if max_norm is not None:
-            norm = torch.empty(2, dtype=torch.float32, device=self._plan.device)
-            size = lib.lp_adamw_grad_norm_workspace_size(elements)
-            work = torch.empty(size, dtype=torch.uint8, device=self._plan.device)
-            status = lib.lp_adamw_grad_norm(plan, n, elements, max_norm, norm.data_ptr(),
-                                            work.data_ptr(), size, current)
-            if status != 0:
-                raise LpError("lp_adamw_grad_norm", status)
-            scale = norm.data_ptr() + 4
-        status = lib.lp_adamw_step(
-            plan, n, elements, self.state_bits, self.exp_avg.data_ptr(),
-            self.exp_avg_sq.data_ptr(), _ptr(self.exp_avg_scale), _ptr(self.exp_avg_sq_scale),
-            self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
-            self.step_count + 1, self.seed, scale, current)
-        if status != 0:
-            raise LpError("lp_adamw_step", status)
+        norm = (_calls or load_calls()).adamw_step(
+            self._plan, len(self.params), self.state_elements, self.state_bits, self.exp_avg,
+            self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.lr if lr is None else lr,
+            self.betas[0], self.betas[1], self.eps, self.step_count + 1, self.seed, max_norm)
         self.step_count += 1
-        return None if norm is None else norm[0]
+        return norm
 
     def state_values(self, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         """(first moment, second moment) as flat float32: the buffers themselves for 32-bit
@@ -548,16 +393,8 @@ class AdamW:
             return self.exp_avg, self.exp_avg_sq
         if stream is not None:
             return _on_stream(stream, self.state_values)
-        n, device = self.state_elements, self.exp_avg.device
-        m = torch.empty(n, dtype=torch.float32, device=device)
-        v = torch.empty(n, dtype=torch.float32, device=device)
-        status = load().lp_adamw_state_values(
-            self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), self.exp_avg_scale.data_ptr(),
-            self.exp_avg_sq_scale.data_ptr(), n, m.data_ptr(), v.data_ptr(),
-            _current_stream(self._index))
-        if status != 0:
-            raise LpError("lp_adamw_state_values", status)
-        return m, v
+        return (_calls or load_calls()).adamw_state_values(
+            self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
 
     def views(self, flat: torch.Tensor) -> list[torch.Tensor]:
         """The part of a flat moment buffer that belongs to each param, in its shape."""
