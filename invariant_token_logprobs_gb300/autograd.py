@@ -1,14 +1,18 @@
-"""torch.autograd bindings of the fused path and of the logits path.
+"""torch.autograd bindings of the fused path, of the logits path and of the
+training-step operators.
 
     logp, entropy = linear_logprob(H, W, y, temperature=1.0)
     logp, entropy = logprob_from_logits(z, y, temperature=1.0)
     logp, entropy = vocab_parallel_linear_logprob(H, W_shard, y, V, group)
     logp, entropy = vocab_parallel_logprob_from_logits(z_shard, y, V, group)
+    h, residual   = residual_norm(residual, branch, weight=..., branch_weight=..., gate=...)
+    loss, stats   = policy_loss(logp, old_logp, advantages, entropy=entropy, ...)
 
-returns the selected-token log-probabilities and entropies of z = H W^T / tau
-(lp_linear_logprob_lse) and back-propagates into H and W through
+The first four return the selected-token log-probabilities and entropies of
+z = H W^T / tau (lp_linear_logprob_lse) and back-propagate into H and W through
 lp_linear_logprob_backward with the forward's log Z and entropy kept, so the
-backward does not recompute them.  This is argument marshalling only: every
+backward does not recompute them.  The last two are train.residual_norm and
+train.policy_loss, on either side of them in a training step.  This is argument marshalling only: every
 step runs in liblp's kernels, on the current stream.
 
 The vocabulary-parallel forms run on every rank of a torch.distributed group
@@ -28,9 +32,11 @@ use contributes nothing (its upstream gradient is passed as absent).
 
 from __future__ import annotations
 
+from typing import Optional
+
 import torch
 
-from . import lp
+from . import lp, train
 from . import vocab_parallel as vp
 
 
@@ -165,3 +171,80 @@ def vocab_parallel_logprob_from_logits(z_shard: torch.Tensor, y: torch.Tensor, v
     of `group`, differentiable in z_shard (its columns of dL/dz; no exchange in
     the backward)."""
     return _VocabParallelLogprobFromLogits.apply(z_shard, y, vocab_total, group, temperature)
+
+
+def _rows(g):
+    """A gradient as rows that the library can read."""
+    return g if g is None or (g.stride(1) == 1 and g.stride(0) >= g.shape[1]) else g.contiguous()
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, residual, branch, weight, branch_weight, gate, residual_scale, branch_scale,
+                eps):
+        out = train.residual_norm(residual, branch, weight=weight, branch_weight=branch_weight,
+                                  gate=gate, residual_scale=residual_scale,
+                                  branch_scale=branch_scale, eps=eps)
+        ctx.save_for_backward(branch, weight, branch_weight, gate, out.residual, out.rstd,
+                              out.branch_rstd)
+        ctx.scales = float(residual_scale), float(branch_scale)
+        ctx.set_materialize_grads(False)
+        # without a branch the stream is the input, which is no output of this function
+        return out.normed, None if branch is None else out.residual
+
+    @staticmethod
+    def backward(ctx, g_normed, g_residual):
+        branch, weight, branch_weight, gate, residual, rstd, branch_rstd = ctx.saved_tensors
+        if g_normed is None and g_residual is None:
+            return (None,) * 8
+        if weight is not None and g_normed is None:
+            g_normed = torch.zeros_like(residual if branch is None else branch)
+        _, _, need_w, need_bw, need_gate = ctx.needs_input_grad[:5]
+        row_gate = gate is not None and gate.dim() == 1
+        g = train.residual_norm_backward(
+            _rows(g_normed), _rows(g_residual), residual, rstd, branch=branch, weight=weight,
+            branch_weight=branch_weight, branch_rstd=branch_rstd, gate=gate,
+            residual_scale=ctx.scales[0], branch_scale=ctx.scales[1],
+            weight_grads=need_w or need_bw or (need_gate and row_gate))
+        cast = lambda t, like: None if t is None else t.to(like.dtype)  # noqa: E731
+        return (g.residual, g.branch, cast(g.weight, weight), cast(g.branch_weight, branch_weight),
+                cast(g.gate, gate), None, None, None)
+
+
+def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None, *,
+                  weight: Optional[torch.Tensor] = None,
+                  branch_weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                  branch_scale: float = 1.0, eps: float = 1e-6):
+    """(normed, new residual stream) of train.residual_norm, differentiable in the residual, the
+    branch, both weights and the gate; the backward is lp_residual_norm_backward with the
+    forward's reciprocal roots kept.  Gradients come in the inputs' dtypes (those of the weights
+    and of a one-row gate are float32 sums rounded once)."""
+    normed, new = _ResidualNorm.apply(residual, branch, weight, branch_weight, gate,
+                                      residual_scale, branch_scale, eps)
+    return normed, residual if branch is None else new
+
+
+class _PolicyLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, entropy, old_logp, advantages, kw):
+        out = train.policy_loss(logp, old_logp, advantages, entropy=entropy, **kw)
+        ctx.save_for_backward(out.grad_logp, out.grad_entropy)
+        ctx.mark_non_differentiable(out.stats)
+        return out.stats[0].clone(), out.stats
+
+    @staticmethod
+    def backward(ctx, g_loss, _):
+        g_logp, g_entropy = ctx.saved_tensors
+        need_logp, need_entropy = ctx.needs_input_grad[:2]
+        return (g_logp * g_loss if need_logp else None,
+                g_entropy * g_loss if need_entropy and g_entropy is not None else None,
+                None, None, None)
+
+
+def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
+                entropy: Optional[torch.Tensor] = None, **kw):
+    """(loss, stats [5]) of train.policy_loss, the loss a float32 scalar that is differentiable in
+    logp and entropy: the gradients are written by the forward call and scaled in the backward.
+    Keyword arguments are train.policy_loss's."""
+    return _PolicyLoss.apply(logp, entropy, old_logp, advantages, kw)

@@ -262,8 +262,9 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
   const int64_t row = blockIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int32_t index = a.table[row];
-  if (!LP_CHECK(index >= 0 && index < a.n_tensors, kChkPlan)) return;
+  if (!LP_CHECK(row < a.rows && index >= 0 && index < a.n_tensors, kChkPlan)) return;
   const AdamwRecord rec = a.records[index];
+  if (!LP_CHECK(row >= rec.first_row && (row - rec.first_row) * kRow < rec.n, kChkPlan)) return;
   const float clip = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
   if (clip != clip) return;
   const float lr = a.lr * rec.lr_scale;
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kThreads)
   const int32_t index = table[row];
   if (!LP_CHECK(index >= 0 && index < n_tensors, kChkPlan)) return;
   const AdamwRecord rec = records[index];
+  if (!LP_CHECK(row >= rec.first_row && (row - rec.first_row) * kRow < rec.n, kChkPlan)) return;
   const int64_t first = (row - rec.first_row) * kRow;
   const int count = int(min(rec.n - first, int64_t(kRow)));
   float s = 0.f;
