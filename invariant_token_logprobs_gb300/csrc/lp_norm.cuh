@@ -170,27 +170,38 @@ struct Stream {
       }
       // the warp's stretch, 32 neighbours an access
       const int first = 8 * (p.i - p.lane + k * p.team);
-      const uint32_t stretch = to - 8 * p.lane * int(sizeof(T));
+      const bool whole = mine && first + 256 <= p.d;
       const int d = mine ? p.d : 0;
       if (access != kPlain) {
         constexpr int kOf4 = 4 / sizeof(T);
+        const uint32_t stretch = to - 8 * p.lane * int(sizeof(T)) + 4 * p.lane;
+        const T* from = row + first + p.lane * kOf4;
+        if (whole) {
+#pragma unroll
+          for (int q = 0; q < 2 * int(sizeof(T)); ++q)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stretch + 128 * q),
+                         "l"(from + 32 * q * kOf4)
+                         : "memory");
+          continue;
+        }
 #pragma unroll
         for (int q = 0; q < 2 * int(sizeof(T)); ++q) {
-          const int e = (32 * q + p.lane) * kOf4, left = d - first - e;
+          const int left = d - first - (32 * q + p.lane) * kOf4;
           const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                           stretch + e * int(sizeof(T))),
-                       "l"(bytes ? row + first + e : none), "r"(bytes)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stretch + 128 * q),
+                       "l"(bytes ? from + 32 * q * kOf4 : none), "r"(bytes)
                        : "memory");
         }
       } else {
         T* s = reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(ring) + at) +
-               k * int(blockDim.x) * 8 - 8 * p.lane;
+               k * int(blockDim.x) * 8 - 7 * p.lane;
+        const T* from = row + first + p.lane;
+        T v[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int e = 32 * q + p.lane;
-          s[e] = first + e < d ? row[first + e] : T(0.f);
-        }
+        for (int q = 0; q < 8; ++q)
+          v[q] = whole || first + 32 * q + p.lane < d ? from[32 * q] : T(0.f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[32 * q] = v[q];
       }
     }
     row += advance;
@@ -251,11 +262,16 @@ __device__ __forceinline__ void write_group(const Rows& r, int64_t t, int k, boo
   __syncwarp();
   reinterpret_cast<Group<T>*>(s)[p.lane] = g;
   __syncwarp();
+  T* to = row + first + p.lane;
+  const T* from = s + p.lane;
+  if (first + 256 <= d) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int e = 32 * q + p.lane;
-    if (first + e < d) row[first + e] = s[e];
+    for (int q = 0; q < 8; ++q) to[32 * q] = from[32 * q];
+    return;
   }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (first + 32 * q + p.lane < d) to[32 * q] = from[32 * q];
 }
 
 // Group k of a weight vector, of a type known at run time.  It is read again by every row, so it
