@@ -5,107 +5,169 @@
 namespace lp {
 namespace {
 
+// With one group a thread a team takes two rows a turn: their waits for the team are one, the
+// weights are read once, and the work of one hides the latencies of the other.
+template <int G>
+constexpr int kRowsATurn = G == 1 ? 2 : 1;
+
 template <class R, class A, int G, bool kPost, bool kFast>
-__global__ void __launch_bounds__(kMaxTeam)
+__global__ void __launch_bounds__(kMaxTeam, 2)
     lp_residual_norm_kernel(const __grid_constant__ NormArgs a, const Plan plan) {
-  __shared__ float slots[2][2][kMaxWarps][1];
+  constexpr int kRows = kRowsATurn<G>;
+  __shared__ float slots[2][2][kMaxWarps][kRows];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
-  const bool branch = a.branch.p != nullptr, gate = a.gate.p != nullptr;
+  const bool branch = a.branch.p != nullptr, gate = a.gate.p != nullptr, norm = a.weight != nullptr;
   const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
   int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
   if (!LP_CHECK(a.d <= a.residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
+  clear_ring<kFast, G>(ring, plan.stages * plan.stage_bytes, p);
   // a stage: the residual's rows, the branch's, the gate's
   Stream<R> residual;
   Stream<A> y, g;
+  Out<R> out;
+  Out<A> normed;
   int offset = 0;
-  residual.template start<kFast, G>(a.residual, t, step, p, ring, &offset);
-  if (branch) y.template start<kFast, G>(a.branch, t, step, p, ring, &offset);
-  if (gate) g.template start<kFast, G>(a.gate, t, step, p, ring, &offset);
+  residual.template start<kFast, G>(a.residual, t, p, ring, &offset);
+  if (branch) y.template start<kFast, G>(a.branch, t, p, ring, &offset);
+  if (gate) g.template start<kFast, G>(a.gate, t, p, ring, &offset);
+  if (branch) out.template start<kFast>(a.residual_out, t, p);
+  if (norm) normed.template start<kFast>(a.normed, t, p);
   void* stretch = ring + plan.stages * plan.stage_bytes + p.warp * kStretch;
   const uint32_t accesses = plan.accesses;
   int64_t next = t;  // the row that is fetched next
   const auto fetch = [&](int stage) {
-    if (next - p.in_cta < a.T) {  // the CTA has a turn for it
+    if (next < a.T) {
       const uint32_t at = stage * plan.stage_bytes;
-      const bool mine = next < a.T;
-      residual.template fetch<kFast, G>(at, mine, access_of(accesses, kResidual), p, a.residual.p);
-      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p, a.branch.p);
-      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p, a.gate.p);
+      residual.template fetch<kFast, G>(at, access_of(accesses, kResidual), p, a.residual.p);
+      residual.row += step * a.residual.ld;
+      if (branch) {
+        y.template fetch<kFast, G>(at, access_of(accesses, kBranch), p, a.branch.p);
+        y.row += step * a.branch.ld;
+      }
+      if (gate) {
+        g.template fetch<kFast, G>(at, access_of(accesses, kGate), p, a.gate.p);
+        g.row += step * a.gate.ld;
+      }
     }
     next += step;
     commit_copies();
   };
-  for (int s = 0; s + 1 < plan.stages; ++s) fetch(s);
+  for (int s = 0; s + kRows < plan.stages; ++s) fetch(s);
+  const bool wide_w = access_of(accesses, kWeight) == kWide;
+  const bool wide_b = access_of(accesses, kBranchWeight) == kWide;
   int stage = 0, turn = 0;
   // every team runs as many turns as the CTA's first, so that all meet at the barriers
-  for (; t - p.in_cta < a.T; t += step, turn ^= 1) {
-    const int ahead = plan.stages - 1;
-    __syncwarp();  // the stage that is copied into has been read by the warp
-    fetch(stage == 0 ? ahead : stage - 1);
-    wait_copies(ahead);
+  for (; t - p.in_cta < a.T; t += kRows * step, turn ^= 1) {
+    __syncwarp();  // the stages that are copied into have been read by the warp
+    int to = stage - kRows;
+    if (to < 0) to += plan.stages;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      fetch(to);
+      if (++to == plan.stages) to = 0;
+    }
+    wait_copies(plan.stages - kRows);
     __syncwarp();
-    const bool mine = t < a.T;
-    const uint32_t at = stage * plan.stage_bytes;
-    float v[G][8], root_y[1] = {0.f}, root[1] = {0.f};
+    uint32_t at[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      at[j] = stage * plan.stage_bytes;
+      if (++stage == plan.stages) stage = 0;
+    }
+    // a row that the team does not have is computed like the others, of what the ring holds, and
+    // not written
+    Pairs v[kRows][G];
+    float root_y[kRows] = {}, root[kRows] = {};
     if (kPost) {
 #pragma unroll
-      for (int k = 0; k < G; ++k) {
-        float n[8];
-        y.get(at, k, n);
+      for (int j = 0; j < kRows; ++j) {
+        float2 s = both(0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) root_y[0] = __fmaf_rn(n[e], n[e], root_y[0]);
+        for (int k = 0; k < G; ++k) {
+          Pairs n;
+          y.get(at[j], k, n);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s = fma(n[e], n[e], s);
+        }
+        root_y[j] = s.x + s.y;
       }
       team_sum(root_y, slots[turn][0], p);
-      root_y[0] = 1.f / sqrtf(__fmaf_rn(root_y[0], inv_d, a.eps));
-      if (a.branch_rstd != nullptr && p.i == 0 && mine) a.branch_rstd[t] = root_y[0];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        root_y[j] = 1.f / sqrtf(__fmaf_rn(root_y[j], inv_d, a.eps));
+        if (a.branch_rstd != nullptr && p.i == 0 && t + j * step < a.T)
+          a.branch_rstd[t + j * step] = root_y[j];
+      }
     }
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-      residual.get(at, k, v[k]);
-      if (branch) {
-        float n[8];
-        y.get(at, k, n);
-        if (kPost) {
-          float w[8];
-          read_weight(a.branch_weight, a.weight_bf16, k, access_of(accesses, kBranchWeight) == kWide, p, w);
+      Pairs wb;
+      if (kPost) read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) n[e] = n[e] * root_y[0] * w[e];
-        }
+      for (int j = 0; j < kRows; ++j) {
+        Pairs& vk = v[j][k];
+        residual.get(at[j], k, vk);
+        if (!branch) continue;
+        Pairs n;
+        y.get(at[j], k, n);
+        if (kPost)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) n[e] = mul(mul(n[e], both(root_y[j])), wb[e]);
         if (gate) {
-          float f[8];
-          g.get(at, k, f);
+          Pairs f;
+          g.get(at[j], k, f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) n[e] *= f[e];
+          for (int e = 0; e < 4; ++e) n[e] = mul(n[e], f[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[k][e] = __fmaf_rn(a.branch_scale, n[e], a.residual_scale * v[k][e]);
-        write_group<kFast, R>(a.residual_out, t, k, mine, access_of(accesses, kOut), p, stretch, v[k]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) root[0] = __fmaf_rn(v[k][e], v[k][e], root[0]);
-    }
-    if (a.weight != nullptr) {
-      team_sum(root, slots[turn][1], p);
-      root[0] = 1.f / sqrtf(__fmaf_rn(root[0], inv_d, a.eps));
-      if (a.rstd != nullptr && p.i == 0 && mine) a.rstd[t] = root[0];
-#pragma unroll
-      for (int k = 0; k < G; ++k) {
-        float w[8];
-        read_weight(a.weight, a.weight_bf16, k, access_of(accesses, kWeight) == kWide, p, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = v[k][e] * root[0] * w[e];
-        write_group<kFast, A>(a.normed, t, k, mine, access_of(accesses, kNormed), p, stretch, w);
+        for (int e = 0; e < 4; ++e)
+          vk[e] = fma(both(a.branch_scale), n[e], mul(both(a.residual_scale), vk[e]));
       }
     }
-    stage = stage + 1 == plan.stages ? 0 : stage + 1;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      float2 s = both(0.f);
+#pragma unroll
+      for (int k = 0; k < G; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = fma(v[j][k][e], v[j][k][e], s);
+      root[j] = s.x + s.y;
+      if (branch) {
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+          out.template put<kFast>(out.row, k, t + j * step < a.T, access_of(accesses, kOut), p,
+                                  stretch, v[j][k]);
+        out.row += step * a.residual_out.ld;
+      }
+    }
+    if (!norm) continue;
+    team_sum(root, slots[turn][1], p);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      root[j] = 1.f / sqrtf(__fmaf_rn(root[j], inv_d, a.eps));
+      if (a.rstd != nullptr && p.i == 0 && t + j * step < a.T) a.rstd[t + j * step] = root[j];
+    }
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      Pairs w;
+      read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][k][e] = mul(mul(v[j][k][e], both(root[j])), w[e]);
+        normed.template put<kFast>(normed.row + j * step * a.normed.ld, k, t + j * step < a.T,
+                                   access_of(accesses, kNormed), p, stretch, v[j][k]);
+      }
+    }
+    normed.row += kRows * step * a.normed.ld;
   }
 }
 
-// Several CTAs share an SM, each with rows in flight of its own.
-constexpr int kForwardBudget = 48 << 10;  // of a CTA of 256 threads
+// The CTAs of an SM have 1024 threads between them, each CTA with rows in flight of its own, and
+// this much shared memory for them.
+constexpr int kForwardBytes = 192 << 10;
 
 template <int G>
 lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses, bool fast,
@@ -116,12 +178,12 @@ lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses
     const auto launch = [&](auto* kernel, PerContextOnce* once) {
       if (!allow_ring(kernel, dev, once)) return LP_ERR_CUDA;
       Plan plan{shape_of(a.d, G, a.T), accesses, 1, 0};
-      const int threads = plan.shape.team * plan.shape.teams;
+      const int threads = plan.shape.team * plan.shape.teams, ctas = 1024 / threads;
       const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
-      const int64_t blocks = std::min<int64_t>(all, kSlots * (1024 / threads));
+      const int64_t blocks = std::min<int64_t>(all, kSlots * ctas);
       const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
-      const int smem = plan_ring(&plan, columns, G, !fast, (all + blocks - 1) / blocks, 1,
-                                 std::max(kForwardBudget * threads / 256, threads * G * 8 * columns));
+      const int smem = plan_ring(&plan, columns, G, !fast, (all + blocks - 1) / blocks,
+                                 kRowsATurn<G>, kForwardBytes / ctas);
       kernel<<<unsigned(blocks), threads, smem, stream>>>(a, plan);
       return launched();
     };
@@ -145,9 +207,8 @@ lp_status launch_residual_norm(const Device& dev, const NormArgs& a, cudaStream_
                             access_bits(kOut, a.residual_out, a.residual_bf16) |
                             access_bits(kNormed, a.normed, a.act_bf16);
   const bool fast = all_wide(accesses, {kResidual, kBranch, kGate, kOut, kNormed}, a.d);
-  // a thread's groups: one while that leaves a CTA of 256 threads or fewer, so that several
-  // CTAs fit an SM; more only for rows that 512 threads do not cover
-  if (a.d <= kMaxTeam / 2 * 8) return launch_forward<1>(dev, a, accesses, fast, stream);
+  // as few groups a thread as its team's 512 threads allow
+  if (a.d <= kMaxTeam * 8) return launch_forward<1>(dev, a, accesses, fast, stream);
   if (a.d <= kMaxTeam * 16) return launch_forward<2>(dev, a, accesses, fast, stream);
   return launch_forward<4>(dev, a, accesses, fast, stream);
 }

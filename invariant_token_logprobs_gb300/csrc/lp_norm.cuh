@@ -51,34 +51,61 @@ __device__ __forceinline__ void store_group(float* p, const Group32& g) {
                : "memory");
 }
 
-__device__ __forceinline__ float element(const Group32& g, int i) { return __uint_as_float(g.w[i]); }
-__device__ __forceinline__ float element(const Group16& g, int i) {
-  return __uint_as_float(i & 1 ? g.w[i / 2] & 0xffff0000u : g.w[i / 2] << 16);
+// The columns as four pairs, and back: the arithmetic is on pairs, two columns an instruction.
+using Pairs = float2[4];
+__device__ __forceinline__ void unpack(const Group32& g, Pairs& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_float2(__uint_as_float(g.w[2 * i]), __uint_as_float(g.w[2 * i + 1]));
+}
+__device__ __forceinline__ void unpack(const Group16& g, Pairs& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_float2(__uint_as_float(g.w[i] << 16), __uint_as_float(g.w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ Group32 pack(const Pairs& v, float) {
+  Group32 g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    g.w[2 * i] = __float_as_uint(v[i].x), g.w[2 * i + 1] = __float_as_uint(v[i].y);
+  return g;
+}
+__device__ __forceinline__ Group16 pack(const Pairs& v, __nv_bfloat16) {
+  Group16 g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 two = __floats2bfloat162_rn(v[i].x, v[i].y);
+    g.w[i] = *reinterpret_cast<const uint32_t*>(&two);
+  }
+  return g;
 }
 // Element i as it is stored.
-template <class T>
-__device__ __forceinline__ T item(const Group<T>& g, int i);
-template <>
-__device__ __forceinline__ float item(const Group32& g, int i) { return element(g, i); }
-template <>
+__device__ __forceinline__ float item(const Group32& g, int i) { return __uint_as_float(g.w[i]); }
 __device__ __forceinline__ __nv_bfloat16 item(const Group16& g, int i) {
   return __ushort_as_bfloat16(
       static_cast<unsigned short>(i & 1 ? g.w[i / 2] >> 16 : g.w[i / 2] & 0xffffu));
 }
-__device__ __forceinline__ Group32 pack(const float (&v)[8], float) {
-  Group32 g;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) g.w[i] = __float_as_uint(v[i]);
-  return g;
+
+__device__ __forceinline__ uint64_t as_bits(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
 }
-__device__ __forceinline__ Group16 pack(const float (&v)[8], __nv_bfloat16) {
-  Group16 g;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    g.w[i] = *reinterpret_cast<const uint32_t*>(&two);
-  }
-  return g;
+__device__ __forceinline__ float2 as_pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_bits(a)), "l"(as_bits(b)));
+  return as_pair(r);
+}
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_bits(a)), "l"(as_bits(b)), "l"(as_bits(c)));
+  return as_pair(r);
 }
 
 // How an operand's rows can be reached: whole groups, 4 bytes at a time, or only element by
@@ -134,44 +161,40 @@ template <class T>
 struct Stream {
   const T* row;     // the row that is fetched next, from the thread's first group on; from its
                     // first column on where it is not kFast
-  int64_t advance;  // elements from one turn's row to the next
-  uint32_t slot;    // the thread's first group in stage 0, as a shared address
-  T* ring;          // the same as a pointer
+  T* ring;          // the thread's first group in stage 0
 
   // `offset` is the operand's first byte in a stage, moved past it.
   template <bool kFast, int G>
-  __device__ __forceinline__ void start(const Rows& r, int64_t t, int64_t step, const Place& p,
+  __device__ __forceinline__ void start(const Rows& r, int64_t t, const Place& p,
                                         unsigned char* stage0, int* offset) {
     row = static_cast<const T*>(r.p) + t * r.ld + (kFast ? 8 * p.i : 0);
-    advance = step * r.ld;
     ring = reinterpret_cast<T*>(stage0 + *offset) + 8 * threadIdx.x;
-    slot = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     *offset += int(blockDim.x) * G * 8 * int(sizeof(T));
   }
-  // Starts the copy of the next row's groups into the stage `at` bytes on; zeros where the team
-  // has no row (or past its columns), as a row of zeros adds nothing to any sum.
+  __device__ __forceinline__ T* slot(uint32_t at, int k) const {
+    return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(ring) + at) +
+           k * int(blockDim.x) * 8;
+  }
+  // Starts the copy of the next row's groups into the stage `at` bytes on.  Columns past the row
+  // become zero (with kFast they are never written: the ring starts as zeros).
   template <bool kFast, int G>
-  // `base`: an address in the operand, for copies of no bytes.
-  __device__ __forceinline__ void fetch(uint32_t at, bool mine, uint32_t access, const Place& p,
+  __device__ __forceinline__ void fetch(uint32_t at, uint32_t access, const Place& p,
                                         const void* base) {
-    const T* none = static_cast<const T*>(base);
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-      const uint32_t to = slot + at + k * int(blockDim.x) * 8 * int(sizeof(T));
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(slot(at, k)));
       if (kFast) {
-        const int c = 8 * (p.i + k * p.team);
-        const uint32_t bytes = mine && c < p.d ? 16u : 0u;
+        if (8 * (p.i + k * p.team) < p.d)
 #pragma unroll
-        for (int q = 0; q < int(sizeof(T)) / 2; ++q)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * q),
-                       "l"(bytes ? row + k * p.team * 8 + q * (16 / int(sizeof(T))) : none), "r"(bytes)
-                       : "memory");
+          for (int q = 0; q < int(sizeof(T)) / 2; ++q)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * q),
+                         "l"(row + k * p.team * 8 + q * (16 / int(sizeof(T))))
+                         : "memory");
         continue;
       }
       // the warp's stretch, 32 neighbours an access
       const int first = 8 * (p.i - p.lane + k * p.team);
-      const bool whole = mine && first + 256 <= p.d;
-      const int d = mine ? p.d : 0;
+      const bool whole = first + 256 <= p.d;
       if (access != kPlain) {
         constexpr int kOf4 = 4 / sizeof(T);
         const uint32_t stretch = to - 8 * p.lane * int(sizeof(T)) + 4 * p.lane;
@@ -184,120 +207,147 @@ struct Stream {
                          : "memory");
           continue;
         }
+        // `base`: an address in the operand, for copies of no bytes
+        const T* none = static_cast<const T*>(base);
 #pragma unroll
         for (int q = 0; q < 2 * int(sizeof(T)); ++q) {
-          const int left = d - first - (32 * q + p.lane) * kOf4;
+          const int left = p.d - first - (32 * q + p.lane) * kOf4;
           const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stretch + 128 * q),
                        "l"(bytes ? from + 32 * q * kOf4 : none), "r"(bytes)
                        : "memory");
         }
       } else {
-        T* s = reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(ring) + at) +
-               k * int(blockDim.x) * 8 - 7 * p.lane;
+        T* s = slot(at, k) - 7 * p.lane;
         const T* from = row + first + p.lane;
         T v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          v[q] = whole || first + 32 * q + p.lane < d ? from[32 * q] : T(0.f);
+          v[q] = whole || first + 32 * q + p.lane < p.d ? from[32 * q] : T(0.f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) s[32 * q] = v[q];
       }
     }
-    row += advance;
+  }
+  // Zeros instead of a row that the team does not have: it then adds nothing to any sum.
+  template <int G>
+  __device__ __forceinline__ void zero(uint32_t at) {
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+#pragma unroll
+      for (int q = 0; q < int(sizeof(T)) / 2; ++q)
+        reinterpret_cast<uint4*>(slot(at, k))[q] = make_uint4(0u, 0u, 0u, 0u);
   }
   // The thread's group k in the stage `at` bytes on.
-  __device__ __forceinline__ void get(uint32_t at, int k, float (&v)[8]) const {
-    const uint4* from = reinterpret_cast<const uint4*>(
-        reinterpret_cast<const unsigned char*>(ring) + at + k * int(blockDim.x) * 8 * int(sizeof(T)));
+  __device__ __forceinline__ void get(uint32_t at, int k, Pairs& v) const {
+    const uint4* from = reinterpret_cast<const uint4*>(slot(at, k));
     Group<T> g;
 #pragma unroll
     for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
       const uint4 x = from[q];
       g.w[4 * q] = x.x, g.w[4 * q + 1] = x.y, g.w[4 * q + 2] = x.z, g.w[4 * q + 3] = x.w;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = element(g, e);
+    unpack(g, v);
   }
 };
 
-// Waits for all but the newest `ahead` commits of this thread's copies.
+// Zeros in the ring, for the threads whose groups lie past the row's columns.
+template <bool kFast, int G>
+__device__ __forceinline__ void clear_ring(unsigned char* ring, int bytes, const Place& p) {
+  if (!kFast || 8 * G * p.team == p.d) return;  // every group is written (or copied as zeros)
+  for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
+    reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+}
+
+// Rows of a team in the ring.  Eight, for deeper copies, made the backward of 4864 x 4096 69 us
+// instead of 63, and no case faster.
+constexpr int kMaxStages = 4;
+// Waits for all but the newest `ahead` commits of this thread's copies; ahead < kMaxStages.
 __device__ __forceinline__ void wait_copies(int ahead) {
-  if (ahead >= 3)
-    asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (ahead == 2)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (ahead == 1)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  switch (ahead) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
 }
 __device__ __forceinline__ void commit_copies() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Writes the thread's group k of row t, through a warp's stretch of 256 elements where rows are
-// not aligned.  All threads of a warp call it together; `mine`: the team has a row.
-template <bool kFast, class T>
-__device__ __forceinline__ void write_group(const Rows& r, int64_t t, int k, bool mine,
-                                            uint32_t access, const Place& p, void* stretch,
-                                            const float (&v)[8]) {
-  const Group<T> g = pack(v, T());
-  const int c = 8 * (p.i + k * p.team);
-  T* row = static_cast<T*>(r.p) + t * r.ld;
-  if (kFast) {
-    if (mine && c < p.d) store_group(row + c, g);
-    return;
+// A row output: the row that is written next.
+template <class T>
+struct Out {
+  T* row;
+  template <bool kFast>
+  __device__ __forceinline__ void start(const Rows& r, int64_t t, const Place& p) {
+    row = static_cast<T*>(r.p) + t * r.ld + (kFast ? 8 * p.i : 0);
   }
-  const int d = mine ? p.d : 0;
-  if (access == kWide) {
-    if (c + 8 <= d) return store_group(row + c, g);
+  // Writes the thread's group k of `row`, this one or a later, through a warp's stretch of 256 elements where rows are not
+  // aligned, if the team has the row.  All threads of a warp call it together.
+  template <bool kFast>
+  __device__ __forceinline__ void put(T* row, int k, bool mine, uint32_t access, const Place& p,
+                                      void* stretch, const Pairs& v) const {
+    if (!mine) return;
+    const Group<T> g = pack(v, T());
+    const int c = 8 * (p.i + k * p.team);
+    if (kFast) {
+      if (c < p.d) store_group(row + k * p.team * 8, g);
+      return;
+    }
+    if (access == kWide) {
+      if (c + 8 <= p.d) return store_group(row + c, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < d) row[c + e] = item<T>(g, e);
-    return;
+      for (int e = 0; e < 8; ++e)
+        if (c + e < p.d) row[c + e] = item(g, e);
+      return;
+    }
+    T* s = static_cast<T*>(stretch);
+    const int first = c - 8 * p.lane;
+    __syncwarp();
+    reinterpret_cast<Group<T>*>(s)[p.lane] = g;
+    __syncwarp();
+    T* to = row + first + p.lane;
+    const T* from = s + p.lane;
+    if (first + 256 <= p.d) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) to[32 * q] = from[32 * q];
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (first + 32 * q + p.lane < p.d) to[32 * q] = from[32 * q];
   }
-  T* s = static_cast<T*>(stretch);
-  const int first = c - 8 * p.lane;
-  __syncwarp();
-  reinterpret_cast<Group<T>*>(s)[p.lane] = g;
-  __syncwarp();
-  T* to = row + first + p.lane;
-  const T* from = s + p.lane;
-  if (first + 256 <= d) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) to[32 * q] = from[32 * q];
-    return;
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    if (first + 32 * q + p.lane < d) to[32 * q] = from[32 * q];
-}
+};
 
 // Group k of a weight vector, of a type known at run time.  It is read again by every row, so it
 // may stay in L1.
 __device__ __forceinline__ void read_weight(const void* w, bool bf16, int k, bool wide,
-                                            const Place& p, float (&v)[8]) {
+                                            const Place& p, Pairs& v) {
   const int index = p.i + k * p.team, c = 8 * index;
   if (wide && c + 8 <= p.d) {
     if (bf16) {
       const uint4 x = __ldg(static_cast<const uint4*>(w) + index);
-      const Group16 g{{x.x, x.y, x.z, x.w}};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = element(g, e);
+      unpack(Group16{{x.x, x.y, x.z, x.w}}, v);
     } else {
       const float4 a = __ldg(static_cast<const float4*>(w) + 2 * index);
       const float4 b = __ldg(static_cast<const float4*>(w) + 2 * index + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
+      v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
     }
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    v[e] = c + e >= p.d ? 0.f
-           : bf16       ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c + e])
-                        : static_cast<const float*>(w)[c + e];
+  for (int e = 0; e < 8; ++e) {
+    const float x = c + e >= p.d ? 0.f
+                    : bf16       ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c + e])
+                                 : static_cast<const float*>(w)[c + e];
+    if (e & 1)
+      v[e / 2].y = x;
+    else
+      v[e / 2].x = x;
+  }
 }
 
 // N sums over a team at once, the same bits for all its threads: shuffles within the warps, then
@@ -351,7 +401,6 @@ bool all_wide(uint32_t accesses, std::initializer_list<int> operands, int64_t d)
 
 // The ring and, where an output is not aligned, the warps' stretches.
 constexpr int kRingBytes = 200 << 10;
-constexpr int kMaxStages = 4;
 constexpr int kStretch = 256 * int(sizeof(float));
 // Sets the stages, of one row a team, that fit `budget` bytes, at least `least`, and returns the
 // dynamic shared bytes.  `rows`: that a team takes in all.

@@ -21,7 +21,8 @@ __host__ __device__ __forceinline__ int64_t pitch_of(int64_t d) { return (d + 7)
 template <class R, class A, int G>
 constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) <= 6 ? 2 : 1;
 
-template <class R, class A, int G, bool kPost, bool kFast>
+// kSolo: the CTA is one team, so that a turn's first row is there without asking.
+template <class R, class A, int G, bool kPost, bool kFast, bool kSolo>
 __global__ void __launch_bounds__(kMaxTeam)
     lp_residual_norm_grad_kernel(const __grid_constant__ NormGradArgs a, const Plan plan) {
   constexpr int kSums = kPost ? 3 : 1;
@@ -32,31 +33,56 @@ __global__ void __launch_bounds__(kMaxTeam)
   const float inv_d = 1.f / static_cast<float>(a.d);
   const bool norm = a.weight != nullptr, branch = a.branch.p != nullptr, gate = a.gate.p != nullptr;
   const bool has_dr = a.grad_residual_out.p != nullptr, gate_sum = gate && a.gate.ld == 0;
-  float sum_w[G][8] = {}, sum_b[G][8] = {}, sum_g[G][8] = {};
+  Pairs sum_w[G] = {}, sum_b[G] = {}, sum_g[G] = {};
   const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
   int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
   if (!LP_CHECK(a.d <= a.grad_residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
+  clear_ring<kFast, G>(ring, plan.stages * plan.stage_bytes, p);
   // a stage: the rows of the stream, its gradient, the norm's gradient, the branch, the gate
   Stream<R> s, dr;
   Stream<A> dh, y, g;
+  Out<R> grad_residual;
+  Out<A> grad_branch, grad_gate;
   int offset = 0;
-  if (norm) s.template start<kFast, G>(a.residual_out, t, step, p, ring, &offset);
-  if (has_dr) dr.template start<kFast, G>(a.grad_residual_out, t, step, p, ring, &offset);
-  if (norm) dh.template start<kFast, G>(a.grad_normed, t, step, p, ring, &offset);
-  if (branch) y.template start<kFast, G>(a.branch, t, step, p, ring, &offset);
-  if (gate) g.template start<kFast, G>(a.gate, t, step, p, ring, &offset);
+  if (norm) s.template start<kFast, G>(a.residual_out, t, p, ring, &offset);
+  if (has_dr) dr.template start<kFast, G>(a.grad_residual_out, t, p, ring, &offset);
+  if (norm) dh.template start<kFast, G>(a.grad_normed, t, p, ring, &offset);
+  if (branch) y.template start<kFast, G>(a.branch, t, p, ring, &offset);
+  if (gate) g.template start<kFast, G>(a.gate, t, p, ring, &offset);
+  const bool write_gate = gate && !gate_sum && a.grad_gate.p != nullptr;
+  grad_residual.template start<kFast>(a.grad_residual, t, p);
+  if (branch) grad_branch.template start<kFast>(a.grad_branch, t, p);
+  if (write_gate) grad_gate.template start<kFast>(a.grad_gate, t, p);
   void* stretch = ring + plan.stages * plan.stage_bytes + p.warp * kStretch;
   const uint32_t accesses = plan.accesses;
   int64_t next = t;  // the row that is fetched next
   const auto fetch = [&](int stage) {
-    if (next - p.in_cta < a.T) {  // the CTA has a turn for it
+    if (next < a.T) {
       const uint32_t at = stage * plan.stage_bytes;
-      const bool mine = next < a.T;
-      if (norm) s.template fetch<kFast, G>(at, mine, access_of(accesses, kOut), p, a.residual_out.p);
-      if (has_dr) dr.template fetch<kFast, G>(at, mine, access_of(accesses, kGradOut), p, a.grad_residual_out.p);
-      if (norm) dh.template fetch<kFast, G>(at, mine, access_of(accesses, kGradNormed), p, a.grad_normed.p);
-      if (branch) y.template fetch<kFast, G>(at, mine, access_of(accesses, kBranch), p, a.branch.p);
-      if (gate) g.template fetch<kFast, G>(at, mine, access_of(accesses, kGate), p, a.gate.p);
+      if (norm) {
+        s.template fetch<kFast, G>(at, access_of(accesses, kOut), p, a.residual_out.p);
+        s.row += step * a.residual_out.ld;
+        dh.template fetch<kFast, G>(at, access_of(accesses, kGradNormed), p, a.grad_normed.p);
+        dh.row += step * a.grad_normed.ld;
+      }
+      if (has_dr) {
+        dr.template fetch<kFast, G>(at, access_of(accesses, kGradOut), p, a.grad_residual_out.p);
+        dr.row += step * a.grad_residual_out.ld;
+      }
+      if (branch) {
+        y.template fetch<kFast, G>(at, access_of(accesses, kBranch), p, a.branch.p);
+        y.row += step * a.branch.ld;
+      }
+      if (gate) {
+        g.template fetch<kFast, G>(at, access_of(accesses, kGate), p, a.gate.p);
+        g.row += step * a.gate.ld;
+      }
+    } else {
+      const uint32_t at = stage * plan.stage_bytes;
+      if (norm) s.template zero<G>(at), dh.template zero<G>(at);
+      if (has_dr) dr.template zero<G>(at);
+      if (branch) y.template zero<G>(at);
+      if (gate) g.template zero<G>(at);
     }
     next += step;
     commit_copies();
@@ -64,10 +90,10 @@ __global__ void __launch_bounds__(kMaxTeam)
   for (int n = 0; n + kRows < plan.stages; ++n) fetch(n);
   const bool wide_w = access_of(accesses, kWeight) == kWide;
   const bool wide_b = access_of(accesses, kBranchWeight) == kWide;
-  // with one group a thread the weights stay in registers
-  float w0[8], wb0[8];
-  if (G == 1 && norm) read_weight(a.weight, a.weight_bf16, 0, wide_w, p, w0);
-  if (G == 1 && kPost) read_weight(a.branch_weight, a.weight_bf16, 0, wide_b, p, wb0);
+  // the common pre-norm block's weight stays in registers
+  Pairs kept_w;
+  constexpr bool kKeep = G == 1 && !kPost;
+  if (kKeep && norm) read_weight(a.weight, a.weight_bf16, 0, wide_w, p, kept_w);
   // the rows' roots, loaded a turn ahead
   float root[kRows], root_y[kRows];
   const auto load_roots = [&](int64_t first) {
@@ -98,69 +124,71 @@ __global__ void __launch_bounds__(kMaxTeam)
       at[j] = stage * plan.stage_bytes;
       if (++stage == plan.stages) stage = 0;
     }
-    float x[kRows][G][8], D[kRows][G][8], m[kRows * kSums] = {};
+    Pairs x[kRows][G], D[kRows][G];
+    float m[kRows * kSums];
+    float2 sums[kRows][kSums];
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
 #pragma unroll
-      for (int k = 0; k < G; ++k) {
-        float(&xk)[8] = x[j][k];
-        float(&Dk)[8] = D[j][k];
-        if (j > 0 && t + j * step - p.in_cta >= a.T) {  // no team has the row: nothing was copied
+      for (int q = 0; q < kSums; ++q) sums[j][q] = both(0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) Dk[e] = xk[e] = 0.f;
-          continue;
-        }
+    for (int k = 0; k < G; ++k) {
+      Pairs w, wb;
+      if (norm && !kKeep) read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
+      if (kPost) {
+        read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wb[e] = mul(both(a.branch_scale), wb[e]);
+      }
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        Pairs& xk = x[j][k];
+        Pairs& Dk = D[j][k];
         if (has_dr) {
           dr.get(at[j], k, Dk);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) Dk[e] = 0.f;
+          for (int e = 0; e < 4; ++e) Dk[e] = both(0.f);
         }
         if (norm) {
-          float h[8], w[8];
+          Pairs h;
           s.get(at[j], k, xk);
           dh.get(at[j], k, h);
-          if (G == 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = w0[e];
-          } else {
-            read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float dx = h[e] * w[e];
-            xk[e] *= root[j];
-            m[j * kSums] = __fmaf_rn(dx, xk[e], m[j * kSums]);
-            sum_w[k][e] = __fmaf_rn(h[e], xk[e], sum_w[k][e]);
-            Dk[e] = __fmaf_rn(root[j], dx, Dk[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 dx = mul(h[e], kKeep ? kept_w[e] : w[e]);
+            xk[e] = mul(xk[e], both(root[j]));
+            sums[j][0] = fma(dx, xk[e], sums[j][0]);
+            sum_w[k][e] = fma(h[e], xk[e], sum_w[k][e]);
+            Dk[e] = fma(both(root[j]), dx, Dk[e]);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) xk[e] = 0.f;
+          for (int e = 0; e < 4; ++e) xk[e] = both(0.f);
         }
         if (kPost) {
-          float f[8], wb[8];
+          Pairs f;
           y.get(at[j], k, f);
-          if (G == 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
-          } else {
-            read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = a.branch_scale * (f[e] * root_y[j]) * wb[e];
+          for (int e = 0; e < 4; ++e) f[e] = mul(mul(f[e], both(root_y[j])), wb[e]);
           if (gate) {
-            g.get(at[j], k, wb);
+            Pairs by;
+            g.get(at[j], k, by);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= wb[e];
+            for (int e = 0; e < 4; ++e) f[e] = mul(f[e], by[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            m[j * kSums + 1 % kSums] = __fmaf_rn(f[e], Dk[e], m[j * kSums + 1 % kSums]);
-            m[j * kSums + 2 % kSums] = __fmaf_rn(f[e], xk[e], m[j * kSums + 2 % kSums]);
+          for (int e = 0; e < 4; ++e) {
+            sums[j][1 % kSums] = fma(f[e], Dk[e], sums[j][1 % kSums]);
+            sums[j][2 % kSums] = fma(f[e], xk[e], sums[j][2 % kSums]);
           }
         }
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+#pragma unroll
+      for (int q = 0; q < kSums; ++q) m[j * kSums + q] = sums[j][q].x + sums[j][q].y;
     if (norm || kPost) team_sum(m, slots[turn], p);
     float m1[kRows], m2[kRows], scale_y[kRows];
 #pragma unroll
@@ -172,71 +200,68 @@ __global__ void __launch_bounds__(kMaxTeam)
     }
     load_roots(t + kRows * step);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int64_t row = t + j * step;
-      const bool mine = row < a.T;
-      if (j > 0 && row - p.in_cta >= a.T) continue;  // no team has it
+    for (int k = 0; k < G; ++k) {
+      Pairs wb;
+      if (kPost) read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
 #pragma unroll
-      for (int k = 0; k < G; ++k) {
-        float(&Dk)[8] = D[j][k];
-        float out[8];
+      for (int j = 0; j < kRows; ++j) {
+        const bool mine = (kSolo && j == 0) || t + j * step < a.T;
+        Pairs& Dk = D[j][k];
+        Pairs out;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          Dk[e] = __fmaf_rn(-m1[j], x[j][k][e], Dk[e]);
-          out[e] = a.residual_scale * Dk[e];
+        for (int e = 0; e < 4; ++e) {
+          Dk[e] = fma(both(-m1[j]), x[j][k][e], Dk[e]);
+          out[e] = mul(both(a.residual_scale), Dk[e]);
         }
-        write_group<kFast, R>(a.grad_residual, row, k, mine, access_of(accesses, kGradResidual), p,
-                              stretch, out);
+        grad_residual.template put<kFast>(grad_residual.row + j * step * a.grad_residual.ld, k, mine,
+                                          access_of(accesses, kGradResidual), p, stretch, out);
         if (!branch) continue;
-        float yh[8], wb[8];
+        Pairs yh;
         if (kPost || gate) {
           y.get(at[j], k, yh);
+          if (kPost)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) yh[e] *= scale_y[j];
-        }
-        if (kPost) {
-          if (G == 1) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) wb[e] = wb0[e];
-          } else {
-            read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
-          }
+            for (int e = 0; e < 4; ++e) yh[e] = mul(yh[e], both(scale_y[j]));
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) out[e] = a.branch_scale * Dk[e];
+        for (int e = 0; e < 4; ++e) out[e] = mul(both(a.branch_scale), Dk[e]);
         if (gate) {
-          float f[8], dg[8];
+          Pairs f, dg;
           g.get(at[j], k, f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dg[e] = out[e] * (kPost ? yh[e] * wb[e] : yh[e]);
-            if (gate_sum) sum_g[k][e] += dg[e];
-            out[e] *= f[e];
+          for (int e = 0; e < 4; ++e) {
+            dg[e] = kPost ? mul(yh[e], wb[e]) : yh[e];
+            if (gate_sum) sum_g[k][e] = fma(out[e], dg[e], sum_g[k][e]);
+            dg[e] = mul(out[e], dg[e]);
+            out[e] = mul(out[e], f[e]);
           }
-          if (!gate_sum && a.grad_gate.p != nullptr)
-            write_group<kFast, A>(a.grad_gate, row, k, mine, access_of(accesses, kGradGate), p,
-                                  stretch, dg);
+          if (write_gate)
+            grad_gate.template put<kFast>(grad_gate.row + j * step * a.grad_gate.ld, k, mine,
+                                          access_of(accesses, kGradGate), p, stretch, dg);
         }
         if (kPost) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum_b[k][e] = __fmaf_rn(out[e], yh[e], sum_b[k][e]);
-            out[e] = scale_y[j] * __fmaf_rn(out[e], wb[e], -(yh[e] * m2[j]));
+          for (int e = 0; e < 4; ++e) {
+            sum_b[k][e] = fma(out[e], yh[e], sum_b[k][e]);
+            out[e] = mul(both(scale_y[j]), fma(out[e], wb[e], mul(yh[e], both(-m2[j]))));
           }
         }
-        write_group<kFast, A>(a.grad_branch, row, k, mine, access_of(accesses, kGradBranch), p,
-                              stretch, out);
+        grad_branch.template put<kFast>(grad_branch.row + j * step * a.grad_branch.ld, k, mine,
+                                        access_of(accesses, kGradBranch), p, stretch, out);
       }
     }
+    grad_residual.row += kRows * step * a.grad_residual.ld;
+    if (branch) grad_branch.row += kRows * step * a.grad_branch.ld;
+    if (write_gate) grad_gate.row += kRows * step * a.grad_gate.ld;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partials == nullptr) return;
   // the teams' sums in order, then the CTA's, three rows of whole groups
-  float* shared = reinterpret_cast<float*>(ring);  // all copies have been waited for
+  float2* shared = reinterpret_cast<float2*>(ring);  // all copies have been waited for
   float* part = a.partials + int64_t(blockIdx.x) * 3 * pitch_of(a.d);
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    float(&sum)[G][8] = q == 0 ? sum_w : q == 1 ? sum_b : sum_g;
+    Pairs(&sum)[G] = q == 0 ? sum_w : q == 1 ? sum_b : sum_g;
     if (q == 0 ? a.grad_weight == nullptr : q == 1 ? a.grad_branch_weight == nullptr : !gate_sum)
       continue;
     for (int from = 1; from < plan.shape.teams; ++from) {
@@ -245,13 +270,16 @@ __global__ void __launch_bounds__(kMaxTeam)
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) shared[(k * p.team + p.i) * 8 + e] = sum[k][e];
+          for (int e = 0; e < 4; ++e) shared[(k * p.team + p.i) * 4 + e] = sum[k][e];
       __syncthreads();
       if (p.in_cta == 0)
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[k][e] += shared[(k * p.team + p.i) * 8 + e];
+          for (int e = 0; e < 4; ++e) {
+            const float2 other = shared[(k * p.team + p.i) * 4 + e];
+            sum[k][e] = make_float2(sum[k][e].x + other.x, sum[k][e].y + other.y);
+          }
     }
     if (p.in_cta == 0)
 #pragma unroll
@@ -426,12 +454,15 @@ lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t acc
       kernel<<<unsigned(blocks), plan.shape.team * plan.shape.teams, smem, stream>>>(a, plan);
       return launched();
     };
-    static PerContextOnce once[4];
+    static PerContextOnce once[6];
+    const bool solo = fast && shape_of(a.d, G, a.T).teams == 1;
     if (a.branch_weight != nullptr)
-      return fast ? launch(lp_residual_norm_grad_kernel<R, A, G, true, true>, &once[0])
-                  : launch(lp_residual_norm_grad_kernel<R, A, G, true, false>, &once[1]);
-    return fast ? launch(lp_residual_norm_grad_kernel<R, A, G, false, true>, &once[2])
-                : launch(lp_residual_norm_grad_kernel<R, A, G, false, false>, &once[3]);
+      return solo   ? launch(lp_residual_norm_grad_kernel<R, A, G, true, true, true>, &once[0])
+             : fast ? launch(lp_residual_norm_grad_kernel<R, A, G, true, true, false>, &once[1])
+                    : launch(lp_residual_norm_grad_kernel<R, A, G, true, false, false>, &once[2]);
+    return solo   ? launch(lp_residual_norm_grad_kernel<R, A, G, false, true, true>, &once[3])
+           : fast ? launch(lp_residual_norm_grad_kernel<R, A, G, false, true, false>, &once[4])
+                  : launch(lp_residual_norm_grad_kernel<R, A, G, false, false, false>, &once[5]);
   });
 }
 
