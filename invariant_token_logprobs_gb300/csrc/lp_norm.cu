@@ -165,9 +165,9 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   }
 }
 
-// The CTAs of an SM have 1024 threads between them, each CTA with rows in flight of its own, and
-// this much shared memory for them.
-constexpr int kForwardBytes = 192 << 10;
+// The CTAs of an SM have up to 1024 threads between them, each CTA with rows in flight of its own,
+// and this much shared memory for them.
+constexpr int kForwardBytes = 216 << 10;
 
 template <int G>
 lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses, bool fast,
@@ -178,10 +178,14 @@ lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses
     const auto launch = [&](auto* kernel, PerContextOnce* once) {
       if (!allow_ring(kernel, dev, once)) return LP_ERR_CUDA;
       Plan plan{shape_of(a.d, G, a.T), accesses, 1, 0};
-      const int threads = plan.shape.team * plan.shape.teams, ctas = 1024 / threads;
+      const int threads = plan.shape.team * plan.shape.teams;
+      const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
+      // as many CTAs as leave each the rows that it works on: 4864 x 2048 in float32 with a gate
+      // takes 34.8 us so, and 38 with one row more ahead and half of the CTAs
+      const int least = threads * G * 8 * columns * kRowsATurn<G> + (fast ? 0 : threads / 32 * kStretch);
+      const int ctas = std::max(1, std::min(1024 / threads, kForwardBytes / least));
       const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
       const int64_t blocks = std::min<int64_t>(all, kSlots * ctas);
-      const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
       const int smem = plan_ring(&plan, columns, G, !fast, (all + blocks - 1) / blocks,
                                  kRowsATurn<G>, kForwardBytes / ctas);
       kernel<<<unsigned(blocks), threads, smem, stream>>>(a, plan);

@@ -192,6 +192,20 @@ struct Stream {
                          : "memory");
         continue;
       }
+      // `base`: an address in the operand, for copies of no bytes
+      const T* none = static_cast<const T*>(base);
+      if (access == kWide) {  // aligned rows whose last group is not whole
+        const int c = 8 * (p.i + k * p.team);
+#pragma unroll
+        for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
+          constexpr int kOf16 = 16 / int(sizeof(T));
+          const int bytes = min(max((p.d - c - q * kOf16) * int(sizeof(T)), 0), 16);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * q),
+                       "l"(bytes ? row + c + q * kOf16 : none), "r"(bytes)
+                       : "memory");
+        }
+        continue;
+      }
       // the warp's stretch, 32 neighbours an access
       const int first = 8 * (p.i - p.lane + k * p.team);
       const bool whole = first + 256 <= p.d;
@@ -207,8 +221,6 @@ struct Stream {
                          : "memory");
           continue;
         }
-        // `base`: an address in the operand, for copies of no bytes
-        const T* none = static_cast<const T*>(base);
 #pragma unroll
         for (int q = 0; q < 2 * int(sizeof(T)); ++q) {
           const int left = p.d - first - (32 * q + p.lane) * kOf4;

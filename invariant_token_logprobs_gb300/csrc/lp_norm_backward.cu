@@ -90,10 +90,12 @@ __global__ void __launch_bounds__(kMaxTeam)
   for (int n = 0; n + kRows < plan.stages; ++n) fetch(n);
   const bool wide_w = access_of(accesses, kWeight) == kWide;
   const bool wide_b = access_of(accesses, kBranchWeight) == kWide;
-  // the common pre-norm block's weight stays in registers
-  Pairs kept_w;
-  constexpr bool kKeep = G == 1 && !kPost;
+  // the weights stay in registers where these allow: without a norm of the branch, or with one row
+  // a turn
+  constexpr bool kKeep = G == 1 && (!kPost || kRows == 1);
+  Pairs kept_w, kept_b;
   if (kKeep && norm) read_weight(a.weight, a.weight_bf16, 0, wide_w, p, kept_w);
+  if (kKeep && kPost) read_weight(a.branch_weight, a.weight_bf16, 0, wide_b, p, kept_b);
   // the rows' roots, loaded a turn ahead
   float root[kRows], root_y[kRows];
   const auto load_roots = [&](int64_t first) {
@@ -136,9 +138,9 @@ __global__ void __launch_bounds__(kMaxTeam)
       Pairs w, wb;
       if (norm && !kKeep) read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
       if (kPost) {
-        read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+        if (!kKeep) read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) wb[e] = mul(both(a.branch_scale), wb[e]);
+        for (int e = 0; e < 4; ++e) wb[e] = mul(both(a.branch_scale), kKeep ? kept_b[e] : wb[e]);
       }
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
@@ -202,7 +204,10 @@ __global__ void __launch_bounds__(kMaxTeam)
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       Pairs wb;
-      if (kPost) read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+      if (kPost && !kKeep) read_weight(a.branch_weight, a.weight_bf16, k, wide_b, p, wb);
+      if (kPost && kKeep)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wb[e] = kept_b[e];
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         const bool mine = (kSolo && j == 0) || t + j * step < a.T;
