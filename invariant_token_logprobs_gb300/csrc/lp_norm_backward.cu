@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kMaxTeam)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partials == nullptr) return;
-  // the teams' sums in order, then the CTA's, three rows of whole groups
+  // the teams' sums in order, then the CTA's: three rows of whole groups in the workspace, or of a
+  // lone CTA the sums themselves
   float2* shared = reinterpret_cast<float2*>(ring);  // all copies have been waited for
   float* part = a.partials + int64_t(blockIdx.x) * 3 * pitch_of(a.d);
 #pragma unroll
@@ -290,7 +291,16 @@ __global__ void __launch_bounds__(kMaxTeam)
 #pragma unroll
       for (int k = 0; k < G; ++k) {
         const int c = 8 * (p.i + k * p.team);
-        if (c < p.d) store_group(part + q * pitch_of(a.d) + c, pack(sum[k], float()));
+        if (gridDim.x > 1) {
+          if (c < p.d) store_group(part + q * pitch_of(a.d) + c, pack(sum[k], float()));
+          continue;
+        }
+        float* out = q == 0   ? a.grad_weight
+                     : q == 1 ? a.grad_branch_weight
+                              : static_cast<float*>(a.grad_gate.p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < p.d) out[c + e] = e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x;
       }
   }
 }
@@ -519,6 +529,7 @@ lp_status launch_residual_norm_backward(const Device& dev, const NormGradArgs& a
   float* gate_sum = a.gate.ld == 0 ? static_cast<float*>(a.grad_gate.p) : nullptr;
   if (a.grad_weight == nullptr && a.grad_branch_weight == nullptr && gate_sum == nullptr)
     return LP_OK;
+  if (blocks == 1 && a.d <= kTeamDim) return LP_OK;  // the CTA wrote them
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((a.d + 31) / 32), 3);
   cfg.blockDim = dim3(32 * kSumLanes);
