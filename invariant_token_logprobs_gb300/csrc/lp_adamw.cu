@@ -15,11 +15,6 @@ constexpr int kRow = LP_ADAMW_ALIGN;    // state elements of a CTA
 constexpr int kBlock = LP_ADAMW_BLOCK;  // elements of a warp, with one scale
 static_assert(kRow == kBlock * kThreads / 32, "one block of elements a warp");
 
-template <int j>
-struct Byte {
-  static constexpr int value = j;
-};
-
 // The magnitude codes of 8-bit moments: code c > 0 is the float of bits (c + kFirst) << kShift.
 // The code of a float is its own leading bits, so both ways are a few integer operations on
 // bytes where they lie in a word of four.
@@ -33,50 +28,61 @@ struct Code {
   // magnitude below that value to it or to zero
   static constexpr float kLow = kSigned ? 0x1.4p-36f : 0x1.2p-35f;
 
-  // byte j of the word.  For the first moment the sign's bit, multiplied up with the code, adds
+  // Whether no byte of the word is a code for zero.
+  static __device__ __forceinline__ bool none_zero(uint32_t word) {
+    if (kSigned) return ((word & 0x7f7f7f7fu) + 0x7f7f7f7fu & 0x80808080u) == 0x80808080u;
+    return (word - 0x01010101u & ~word & 0x80808080u) == 0u;
+  }
+  // Byte j of the word.  For the first moment the sign's bit, multiplied up with the code, adds
   // 16 to the exponent, which the factor of a negative value takes back.
-  template <int j>
+  template <int j, bool kZeros>
   static __device__ __forceinline__ float decode(uint32_t word, float scale) {
     const uint32_t byte = __byte_perm(word, 0u, 0x4440u + j);
     const float value = __uint_as_float(byte * (1u << kShift) + (kFirst << kShift));
     float factor = kSigned && byte >= 128u ? scale * -0x1p-16f : scale;
-    if ((byte & kMask) == 0u) factor = 0.f * scale;
+    if (kZeros && (byte & kMask) == 0u) factor = 0.f * scale;
     return value * factor;
   }
-  // The random bits that a word's half rounds with, in place for the code.
-  static __device__ __forceinline__ uint32_t random(uint32_t word) {
-    return kSigned ? word << 4 & 0xffff0u : word >> 13 & 0x7fff8u;
+  template <bool kZeros>
+  static __device__ __forceinline__ void decode4(uint32_t word, float scale, float* v) {
+    v[0] = decode<0, kZeros>(word, scale), v[1] = decode<1, kZeros>(word, scale);
+    v[2] = decode<2, kZeros>(word, scale), v[3] = decode<3, kZeros>(word, scale);
   }
   // |x| over the block's largest magnitude, at most 1
   static __device__ __forceinline__ float part(float x, float inverse) {
     return fminf(fabsf(x) * inverse, 1.f);
   }
-  // Puts the code of x, whose part is given, into byte j.  Parts between zero and the lowest
-  // code become zero here; `least`, the smallest of all parts' bits less one, tells of them.
-  template <int j>
-  static __device__ __forceinline__ void encode(float x, float part, uint32_t random, uint32_t* word,
-                                                uint32_t* least) {
+  // A part with its random bits added, moved up so that the code, plus the low byte of kFirst, is
+  // the top byte; of a part below the lowest code's value, the top byte for zero.
+  static __device__ __forceinline__ uint32_t rounded(float part, uint32_t word) {
     const uint32_t bits = __float_as_uint(part);
-    *least = min(*least, bits - 1u);
-    const bool whole = bits >= kLowest;
-    const uint32_t code = whole ? bits + random - (kFirst << kShift) : 0u;
-    constexpr int right = kShift - 8 * j;
-    const uint32_t moved = right >= 0 ? code >> (right >= 0 ? right : 0) : code << (right < 0 ? -right : 0);
-    *word |= moved & kMask << 8 * j;
-    if (kSigned) {
-      const uint32_t sign = whole ? __float_as_uint(x) : 0u;
-      *word |= sign >> (24 - 8 * j) & 0x80u << 8 * j;
-    }
+    const uint32_t random = __byte_perm(word, 0u, kSigned ? 0x4104u : 0x4324u);  // 16 bits, << 8
+    return bits >= kLowest ? bits * (1u << (24 - kShift)) + random : kFirst << 24;
   }
-  // The same for those parts, and nothing for others.
-  template <int j>
-  static __device__ __forceinline__ void encode_between(float x, float part, uint32_t random,
-                                                        uint32_t* word) {
-    if (__float_as_uint(part) - 1u >= kLowest - 1u) return;
-    if (part > static_cast<float>(random) * kLow)
-      *word |= (1u | (kSigned && x < 0.f ? 128u : 0u)) << 8 * j;
+  // The codes of four elements x with these rounded parts.
+  static __device__ __forceinline__ uint32_t encode4(const uint32_t (&rounded)[4], const float* x) {
+    uint32_t codes = top_bytes(rounded[0], rounded[1], rounded[2], rounded[3]);
+    if (!kSigned)  // minus 0xf1 in every byte, without a carry between them
+      return (codes & 0x7f7f7f7fu) + 0x0f0f0f0fu ^ (codes & 0x80808080u);
+    codes -= 0x79797979u;  // every byte is 0x79 at least
+    const uint32_t signs = top_bytes(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                     __float_as_uint(x[2]), __float_as_uint(x[3]));
+    return codes | (signs & codes + 0x7f7f7f7fu & 0x80808080u);  // zero has none
+  }
+  static __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073u), __byte_perm(c, d, 0x0073u), 0x5410u);
+  }
+  // The code of an element whose part lies between zero and the lowest code's value, in its byte;
+  // nothing for others.
+  static __device__ __forceinline__ uint32_t encode_between(float x, float part, uint32_t word, int j) {
+    if (__float_as_uint(part) - 1u >= kLowest - 1u) return 0u;
+    const uint32_t random = kSigned ? (word & 0xffffu) << 4 : (word >> 16) << 3;
+    if (!(part > static_cast<float>(random) * kLow)) return 0u;
+    return (1u | (kSigned && x < 0.f ? 128u : 0u)) << 8 * j;
   }
 };
+static_assert((Code<true>::kFirst & 255u) == 0x79u && (Code<false>::kFirst & 255u) == 0xf1u,
+              "the low bytes that encode4 takes off");
 
 // Philox 4x32 with 7 rounds (Salmon, Moraes, Dror and Shaw, "Parallel random numbers:
 // as easy as 1, 2, 3", SC11) at counter (group, step), with the rounds' keys at hand.
@@ -349,16 +355,20 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
 #pragma unroll
       for (int k = 0; k < 8; ++k) g[k] *= clip;
     if (kSmall) {
+      // a lane whose bytes are none of them zero, as mostly, does not ask each
+      if (Code<true>::none_zero(old_m[0]) && Code<true>::none_zero(old_m[1]) &&
+          Code<false>::none_zero(old_u[0]) && Code<false>::none_zero(old_u[1])) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        m[4 * h] = Code<true>::decode<0>(old_m[h], old_scale_m);
-        m[4 * h + 1] = Code<true>::decode<1>(old_m[h], old_scale_m);
-        m[4 * h + 2] = Code<true>::decode<2>(old_m[h], old_scale_m);
-        m[4 * h + 3] = Code<true>::decode<3>(old_m[h], old_scale_m);
-        v[4 * h] = Code<false>::decode<0>(old_u[h], old_scale_u);
-        v[4 * h + 1] = Code<false>::decode<1>(old_u[h], old_scale_u);
-        v[4 * h + 2] = Code<false>::decode<2>(old_u[h], old_scale_u);
-        v[4 * h + 3] = Code<false>::decode<3>(old_u[h], old_scale_u);
+        for (int h = 0; h < 2; ++h) {
+          Code<true>::decode4<false>(old_m[h], old_scale_m, m + 4 * h);
+          Code<false>::decode4<false>(old_u[h], old_scale_u, v + 4 * h);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          Code<true>::decode4<true>(old_m[h], old_scale_m, m + 4 * h);
+          Code<false>::decode4<true>(old_u[h], old_scale_u, v + 4 * h);
+        }
       }
     }
     float u[8];
@@ -392,28 +402,28 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t w[4], new_m = 0, new_u = 0;
+      uint32_t w[4], rounded_m[4], rounded_u[4];
       random_words(uint64_t(flat / 4 + h * 32 + lane), a.step, a.round_keys, w);
       float part_m[4], part_u[4];
+      uint32_t least_m = ~0u, least_u = ~0u;  // the smallest parts' bits, less one
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         part_m[j] = Code<true>::part(m[4 * h + j], inv_m);
         part_u[j] = Code<false>::part(u[4 * h + j], inv_u);
+        rounded_m[j] = Code<true>::rounded(part_m[j], w[j]);
+        rounded_u[j] = Code<false>::rounded(part_u[j], w[j]);
+        least_m = min(least_m, __float_as_uint(part_m[j]) - 1u);
+        least_u = min(least_u, __float_as_uint(part_u[j]) - 1u);
       }
-      uint32_t least_m = ~0u, least_u = ~0u;
-      const auto each = [&](auto byte) {
-        constexpr int j = decltype(byte)::value;
-        Code<true>::encode<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m, &least_m);
-        Code<false>::encode<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u, &least_u);
-      };
-      each(Byte<0>()), each(Byte<1>()), each(Byte<2>()), each(Byte<3>());
-      if (least_m < Code<true>::kLowest - 1u || least_u < Code<false>::kLowest - 1u) {  // rare: a magnitude below 2^-16 of its block's largest
-        const auto rest = [&](auto byte) {
-          constexpr int j = decltype(byte)::value;
-          Code<true>::encode_between<j>(m[4 * h + j], part_m[j], Code<true>::random(w[j]), &new_m);
-          Code<false>::encode_between<j>(u[4 * h + j], part_u[j], Code<false>::random(w[j]), &new_u);
-        };
-        rest(Byte<0>()), rest(Byte<1>()), rest(Byte<2>()), rest(Byte<3>());
+      uint32_t new_m = Code<true>::encode4(rounded_m, m + 4 * h);
+      uint32_t new_u = Code<false>::encode4(rounded_u, u + 4 * h);
+      if (least_m < Code<true>::kLowest - 1u || least_u < Code<false>::kLowest - 1u) {
+        // rare: a magnitude below 2^-16 of its block's largest
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          new_m |= Code<true>::encode_between(m[4 * h + j], part_m[j], w[j], j);
+          new_u |= Code<false>::encode_between(u[4 * h + j], part_u[j], w[j], j);
+        }
       }
       static_cast<uint32_t*>(a.exp_avg)[flat / 4 + 32 * h + lane] = new_m;
       static_cast<uint32_t*>(a.exp_avg_sq)[flat / 4 + 32 * h + lane] = new_u;
@@ -508,11 +518,11 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t i = int64_t(blockIdx.x) * (kRow / 4) + k * kThreads + threadIdx.x;
     const uint32_t cm = __ldg(m + i), cu = __ldg(u + i);
     const float sm = __ldg(m_scale + i / (kBlock / 4)), su = __ldg(u_scale + i / (kBlock / 4));
-    m_out[i] = make_float4(Code<true>::decode<0>(cm, sm), Code<true>::decode<1>(cm, sm),
-                           Code<true>::decode<2>(cm, sm), Code<true>::decode<3>(cm, sm));
-    const float4 u4 = make_float4(Code<false>::decode<0>(cu, su), Code<false>::decode<1>(cu, su),
-                                  Code<false>::decode<2>(cu, su), Code<false>::decode<3>(cu, su));
-    v_out[i] = make_float4(u4.x * u4.x, u4.y * u4.y, u4.z * u4.z, u4.w * u4.w);
+    float a[4], b[4];
+    Code<true>::decode4<true>(cm, sm, a);
+    Code<false>::decode4<true>(cu, su, b);
+    m_out[i] = make_float4(a[0], a[1], a[2], a[3]);
+    v_out[i] = make_float4(b[0] * b[0], b[1] * b[1], b[2] * b[2], b[3] * b[3]);
   }
 }
 
