@@ -142,9 +142,12 @@ __device__ __forceinline__ float reciprocal(float x) {
 // Two elements: the moments from m, v and the gradient, the new param, and the roots of v.
 __device__ __forceinline__ float2 update(const AdamwArgs& a, float2 g, float kept, float step_size,
                                          float2* p, float2* m, float2* v) {
-  // element by element: the moments' products are each rounded, and a pair's may be fused
-  m->x = a.beta1 * m->x + a.rest1 * g.x, m->y = a.beta1 * m->y + a.rest1 * g.y;
-  v->x = a.beta2 * v->x + a.rest2 * (g.x * g.x), v->y = a.beta2 * v->y + a.rest2 * (g.y * g.y);
+  // the products in pairs and the sums one by one: a pair's product and sum would be fused into
+  // one rounding, and the moments' products are each rounded
+  const float2 m0 = mul2(both(a.beta1), *m), m1 = mul2(both(a.rest1), g);
+  const float2 v0 = mul2(both(a.beta2), *v), v1 = mul2(both(a.rest2), mul2(g, g));
+  *m = make_float2(__fadd_rn(m0.x, m1.x), __fadd_rn(m0.y, m1.y));
+  *v = make_float2(__fadd_rn(v0.x, v1.x), __fadd_rn(v0.y, v1.y));
   const float2 u = make_float2(sqrtf(v->x), sqrtf(v->y));
   const float2 below = add2(mul2(u, both(a.root_scale)), both(a.eps));
   // the quotient by an approximate reciprocal, within 3 units in the last place: it is far below
