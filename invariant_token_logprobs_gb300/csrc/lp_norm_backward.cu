@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(kMaxTeam)
   const Place p(a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
   const bool norm = a.weight != nullptr, branch = a.branch.p != nullptr, gate = a.gate.p != nullptr;
-  const bool has_dr = a.grad_residual_out.p != nullptr, gate_sum = gate && a.gate.ld == 0;
+  const bool has_dr = a.grad_residual_out.p != nullptr;
+  const bool gate_sum = gate && a.gate.ld == 0 && a.grad_gate.p != nullptr;
   Pairs sum_w[G] = {}, sum_b[G] = {}, sum_g[G] = {};
   const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
   int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(kMaxTeam)
   if (norm) dh.template start<kFast, G>(a.grad_normed, t, p, ring, &offset);
   if (branch) y.template start<kFast, G>(a.branch, t, p, ring, &offset);
   if (gate) g.template start<kFast, G>(a.gate, t, p, ring, &offset);
-  const bool write_gate = gate && !gate_sum && a.grad_gate.p != nullptr;
+  const bool write_gate = gate && a.gate.ld != 0 && a.grad_gate.p != nullptr;
   grad_residual.template start<kFast>(a.grad_residual, t, p);
   if (branch) grad_branch.template start<kFast>(a.grad_branch, t, p);
   if (write_gate) grad_gate.template start<kFast>(a.grad_gate, t, p);

@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
@@ -263,6 +264,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const float a = float(number(v[5])), b = float(number(v[6])), eps = float(number(v[7]));
     const at::Tensor& act = branch != nullptr ? *branch : residual;
     const c10::Device device = device_of(residual, {branch, gate, branch_weight, weight});
+    const c10::cuda::CUDAGuard guard(device);
     const NormOperands o(residual, branch, gate, branch_weight, weight, act);
     at::Tensor stream = residual, normed, rstd, branch_rstd;
     int64_t ld_stream = o.ld_residual;
@@ -313,6 +315,7 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const at::Tensor& act = branch != nullptr ? *branch : residual;
     const c10::Device device = device_of(residual, {grad_normed, grad_residual, branch, gate, weight,
                                                     branch_weight, rstd, branch_rstd, given});
+    const c10::cuda::CUDAGuard guard(device);
     const NormOperands o(residual, branch, gate, branch_weight, weight, act);
     same_dtype(grad_normed, act.scalar_type(), "grad_normed");
     same_dtype(grad_residual, residual.scalar_type(), "grad_residual");
@@ -368,6 +371,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (logp.dim() != 1) value_error("expected a 1-D logp");
     const c10::Device device =
         device_of(logp, {&old_logp, &advantages, mask, ref_logp, entropy, cu_seqlens, given});
+    const c10::cuda::CUDAGuard guard(device);
     const int64_t T = logp.size(0);
     vector(&logp, T, "logp");
     vector(&old_logp, T, "old_logp");
@@ -422,6 +426,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const uint64_t seed = PyLong_AsUnsignedLongLong(v[13]);
     if (PyErr_Occurred()) throw Refused{};
     const c10::Device device = device_of(plan, {&m, &u, m_scale, u_scale});
+    const c10::cuda::CUDAGuard guard(device);
     void* stream = current_stream(device);
     at::Tensor norm;
     const float* scale = nullptr;
@@ -454,6 +459,7 @@ PyObject* adamw_state_values(PyObject*, PyObject* const* v, Py_ssize_t n) {
                      &m_scale = required(v[2], "exp_avg_scale"),
                      &u_scale = required(v[3], "exp_avg_sq_scale");
     const c10::Device device = device_of(m, {&u, &m_scale, &u_scale});
+    const c10::cuda::CUDAGuard guard(device);
     const int64_t elements = m.numel();
     at::Tensor values, squares;
     Tensors made(device);

@@ -322,6 +322,33 @@ def test_offsets_past_32_bits():
     assert torch.equal(got.residual[-3:], part.residual) and torch.equal(got.branch[-3:], part.branch)
 
 
+@pytest.mark.parametrize("T", [1, 5, 700])
+@pytest.mark.parametrize("skipped", [("gate",), ("weight", "gate"), ("branch_weight",)])
+def test_sums_that_are_not_asked_for(T, skipped):
+    """Through the C entry: a null sum is left out and the others keep their bits."""
+    d = 520
+    x = make(T, d, BF16, BF16, F32, True, "channel")
+    residual, kw = split(x)
+    out = train.residual_norm(residual, **kw)
+    gh, gr = x["grads"]
+    ref = train.residual_norm_backward(gh, gr, out.residual, out.rstd, branch_rstd=out.branch_rstd, **kw)
+    sums = {k: torch.full((d,), 7.0, device=DEV) for k in ("gate", "branch_weight", "weight")}
+    ptr = {k: None if k in skipped else v.data_ptr() for k, v in sums.items()}
+    g, gb = torch.empty_like(residual), torch.empty_like(residual)
+    size = train.residual_norm_backward_workspace_size(T, d)
+    work = torch.empty(size, dtype=torch.uint8, device=DEV)
+    status = train.load().lp_residual_norm_backward(
+        out.residual.data_ptr(), d, 1, kw["branch"].data_ptr(), d, kw["gate"].data_ptr(), 0, 1,
+        kw["branch_weight"].data_ptr(), kw["weight"].data_ptr(), 0, T, d, 1.0, 1.0,
+        out.branch_rstd.data_ptr(), out.rstd.data_ptr(), gh.data_ptr(), d, gr.data_ptr(), d,
+        g.data_ptr(), d, gb.data_ptr(), d, ptr["gate"], 0, ptr["branch_weight"], ptr["weight"],
+        work.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    assert torch.equal(g, ref.residual) and torch.equal(gb, ref.branch)
+    for k, v in sums.items():
+        assert torch.equal(v, torch.full_like(v, 7.0) if k in skipped else getattr(ref, k)), k
+
+
 def test_refusals():
     x = make(4, 64, BF16, BF16, BF16, True, "channel")
     residual, kw = split(x)
