@@ -18,15 +18,15 @@ __host__ __device__ __forceinline__ int64_t pitch_of(int64_t d) { return (d + 7)
 //
 // Where the registers and the ring allow, a team takes two rows a turn: their waits for the
 // team are one, and the work of one hides the latencies of the other.
-template <class R, class A, int G>
-constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) <= 6 ? 2 : 1;
+template <class R, class A, int G, bool kFast>
+constexpr int kRowsATurn = kFast && G == 1 && sizeof(R) + sizeof(A) <= 6 ? 2 : 1;
 
 // kSolo: the CTA is one team, so that a turn's first row is there without asking.
 template <class R, class A, int G, bool kPost, bool kFast, bool kSolo>
 __global__ void __launch_bounds__(kMaxTeam)
     lp_residual_norm_grad_kernel(const __grid_constant__ NormGradArgs a, const Plan plan) {
   constexpr int kSums = kPost ? 3 : 1;
-  constexpr int kRows = kRowsATurn<R, A, G>;
+  constexpr int kRows = kRowsATurn<R, A, G, kFast>;
   __shared__ float slots[2][kMaxWarps][kRows * kSums];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.d, plan.shape);
@@ -464,7 +464,7 @@ lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t acc
                           (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
       const int64_t at_once = blocks * plan.shape.teams;
       int smem = plan_ring(&plan, columns, G, !fast, (a.T + at_once - 1) / at_once,
-                           kRowsATurn<R, A, G>,
+                           fast ? kRowsATurn<R, A, G, true> : 1,
                            kRingBytes / ctas_of_sm(plan.shape.team * plan.shape.teams));
       if (plan.shape.teams > 1) smem = std::max(smem, plan.shape.team * G * 8 * int(sizeof(float)));
       kernel<<<unsigned(blocks), plan.shape.team * plan.shape.teams, smem, stream>>>(a, plan);
