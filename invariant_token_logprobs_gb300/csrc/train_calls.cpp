@@ -132,28 +132,30 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType s, c10::Device device) {
 }
 
 // The tensors that a call allocates.  An allocation takes 1.4 us on the host, about half of what a
-// launch does, so those of a small call are parts of one; large ones are allocated each, so that
-// none keeps another's memory.
+// launch does, so the small ones, and all of a small call's, are parts of one; large ones are
+// allocated each, so that none keeps another's memory.
 class Tensors {
  public:
   explicit Tensors(c10::Device device) : device_(device) {}
   // A tensor to be allocated, contiguous; `out` is set by allocate().
   void add(at::Tensor* out, std::initializer_list<int64_t> sizes, at::ScalarType type) {
     Item& item = items_[count_++];
-    item = {out, {1, 1}, int(sizes.size()), type, bytes_};
-    int64_t bytes = int64_t(c10::elementSize(type));
+    item = {out, {1, 1}, int(sizes.size()), type, int64_t(c10::elementSize(type))};
     int i = 0;
-    for (int64_t n : sizes) bytes *= item.sizes[i++] = n;
-    bytes_ += (bytes + 255) / 256 * 256;
+    for (int64_t n : sizes) item.bytes *= item.sizes[i++] = n;
+    item.bytes = (item.bytes + 255) / 256 * 256;
+    all_ += item.bytes;
   }
   void allocate() {
-    const bool together = bytes_ <= kTogether && count_ > 1;
-    at::Tensor whole;
-    if (together) whole = empty({bytes_}, at::kByte, device_);
+    const int64_t part = all_ <= kSmallCall ? kSmallCall : kSmallTensor;  // the largest part
+    int64_t together = 0, at = 0;
+    for (int i = 0; i < count_; ++i)
+      if (items_[i].bytes <= part) together += items_[i].bytes;
+    const at::Tensor whole = empty({together}, at::kByte, device_);
     for (int i = 0; i < count_; ++i) {
       const Item& item = items_[i];
       const at::IntArrayRef sizes(item.sizes, size_t(item.dims));
-      if (!together) {
+      if (item.bytes > part) {
         *item.out = empty(sizes, item.type, device_);
         continue;
       }
@@ -161,24 +163,25 @@ class Tensors {
           c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
           c10::scalarTypeToTypeMeta(item.type));
       c10::TensorImpl* impl = item.out->unsafeGetTensorImpl();
-      impl->set_storage_offset(item.at / int64_t(c10::elementSize(item.type)));
+      impl->set_storage_offset(at / int64_t(c10::elementSize(item.type)));
       impl->set_sizes_contiguous(sizes);
+      at += item.bytes;
     }
   }
 
  private:
-  static constexpr int64_t kTogether = 256 << 10;
+  static constexpr int64_t kSmallTensor = 64 << 10, kSmallCall = 256 << 10;
   struct Item {
     at::Tensor* out;
     int64_t sizes[2];
     int dims;
     at::ScalarType type;
-    int64_t at;
+    int64_t bytes;
   };
   c10::Device device_;
   Item items_[8];
   int count_ = 0;
-  int64_t bytes_ = 0;
+  int64_t all_ = 0;
 };
 
 // A tuple of tensors, None for undefined ones.
