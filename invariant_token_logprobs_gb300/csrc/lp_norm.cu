@@ -14,7 +14,7 @@ template <class R, class A, int G, bool kPost, bool kFast>
 __global__ void __launch_bounds__(kMaxTeam, 2)
     lp_residual_norm_kernel(const __grid_constant__ NormArgs a, const Plan plan) {
   constexpr int kRows = kRowsATurn<G>;
-  __shared__ float slots[2][2][kMaxWarps][kRows];
+  __shared__ __align__(16) float slots[2][2][kMaxWarps][padded(kRows)];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
@@ -26,30 +26,20 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   // a stage: the residual's rows, the branch's, the gate's
   Stream<R> residual;
   Stream<A> y, g;
-  Out<R> out;
-  Out<A> normed;
-  int offset = 0;
-  residual.template start<kFast, G>(a.residual, t, p, ring, &offset);
-  if (branch) y.template start<kFast, G>(a.branch, t, p, ring, &offset);
-  if (gate) g.template start<kFast, G>(a.gate, t, p, ring, &offset);
-  if (branch) out.template start<kFast>(a.residual_out, t, p);
-  if (norm) normed.template start<kFast>(a.normed, t, p);
+  uint32_t offset = 0;
+  const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  residual.template start<G>(stage0, &offset);
+  if (branch) y.template start<G>(stage0, &offset);
+  if (gate) g.template start<G>(stage0, &offset);
   void* stretch = ring + plan.stages * plan.stage_bytes + p.warp * kStretch;
   const uint32_t accesses = plan.accesses;
   int64_t next = t;  // the row that is fetched next
   const auto fetch = [&](int stage) {
     if (next < a.T) {
       const uint32_t at = stage * plan.stage_bytes;
-      residual.template fetch<kFast, G>(at, access_of(accesses, kResidual), p, a.residual.p);
-      residual.row += step * a.residual.ld;
-      if (branch) {
-        y.template fetch<kFast, G>(at, access_of(accesses, kBranch), p, a.branch.p);
-        y.row += step * a.branch.ld;
-      }
-      if (gate) {
-        g.template fetch<kFast, G>(at, access_of(accesses, kGate), p, a.gate.p);
-        g.row += step * a.gate.ld;
-      }
+      residual.template fetch<kFast, G>(a.residual, next, at, access_of(accesses, kResidual), p);
+      if (branch) y.template fetch<kFast, G>(a.branch, next, at, access_of(accesses, kBranch), p);
+      if (gate) g.template fetch<kFast, G>(a.gate, next, at, access_of(accesses, kGate), p);
     }
     next += step;
     commit_copies();
@@ -134,13 +124,11 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s = fma(v[j][k][e], v[j][k][e], s);
       root[j] = s.x + s.y;
-      if (branch) {
+      if (branch)
 #pragma unroll
         for (int k = 0; k < G; ++k)
-          out.template put<kFast>(out.row, k, t + j * step < a.T, access_of(accesses, kOut), p,
-                                  stretch, v[j][k]);
-        out.row += step * a.residual_out.ld;
-      }
+          put<R, kFast>(a.residual_out, t + j * step, k, t + j * step < a.T,
+                        access_of(accesses, kOut), p, stretch, v[j][k]);
     }
     if (!norm) continue;
     team_sum(root, slots[turn][1], p);
@@ -157,11 +145,10 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
       for (int j = 0; j < kRows; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][k][e] = mul(mul(v[j][k][e], both(root[j])), w[e]);
-        normed.template put<kFast>(normed.row + j * step * a.normed.ld, k, t + j * step < a.T,
-                                   access_of(accesses, kNormed), p, stretch, v[j][k]);
+        put<A, kFast>(a.normed, t + j * step, k, t + j * step < a.T, access_of(accesses, kNormed),
+                      p, stretch, v[j][k]);
       }
     }
-    normed.row += kRows * step * a.normed.ld;
   }
 }
 
@@ -210,7 +197,9 @@ lp_status launch_residual_norm(const Device& dev, const NormArgs& a, cudaStream_
                             access_bits(kWeight, a.weight, 0, a.weight_bf16) |
                             access_bits(kOut, a.residual_out, a.residual_bf16) |
                             access_bits(kNormed, a.normed, a.act_bf16);
-  const bool fast = all_wide(accesses, {kResidual, kBranch, kGate, kOut, kNormed}, a.d);
+  const bool fast = all_wide(accesses, {kResidual, kBranch, kGate, kOut, kNormed}, a.d) &&
+                    near(a.residual) && near(a.branch) && near(a.gate) && near(a.residual_out) &&
+                    near(a.normed);
   // as few groups a thread as its team's 512 threads allow
   if (a.d <= kMaxTeam * 8) return launch_forward<1>(dev, a, accesses, fast, stream);
   if (a.d <= kMaxTeam * 16) return launch_forward<2>(dev, a, accesses, fast, stream);

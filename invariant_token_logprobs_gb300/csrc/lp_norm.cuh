@@ -156,46 +156,53 @@ struct Place {
   }
 };
 
-// A row operand on its way through the ring: this thread's place in the rows and in a stage.
+// Where row t of an operand begins, `column` elements on.  With kFast rows are less than 2^32 bytes
+// apart, and the address is one multiplication.
+template <class T, bool kFast>
+__device__ __forceinline__ T* row_at(const Rows& r, int64_t t, int column) {
+  if (kFast) {
+    const uint64_t first = reinterpret_cast<uint64_t>(r.p) + uint32_t(column) * uint32_t(sizeof(T));
+    return reinterpret_cast<T*>(first + uint64_t(uint32_t(t)) * uint32_t(r.ld * int64_t(sizeof(T))));
+  }
+  return static_cast<T*>(r.p) + t * r.ld + column;
+}
+
+// A row operand on its way through the ring: this thread's first group in stage 0.
 template <class T>
 struct Stream {
-  const T* row;     // the row that is fetched next, from the thread's first group on; from its
-                    // first column on where it is not kFast
-  T* ring;          // the thread's first group in stage 0
+  uint32_t first;  // shared address
 
   // `offset` is the operand's first byte in a stage, moved past it.
-  template <bool kFast, int G>
-  __device__ __forceinline__ void start(const Rows& r, int64_t t, const Place& p,
-                                        unsigned char* stage0, int* offset) {
-    row = static_cast<const T*>(r.p) + t * r.ld + (kFast ? 8 * p.i : 0);
-    ring = reinterpret_cast<T*>(stage0 + *offset) + 8 * threadIdx.x;
-    *offset += int(blockDim.x) * G * 8 * int(sizeof(T));
+  template <int G>
+  __device__ __forceinline__ void start(uint32_t stage0, uint32_t* offset) {
+    first = stage0 + *offset + 8 * threadIdx.x * uint32_t(sizeof(T));
+    *offset += blockDim.x * G * 8 * uint32_t(sizeof(T));
   }
-  __device__ __forceinline__ T* slot(uint32_t at, int k) const {
-    return reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(ring) + at) +
-           k * int(blockDim.x) * 8;
+  __device__ __forceinline__ uint32_t slot(uint32_t at, int k) const {
+    return first + at + k * blockDim.x * 8 * uint32_t(sizeof(T));
   }
-  // Starts the copy of the next row's groups into the stage `at` bytes on.  Columns past the row
-  // become zero (with kFast they are never written: the ring starts as zeros).
+  // Starts the copy of row t's groups into the stage `at` bytes on.  Columns past the row become
+  // zero (with kFast they are never written: the ring starts as zeros).
   template <bool kFast, int G>
-  __device__ __forceinline__ void fetch(uint32_t at, uint32_t access, const Place& p,
-                                        const void* base) {
+  __device__ __forceinline__ void fetch(const Rows& r, int64_t t, uint32_t at, uint32_t access,
+                                        const Place& p) const {
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(slot(at, k)));
+      const uint32_t to = slot(at, k);
+      const int c = 8 * (p.i + k * p.team);
       if (kFast) {
-        if (8 * (p.i + k * p.team) < p.d)
+        const T* from = row_at<const T, true>(r, t, c);
+        if (c < p.d)
 #pragma unroll
           for (int q = 0; q < int(sizeof(T)) / 2; ++q)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * q),
-                         "l"(row + k * p.team * 8 + q * (16 / int(sizeof(T))))
+                         "l"(from + q * (16 / int(sizeof(T))))
                          : "memory");
         continue;
       }
-      // `base`: an address in the operand, for copies of no bytes
-      const T* none = static_cast<const T*>(base);
+      const T* row = row_at<const T, false>(r, t, 0);
+      const T* none = static_cast<const T*>(r.p);  // an address for copies of no bytes
       if (access == kWide) {  // aligned rows whose last group is not whole
-        const int c = 8 * (p.i + k * p.team);
 #pragma unroll
         for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
           constexpr int kOf16 = 16 / int(sizeof(T));
@@ -207,12 +214,12 @@ struct Stream {
         continue;
       }
       // the warp's stretch, 32 neighbours an access
-      const int first = 8 * (p.i - p.lane + k * p.team);
-      const bool whole = first + 256 <= p.d;
+      const int first_column = 8 * (p.i - p.lane + k * p.team);
+      const bool whole = first_column + 256 <= p.d;
       if (access != kPlain) {
         constexpr int kOf4 = 4 / sizeof(T);
-        const uint32_t stretch = to - 8 * p.lane * int(sizeof(T)) + 4 * p.lane;
-        const T* from = row + first + p.lane * kOf4;
+        const uint32_t stretch = to - 8 * p.lane * uint32_t(sizeof(T)) + 4 * p.lane;
+        const T* from = row + first_column + p.lane * kOf4;
         if (whole) {
 #pragma unroll
           for (int q = 0; q < 2 * int(sizeof(T)); ++q)
@@ -223,19 +230,19 @@ struct Stream {
         }
 #pragma unroll
         for (int q = 0; q < 2 * int(sizeof(T)); ++q) {
-          const int left = p.d - first - (32 * q + p.lane) * kOf4;
+          const int left = p.d - first_column - (32 * q + p.lane) * kOf4;
           const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stretch + 128 * q),
                        "l"(bytes ? from + 32 * q * kOf4 : none), "r"(bytes)
                        : "memory");
         }
       } else {
-        T* s = slot(at, k) - 7 * p.lane;
-        const T* from = row + first + p.lane;
+        T* s = shared_pointer(to) - 7 * p.lane;
+        const T* from = row + first_column + p.lane;
         T v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          v[q] = whole || first + 32 * q + p.lane < p.d ? from[32 * q] : T(0.f);
+          v[q] = whole || first_column + 32 * q + p.lane < p.d ? from[32 * q] : T(0.f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) s[32 * q] = v[q];
       }
@@ -243,30 +250,36 @@ struct Stream {
   }
   // Zeros instead of a row that the team does not have: it then adds nothing to any sum.
   template <int G>
-  __device__ __forceinline__ void zero(uint32_t at) {
+  __device__ __forceinline__ void zero(uint32_t at) const {
 #pragma unroll
     for (int k = 0; k < G; ++k)
 #pragma unroll
       for (int q = 0; q < int(sizeof(T)) / 2; ++q)
-        reinterpret_cast<uint4*>(slot(at, k))[q] = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot(at, k) + 16 * q), "r"(0)
+                     : "memory");
   }
   // The thread's group k in the stage `at` bytes on.
   __device__ __forceinline__ void get(uint32_t at, int k, Pairs& v) const {
-    const uint4* from = reinterpret_cast<const uint4*>(slot(at, k));
+    const uint32_t from = slot(at, k);
     Group<T> g;
 #pragma unroll
-    for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
-      const uint4 x = from[q];
-      g.w[4 * q] = x.x, g.w[4 * q + 1] = x.y, g.w[4 * q + 2] = x.z, g.w[4 * q + 3] = x.w;
-    }
+    for (int q = 0; q < int(sizeof(T)) / 2; ++q)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(g.w[4 * q]), "=r"(g.w[4 * q + 1]), "=r"(g.w[4 * q + 2]), "=r"(g.w[4 * q + 3])
+                   : "r"(from + 16 * q)
+                   : "memory");
     unpack(g, v);
+  }
+  static __device__ __forceinline__ T* shared_pointer(uint32_t address) {
+    return static_cast<T*>(__cvta_shared_to_generic(address));
   }
 };
 
 // Zeros in the ring, for the threads whose groups lie past the row's columns.
 template <bool kFast, int G>
 __device__ __forceinline__ void clear_ring(unsigned char* ring, int bytes, const Place& p) {
-  if (!kFast || 8 * G * p.team == p.d) return;  // every group is written (or copied as zeros)
+  const bool ragged = kFast && 8 * G * p.team != p.d;  // else every group is written, or copied as zeros
+  if (!ragged) return;
   for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
     reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
@@ -288,50 +301,43 @@ __device__ __forceinline__ void commit_copies() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// A row output: the row that is written next.
-template <class T>
-struct Out {
-  T* row;
-  template <bool kFast>
-  __device__ __forceinline__ void start(const Rows& r, int64_t t, const Place& p) {
-    row = static_cast<T*>(r.p) + t * r.ld + (kFast ? 8 * p.i : 0);
+// Writes the thread's group k of row t, through a warp's stretch of 256 elements where rows are not
+// aligned, if the team has the row.  All threads of a warp call it together.
+template <class T, bool kFast>
+__device__ __forceinline__ void put(const Rows& r, int64_t t, int k, bool mine, uint32_t access,
+                                    const Place& p, void* stretch, const Pairs& v) {
+  if (!mine) return;
+  const Group<T> g = pack(v, T());
+  const int c = 8 * (p.i + k * p.team);
+  if (kFast) {
+    T* to = row_at<T, true>(r, t, c);
+    if (c < p.d) store_group(to, g);
+    return;
   }
-  // Writes the thread's group k of `row`, this one or a later, through a warp's stretch of 256 elements where rows are not
-  // aligned, if the team has the row.  All threads of a warp call it together.
-  template <bool kFast>
-  __device__ __forceinline__ void put(T* row, int k, bool mine, uint32_t access, const Place& p,
-                                      void* stretch, const Pairs& v) const {
-    if (!mine) return;
-    const Group<T> g = pack(v, T());
-    const int c = 8 * (p.i + k * p.team);
-    if (kFast) {
-      if (c < p.d) store_group(row + k * p.team * 8, g);
-      return;
-    }
-    if (access == kWide) {
-      if (c + 8 <= p.d) return store_group(row + c, g);
+  T* row = row_at<T, false>(r, t, 0);
+  if (access == kWide) {
+    if (c + 8 <= p.d) return store_group(row + c, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < p.d) row[c + e] = item(g, e);
-      return;
-    }
-    T* s = static_cast<T*>(stretch);
-    const int first = c - 8 * p.lane;
-    __syncwarp();
-    reinterpret_cast<Group<T>*>(s)[p.lane] = g;
-    __syncwarp();
-    T* to = row + first + p.lane;
-    const T* from = s + p.lane;
-    if (first + 256 <= p.d) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) to[32 * q] = from[32 * q];
-      return;
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (first + 32 * q + p.lane < p.d) to[32 * q] = from[32 * q];
+    for (int e = 0; e < 8; ++e)
+      if (c + e < p.d) row[c + e] = item(g, e);
+    return;
   }
-};
+  T* s = static_cast<T*>(stretch);
+  const int first = c - 8 * p.lane;
+  __syncwarp();
+  reinterpret_cast<Group<T>*>(s)[p.lane] = g;
+  __syncwarp();
+  T* to = row + first + p.lane;
+  const T* from = s + p.lane;
+  if (first + 256 <= p.d) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) to[32 * q] = from[32 * q];
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (first + 32 * q + p.lane < p.d) to[32 * q] = from[32 * q];
+}
 
 // Group k of a weight vector, of a type known at run time.  It is read again by every row, so it
 // may stay in L1.
@@ -362,27 +368,68 @@ __device__ __forceinline__ void read_weight(const void* w, bool bf16, int k, boo
   }
 }
 
-// N sums over a team at once, the same bits for all its threads: shuffles within the warps, then
-// over the warps' sums, of which there are at most 16.  `slots` is written again only after
-// another barrier.
+// Sums over lanes of kCount values at once: in each step a lane hands half of its values to the
+// lane `distance` away and takes that one's share of the other half, until it has one; its index is
+// in the lane's bits from the first distance down.  Then the rest of the distances down to kLast.
+template <int kCount>
+__device__ __forceinline__ float exchange_sum(float (&v)[kCount], int lane, int last) {
+  int distance = 16;
+#pragma unroll
+  for (int half = kCount / 2; half > 0; half /= 2, distance /= 2) {
+    const bool upper = (lane & distance) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, distance);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (; distance >= last; distance /= 2) s += __shfl_xor_sync(0xffffffffu, s, distance);
+  return s;
+}
+// N sums over a team at once, the same bits for all its threads: over the warps' lanes, then over
+// the warps, of which there are at most 16.  `slots` is written again only after another barrier.
+__host__ __device__ constexpr int padded(int n) { return n <= 2 ? n : n <= 4 ? 4 : 8; }
 template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], float (*slots)[N], const Place& p) {
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*slots)[padded(N)], const Place& p) {
+  constexpr int kCount = padded(N), kLanes = 32 / kCount;
+  float all[kCount];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int i = 0; i < kCount; ++i) all[i] = i < N ? v[i] : 0.f;
+  const float mine = exchange_sum(all, p.lane, 1);  // of value lane / kLanes
+  if (p.team == 32) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (p.team == 32) return;
-  if (p.lane == 0)
-#pragma unroll
-    for (int k = 0; k < N; ++k) slots[p.warp][k] = v[k];
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * kLanes);
+    return;
+  }
+  if (p.lane % kLanes == 0) slots[p.warp][p.lane / kLanes] = mine;
   __syncthreads();
-  const int w = p.lane & (kMaxWarps - 1);
+  if (kCount == 1) {
+    const int w = p.lane & (kMaxWarps - 1);
+    float s = 32 * w < p.team ? slots[p.first_warp + w][0] : 0.f;
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 32 * w < p.team ? slots[p.first_warp + w][k] : 0.f;
+    for (int o = kMaxWarps / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    v[0] = s;
+    return;
+  }
+  // lane 2 w + h: half h of warp w's values
+  constexpr int kHalf = kCount > 1 ? kCount / 2 : 1;
+  const int w = p.lane / 2, h = p.lane & 1;
+  float part[kHalf];
 #pragma unroll
-  for (int o = kMaxWarps / 2; o > 0; o >>= 1)
+  for (int i = 0; i < kHalf; ++i)
+    part[i] = 32 * w < p.team ? slots[p.first_warp + w][h * kHalf + i] : 0.f;
+  const float sum = exchange_sum(part, p.lane, 2);
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  for (int i = 0; i < N; ++i) {
+    // value i: half i / kHalf, and the bits of i % kHalf are the lane's from 16 down
+    const int in_half = i % kHalf;
+    const int from = i / kHalf + (kHalf == 4   ? (in_half >> 1) * 16 + (in_half & 1) * 8
+                                  : kHalf == 2 ? in_half * 16
+                                               : 0);
+    v[i] = __shfl_sync(0xffffffffu, sum, from);
+  }
 }
 
 // ------------------------------------------------------------------------- host
@@ -410,6 +457,8 @@ bool all_wide(uint32_t accesses, std::initializer_list<int> operands, int64_t d)
     if (access_of(accesses, o) != kWide) return false;
   return d % 8 == 0;
 }
+// Whether rows are near enough for 32-bit pitches in bytes.
+bool near(const Rows& r) { return r.p == nullptr || r.ld < (int64_t(1) << 30); }
 
 // The ring and, where an output is not aligned, the warps' stretches.
 constexpr int kRingBytes = 200 << 10;

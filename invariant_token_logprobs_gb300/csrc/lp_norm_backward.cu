@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kMaxTeam)
     lp_residual_norm_grad_kernel(const __grid_constant__ NormGradArgs a, const Plan plan) {
   constexpr int kSums = kPost ? 3 : 1;
   constexpr int kRows = kRowsATurn<R, A, G, kFast>;
-  __shared__ float slots[2][kMaxWarps][kRows * kSums];
+  __shared__ __align__(16) float slots[2][kMaxWarps][padded(kRows * kSums)];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
@@ -42,44 +42,29 @@ __global__ void __launch_bounds__(kMaxTeam)
   // a stage: the rows of the stream, its gradient, the norm's gradient, the branch, the gate
   Stream<R> s, dr;
   Stream<A> dh, y, g;
-  Out<R> grad_residual;
-  Out<A> grad_branch, grad_gate;
-  int offset = 0;
-  if (norm) s.template start<kFast, G>(a.residual_out, t, p, ring, &offset);
-  if (has_dr) dr.template start<kFast, G>(a.grad_residual_out, t, p, ring, &offset);
-  if (norm) dh.template start<kFast, G>(a.grad_normed, t, p, ring, &offset);
-  if (branch) y.template start<kFast, G>(a.branch, t, p, ring, &offset);
-  if (gate) g.template start<kFast, G>(a.gate, t, p, ring, &offset);
+  uint32_t offset = 0;
+  const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  if (norm) s.template start<G>(stage0, &offset);
+  if (has_dr) dr.template start<G>(stage0, &offset);
+  if (norm) dh.template start<G>(stage0, &offset);
+  if (branch) y.template start<G>(stage0, &offset);
+  if (gate) g.template start<G>(stage0, &offset);
   const bool write_gate = gate && a.gate.ld != 0 && a.grad_gate.p != nullptr;
-  grad_residual.template start<kFast>(a.grad_residual, t, p);
-  if (branch) grad_branch.template start<kFast>(a.grad_branch, t, p);
-  if (write_gate) grad_gate.template start<kFast>(a.grad_gate, t, p);
   void* stretch = ring + plan.stages * plan.stage_bytes + p.warp * kStretch;
   const uint32_t accesses = plan.accesses;
   int64_t next = t;  // the row that is fetched next
   const auto fetch = [&](int stage) {
+    const uint32_t at = stage * plan.stage_bytes;
     if (next < a.T) {
-      const uint32_t at = stage * plan.stage_bytes;
       if (norm) {
-        s.template fetch<kFast, G>(at, access_of(accesses, kOut), p, a.residual_out.p);
-        s.row += step * a.residual_out.ld;
-        dh.template fetch<kFast, G>(at, access_of(accesses, kGradNormed), p, a.grad_normed.p);
-        dh.row += step * a.grad_normed.ld;
+        s.template fetch<kFast, G>(a.residual_out, next, at, access_of(accesses, kOut), p);
+        dh.template fetch<kFast, G>(a.grad_normed, next, at, access_of(accesses, kGradNormed), p);
       }
-      if (has_dr) {
-        dr.template fetch<kFast, G>(at, access_of(accesses, kGradOut), p, a.grad_residual_out.p);
-        dr.row += step * a.grad_residual_out.ld;
-      }
-      if (branch) {
-        y.template fetch<kFast, G>(at, access_of(accesses, kBranch), p, a.branch.p);
-        y.row += step * a.branch.ld;
-      }
-      if (gate) {
-        g.template fetch<kFast, G>(at, access_of(accesses, kGate), p, a.gate.p);
-        g.row += step * a.gate.ld;
-      }
+      if (has_dr)
+        dr.template fetch<kFast, G>(a.grad_residual_out, next, at, access_of(accesses, kGradOut), p);
+      if (branch) y.template fetch<kFast, G>(a.branch, next, at, access_of(accesses, kBranch), p);
+      if (gate) g.template fetch<kFast, G>(a.gate, next, at, access_of(accesses, kGate), p);
     } else {
-      const uint32_t at = stage * plan.stage_bytes;
       if (norm) s.template zero<G>(at), dh.template zero<G>(at);
       if (has_dr) dr.template zero<G>(at);
       if (branch) y.template zero<G>(at);
@@ -219,8 +204,8 @@ __global__ void __launch_bounds__(kMaxTeam)
           Dk[e] = fma(both(-m1[j]), x[j][k][e], Dk[e]);
           out[e] = mul(both(a.residual_scale), Dk[e]);
         }
-        grad_residual.template put<kFast>(grad_residual.row + j * step * a.grad_residual.ld, k, mine,
-                                          access_of(accesses, kGradResidual), p, stretch, out);
+        put<R, kFast>(a.grad_residual, t + j * step, k, mine, access_of(accesses, kGradResidual), p,
+                      stretch, out);
         if (!branch) continue;
         Pairs yh;
         if (kPost || gate) {
@@ -242,8 +227,8 @@ __global__ void __launch_bounds__(kMaxTeam)
             out[e] = mul(out[e], f[e]);
           }
           if (write_gate)
-            grad_gate.template put<kFast>(grad_gate.row + j * step * a.grad_gate.ld, k, mine,
-                                          access_of(accesses, kGradGate), p, stretch, dg);
+            put<A, kFast>(a.grad_gate, t + j * step, k, mine, access_of(accesses, kGradGate), p,
+                          stretch, dg);
         }
         if (kPost) {
 #pragma unroll
@@ -252,13 +237,10 @@ __global__ void __launch_bounds__(kMaxTeam)
             out[e] = mul(both(scale_y[j]), fma(out[e], wb[e], mul(yh[e], both(-m2[j]))));
           }
         }
-        grad_branch.template put<kFast>(grad_branch.row + j * step * a.grad_branch.ld, k, mine,
-                                        access_of(accesses, kGradBranch), p, stretch, out);
+        put<A, kFast>(a.grad_branch, t + j * step, k, mine, access_of(accesses, kGradBranch), p,
+                      stretch, out);
       }
     }
-    grad_residual.row += kRows * step * a.grad_residual.ld;
-    if (branch) grad_branch.row += kRows * step * a.grad_branch.ld;
-    if (write_gate) grad_gate.row += kRows * step * a.grad_gate.ld;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partials == nullptr) return;
@@ -521,7 +503,10 @@ lp_status launch_residual_norm_backward(const Device& dev, const NormGradArgs& a
     const bool fast = all_wide(accesses,
                                {kOut, kBranch, kGate, kGradNormed, kGradOut, kGradResidual, kGradBranch,
                                 kGradGate},
-                               a.d);
+                               a.d) &&
+                      near(a.residual_out) && near(a.branch) && near(a.gate) && near(a.grad_normed) &&
+                      near(a.grad_residual_out) && near(a.grad_residual) && near(a.grad_branch) &&
+                      near(a.grad_gate);
     const lp_status st = a.d > kTeamDim        ? launch_backward_wide(dev, a, blocks, stream)
                          : groups_of(a.d) == 1 ? launch_backward<1>(dev, a, accesses, fast, blocks, stream)
                                                : launch_backward<2>(dev, a, accesses, fast, blocks, stream);
