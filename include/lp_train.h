@@ -61,9 +61,9 @@ typedef enum lp_dtype { LP_FLOAT32 = 0, LP_BFLOAT16 = 1 } lp_dtype;
  *   branch_rstd, rstd  [T] float32, or NULL: the reciprocal roots
  *                 rsqrt(mean + eps) of the two norms, for the backward pass;
  *                 branch_rstd needs branch_weight and rstd needs weight.
- * Pointers are aligned to their element; rows whose pointers and strides are
- * multiples of 16 bytes are read and written 16 bytes at a time, with the same
- * results.  Outputs must not overlap the inputs or one another, other than
+ * Pointers are aligned to their element; rows that all start on multiples of 8
+ * elements, in memory and by their strides, with d a multiple of 8, are read and
+ * written 8 columns at a time; others are slower, with the same results.  Outputs must not overlap the inputs or one another, other than
  * residual_out in place (LP_ERR_INVALID_ARGUMENT).
  */
 LP_API lp_status lp_residual_norm(const void* residual, int64_t ld_residual, int residual_dtype,

@@ -1,5 +1,17 @@
 // lp_adamw.cu: AdamW over many tensors, the norm of their gradients, and the values
 // of 8-bit moments (include/lp_train.h).
+//
+// Every element is computed alone, so the step is bound by its bytes: with 32-bit moments, float32
+// gradients and a bfloat16 copy 30 an element, and 622 M elements take 2.63 ms, 7.1 TB/s.  With
+// 8-bit moments the bytes halve and the codes' integer work comes to light: 300 M elements with
+// float32 gradients took 926 us at 106 instructions an element and take 880 at 84, of 795 us at
+// the copy rate (issue slots 73%, ALU pipe 58% busy).  The values of 311 M elements' 8-bit moments
+// are written in 448 us, 6.9 TB/s.  300 tensors of 64 to 4 M elements, 113 M in all, take 578 us with
+// their norm, of which the step is 490 and reading the gradients for the norm 77.
+//
+// One launch: a table gives each CTA's row its tensor, and a tensor's blocks of 256 elements are a
+// warp's.  The moments' products are each rounded (no fused multiplication), so that 8-bit moments,
+// which are rounded by comparing bits, do not depend on how the arithmetic was compiled.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

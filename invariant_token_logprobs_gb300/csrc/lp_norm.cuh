@@ -275,14 +275,16 @@ struct Stream {
   }
 };
 
-// Zeros in the ring, for the threads whose groups lie past the row's columns.
+// Zeros in the ring, for the threads of kFast whose groups lie past the row's columns.  (Elsewhere
+// every group is written, or copied as zeros.)
 template <bool kFast, int G>
 __device__ __forceinline__ void clear_ring(unsigned char* ring, int bytes, const Place& p) {
-  const bool ragged = kFast && 8 * G * p.team != p.d;  // else every group is written, or copied as zeros
-  if (!ragged) return;
-  for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
-    reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
-  __syncthreads();
+  if constexpr (kFast) {
+    if (8 * G * p.team == p.d) return;
+    for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
+      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
 }
 
 // Rows of a team in the ring.  Eight, for deeper copies, made the backward of 4864 x 4096 69 us

@@ -5,6 +5,12 @@
 // the rest.  Up to kSmallRows rows one CTA does both from registers in one launch; beyond
 // that they are two grids over chunks of rows, launched as programmatic dependents.
 //
+// 512 rows take 3.3 us, next to nothing of it bytes: a launch, the loads, two barriers.  4.2 M rows
+// of 1024 ragged sequences take 34 us where their 103 MB are 15: the first pass reads 4 MB but
+// finds its sequences and adds its counts in a chain of some 8 us, and the second, 7 turns of rows a
+// CTA, spends a third of its time on the chain before the first turn and after the last.  One CTA
+// for everything took 11.6 ms; a chunk of 4096 rows a CTA 51 us, with 64-bit searches for each row.
+//
 // Counts are integers added by atomics, whose order does not show.  The loss's sums are
 // taken in a fixed order: a thread's rows, the CTA's tree, then the CTAs' sums by whichever
 // CTA finishes last.
