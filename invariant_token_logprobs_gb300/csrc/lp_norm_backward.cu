@@ -291,6 +291,10 @@ __global__ void __launch_bounds__(kMaxTeam)
         float* out = q == 0   ? a.grad_weight
                      : q == 1 ? a.grad_branch_weight
                               : static_cast<float*>(a.grad_gate.p);
+        if (c + 8 <= p.d && reinterpret_cast<uintptr_t>(out) % 32 == 0) {
+          store_group(out + c, pack(sum[k], float()));
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (c + e < p.d) out[c + e] = e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x;
