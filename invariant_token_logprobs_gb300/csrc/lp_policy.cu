@@ -5,11 +5,14 @@
 // the rest.  Up to kSmallRows rows one CTA does both from registers in one launch; beyond
 // that they are two grids over chunks of rows, launched as programmatic dependents.
 //
-// 512 rows take 3.3 us, next to nothing of it bytes: a launch, the loads, two barriers.  4.2 M rows
-// of 1024 ragged sequences take 34 us where their 103 MB are 15: the first pass reads 4 MB but
-// finds its sequences and adds its counts in a chain of some 8 us, and the second, 7 turns of rows a
-// CTA, spends a third of its time on the chain before the first turn and after the last.  One CTA
-// for everything took 11.6 ms; a chunk of 4096 rows a CTA 51 us, with 64-bit searches for each row.
+// 512 rows take 2.8 us, next to nothing of it bytes: a launch, the loads, two barriers.  4.2 M rows
+// of 1024 ragged sequences take 34 us where their 103 MB are 15: a turn of rows on all SMs takes
+// 2.7 us, 5.7 TB/s, and there are 7, but 15 us pass outside them.  The first pass reads 4 MB in some
+// 7 us, most of it the search for a CTA's sequences and the atomics' way; the second has its own
+// search before its first turn, and 3 us for the last CTA's sum.  Copies two turns ahead (34 us),
+// three or five CTAs an SM (34, 41) and a first pass of a quarter of the CTAs, to leave room for the
+// second's start (36), gained nothing.  One CTA for everything took 11.6 ms; a chunk of 4096 rows a
+// CTA 51 us, with 64-bit searches for each row.
 //
 // Counts are integers added by atomics, whose order does not show.  The loss's sums are
 // taken in a fixed order: a thread's rows, the CTA's tree, then the CTAs' sums by whichever
@@ -136,28 +139,29 @@ __device__ __forceinline__ void load_rows(const PolicyArgs& a, int64_t t, int64_
 __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int64_t T,
                                             const Four& f, unsigned kept, const float (&w)[4],
                                             float (&sum)[kStats]) {
-  float grad[4], grad_entropy[4];
+  float grad[4] = {0.f, 0.f, 0.f, 0.f}, grad_entropy[4] = {0.f, 0.f, 0.f, 0.f};
+  // A row that does not count, whatever it holds, is one of zeros: without branches the four rows'
+  // chains run side by side (512 rows: 2.8 us instead of 3.2).
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    grad[j] = grad_entropy[j] = 0.f;
-    if (!(kept >> j & 1u)) continue;  // whatever it holds
-    const float A = f.advantage[j], delta = f.logp[j] - f.old[j];
+    if (kept == 0) break;
+    const bool counts = kept >> j & 1u;
+    const float weight = counts ? w[j] : 0.f, A = counts ? f.advantage[j] : 0.f;
+    const float delta = counts ? f.logp[j] - f.old[j] : 0.f;
     const float ratio = __expf(delta);  // within 2 + |1.2 delta| units in the last place
     const bool over = A > 0.f && delta > a.high, under = A < 0.f && delta < a.low;
     const bool clipped = over || under;
     float g = clipped ? 0.f : -A * ratio;
-    sum[0] += w[j] * (-A * (over ? a.ratio_high : under ? a.ratio_low : ratio));
+    sum[0] += weight * (-A * (over ? a.ratio_high : under ? a.ratio_low : ratio));
     if (a.ref_logp != nullptr) {
-      const float r = f.ref[j] - f.logp[j], up = expm1f(r);
-      sum[1] += w[j] * (up - r);
+      const float r = counts ? f.ref[j] - f.logp[j] : 0.f, up = expm1f(r);
+      sum[1] += weight * (up - r);
       g -= a.kl_coef * up;
     }
-    if (a.entropy != nullptr) {
-      sum[2] += w[j] * f.entropy[j];
-      grad_entropy[j] = -a.entropy_coef * w[j];
-    }
-    if (clipped) sum[3] += w[j];
-    grad[j] = w[j] * g;
+    if (a.entropy != nullptr) sum[2] += weight * (counts ? f.entropy[j] : 0.f);
+    sum[3] += clipped ? weight : 0.f;
+    grad[j] = counts ? weight * g : 0.f;
+    grad_entropy[j] = counts ? -a.entropy_coef * weight : 0.f;
   }
   store4(a.grad_logp, t, T, a.wide, grad);
   if (a.grad_entropy != nullptr) store4(a.grad_entropy, t, T, a.wide, grad_entropy);
