@@ -8,6 +8,8 @@
 // 5.0 us, of which its 16.8 MB are 2.5: the rest is the launch and the chain of loads, two sums
 // and stores.  Rows that are not aligned cost up to twice that, in instructions (4864 x 2047
 // bfloat16 26 us, 4864 x 2048 12).  lp_norm.cuh says how rows lie over threads and come on chip.
+#include <type_traits>
+
 #include "lp_norm.cuh"
 
 namespace lp {
@@ -18,7 +20,7 @@ namespace {
 template <int G>
 constexpr int kRowsATurn = G == 1 ? 2 : 1;
 
-template <class R, class A, int G, bool kPost, bool kFast>
+template <class R, class A, int G, bool kPost, int kAlign>
 __global__ void __launch_bounds__(kMaxTeam, 2)
     lp_residual_norm_kernel(const __grid_constant__ NormArgs a, const Plan plan) {
   constexpr int kRows = kRowsATurn<G>;
@@ -30,10 +32,10 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
   int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
   if (!LP_CHECK(a.d <= a.residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
-  clear_ring<kFast, G>(ring, plan.stages * plan.stage_bytes, p);
+  clear_ring<kAlign, G>(ring, plan.stages * plan.stage_bytes, p);
   // a stage: the residual's rows, the branch's, the gate's
-  Stream<R> residual;
-  Stream<A> y, g;
+  Stream<R, kAlign> residual;
+  Stream<A, kAlign> y, g;
   uint32_t offset = 0;
   const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   residual.template start<G>(stage0, &offset);
@@ -45,9 +47,9 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   const auto fetch = [&](int stage) {
     if (next < a.T) {
       const uint32_t at = stage * plan.stage_bytes;
-      residual.template fetch<kFast, G>(a.residual, next, at, access_of(accesses, kResidual), p);
-      if (branch) y.template fetch<kFast, G>(a.branch, next, at, access_of(accesses, kBranch), p);
-      if (gate) g.template fetch<kFast, G>(a.gate, next, at, access_of(accesses, kGate), p);
+      residual.template fetch<G>(a.residual, next, at, access_of(accesses, kResidual), p);
+      if (branch) y.template fetch<G>(a.branch, next, at, access_of(accesses, kBranch), p);
+      if (gate) g.template fetch<G>(a.gate, next, at, access_of(accesses, kGate), p);
     }
     next += step;
     commit_copies();
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
 #pragma unroll
         for (int k = 0; k < G; ++k) {
           Pairs n;
-          y.get(at[j], k, n);
+          y.get(a.branch, t + j * step, at[j], k, n);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s = fma(n[e], n[e], s);
         }
@@ -106,16 +108,16 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         Pairs& vk = v[j][k];
-        residual.get(at[j], k, vk);
+        residual.get(a.residual, t + j * step, at[j], k, vk);
         if (!branch) continue;
         Pairs n;
-        y.get(at[j], k, n);
+        y.get(a.branch, t + j * step, at[j], k, n);
         if (kPost)
 #pragma unroll
           for (int e = 0; e < 4; ++e) n[e] = mul(mul(n[e], both(root_y[j])), wb[e]);
         if (gate) {
           Pairs f;
-          g.get(at[j], k, f);
+          g.get(a.gate, t + j * step, at[j], k, f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) n[e] = mul(n[e], f[e]);
         }
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
       if (branch)
 #pragma unroll
         for (int k = 0; k < G; ++k)
-          put<R, kFast>(a.residual_out, t + j * step, k, t + j * step < a.T,
+          put<R, kAlign>(a.residual_out, t + j * step, k, t + j * step < a.T,
                         access_of(accesses, kOut), p, stretch, v[j][k]);
     }
     if (!norm) continue;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
       for (int j = 0; j < kRows; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][k][e] = mul(mul(v[j][k][e], both(root[j])), w[e]);
-        put<A, kFast>(a.normed, t + j * step, k, t + j * step < a.T, access_of(accesses, kNormed),
+        put<A, kAlign>(a.normed, t + j * step, k, t + j * step < a.T, access_of(accesses, kNormed),
                       p, stretch, v[j][k]);
       }
     }
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
 constexpr int kForwardBytes = 216 << 10;
 
 template <int G>
-lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses, bool fast,
+lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses, Align align,
                          cudaStream_t stream) {
   return with_types(a.residual_bf16, a.act_bf16, [&](auto r, auto x) {
     using R = decltype(r);
@@ -177,21 +179,26 @@ lp_status launch_forward(const Device& dev, const NormArgs& a, uint32_t accesses
       const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
       // as many CTAs as leave each the rows that it works on: 4864 x 2048 in float32 with a gate
       // takes 34.8 us so, and 38 with one row more ahead and half of the CTAs
-      const int least = threads * G * 8 * columns * kRowsATurn<G> + (fast ? 0 : threads / 32 * kStretch);
+      const int least = stage_bytes_of(threads, G, columns, align != kAligned) * kRowsATurn<G> +
+                        (align == kAligned ? 0 : threads / 32 * kStretch);
       const int ctas = std::max(1, std::min(1024 / threads, kForwardBytes / least));
       const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
       const int64_t blocks = std::min<int64_t>(all, kSlots * ctas);
-      const int smem = plan_ring(&plan, columns, G, !fast, (all + blocks - 1) / blocks,
+      const int smem = plan_ring(&plan, columns, G, align != kAligned, (all + blocks - 1) / blocks,
                                  kRowsATurn<G>, kForwardBytes / ctas);
       kernel<<<unsigned(blocks), threads, smem, stream>>>(a, plan);
       return launched();
     };
-    static PerContextOnce once[4];
-    if (a.branch_weight != nullptr)
-      return fast ? launch(lp_residual_norm_kernel<R, A, G, true, true>, &once[0])
-                  : launch(lp_residual_norm_kernel<R, A, G, true, false>, &once[1]);
-    return fast ? launch(lp_residual_norm_kernel<R, A, G, false, true>, &once[2])
-                : launch(lp_residual_norm_kernel<R, A, G, false, false>, &once[3]);
+    static PerContextOnce once[6];
+    const auto with_post = [&](auto post, PerContextOnce* once) {
+      constexpr bool kPost = decltype(post)::value;
+      constexpr Align kLeast = sizeof(R) + sizeof(A) < 8 ? kByElements : kByWords;
+      return align == kAligned   ? launch(lp_residual_norm_kernel<R, A, G, kPost, kAligned>, once)
+             : align == kByWords ? launch(lp_residual_norm_kernel<R, A, G, kPost, kByWords>, once + 1)
+                                 : launch(lp_residual_norm_kernel<R, A, G, kPost, kLeast>, once + 2);
+    };
+    return a.branch_weight != nullptr ? with_post(std::true_type(), once)
+                                      : with_post(std::false_type(), once + 3);
   });
 }
 
@@ -208,10 +215,13 @@ lp_status launch_residual_norm(const Device& dev, const NormArgs& a, cudaStream_
   const bool fast = all_wide(accesses, {kResidual, kBranch, kGate, kOut, kNormed}, a.d) &&
                     near(a.residual) && near(a.branch) && near(a.gate) && near(a.residual_out) &&
                     near(a.normed);
+  const Align align = fast ? kAligned
+                      : any_halves(accesses, {kResidual, kBranch, kGate, kOut, kNormed}) ? kByElements
+                                                                                         : kByWords;
   // as few groups a thread as its team's 512 threads allow
-  if (a.d <= kMaxTeam * 8) return launch_forward<1>(dev, a, accesses, fast, stream);
-  if (a.d <= kMaxTeam * 16) return launch_forward<2>(dev, a, accesses, fast, stream);
-  return launch_forward<4>(dev, a, accesses, fast, stream);
+  if (a.d <= kMaxTeam * 8) return launch_forward<1>(dev, a, accesses, align, stream);
+  if (a.d <= kMaxTeam * 16) return launch_forward<2>(dev, a, accesses, align, stream);
+  return launch_forward<4>(dev, a, accesses, align, stream);
 }
 
 cudaError_t take_check_word_norm(uint32_t* out) { return take_check_word(out); }

@@ -9,9 +9,11 @@
 // A CTA takes rows in turn.  The operands of the next rows are on their way into a ring
 // of shared memory (cp.async) while the current one is computed, so that the two
 // sums of a row, each a wait for all its threads, do not leave the memory idle.  A thread
-// copies its own groups where every row is aligned for it (the kernels' kFast); else its
-// warp copies its stretch of the row, 32 neighbours an access.  The arithmetic and its
-// order are the same.
+// copies its own groups where every row is aligned for it; else its warp copies its stretch of
+// the row, 32 neighbouring words an access.  Where bfloat16 rows begin in the middle of a word,
+// the forward, whose two CTAs an SM hide the wait, loads elements; the backward copies the words that
+// hold the stretch and shifts the group out of them.  (4864 x 2397: 30 and 65 us.  The forward with
+// shifts takes 33, the backward with elements 116.)  The arithmetic and its order are the same.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -108,9 +110,12 @@ __device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
   return as_pair(r);
 }
 
-// How an operand's rows can be reached: whole groups, 4 bytes at a time, or only element by
-// element (bfloat16 at odd places).  2 bits an operand.
-enum Access : uint32_t { kPlain = 0, kWords = 1, kWide = 2 };
+// How an operand's rows can be reached: by whole groups, by words, or by words that some rows begin
+// in the middle of (bfloat16).  2 bits an operand.
+enum Access : uint32_t { kHalves = 0, kWords = 1, kWide = 2 };
+// What a kernel is built for: row operands of whole groups (d a multiple of 8, rows less than 2^32
+// bytes apart), none in the middle of a word, any by elements, any by words and shifts.
+enum Align : int { kAligned, kByWords, kByElements, kShifted };
 enum Operand : int {
   kResidual, kBranch, kGate, kOut, kNormed, kGradNormed, kGradOut, kGradResidual, kGradBranch,
   kGradGate, kBranchWeight, kWeight,
@@ -156,42 +161,51 @@ struct Place {
   }
 };
 
-// Where row t of an operand begins, `column` elements on.  With kFast rows are less than 2^32 bytes
+// Where row t of an operand begins, `column` elements on.  With kAligned rows are less than 2^32 bytes
 // apart, and the address is one multiplication.
-template <class T, bool kFast>
+template <class T, int kAlign>
 __device__ __forceinline__ T* row_at(const Rows& r, int64_t t, int column) {
-  if (kFast) {
+  if (kAlign == kAligned) {
     const uint64_t first = reinterpret_cast<uint64_t>(r.p) + uint32_t(column) * uint32_t(sizeof(T));
     return reinterpret_cast<T*>(first + uint64_t(uint32_t(t)) * uint32_t(r.ld * int64_t(sizeof(T))));
   }
   return static_cast<T*>(r.p) + t * r.ld + column;
 }
 
-// A row operand on its way through the ring: this thread's first group in stage 0.
-template <class T>
+// Whether row t of bfloat16 begins in the middle of a word.
+__device__ __forceinline__ bool mid_word(const Rows& r, int64_t t) {
+  return ((reinterpret_cast<uintptr_t>(r.p) >> 1) + uint32_t(t) * uint32_t(r.ld)) & 1u;
+}
+
+// A row operand on its way through the ring.
+template <class T, int kAlign>
 struct Stream {
-  uint32_t first;  // shared address
+  // rows that may begin in the middle of a word: a warp's stretch of such a row is copied from that
+  // word on, so that it takes a word more
+  static constexpr bool kMayShift = kAlign == kShifted && sizeof(T) == 2;
+  static constexpr uint32_t kWarp = 256 * uint32_t(sizeof(T)) + (kMayShift ? 16 : 0);
+  uint32_t first;  // the shared address of the thread's first group in stage 0
 
   // `offset` is the operand's first byte in a stage, moved past it.
   template <int G>
   __device__ __forceinline__ void start(uint32_t stage0, uint32_t* offset) {
-    first = stage0 + *offset + 8 * threadIdx.x * uint32_t(sizeof(T));
-    *offset += blockDim.x * G * 8 * uint32_t(sizeof(T));
+    first = stage0 + *offset + threadIdx.x / 32 * kWarp + (threadIdx.x & 31) * 8 * uint32_t(sizeof(T));
+    *offset += blockDim.x / 32 * G * kWarp;
   }
   __device__ __forceinline__ uint32_t slot(uint32_t at, int k) const {
-    return first + at + k * blockDim.x * 8 * uint32_t(sizeof(T));
+    return first + at + k * (blockDim.x / 32) * kWarp;
   }
   // Starts the copy of row t's groups into the stage `at` bytes on.  Columns past the row become
-  // zero (with kFast they are never written: the ring starts as zeros).
-  template <bool kFast, int G>
+  // zero (with kAligned they are never written: the ring starts as zeros).
+  template <int G>
   __device__ __forceinline__ void fetch(const Rows& r, int64_t t, uint32_t at, uint32_t access,
                                         const Place& p) const {
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       const uint32_t to = slot(at, k);
       const int c = 8 * (p.i + k * p.team);
-      if (kFast) {
-        const T* from = row_at<const T, true>(r, t, c);
+      if (kAlign == kAligned) {
+        const T* from = row_at<const T, kAligned>(r, t, c);
         if (c < p.d)
 #pragma unroll
           for (int q = 0; q < int(sizeof(T)) / 2; ++q)
@@ -200,8 +214,9 @@ struct Stream {
                          : "memory");
         continue;
       }
-      const T* row = row_at<const T, false>(r, t, 0);
-      const T* none = static_cast<const T*>(r.p);  // an address for copies of no bytes
+      const T* row = row_at<const T, kAlign>(r, t, 0);
+      // an address for copies of no bytes
+      const T* none = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(r.p) & ~uintptr_t(3));
       if (access == kWide) {  // aligned rows whose last group is not whole
 #pragma unroll
         for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
@@ -216,36 +231,47 @@ struct Stream {
       // the warp's stretch, 32 neighbours an access
       const int first_column = 8 * (p.i - p.lane + k * p.team);
       const bool whole = first_column + 256 <= p.d;
-      if (access != kPlain) {
-        constexpr int kOf4 = 4 / sizeof(T);
-        const uint32_t stretch = to - 8 * p.lane * uint32_t(sizeof(T)) + 4 * p.lane;
-        const T* from = row + first_column + p.lane * kOf4;
-        if (whole) {
-#pragma unroll
-          for (int q = 0; q < 2 * int(sizeof(T)); ++q)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stretch + 128 * q),
-                         "l"(from + 32 * q * kOf4)
-                         : "memory");
-          continue;
-        }
-#pragma unroll
-        for (int q = 0; q < 2 * int(sizeof(T)); ++q) {
-          const int left = p.d - first_column - (32 * q + p.lane) * kOf4;
-          const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stretch + 128 * q),
-                       "l"(bytes ? from + 32 * q * kOf4 : none), "r"(bytes)
-                       : "memory");
-        }
-      } else {
-        T* s = shared_pointer(to) - 7 * p.lane;
+      if (kAlign == kByElements && sizeof(T) == 2 && access == kHalves) {
+        T* to_first = shared_pointer(to) - 7 * p.lane;
         const T* from = row + first_column + p.lane;
         T v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           v[q] = whole || first_column + 32 * q + p.lane < p.d ? from[32 * q] : T(0.f);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s[32 * q] = v[q];
+        for (int q = 0; q < 8; ++q) to_first[32 * q] = v[q];
+        continue;
       }
+      constexpr int kOf4 = 4 / sizeof(T);
+      const int shift = kMayShift && mid_word(r, t) ? 1 : 0;
+      const uint32_t stretch = to - 8 * p.lane * uint32_t(sizeof(T)) + 4 * p.lane;
+      const T* from = row + first_column + p.lane * kOf4 - shift;
+      const auto copy = [&](int q) {
+        const int left = p.d - first_column + shift - (32 * q + p.lane) * kOf4;
+        const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stretch + 128 * q),
+                     "l"(bytes ? from + 32 * q * kOf4 : none), "r"(bytes)
+                     : "memory");
+      };
+      const T* begin = static_cast<const T*>(r.p);
+      const bool before = kMayShift && from < begin;  // nothing before the operand is read
+      if (kMayShift && shift != 0 && p.lane == 0) copy(2 * int(sizeof(T)));  // the word more
+      if (whole && !before) {
+#pragma unroll
+        for (int q = 0; q < 2 * int(sizeof(T)); ++q)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stretch + 128 * q),
+                       "l"(from + 32 * q * kOf4)
+                       : "memory");
+        continue;
+      }
+      if (before) {
+        shared_pointer(stretch)[0] = T(0.f);
+        shared_pointer(stretch)[1] = *begin;
+      } else {
+        copy(0);
+      }
+#pragma unroll
+      for (int q = 1; q < 2 * int(sizeof(T)); ++q) copy(q);
     }
   }
   // Zeros instead of a row that the team does not have: it then adds nothing to any sum.
@@ -254,12 +280,12 @@ struct Stream {
 #pragma unroll
     for (int k = 0; k < G; ++k)
 #pragma unroll
-      for (int q = 0; q < int(sizeof(T)) / 2; ++q)
+      for (int q = 0; q < int(sizeof(T)) / 2 + (kMayShift ? 1 : 0); ++q)
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot(at, k) + 16 * q), "r"(0)
                      : "memory");
   }
-  // The thread's group k in the stage `at` bytes on.
-  __device__ __forceinline__ void get(uint32_t at, int k, Pairs& v) const {
+  // The thread's group k of row t in the stage `at` bytes on.
+  __device__ __forceinline__ void get(const Rows& r, int64_t t, uint32_t at, int k, Pairs& v) const {
     const uint32_t from = slot(at, k);
     Group<T> g;
 #pragma unroll
@@ -268,6 +294,14 @@ struct Stream {
                    : "=r"(g.w[4 * q]), "=r"(g.w[4 * q + 1]), "=r"(g.w[4 * q + 2]), "=r"(g.w[4 * q + 3])
                    : "r"(from + 16 * q)
                    : "memory");
+    if constexpr (kMayShift) {
+      if (mid_word(r, t)) {
+        uint32_t after;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(after) : "r"(from + 16) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g.w[i] = __funnelshift_r(g.w[i], i < 3 ? g.w[i + 1] : after, 16);
+      }
+    }
     unpack(g, v);
   }
   static __device__ __forceinline__ T* shared_pointer(uint32_t address) {
@@ -275,11 +309,11 @@ struct Stream {
   }
 };
 
-// Zeros in the ring, for the threads of kFast whose groups lie past the row's columns.  (Elsewhere
+// Zeros in the ring, for the threads of kAligned whose groups lie past the row's columns.  (Elsewhere
 // every group is written, or copied as zeros.)
-template <bool kFast, int G>
+template <int kAlign, int G>
 __device__ __forceinline__ void clear_ring(unsigned char* ring, int bytes, const Place& p) {
-  if constexpr (kFast) {
+  if constexpr (kAlign == kAligned) {
     if (8 * G * p.team == p.d) return;
     for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -305,18 +339,18 @@ __device__ __forceinline__ void commit_copies() {
 
 // Writes the thread's group k of row t, through a warp's stretch of 256 elements where rows are not
 // aligned, if the team has the row.  All threads of a warp call it together.
-template <class T, bool kFast>
+template <class T, int kAlign>
 __device__ __forceinline__ void put(const Rows& r, int64_t t, int k, bool mine, uint32_t access,
                                     const Place& p, void* stretch, const Pairs& v) {
   if (!mine) return;
   const Group<T> g = pack(v, T());
   const int c = 8 * (p.i + k * p.team);
-  if (kFast) {
-    T* to = row_at<T, true>(r, t, c);
+  if (kAlign == kAligned) {
+    T* to = row_at<T, kAligned>(r, t, c);
     if (c < p.d) store_group(to, g);
     return;
   }
-  T* row = row_at<T, false>(r, t, 0);
+  T* row = row_at<T, kAlign>(r, t, 0);
   if (access == kWide) {
     if (c + 8 <= p.d) return store_group(row + c, g);
 #pragma unroll
@@ -329,16 +363,23 @@ __device__ __forceinline__ void put(const Rows& r, int64_t t, int k, bool mine, 
   __syncwarp();
   reinterpret_cast<Group<T>*>(s)[p.lane] = g;
   __syncwarp();
+  // 32 neighbours an access: words, or elements where rows may begin in the middle of a word (to shift
+  // a group over the warp instead cost 2 us of the forward's 33 for 4864 x 2397)
   T* to = row + first + p.lane;
   const T* from = s + p.lane;
-  if (first + 256 <= p.d) {
+  if (first + 256 > p.d) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (first + 32 * q + p.lane < p.d) to[32 * q] = from[32 * q];
+  } else if (kAlign == kByWords && sizeof(T) == 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      reinterpret_cast<uint32_t*>(row + first)[32 * q + p.lane] =
+          reinterpret_cast<const uint32_t*>(s)[32 * q + p.lane];
+  } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) to[32 * q] = from[32 * q];
-    return;
   }
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    if (first + 32 * q + p.lane < p.d) to[32 * q] = from[32 * q];
 }
 
 // Group k of a weight vector, of a type known at run time.  It is read again by every row, so it
@@ -448,7 +489,7 @@ Shape shape_of(int64_t d, int groups_per_thread, int64_t T) {
 uint32_t access_bits(int operand, const void* p, int64_t ld, bool bf16) {
   const uintptr_t size = bf16 ? 2 : 4;
   const uintptr_t at = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld) * size;
-  return (at % (8 * size) == 0 ? kWide : at % 4 == 0 ? kWords : kPlain) << 2 * operand;
+  return (at % (8 * size) == 0 ? kWide : at % 4 == 0 ? kWords : kHalves) << 2 * operand;
 }
 uint32_t access_bits(int operand, const Rows& r, bool bf16) {
   return access_bits(operand, r.p, r.p != nullptr ? r.ld : 0, bf16);
@@ -459,18 +500,27 @@ bool all_wide(uint32_t accesses, std::initializer_list<int> operands, int64_t d)
     if (access_of(accesses, o) != kWide) return false;
   return d % 8 == 0;
 }
+bool any_halves(uint32_t accesses, std::initializer_list<int> operands) {
+  for (int o : operands)
+    if (access_of(accesses, o) == kHalves) return true;
+  return false;
+}
 // Whether rows are near enough for 32-bit pitches in bytes.
 bool near(const Rows& r) { return r.p == nullptr || r.ld < (int64_t(1) << 30); }
 
 // The ring and, where an output is not aligned, the warps' stretches.
 constexpr int kRingBytes = 200 << 10;
 constexpr int kStretch = 256 * int(sizeof(float));
+// A stage: a row a team; where rows are not aligned 16 bytes more for each stretch of up to five operands.
+int stage_bytes_of(int threads, int groups, int column_bytes, bool stretches) {
+  return threads * groups * 8 * column_bytes + (stretches ? threads / 32 * groups * 6 * 16 : 0);
+}
 // Sets the stages, of one row a team, that fit `budget` bytes, at least `least`, and returns the
 // dynamic shared bytes.  `rows`: that a team takes in all.
 int plan_ring(Plan* plan, int column_bytes, int groups, bool stretches, int64_t rows, int least,
               int budget) {
   const int threads = plan->shape.team * plan->shape.teams;
-  plan->stage_bytes = threads * groups * 8 * column_bytes;
+  plan->stage_bytes = stage_bytes_of(threads, groups, column_bytes, stretches);
   const int extra = stretches ? threads / 32 * kStretch : 0;
   plan->stages = std::max(least, std::min({kMaxStages, (budget - extra) / plan->stage_bytes,
                                            int(std::min<int64_t>(rows, kMaxStages))}));

@@ -6,8 +6,9 @@
 // for the row's sums.  In float32 that is 52 us of 47 for 4864 x 2048.  The sums over rows cost
 // some 3 us a call, for the CTAs' partial sums and the second kernel.  History at 8192 x 4096: sums
 // in shared memory 1083 us, rows and sums in registers 158, with the ring and kept addresses 100,
-// two rows a turn 69, two columns an instruction 66.  lp_norm.cuh says how rows lie over threads
-// and come on chip.
+// two rows a turn 69, two columns an instruction 66.  A row's second pass beside the next row's
+// first one gained only with a normed branch of 4096 (59 us) and lost elsewhere (4864 x 2400: 58 us
+// instead of 50).  lp_norm.cuh says how rows lie over threads and come on chip.
 #include <type_traits>
 
 #include "lp_norm.cuh"
@@ -33,7 +34,7 @@ template <class R, class A, int G>
 constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) <= 6 ? 2 : 1;
 
 // kSolo: the CTA is one team, so that a turn's first row is there without asking.
-template <class R, class A, int G, int kRows, bool kPost, bool kFast, bool kSolo>
+template <class R, class A, int G, int kRows, bool kPost, int kAlign, bool kSolo>
 __global__ void __launch_bounds__(kMaxTeam)
     lp_residual_norm_grad_kernel(const __grid_constant__ NormGradArgs a, const Plan plan) {
   constexpr int kSums = kPost ? 3 : 1;
@@ -48,10 +49,10 @@ __global__ void __launch_bounds__(kMaxTeam)
   const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
   int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
   if (!LP_CHECK(a.d <= a.grad_residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
-  clear_ring<kFast, G>(ring, plan.stages * plan.stage_bytes, p);
+  clear_ring<kAlign, G>(ring, plan.stages * plan.stage_bytes, p);
   // a stage: the rows of the stream, its gradient, the norm's gradient, the branch, the gate
-  Stream<R> s, dr;
-  Stream<A> dh, y, g;
+  Stream<R, kAlign> s, dr;
+  Stream<A, kAlign> dh, y, g;
   uint32_t offset = 0;
   const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   if (norm) s.template start<G>(stage0, &offset);
@@ -67,13 +68,13 @@ __global__ void __launch_bounds__(kMaxTeam)
     const uint32_t at = stage * plan.stage_bytes;
     if (next < a.T) {
       if (norm) {
-        s.template fetch<kFast, G>(a.residual_out, next, at, access_of(accesses, kOut), p);
-        dh.template fetch<kFast, G>(a.grad_normed, next, at, access_of(accesses, kGradNormed), p);
+        s.template fetch<G>(a.residual_out, next, at, access_of(accesses, kOut), p);
+        dh.template fetch<G>(a.grad_normed, next, at, access_of(accesses, kGradNormed), p);
       }
       if (has_dr)
-        dr.template fetch<kFast, G>(a.grad_residual_out, next, at, access_of(accesses, kGradOut), p);
-      if (branch) y.template fetch<kFast, G>(a.branch, next, at, access_of(accesses, kBranch), p);
-      if (gate) g.template fetch<kFast, G>(a.gate, next, at, access_of(accesses, kGate), p);
+        dr.template fetch<G>(a.grad_residual_out, next, at, access_of(accesses, kGradOut), p);
+      if (branch) y.template fetch<G>(a.branch, next, at, access_of(accesses, kBranch), p);
+      if (gate) g.template fetch<G>(a.gate, next, at, access_of(accesses, kGate), p);
     } else {
       if (norm) s.template zero<G>(at), dh.template zero<G>(at);
       if (has_dr) dr.template zero<G>(at);
@@ -143,15 +144,15 @@ __global__ void __launch_bounds__(kMaxTeam)
         Pairs& xk = x[j][k];
         Pairs& Dk = D[j][k];
         if (has_dr) {
-          dr.get(at[j], k, Dk);
+          dr.get(a.grad_residual_out, t + j * step, at[j], k, Dk);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) Dk[e] = both(0.f);
         }
         if (norm) {
           Pairs h;
-          s.get(at[j], k, xk);
-          dh.get(at[j], k, h);
+          s.get(a.residual_out, t + j * step, at[j], k, xk);
+          dh.get(a.grad_normed, t + j * step, at[j], k, h);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 dx = mul(h[e], kKeep ? kept_w[e] : w[e]);
@@ -166,12 +167,12 @@ __global__ void __launch_bounds__(kMaxTeam)
         }
         if (kPost) {
           Pairs f;
-          y.get(at[j], k, f);
+          y.get(a.branch, t + j * step, at[j], k, f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[e] = mul(mul(f[e], both(root_y[j])), wb[e]);
           if (gate) {
             Pairs by;
-            g.get(at[j], k, by);
+            g.get(a.gate, t + j * step, at[j], k, by);
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = mul(f[e], by[e]);
           }
@@ -214,12 +215,12 @@ __global__ void __launch_bounds__(kMaxTeam)
           Dk[e] = fma(both(-m1[j]), x[j][k][e], Dk[e]);
           out[e] = mul(both(a.residual_scale), Dk[e]);
         }
-        put<R, kFast>(a.grad_residual, t + j * step, k, mine, access_of(accesses, kGradResidual), p,
+        put<R, kAlign>(a.grad_residual, t + j * step, k, mine, access_of(accesses, kGradResidual), p,
                       stretch, out);
         if (!branch) continue;
         Pairs yh;
         if (kPost || gate) {
-          y.get(at[j], k, yh);
+          y.get(a.branch, t + j * step, at[j], k, yh);
           if (kPost)
 #pragma unroll
             for (int e = 0; e < 4; ++e) yh[e] = mul(yh[e], both(scale_y[j]));
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kMaxTeam)
         for (int e = 0; e < 4; ++e) out[e] = mul(both(a.branch_scale), Dk[e]);
         if (gate) {
           Pairs f, dg;
-          g.get(at[j], k, f);
+          g.get(a.gate, t + j * step, at[j], k, f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             dg[e] = kPost ? mul(yh[e], wb[e]) : yh[e];
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kMaxTeam)
             out[e] = mul(out[e], f[e]);
           }
           if (write_gate)
-            put<A, kFast>(a.grad_gate, t + j * step, k, mine, access_of(accesses, kGradGate), p,
+            put<A, kAlign>(a.grad_gate, t + j * step, k, mine, access_of(accesses, kGradGate), p,
                           stretch, dg);
         }
         if (kPost) {
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kMaxTeam)
             out[e] = mul(both(scale_y[j]), fma(out[e], wb[e], mul(yh[e], both(-m2[j]))));
           }
         }
-        put<A, kFast>(a.grad_branch, t + j * step, k, mine, access_of(accesses, kGradBranch), p,
+        put<A, kAlign>(a.grad_branch, t + j * step, k, mine, access_of(accesses, kGradBranch), p,
                       stretch, out);
       }
     }
@@ -447,7 +448,7 @@ int64_t backward_blocks(int64_t T, int64_t d) {
 }
 
 template <int G>
-lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t accesses, bool fast,
+lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t accesses, Align align,
                           int64_t blocks, cudaStream_t stream) {
   return with_types(a.residual_bf16, a.act_bf16, [&](auto r, auto x) {
     using R = decltype(r);
@@ -460,27 +461,31 @@ lp_status launch_backward(const Device& dev, const NormGradArgs& a, uint32_t acc
       const int columns = (a.weight ? int(sizeof(R) + sizeof(A)) : 0) +
                           (a.grad_residual_out.p ? int(sizeof(R)) : 0) +
                           (a.branch.p ? int(sizeof(A)) : 0) + (a.gate.p ? int(sizeof(A)) : 0);
-      int smem = plan_ring(&plan, columns, G, !fast, rows, least,
+      int smem = plan_ring(&plan, columns, G, align != kAligned, rows, least,
                            kRingBytes / ctas_of_sm(plan.shape.team * plan.shape.teams));
       if (plan.shape.teams > 1) smem = std::max(smem, plan.shape.team * G * 8 * int(sizeof(float)));
       kernel<<<unsigned(blocks), plan.shape.team * plan.shape.teams, smem, stream>>>(a, plan);
       return launched();
     };
-    static PerContextOnce once[8];
+    static PerContextOnce once[10];
     const bool solo = plan.shape.teams == 1;
     const auto with_post = [&](auto post_, PerContextOnce* once) {
       constexpr bool kPost = decltype(post_)::value;
-      if (!fast) return launch(lp_residual_norm_grad_kernel<R, A, G, 1, kPost, false, false>, 1, once);
+      constexpr Align kLeast = sizeof(R) + sizeof(A) < 8 ? kShifted : kByWords;
+      if (align == kByWords)
+        return launch(lp_residual_norm_grad_kernel<R, A, G, 1, kPost, kByWords, false>, 1, once);
+      if (align == kShifted)
+        return launch(lp_residual_norm_grad_kernel<R, A, G, 1, kPost, kLeast, false>, 1, once + 1);
       if constexpr (kMost > 1)
         if (rows == 1)
-          return launch(lp_residual_norm_grad_kernel<R, A, G, 1, kPost, true, false>, 1, once + 1);
+          return launch(lp_residual_norm_grad_kernel<R, A, G, 1, kPost, kAligned, false>, 1, once + 2);
       return solo
-                 ? launch(lp_residual_norm_grad_kernel<R, A, G, kMost, kPost, true, true>, kMost, once + 2)
-                 : launch(lp_residual_norm_grad_kernel<R, A, G, kMost, kPost, true, false>, kMost,
-                          once + 3);
+                 ? launch(lp_residual_norm_grad_kernel<R, A, G, kMost, kPost, kAligned, true>, kMost, once + 3)
+                 : launch(lp_residual_norm_grad_kernel<R, A, G, kMost, kPost, kAligned, false>, kMost,
+                          once + 4);
     };
     return a.branch_weight != nullptr ? with_post(std::true_type(), once)
-                                      : with_post(std::false_type(), once + 4);
+                                      : with_post(std::false_type(), once + 5);
   });
 }
 
@@ -527,9 +532,14 @@ lp_status launch_residual_norm_backward(const Device& dev, const NormGradArgs& a
                       near(a.residual_out) && near(a.branch) && near(a.gate) && near(a.grad_normed) &&
                       near(a.grad_residual_out) && near(a.grad_residual) && near(a.grad_branch) &&
                       near(a.grad_gate);
+    const Align align =
+        fast ? kAligned
+        : any_halves(accesses, {kOut, kBranch, kGate, kGradNormed, kGradOut, kGradResidual, kGradBranch, kGradGate})
+            ? kShifted
+            : kByWords;
     const lp_status st = a.d > kTeamDim        ? launch_backward_wide(dev, a, blocks, stream)
-                         : groups_of(a.d) == 1 ? launch_backward<1>(dev, a, accesses, fast, blocks, stream)
-                                               : launch_backward<2>(dev, a, accesses, fast, blocks, stream);
+                         : groups_of(a.d) == 1 ? launch_backward<1>(dev, a, accesses, align, blocks, stream)
+                                               : launch_backward<2>(dev, a, accesses, align, blocks, stream);
     if (st != LP_OK) return st;
   }
   float* gate_sum = a.gate.ld == 0 ? static_cast<float*>(a.grad_gate.p) : nullptr;

@@ -185,6 +185,31 @@ def test_strides_and_alignment_keep_the_bits(pad, shift, gate):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("residual", [BF16, F32])
+@pytest.mark.parametrize("d", [1, 7, 255, 257, 1031, 4099])
+def test_rows_in_the_middle_of_a_word(d, residual):
+    """Rows at odd places, between NaN, have the bits that they have on boundaries of 16 columns."""
+    x = make(9, d, residual, BF16, BF16, True, "channel", seed=5)
+
+    def placed(t, ld, shift):
+        rows_of = t.view(1, -1) if t.dim() == 1 else t
+        out = torch.full((rows_of.shape[0] * ld + shift,), float("nan"), dtype=t.dtype, device=DEV)
+        out = out[shift:].view(-1, ld)[:, :d]
+        out.copy_(rows_of)
+        return out[0] if t.dim() == 1 else out
+
+    def run(ld, shift):
+        at = {k: tuple(placed(t, ld, shift) for t in v) if k == "grads" else placed(v, ld, shift)
+              for k, v in x.items()}
+        out = check_forward(at, 1.0, 0.5, 1e-6)
+        return list(out) + list(check_backward(at, out, 1.0, 0.5))
+
+    boundaries = run((d + 15) // 16 * 16, 0)
+    for ld, shift in ((d | 1, 0), (d | 1, 1), (d + 3 & ~1, 1)):
+        for a, b in zip(run(ld, shift), boundaries):
+            assert (a is None and b is None) or torch.equal(a, b)
+
+
 def test_without_branch_and_without_residual_gradient():
     x = make(11, 768, BF16, BF16, F32, False, None, branch=False)
     check_backward(x, check_forward(x, 1.0, 1.0, 1e-6), 1.0, 1.0, with_residual=False)
