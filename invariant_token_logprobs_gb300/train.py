@@ -323,13 +323,14 @@ class AdamW:
         self._allocate(state)
 
     def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
-        """Lays the plan of the step out for these gradient tensors."""
-        self.grads = list(grads)
-        if len(self.grads) != len(self.params):
+        """Lays the plan of the step out for these gradient tensors.  When they are refused the
+        optimizer stays as it was."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
             raise ValueError("grads must have one tensor for each param")
         written = self.params + [c for c in self.copies if c is not None]
-        _on_one_device(written + self.grads)
-        for p, g in zip(self.params, self.grads):
+        _on_one_device(written + grads)
+        for p, g in zip(self.params, grads):
             _dtype_code(g, "gradients")
             if g.shape != p.shape or not g.is_contiguous():
                 raise ValueError("gradients must be contiguous and of the params' shapes")
@@ -340,13 +341,14 @@ class AdamW:
         records = (_AdamwTensor * n)(*[
             _AdamwTensor(p.data_ptr(), None if c is None else c.data_ptr(), g.data_ptr(), p.numel(), s, w,
                          _dtype_code(g, "gradients"), 0)
-            for p, c, g, s, w in zip(self.params, self.copies, self.grads, self.lr_scale,
+            for p, c, g, s, w in zip(self.params, self.copies, grads, self.lr_scale,
                                      self.weight_decay)])
-        self.state_elements = int(lib.lp_adamw_state_elements(records, n))
+        elements = int(lib.lp_adamw_state_elements(records, n))
         size = int(lib.lp_adamw_plan_size(records, n))
         host = torch.empty(max(size, 1), dtype=torch.uint8)
         lp._check("lp_adamw_plan", lib.lp_adamw_plan(records, n, host.data_ptr(), size))
-        self._plan = host.to(self.params[0].device)
+        plan = host.to(self.params[0].device)
+        self.grads, self.state_elements, self._plan = grads, elements, plan
 
     def _allocate(self, state: Optional[dict]) -> None:
         n, device = self.state_elements, self.params[0].device
