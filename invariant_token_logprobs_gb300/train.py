@@ -275,10 +275,16 @@ def _per_tensor(value: Union[float, Sequence[float]], n: int, what: str) -> list
     return values
 
 
-def _disjoint(tensors: Sequence[torch.Tensor]) -> bool:
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                   for t in tensors if t.numel() > 0)
-    return all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+def _disjoint(written: Sequence[torch.Tensor], read: Sequence[torch.Tensor] = ()) -> bool:
+    """Whether no tensor that is written shares memory with another, written or read."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), kind)
+                   for kind, tensors in ((0, written), (1, read)) for t in tensors if t.numel() > 0)
+    end = [0, 0]  # of the spans before, by kind
+    for start, stop, kind in spans:
+        if start < end[0] or (kind == 0 and start < end[1]):
+            return False
+        end[kind] = max(end[kind], stop)
+    return True
 
 
 class AdamW:
@@ -347,6 +353,8 @@ class AdamW:
         size = int(lib.lp_adamw_plan_size(records, n))
         host = torch.empty(max(size, 1), dtype=torch.uint8)
         lp._check("lp_adamw_plan", lib.lp_adamw_plan(records, n, host.data_ptr(), size))
+        if not _disjoint(written, grads):
+            raise ValueError("gradients must not share memory with params or copies")
         plan = host.to(self.params[0].device)
         self.grads, self.state_elements, self._plan = grads, elements, plan
 

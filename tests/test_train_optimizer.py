@@ -26,3 +26,20 @@ def test_refused_gradients_leave_the_optimizer_as_it_was(on_cpu):
     other = torch.ones(300)
     opt.set_grads([other])
     assert opt.grads[0] is other and not torch.equal(opt._plan, plan)
+
+
+def test_gradients_in_the_memory_of_other_params_are_refused(on_cpu):
+    """A step takes its tensors in any order, so no gradient may lie in what it writes."""
+    flat = torch.zeros(1200)
+    p, g = [flat[:300], flat[300:600]], [flat[600:900], flat[900:]]
+    opt = train.AdamW(p, g)
+    copy = torch.zeros(300, dtype=torch.bfloat16)
+    for bad in ([g[0], p[0]], [p[1], g[1]], [flat[450:750], g[1]], [g[0], flat[299:599]]):
+        with pytest.raises((ValueError, train.LpError), match="share memory|INVALID"):
+            opt.set_grads(bad)
+    with pytest.raises(ValueError, match="share memory"):
+        train.AdamW(p, [g[0], copy], copies=[copy, None])
+    # one gradient of two params, and gradients that touch params without sharing a byte, are fine
+    opt.set_grads([g[0], g[0]])
+    opt.set_grads([flat[600:900], flat[600:900]])
+    train.AdamW([torch.zeros(0), flat[:300]], [torch.zeros(0), g[0]])
