@@ -287,6 +287,9 @@ def _disjoint(written: Sequence[torch.Tensor], read: Sequence[torch.Tensor] = ()
     return True
 
 
+_MOMENTS = ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
+
+
 class AdamW:
     """AdamW with decoupled weight decay over a list of tensors, one launch a step.
 
@@ -334,14 +337,14 @@ class AdamW:
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("grads must have one tensor for each param")
-        written = self.params + [c for c in self.copies if c is not None]
+        written = self._written()
         _on_one_device(written + grads)
         for p, g in zip(self.params, grads):
             _dtype_code(g, "gradients")
             if g.shape != p.shape or not g.is_contiguous():
                 raise ValueError("gradients must be contiguous and of the params' shapes")
         if not _disjoint(written):
-            raise ValueError("params and copies must not share memory")
+            raise ValueError("params, copies and moments must not share memory")
         lib = load()
         n = len(self.params)
         records = (_AdamwTensor * n)(*[
@@ -354,7 +357,7 @@ class AdamW:
         host = torch.empty(max(size, 1), dtype=torch.uint8)
         lp._check("lp_adamw_plan", lib.lp_adamw_plan(records, n, host.data_ptr(), size))
         if not _disjoint(written, grads):
-            raise ValueError("gradients must not share memory with params or copies")
+            raise ValueError("gradients must not share memory with params, copies or moments")
         plan = host.to(self.params[0].device)
         self.grads, self.state_elements, self._plan = grads, elements, plan
 
@@ -376,6 +379,13 @@ class AdamW:
                     raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector of {count}")
                 _on_one_device([self.params[0], t])
             setattr(self, name, t)
+        if not _disjoint(self._written(), self.grads):
+            raise ValueError("moments must not share memory with params, copies or gradients")
+
+    def _written(self) -> list[torch.Tensor]:
+        """What a step writes: params, copies and, once they are there, the moments."""
+        moments = [getattr(self, name, None) for name in _MOMENTS]
+        return self.params + [t for t in self.copies + moments if t is not None]
 
     def state_dict(self) -> dict:
         """The step count and the moments' buffers (not copied)."""

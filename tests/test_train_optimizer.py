@@ -43,3 +43,17 @@ def test_gradients_in_the_memory_of_other_params_are_refused(on_cpu):
     opt.set_grads([g[0], g[0]])
     opt.set_grads([flat[600:900], flat[600:900]])
     train.AdamW([torch.zeros(0), flat[:300]], [torch.zeros(0), g[0]])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_in_other_memory_of_the_step_are_refused(on_cpu, bits):
+    p, g = torch.zeros(4096), torch.zeros(4096)
+    kept = train.AdamW([p], [g], state_bits=bits).state_dict()
+    for name, spoiled in (("exp_avg", p), ("exp_avg_sq", g), ("exp_avg", kept["exp_avg_sq"])):
+        bad = spoiled if bits == 32 or spoiled.dtype == torch.uint8 else spoiled.view(torch.uint8)[:4096]
+        with pytest.raises(ValueError, match="share memory"):
+            train.AdamW([p], [g], state_bits=bits, state={**kept, name: bad})
+    opt = train.AdamW([p], [g], state_bits=bits, state=kept)
+    if bits == 32:
+        with pytest.raises(ValueError, match="share memory"):
+            opt.set_grads([opt.exp_avg])
