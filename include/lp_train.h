@@ -251,7 +251,7 @@ LP_API lp_status lp_adamw_grad_norm(const void* plan, int64_t n_tensors, int64_t
  *   grad_scale     [1] float32 that every gradient is multiplied by (norm_out + 1 of
  *                  lp_adamw_grad_norm), or NULL.  When it is NaN the step changes nothing.
  *   step           t >= 1, the number of this step; seed: of the 8-bit rounding.
- *   lr >= 0, 0 <= beta1, beta2 < 1, eps > 0, all finite.
+ *   lr >= 0, 0 <= beta1, beta2 < 1, eps >= 2^-126 (as a float32), all finite.
  */
 LP_API lp_status lp_adamw_step(const void* plan, int64_t n_tensors, int64_t state_elements,
                                int state_bits, void* exp_avg, void* exp_avg_sq,

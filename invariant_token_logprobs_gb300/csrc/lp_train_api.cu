@@ -4,6 +4,7 @@
 // workspace, device, and enqueues nothing before all checks pass.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -438,8 +439,11 @@ lp_status lp_adamw_step(const void* plan, int64_t n_tensors, int64_t state_eleme
   if (bad_plan(plan, n_tensors, state_elements) || (state_bits != 32 && state_bits != 8))
     return LP_ERR_INVALID_ARGUMENT;
   if (!(lr >= 0.0) || !std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) ||
-      !(beta2 >= 0.0 && beta2 < 1.0) || !(eps > 0.0) || !std::isfinite(eps) || step < 1)
+      !(beta2 >= 0.0 && beta2 < 1.0) || !std::isfinite(eps) || step < 1)
     return LP_ERR_INVALID_ARGUMENT;
+  // where both moments are zero the step divides by eps, in float32 arithmetic that reads a
+  // subnormal as zero
+  if (!(static_cast<float>(eps) >= FLT_MIN)) return LP_ERR_INVALID_ARGUMENT;
   const bool small = state_bits == 8;
   if (state_elements > 0 && (exp_avg == nullptr || exp_avg_sq == nullptr ||
                              mismatch(exp_avg_scale, small) || mismatch(exp_avg_sq_scale, small)))

@@ -57,3 +57,19 @@ def test_moments_in_other_memory_of_the_step_are_refused(on_cpu, bits):
     if bits == 32:
         with pytest.raises(ValueError, match="share memory"):
             opt.set_grads([opt.exp_avg])
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses stay off the GPU")
+def test_an_eps_that_the_step_would_read_as_zero_is_refused():
+    """With both moments zero the step divides by eps: one that is zero or subnormal in float32
+    made every such element NaN."""
+    a = [(1 << 20) + (i << 24) for i in range(5)]
+
+    def status(eps):
+        return train.load().lp_adamw_step(a[0], 1, 2048, 32, a[1], a[2], None, None, 1e-3, 0.9, 0.99,
+                                          eps, 1, 0, None, None)
+    invalid, unsupported = 1, 3  # the latter is what a valid call answers without a GPU
+    for eps in (0.0, -1e-8, 1e-300, 1e-46, 1e-40, 1.17e-38, float("nan"), float("inf")):
+        assert status(eps) == invalid, eps
+    for eps in (2.0 ** -126, 1.2e-38, 1e-30, 1e-8, 1.0):
+        assert status(eps) == unsupported, eps
