@@ -231,7 +231,8 @@ LP_API size_t lp_adamw_grad_norm_workspace_size(int64_t state_elements);
 
 /*
  * lp_adamw_grad_norm: norm_out[0] = the 2-norm of all gradients of the plan
- * (float32 within 2048 elements, float pairs across them, in a fixed order) and
+ * (float32 within 2048 elements, float pairs across them, in a fixed order; an
+ * infinity where the sum of the squares is none) and
  * norm_out[1] = min(1, max_norm / (norm + 1e-6)), NaN when the norm is not
  * finite.  plan, n_tensors and state_elements as in lp_adamw_step; max_norm > 0;
  * workspace 256-byte aligned.

@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(kNormThreads)
     s.add(slots[i].hi);
     s.lo += slots[i].lo;
   }
-  const float norm = sqrtf(s.hi + s.lo);
+  // beside an infinite sum the part that was lost is no number
+  const float norm = sqrtf(s.hi <= 0x1.fffffep127f ? s.hi + s.lo : s.hi);
   norm_out[0] = norm;
   norm_out[1] = norm <= 0x1.fffffep127f ? fminf(max_norm / (norm + 1e-6f), 1.f)
                                         : __int_as_float(0x7fffffff);
