@@ -9,6 +9,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -126,6 +128,11 @@ c10::Device device_of(const at::Tensor& first, std::initializer_list<const at::T
 }
 void* current_stream(c10::Device device) {
   return c10::cuda::getCurrentCUDAStream(device.index()).stream();
+}
+// The memory of a tensor that the caller cannot see or may drop is not handed out again before the
+// call on this stream is done.  (On the stream that it was allocated on this changes nothing.)
+void used_on(c10::cuda::CUDAStream stream, const at::Tensor* t) {
+  if (t != nullptr) c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), stream);
 }
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType s, c10::Device device) {
   return at::empty(sizes, at::TensorOptions().dtype(s).device(device));
@@ -418,10 +425,37 @@ PyObject* policy_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// Keeps what an optimizer's step reads and writes until it is done, wherever it runs: the plan and
+// the moments, and the tensors that the optimizer was given where the step is on another stream than
+// `home`, the one that the plan was laid out on.  A captured step reads its plan and gradients at
+// every replay: `captured` keeps them.
+void keep_for_step(c10::cuda::CUDAStream stream, PyObject* plan,
+                   std::initializer_list<const at::Tensor*> moments, PyObject* written, PyObject* grads,
+                   PyObject* home, PyObject* captured) {
+  if (!PyTuple_Check(written) || !PyTuple_Check(grads) || !PyList_Check(captured))
+    type_error("expected tuples of tensors and a list");
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+    const Py_ssize_t last = PyList_GET_SIZE(captured) - 1;
+    if (last >= 0 && PyTuple_GET_ITEM(PyList_GET_ITEM(captured, last), 0) == plan) return;
+    PyObject* both = PyTuple_Pack(2, plan, grads);
+    const int failed = both == nullptr ? -1 : PyList_Append(captured, both);
+    Py_XDECREF(both);
+    if (failed) throw Refused{};
+    return;
+  }
+  used_on(stream, tensor(plan, "plan"));
+  for (const at::Tensor* t : moments) used_on(stream, t);
+  if (integer(home) == int64_t(reinterpret_cast<intptr_t>(stream.stream()))) return;
+  for (PyObject* tensors : {written, grads})
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tensors); ++i)
+      used_on(stream, &required(PyTuple_GET_ITEM(tensors, i), "a tensor of the step"));
+}
+
 // plan, n_tensors, state_elements, state_bits, exp_avg, exp_avg_sq, exp_avg_scale,
-// exp_avg_sq_scale, lr, beta1, beta2, eps, step, seed, max_norm or None: the norm's tensor or None
+// exp_avg_sq_scale, lr, beta1, beta2, eps, step, seed, max_norm or None, written, grads, home,
+// captured: the norm's tensor or None
 PyObject* adamw_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 15, [&] {
+  return guarded(n, 19, [&] {
     const at::Tensor& plan = required(v[0], "plan");
     const int64_t tensors = integer(v[1]), elements = integer(v[2]);
     const at::Tensor &m = required(v[4], "exp_avg"), &u = required(v[5], "exp_avg_sq");
@@ -430,7 +464,9 @@ PyObject* adamw_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (PyErr_Occurred()) throw Refused{};
     const c10::Device device = device_of(plan, {&m, &u, m_scale, u_scale});
     const c10::cuda::CUDAGuard guard(device);
-    void* stream = current_stream(device);
+    const c10::cuda::CUDAStream on = c10::cuda::getCurrentCUDAStream(device.index());
+    void* stream = on.stream();
+    keep_for_step(on, v[0], {&m, &u, m_scale, u_scale}, v[15], v[16], v[17], v[18]);
     at::Tensor norm;
     const float* scale = nullptr;
     if (v[14] != Py_None) {
@@ -469,6 +505,8 @@ PyObject* adamw_state_values(PyObject*, PyObject* const* v, Py_ssize_t n) {
     made.add(&values, {elements}, at::kFloat);
     made.add(&squares, {elements}, at::kFloat);
     made.allocate();
+    for (const at::Tensor* t : {&m, &u, &m_scale, &u_scale})
+      used_on(c10::cuda::getCurrentCUDAStream(device.index()), t);
     check_status("lp_adamw_state_values",
                  lp.state_values(data(m), data(u), floats(m_scale), floats(u_scale), elements,
                                  floats(values), floats(squares), current_stream(device)));

@@ -301,7 +301,9 @@ class AdamW:
 
     state_bits=8 holds both moments in a byte an element and one scale for 256 elements, rounded
     without bias under `seed`; 32 holds them in float32.  `state`, as state_dict() gives it,
-    continues from it with its buffers.  set_grads() names other gradient tensors."""
+    continues from it with its buffers.  set_grads() names other gradient tensors.  A step on any
+    stream keeps its tensors' memory until it is done, so that they, and the optimizer, may be
+    dropped right after it."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], *,
                  copies: Optional[Sequence[Optional[torch.Tensor]]] = None, lr: float = 1e-3,
@@ -328,12 +330,14 @@ class AdamW:
             if c is not None and (c.dtype != torch.bfloat16 or c.shape != p.shape or
                                   not c.is_contiguous()):
                 raise TypeError("copies must be contiguous bfloat16 tensors of the params' shapes")
+        self._captured: list = []  # plans and gradients of steps that are parts of graphs
         self.set_grads(grads)
         self._allocate(state)
 
     def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
         """Lays the plan of the step out for these gradient tensors.  When they are refused the
-        optimizer stays as it was."""
+        optimizer stays as it was.  A step that was captured before goes on reading the gradients
+        that it was captured with, which the optimizer keeps."""
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("grads must have one tensor for each param")
@@ -359,7 +363,9 @@ class AdamW:
         if not _disjoint(written, grads):
             raise ValueError("gradients must not share memory with params, copies or moments")
         plan = host.to(self.params[0].device)
-        self.grads, self.state_elements, self._plan = grads, elements, plan
+        home = torch.cuda.current_stream(plan.device).cuda_stream if plan.is_cuda else 0
+        self.grads, self.state_elements, self._plan, self._home = grads, elements, plan, home
+        self._given = (tuple(self.params + [c for c in self.copies if c is not None]), tuple(grads))
 
     def _allocate(self, state: Optional[dict]) -> None:
         n, device = self.state_elements, self.params[0].device
@@ -402,7 +408,8 @@ class AdamW:
         norm = (_calls or load_calls()).adamw_step(
             self._plan, len(self.params), self.state_elements, self.state_bits, self.exp_avg,
             self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.lr if lr is None else lr,
-            self.betas[0], self.betas[1], self.eps, self.step_count + 1, self.seed, max_norm)
+            self.betas[0], self.betas[1], self.eps, self.step_count + 1, self.seed, max_norm,
+            *self._given, self._home, self._captured)
         self.step_count += 1
         return norm
 

@@ -21,3 +21,87 @@ def test_norm_of_gradients_that_are_not_finite(bits, value, want, at):
     norm = train.AdamW([p], [g], state_bits=bits).step(max_norm=1.0)
     assert str(float(norm)) == want
     assert torch.equal(p, torch.ones_like(p))
+
+
+def make_optimizer(bits, seed=1, sizes=(700, 9000)):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda n: torch.randn(n, generator=g, device=DEV)  # noqa: E731
+    return train.AdamW([r(n) for n in sizes], [r(n) for n in sizes],
+                       copies=[torch.zeros(n, dtype=BF16, device=DEV) for n in sizes], lr=1e-2, state_bits=bits)
+
+
+def busy_stream():
+    """A stream that is ordered after what was made so far and has some 0.1 s of work ahead."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    return side
+
+
+def overwrite(sizes):
+    """What comes next in memory of these sizes: tensors full of ones bits."""
+    return [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(64)]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("max_norm", [None, 0.5])
+def test_new_gradients_right_after_a_step_on_another_stream(bits, max_norm):
+    """Plan and gradients of a step that has not run yet are not handed out again."""
+    opt, twin = make_optimizer(bits), make_optimizer(bits)
+    twin.step(max_norm=max_norm)
+    twin.set_grads([g * 2 for g in twin.grads])
+    twin.step(max_norm=max_norm)
+    new = [g * 2 for g in opt.grads]
+    held = [opt._plan] + opt.grads
+    old = {t.data_ptr(): t.numel() * t.element_size() for t in held}
+    del held
+    side = busy_stream()
+    opt.step(max_norm=max_norm, stream=side)
+    opt.set_grads(new)
+    after = overwrite(old.values())
+    assert not side.query(), "the step has run: the test says nothing"
+    assert not {t.data_ptr() for t in after} & set(old)
+    torch.cuda.current_stream().wait_stream(side)
+    opt.step(max_norm=max_norm)
+    for a, b in zip(opt.params + opt.copies + list(opt.state_values()),
+                    twin.params + twin.copies + list(twin.state_values())):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_optimizer_that_is_dropped_right_after_a_step_on_another_stream(bits):
+    opt, twin = make_optimizer(bits), make_optimizer(bits)
+    twin.step()
+    params, copies = opt.params, opt.copies
+    held = [opt._plan, opt.exp_avg, opt.exp_avg_sq] + opt.grads
+    old = {t.data_ptr(): t.numel() * t.element_size() for t in held}
+    del held
+    side = busy_stream()
+    opt.step(stream=side)
+    del opt
+    after = overwrite(old.values())
+    assert not side.query(), "the step has run: the test says nothing"
+    assert not {t.data_ptr() for t in after} & set(old)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(params + copies, twin.params + twin.copies):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_step_keeps_the_plan_that_it_was_captured_with(bits):
+    opt, twin = make_optimizer(bits), make_optimizer(bits)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step(max_norm=0.5)
+    held = [opt._plan] + opt.grads
+    old = {t.data_ptr(): t.numel() * t.element_size() for t in held}
+    del held
+    opt.set_grads([g * 2 for g in opt.grads])
+    after = overwrite(old.values())
+    assert not {t.data_ptr() for t in after} & set(old)
+    graph.replay()
+    twin.step(max_norm=0.5)
+    for a, b in zip(opt.params + opt.copies + list(opt.state_values()),
+                    twin.params + twin.copies + list(twin.state_values())):
+        assert torch.equal(a, b)
