@@ -134,6 +134,11 @@ void* current_stream(c10::Device device) {
 void used_on(c10::cuda::CUDAStream stream, const at::Tensor* t) {
   if (t != nullptr) c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), stream);
 }
+// Tells autograd that a call has written a tensor of the caller's: a graph that saved the old values
+// refuses to go back through the new ones.
+void written_in_place(const at::Tensor* t) {
+  if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType s, c10::Device device) {
   return at::empty(sizes, at::TensorOptions().dtype(s).device(device));
 }
@@ -297,6 +302,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                   normed.defined() ? data(normed) : nullptr, o.d,
                                   branch_rstd.defined() ? floats(branch_rstd) : nullptr,
                                   rstd.defined() ? floats(rstd) : nullptr, current_stream(device)));
+    if (branch != nullptr && truth(v[8])) written_in_place(&residual);
     if (branch == nullptr || truth(v[8])) {  // the very object that was given
       PyObject* out = tuple_of({&normed, &normed, &rstd, &branch_rstd});
       PyObject* old = PyTuple_GET_ITEM(out, 1);
@@ -486,6 +492,9 @@ PyObject* adamw_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
                  lp.adamw_step(data(plan), tensors, elements, int(integer(v[3])), data(m), data(u),
                                floats(m_scale), floats(u_scale), number(v[8]), number(v[9]),
                                number(v[10]), number(v[11]), integer(v[12]), seed, scale, stream));
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(v[15]); ++i)
+      written_in_place(&required(PyTuple_GET_ITEM(v[15], i), "a tensor of the step"));
+    for (const at::Tensor* t : {&m, &u, m_scale, u_scale}) written_in_place(t);
     if (!norm.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(norm);
   });

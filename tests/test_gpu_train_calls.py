@@ -105,3 +105,37 @@ def test_a_captured_step_keeps_the_plan_that_it_was_captured_with(bits):
     for a, b in zip(opt.params + opt.copies + list(opt.state_values()),
                     twin.params + twin.copies + list(twin.state_values())):
         assert torch.equal(a, b)
+
+
+def test_writes_in_place_show_to_autograd():
+    """A graph that saved the old values does not go back through the new ones."""
+    residual, branch, w = (torch.randn(*s, device=DEV) for s in ((8, 64), (8, 64), (64,)))
+    x = torch.randn(8, 64, device=DEV, requires_grad=True)
+    y = (x * residual).sum()
+    train.residual_norm(residual, branch, weight=w)  # writes none of its inputs
+    y.backward(retain_graph=True)
+    train.residual_norm(residual, branch, weight=w, in_place=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        y.backward()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_step_shows_to_autograd(bits):
+    opt = make_optimizer(bits)
+    for t in opt.params + opt.copies:
+        x = torch.ones_like(t, requires_grad=True)
+        y = (x * t).sum()
+        opt.step(max_norm=1.0)
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            y.backward()
+    # gradients are read, and params may be of inference mode, where nothing is counted
+    for g in opt.grads:
+        x = torch.ones_like(g, requires_grad=True)
+        y = (x * g).sum()
+        opt.step()
+        y.backward()
+    with torch.inference_mode():
+        p = torch.ones(300, device=DEV)
+        before = p.clone()
+        train.AdamW([p], [torch.ones(300, device=DEV)], state_bits=bits).step()
+        assert not torch.equal(p, before)
