@@ -148,10 +148,16 @@ def _on_one_device(tensors: Sequence[torch.Tensor]) -> None:
         raise ValueError("expected CUDA tensors of one device")
 
 
-def _on_stream(stream, call, *args, **kw):
-    """call(*args, **kw) with `stream` (a torch stream or a handle) as the current one."""
+def _on_stream(stream, near, call, *args, **kw):
+    """call(*args, **kw) with `stream` (a torch stream, or a handle of the device that the tensor
+    `near` is on) as the current one."""
+    device = getattr(near, "device", None)
+    if device is None or device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError("the stream is one of another device")
     with torch.cuda.stream(stream):
         return call(*args, **kw)
 
@@ -188,7 +194,7 @@ def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
     (the residual's without branch).  Without branch the residual is normed as it stands.
     in_place=True writes r' over the residual."""
     if stream is not None:
-        return _on_stream(stream, residual_norm, residual, branch, weight=weight,
+        return _on_stream(stream, residual, residual_norm, residual, branch, weight=weight,
                           branch_weight=branch_weight, gate=gate, residual_scale=residual_scale,
                           branch_scale=branch_scale, eps=eps, in_place=in_place)
     return ResidualNorm._make((_calls or load_calls()).residual_norm(
@@ -216,8 +222,8 @@ def residual_norm_backward(grad_normed: Optional[torch.Tensor],
     weight_grads=False leaves out the gradients that are sums over the rows (weight,
     branch_weight and a one-row gate)."""
     if stream is not None:
-        return _on_stream(stream, residual_norm_backward, grad_normed, grad_residual, residual,
-                          rstd, branch=branch, weight=weight, branch_weight=branch_weight,
+        return _on_stream(stream, residual, residual_norm_backward, grad_normed, grad_residual,
+                          residual, rstd, branch=branch, weight=weight, branch_weight=branch_weight,
                           branch_rstd=branch_rstd, gate=gate, residual_scale=residual_scale,
                           branch_scale=branch_scale, weight_grads=weight_grads,
                           workspace=workspace)
@@ -254,7 +260,7 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     exp(r) - r - 1 of the divergence from the reference, entropy subtracts entropy_coef times the
     entropy."""
     if stream is not None:
-        return _on_stream(stream, policy_loss, logp, old_logp, advantages, mask=mask,
+        return _on_stream(stream, logp, policy_loss, logp, old_logp, advantages, mask=mask,
                           ref_logp=ref_logp, entropy=entropy, cu_seqlens=cu_seqlens,
                           reduction=reduction, per_sequence=per_sequence, clip_low=clip_low,
                           clip_high=clip_high, kl_coef=kl_coef, entropy_coef=entropy_coef,
@@ -404,7 +410,7 @@ class AdamW:
         of their global 2-norm, which is returned as a float32 scalar on the device; a norm that
         is not finite leaves every param and moment as it was (the step is counted)."""
         if stream is not None:
-            return _on_stream(stream, self.step, lr, max_norm)
+            return _on_stream(stream, self.params[0], self.step, lr, max_norm)
         norm = (_calls or load_calls()).adamw_step(
             self._plan, len(self.params), self.state_elements, self.state_bits, self.exp_avg,
             self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.lr if lr is None else lr,
@@ -419,7 +425,7 @@ class AdamW:
         if self.state_bits == 32:
             return self.exp_avg, self.exp_avg_sq
         if stream is not None:
-            return _on_stream(stream, self.state_values)
+            return _on_stream(stream, self.exp_avg, self.state_values)
         return (_calls or load_calls()).adamw_state_values(
             self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
 
