@@ -243,8 +243,13 @@ class _PolicyLoss(torch.autograd.Function):
 
 
 def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, *,
-                entropy: Optional[torch.Tensor] = None, **kw):
+                entropy: Optional[torch.Tensor] = None, stream=None, **kw):
     """(loss, stats [5]) of train.policy_loss, the loss a float32 scalar that is differentiable in
     logp and entropy: the gradients are written by the forward call and scaled in the backward.
-    Keyword arguments are train.policy_loss's."""
+    Keyword arguments are train.policy_loss's.  With a stream all of the forward runs there, and so
+    does its part of the backward, which autograd orders; using the results after the work on that
+    stream is the caller's to order, as in train.py."""
+    if stream is not None:
+        return train._on_stream(stream, logp, policy_loss, logp, old_logp, advantages,
+                                entropy=entropy, **kw)
     return _PolicyLoss.apply(logp, entropy, old_logp, advantages, kw)

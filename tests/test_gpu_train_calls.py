@@ -139,3 +139,23 @@ def test_a_step_shows_to_autograd(bits):
         before = p.clone()
         train.AdamW([p], [torch.ones(300, device=DEV)], state_bits=bits).step()
         assert not torch.equal(p, before)
+
+
+def test_policy_loss_autograd_on_another_stream():
+    """The loss is a copy of the call's first statistic: made on the call's stream, after it."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    T = 3000
+    logp = -torch.rand(T, generator=g, device=DEV)
+    old = logp + 0.2 * torch.randn(T, generator=g, device=DEV)
+    A, ent = torch.randn(T, generator=g, device=DEV), torch.rand(T, generator=g, device=DEV)
+    ref = train.policy_loss(logp, old, A, entropy=ent, entropy_coef=0.1)
+    a, b = logp.clone().requires_grad_(), ent.clone().requires_grad_()
+    for given in (lambda s: s, lambda s: s.cuda_stream):
+        overwrite([512, 4 * T])  # what is left in memory that the outputs may get
+        side = busy_stream()
+        loss, stats = autograd.policy_loss(a, old, A, entropy=b, entropy_coef=0.1, stream=given(side))
+        assert not side.query(), "the call has run: the test says nothing"
+        torch.cuda.current_stream().wait_stream(side)
+        ga, gb = torch.autograd.grad(3 * loss, (a, b))
+        assert torch.equal(stats, ref.stats) and float(loss.detach()) == float(ref.stats[0])
+        assert torch.equal(ga, 3 * ref.grad_logp) and torch.equal(gb, 3 * ref.grad_entropy)
