@@ -27,17 +27,46 @@ Gradients come back in the inputs' dtypes: grad_H is the float32 result
 rounded to H's dtype; grad_W is asked of the library in bfloat16 when W is
 bfloat16 (the float32 result rounded to nearest even, the same bits as
 rounding it afterwards) and in float32 otherwise.  An output the loss does not
-use contributes nothing (its upstream gradient is passed as absent).
+use contributes nothing (its upstream gradient is passed as absent).  A
+gradient of a gradient is refused: the backward kernels have no derivative.
 """
 
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
 
 from . import lp, train
 from . import vocab_parallel as vp
+
+
+class _Refusal(torch.autograd.Function):
+    """Gradients as they are, whose own gradient is refused."""
+
+    @staticmethod
+    def forward(ctx, *grads):
+        return tuple(None if g is None else g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("a gradient of a gradient was asked for: the library's backward calls "
+                           "have no derivative")
+
+
+def _first_order(backward):
+    """A backward whose gradients are no constants of a graph made with create_graph=True: going
+    back through them raises.  (torch's once_differentiable refuses only where an upstream gradient
+    has a graph, so that the plain sum of an output would still lose its second-order terms.)"""
+    @functools.wraps(backward)
+    def wrapped(ctx, *upstream):
+        with torch.no_grad():
+            grads = backward(ctx, *upstream)
+        if not torch.is_grad_enabled():
+            return grads
+        return _Refusal.apply(*[None if g is None else g.detach().requires_grad_() for g in grads])
+    return wrapped
 
 
 class _LinearLogprob(torch.autograd.Function):
@@ -50,6 +79,7 @@ class _LinearLogprob(torch.autograd.Function):
         return logp, entropy
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_logp, g_entropy):
         H, W, y, lse, entropy = ctx.saved_tensors
         need_h, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -83,6 +113,7 @@ class _LogprobFromLogits(torch.autograd.Function):
         return logp, entropy
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_logp, g_entropy):
         z, y, lse, entropy = ctx.saved_tensors
         if not ctx.needs_input_grad[0] or (g_logp is None and g_entropy is None):
@@ -114,6 +145,7 @@ class _VocabParallelLinearLogprob(torch.autograd.Function):
         return logp, entropy
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_logp, g_entropy):
         H, W_shard, y, lse, entropy = ctx.saved_tensors
         need_h, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -154,6 +186,7 @@ class _VocabParallelLogprobFromLogits(torch.autograd.Function):
         return logp, entropy
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_logp, g_entropy):
         z_shard, y, lse, entropy = ctx.saved_tensors
         if not ctx.needs_input_grad[0] or (g_logp is None and g_entropy is None):
@@ -193,6 +226,7 @@ class _ResidualNorm(torch.autograd.Function):
         return out.normed, None if branch is None else out.residual
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_normed, g_residual):
         branch, weight, branch_weight, gate, residual, rstd, branch_rstd = ctx.saved_tensors
         if g_normed is None and g_residual is None:
@@ -234,6 +268,7 @@ class _PolicyLoss(torch.autograd.Function):
         return out.stats[0].clone(), out.stats
 
     @staticmethod
+    @_first_order
     def backward(ctx, g_loss, _):
         g_logp, g_entropy = ctx.saved_tensors
         need_logp, need_entropy = ctx.needs_input_grad[:2]

@@ -159,3 +159,27 @@ def test_policy_loss_autograd_on_another_stream():
         ga, gb = torch.autograd.grad(3 * loss, (a, b))
         assert torch.equal(stats, ref.stats) and float(loss.detach()) == float(ref.stats[0])
         assert torch.equal(ga, 3 * ref.grad_logp) and torch.equal(gb, 3 * ref.grad_entropy)
+
+
+def second_order(y, x):
+    g, = torch.autograd.grad(y, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="gradient of a gradient"):
+        (g.float().square().sum() + y).backward()  # a penalty on the gradient beside the loss
+
+
+def test_a_gradient_of_a_gradient_is_refused():
+    """The backward calls have no derivative; leaving its terms out in silence would be wrong."""
+    x = torch.randn(4, 64, device=DEV, requires_grad=True)
+    branch = torch.randn(4, 64, device=DEV, requires_grad=True)
+    w = torch.ones(64, device=DEV, requires_grad=True)
+    for wanted in (x, branch, w):
+        h, new = autograd.residual_norm(x, branch, weight=w)
+        second_order((h * new).sum(), wanted)
+    logp = (-torch.rand(9, device=DEV)).requires_grad_()
+    second_order(autograd.policy_loss(logp, logp.detach(), torch.ones(9, device=DEV))[0], logp)
+    H = torch.randn(16, 64, device=DEV).to(BF16).requires_grad_()
+    W = torch.randn(512, 64, device=DEV).to(BF16)
+    y = torch.arange(16, device=DEV)
+    second_order(autograd.linear_logprob(H, W, y)[0].sum(), H)
+    z = torch.randn(16, 512, device=DEV, requires_grad=True)
+    second_order(autograd.logprob_from_logits(z, y)[0].sum(), z)
