@@ -143,41 +143,57 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType s, c10::Device device) {
   return at::empty(sizes, at::TensorOptions().dtype(s).device(device));
 }
 
-// The tensors that a call allocates.  An allocation takes 1.4 us on the host, about half of what a
-// launch does, so the small ones, and all of a small call's, are parts of one; large ones are
-// allocated each, so that none keeps another's memory.
+// The tensors that a call allocates.  An allocation takes 1 us on the host, half of what a launch
+// does, so the small ones of one dtype, and all of one dtype of a small call's, are parts of one;
+// large ones are allocated each, so that none keeps another's memory.  Tensors of two dtypes share
+// none: torch.save refuses them.
 class Tensors {
  public:
   explicit Tensors(c10::Device device) : device_(device) {}
   // A tensor to be allocated, contiguous; `out` is set by allocate().
   void add(at::Tensor* out, std::initializer_list<int64_t> sizes, at::ScalarType type) {
     Item& item = items_[count_++];
-    item = {out, {1, 1}, int(sizes.size()), type, int64_t(c10::elementSize(type))};
+    item = {out, {1, 1}, int(sizes.size()), type, type, int64_t(c10::elementSize(type))};
     int i = 0;
     for (int64_t n : sizes) item.bytes *= item.sizes[i++] = n;
     item.bytes = (item.bytes + 255) / 256 * 256;
     all_ += item.bytes;
   }
+  // Scratch of so many bytes.  It is a part of the float32 tensors' allocation if it is next to
+  // nothing, and is not kept by what the call returns otherwise.
+  void scratch(at::Tensor* out, size_t bytes) {
+    const int64_t n = std::max<int64_t>(int64_t(bytes), 256);
+    if (n > 256) {
+      *out = empty({n}, at::kByte, device_);
+      return;
+    }
+    add(out, {n}, at::kByte);
+    items_[count_ - 1].with = at::kFloat;
+  }
   void allocate() {
     const int64_t part = all_ <= kSmallCall ? kSmallCall : kSmallTensor;  // the largest part
-    int64_t together = 0, at = 0;
-    for (int i = 0; i < count_; ++i)
-      if (items_[i].bytes <= part) together += items_[i].bytes;
-    const at::Tensor whole = empty({together}, at::kByte, device_);
-    for (int i = 0; i < count_; ++i) {
-      const Item& item = items_[i];
-      const at::IntArrayRef sizes(item.sizes, size_t(item.dims));
-      if (item.bytes > part) {
-        *item.out = empty(sizes, item.type, device_);
-        continue;
+    for (at::ScalarType type : {at::kFloat, at::kBFloat16}) {
+      int64_t together = 0, at = 0;
+      for (int i = 0; i < count_; ++i)
+        if (items_[i].with == type && items_[i].bytes <= part) together += items_[i].bytes;
+      at::Tensor whole;
+      for (int i = 0; i < count_; ++i) {
+        const Item& item = items_[i];
+        if (item.with != type) continue;
+        const at::IntArrayRef sizes(item.sizes, size_t(item.dims));
+        if (item.bytes > part) {
+          *item.out = empty(sizes, item.type, device_);
+          continue;
+        }
+        if (!whole.defined()) whole = empty({together}, at::kByte, device_);
+        *item.out = at::detail::make_tensor<c10::TensorImpl>(
+            c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+            c10::scalarTypeToTypeMeta(item.type));
+        c10::TensorImpl* impl = item.out->unsafeGetTensorImpl();
+        impl->set_storage_offset(at / int64_t(c10::elementSize(item.type)));
+        impl->set_sizes_contiguous(sizes);
+        at += item.bytes;
       }
-      *item.out = at::detail::make_tensor<c10::TensorImpl>(
-          c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
-          c10::scalarTypeToTypeMeta(item.type));
-      c10::TensorImpl* impl = item.out->unsafeGetTensorImpl();
-      impl->set_storage_offset(at / int64_t(c10::elementSize(item.type)));
-      impl->set_sizes_contiguous(sizes);
-      at += item.bytes;
     }
   }
 
@@ -188,6 +204,7 @@ class Tensors {
     int64_t sizes[2];
     int dims;
     at::ScalarType type;
+    at::ScalarType with;  // the dtype whose allocation it is a part of
     int64_t bytes;
   };
   c10::Device device_;
@@ -354,7 +371,7 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
         bytes = given->nbytes();
       } else {
         bytes = lp.norm_workspace(o.T, o.d);
-        made.add(&workspace, {int64_t(std::max<size_t>(bytes, 256))}, at::kByte);
+        made.scratch(&workspace, bytes);
       }
     }
     made.allocate();
@@ -416,7 +433,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
       bytes = given->nbytes();
     } else {
       bytes = lp.policy_workspace(T, sequences);
-      made.add(&workspace, {int64_t(std::max<size_t>(bytes, 256))}, at::kByte);
+      made.scratch(&workspace, bytes);
     }
     made.allocate();
     check_status("lp_policy_loss",
@@ -480,7 +497,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
       at::Tensor workspace;
       Tensors made(device);
       made.add(&norm, {2}, at::kFloat);
-      made.add(&workspace, {int64_t(std::max<size_t>(bytes, 256))}, at::kByte);
+      made.scratch(&workspace, bytes);
       made.allocate();
       check_status("lp_adamw_grad_norm",
                    lp.grad_norm(data(plan), tensors, elements, float(number(v[14])), floats(norm),

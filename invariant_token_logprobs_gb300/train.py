@@ -12,6 +12,9 @@ checks and allocations are compiled (csrc/train_calls.cpp, built next to liblp),
 since the smallest ones take 3 us on the GPU.  A call given
 another stream runs there, its outputs and workspace are allocated for that
 stream, and ordering it after the work that made its inputs is the caller's.
+
+Small outputs of one dtype (up to 64 KB each, or 256 KB a call) are parts of one allocation:
+any of them keeps its memory, and torch.save writes all of it.
 """
 
 from __future__ import annotations

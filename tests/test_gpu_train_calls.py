@@ -183,3 +183,26 @@ def test_a_gradient_of_a_gradient_is_refused():
     second_order(autograd.linear_logprob(H, W, y)[0].sum(), H)
     z = torch.randn(16, 512, device=DEV, requires_grad=True)
     second_order(autograd.logprob_from_logits(z, y)[0].sum(), z)
+
+
+@pytest.mark.parametrize("T", [1, 4, 300, 3000])
+def test_results_can_be_saved(T, tmp_path):
+    """Whatever the sizes, all results of a call go through torch.save, of small calls in little."""
+    d = 64
+    r, y = (torch.randn(T, d, device=DEV).to(BF16) for _ in range(2))
+    w, gate = torch.ones(d, device=DEV), torch.ones(d, device=DEV, dtype=BF16)
+    out = train.residual_norm(r, y, weight=w, branch_weight=w, gate=gate)
+    grads = train.residual_norm_backward(r, y, out.residual, out.rstd, branch=y, weight=w, branch_weight=w,
+                                         branch_rstd=out.branch_rstd, gate=gate)
+    logp = -torch.rand(T, device=DEV)
+    loss = train.policy_loss(logp, logp, logp, entropy=-logp)
+    opt = train.AdamW([torch.ones(9000, device=DEV)], [torch.ones(9000, device=DEV)], state_bits=8)
+    step = (opt.step(max_norm=1.0), *opt.state_values())
+    for results in (out, grads, loss, step):
+        path = tmp_path / "results.pt"
+        torch.save(tuple(results), path)
+        for a, b in zip(torch.load(path), results):
+            assert torch.equal(a, b) and a.dtype == b.dtype
+        held = sum({t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in results}.values())
+        whole = sum(t.numel() * t.element_size() for t in results)
+        assert held <= whole + 256 * (len(results) + 1)  # each rounded up, and next to no scratch
