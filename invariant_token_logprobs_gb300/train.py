@@ -310,7 +310,7 @@ class AdamW:
 
     state_bits=8 holds both moments in a byte an element and one scale for 256 elements, rounded
     without bias under `seed`; 32 holds them in float32.  `state`, as state_dict() gives it,
-    continues from it with its buffers.  set_grads() names other gradient tensors.  A step on any
+    continues from it with its buffers, and with its seed where none is given.  set_grads() names other gradient tensors.  A step on any
     stream keeps its tensors' memory until it is done, so that they, and the optimizer, may be
     dropped right after it."""
 
@@ -319,7 +319,7 @@ class AdamW:
                  betas: tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: Union[float, Sequence[float]] = 0.01,
                  lr_scale: Union[float, Sequence[float]] = 1.0, state_bits: int = 32,
-                 seed: int = 0, state: Optional[dict] = None):
+                 seed: Optional[int] = None, state: Optional[dict] = None):
         self.params = list(params)
         n = len(self.params)
         if n == 0:
@@ -332,6 +332,8 @@ class AdamW:
         self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
         self.weight_decay = _per_tensor(weight_decay, n, "weight_decay")
         self.lr_scale = _per_tensor(lr_scale, n, "lr_scale")
+        if seed is None:
+            seed = 0 if state is None else state.get("seed", 0)
         self.state_bits, self.seed = state_bits, int(seed) & (2**64 - 1)
         for p, c in zip(self.params, self.copies):
             if p.dtype != torch.float32 or not p.is_contiguous():
@@ -403,9 +405,10 @@ class AdamW:
         return self.params + [t for t in self.copies + moments if t is not None]
 
     def state_dict(self) -> dict:
-        """The step count and the moments' buffers (not copied)."""
-        return {"step": self.step_count, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
-                "exp_avg_scale": self.exp_avg_scale, "exp_avg_sq_scale": self.exp_avg_sq_scale}
+        """The step count, the seed and the moments' buffers (not copied)."""
+        return {"step": self.step_count, "seed": self.seed, "exp_avg": self.exp_avg,
+                "exp_avg_sq": self.exp_avg_sq, "exp_avg_scale": self.exp_avg_scale,
+                "exp_avg_sq_scale": self.exp_avg_sq_scale}
 
     def step(self, lr: Optional[float] = None, max_norm: Optional[float] = None,
              stream=None) -> Optional[torch.Tensor]:

@@ -73,3 +73,15 @@ def test_an_eps_that_the_step_would_read_as_zero_is_refused():
         assert status(eps) == invalid, eps
     for eps in (2.0 ** -126, 1.2e-38, 1e-30, 1e-8, 1.0):
         assert status(eps) == unsupported, eps
+
+
+def test_a_state_brings_its_seed(on_cpu):
+    """The rounding of 8-bit moments goes on as it would have."""
+    p, g = torch.zeros(300), torch.zeros(300)
+    state = train.AdamW([p], [g], state_bits=8, seed=77).state_dict()
+    assert train.AdamW([p], [g], state_bits=8, state=state).seed == 77
+    assert train.AdamW([p], [g], state_bits=8, state=state, seed=0).seed == 0
+    del state["seed"]
+    assert train.AdamW([p], [g], state_bits=8, state=state).seed == 0
+    assert train.AdamW([p], [g], state_bits=8).seed == 0
+    assert train.AdamW([p], [g], state_bits=8, seed=-1).seed == 2 ** 64 - 1
