@@ -277,8 +277,8 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
 
 # ------------------------------------------------------------------------ AdamW
 
-def _per_tensor(value: Union[float, Sequence[float]], n: int, what: str) -> list[float]:
-    values = [float(value)] * n if isinstance(value, (int, float)) else [float(v) for v in value]
+def _per_tensor(value: Union[float, Sequence[float]], n: int, what: str) -> tuple[float, ...]:
+    values = (float(value),) * n if isinstance(value, (int, float)) else tuple(float(v) for v in value)
     if len(values) != n:
         raise ValueError(f"{what} must be a number or one for each tensor")
     return values
@@ -330,8 +330,8 @@ class AdamW:
         if len(self.copies) != n:
             raise ValueError("copies must have one tensor or None for each param")
         self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
-        self.weight_decay = _per_tensor(weight_decay, n, "weight_decay")
-        self.lr_scale = _per_tensor(lr_scale, n, "lr_scale")
+        self._weight_decay = _per_tensor(weight_decay, n, "weight_decay")
+        self._lr_scale = _per_tensor(lr_scale, n, "lr_scale")
         if seed is None:
             seed = 0 if state is None else state.get("seed", 0)
         self.state_bits, self.seed = state_bits, int(seed) & (2**64 - 1)
@@ -349,7 +349,30 @@ class AdamW:
         """Lays the plan of the step out for these gradient tensors.  When they are refused the
         optimizer stays as it was.  A step that was captured before goes on reading the gradients
         that it was captured with, which the optimizer keeps."""
-        grads = list(grads)
+        self._lay_out(list(grads), self._weight_decay, self._lr_scale)
+
+    @property
+    def weight_decay(self) -> tuple[float, ...]:
+        """Each tensor's weight decay; assigned as a number or one for each tensor, it holds from
+        the next step on."""
+        return self._weight_decay
+
+    @weight_decay.setter
+    def weight_decay(self, value: Union[float, Sequence[float]]) -> None:
+        self._lay_out(self.grads, _per_tensor(value, len(self.params), "weight_decay"), self._lr_scale)
+
+    @property
+    def lr_scale(self) -> tuple[float, ...]:
+        """Each tensor's factor of the learning rate, assigned like weight_decay."""
+        return self._lr_scale
+
+    @lr_scale.setter
+    def lr_scale(self, value: Union[float, Sequence[float]]) -> None:
+        self._lay_out(self.grads, self._weight_decay, _per_tensor(value, len(self.params), "lr_scale"))
+
+    def _lay_out(self, grads: list[torch.Tensor], weight_decay: tuple[float, ...],
+                 lr_scale: tuple[float, ...]) -> None:
+        """Checks these and lays the plan out; nothing is kept of what is refused."""
         if len(grads) != len(self.params):
             raise ValueError("grads must have one tensor for each param")
         written = self._written()
@@ -365,8 +388,7 @@ class AdamW:
         records = (_AdamwTensor * n)(*[
             _AdamwTensor(p.data_ptr(), None if c is None else c.data_ptr(), g.data_ptr(), p.numel(), s, w,
                          _dtype_code(g, "gradients"), 0)
-            for p, c, g, s, w in zip(self.params, self.copies, grads, self.lr_scale,
-                                     self.weight_decay)])
+            for p, c, g, s, w in zip(self.params, self.copies, grads, lr_scale, weight_decay)])
         elements = int(lib.lp_adamw_state_elements(records, n))
         size = int(lib.lp_adamw_plan_size(records, n))
         host = torch.empty(max(size, 1), dtype=torch.uint8)
@@ -376,6 +398,7 @@ class AdamW:
         plan = host.to(self.params[0].device)
         home = torch.cuda.current_stream(plan.device).cuda_stream if plan.is_cuda else 0
         self.grads, self.state_elements, self._plan, self._home = grads, elements, plan, home
+        self._weight_decay, self._lr_scale = weight_decay, lr_scale
         self._given = (tuple(self.params + [c for c in self.copies if c is not None]), tuple(grads))
 
     def _allocate(self, state: Optional[dict]) -> None:

@@ -1,6 +1,8 @@
 """train.AdamW on the host: what it keeps, refuses and lays out.  The plan is host work; with the
 check of the device taken out these tests run on CPU tensors, and no step is taken."""
 
+import struct
+
 import pytest
 import torch
 
@@ -85,3 +87,23 @@ def test_a_state_brings_its_seed(on_cpu):
     assert train.AdamW([p], [g], state_bits=8, state=state).seed == 0
     assert train.AdamW([p], [g], state_bits=8).seed == 0
     assert train.AdamW([p], [g], state_bits=8, seed=-1).seed == 2 ** 64 - 1
+
+
+def test_factors_hold_when_they_are_assigned(on_cpu):
+    """The factors of each tensor are part of the plan: assigning them lays it out again."""
+    def planned(opt):  # (lr_scale, weight_decay) of each record of 56 bytes
+        return [struct.unpack_from("ff", bytes(opt._plan.tolist()), 56 * i + 40) for i in range(2)]
+    params, grads = [torch.zeros(300), torch.zeros(9)], [torch.zeros(300), torch.zeros(9)]
+    opt = train.AdamW(params, grads, weight_decay=0.5)
+    assert planned(opt) == [(1.0, 0.5)] * 2 and opt.weight_decay == (0.5, 0.5)
+    opt.weight_decay = [0.25, 0]
+    opt.lr_scale = 2
+    assert planned(opt) == [(2.0, 0.25), (2.0, 0.0)] and opt.lr_scale == (2.0, 2.0)
+    for name, bad in (("weight_decay", [0.1]), ("weight_decay", -1.0), ("lr_scale", float("nan"))):
+        with pytest.raises((ValueError, train.LpError)):
+            setattr(opt, name, bad)
+    assert planned(opt) == [(2.0, 0.25), (2.0, 0.0)] and opt.weight_decay == (0.25, 0.0)
+    with pytest.raises(TypeError):
+        opt.weight_decay[0] = 0.5  # would change nothing
+    opt.set_grads([torch.ones(300), grads[1]])
+    assert planned(opt) == [(2.0, 0.25), (2.0, 0.0)]
