@@ -229,7 +229,11 @@ __global__ void __launch_bounds__(kSmallThreads) lp_policy_small_kernel(const __
       int s = t < a.T ? int(upper_bound(offsets + 1, B, t)) : B;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        while (s < B && offsets[s + 1] <= t + j) ++s;
+        // the next sequence is mostly the next row's; past empty ones it is searched for
+        if ((kept[k] >> j & 1u) && s < B && offsets[s + 1] <= t + j) {
+          ++s;
+          s += int(upper_bound(offsets + 1 + s, B - s, t + j));
+        }
         sequence[k][j] = s;
         if (s == B || t + j < offsets[0]) kept[k] &= ~(1u << j);
         if (a.by_sequence && kept[k] >> j & 1u) mine += atomicAdd(&counts[s], 1u) == 0 ? 1u : 0u;
@@ -372,6 +376,10 @@ __global__ void __launch_bounds__(kThreads)
         mine += atomicAdd(&counts[span.first + i], n) == 0 ? 1u : 0u;
       }
       ++i;
+      if (left != 0 && i < span.sequences) {  // past empty sequences the next row's is searched for
+        const int row = r + __ffs(left) - 1;
+        if (local_end(a, span, ends, t0, i) <= row) i = local_sequence(a, span, ends, t0, row, i + 1);
+      }
     }
   }
   if (a.by_sequence) {
@@ -441,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         int s = i;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          while (s < span.sequences && local_end(a, span, ends, t0, s) <= r + j) ++s;
+          if ((kept >> j & 1u) && s < span.sequences && local_end(a, span, ends, t0, s) <= r + j)
+            s = local_sequence(a, span, ends, t0, r + j, s + 1);
           if (s == span.sequences || r + j < span.begin) {
             kept &= ~(1u << j);
           } else {

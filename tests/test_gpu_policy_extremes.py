@@ -1,0 +1,65 @@
+"""The policy loss at the ends of its range: sequences by the thousand million, differences whose
+exponentials pass float32, coefficients of zero."""
+
+import numpy as np
+import pytest
+import torch
+
+from invariant_token_logprobs_gb300 import train
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def milliseconds(call):
+    """The fastest of three, on the GPU."""
+    call()
+    times = []
+    for _ in range(3):
+        start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        call()
+        stop.record()
+        stop.synchronize()
+        times.append(start.elapsed_time(stop))
+    return min(times)
+
+
+@pytest.mark.parametrize("T,first,empty", [(9002, 4502, 300_000), (2_000_002, 4502, 300_000),
+                                           (9002, 0, 300_000), (8002, 4001, 1900)])
+@pytest.mark.parametrize("reduction", ["sequence", "token"])
+def test_empty_sequences_are_passed_at_once(T, first, empty, reduction):
+    """Two sequences on either side of many empty ones have the weights of the two alone, and the
+    call takes no time for the others (walked one by one, 300 000 took 60 ms; they may take 2)."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    logp = -torch.rand(T, generator=g, device=DEV)
+    old = logp + 0.1 * torch.randn(T, generator=g, device=DEV)
+    A = torch.randn(T, generator=g, device=DEV)
+    mask = torch.rand(T, generator=g, device=DEV) < 0.5
+    mask[first - 4:first + 4] = True
+    cu = torch.full((empty + 3,), first, dtype=torch.int64, device=DEV)
+    cu[0], cu[-1] = 0, T
+    small = torch.tensor([0, first, T], device=DEV)
+    run = lambda c: train.policy_loss(logp, old, A, mask=mask, cu_seqlens=c, reduction=reduction,  # noqa: E731
+                                      per_sequence=False)
+    for a, b in zip(run(cu), run(small)):
+        assert (a is None and b is None) or torch.equal(a, b)
+    advantages = torch.zeros(empty + 2, device=DEV)
+    advantages[0], advantages[-1] = 1.5, -0.5
+    with_each = lambda c, v: train.policy_loss(logp, old, v, mask=mask, cu_seqlens=c, reduction=reduction,  # noqa: E731
+                                               per_sequence=True)
+    for a, b in zip(with_each(cu, advantages), with_each(small, advantages[[0, -1]])):
+        assert (a is None and b is None) or torch.equal(a, b)
+    assert milliseconds(lambda: with_each(cu, advantages)) < 2.0
+
+
+def test_offsets_padded_to_a_capacity():
+    """Offsets that repeat the last one, as for a fixed capacity of sequences."""
+    T = 61
+    logp = -torch.rand(T, device=DEV)
+    cu = torch.tensor([0, 20, 61], device=DEV)
+    padded = torch.cat([cu, torch.full((2000,), T, device=DEV)])
+    for reduction in ("sequence", "token"):
+        run = lambda c: train.policy_loss(logp, logp * 1.1, -logp, cu_seqlens=c, reduction=reduction)  # noqa: E731
+        for a, b in zip(run(padded), run(cu)):
+            assert (a is None and b is None) or torch.equal(a, b)
