@@ -298,7 +298,7 @@ __device__ __forceinline__ int local_sequence(const PolicyArgs& a, const Span& s
                                               int64_t t0, int r, int lo) {
   int hi = span.sequences;
   while (lo < hi) {
-    const int mid = (lo + hi) / 2;
+    const int mid = lo + (hi - lo) / 2;  // lo + hi may pass 32 bits
     const int end = span.staged ? ends[mid] : from_chunk(a.cu_seqlens[span.first + 1 + mid], t0);
     if (end <= r)
       lo = mid + 1;

@@ -63,3 +63,24 @@ def test_offsets_padded_to_a_capacity():
         run = lambda c: train.policy_loss(logp, logp * 1.1, -logp, cu_seqlens=c, reduction=reduction)  # noqa: E731
         for a, b in zip(run(padded), run(cu)):
             assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_more_than_2_to_30_sequences_in_a_chunk():
+    """The search for a row's sequence among n has sums of up to 2 n.  Two sequences lie on either
+    side of 1.2e9 empty ones: the weights are those of the two alone."""
+    empty, first, T = 1_200_000_000, 4502, 9002
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 24 GB")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    logp = -torch.rand(T, generator=g, device=DEV)
+    old = logp + 0.1 * torch.randn(T, generator=g, device=DEV)
+    A = torch.randn(T, generator=g, device=DEV)
+    cu = torch.full((empty + 3,), first, dtype=torch.int64, device=DEV)
+    cu[0], cu[-1] = 0, T
+    small = torch.tensor([0, first, T], device=DEV)
+    for reduction in ("sequence", "token"):
+        got = train.policy_loss(logp, old, A, cu_seqlens=cu, reduction=reduction)
+        ref = train.policy_loss(logp, old, A, cu_seqlens=small, reduction=reduction)
+        for a, b in zip(got, ref):
+            assert (a is None and b is None) or torch.equal(a, b)
