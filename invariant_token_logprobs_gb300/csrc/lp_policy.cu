@@ -148,7 +148,7 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int6
     const bool counts = kept >> j & 1u;
     const float weight = counts ? w[j] : 0.f, A = counts ? f.advantage[j] : 0.f;
     const float delta = counts ? f.logp[j] - f.old[j] : 0.f;
-    const float ratio = __expf(delta);  // within 2 + |1.2 delta| units in the last place
+    const float ratio = expf(delta);
     const bool over = A > 0.f && delta > a.high, under = A < 0.f && delta < a.low;
     const bool clipped = over || under;
     float g = clipped ? 0.f : -A * ratio;

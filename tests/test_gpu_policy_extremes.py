@@ -84,3 +84,19 @@ def test_more_than_2_to_30_sequences_in_a_chunk():
         ref = train.policy_loss(logp, old, A, cu_seqlens=small, reduction=reduction)
         for a, b in zip(got, ref):
             assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_exponentials_are_good_to_the_last_places():
+    """The gradient of a row with advantage -1 is its weight, a power of two here, times the ratio:
+    the float32 exponential of an exact difference, whose error CUDA gives as at most 1 unit in the
+    last place; 2 are asked.  An exponential by way of a rounded exponent is 14 off at 10."""
+    n = 8192
+    delta = torch.linspace(-13, 85, n, dtype=torch.float64).float()
+    zero = torch.zeros(n, device=DEV)
+    got = train.policy_loss(delta.to(DEV), zero, zero - 1, clip_low=1 - 1e-6).grad_logp
+    want = np.exp(delta.double().numpy())
+    assert np.all(np.abs(got.double().cpu().numpy() * n - want) <= 2 * 2.0 ** -23 * want)
+    # and that of the divergence's, with no advantage: minus its coefficient times expm1
+    got = train.policy_loss(zero, zero, zero, ref_logp=delta.to(DEV), kl_coef=1.0).grad_logp
+    want = -np.expm1(delta.double().numpy())
+    assert np.all(np.abs(got.double().cpu().numpy() * n - want) <= 2 * 2.0 ** -23 * np.abs(want))
