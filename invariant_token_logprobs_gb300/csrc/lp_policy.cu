@@ -149,10 +149,12 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int6
     const float weight = counts ? w[j] : 0.f, A = counts ? f.advantage[j] : 0.f;
     const float delta = counts ? f.logp[j] - f.old[j] : 0.f;
     const float ratio = expf(delta);
+    // a finite difference whose exponential passes float32 gains nothing where there is no advantage
+    const float gain = A != 0.f || !(fabsf(delta) <= 0x1.fffffep127f) ? A * ratio : 0.f;
     const bool over = A > 0.f && delta > a.high, under = A < 0.f && delta < a.low;
     const bool clipped = over || under;
-    float g = clipped ? 0.f : -A * ratio;
-    sum[0] += weight * (-A * (over ? a.ratio_high : under ? a.ratio_low : ratio));
+    float g = clipped ? 0.f : -gain;
+    sum[0] -= weight * (over ? A * a.ratio_high : under ? A * a.ratio_low : gain);
     if (a.ref_logp != nullptr) {
       const float r = counts ? f.ref[j] - f.logp[j] : 0.f, up = expm1f(r);
       sum[1] += weight * (up - r);

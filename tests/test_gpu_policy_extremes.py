@@ -100,3 +100,23 @@ def test_exponentials_are_good_to_the_last_places():
     got = train.policy_loss(zero, zero, zero, ref_logp=delta.to(DEV), kl_coef=1.0).grad_logp
     want = -np.expm1(delta.double().numpy())
     assert np.all(np.abs(got.double().cpu().numpy() * n - want) <= 2 * 2.0 ** -23 * np.abs(want))
+
+
+@pytest.mark.parametrize("T", [4, 20000])
+def test_a_row_without_advantage_adds_nothing(T):
+    """exp(delta) passes float32 from 88.7 on; the product with an advantage of 0 is 0 in the
+    definition, not NaN.  (T: one launch, two passes.)"""
+    delta, A = torch.full((T,), 0.1, device=DEV), torch.ones(T, device=DEV)
+    delta[1], A[1] = 100.0, 0.0
+    delta[2], A[2] = 100.0, 2.0    # clipped: the value is that of the limit
+    delta[3], A[3] = -100.0, -2.0  # clipped on the other side
+    zero = torch.zeros(T, device=DEV)
+    got = train.policy_loss(delta, zero, A)
+    assert torch.isfinite(got.grad_logp).all() and not got.grad_logp[1:4].any()
+    want = -((T - 3) * np.exp(np.float64(np.float32(0.1))) + 2 * 1.2 - 2 * 0.8) / T
+    assert abs(float(got.stats[0]) - want) <= 4200 * 2.0 ** -24 * abs(want)
+    # an infinite difference is one, and an advantage that is not zero loses that much
+    delta[1] = float("inf")
+    assert torch.isnan(train.policy_loss(delta, zero, A).grad_logp[1])
+    delta[1], A[1] = 100.0, -1e3
+    assert float(train.policy_loss(delta, zero, A).grad_logp[1]) == float("inf")
