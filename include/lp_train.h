@@ -142,6 +142,7 @@ LP_API size_t lp_policy_loss_workspace_size(int64_t T, int64_t n_sequences);
  *   logp, old_logp  [T] float32.
  *   ref_logp        [T] float32, or NULL (no kl term; kl_coef is not used).
  *   entropy         [T] float32, or NULL (no entropy term).
+ *   kl_coef, entropy_coef  finite; with 0 the term is in the stats alone, whatever it holds.
  *   advantages      [T] float32, or [n_sequences] when advantages_per_sequence != 0.
  *   mask            [T] bytes (0: the row does not count), or NULL (all count).
  *   cu_seqlens      [n_sequences + 1] int64 ascending row offsets: sequence i is the

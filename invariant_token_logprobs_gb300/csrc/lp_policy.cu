@@ -158,7 +158,7 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int6
     if (a.ref_logp != nullptr) {
       const float r = counts ? f.ref[j] - f.logp[j] : 0.f, up = expm1f(r);
       sum[1] += weight * (up - r);
-      g -= a.kl_coef * up;
+      if (a.kl_coef != 0.f) g -= a.kl_coef * up;
     }
     if (a.entropy != nullptr) sum[2] += weight * (counts ? f.entropy[j] : 0.f);
     sum[3] += clipped ? weight : 0.f;
@@ -187,7 +187,9 @@ __device__ __forceinline__ void cta_sum(float (&sum)[kStats], float (*slots)[kSt
 }
 
 __device__ __forceinline__ void write_stats(const PolicyArgs& a, const float (&sum)[kStats]) {
-  a.stats[0] = sum[0] + a.kl_coef * sum[1] - a.entropy_coef * sum[2];
+  // a term with a coefficient of 0 is watched only: what it sums to may be no float32 number
+  a.stats[0] = sum[0] + (a.kl_coef != 0.f ? a.kl_coef * sum[1] : 0.f) -
+               (a.entropy_coef != 0.f ? a.entropy_coef * sum[2] : 0.f);
 #pragma unroll
   for (int k = 0; k < kStats; ++k) a.stats[k + 1] = sum[k];
 }

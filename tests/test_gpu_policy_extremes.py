@@ -120,3 +120,19 @@ def test_a_row_without_advantage_adds_nothing(T):
     assert torch.isnan(train.policy_loss(delta, zero, A).grad_logp[1])
     delta[1], A[1] = 100.0, -1e3
     assert float(train.policy_loss(delta, zero, A).grad_logp[1]) == float("inf")
+
+
+@pytest.mark.parametrize("T", [4, 20000])
+def test_terms_with_a_coefficient_of_zero_are_only_watched(T):
+    """An estimate of the divergence that passes float32, or an entropy that is none, shows in its
+    statistic and nowhere else."""
+    logp = torch.full((T,), -0.5, device=DEV)
+    logp[1] = -100.0
+    entropy = torch.ones(T, device=DEV)
+    entropy[2] = float("nan")
+    A = torch.ones(T, device=DEV)
+    ref = train.policy_loss(logp, logp, A)
+    got = train.policy_loss(logp, logp, A, ref_logp=torch.zeros(T, device=DEV), entropy=entropy)
+    assert float(got.stats[2]) == float("inf") and torch.isnan(got.stats[3])
+    assert torch.equal(got.stats[:2], ref.stats[:2]) and torch.equal(got.grad_logp, ref.grad_logp)
+    assert not got.grad_entropy.any()
