@@ -109,6 +109,11 @@ void vector(const at::Tensor* t, int64_t n, const char* what, at::ScalarType s =
   if (t->dim() != 1 || t->size(0) != n || !t->is_contiguous())
     value_error(std::string(what) + " must be a contiguous vector of " + std::to_string(n));
 }
+// The bytes of a workspace that the caller gives: all that its elements span, each once.
+size_t workspace_bytes(const at::Tensor& t) {
+  if (!t.is_contiguous()) value_error("workspace must be contiguous");
+  return t.nbytes();
+}
 // Row stride of a 2-D operand; a single row may have any.
 int64_t row_stride(const at::Tensor* t, int64_t T, int64_t d, const char* what) {
   if (t == nullptr) return 0;
@@ -368,7 +373,7 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
       if (branch_weight != nullptr) made.add(&grad_branch_weight, {o.d}, at::kFloat);
       if (given != nullptr) {
         workspace = *given;
-        bytes = given->nbytes();
+        bytes = workspace_bytes(*given);
       } else {
         bytes = lp.norm_workspace(o.T, o.d);
         made.scratch(&workspace, bytes);
@@ -430,7 +435,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
     size_t bytes;
     if (given != nullptr) {
       workspace = *given;
-      bytes = given->nbytes();
+      bytes = workspace_bytes(*given);
     } else {
       bytes = lp.policy_workspace(T, sequences);
       made.scratch(&workspace, bytes);

@@ -206,3 +206,29 @@ def test_results_can_be_saved(T, tmp_path):
         held = sum({t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in results}.values())
         whole = sum(t.numel() * t.element_size() for t in results)
         assert held <= whole + 256 * (len(results) + 1)  # each rounded up, and next to no scratch
+
+
+def test_a_workspace_spans_what_it_says():
+    """An expanded tensor has more elements than memory; it is refused, not written past."""
+    T, d = 2000, 256
+    r = torch.randn(T, d, device=DEV)
+    w = torch.ones(d, device=DEV)
+    rstd = torch.ones(T, device=DEV)
+    size = train.residual_norm_backward_workspace_size(T, d)
+    ref = train.residual_norm_backward(r, None, r, rstd, weight=w)
+    got = train.residual_norm_backward(r, None, r, rstd, weight=w,
+                                       workspace=torch.empty(size, dtype=torch.uint8, device=DEV))
+    assert torch.equal(got.weight, ref.weight)
+    logp = torch.rand(20000, device=DEV)
+    need = train.policy_loss_workspace_size(20000, 0)
+    loss = train.policy_loss(logp, logp, logp, workspace=torch.empty(need // 4 + 1, device=DEV))
+    assert torch.equal(loss.stats, train.policy_loss(logp, logp, logp).stats)
+    one = torch.empty(256, dtype=torch.uint8, device=DEV)
+    for bad in (one[:1].expand(size), one.expand(size // 256 + 1, 256),
+                torch.empty(2 * size, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            train.residual_norm_backward(r, None, r, rstd, weight=w, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            train.policy_loss(logp, logp, logp, workspace=bad)
+    with pytest.raises(train.LpError, match="WORKSPACE"):
+        train.policy_loss(logp, logp, logp, workspace=one)
