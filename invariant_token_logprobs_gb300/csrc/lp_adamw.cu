@@ -293,6 +293,11 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps)
   float* stretch = stretches[warp];
   const int64_t first = (row - rec.first_row) * kRow;  // of the row in the tensor
   const int left = int(min(rec.n - first, int64_t(kRow)));
+  // every access below is of the row's first `left` elements, or of its kRow in the moments
+  if (!LP_CHECK(left > 0 && first >= 0 && first + left <= rec.n && rec.first_row >= 0 &&
+                    rec.first_row + (rec.n + kRow - 1) / kRow <= a.rows,
+                kChkPlan))
+    return;
   const bool is_wide = rec.wide != 0;
   float* const params = rec.param + first;
   __nv_bfloat16* const copies = rec.copy != nullptr ? rec.copy + first : nullptr;
@@ -502,6 +507,7 @@ __global__ void __launch_bounds__(kNormThreads)
   const int64_t quads = rows / 4;
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < quads; i += kNormThreads) {
+    if (!LP_CHECK(4 * i + 4 <= rows, kChkStateIndex)) break;
     const float4 x = __ldcg(reinterpret_cast<const float4*>(sums) + i);
     s.add(x.x), s.add(x.y), s.add(x.z), s.add(x.w);
   }
@@ -532,6 +538,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int k = 0; k < kRow / 4 / kThreads; ++k) {
     const int64_t i = int64_t(blockIdx.x) * (kRow / 4) + k * kThreads + threadIdx.x;
+    if (!LP_CHECK(i >= 0 && i < int64_t(gridDim.x) * (kRow / 4), kChkStateIndex)) return;
     const uint32_t cm = __ldg(m + i), cu = __ldg(u + i);
     const float sm = __ldg(m_scale + i / (kBlock / 4)), su = __ldg(u_scale + i / (kBlock / 4));
     float a[4], b[4];

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   constexpr int kRows = kRowsATurn<G>;
   __shared__ __align__(16) float slots[2][2][kMaxWarps][padded(kRows)];
   extern __shared__ __align__(32) unsigned char ring[];
-  const Place p(a.d, plan.shape);
+  const Place p(a.T, a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
   const bool branch = a.branch.p != nullptr, gate = a.gate.p != nullptr, norm = a.weight != nullptr;
   const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         root_y[j] = 1.f / sqrtf(__fmaf_rn(root_y[j], inv_d, a.eps));
-        if (a.branch_rstd != nullptr && p.i == 0 && t + j * step < a.T)
+        if (a.branch_rstd != nullptr && p.i == 0 && t + j * step < a.T &&
+            LP_CHECK(p.has(t + j * step), kChkRowIndex))
           a.branch_rstd[t + j * step] = root_y[j];
       }
     }
@@ -145,7 +146,9 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       root[j] = 1.f / sqrtf(__fmaf_rn(root[j], inv_d, a.eps));
-      if (a.rstd != nullptr && p.i == 0 && t + j * step < a.T) a.rstd[t + j * step] = root[j];
+      if (a.rstd != nullptr && p.i == 0 && t + j * step < a.T &&
+          LP_CHECK(p.has(t + j * step), kChkRowIndex))
+        a.rstd[t + j * step] = root[j];
     }
 #pragma unroll
     for (int k = 0; k < G; ++k) {

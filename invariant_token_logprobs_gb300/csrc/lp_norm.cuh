@@ -138,15 +138,17 @@ struct Plan {
   int stage_bytes;
 };
 
-// A thread's place in its CTA.
+// A thread's place in its CTA, and the call's rows.
 struct Place {
+  int64_t rows;
   int d;           // the row's columns
   int i, team;     // which thread of its team
   int lane, warp;
   int in_cta;      // which team of the CTA
   int first_warp;  // of the team
-  __device__ __forceinline__ Place(int64_t columns, const Shape& s)
-      : d(int(columns)),
+  __device__ __forceinline__ Place(int64_t rows, int64_t columns, const Shape& s)
+      : rows(rows),
+        d(int(columns)),
         i(int(threadIdx.x)),
         team(s.team),
         lane(int(threadIdx.x & 31)),
@@ -158,6 +160,11 @@ struct Place {
       i -= in_cta * s.team;
       first_warp = in_cta * (s.team / 32);
     }
+  }
+  // What the checked build tests: that the operands have row t, and in it `n` columns from `from` on.
+  __device__ __forceinline__ bool has(int64_t t) const { return t >= 0 && t < rows; }
+  __device__ __forceinline__ bool has(int64_t t, int from, int n) const {
+    return has(t) && from >= 0 && from + n <= d;
   }
 };
 
@@ -206,7 +213,7 @@ struct Stream {
       const int c = 8 * (p.i + k * p.team);
       if (kAlign == kAligned) {
         const T* from = row_at<const T, kAligned>(r, t, c);
-        if (c < p.d)
+        if (c < p.d && LP_CHECK(p.has(t, c, 8), kChkCopyIndex))
 #pragma unroll
           for (int q = 0; q < int(sizeof(T)) / 2; ++q)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * q),
@@ -222,6 +229,7 @@ struct Stream {
         for (int q = 0; q < int(sizeof(T)) / 2; ++q) {
           constexpr int kOf16 = 16 / int(sizeof(T));
           const int bytes = min(max((p.d - c - q * kOf16) * int(sizeof(T)), 0), 16);
+          if (!LP_CHECK(bytes == 0 || p.has(t, c + q * kOf16, bytes / int(sizeof(T))), kChkCopyIndex)) continue;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * q),
                        "l"(bytes ? row + c + q * kOf16 : none), "r"(bytes)
                        : "memory");
@@ -237,7 +245,10 @@ struct Stream {
         T v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          v[q] = whole || first_column + 32 * q + p.lane < p.d ? from[32 * q] : T(0.f);
+          v[q] = (whole || first_column + 32 * q + p.lane < p.d) &&
+                         LP_CHECK(p.has(t, first_column + 32 * q + p.lane, 1), kChkCopyIndex)
+                     ? from[32 * q]
+                     : T(0.f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) to_first[32 * q] = v[q];
         continue;
@@ -246,27 +257,36 @@ struct Stream {
       const int shift = kMayShift && mid_word(r, t) ? 1 : 0;
       const uint32_t stretch = to - 8 * p.lane * uint32_t(sizeof(T)) + 4 * p.lane;
       const T* from = row + first_column + p.lane * kOf4 - shift;
+      const T* begin = static_cast<const T*>(r.p);
+      // whether word q's elements, the first `n` of them, are the row's; a shifted row's first word
+      // begins with the element in front of it, which is the operand's unless the row is its first
+      const auto inside = [&](int q, int n) {
+        const int first = first_column + (32 * q + p.lane) * kOf4 - shift;
+        const int front = first < 0 && from + 32 * q * kOf4 >= begin ? 1 : 0;
+        return p.has(t, first + front, n - front);
+      };
       const auto copy = [&](int q) {
         const int left = p.d - first_column + shift - (32 * q + p.lane) * kOf4;
         const uint32_t bytes = left >= kOf4 ? 4u : left > 0 ? uint32_t(sizeof(T)) : 0u;
+        if (!LP_CHECK(bytes == 0u || inside(q, int(bytes / sizeof(T))), kChkCopyIndex)) return;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(stretch + 128 * q),
                      "l"(bytes ? from + 32 * q * kOf4 : none), "r"(bytes)
                      : "memory");
       };
-      const T* begin = static_cast<const T*>(r.p);
       const bool before = kMayShift && from < begin;  // nothing before the operand is read
       if (kMayShift && shift != 0 && p.lane == 0) copy(2 * int(sizeof(T)));  // the word more
       if (whole && !before) {
 #pragma unroll
         for (int q = 0; q < 2 * int(sizeof(T)); ++q)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stretch + 128 * q),
-                       "l"(from + 32 * q * kOf4)
-                       : "memory");
+          if (LP_CHECK(inside(q, kOf4), kChkCopyIndex))
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stretch + 128 * q),
+                         "l"(from + 32 * q * kOf4)
+                         : "memory");
         continue;
       }
       if (before) {
         shared_pointer(stretch)[0] = T(0.f);
-        shared_pointer(stretch)[1] = *begin;
+        if (LP_CHECK(p.has(t, 0, 1), kChkCopyIndex)) shared_pointer(stretch)[1] = *begin;
       } else {
         copy(0);
       }
@@ -347,11 +367,12 @@ __device__ __forceinline__ void put(const Rows& r, int64_t t, int k, bool mine, 
   const int c = 8 * (p.i + k * p.team);
   if (kAlign == kAligned) {
     T* to = row_at<T, kAligned>(r, t, c);
-    if (c < p.d) store_group(to, g);
+    if (c < p.d && LP_CHECK(p.has(t, c, 8), kChkRowIndex)) store_group(to, g);
     return;
   }
   T* row = row_at<T, kAlign>(r, t, 0);
   if (access == kWide) {
+    if (!LP_CHECK(p.has(t), kChkRowIndex)) return;
     if (c + 8 <= p.d) return store_group(row + c, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -367,6 +388,7 @@ __device__ __forceinline__ void put(const Rows& r, int64_t t, int k, bool mine, 
   // a group over the warp instead cost 2 us of the forward's 33 for 4864 x 2397)
   T* to = row + first + p.lane;
   const T* from = s + p.lane;
+  if (!LP_CHECK(p.has(t) && first >= 0, kChkRowIndex)) return;
   if (first + 256 > p.d) {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -387,6 +409,7 @@ __device__ __forceinline__ void put(const Rows& r, int64_t t, int k, bool mine, 
 __device__ __forceinline__ void read_weight(const void* w, bool bf16, int k, bool wide,
                                             const Place& p, Pairs& v) {
   const int index = p.i + k * p.team, c = 8 * index;
+  if (!LP_CHECK(index >= 0, kChkCopyIndex)) return;
   if (wide && c + 8 <= p.d) {
     if (bf16) {
       const uint4 x = __ldg(static_cast<const uint4*>(w) + index);

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kMaxTeam)
   constexpr int kSums = kPost ? 3 : 1;
   __shared__ __align__(16) float slots[2][kMaxWarps][padded(kRows * kSums)];
   extern __shared__ __align__(32) unsigned char ring[];
-  const Place p(a.d, plan.shape);
+  const Place p(a.T, a.d, plan.shape);
   const float inv_d = 1.f / static_cast<float>(a.d);
   const bool norm = a.weight != nullptr, branch = a.branch.p != nullptr, gate = a.gate.p != nullptr;
   const bool has_dr = a.grad_residual_out.p != nullptr;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kMaxTeam)
   const auto load_roots = [&](int64_t first) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const bool mine = first + j * step < a.T;
+      const bool mine = first + j * step < a.T && LP_CHECK(p.has(first + j * step), kChkRowIndex);
       root[j] = norm && mine ? a.rstd[first + j * step] : 0.f;
       root_y[j] = kPost && mine ? a.branch_rstd[first + j * step] : 1.f;
     }
@@ -286,12 +286,14 @@ __global__ void __launch_bounds__(kMaxTeam)
       for (int k = 0; k < G; ++k) {
         const int c = 8 * (p.i + k * p.team);
         if (gridDim.x > 1) {
-          if (c < p.d) store_group(part + q * pitch_of(a.d) + c, pack(sum[k], float()));
+          if (c < p.d && LP_CHECK(c >= 0 && c + 8 <= pitch_of(a.d), kChkSplitIndex))
+            store_group(part + q * pitch_of(a.d) + c, pack(sum[k], float()));
           continue;
         }
         float* out = q == 0   ? a.grad_weight
                      : q == 1 ? a.grad_branch_weight
                               : static_cast<float*>(a.grad_gate.p);
+        if (!LP_CHECK(c >= 0, kChkCopyIndex)) continue;
         if (c + 8 <= p.d && reinterpret_cast<uintptr_t>(out) % 32 == 0) {
           store_group(out + c, pack(sum[k], float()));
           continue;
@@ -353,6 +355,11 @@ __global__ void __launch_bounds__(kWideThreads)
     sums[c] = sums[d + c] = sums[2 * d + c] = 0.f;
   int turn = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    // every operand's row has d columns (a one-row gate's pitch is 0)
+    if (!LP_CHECK(t >= 0 && d <= kNormMaxDim && d <= a.grad_residual.ld && (!norm || d <= a.residual_out.ld) &&
+                      (a.branch.p == nullptr || (d <= a.branch.ld && d <= a.grad_branch.ld)),
+                  kChkRowIndex))
+      break;
     const R* s = norm ? row_of<const R>(a.residual_out, t) : nullptr;
     const A* y = a.branch.p ? row_of<const A>(a.branch, t) : nullptr;
     const A* g = a.gate.p ? row_of<const A>(a.gate, t) : nullptr;
@@ -406,7 +413,8 @@ __global__ void __launch_bounds__(kWideThreads)
   float* part = a.partials + int64_t(blockIdx.x) * 3 * pitch_of(d);
   for (int64_t c = threadIdx.x; c < d; c += kWideThreads)
 #pragma unroll
-    for (int q = 0; q < 3; ++q) part[q * pitch_of(d) + c] = sums[q * d + c];
+    for (int q = 0; q < 3; ++q)
+      if (LP_CHECK(c < pitch_of(d), kChkSplitIndex)) part[q * pitch_of(d) + c] = sums[q * d + c];
 }
 
 // The CTAs' partial sums: 16 threads a column take every sixteenth part in order, and their
@@ -426,7 +434,8 @@ __global__ void __launch_bounds__(32 * kSumLanes)
   if (c < d) {
     const float* p = partials + (int64_t(from) * 3 + blockIdx.y) * pitch + c;
 #pragma unroll 4
-    for (int64_t k = from; k < parts; k += kSumLanes, p += 3 * kSumLanes * pitch) s += __ldcg(p);
+    for (int64_t k = from; k < parts; k += kSumLanes, p += 3 * kSumLanes * pitch)
+      if (LP_CHECK(p >= partials && p < partials + parts * 3 * pitch, kChkSplitIndex)) s += __ldcg(p);
   }
   slots[from][lane] = s;
   __syncthreads();

@@ -129,6 +129,7 @@ struct Four {
   float logp[4], old[4], ref[4], entropy[4], advantage[4];
 };
 __device__ __forceinline__ void load_rows(const PolicyArgs& a, int64_t t, int64_t T, Four& f) {
+  if (!LP_CHECK(t >= 0 && T <= a.T, kChkRowIndex)) return;
   load4(a.logp, t, T, a.wide, f.logp);
   load4(a.old_logp, t, T, a.wide, f.old);
   if (a.ref_logp != nullptr) load4(a.ref_logp, t, T, a.wide, f.ref);
@@ -165,6 +166,7 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int6
     grad[j] = counts ? weight * g : 0.f;
     grad_entropy[j] = counts ? -a.entropy_coef * weight : 0.f;
   }
+  if (!LP_CHECK(t >= 0 && T <= a.T, kChkRowIndex)) return;
   store4(a.grad_logp, t, T, a.wide, grad);
   if (a.grad_entropy != nullptr) store4(a.grad_entropy, t, T, a.wide, grad_entropy);
 }
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kSmallThreads) lp_policy_small_kernel(const __
   if (threadIdx.x == 0) whole = 0;
   if (sequences)
     for (int i = threadIdx.x; i <= B; i += threads) {
+      if (!LP_CHECK(i <= a.n_sequences && i <= kSmallSequences, kChkRowIndex)) continue;
       const int64_t c = a.cu_seqlens[i];
       offsets[i] = int(min(max(c, int64_t(0)), a.T));
       if (i < B) counts[i] = 0;
@@ -257,7 +260,8 @@ __global__ void __launch_bounds__(kSmallThreads) lp_policy_small_kernel(const __
     for (int j = 0; j < 4; ++j) {
       if (!(kept[k] >> j & 1u)) continue;
       w[j] = weight_of(a.by_sequence, a.by_sequence ? counts[sequence[k][j]] : 0u, whole);
-      if (a.per_sequence) rows[k].advantage[j] = a.advantages[sequence[k][j]];
+      if (a.per_sequence && LP_CHECK(sequence[k][j] >= 0 && sequence[k][j] < B, kChkRowIndex))
+        rows[k].advantage[j] = a.advantages[sequence[k][j]];
     }
     finish_rows(a, t, a.T, rows[k], kept[k], w, sum);
   }
@@ -272,6 +276,10 @@ struct Span {
   int begin;      // where the first sequence of all begins
   bool staged;    // their ends are in shared memory
 };
+// Whether sequence i of the span is one of the call's.
+__device__ __forceinline__ bool in_call(const PolicyArgs& a, const Span& span, int64_t i) {
+  return i >= 0 && span.first >= 0 && span.first + i < a.n_sequences;
+}
 __device__ __forceinline__ int from_chunk(int64_t offset, int64_t t0) {
   return int(min(max(offset - t0, int64_t(0)), int64_t(1) << 30));
 }
@@ -291,10 +299,17 @@ __device__ __forceinline__ Span find_span(const PolicyArgs& a, int64_t t0, int64
   span.sequences = int(min(sequences, a.n_sequences));
   if (span.staged) {
     for (int i = threadIdx.x; i < span.sequences; i += kThreads)
-      ends[i] = from_chunk(a.cu_seqlens[span.first + 1 + i], t0);
+      if (LP_CHECK(in_call(a, span, i), kChkRowIndex)) ends[i] = from_chunk(a.cu_seqlens[span.first + 1 + i], t0);
     __syncthreads();
   }
   return span;
+}
+// Where the span's sequence i ends.
+__device__ __forceinline__ int local_end(const PolicyArgs& a, const Span& span, const int* ends,
+                                         int64_t t0, int i) {
+  if (span.staged) return ends[i];
+  if (!LP_CHECK(in_call(a, span, i), kChkRowIndex)) return 0;
+  return from_chunk(a.cu_seqlens[span.first + 1 + i], t0);
 }
 // Which of the span's sequences the chunk's row `r` lies in; span.sequences: in none.
 // It is `lo` or a later one.
@@ -303,17 +318,12 @@ __device__ __forceinline__ int local_sequence(const PolicyArgs& a, const Span& s
   int hi = span.sequences;
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;  // lo + hi may pass 32 bits
-    const int end = span.staged ? ends[mid] : from_chunk(a.cu_seqlens[span.first + 1 + mid], t0);
-    if (end <= r)
+    if (local_end(a, span, ends, t0, mid) <= r)
       lo = mid + 1;
     else
       hi = mid;
   }
   return lo;
-}
-__device__ __forceinline__ int local_end(const PolicyArgs& a, const Span& span, const int* ends,
-                                         int64_t t0, int i) {
-  return span.staged ? ends[i] : from_chunk(a.cu_seqlens[span.first + 1 + i], t0);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(kThreads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (i == 0) header->counted = header->sequences = header->finished = 0;
-  if (i < n) counts[i] = 0;
+  if (i < n && LP_CHECK(i >= 0, kChkStateIndex)) counts[i] = 0;
 }
 
 // Bit j: byte j of the word is not zero.
@@ -377,7 +387,8 @@ __global__ void __launch_bounds__(kThreads)
         in_last = n;
         last = i;
       } else if (n > 0) {
-        mine += atomicAdd(&counts[span.first + i], n) == 0 ? 1u : 0u;
+        if (LP_CHECK(in_call(a, span, i), kChkStateIndex))
+          mine += atomicAdd(&counts[span.first + i], n) == 0 ? 1u : 0u;
       }
       ++i;
       if (left != 0 && i < span.sequences) {  // past empty sequences the next row's is searched for
@@ -391,7 +402,8 @@ __global__ void __launch_bounds__(kThreads)
     int same;
     __match_all_sync(0xffffffffu, last, &same);
     if (same) in_last = __reduce_add_sync(0xffffffffu, in_last);
-    if (in_last > 0 && (!same || (threadIdx.x & 31) == 0))
+    if (in_last > 0 && (!same || (threadIdx.x & 31) == 0) &&
+        LP_CHECK(in_call(a, span, last), kChkStateIndex))
       mine += atomicAdd(&counts[span.first + last], in_last) == 0 ? 1u : 0u;
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
@@ -423,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const unsigned whole = __ldcg(a.by_sequence ? &header->sequences : &header->counted);
   if (a.cu_seqlens != nullptr && span.staged) {
     for (int i = threadIdx.x; i < span.sequences; i += kThreads) {
+      if (!LP_CHECK(in_call(a, span, i), kChkStateIndex)) continue;
       weights[i] = weight_of(a.by_sequence, a.by_sequence ? __ldcg(counts + span.first + i) : 0u, whole);
       if (a.per_sequence) advantages[i] = __ldg(a.advantages + span.first + i);
     }
@@ -458,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 4)
           if (s == span.sequences || r + j < span.begin) {
             kept &= ~(1u << j);
           } else {
+            if (!LP_CHECK(in_call(a, span, s), kChkStateIndex)) continue;
             const int64_t at = span.first + s;
             if (a.by_sequence) w[j] = weight_of(true, __ldcg(counts + at), whole);
             if (a.per_sequence) four.advantage[j] = __ldg(a.advantages + at);
