@@ -63,8 +63,9 @@ typedef enum lp_dtype { LP_FLOAT32 = 0, LP_BFLOAT16 = 1 } lp_dtype;
  *                 branch_rstd needs branch_weight and rstd needs weight.
  * Pointers are aligned to their element; rows that all start on multiples of 8
  * elements, in memory and by their strides, with d a multiple of 8, are read and
- * written 8 columns at a time; others are slower, with the same results.  Outputs must not overlap the inputs or one another, other than
- * residual_out in place (LP_ERR_INVALID_ARGUMENT).
+ * written 8 columns at a time; others are slower, with the same results.  Outputs
+ * must not overlap the inputs or one another, other than residual_out in place
+ * (LP_ERR_INVALID_ARGUMENT).
  */
 LP_API lp_status lp_residual_norm(const void* residual, int64_t ld_residual, int residual_dtype,
                                   const void* branch, int64_t ld_branch, const void* gate,
@@ -86,7 +87,9 @@ LP_API size_t lp_residual_norm_backward_workspace_size(int64_t T, int64_t d);
  *     grad_residual = a * D;   grad_gate = b * D * n  (summed over the rows for one row [d])
  *     grad_weight = sum_t grad_normed * x;   grad_branch_weight = sum_t b * g * D * yh
  *     grad_branch = branch_rstd * (e - yh * mean(e * yh)),  e = b * g * D * branch_weight
- * (without branch_weight grad_branch = b * g * D).
+ * (without branch_weight grad_branch = b * g * D).  mean(e * yh) is taken with
+ * mean(dx * x) in one round of float32 sums, as mean(f * (grad_residual_out + rstd *
+ * dx)) - rstd * mean(dx * x) * mean(f * x) with f = b * g * branch_weight * yh.
  *
  *   residual_out  [T, d] residual_dtype: the forward's residual_out (its
  *                 `residual` when it had no branch).  NULL when weight is NULL.
@@ -175,6 +178,8 @@ LP_API lp_status lp_policy_loss(const float* logp, const float* old_logp, const 
  *
  * with l = lr * lr_scale of the tensor.  p is float32; a bfloat16 copy of it
  * (the weights the forward pass reads) is written in the same pass when asked.
+ * The moments' products and sums are each rounded once; the change of p divides by
+ * way of an approximate reciprocal, within 3 units in the last place of the change.
  *
  * The moments of all tensors lie in flat buffers: tensor i's start at the sum
  * over the tensors before it of their lengths rounded up to
@@ -188,7 +193,13 @@ LP_API lp_status lp_policy_loss(const float* logp, const float* old_logp, const 
  * (c + 1777) << 19 for u (8 bits, 16 steps an octave): 1 at the largest code
  * down to about 2^-16.  They are rounded up with the probability of the part
  * cut off (to 16 bits), so that a decay of 0.1% a step, far less than a step of
- * the code, is kept on average.  The random bits are those of Philox 4x32 with
+ * the code, is kept on average: m and u come out without bias, and v = u^2 2 to 3%
+ * high on average (u itself under 1% over the root of the averaged squares).  A
+ * magnitude below code 1 becomes zero or code 1.  Where that leaves a u of zero
+ * beside an m that is not, the next step divides that m by the root of its own
+ * gradient's square alone, or by eps where that is zero: tensors whose blocks mix
+ * magnitudes of 2^16 and more apart want 32 bits, or an eps of that part of their
+ * largest gradients.  The random bits are those of Philox 4x32 with
  * 7 rounds (Salmon et al., SC11) at counter (flat index / 4, t) and key seed;
  * the low half of word (flat index mod 4) rounds m, the high half u.  The
  * update itself uses the moments before they are rounded.  A block with a NaN
@@ -253,6 +264,8 @@ LP_API lp_status lp_adamw_grad_norm(const void* plan, int64_t n_tensors, int64_t
  *   grad_scale     [1] float32 that every gradient is multiplied by (norm_out + 1 of
  *                  lp_adamw_grad_norm), or NULL.  When it is NaN the step changes nothing.
  *   step           t >= 1, the number of this step; seed: of the 8-bit rounding.
+ *                  step, lr and the betas are arguments of the launch: a captured call
+ *                  repeats this step at every replay, with the same random bits.
  *   lr >= 0, 0 <= beta1, beta2 < 1, eps >= 2^-126 (as a float32), all finite.
  */
 LP_API lp_status lp_adamw_step(const void* plan, int64_t n_tensors, int64_t state_elements,

@@ -12,8 +12,9 @@ The first four return the selected-token log-probabilities and entropies of
 z = H W^T / tau (lp_linear_logprob_lse) and back-propagate into H and W through
 lp_linear_logprob_backward with the forward's log Z and entropy kept, so the
 backward does not recompute them.  The last two are train.residual_norm and
-train.policy_loss, on either side of them in a training step.  This is argument marshalling only: every
-step runs in liblp's kernels, on the current stream.
+train.policy_loss, on either side of them in a training step.  This is argument marshalling only: the
+computation runs in liblp's kernels, on the current stream; torch casts
+gradients, and scales those that the policy loss has written by the loss's own.
 
 The vocabulary-parallel forms run on every rank of a torch.distributed group
 (1, 2 or 4 ranks, rank r holding shard r of W's rows or of the logits'

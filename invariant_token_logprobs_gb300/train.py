@@ -308,11 +308,16 @@ class AdamW:
     bfloat16 tensors (or None) that receive the updated params.  weight_decay and lr_scale are
     numbers or one for each tensor.
 
-    state_bits=8 holds both moments in a byte an element and one scale for 256 elements, rounded
-    without bias under `seed`; 32 holds them in float32.  `state`, as state_dict() gives it,
-    continues from it with its buffers, and with its seed where none is given.  set_grads() names other gradient tensors.  A step on any
-    stream keeps its tensors' memory until it is done, so that they, and the optimizer, may be
-    dropped right after it."""
+    state_bits=8 holds the first moment and the root of the second in a byte an element and one
+    scale for 256 elements, rounded without bias under `seed`, which leaves the second moment 2 to
+    3% high on average; 32 holds both moments in float32.  With 8 bits an element far below its
+    block's largest (by 2^16 and more) may lose its root before its first moment and then take one
+    step of up to lr * |first moment| / eps: use 32 for tensors that mix such sizes.
+
+    `state`, as state_dict() gives it, continues from it with its buffers, and with its seed where
+    none is given.  set_grads() names other gradient tensors.  A step on any stream keeps its
+    tensors' memory until it is done, so that they, and the optimizer, may be dropped right after
+    it.  eps is 2^-126 at least."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], *,
                  copies: Optional[Sequence[Optional[torch.Tensor]]] = None, lr: float = 1e-3,
@@ -437,7 +442,11 @@ class AdamW:
              stream=None) -> Optional[torch.Tensor]:
         """One step.  With max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))
         of their global 2-norm, which is returned as a float32 scalar on the device; a norm that
-        is not finite leaves every param and moment as it was (the step is counted)."""
+        is not finite leaves every param and moment as it was (the step is counted).
+
+        A step that is captured in a graph repeats itself at every replay: its number, learning
+        rate and random bits are part of it, and nothing is counted.  The optimizer has to outlive
+        the graph."""
         if stream is not None:
             return _on_stream(stream, self.params[0], self.step, lr, max_norm)
         norm = (_calls or load_calls()).adamw_step(
