@@ -454,14 +454,15 @@ PyObject* policy_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
 }
 
 // Keeps what an optimizer's step reads and writes until it is done, wherever it runs: the plan and
-// the moments, and the tensors that the optimizer was given where the step is on another stream than
-// `home`, the one that the plan was laid out on.  A captured step reads its plan and gradients at
-// every replay: `captured` keeps them.
+// the moments, and the tensors that the optimizer was given where the step is on a stream that is not
+// in `streams`: those that have it on record (which lasts as long as the tensor), and the one that
+// the plan was laid out on.  A captured step reads its plan and gradients at every replay:
+// `captured` keeps them.
 void keep_for_step(c10::cuda::CUDAStream stream, PyObject* plan,
                    std::initializer_list<const at::Tensor*> moments, PyObject* written, PyObject* grads,
-                   PyObject* home, PyObject* captured) {
-  if (!PyTuple_Check(written) || !PyTuple_Check(grads) || !PyList_Check(captured))
-    type_error("expected tuples of tensors and a list");
+                   PyObject* streams, PyObject* captured) {
+  if (!PyTuple_Check(written) || !PyTuple_Check(grads) || !PyList_Check(streams) || !PyList_Check(captured))
+    type_error("expected tuples of tensors and lists");
   if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
     const Py_ssize_t last = PyList_GET_SIZE(captured) - 1;
     if (last >= 0 && PyTuple_GET_ITEM(PyList_GET_ITEM(captured, last), 0) == plan) return;
@@ -473,14 +474,20 @@ void keep_for_step(c10::cuda::CUDAStream stream, PyObject* plan,
   }
   used_on(stream, tensor(plan, "plan"));
   for (const at::Tensor* t : moments) used_on(stream, t);
-  if (integer(home) == int64_t(reinterpret_cast<intptr_t>(stream.stream()))) return;
+  const int64_t handle = int64_t(reinterpret_cast<intptr_t>(stream.stream()));
+  for (Py_ssize_t i = 0; i < PyList_GET_SIZE(streams); ++i)
+    if (integer(PyList_GET_ITEM(streams, i)) == handle) return;
   for (PyObject* tensors : {written, grads})
     for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(tensors); ++i)
       used_on(stream, &required(PyTuple_GET_ITEM(tensors, i), "a tensor of the step"));
+  PyObject* seen = PyLong_FromLongLong(handle);
+  const int failed = seen == nullptr ? -1 : PyList_Append(streams, seen);
+  Py_XDECREF(seen);
+  if (failed) throw Refused{};
 }
 
 // plan, n_tensors, state_elements, state_bits, exp_avg, exp_avg_sq, exp_avg_scale,
-// exp_avg_sq_scale, lr, beta1, beta2, eps, step, seed, max_norm or None, written, grads, home,
+// exp_avg_sq_scale, lr, beta1, beta2, eps, step, seed, max_norm or None, written, grads, streams,
 // captured: the norm's tensor or None
 PyObject* adamw_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 19, [&] {

@@ -402,7 +402,7 @@ class AdamW:
             raise ValueError("gradients must not share memory with params, copies or moments")
         plan = host.to(self.params[0].device)
         home = torch.cuda.current_stream(plan.device).cuda_stream if plan.is_cuda else 0
-        self.grads, self.state_elements, self._plan, self._home = grads, elements, plan, home
+        self.grads, self.state_elements, self._plan, self._streams = grads, elements, plan, [home]
         self._weight_decay, self._lr_scale = weight_decay, lr_scale
         self._given = (tuple(self.params + [c for c in self.copies if c is not None]), tuple(grads))
 
@@ -453,7 +453,7 @@ class AdamW:
             self._plan, len(self.params), self.state_elements, self.state_bits, self.exp_avg,
             self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.lr if lr is None else lr,
             self.betas[0], self.betas[1], self.eps, self.step_count + 1, self.seed, max_norm,
-            *self._given, self._home, self._captured)
+            *self._given, self._streams, self._captured)
         self.step_count += 1
         return norm
 
