@@ -7,7 +7,10 @@
 // float32 gradients took 926 us at 106 instructions an element and take 880 at 84, of 795 us at
 // the copy rate (issue slots 73%, ALU pipe 58% busy).  The values of 311 M elements' 8-bit moments
 // are written in 448 us, 6.9 TB/s.  300 tensors of 64 to 4 M elements, 113 M in all, take 578 us with
-// their norm, of which the step is 490 and reading the gradients for the norm 77.
+// their norm, of which the step is 490 and reading the gradients for the norm 77.  Tensors off a
+// 16-byte boundary go through shared memory: 40 M elements take 363 us instead of 175 with 32 bits, 340
+// instead of 122 with 8.  Where each warp has one block, no copy runs ahead: 4.9 M elements of 8 bits
+// take 19.4 us of 11.6.
 //
 // One launch: a table gives each CTA's row its tensor, and a tensor's blocks of 256 elements are a
 // warp's.  The moments' products are each rounded (no fused multiplication), so that 8-bit moments,

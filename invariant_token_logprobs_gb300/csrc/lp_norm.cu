@@ -6,8 +6,11 @@
 // branch takes 65 us, 6.2 TB/s; one CTA a row that reads its operands three times took 123, a row
 // in registers with a CTA each 88, with the ring 75, with two rows a turn 65.  512 x 4096 takes
 // 5.0 us, of which its 16.8 MB are 2.5: the rest is the launch and the chain of loads, two sums
-// and stores.  Rows that are not aligned cost up to twice that, in instructions (4864 x 2047
-// bfloat16 26 us, 4864 x 2048 12).  lp_norm.cuh says how rows lie over threads and come on chip.
+// and stores.  Wider rows, bfloat16: 4096 x 7168 takes 40 us of 35 at the copy rate and 53 with a normed
+// branch, 4096 x 12288 68 and 105 of 59; from 8193 columns on a thread holds four groups, which its 64
+// registers do not (8 to 96 bytes spill).  Rows that are not aligned cost up to twice that, in
+// instructions (4864 x 2047 bfloat16 26 us, 4864 x 2048 13).  lp_norm.cuh says how rows lie over threads
+// and come on chip.
 #include <type_traits>
 
 #include "lp_norm.cuh"

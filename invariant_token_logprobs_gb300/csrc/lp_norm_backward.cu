@@ -1,14 +1,18 @@
 // lp_norm_backward.cu: the backward pass of the residual norm (include/lp_train.h).
 //
 // Bound by HBM (12 bytes a column in bfloat16) where a row has one sum: 8192 x 4096 takes 66 us,
-// 6.1 TB/s.  With a normed branch (three sums) 4864 x 4096 takes 64 us of 35 at the copy rate: the
-// sums over rows hold 24 of each thread's registers, so 16 warps fit an SM, and all of them wait
-// for the row's sums.  In float32 that is 52 us of 47 for 4864 x 2048.  The sums over rows cost
-// some 3 us a call, for the CTAs' partial sums and the second kernel.  History at 8192 x 4096: sums
-// in shared memory 1083 us, rows and sums in registers 158, with the ring and kept addresses 100,
-// two rows a turn 69, two columns an instruction 66.  A row's second pass beside the next row's
-// first one gained only with a normed branch of 4096 (59 us) and lost elsewhere (4864 x 2400: 58 us
-// instead of 50).  lp_norm.cuh says how rows lie over threads and come on chip.
+// 6.1 TB/s.  With a normed branch (three sums) 4864 x 4096 takes 65 us of 35 at the copy rate and
+// 8192 x 4096 101 of 59: a team of 16 warps owns a row, the sums over rows hold 24 of each thread's
+// registers, so one team fits an SM, and all of it waits for the row's sums (the two-row kernels also
+// spill 36 to 44 bytes a thread at 128 registers).  In float32 that is 45 us of 35 for 4864 x 2048.
+// The sums over rows cost some 3 us a call, for the CTAs' partial sums and the second kernel: 512 x 4096
+// takes 13 us of 4.  Two groups a thread spill 92 to 156 bytes with a normed branch: 4096 x 7168 takes
+// 77 us of 52 without one, 127 with it.  From 8193 columns on the row is read twice, a column a thread at
+// a time: 4096 x 12288 takes 514 us of 89.  History at 8192 x 4096: sums in shared memory 1083 us, rows
+// and sums in registers 158, with the ring and kept addresses 100, two rows a turn 69, two columns an
+// instruction 66.  A row's second pass beside the next row's first one gained only with a normed branch
+// of 4096 (59 us) and lost elsewhere (4864 x 2400: 58 us instead of 50).  lp_norm.cuh says how rows lie
+// over threads and come on chip.
 #include <type_traits>
 
 #include "lp_norm.cuh"
@@ -306,7 +310,9 @@ __global__ void __launch_bounds__(kMaxTeam)
 }
 
 // Backward of rows wider than that: the row is read twice (the second time from L2) and the
-// sums over rows lie in shared memory, where each column has one owner.
+// sums over rows lie in shared memory, where each column has one owner.  4096 x 12288 bfloat16 takes
+// 514 us, 647 with a normed branch, of 89 at the copy rate: loads of 2 and 4 bytes, weights from L2 at
+// every row, one CTA an SM (issue slots 30%, DRAM 13% busy).
 constexpr int kWideThreads = 1024;
 
 template <class T>

@@ -5,14 +5,15 @@
 // the rest.  Up to kSmallRows rows one CTA does both from registers in one launch; beyond
 // that they are two grids over chunks of rows, launched as programmatic dependents.
 //
-// 512 rows take 2.8 us, next to nothing of it bytes: a launch, the loads, two barriers.  4.2 M rows
+// 512 rows take 3.0 us, next to nothing of it bytes: a launch, the loads, two barriers.  4.2 M rows
 // of 1024 ragged sequences take 34 us where their 103 MB are 15: a turn of rows on all SMs takes
 // 2.7 us, 5.7 TB/s, and there are 7, but 15 us pass outside them.  The first pass reads 4 MB in some
 // 7 us, most of it the search for a CTA's sequences and the atomics' way; the second has its own
 // search before its first turn, and 3 us for the last CTA's sum.  Copies two turns ahead (34 us),
 // three or five CTAs an SM (34, 41) and a first pass of a quarter of the CTAs, to leave room for the
 // second's start (36), gained nothing.  One CTA for everything took 11.6 ms; a chunk of 4096 rows a
-// CTA 51 us, with 64-bit searches for each row.
+// CTA 51 us, with 64-bit searches for each row.  Without a mask the counts are differences of the
+// offsets, but the first pass runs all the same (36 us a call).
 //
 // Counts are integers added by atomics, whose order does not show.  The loss's sums are
 // taken in a fixed order: a thread's rows, the CTA's tree, then the CTAs' sums by whichever
@@ -142,7 +143,7 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int64_t t, int6
                                             float (&sum)[kStats]) {
   float grad[4] = {0.f, 0.f, 0.f, 0.f}, grad_entropy[4] = {0.f, 0.f, 0.f, 0.f};
   // A row that does not count, whatever it holds, is one of zeros: without branches the four rows'
-  // chains run side by side (512 rows: 2.8 us instead of 3.2).
+  // chains run side by side (512 rows: 0.4 us less).
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (kept == 0) break;
