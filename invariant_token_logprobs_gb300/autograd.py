@@ -48,7 +48,8 @@ class _Refusal(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, *grads):
-        return tuple(None if g is None else g.view_as(g) for g in grads)
+        # copies: a view could not be scaled in place, as a clip by the norm does
+        return tuple(None if g is None else g.clone() for g in grads)
 
     @staticmethod
     def backward(ctx, *_):

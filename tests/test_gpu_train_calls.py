@@ -31,11 +31,12 @@ def make_optimizer(bits, seed=1, sizes=(700, 9000)):
 
 
 def busy_stream():
-    """A stream that is ordered after what was made so far and has some 0.1 s of work ahead."""
+    """A stream that is ordered after what was made so far and has some 0.2 s of work ahead."""
+    overwrite([512])  # its kernel is loaded before the clock runs
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(400_000_000)
     return side
 
 
@@ -163,6 +164,8 @@ def test_policy_loss_autograd_on_another_stream():
 
 def second_order(y, x):
     g, = torch.autograd.grad(y, x, create_graph=True)
+    with torch.no_grad():
+        g.mul_(1)  # as a clip by the norm does
     with pytest.raises(RuntimeError, match="gradient of a gradient"):
         (g.float().square().sum() + y).backward()  # a penalty on the gradient beside the loss
 
