@@ -233,7 +233,9 @@ LP_API size_t lp_adamw_plan_size(const lp_adamw_tensor* tensors, int64_t n_tenso
  * aligned device memory once and pass it to the calls below; lay it out again
  * when a pointer, length or factor changes.  Pointers are aligned to their
  * element; tensors whose pointers are multiples of 16 bytes go 16 bytes at a
- * time, with the same results.  A tensor must not appear twice.  Host function.
+ * time, with the same results.  A tensor must not appear twice, and no param or copy
+ * may share memory with another tensor's param, copy or gradient: a tensor's own are
+ * compared here, those of others are the caller's to keep apart.  Host function.
  */
 LP_API lp_status lp_adamw_plan(const lp_adamw_tensor* tensors, int64_t n_tensors, void* plan_host,
                                size_t plan_bytes);
