@@ -1,0 +1,104 @@
+/*
+ * lp_tune.h: C ABI of liblp's fine-tuning operators on GB300 (sm_103a), beside
+ * the training-step operators of lp_train.h:
+ *
+ *   layer norm       the sum of a residual stream and a block's output, and its
+ *                    layer norm (the H of lp_linear_logprob for models whose
+ *                    head is fed by one), in one pass; and its backward pass.
+ *   preference loss  the loss of pairs of a chosen and a rejected sequence, from
+ *                    the selected tokens' log-probabilities, with the grad_logp
+ *                    that lp_linear_logprob_backward takes.
+ *   Muon             one optimizer step over many matrices, whose momentum is
+ *                    orthogonalised by Newton-Schulz products.
+ *
+ * The conventions are those of lp.h and lp_train.h: pointers are device memory
+ * owned by the caller unless a comment says host, nothing is allocated, all work
+ * is enqueued on `stream` without synchronising with the host, argument errors
+ * are returned before anything is enqueued, and the current device must be of
+ * compute capability 10.3.  Strides are in elements.  Data on the device (row
+ * offsets, masks, NaN or infinities) never makes a call fault.
+ */
+#ifndef LP_TUNE_H_
+#define LP_TUNE_H_
+
+#include "lp_train.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------------
+ * Layer norm.  Per row of d channels, with residual stream r and block output
+ * (branch) y:
+ *
+ *     r' = r + y
+ *     h  = (r' - mean) * rstd * weight + bias,  rstd = rsqrt(mean((r' - mean)^2) + eps)
+ *
+ * branch, weight and bias are optional (without branch r' = r).  All arithmetic
+ * and the sums are float32; the squares are of the deviations from the row's
+ * mean, h is formed from the unrounded r', and each output is rounded once.  A
+ * row's results do not depend on the other rows, on T or on the row's place.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * lp_layer_norm:
+ *   residual      [T, d] residual_dtype, row stride ld_residual >= d.
+ *   branch        [T, d] act_dtype, row stride ld_branch >= d, or NULL.
+ *   weight, bias  [d] weight_dtype, or NULL.
+ *   T >= 0 (0 enqueues nothing), 1 <= d <= 16384, eps >= 0 and finite.
+ *   residual_out  [T, d] residual_dtype, required with branch and NULL without;
+ *                 it may be `residual` itself (same pointer and stride).
+ *   normed        [T, d] act_dtype, required.
+ *   mean, rstd    [T] float32, or NULL: for the backward pass.
+ * Pointers are aligned to their element; rows that all start on multiples of 8
+ * elements, in memory and by their strides, with d a multiple of 8, are read and
+ * written 8 columns at a time; others are slower, with the same results.  Outputs
+ * must not overlap the inputs or one another, other than residual_out in place
+ * (LP_ERR_INVALID_ARGUMENT).
+ */
+LP_API lp_status lp_layer_norm(const void* residual, int64_t ld_residual, int residual_dtype,
+                               const void* branch, int64_t ld_branch, int act_dtype,
+                               const void* weight, const void* bias, int weight_dtype, int64_t T,
+                               int64_t d, float eps, void* residual_out, int64_t ld_residual_out,
+                               void* normed, int64_t ld_normed, float* mean, float* rstd,
+                               void* stream);
+
+/* Workspace bytes of lp_layer_norm_backward; 0 for invalid sizes. */
+LP_API size_t lp_layer_norm_backward_workspace_size(int64_t T, int64_t d);
+
+/*
+ * lp_layer_norm_backward: the gradients of lp_layer_norm from those of its
+ * outputs.  With x = (r' - mean) * rstd and dx = grad_normed * weight:
+ *     D = grad_residual_out + rstd * (dx - mean(dx) - x * mean(dx * x))
+ *     grad_residual = grad_branch = D
+ *     grad_weight = sum_t grad_normed * x;   grad_bias = sum_t grad_normed
+ *
+ *   residual_out  [T, d] residual_dtype: the forward's residual_out (its
+ *                 `residual` when it had no branch).
+ *   weight        the forward's, or NULL.
+ *   mean, rstd    [T] float32 from the forward.
+ *   grad_normed   [T, d] act_dtype.
+ *   grad_residual_out  [T, d] residual_dtype, or NULL (zero).
+ *   grad_residual [T, d] residual_dtype; may be grad_residual_out itself.
+ *   grad_branch   [T, d] act_dtype: the same gradient in the branch's type, or
+ *                 NULL to skip (it is grad_residual where the types are equal).
+ *   grad_weight, grad_bias  [d] float32, each NULL to skip.
+ *   workspace     256-byte aligned, lp_layer_norm_backward_workspace_size(T, d)
+ *                 bytes; its contents on entry do not matter.  NULL when neither
+ *                 sum is asked for.
+ * T >= 1 rows are summed in a fixed order (float32), so repeated calls give the
+ * same bits; T == 0 writes zeros to the summed gradients.
+ */
+LP_API lp_status lp_layer_norm_backward(
+    const void* residual_out, int64_t ld_residual_out, int residual_dtype, int act_dtype,
+    const void* weight, int weight_dtype, int64_t T, int64_t d, const float* mean,
+    const float* rstd, const void* grad_normed, int64_t ld_grad_normed,
+    const void* grad_residual_out, int64_t ld_grad_residual_out, void* grad_residual,
+    int64_t ld_grad_residual, void* grad_branch, int64_t ld_grad_branch, float* grad_weight,
+    float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LP_TUNE_H_ */

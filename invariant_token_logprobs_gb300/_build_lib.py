@@ -26,14 +26,15 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liblp.so")
 SOURCES = ["lp_api.cu", "lp_logits.cu", "lp_linear.cu", "lp_backward.cu", "lp_train_api.cu",
-           "lp_norm.cu", "lp_norm_backward.cu", "lp_policy.cu", "lp_adamw.cu"]
-HEADERS = [os.path.join(ROOT, "include", f) for f in ("lp.h", "lp_train.h")] + [
+           "lp_norm.cu", "lp_norm_backward.cu", "lp_policy.cu", "lp_adamw.cu", "lp_tune_api.cu",
+           "lp_layer_norm.cu", "lp_layer_norm_backward.cu"]
+HEADERS = [os.path.join(ROOT, "include", f) for f in ("lp.h", "lp_train.h", "lp_tune.h")] + [
     os.path.join(CSRC, f) for f in ("lp_device.cuh", "lp_internal.h", "lp_tcgen05.cuh",
-                                    "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh")
+                                    "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh",
+                                    "lp_args.h", "lp_tune_internal.h")
 ]
-# the Python calls of train.py: host code against torch's headers, no part of liblp
-CALLS_SOURCE = os.path.join(CSRC, "train_calls.cpp")
-CALLS = os.path.join(BUILD, "_train_calls.so")
+# the Python calls of train.py and tune.py: host code against torch's headers, no part of liblp
+CALLS_MODULES = ("train", "tune")
 # the checked build (-DLP_CHECKED: index and coordinate tests in every kernel)
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "liblp.so")
@@ -92,7 +93,12 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     return obj
 
 
-def _calls_command(out: str) -> list[str]:
+def _calls_paths(module: str) -> tuple[str, str]:
+    """The source and the library of a module's compiled calls."""
+    return os.path.join(CSRC, f"{module}_calls.cpp"), os.path.join(BUILD, f"_{module}_calls.so")
+
+
+def _calls_command(module: str, out: str) -> list[str]:
     import torch
     root = os.path.dirname(torch.__file__)
     include = os.path.join(root, "include")
@@ -102,41 +108,44 @@ def _calls_command(out: str) -> list[str]:
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", sysconfig.get_paths()["include"], "-I", include,
             "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", cuda,
-            CALLS_SOURCE, "-o", out, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            _calls_paths(module)[0], "-o", out, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
             "-lc10_cuda", f"-Wl,-rpath,{libs}"]
 
 
-def calls_hash() -> str:
-    """SHA-256 over train.py's compiled calls: their source, the header, the command (which names
+def calls_hash(module: str = "train") -> str:
+    """SHA-256 over a module's compiled calls: their source, the headers, the command (which names
     the flags and torch) and the versions of torch and Python."""
     import torch
+    source, library = _calls_paths(module)
     h = hashlib.sha256()
-    for path in (CALLS_SOURCE, HEADERS[0], HEADERS[1]):
+    for path in (source, os.path.join(CSRC, "calls.h"), *HEADERS[:3]):
         with open(path, "rb") as f:
             h.update(f.read())
-    h.update(" ".join(_calls_command(CALLS)).encode())
+    h.update(" ".join(_calls_command(module, library)).encode())
     h.update(f"{torch.__version__} {sys.version}".encode())
     return h.hexdigest()
 
 
-def build_calls(force: bool = False, quiet: bool = False) -> str:
-    """Compile _train_calls.so unless it was built from exactly this source; return its path."""
-    digest, stamp = calls_hash(), CALLS + ".sha256"
-    if not force and os.path.exists(CALLS) and os.path.exists(stamp):
+def build_calls(force: bool = False, quiet: bool = False, module: str = "train") -> str:
+    """Compile a module's calls (_train_calls.so, _tune_calls.so) unless they were built from exactly
+    this source; return their path."""
+    library = _calls_paths(module)[1]
+    digest, stamp = calls_hash(module), library + ".sha256"
+    if not force and os.path.exists(library) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == digest:
-                return CALLS
+                return library
     os.makedirs(BUILD, exist_ok=True)
-    tmp = f"{CALLS}.{os.getpid()}.tmp"
-    res = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+    tmp = f"{library}.{os.getpid()}.tmp"
+    res = subprocess.run(_calls_command(module, tmp), capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"g++ failed for train_calls.cpp:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, CALLS)
+        raise RuntimeError(f"g++ failed for {module}_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, library)
     with open(stamp, "w") as f:
         f.write(digest + "\n")
     if not quiet:
-        print("train calls: compiled", flush=True)
-    return CALLS
+        print(f"{module} calls: compiled", flush=True)
+    return library
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False,

@@ -7,12 +7,13 @@ training-step operators.
     logp, entropy = vocab_parallel_logprob_from_logits(z_shard, y, V, group)
     h, residual   = residual_norm(residual, branch, weight=..., branch_weight=..., gate=...)
     loss, stats   = policy_loss(logp, old_logp, advantages, entropy=entropy, ...)
+    h, residual   = layer_norm(residual, branch, weight=..., bias=...)
 
 The first four return the selected-token log-probabilities and entropies of
 z = H W^T / tau (lp_linear_logprob_lse) and back-propagate into H and W through
 lp_linear_logprob_backward with the forward's log Z and entropy kept, so the
-backward does not recompute them.  The last two are train.residual_norm and
-train.policy_loss, on either side of them in a training step.  This is argument marshalling only: the
+backward does not recompute them.  The next two are train.residual_norm and
+train.policy_loss, on either side of them in a training step, and the last tune's.  This is argument marshalling only: the
 computation runs in liblp's kernels, on the current stream; torch casts
 gradients, and scales those that the policy loss has written by the loss's own.
 
@@ -39,7 +40,7 @@ from typing import Optional
 
 import torch
 
-from . import lp, train
+from . import lp, train, tune
 from . import vocab_parallel as vp
 
 
@@ -258,6 +259,43 @@ def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
     and of a one-row gate are float32 sums rounded once)."""
     normed, new = _ResidualNorm.apply(residual, branch, weight, branch_weight, gate,
                                       residual_scale, branch_scale, eps)
+    return normed, residual if branch is None else new
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, residual, branch, weight, bias, eps):
+        out = tune.layer_norm(residual, branch, weight=weight, bias=bias, eps=eps)
+        ctx.save_for_backward(weight, bias, out.residual, out.mean, out.rstd)
+        ctx.act = None if branch is None else branch.dtype
+        ctx.set_materialize_grads(False)
+        # without a branch the stream is the input, which is no output of this function
+        return out.normed, None if branch is None else out.residual
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, g_normed, g_residual):
+        weight, bias, residual, mean, rstd = ctx.saved_tensors
+        if g_normed is None and g_residual is None:
+            return (None,) * 5
+        if g_normed is None:
+            g_normed = torch.zeros_like(residual, dtype=ctx.act or residual.dtype)
+        need_w, need_b = ctx.needs_input_grad[2:4]
+        g = tune.layer_norm_backward(_rows(g_normed), _rows(g_residual), residual, mean, rstd,
+                                     weight=weight, bias=bias, branch=ctx.act is not None,
+                                     weight_grads=need_w or need_b)
+        cast = lambda t, like: None if t is None else t.to(like.dtype)  # noqa: E731
+        return g.residual, g.branch, cast(g.weight, weight), cast(g.bias, bias), None
+
+
+def layer_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None, *,
+               weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5):
+    """(normed, new residual stream) of tune.layer_norm, differentiable in the residual, the branch,
+    the weight and the bias; the backward is lp_layer_norm_backward with the forward's means and
+    reciprocal roots kept.  Gradients come in the inputs' dtypes (those of weight and bias are float32
+    sums rounded once)."""
+    normed, new = _LayerNorm.apply(residual, branch, weight, bias, eps)
     return normed, residual if branch is None else new
 
 

@@ -16,7 +16,7 @@
 #include "lp_check.cuh"
 #include "lp_device.cuh"
 #include "lp_internal.h"
-#include "lp_train_internal.h"
+#include "lp_tune_internal.h"
 
 namespace lp {
 
@@ -164,18 +164,20 @@ lp_status lp_get_check_word(uint32_t* word_out) {
   const lp_status st = lp::current_device(&dev);
   if (st != LP_OK) return st;
   if (cudaDeviceSynchronize() != cudaSuccess) return LP_ERR_CUDA;
-  uint32_t a = 0, b = 0, c = 0, n = 0, nb = 0, p = 0, w = 0;
-  if (lp::take_check_word_logits(&a) != cudaSuccess ||
-      lp::take_check_word_linear(&b) != cudaSuccess ||
-      lp::take_check_word_backward(&c) != cudaSuccess ||
-      lp::take_check_word_norm(&n) != cudaSuccess ||
-      lp::take_check_word_norm_backward(&nb) != cudaSuccess ||
-      lp::take_check_word_policy(&p) != cudaSuccess ||
-      lp::take_check_word_adamw(&w) != cudaSuccess) {
-    cudaGetLastError();
-    return LP_ERR_CUDA;
+  uint32_t all = 0;
+  for (const auto take :
+       {lp::take_check_word_logits, lp::take_check_word_linear, lp::take_check_word_backward,
+        lp::take_check_word_norm, lp::take_check_word_norm_backward, lp::take_check_word_policy,
+        lp::take_check_word_adamw, lp::take_check_word_layer_norm,
+        lp::take_check_word_layer_norm_backward}) {
+    uint32_t word = 0;
+    if (take(&word) != cudaSuccess) {
+      cudaGetLastError();
+      return LP_ERR_CUDA;
+    }
+    all |= word;
   }
-  *word_out = a | b | c | n | nb | p | w;
+  *word_out = all;
   return LP_OK;
 }
 

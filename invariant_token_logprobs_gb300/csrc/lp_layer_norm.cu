@@ -1,0 +1,197 @@
+// lp_layer_norm.cu: the layer norm (include/lp_tune.h).
+//
+// The squares are of the deviations from the row's mean, so a row takes two rounds of sums; it
+// stays in registers between them.  (Taking the mean of the squares less the square of the mean
+// would need one, and lose what a row's mean is above its spread.)  lp_norm.cuh says how rows lie
+// over threads and come on chip.
+#include <type_traits>
+
+#include "lp_norm.cuh"
+#include "lp_tune_internal.h"
+
+namespace lp {
+namespace {
+
+// With one group a thread a team takes two rows a turn: their waits for the team are one, and the
+// weights are read once.
+template <int G>
+constexpr int kRowsATurn = G == 1 ? 2 : 1;
+
+template <class R, class A, int G, int kAlign>
+__global__ void __launch_bounds__(kMaxTeam, 2)
+    lp_layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Plan plan) {
+  constexpr int kRows = kRowsATurn<G>;
+  __shared__ __align__(16) float slots[2][2][kMaxWarps][padded(kRows)];
+  extern __shared__ __align__(32) unsigned char ring[];
+  const Place p(a.T, a.d, plan.shape);
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  const bool branch = a.branch.p != nullptr;
+  const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
+  int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
+  if (!LP_CHECK(a.d <= a.residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
+  clear_ring<kAlign, G>(ring, plan.stages * plan.stage_bytes, p);
+  // a stage: the residual's rows, the branch's
+  Stream<R, kAlign> residual;
+  Stream<A, kAlign> y;
+  uint32_t offset = 0;
+  const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  residual.template start<G>(stage0, &offset);
+  if (branch) y.template start<G>(stage0, &offset);
+  void* stretch = ring + plan.stages * plan.stage_bytes + p.warp * kStretch;
+  const uint32_t accesses = plan.accesses;
+  int64_t next = t;  // the row that is fetched next
+  const auto fetch = [&](int stage) {
+    if (next < a.T) {
+      const uint32_t at = stage * plan.stage_bytes;
+      residual.template fetch<G>(a.residual, next, at, access_of(accesses, kResidual), p);
+      if (branch) y.template fetch<G>(a.branch, next, at, access_of(accesses, kBranch), p);
+    }
+    next += step;
+    commit_copies();
+  };
+  for (int s = 0; s + kRows < plan.stages; ++s) fetch(s);
+  const bool wide_w = access_of(accesses, kWeight) == kWide;
+  const bool wide_b = access_of(accesses, kBranchWeight) == kWide;
+  int stage = 0, turn = 0;
+  // every team runs as many turns as the CTA's first, so that all meet at the barriers
+  for (; t - p.in_cta < a.T; t += kRows * step, turn ^= 1) {
+    __syncwarp();  // the stages that are copied into have been read by the warp
+    int to = stage - kRows;
+    if (to < 0) to += plan.stages;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      fetch(to);
+      if (++to == plan.stages) to = 0;
+    }
+    wait_copies(plan.stages - kRows);
+    __syncwarp();
+    // a row that the team does not have is computed like the others, of what the ring holds, and
+    // not written
+    Pairs v[kRows][G];
+    float mean[kRows], root[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const uint32_t at = stage * plan.stage_bytes;
+      if (++stage == plan.stages) stage = 0;
+      float2 s = both(0.f);
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        Pairs& vk = v[j][k];
+        residual.get(a.residual, t + j * step, at, k, vk);
+        if (branch) {
+          Pairs n;
+          y.get(a.branch, t + j * step, at, k, n);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vk[e] = add(vk[e], n[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = add(s, vk[e]);
+      }
+      mean[j] = s.x + s.y;
+    }
+    team_sum(mean, slots[turn][0], p);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      mean[j] *= inv_d;
+      float2 s = both(0.f);
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        if (branch)
+          put<R, kAlign>(a.residual_out, t + j * step, k, t + j * step < a.T,
+                         access_of(accesses, kOut), p, stretch, v[j][k]);
+        // columns past the row are no part of its spread
+        const int left = p.d - 8 * (p.i + k * p.team);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2& x = v[j][k][e];
+          x = add(x, both(-mean[j]));
+          if (kAlign == kAligned ? left <= 0 : left <= 2 * e) x.x = 0.f;
+          if (kAlign == kAligned ? left <= 0 : left <= 2 * e + 1) x.y = 0.f;
+          s = fma(x, x, s);
+        }
+      }
+      root[j] = s.x + s.y;
+    }
+    team_sum(root, slots[turn][1], p);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      root[j] = 1.f / sqrtf(__fmaf_rn(root[j], inv_d, a.eps));
+      if (p.i == 0 && t + j * step < a.T && LP_CHECK(p.has(t + j * step), kChkRowIndex)) {
+        if (a.mean != nullptr) a.mean[t + j * step] = mean[j];
+        if (a.rstd != nullptr) a.rstd[t + j * step] = root[j];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      Pairs w, b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = both(1.f), b[e] = both(0.f);
+      if (a.weight != nullptr) read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
+      if (a.bias != nullptr) read_weight(a.bias, a.weight_bf16, k, wide_b, p, b);
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][k][e] = fma(mul(v[j][k][e], both(root[j])), w[e], b[e]);
+        put<A, kAlign>(a.normed, t + j * step, k, t + j * step < a.T, access_of(accesses, kNormed),
+                       p, stretch, v[j][k]);
+      }
+    }
+  }
+}
+
+// The CTAs of an SM have up to 1024 threads between them, each CTA with rows in flight of its own,
+// and this much shared memory for them.
+constexpr int kForwardBytes = 216 << 10;
+
+template <int G>
+lp_status launch_forward(const Device& dev, const LayerNormArgs& a, uint32_t accesses, Align align,
+                         cudaStream_t stream) {
+  return with_types(a.residual_bf16, a.act_bf16, [&](auto r, auto x) {
+    using R = decltype(r);
+    using A = decltype(x);
+    const auto launch = [&](auto* kernel, PerContextOnce* once) {
+      if (!allow_ring(kernel, dev, once)) return LP_ERR_CUDA;
+      Plan plan{shape_of(a.d, G, a.T), accesses, 1, 0};
+      const int threads = plan.shape.team * plan.shape.teams;
+      const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0);
+      const int least = stage_bytes_of(threads, G, columns, align != kAligned) * kRowsATurn<G> +
+                        (align == kAligned ? 0 : threads / 32 * kStretch);
+      const int ctas = std::max(1, std::min(1024 / threads, kForwardBytes / least));
+      const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
+      const int64_t blocks = std::min<int64_t>(all, kSlots * ctas);
+      const int smem = plan_ring(&plan, columns, G, align != kAligned, (all + blocks - 1) / blocks,
+                                 kRowsATurn<G>, kForwardBytes / ctas);
+      kernel<<<unsigned(blocks), threads, smem, stream>>>(a, plan);
+      return launched();
+    };
+    static PerContextOnce once[3];
+    constexpr Align kLeast = sizeof(R) + sizeof(A) < 8 ? kByElements : kByWords;
+    return align == kAligned   ? launch(lp_layer_norm_kernel<R, A, G, kAligned>, once)
+           : align == kByWords ? launch(lp_layer_norm_kernel<R, A, G, kByWords>, once + 1)
+                               : launch(lp_layer_norm_kernel<R, A, G, kLeast>, once + 2);
+  });
+}
+
+}  // namespace
+
+lp_status launch_layer_norm(const Device& dev, const LayerNormArgs& a, cudaStream_t stream) {
+  const uint32_t accesses = access_bits(kResidual, a.residual, a.residual_bf16) |
+                            access_bits(kBranch, a.branch, a.act_bf16) |
+                            access_bits(kWeight, a.weight, 0, a.weight_bf16) |
+                            access_bits(kBranchWeight, a.bias, 0, a.weight_bf16) |
+                            access_bits(kOut, a.residual_out, a.residual_bf16) |
+                            access_bits(kNormed, a.normed, a.act_bf16);
+  const bool fast = all_wide(accesses, {kResidual, kBranch, kOut, kNormed}, a.d) &&
+                    near(a.residual) && near(a.branch) && near(a.residual_out) && near(a.normed);
+  const Align align = fast                                                            ? kAligned
+                      : any_halves(accesses, {kResidual, kBranch, kOut, kNormed}) ? kByElements
+                                                                                      : kByWords;
+  // as few groups a thread as its team's 512 threads allow
+  if (a.d <= kMaxTeam * 8) return launch_forward<1>(dev, a, accesses, align, stream);
+  if (a.d <= kMaxTeam * 16) return launch_forward<2>(dev, a, accesses, align, stream);
+  return launch_forward<4>(dev, a, accesses, align, stream);
+}
+
+cudaError_t take_check_word_layer_norm(uint32_t* out) { return take_check_word(out); }
+
+}  // namespace lp

@@ -1,4 +1,5 @@
-// lp_norm.cuh: what the residual norm's forward and backward kernels share.
+// lp_norm.cuh: what the forward and backward kernels of the residual norm and of the layer norm
+// share.
 //
 // Both are bound by the bytes of their row operands, so a row is read once and held
 // on chip.  A row belongs to a team of whole warps; thread i of a team of n owns the
@@ -107,6 +108,12 @@ __device__ __forceinline__ float2 mul(float2 a, float2 b) {
 __device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_bits(a)), "l"(as_bits(b)), "l"(as_bits(c)));
+  return as_pair(r);
+}
+
+__device__ __forceinline__ float2 add(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_bits(a)), "l"(as_bits(b)));
   return as_pair(r);
 }
 

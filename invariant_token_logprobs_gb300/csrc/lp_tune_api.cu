@@ -1,0 +1,152 @@
+// lp_tune_api.cu: the C-ABI front end of the fine-tuning operators (declared in
+// include/lp_tune.h).  As in lp_api.cu, every entry point validates its arguments
+// on the host in the order sizes and null pointers, alignment, workspace, device,
+// and enqueues nothing before all checks pass.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "lp_args.h"
+#include "lp_tune_internal.h"
+
+extern "C" {
+
+lp_status lp_layer_norm(const void* residual, int64_t ld_residual, int residual_dtype,
+                        const void* branch, int64_t ld_branch, int act_dtype, const void* weight,
+                        const void* bias, int weight_dtype, int64_t T, int64_t d, float eps,
+                        void* residual_out, int64_t ld_residual_out, void* normed,
+                        int64_t ld_normed, float* mean, float* rstd, void* stream) {
+  using namespace lp;
+  if (T < 0 || T > kMaxRows || d < 1 || d > kNormMaxDim || !is_dtype(residual_dtype) ||
+      !is_dtype(act_dtype) || !is_dtype(weight_dtype) || !(eps >= 0.0f) || !std::isfinite(eps))
+    return LP_ERR_INVALID_ARGUMENT;
+  if (T == 0) return LP_OK;  // operands without rows may be null
+  if (residual == nullptr || normed == nullptr || mismatch(residual_out, branch != nullptr))
+    return LP_ERR_INVALID_ARGUMENT;
+  if (bad_rows(ld_residual, d) || bad_rows(ld_normed, d) ||
+      (branch != nullptr && (bad_rows(ld_branch, d) || bad_rows(ld_residual_out, d))))
+    return LP_ERR_INVALID_ARGUMENT;
+  const bool rb = residual_dtype == LP_BFLOAT16, ab = act_dtype == LP_BFLOAT16,
+             wb = weight_dtype == LP_BFLOAT16;
+  const int64_t rs = size_of(rb), as = size_of(ab), ws = size_of(wb);
+  const Extent in[4] = {extent(residual, T, ld_residual, d, rs), extent(branch, T, ld_branch, d, as),
+                        extent(weight, 1, d, d, ws), extent(bias, 1, d, d, ws)};
+  const Extent out[4] = {extent(residual_out, T, ld_residual_out, d, rs),
+                         extent(normed, T, ld_normed, d, as), extent(mean, T, 1, 1, 4),
+                         extent(rstd, T, 1, 1, 4)};
+  const bool in_place = residual_out == residual && ld_residual_out == ld_residual;
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(out[i], in[j]) && !(i == 0 && j == 0 && in_place)) return LP_ERR_INVALID_ARGUMENT;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return LP_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(residual, rs) || !aligned(residual_out, rs) || !aligned(branch, as) ||
+      !aligned(normed, as) || !aligned(weight, ws) || !aligned(bias, ws) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return LP_ERR_MISALIGNED;
+  Device dev;
+  const lp_status st = current_device(&dev);
+  if (st != LP_OK) return st;
+  LayerNormArgs a{};
+  a.residual = {const_cast<void*>(residual), ld_residual};
+  a.branch = {const_cast<void*>(branch), ld_branch};
+  a.weight = weight;
+  a.bias = bias;
+  a.residual_bf16 = rb;
+  a.act_bf16 = ab;
+  a.weight_bf16 = wb;
+  a.T = T;
+  a.d = d;
+  a.eps = eps;
+  a.residual_out = {residual_out, ld_residual_out};
+  a.normed = {normed, ld_normed};
+  a.mean = mean;
+  a.rstd = rstd;
+  return launch_layer_norm(dev, a, static_cast<cudaStream_t>(stream));
+}
+
+size_t lp_layer_norm_backward_workspace_size(int64_t T, int64_t d) {
+  if (T < 0 || T > lp::kMaxRows || d < 1 || d > lp::kNormMaxDim) return 0;
+  return lp::layer_norm_backward_workspace(T, d);
+}
+
+lp_status lp_layer_norm_backward(
+    const void* residual_out, int64_t ld_residual_out, int residual_dtype, int act_dtype,
+    const void* weight, int weight_dtype, int64_t T, int64_t d, const float* mean,
+    const float* rstd, const void* grad_normed, int64_t ld_grad_normed,
+    const void* grad_residual_out, int64_t ld_grad_residual_out, void* grad_residual,
+    int64_t ld_grad_residual, void* grad_branch, int64_t ld_grad_branch, float* grad_weight,
+    float* grad_bias, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace lp;
+  if (T < 0 || T > kMaxRows || d < 1 || d > kNormMaxDim || !is_dtype(residual_dtype) ||
+      !is_dtype(act_dtype) || !is_dtype(weight_dtype))
+    return LP_ERR_INVALID_ARGUMENT;
+  const bool sums = grad_weight != nullptr || grad_bias != nullptr;
+  if (T == 0 && !sums) return LP_OK;
+  if (sums && workspace == nullptr) return LP_ERR_INVALID_ARGUMENT;
+  if (T > 0) {  // operands without rows may be null
+    if (residual_out == nullptr || mean == nullptr || rstd == nullptr || grad_normed == nullptr ||
+        grad_residual == nullptr)
+      return LP_ERR_INVALID_ARGUMENT;
+    if (bad_rows(ld_residual_out, d) || bad_rows(ld_grad_normed, d) ||
+        bad_rows(ld_grad_residual, d) ||
+        (grad_residual_out != nullptr && bad_rows(ld_grad_residual_out, d)) ||
+        (grad_branch != nullptr && bad_rows(ld_grad_branch, d)))
+      return LP_ERR_INVALID_ARGUMENT;
+  }
+  const bool rb = residual_dtype == LP_BFLOAT16, ab = act_dtype == LP_BFLOAT16,
+             wb = weight_dtype == LP_BFLOAT16;
+  const int64_t rs = size_of(rb), as = size_of(ab), ws = size_of(wb);
+  const Extent in[6] = {extent(residual_out, T, ld_residual_out, d, rs),
+                        extent(weight, 1, d, d, ws),
+                        extent(mean, T, 1, 1, 4),
+                        extent(rstd, T, 1, 1, 4),
+                        extent(grad_normed, T, ld_grad_normed, d, as),
+                        extent(grad_residual_out, T, ld_grad_residual_out, d, rs)};
+  const Extent out[5] = {extent(grad_residual, T, ld_grad_residual, d, rs),
+                         extent(grad_branch, T, ld_grad_branch, d, as),
+                         extent(grad_weight, 1, d, d, 4), extent(grad_bias, 1, d, d, 4),
+                         extent(sums ? workspace : nullptr, 1, 0,
+                                static_cast<int64_t>(layer_norm_backward_workspace(T, d)), 1)};
+  const bool in_place =
+      grad_residual == grad_residual_out && ld_grad_residual == ld_grad_residual_out;
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (overlap(out[i], in[j]) && !(i == 0 && j == 5 && in_place)) return LP_ERR_INVALID_ARGUMENT;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return LP_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(residual_out, rs) || !aligned(grad_residual_out, rs) ||
+      !aligned(grad_residual, rs) || !aligned(grad_normed, as) || !aligned(grad_branch, as) ||
+      !aligned(weight, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(grad_weight, 4) ||
+      !aligned(grad_bias, 4) || (sums && !aligned(workspace, 256)))
+    return LP_ERR_MISALIGNED;
+  if (sums && workspace_bytes < layer_norm_backward_workspace(T, d))
+    return LP_ERR_WORKSPACE_TOO_SMALL;
+  Device dev;
+  const lp_status st = current_device(&dev);
+  if (st != LP_OK) return st;
+  LayerNormGradArgs a{};
+  a.residual_out = {const_cast<void*>(residual_out), ld_residual_out};
+  a.weight = weight;
+  a.residual_bf16 = rb;
+  a.act_bf16 = ab;
+  a.weight_bf16 = wb;
+  a.T = T;
+  a.d = d;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.grad_normed = {const_cast<void*>(grad_normed), ld_grad_normed};
+  a.grad_residual_out = {const_cast<void*>(grad_residual_out), ld_grad_residual_out};
+  a.grad_residual = {grad_residual, ld_grad_residual};
+  a.grad_branch = {grad_branch, ld_grad_branch};
+  a.grad_weight = grad_weight;
+  a.grad_bias = grad_bias;
+  a.partials = sums ? static_cast<float*>(workspace) : nullptr;
+  return launch_layer_norm_backward(dev, a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
