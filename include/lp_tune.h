@@ -97,6 +97,67 @@ LP_API lp_status lp_layer_norm_backward(
     int64_t ld_grad_residual, void* grad_branch, int64_t ld_grad_branch, float* grad_weight,
     float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Preference loss.  Sequence i has the rows [cu_seqlens[i], cu_seqlens[i + 1]),
+ * of which those count whose mask is not zero, n_i of them.  Its score is
+ *
+ *     s_i = sum over its counted rows of (logp - ref_logp)      (divided by n_i with `average`)
+ *
+ * and a pair of a chosen sequence c and a rejected one r, which counts when both
+ * have a counted row, has z = beta (s_c - s_r) - margin and the loss
+ *
+ *     SIGMOID  (1 - e) log(1 + exp(-z)) + e log(1 + exp(z)),  e = label_smoothing
+ *     HINGE    max(0, 1 - z)
+ *     SQUARE   ((z - 1/2) / beta)^2
+ *
+ * plus nll_coef times the chosen sequence's mean of -logp.  The call's loss is
+ * the mean over the counted pairs; without one everything is 0.  Rows that do
+ * not count have no gradient whatever they hold (their logp is NaN where the
+ * target is padding), and neither do the rows of pairs that do not count.
+ *
+ * A sequence's sums are held to 48 bits or more and everything of a pair in
+ * float64 (the exponential in float32), each output rounded once: differences
+ * of sums of 10^5 rows keep float32's precision.  The sums are taken in a fixed
+ * order.
+ * ------------------------------------------------------------------------ */
+
+typedef enum lp_preference {
+  LP_PREFERENCE_SIGMOID = 0,
+  LP_PREFERENCE_HINGE = 1,
+  LP_PREFERENCE_SQUARE = 2
+} lp_preference;
+
+/* Workspace bytes of lp_preference_loss for T rows in n_sequences; 0 for invalid sizes. */
+LP_API size_t lp_preference_loss_workspace_size(int64_t T, int64_t n_sequences);
+
+/*
+ * lp_preference_loss:
+ *   logp            [T] float32.
+ *   ref_logp        [T] float32, or NULL (zero: no reference).
+ *   mask            [T] bytes (0: the row does not count), or NULL (all count).
+ *   cu_seqlens      [n_sequences + 1] int64 ascending row offsets; rows in no sequence
+ *                   do not count.
+ *   n_sequences     even.  Pair i is of the sequences 2 i (chosen) and 2 i + 1
+ *                   (rejected), or with `halves` of i and i + n_sequences / 2.
+ *   kind            an lp_preference.
+ *   beta > 0, margin, 0 <= label_smoothing <= 1 (0 unless SIGMOID), nll_coef: finite;
+ *                   with an nll_coef of 0 the term is in the stats alone, whatever it holds.
+ *   stats           [6] float32: the loss, and the means over the counted pairs of the
+ *                   loss without the nll term, of the chosen's -logp, of s_c > s_r, and of
+ *                   beta s_c and beta s_r.
+ *   rewards         [n_sequences] float32: beta s_i, 0 for a sequence without a counted row.
+ *   grad_logp       [T] float32, d loss / d logp.
+ *   workspace       256-byte aligned, lp_preference_loss_workspace_size(T, n_sequences)
+ *                   bytes; its contents on entry do not matter.
+ * 0 <= T < 2^31, 0 <= n_sequences < 2^31.
+ */
+LP_API lp_status lp_preference_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
+                                    const int64_t* cu_seqlens, int64_t T, int64_t n_sequences,
+                                    int kind, int average, int halves, double beta, double margin,
+                                    double label_smoothing, double nll_coef, float* stats,
+                                    float* rewards, float* grad_logp, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,14 +8,15 @@ training-step operators.
     h, residual   = residual_norm(residual, branch, weight=..., branch_weight=..., gate=...)
     loss, stats   = policy_loss(logp, old_logp, advantages, entropy=entropy, ...)
     h, residual   = layer_norm(residual, branch, weight=..., bias=...)
+    loss, stats, rewards = preference_loss(logp, cu_seqlens, ref_logp=..., ...)
 
 The first four return the selected-token log-probabilities and entropies of
 z = H W^T / tau (lp_linear_logprob_lse) and back-propagate into H and W through
 lp_linear_logprob_backward with the forward's log Z and entropy kept, so the
 backward does not recompute them.  The next two are train.residual_norm and
-train.policy_loss, on either side of them in a training step, and the last tune's.  This is argument marshalling only: the
+train.policy_loss, on either side of them in a training step, and the last two tune's.  This is argument marshalling only: the
 computation runs in liblp's kernels, on the current stream; torch casts
-gradients, and scales those that the policy loss has written by the loss's own.
+gradients, and scales those that a loss has written by its own.
 
 The vocabulary-parallel forms run on every rank of a torch.distributed group
 (1, 2 or 4 ranks, rank r holding shard r of W's rows or of the logits'
@@ -328,3 +329,26 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
         return train._on_stream(stream, logp, policy_loss, logp, old_logp, advantages,
                                 entropy=entropy, **kw)
     return _PolicyLoss.apply(logp, entropy, old_logp, advantages, kw)
+
+
+class _PreferenceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, cu_seqlens, kw):
+        out = tune.preference_loss(logp, cu_seqlens, **kw)
+        ctx.save_for_backward(out.grad_logp)
+        ctx.mark_non_differentiable(out.stats, out.rewards)
+        return out.stats[0].clone(), out.stats, out.rewards
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, g_loss, *_):
+        return ctx.saved_tensors[0] * g_loss, None, None
+
+
+def preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, *, stream=None, **kw):
+    """(loss, stats [6], rewards [n]) of tune.preference_loss, the loss a float32 scalar that is
+    differentiable in logp: the gradient is written by the forward call and scaled in the backward.
+    Keyword arguments are tune.preference_loss's; a stream is treated as policy_loss does."""
+    if stream is not None:
+        return train._on_stream(stream, logp, preference_loss, logp, cu_seqlens, **kw)
+    return _PreferenceLoss.apply(logp, cu_seqlens, kw)

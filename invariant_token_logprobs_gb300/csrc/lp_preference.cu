@@ -1,0 +1,527 @@
+// lp_preference.cu: the preference loss of pairs of sequences and its gradient (include/lp_tune.h).
+//
+// A row's gradient needs its pair's loss, which needs the sums of two whole sequences, and the number
+// of pairs that count.  Up to kSmallRows rows one CTA does all of it in one launch.  Beyond that there
+// are three launches, each a programmatic dependent of the one before:
+//   sums   a warp takes kChunk neighbouring rows, however they lie in sequences, and writes a sum for
+//          each sequence that it meets: long sequences are split over many warps, short ones share one;
+//   pairs  a few lanes a pair add its sequences' sums and write its loss and both gradients;
+//   rows   as in the first, a warp takes kChunk rows and writes their gradients.
+// Bound by HBM: 9 bytes a row in, the mask again and 4 bytes out.
+//
+// The difference of two sums of 10^5 rows is what counts, to a few units of float32: a lane's sums
+// are float pairs (Knuth's two-sum), everything past the lane is float64.  Every sum is taken in a
+// fixed order: a lane's rows, the lanes' tree, the chunks of a sequence in order.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "lp_check.cuh"
+#include "lp_tune_internal.h"
+
+namespace lp {
+namespace {
+
+// ---- one CTA
+constexpr int kSmallThreads = 1024;
+constexpr int64_t kSmallRows = 8192;
+constexpr int kSmallSequences = 64;  // a lane of one warp for each pair
+
+// ---- three launches
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = 4;                // of 4 rows, a lane
+constexpr int kChunk = kGroups * 4 * 32;  // rows of a warp
+constexpr int kPairThreads = 64;
+
+// A sequence's sums over its counted rows, whole or of one chunk.
+struct Sums {
+  double logp, ref;
+  int64_t count;
+};
+// What a CTA of the pairs' kernel adds to the call's sums.
+struct Part {
+  double loss, nll, right, chosen, rejected;
+  int64_t count;
+};
+
+// s + e is the sum of float32 values to about 48 bits; once s is no number or infinite, e is nothing.
+struct Two {
+  float s = 0.f, e = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b);
+    s = t;
+  }
+  __device__ __forceinline__ double value() const {
+    return fabsf(s) <= 0x1.fffffep127f ? double(s) + double(e) : double(s);
+  }
+};
+
+template <int kLanes>
+__device__ __forceinline__ double lane_sum(double v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double sum_over(double v, int lanes) {
+  for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int64_t sum_over(int64_t v, int lanes) {
+  for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The sequences of pair i.
+__device__ __forceinline__ int64_t chosen_of(const PreferenceArgs& a, int64_t i) {
+  return a.halves ? i : 2 * i;
+}
+__device__ __forceinline__ int64_t rejected_of(const PreferenceArgs& a, int64_t i) {
+  return a.halves ? i + a.n_sequences / 2 : 2 * i + 1;
+}
+// An offset, whatever it holds, as a row of the call.
+__device__ __forceinline__ int64_t row_of(const PreferenceArgs& a, int64_t i) {
+  if (!LP_CHECK(i >= 0 && i <= a.n_sequences, kChkRowIndex)) return 0;
+  return min(max(__ldg(a.cu_seqlens + i), int64_t(0)), a.T);
+}
+
+struct Pair {
+  Part part;               // the pair's, all zeros when it does not count
+  double chosen, rejected; // d loss / d logp of a counted row, times the number of pairs
+  float reward[2];
+};
+__device__ __forceinline__ double score_of(const PreferenceArgs& a, const Sums& s) {
+  const double v = a.ref_logp != nullptr ? s.logp - s.ref : s.logp;
+  return a.average && s.count > 0 ? v / double(s.count) : v;
+}
+__device__ __forceinline__ Pair pair_of(const PreferenceArgs& a, const Sums& c, const Sums& r) {
+  Pair p{};
+  const double sc = score_of(a, c), sr = score_of(a, r);
+  p.reward[0] = float(a.beta * sc);
+  p.reward[1] = float(a.beta * sr);
+  if (c.count == 0 || r.count == 0) return p;
+  const double z = a.beta * (sc - sr) - a.margin;
+  double slope;
+  if (a.kind == LP_PREFERENCE_SIGMOID) {
+    // exp(-|z|) by float32's, of z's leading part, with the rest to first order: the float64 one
+    // takes hundreds of instructions at 1/64 of the rate
+    const double m = fabs(z);
+    const float high = float(m), low = high <= 0x1.fffffep127f ? float(m - double(high)) : 0.f;
+    const float e = expf(-high), small = e - e * low;
+    const float log_part = log1pf(small), near = 1.f / (1.f + small), far = small * near;
+    // softplus(-z), softplus(z), and their derivatives' sizes
+    const double down = z > 0 ? double(log_part) : m + double(log_part);
+    const double up = z > 0 ? m + double(log_part) : double(log_part);
+    const double to_down = z > 0 ? far : near, to_up = z > 0 ? near : far;
+    p.part.loss = (1.0 - a.smoothing) * down;
+    slope = -(1.0 - a.smoothing) * to_down;
+    if (a.smoothing != 0.0) {  // an infinite term without a weight is none
+      p.part.loss += a.smoothing * up;
+      slope += a.smoothing * to_up;
+    }
+    if (z != z) p.part.loss = slope = z;
+  } else if (a.kind == LP_PREFERENCE_HINGE) {
+    p.part.loss = z < 1.0 ? 1.0 - z : z != z ? z : 0.0;
+    slope = z < 1.0 ? -1.0 : z != z ? z : 0.0;
+  } else {
+    const double off = (z - 0.5) * a.inverse_beta;
+    p.part.loss = off * off;
+    slope = 2.0 * off * a.inverse_beta;
+  }
+  slope *= a.beta;
+  p.part.nll = -c.logp / double(c.count);
+  p.part.right = sc > sr ? 1.0 : 0.0;
+  p.part.chosen = a.beta * sc;
+  p.part.rejected = a.beta * sr;
+  p.part.count = 1;
+  p.chosen = a.average ? slope / double(c.count) : slope;
+  p.rejected = a.average ? -slope / double(r.count) : -slope;
+  if (a.nll_coef != 0.0) p.chosen -= a.nll_coef / double(c.count);
+  return p;
+}
+__device__ __forceinline__ void write_stats(const PreferenceArgs& a, const Part& s) {
+  const double w = s.count > 0 ? 1.0 / double(s.count) : 0.0;
+  // a likelihood term with a coefficient of 0 is watched only
+  a.stats[0] = float((a.nll_coef != 0.0 ? s.loss + a.nll_coef * s.nll : s.loss) * w);
+  a.stats[1] = float(s.loss * w);
+  a.stats[2] = float(s.nll * w);
+  a.stats[3] = float(s.right * w);
+  a.stats[4] = float(s.chosen * w);
+  a.stats[5] = float(s.rejected * w);
+}
+__device__ __forceinline__ Part sum_parts(Part s, int lanes) {
+  s.loss = sum_over(s.loss, lanes);
+  s.nll = sum_over(s.nll, lanes);
+  s.right = sum_over(s.right, lanes);
+  s.chosen = sum_over(s.chosen, lanes);
+  s.rejected = sum_over(s.rejected, lanes);
+  s.count = sum_over(s.count, lanes);
+  return s;
+}
+
+// A few rows: a team of warps a sequence, a lane a pair.
+__global__ void __launch_bounds__(kSmallThreads)
+    lp_preference_small_kernel(const __grid_constant__ PreferenceArgs a, int team) {
+  __shared__ Sums parts[kSmallThreads / 32];
+  __shared__ Sums sums[kSmallSequences];
+  __shared__ double slopes[kSmallSequences];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const int n = int(a.n_sequences), teams = warps / team, mine = warp / team;
+  const int first = int(threadIdx.x) - mine * team * 32, stride = team * 32;
+  const int from = n > 0 ? int(row_of(a, 0)) : 0, to = n > 0 ? int(row_of(a, n)) : 0;
+  for (int i0 = 0; i0 < n; i0 += teams) {
+    const int i = i0 + mine;
+    Two logp, ref;
+    int64_t count = 0;
+    if (mine < teams && i < n) {
+      const int end = int(row_of(a, i + 1));
+      for (int t = int(row_of(a, i)) + first; t < end; t += stride) {
+        if (!LP_CHECK(t >= 0 && t < a.T, kChkRowIndex)) break;
+        if (a.mask != nullptr && a.mask[t] == 0) continue;
+        logp.add(a.logp[t]);
+        if (a.ref_logp != nullptr) ref.add(a.ref_logp[t]);
+        ++count;
+      }
+    }
+    const Sums s = {lane_sum<32>(logp.value()), lane_sum<32>(ref.value()), sum_over(count, 32)};
+    if (lane == 0) parts[warp] = s;
+    __syncthreads();
+    if (int(threadIdx.x) < teams && i0 + int(threadIdx.x) < n) {
+      Sums whole = parts[threadIdx.x * team];
+      for (int k = 1; k < team; ++k) {
+        const Sums& p = parts[threadIdx.x * team + k];
+        whole.logp += p.logp, whole.ref += p.ref, whole.count += p.count;
+      }
+      if (LP_CHECK(i0 + int(threadIdx.x) < kSmallSequences, kChkStateIndex)) sums[i0 + threadIdx.x] = whole;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    Pair p{};
+    const int64_t c = chosen_of(a, lane), r = rejected_of(a, lane);
+    if (2 * lane < n) {
+      p = pair_of(a, sums[c], sums[r]);
+      a.rewards[c] = p.reward[0];
+      a.rewards[r] = p.reward[1];
+    }
+    const Part whole = sum_parts(p.part, 32);
+    const double w = whole.count > 0 ? 1.0 / double(whole.count) : 0.0;
+    if (2 * lane < n) slopes[c] = p.chosen * w, slopes[r] = p.rejected * w;
+    if (lane == 0) write_stats(a, whole);
+  }
+  __syncthreads();
+  for (int i = mine; mine < teams && i < n; i += teams) {
+    const float g = float(slopes[i]);
+    const int end = int(row_of(a, i + 1));
+    for (int t = int(row_of(a, i)) + first; t < end; t += stride)
+      if (LP_CHECK(t >= 0 && t < a.T, kChkRowIndex))
+        a.grad_logp[t] = a.mask == nullptr || a.mask[t] != 0 ? g : 0.f;
+  }
+  for (int t = threadIdx.x; t < int(a.T); t += blockDim.x)  // rows in no sequence
+    if (t < from || t >= to) a.grad_logp[t] = 0.f;
+}
+
+// The first of n ascending offsets that is above t, in [0, n], by a whole warp: 32 probes a step.
+__device__ __forceinline__ int64_t warp_upper_bound(const int64_t* offsets, int64_t n, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = n;  // the answer is in [lo, hi]
+  while (lo < hi) {
+    const int64_t stride = (hi - lo + 31) / 32;
+    const int64_t at = lo + lane * stride;
+    const bool below = at < hi && __ldg(offsets + at) <= t;
+    const int k = __popc(__ballot_sync(0xffffffffu, below));  // the probes below t come first
+    if (k == 0) return lo;
+    hi = min(hi, lo + k * stride);
+    lo += (k - 1) * stride + 1;
+  }
+  return lo;
+}
+
+// Four values of an operand; rows from T on read as zero.
+__device__ __forceinline__ void load4(const float* p, int64_t t, int64_t T, bool wide, float (&v)[4]) {
+  if (wide && t + 4 <= T) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p + t));
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = t + j < T ? p[t + j] : 0.f;
+}
+// Bit j: row t + j counts by the mask.
+__device__ __forceinline__ unsigned load_mask4(const uint8_t* mask, int64_t t, int64_t T, bool wide) {
+  const unsigned inside = t + 4 <= T ? 0xfu : t < T ? (1u << (T - t)) - 1u : 0u;
+  if (mask == nullptr) return inside;
+  unsigned kept = 0;
+  if (wide && inside == 0xfu) {
+    const uchar4 m = __ldg(reinterpret_cast<const uchar4*>(mask + t));
+    kept = (m.x ? 1u : 0u) | (m.y ? 2u : 0u) | (m.z ? 4u : 0u) | (m.w ? 8u : 0u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (inside >> j & 1u) kept |= mask[t + j] != 0 ? 1u << j : 0u;
+  }
+  return kept;
+}
+
+// Calls f(i, lo, hi) for every sequence i that has rows [lo, hi) in [t0, t1), in order; all of a warp
+// together.
+template <class F>
+__device__ __forceinline__ void for_sequences(const PreferenceArgs& a, int64_t t0, int64_t t1, F&& f) {
+  const int lane = threadIdx.x & 31;
+  int64_t i = warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, t0);
+  while (i < a.n_sequences) {
+    // 32 sequences' offsets at once
+    const int64_t mine = i + lane;
+    int64_t begin = a.T, end = a.T;
+    if (mine < a.n_sequences) begin = row_of(a, mine), end = row_of(a, mine + 1);
+    const int lo = int(max(begin, t0) - t0), hi = int(min(end, t1) - t0);
+    unsigned some = __ballot_sync(0xffffffffu, mine < a.n_sequences && begin < t1 && lo < hi);
+    const bool more = __all_sync(0xffffffffu, mine < a.n_sequences && end < t1);
+    for (; some != 0; some &= some - 1) {
+      const int k = __ffs(some) - 1;
+      f(i + k, __shfl_sync(0xffffffffu, lo, k), __shfl_sync(0xffffffffu, hi, k));
+    }
+    if (!more) return;
+    i += 32;
+  }
+}
+
+// The place of a sequence's sums over a chunk: both go up along the rows, so no two meet.
+__device__ __forceinline__ int64_t slot_of(int64_t chunk, int64_t sequence) { return chunk + sequence; }
+
+__global__ void __launch_bounds__(kThreads)
+    lp_preference_sums_kernel(const __grid_constant__ PreferenceArgs a, Sums* slots, int64_t n_slots) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t chunk = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
+  const int64_t t0 = chunk * kChunk, t1 = min(t0 + kChunk, a.T);
+  if (t0 >= a.T) return;
+  float logp[kGroups][4], ref[kGroups][4];
+  unsigned kept[kGroups];
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const int64_t t = t0 + 128 * k + 4 * lane;
+    if (!LP_CHECK(t >= 0, kChkRowIndex)) return;
+    load4(a.logp, t, a.T, a.wide, logp[k]);
+    if (a.ref_logp != nullptr) load4(a.ref_logp, t, a.T, a.wide, ref[k]);
+    kept[k] = load_mask4(a.mask, t, a.T, a.wide);
+  }
+  for_sequences(a, t0, t1, [&](int64_t i, int lo, int hi) {
+    Two x, y;
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      if (128 * (k + 1) <= lo || 128 * k >= hi) continue;  // the same for the warp
+      const int r = 128 * k + 4 * lane;
+      unsigned in = kept[k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r + j < lo || r + j >= hi) in &= ~(1u << j);
+      count += __popc(in);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x.add(in >> j & 1u ? logp[k][j] : 0.f);
+        if (a.ref_logp != nullptr) y.add(in >> j & 1u ? ref[k][j] : 0.f);
+      }
+    }
+    Sums s;
+    s.logp = lane_sum<32>(x.value());
+    s.ref = a.ref_logp != nullptr ? lane_sum<32>(y.value()) : 0.0;
+    s.count = __reduce_add_sync(0xffffffffu, count);
+    const int64_t at = slot_of(chunk, i);
+    if (lane == 0 && LP_CHECK(at >= 0 && at < n_slots, kChkStateIndex)) slots[at] = s;
+  });
+}
+
+// `lanes` lanes a pair (a power of two).
+__global__ void __launch_bounds__(kPairThreads)
+    lp_preference_pairs_kernel(const __grid_constant__ PreferenceArgs a, const Sums* slots, int64_t n_slots,
+                               int lanes, double* slopes, Part* parts) {
+  __shared__ Part of_warp[kPairThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int sub = int(threadIdx.x) % lanes;
+  const int64_t pair = (int64_t(blockIdx.x) * kPairThreads + threadIdx.x) / lanes;
+  const bool there = 2 * pair < a.n_sequences;
+  const int64_t both[2] = {chosen_of(a, pair), rejected_of(a, pair)};
+  int64_t begin[2] = {0, 0}, end[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (there) begin[k] = row_of(a, both[k]), end[k] = row_of(a, both[k] + 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are done
+  Sums sums[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    Sums s{};
+    if (begin[k] < end[k])
+#pragma unroll 4
+      for (int64_t c = begin[k] / kChunk + sub; c <= (end[k] - 1) / kChunk; c += lanes) {
+        const int64_t at = slot_of(c, both[k]);
+        if (!LP_CHECK(at >= 0 && at < n_slots, kChkStateIndex)) break;
+        s.logp += __ldcg(&slots[at].logp);
+        s.ref += __ldcg(&slots[at].ref);
+        s.count += __ldcg(reinterpret_cast<const long long*>(&slots[at].count));
+      }
+    sums[k] = {sum_over(s.logp, lanes), sum_over(s.ref, lanes), sum_over(s.count, lanes)};
+  }
+  Pair p{};
+  if (there && sub == 0) {
+    p = pair_of(a, sums[0], sums[1]);
+    if (LP_CHECK(both[0] < a.n_sequences && both[1] < a.n_sequences, kChkRowIndex)) {
+      a.rewards[both[0]] = p.reward[0];
+      a.rewards[both[1]] = p.reward[1];
+      slopes[both[0]] = p.chosen;
+      slopes[both[1]] = p.rejected;
+    }
+  }
+  const Part s = sum_parts(p.part, 32);
+  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x / 32] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  Part whole = of_warp[0];
+#pragma unroll
+  for (int k = 1; k < kPairThreads / 32; ++k) {
+    const Part& o = of_warp[k];
+    whole.loss += o.loss, whole.nll += o.nll, whole.right += o.right, whole.chosen += o.chosen;
+    whole.rejected += o.rejected, whole.count += o.count;
+  }
+  parts[blockIdx.x] = whole;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    lp_preference_rows_kernel(const __grid_constant__ PreferenceArgs a, const double* slopes, const Part* parts,
+                              int64_t n_parts) {
+  __shared__ int64_t counts[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int64_t t0 = (int64_t(blockIdx.x) * kWarps + warp) * kChunk, t1 = min(t0 + kChunk, a.T);
+  unsigned kept[kGroups];
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) kept[k] = load_mask4(a.mask, t0 + 128 * k + 4 * lane, a.T, a.wide);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pairs are done
+  int64_t count = 0;
+  for (int64_t i = threadIdx.x; i < n_parts; i += kThreads)
+    count += __ldcg(reinterpret_cast<const long long*>(&parts[i].count));
+  count = sum_over(count, 32);
+  if (lane == 0) counts[warp] = count;
+  __syncthreads();
+  count = 0;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) count += counts[k];
+  if (blockIdx.x == 0 && warp == 0) {
+    Part s{};
+    for (int64_t i = lane; i < n_parts; i += 32) {
+      s.loss += __ldcg(&parts[i].loss), s.nll += __ldcg(&parts[i].nll);
+      s.right += __ldcg(&parts[i].right), s.chosen += __ldcg(&parts[i].chosen);
+      s.rejected += __ldcg(&parts[i].rejected);
+    }
+    s = sum_parts(s, 32);
+    s.count = count;
+    if (lane == 0) write_stats(a, s);
+  }
+  if (t0 >= a.T) return;
+  const double w = count > 0 ? 1.0 / double(count) : 0.0;
+  float g[kGroups][4] = {};  // rows in no sequence have none
+  for_sequences(a, t0, t1, [&](int64_t i, int lo, int hi) {
+    if (!LP_CHECK(i >= 0 && i < a.n_sequences, kChkStateIndex)) return;
+    const float slope = float(__ldcg(slopes + i) * w);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      if (128 * (k + 1) <= lo || 128 * k >= hi) continue;  // the same for the warp
+      const int r = 128 * k + 4 * lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r + j >= lo && r + j < hi) g[k][j] = kept[k] >> j & 1u ? slope : 0.f;
+    }
+  });
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const int64_t t = t0 + 128 * k + 4 * lane;
+    if (!LP_CHECK(t >= 0, kChkRowIndex)) return;
+    if (a.wide && t + 4 <= a.T) {
+      *reinterpret_cast<float4*>(a.grad_logp + t) = make_float4(g[k][0], g[k][1], g[k][2], g[k][3]);
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t + j < a.T) a.grad_logp[t + j] = g[k][j];
+  }
+}
+
+bool one_cta(int64_t T, int64_t n) { return T <= kSmallRows && n <= kSmallSequences; }
+
+// The workspace of the three launches.
+struct Layout {
+  int64_t chunks, slots, parts;
+  int lanes;
+  size_t slopes_at, parts_at, bytes;
+};
+Layout layout_of(int64_t T, int64_t n) {
+  Layout l;
+  l.chunks = (T + kChunk - 1) / kChunk;
+  l.slots = l.chunks + n;
+  // lanes of a pair: about four chunks each of a sequence of the mean length
+  const int64_t pieces = T / (kChunk * std::max<int64_t>(n, 1)) + 1;
+  l.lanes = 1;
+  while (l.lanes < 32 && l.lanes * 4 < pieces) l.lanes *= 2;
+  l.parts = (n / 2 * l.lanes + kPairThreads - 1) / kPairThreads;
+  const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  l.slopes_at = up(size_t(l.slots) * sizeof(Sums));
+  l.parts_at = l.slopes_at + up(size_t(n) * sizeof(double));
+  l.bytes = l.parts_at + up(size_t(l.parts) * sizeof(Part));
+  return l;
+}
+
+template <class... Params, class... Args>
+bool launch_dependent(void (*kernel)(Params...), int64_t blocks, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+}  // namespace
+
+size_t preference_loss_workspace(int64_t T, int64_t n_sequences) {
+  return one_cta(T, n_sequences) ? 256 : layout_of(T, n_sequences).bytes;
+}
+
+lp_status launch_preference_loss(const PreferenceArgs& args, cudaStream_t stream) {
+  PreferenceArgs a = args;
+  const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  a.wide = at16(a.logp) && at16(a.ref_logp) && at16(a.grad_logp) &&
+           reinterpret_cast<uintptr_t>(a.mask) % 4 == 0;
+  if (one_cta(a.T, a.n_sequences)) {
+    // as many warps as there are rows for, a power of two of them a sequence
+    int warps = 1, team = 1;
+    while (warps < kSmallThreads / 32 && (warps * 32 < a.T || warps < a.n_sequences)) warps *= 2;
+    while (2 * team * std::max<int64_t>(a.n_sequences, 1) <= warps) team *= 2;
+    lp_preference_small_kernel<<<1, warps * 32, 0, stream>>>(a, std::min(team, warps));
+    return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  }
+  const Layout l = layout_of(a.T, a.n_sequences);
+  char* ws = static_cast<char*>(a.workspace);
+  Sums* slots = reinterpret_cast<Sums*>(ws);
+  double* slopes = reinterpret_cast<double*>(ws + l.slopes_at);
+  Part* parts = reinterpret_cast<Part*>(ws + l.parts_at);
+  const int64_t blocks = std::max<int64_t>(1, (l.chunks + kWarps - 1) / kWarps);
+  lp_preference_sums_kernel<<<unsigned(blocks), kThreads, 0, stream>>>(a, slots, l.slots);
+  if (cudaGetLastError() != cudaSuccess) return LP_ERR_CUDA;
+  if (l.parts > 0 &&
+      !launch_dependent(lp_preference_pairs_kernel, l.parts, kPairThreads, stream, a,
+                        static_cast<const Sums*>(slots), l.slots, l.lanes, slopes, parts))
+    return LP_ERR_CUDA;
+  if (!launch_dependent(lp_preference_rows_kernel, blocks, kThreads, stream, a,
+                        static_cast<const double*>(slopes), static_cast<const Part*>(parts), l.parts))
+    return LP_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+}
+
+cudaError_t take_check_word_preference(uint32_t* out) { return take_check_word(out); }
+
+}  // namespace lp

@@ -149,4 +149,69 @@ lp_status lp_layer_norm_backward(
   return launch_layer_norm_backward(dev, a, static_cast<cudaStream_t>(stream));
 }
 
+size_t lp_preference_loss_workspace_size(int64_t T, int64_t n_sequences) {
+  if (T < 0 || T > lp::kMaxRows || n_sequences < 0 || n_sequences > lp::kMaxRows) return 0;
+  return lp::preference_loss_workspace(T, n_sequences);
+}
+
+lp_status lp_preference_loss(const float* logp, const float* ref_logp, const uint8_t* mask,
+                             const int64_t* cu_seqlens, int64_t T, int64_t n_sequences, int kind,
+                             int average, int halves, double beta, double margin,
+                             double label_smoothing, double nll_coef, float* stats, float* rewards,
+                             float* grad_logp, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  using namespace lp;
+  if (T < 0 || T > kMaxRows || n_sequences < 0 || n_sequences > kMaxRows || n_sequences % 2 != 0)
+    return LP_ERR_INVALID_ARGUMENT;
+  if (kind != LP_PREFERENCE_SIGMOID && kind != LP_PREFERENCE_HINGE && kind != LP_PREFERENCE_SQUARE)
+    return LP_ERR_INVALID_ARGUMENT;
+  if (!(beta > 0.0) || !std::isfinite(beta) || !std::isfinite(1.0 / beta) ||
+      !std::isfinite(margin) || !std::isfinite(nll_coef) ||
+      !(label_smoothing >= 0.0 && label_smoothing <= 1.0) ||
+      (label_smoothing != 0.0 && kind != LP_PREFERENCE_SIGMOID))
+    return LP_ERR_INVALID_ARGUMENT;
+  if (cu_seqlens == nullptr || stats == nullptr || workspace == nullptr ||
+      (n_sequences > 0 && rewards == nullptr) ||
+      (T > 0 && (logp == nullptr || grad_logp == nullptr)))
+    return LP_ERR_INVALID_ARGUMENT;
+  const Extent in[4] = {extent(logp, T, 1, 1, 4), extent(ref_logp, T, 1, 1, 4),
+                        extent(mask, T, 1, 1, 1), extent(cu_seqlens, n_sequences + 1, 1, 1, 8)};
+  const Extent out[4] = {
+      extent(stats, 6, 1, 1, 4), extent(rewards, n_sequences, 1, 1, 4), extent(grad_logp, T, 1, 1, 4),
+      extent(workspace, 1, 0, static_cast<int64_t>(preference_loss_workspace(T, n_sequences)), 1)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(out[i], in[j])) return LP_ERR_INVALID_ARGUMENT;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return LP_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(logp, 4) || !aligned(ref_logp, 4) || !aligned(cu_seqlens, 8) || !aligned(stats, 4) ||
+      !aligned(rewards, 4) || !aligned(grad_logp, 4) || !aligned(workspace, 256))
+    return LP_ERR_MISALIGNED;
+  if (workspace_bytes < preference_loss_workspace(T, n_sequences)) return LP_ERR_WORKSPACE_TOO_SMALL;
+  Device dev;
+  const lp_status st = current_device(&dev);
+  if (st != LP_OK) return st;
+  PreferenceArgs a{};
+  a.logp = logp;
+  a.ref_logp = ref_logp;
+  a.mask = mask;
+  a.cu_seqlens = cu_seqlens;
+  a.T = T;
+  a.n_sequences = n_sequences;
+  a.kind = kind;
+  a.average = average != 0;
+  a.halves = halves != 0;
+  a.beta = beta;
+  a.inverse_beta = 1.0 / beta;
+  a.margin = margin;
+  a.smoothing = label_smoothing;
+  a.nll_coef = nll_coef;
+  a.stats = stats;
+  a.rewards = rewards;
+  a.grad_logp = grad_logp;
+  a.workspace = workspace;
+  return launch_preference_loss(a, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -37,8 +37,26 @@ size_t layer_norm_backward_workspace(int64_t T, int64_t d);
 lp_status launch_layer_norm_backward(const Device& dev, const LayerNormGradArgs& a,
                                      cudaStream_t stream);
 
+// -------------------------------------------------------------- preference loss
+
+struct PreferenceArgs {
+  const float *logp, *ref_logp;  // ref_logp may be null
+  const uint8_t* mask;           // may be null
+  const int64_t* cu_seqlens;
+  int64_t T, n_sequences;
+  int kind;                      // lp_preference
+  bool average, halves;
+  bool wide;                     // set by the launcher: rows may go 16 bytes at a time
+  double beta, inverse_beta, margin, smoothing, nll_coef;
+  float *stats, *rewards, *grad_logp;
+  void* workspace;
+};
+size_t preference_loss_workspace(int64_t T, int64_t n_sequences);
+lp_status launch_preference_loss(const PreferenceArgs& a, cudaStream_t stream);
+
 // Read and clear the check words of these translation units (lp_check.cuh).
 cudaError_t take_check_word_layer_norm(uint32_t* out);
 cudaError_t take_check_word_layer_norm_backward(uint32_t* out);
+cudaError_t take_check_word_preference(uint32_t* out);
 
 }  // namespace lp

@@ -11,6 +11,8 @@ struct EntryPoints {
   decltype(&lp_layer_norm) layer_norm;
   decltype(&lp_layer_norm_backward_workspace_size) norm_workspace;
   decltype(&lp_layer_norm_backward) layer_norm_backward;
+  decltype(&lp_preference_loss_workspace_size) preference_workspace;
+  decltype(&lp_preference_loss) preference_loss;
 } lp;
 
 // The dtype of weight and bias, which is one.
@@ -129,12 +131,59 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// logp, cu_seqlens, ref_logp, mask, kind, average, halves, beta, margin, label_smoothing, nll_coef,
+// workspace
+PyObject* preference_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const at::Tensor& logp = required(v[0], "logp");
+    const at::Tensor& cu_seqlens = required(v[1], "cu_seqlens");
+    const at::Tensor *ref_logp = tensor(v[2], "ref_logp"), *mask = tensor(v[3], "mask"),
+                     *given = tensor(v[11], "workspace");
+    const int kind = int(integer(v[4]));
+    const bool average = truth(v[5]), halves = truth(v[6]);
+    const double beta = number(v[7]), margin = number(v[8]), smoothing = number(v[9]), nll = number(v[10]);
+    if (logp.dim() != 1) value_error("expected a 1-D logp");
+    const c10::Device device = device_of(logp, {&cu_seqlens, ref_logp, mask, given});
+    const c10::cuda::CUDAGuard guard(device);
+    const int64_t T = logp.size(0);
+    vector(&logp, T, "logp");
+    vector(ref_logp, T, "ref_logp");
+    if (mask != nullptr)
+      vector(mask, T, "mask", mask->scalar_type() == at::kByte ? at::kByte : at::kBool);
+    if (cu_seqlens.dim() != 1 || cu_seqlens.size(0) < 1) value_error("cu_seqlens must be a vector of n + 1");
+    const int64_t sequences = cu_seqlens.size(0) - 1;
+    vector(&cu_seqlens, sequences + 1, "cu_seqlens", at::kLong);
+    if (sequences % 2 != 0) value_error("the sequences must be pairs: an even number of them");
+    at::Tensor stats, rewards, grad_logp, workspace;
+    Tensors made(device);
+    made.add(&stats, {6}, at::kFloat);
+    made.add(&rewards, {sequences}, at::kFloat);
+    made.add(&grad_logp, {T}, at::kFloat);
+    size_t bytes;
+    if (given != nullptr) {
+      workspace = *given;
+      bytes = workspace_bytes(*given);
+    } else {
+      bytes = lp.preference_workspace(T, sequences);
+      made.scratch(&workspace, bytes);
+    }
+    made.allocate();
+    check_status("lp_preference_loss",
+                 lp.preference_loss(floats(logp), floats(ref_logp), static_cast<uint8_t*>(data(mask)),
+                                    static_cast<int64_t*>(data(cu_seqlens)), T, sequences, kind, average,
+                                    halves, beta, margin, smoothing, nll, floats(stats), floats(rewards),
+                                    floats(grad_logp), data(workspace), bytes, current_stream(device)));
+    return tuple_of({&stats, &rewards, &grad_logp});
+  });
+}
+
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return bind_table(reinterpret_cast<void**>(&lp), sizeof(lp) / sizeof(void*), v, n);
 }
 PyMethodDef methods[] = {method<bind>("bind"),
                          method<layer_norm>("layer_norm"),
                          method<layer_norm_backward>("layer_norm_backward"),
+                         method<preference_loss>("preference_loss"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tune_calls", nullptr, -1, methods};
 

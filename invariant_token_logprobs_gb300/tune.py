@@ -3,6 +3,7 @@ declared in include/lp_tune.h.
 
     out  = layer_norm(residual, branch, weight=..., bias=...)
     grad = layer_norm_backward(grad_normed, grad_residual, out.residual, out.mean, out.rstd, ...)
+    loss = preference_loss(logp, cu_seqlens, ref_logp=..., mask=...)
 
 As in train.py this is argument marshalling only: every step of the computation runs in liblp's
 kernels on the current stream, there is no fallback, the calls' checks and allocations are compiled
@@ -29,12 +30,15 @@ from .train import _on_stream
 __all__ = [
     "LayerNorm",
     "LayerNormGrad",
+    "PreferenceLoss",
     "declared_symbols",
     "layer_norm",
     "layer_norm_backward",
     "layer_norm_backward_workspace_size",
     "load",
     "load_calls",
+    "preference_loss",
+    "preference_loss_workspace_size",
 ]
 
 HEADER = os.path.join(os.path.dirname(lp.HEADER), "lp_tune.h")
@@ -44,6 +48,7 @@ _int = ctypes.c_int
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 _SIGNATURES = {
     "lp_layer_norm": (
@@ -53,13 +58,18 @@ _SIGNATURES = {
     "lp_layer_norm_backward": (
         _int, [_vp, _i64, _int, _int, _vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp,
                _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "lp_preference_loss_workspace_size": (_sz, [_i64, _i64]),
+    "lp_preference_loss": (
+        _int, [_vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _f64, _f64, _f64, _f64, _vp, _vp,
+               _vp, _vp, _sz, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
 _calls = None
 
 # what tune_calls.cpp calls, in the order of its table
-_BOUND = ("lp_layer_norm", "lp_layer_norm_backward_workspace_size", "lp_layer_norm_backward")
+_BOUND = ("lp_layer_norm", "lp_layer_norm_backward_workspace_size", "lp_layer_norm_backward",
+          "lp_preference_loss_workspace_size", "lp_preference_loss")
 
 
 def declared_symbols() -> list[str]:
@@ -148,3 +158,45 @@ def layer_norm_backward(grad_normed: torch.Tensor, grad_residual: Optional[torch
                           weight_grads=weight_grads, workspace=workspace)
     return LayerNormGrad._make((_calls or load_calls()).layer_norm_backward(
         grad_normed, grad_residual, residual, mean, rstd, weight, bias, branch, weight_grads, workspace))
+
+
+# -------------------------------------------------------------- preference loss
+
+class PreferenceLoss(NamedTuple):
+    stats: torch.Tensor      # [6]: loss, without the nll term, nll, accuracy, chosen's and rejected's reward
+    rewards: torch.Tensor    # [n]: beta times each sequence's score
+    grad_logp: torch.Tensor  # [T]
+
+
+_KINDS = {"sigmoid": 0, "hinge": 1, "square": 2}
+
+
+def preference_loss_workspace_size(T: int, n_sequences: int) -> int:
+    return int(load().lp_preference_loss_workspace_size(T, n_sequences))
+
+
+def preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                    ref_logp: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                    kind: str = "sigmoid", beta: float = 0.1, margin: float = 0.0,
+                    label_smoothing: float = 0.0, average: bool = False, nll_coef: float = 0.0,
+                    halves: bool = False, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> PreferenceLoss:
+    """The loss of pairs of a chosen and a rejected sequence, from the log-probabilities of their
+    tokens, and its gradient with respect to logp.
+
+    cu_seqlens [n + 1] int64 are the row offsets of n sequences; pair i is of the sequences 2 i (chosen)
+    and 2 i + 1 (rejected), or with halves=True of i and i + n / 2.  A sequence's score is the sum over
+    its counted rows (mask [T], bool or uint8) of logp - ref_logp, or their mean with average=True; a
+    pair's z = beta * (the chosen's score - the rejected's) - margin, and its loss by `kind`
+    "sigmoid" log(1 + exp(-z)), with label_smoothing e (1 - e) of it and e of log(1 + exp(z));
+    "hinge" max(0, 1 - z); "square" ((z - 1/2) / beta)^2.  nll_coef times the chosen's mean of -logp is
+    added.  The loss is the mean over the pairs both of whose sequences have a counted row."""
+    if stream is not None:
+        return _on_stream(stream, logp, preference_loss, logp, cu_seqlens, ref_logp=ref_logp, mask=mask,
+                          kind=kind, beta=beta, margin=margin, label_smoothing=label_smoothing,
+                          average=average, nll_coef=nll_coef, halves=halves, workspace=workspace)
+    if kind not in _KINDS:
+        raise ValueError("kind must be 'sigmoid', 'hinge' or 'square'")
+    return PreferenceLoss._make((_calls or load_calls()).preference_loss(
+        logp, cu_seqlens, ref_logp, mask, _KINDS[kind], average, halves, beta, margin, label_smoothing,
+        nll_coef, workspace))
