@@ -158,6 +158,72 @@ LP_API lp_status lp_preference_loss(const float* logp, const float* ref_logp, co
                                     float* rewards, float* grad_logp, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Muon over many matrices.  Per matrix, with gradient g and momentum M:
+ *
+ *     M = momentum M + g;   u = g + momentum M  (nesterov), or u = M
+ *     X = u / (|u| + eps),  |u| the Frobenius norm
+ *     steps times:  X = a X + b (X X^T) X + c (X X^T)^2 X,  a, b, c = 3.4445, -4.7750, 2.0315
+ *     p = p (1 - l weight_decay) - l update_scale X,  l = lr * lr_scale
+ *
+ * which takes the singular values of X towards 1 and leaves its directions.  p and
+ * M are float32; a bfloat16 copy of p is written in the same pass when asked.  The
+ * products are taken on the tensor cores with operands of 22 bits (pairs of
+ * float16) and float32 sums, on the smaller side of the matrix.
+ *
+ * A matrix whose |u| is not finite in float32 (a NaN or an infinity, or squares
+ * past its range) keeps its p, its copy and its M; the others are not touched by it.
+ * ------------------------------------------------------------------------ */
+
+typedef struct lp_muon_tensor {
+  float* param;        /* [rows, cols] float32, contiguous */
+  void* copy;          /* bfloat16 copy of param to write, or NULL */
+  const void* grad;    /* [rows, cols] grad_dtype, contiguous */
+  float* momentum;     /* [rows, cols] float32, contiguous; zero before the first step */
+  int64_t rows, cols;  /* 0 .. 65536 each */
+  float lr_scale;      /* finite, >= 0 */
+  float weight_decay;  /* finite, >= 0 */
+  float update_scale;  /* finite, >= 0: the factor that the shape gives, such as
+                          sqrt(max(1, rows / cols)) or 0.2 sqrt(max(rows, cols)) */
+  int grad_dtype;      /* an lp_dtype */
+} lp_muon_tensor;
+
+/* Bytes of the plan of these matrices; 0 for invalid arguments.  Host function;
+ * `tensors` is host memory. */
+LP_API size_t lp_muon_plan_size(const lp_muon_tensor* tensors, int64_t n_tensors);
+
+/*
+ * lp_muon_plan: lay out the plan of a step over `tensors` (host memory) in `plan_host`
+ * (host memory, 8-byte aligned, lp_muon_plan_size bytes).  Keep it, copy it to
+ * 256-byte aligned device memory once, and pass both to lp_muon_step; lay it out
+ * again when a pointer, shape or factor changes.  Pointers are aligned to their
+ * element; matrices whose pointers are multiples of 16 bytes and whose cols are a
+ * multiple of 4 go 16 bytes at a time, with the same results.  A matrix must not
+ * appear twice, and what a step writes (params, copies, momenta) may not share memory
+ * with another matrix's tensors: a matrix's own are compared here, those of others
+ * are the caller's to keep apart.  Host function.
+ */
+LP_API lp_status lp_muon_plan(const lp_muon_tensor* tensors, int64_t n_tensors, void* plan_host,
+                              size_t plan_bytes);
+
+/* Workspace bytes of lp_muon_step; 0 when plan_host is no plan.  Host function. */
+LP_API size_t lp_muon_workspace_size(const void* plan_host);
+
+/*
+ * lp_muon_step: one step over every matrix of the plan.
+ *   plan_host      host memory, as laid out by lp_muon_plan; read during the call only.
+ *   plan           device memory, 256-byte aligned: its copy.
+ *   lr >= 0, 0 <= momentum < 1, 1e-16 <= eps, all finite; 1 <= steps <= 32.
+ *   workspace      256-byte aligned, lp_muon_workspace_size(plan_host) bytes; its
+ *                  contents on entry do not matter.
+ * lr and momentum are arguments of the launch: a captured call keeps them at every
+ * replay.  If a device-side wait gives up, the params that depend on it are NaN and
+ * lp_get_device_error on the workspace says so.
+ */
+LP_API lp_status lp_muon_step(const void* plan_host, const void* plan, double lr, double momentum,
+                              int nesterov, int steps, double eps, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liblp.so")
 SOURCES = ["lp_api.cu", "lp_logits.cu", "lp_linear.cu", "lp_backward.cu", "lp_train_api.cu",
            "lp_norm.cu", "lp_norm_backward.cu", "lp_policy.cu", "lp_adamw.cu", "lp_tune_api.cu",
-           "lp_layer_norm.cu", "lp_layer_norm_backward.cu", "lp_preference.cu"]
+           "lp_layer_norm.cu", "lp_layer_norm_backward.cu", "lp_preference.cu",
+           "lp_muon.cu"]
 HEADERS = [os.path.join(ROOT, "include", f) for f in ("lp.h", "lp_train.h", "lp_tune.h")] + [
     os.path.join(CSRC, f) for f in ("lp_device.cuh", "lp_internal.h", "lp_tcgen05.cuh",
                                     "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh",

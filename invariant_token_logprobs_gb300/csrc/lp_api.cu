@@ -169,7 +169,8 @@ lp_status lp_get_check_word(uint32_t* word_out) {
        {lp::take_check_word_logits, lp::take_check_word_linear, lp::take_check_word_backward,
         lp::take_check_word_norm, lp::take_check_word_norm_backward, lp::take_check_word_policy,
         lp::take_check_word_adamw, lp::take_check_word_layer_norm,
-        lp::take_check_word_layer_norm_backward, lp::take_check_word_preference}) {
+        lp::take_check_word_layer_norm_backward, lp::take_check_word_preference,
+        lp::take_check_word_muon}) {
     uint32_t word = 0;
     if (take(&word) != cudaSuccess) {
       cudaGetLastError();

@@ -1,0 +1,736 @@
+// lp_muon.cu: one step of Muon over many matrices (include/lp_tune.h).
+//
+// A matrix is taken as X of m <= n, transposed where it is tall.  Every Newton-Schulz step is three
+// products, each one launch over the tiles of all matrices of a batch:
+//     G = X X^T                      symmetric: the tiles on and below the diagonal
+//     P = a I + b G + c G G          symmetric too, from G in the same way
+//     X = P X
+// Operands are pairs of float16, x = hi + lo (22 bits), scaled by 2^14, which holds them inside
+// float16's range: after the division by the Frobenius norm no singular value passes 1.21 (the
+// polynomial's largest value on [0, 1]), so no element of X, G or P passes 3.45.  A product is
+// hi hi + hi lo + lo hi with float32 accumulators (lo lo is 2^-22 of it): three tensor-core
+// products where one of float16 would lose what a step multiplies by 3.4 in the small
+// singular directions, five times over.  (tests/test_gpu_muon.py derives what is left.)
+//
+// The pairs lie in memory as the tensor core reads them from shared memory: blocks of 128 x 64
+// with 128-byte swizzled rows, 16 KB of hi and 16 KB of lo side by side, so a tile is fetched by
+// plain bulk copies, and the same block serves as a K-major operand (G) and as an N-major one (P X).
+//
+// A CTA takes tiles of 128 x 128 in turn: one warp fetches stages of 64 of K (64 KB), one issues the
+// products, hi x [hi; lo] as one of N = 256, then lo x hi onto its second half; four warps take
+// finished accumulators out of tensor memory, two of which alternate.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "lp_check.cuh"
+#include "lp_tcgen05.cuh"
+#include "lp_tune_internal.h"
+
+namespace lp {
+namespace {
+
+using namespace tc;
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScale = 16384.f;           // of the operands
+constexpr float kUnscale = 1.f / kScale;
+
+constexpr int kTile = 128;                  // rows and columns of a tile, rows of a block
+constexpr int kBlockK = 64;                 // columns of a block, K of a stage
+constexpr uint32_t kHalf = kTile * kBlockK * 2;  // bytes of a block's hi (or lo) part
+constexpr uint32_t kBlock = 2 * kHalf;
+constexpr int kStages = 3;
+// K blocks that are summed in tensor memory before the sum is added to the tile's in registers.  The
+// tensor core cuts sums off where an addition would round: over K of 1000 the singular values came
+// out 8e-6 off, five times what float32 products give; in chunks it is what 16 of its steps cut off.
+constexpr int kChunk = 4;
+constexpr uint32_t kStage = 2 * kBlock;
+constexpr int kBars = 2 * kStages + 5;
+constexpr int kSmem = 1024 + kStages * int(kStage) + kBars * 8 + 16;
+constexpr uint32_t kAccumulator = 2 * kTile;     // tensor-memory columns
+constexpr int kNormThreads = 256;
+constexpr int kSplitThreads = 256;
+
+enum Product { kGram, kPoly, kApply };
+
+// A record's buffers in the workspace.
+__device__ __forceinline__ int64_t block_at(int64_t row_block, int64_t col_block, int64_t col_blocks) {
+  return (row_block * col_blocks + col_block) * int64_t(kBlock);
+}
+__host__ __device__ __forceinline__ int64_t padded_to(int64_t v, int64_t by) { return (v + by - 1) / by * by; }
+
+// ------------------------------------------------------------------ momentum, norm, X
+
+__device__ __forceinline__ float grad_at(const MuonRecord& t, int64_t i) {
+  return t.grad_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.grad)[i])
+                     : static_cast<const float*>(t.grad)[i];
+}
+// The new momentum and what is orthogonalised.
+__device__ __forceinline__ float momentum_of(const MuonArgs& a, float g, float m) {
+  return __fmaf_rn(a.momentum, m, g);
+}
+__device__ __forceinline__ float update_of(const MuonArgs& a, float g, float m) {
+  return a.nesterov ? __fmaf_rn(a.momentum, m, g) : m;
+}
+
+// The squares' sum of kMuonPart elements of a matrix.
+__global__ void __launch_bounds__(kNormThreads)
+    lp_muon_norm_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, double* partials, int first) {
+  __shared__ double slots[kNormThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (first && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
+  const MuonUnit u = units[blockIdx.x];
+  if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
+  const MuonRecord& t = a.records[u.tensor];
+  const int64_t n = t.rows * t.cols, from = int64_t(u.part) * kMuonPart, to = min(from + kMuonPart, n);
+  if (!LP_CHECK(from >= 0 && from < n, kChkCopyIndex)) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t i = from + 4 * threadIdx.x; i < to; i += 4 * kNormThreads) {
+    float g[4], m[4];
+    if (t.wide && i + 4 <= to) {
+      const float4 v = *reinterpret_cast<const float4*>(t.momentum + i);
+      m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
+      if (t.grad_bf16) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.grad) + i));
+        g[0] = __uint_as_float(w.x << 16), g[1] = __uint_as_float(w.x & 0xffff0000u);
+        g[2] = __uint_as_float(w.y << 16), g[3] = __uint_as_float(w.y & 0xffff0000u);
+      } else {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + i));
+        g[0] = w.x, g[1] = w.y, g[2] = w.z, g[3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[j] = i + j < to ? grad_at(t, i + j) : 0.f;
+        m[j] = i + j < to ? t.momentum[i + j] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = update_of(a, g[j], momentum_of(a, g[j], m[j]));
+      sum[j] = __fmaf_rn(x, x, sum[j]);
+    }
+  }
+  double s = (double(sum[0]) + double(sum[1])) + (double(sum[2]) + double(sum[3]));
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int k = 1; k < kNormThreads / 32; ++k) s += slots[k];
+  partials[blockIdx.x] = s;
+}
+
+// hi and lo of eight scaled values, as a block holds them.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 two = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    const float2 back = __half22float2(two);
+    const __half2 rest = __floats2half2_rn(v[2 * i] - back.x, v[2 * i + 1] - back.y);
+    h[i] = *reinterpret_cast<const uint32_t*>(&two);
+    l[i] = *reinterpret_cast<const uint32_t*>(&rest);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// Where columns 8 chunk .. 8 chunk + 7 of row r lie in a block's half.
+__device__ __forceinline__ uint32_t chunk_at(int r, int chunk) {
+  return uint32_t(r) * 128u + (uint32_t(chunk ^ (r & 7)) << 4);
+}
+
+// A block of the first X, and the new momentum of its elements.
+__global__ void __launch_bounds__(kSplitThreads)
+    lp_muon_split_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, const double* partials) {
+  __shared__ double slots[kSplitThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const MuonUnit u = units[blockIdx.x];
+  if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
+  const MuonRecord& t = a.records[u.tensor];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  double s = 0.0;
+  for (int64_t k = threadIdx.x; k < t.parts; k += kSplitThreads) s += __ldcg(partials + t.first_part + k);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kSplitThreads / 32; ++k) s += slots[k];
+  const float norm = float(sqrt(s));
+  const bool fine = norm <= 0x1.fffffep127f;
+  if (u.i == 0 && u.j == 0 && threadIdx.x == 0) a.fine[u.tensor] = fine;
+  const float scale = kScale / (norm + a.eps);
+  unsigned char* block = a.workspace + t.x[0] + block_at(u.i, u.j, padded_to(t.n, kTile) / kBlockK);
+  const int64_t r0 = int64_t(u.i) * kTile, c0 = int64_t(u.j) * kBlockK;
+  for (int k = threadIdx.x; k < kTile * (kBlockK / 8); k += kSplitThreads) {
+    // neighbouring threads go along the matrix's rows, which are X's columns where it is tall
+    const int r = t.tall ? k % kTile : k / (kBlockK / 8), chunk = t.tall ? k / kTile : k % (kBlockK / 8);
+    const int64_t row = r0 + r, col = c0 + 8 * chunk;
+    const int left = row < t.m ? int(min(max(t.n - col, int64_t(0)), int64_t(8))) : 0;
+    const int64_t at = t.tall ? col * t.cols + row : row * t.cols + col, step = t.tall ? t.cols : 1;
+    if (!LP_CHECK(left == 0 || (at >= 0 && at + (left - 1) * step < t.rows * t.cols), kChkCopyIndex)) continue;
+    float v[8];
+    if (!t.tall && t.wide && left == 8) {
+      float m[8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 x = *reinterpret_cast<const float4*>(t.momentum + at + 4 * q);
+        m[4 * q] = x.x, m[4 * q + 1] = x.y, m[4 * q + 2] = x.z, m[4 * q + 3] = x.w;
+        if (t.grad_bf16) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.grad) + at + 4 * q));
+          v[4 * q] = __uint_as_float(w.x << 16), v[4 * q + 1] = __uint_as_float(w.x & 0xffff0000u);
+          v[4 * q + 2] = __uint_as_float(w.y << 16), v[4 * q + 3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + at + 4 * q));
+          v[4 * q] = w.x, v[4 * q + 1] = w.y, v[4 * q + 2] = w.z, v[4 * q + 3] = w.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = momentum_of(a, v[j], m[j]);
+        v[j] = update_of(a, v[j], m[j]) * scale;
+      }
+      if (fine)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<float4*>(t.momentum + at + 4 * q) =
+              make_float4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = 0.f;
+        if (j >= left) continue;
+        const float g = grad_at(t, at + j * step), m = momentum_of(a, g, t.momentum[at + j * step]);
+        if (fine) t.momentum[at + j * step] = m;
+        v[j] = update_of(a, g, m) * scale;
+      }
+    }
+    if (!fine)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    *reinterpret_cast<uint4*>(block + chunk_at(r, chunk)) = hi;
+    *reinterpret_cast<uint4*>(block + kHalf + chunk_at(r, chunk)) = lo;
+  }
+}
+
+// ------------------------------------------------------------------------- products
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// kind::f16 with float16 operands and float32 accumulators, M = 128.
+__host__ __device__ constexpr uint32_t idesc_half(bool b_mn, int n) {
+  return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+}
+
+// 32 consecutive columns of this thread's tensor-memory lane, from two places.
+__device__ __forceinline__ void tmem_load32x2(uint32_t at0, uint32_t at1, float (&v)[32], float (&w)[32]) {
+  uint32_t r[32], q[32];
+#define LP_LOAD32(R, AT)                                                                              \
+  asm volatile(                                                                                       \
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "    \
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "    \
+      "%30, %31}, [%32];"                                                                             \
+      : "=r"(R[0]), "=r"(R[1]), "=r"(R[2]), "=r"(R[3]), "=r"(R[4]), "=r"(R[5]), "=r"(R[6]),           \
+        "=r"(R[7]), "=r"(R[8]), "=r"(R[9]), "=r"(R[10]), "=r"(R[11]), "=r"(R[12]), "=r"(R[13]),       \
+        "=r"(R[14]), "=r"(R[15]), "=r"(R[16]), "=r"(R[17]), "=r"(R[18]), "=r"(R[19]), "=r"(R[20]),    \
+        "=r"(R[21]), "=r"(R[22]), "=r"(R[23]), "=r"(R[24]), "=r"(R[25]), "=r"(R[26]), "=r"(R[27]),    \
+        "=r"(R[28]), "=r"(R[29]), "=r"(R[30]), "=r"(R[31])                                            \
+      : "r"(AT)                                                                                       \
+      : "memory")
+  LP_LOAD32(r, at0);
+  LP_LOAD32(q, at1);
+#undef LP_LOAD32
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]), w[i] = __uint_as_float(q[i]);
+}
+
+// What a tile needs to know of its matrix.
+struct Operands {
+  const unsigned char *a, *b;  // row blocks of A and of B (K-major), or B itself (N-major)
+  int64_t a_blocks, b_blocks;  // blocks of a row
+  int k_blocks;
+  bool same;                   // B's tile is A's
+};
+template <int kProduct>
+__device__ __forceinline__ Operands operands_of(const MuonArgs& a, const MuonRecord& t, const MuonUnit& u, int from) {
+  const int64_t x_blocks = padded_to(t.n, kTile) / kBlockK, g_blocks = padded_to(t.m, kTile) / kBlockK;
+  Operands o;
+  if (kProduct == kApply) {
+    o.a = a.workspace + t.p;
+    o.b = a.workspace + t.x[from];
+    o.a_blocks = g_blocks;
+    o.b_blocks = x_blocks;
+    o.k_blocks = int((t.m + kBlockK - 1) / kBlockK);
+    o.same = false;
+  } else {
+    o.a = o.b = a.workspace + (kProduct == kGram ? t.x[from] : t.g);
+    o.a_blocks = o.b_blocks = kProduct == kGram ? x_blocks : g_blocks;
+    o.k_blocks = int(((kProduct == kGram ? t.n : t.m) + kBlockK - 1) / kBlockK);
+    o.same = u.i == u.j;
+  }
+  return o;
+}
+
+// The step's last product: the parameters' rows and columns of a thread's 32 results.
+__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, int tensor, int64_t row,
+                                             int64_t col, const float (&x)[32], bool poison) {
+  if (row >= t.m || !a.fine[tensor]) return;
+  const double l = a.lr * double(t.lr_scale);
+  const float keep = float(1.0 - l * double(t.weight_decay)), rate = float(l * double(t.update_scale));
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (col + j >= t.n) continue;
+    const int64_t at = t.tall ? (col + j) * t.cols + row : row * t.cols + col + j;
+    if (!LP_CHECK(at >= 0 && at < t.rows * t.cols, kChkOutBox)) continue;
+    float p = __fmaf_rn(-rate, x[j] * (kUnscale * kUnscale), t.param[at] * keep);
+    if (poison) p = __int_as_float(0x7fc00000);
+    t.param[at] = p;
+    if (t.copy != nullptr) t.copy[at] = __float2bfloat16_rn(p);
+  }
+}
+
+// One product over `units` tiles.  from: which X is read; last: P X goes into the parameters instead of
+// the other X.  withhold (tests of the bounded waits only): the first copy is announced and not made.
+template <int kProduct>
+__global__ void __launch_bounds__(kThreads)
+    lp_muon_product_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, int n_units, int from,
+                           int last, int withhold) {
+  constexpr bool kBMn = kProduct == kApply;
+  uint8_t* smem = pipeline_smem_base();
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  const auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  const auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+  const auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+  const auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(full_bar(s), 1), mbar_init(empty_bar(s), 1);
+    for (int b = 0; b < 2; ++b) mbar_init(tfull_bar(b), 1), mbar_init(tempty_bar(b), kEpilogueThreads);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(2 * kAccumulator)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the operands are written
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- loader
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, pending = 0, pending_parity = 0;
+      bool ok = true;
+      for (int n = blockIdx.x; ok && n < n_units; n += gridDim.x) {
+        const MuonUnit u = units[n];
+        if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
+        const Operands o = operands_of<kProduct>(a, a.records[u.tensor], u, from);
+        for (int kb = 0; kb < o.k_blocks; ++kb) {
+          if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, a.err, kErrLoader)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBlock, bar = full_bar(stage);
+          mbar_arrive_expect_tx(bar, o.same ? kBlock : kStage);
+          pending |= 1u << stage;
+          pending_parity = (pending_parity & ~(1u << stage)) | (phase << stage);
+          if (!(withhold != 0 && n == 0 && kb == 0) && LP_CHECK(kb < o.a_blocks, kChkTmaCoord)) {
+            bulk_load(sa, o.a + block_at(u.i, kb, o.a_blocks), kBlock, bar);
+            if (kBMn) {
+              // 64 rows of two neighbouring blocks: the hi parts, then the lo parts
+              const unsigned char* b = o.b + block_at(kb / 2, 2 * u.j, o.b_blocks) + (kb & 1) * (kHalf / 2);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                bulk_load(sb + q * (kHalf / 2), b + (q & 1) * int64_t(kBlock) + (q / 2) * kHalf, kHalf / 2, bar);
+            } else if (!o.same) {
+              bulk_load(sb, o.b + block_at(u.j, kb, o.b_blocks), kBlock, bar);
+            }
+          }
+          if (++stage == kStages) stage = 0, phase ^= 1u;
+        }
+      }
+      if (!ok)  // let every issued copy land before the CTA can exit
+        for (int s = 0; s < kStages; ++s)
+          if (pending & (1u << s)) drain_wait(full_bar(s), (pending_parity >> s) & 1u);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int n = blockIdx.x; ok && n < n_units; n += gridDim.x) {
+        const MuonUnit u = units[n];
+        if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
+        const Operands o = operands_of<kProduct>(a, a.records[u.tensor], u, from);
+        for (int kb = 0; kb < o.k_blocks; ++kb) {
+          const uint32_t d = tmem_base + uint32_t(acc) * kAccumulator;
+          const bool begins = kb % kChunk == 0;
+          if ((begins && !wait_bar(tempty_bar(acc), acc_phase ^ 1u, abort_flag, a.err, kErrMma)) ||
+              !wait_bar(full_bar(stage), phase, abort_flag, a.err, kErrMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * kStage), sb = o.same ? sa : sa + kBlock;
+          const uint64_t hi = sw128_desc(sa), lo = sw128_desc(sa + kHalf);
+          const uint64_t b = kBMn ? sw128_mn_desc(sb, kHalf / 2) : sw128_desc(sb);
+#pragma unroll
+          for (int k = 0; k < kBlockK / kUmmaK; ++k) {
+            const uint32_t ka = k * kUmmaK * 2, kbytes = kBMn ? k * 2048 : ka;
+            tc_mma_single(d, hi + (ka >> 4), b + (kbytes >> 4), !begins || k != 0, idesc_half(kBMn, 2 * kTile));
+            tc_mma_single(d + kTile, lo + (ka >> 4), b + (kbytes >> 4), 1u, idesc_half(kBMn, kTile));
+          }
+          tc_commit_local(empty_bar(stage));
+          if (++stage == kStages) stage = 0, phase ^= 1u;
+          if (kb % kChunk == kChunk - 1 || kb == o.k_blocks - 1) {
+            tc_commit_local(tfull_bar(acc));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+          }
+        }
+      }
+      tc_commit_local(drain_bar);
+      drain_wait(drain_bar, 0);
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int group = warp & 3, r = group * 32 + lane;  // the thread's row of the tile
+    const uint32_t t_lane = tmem_base + (uint32_t(group * 32) << 16);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool poison = last && *reinterpret_cast<volatile uint32_t*>(a.err) != 0u;
+    for (int n = blockIdx.x; n < n_units; n += gridDim.x) {
+      const MuonUnit u = units[n];
+      if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
+      const MuonRecord& t = a.records[u.tensor];
+      const int k_blocks = operands_of<kProduct>(a, t, u, from).k_blocks;
+      float x[kTile];  // the tile's row: the chunks' sums, rounded to nearest
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) x[j] = 0.f;
+      int go = 1;
+      for (int kb = 0; kb < k_blocks && go; kb += kChunk) {
+        if (lane == 0) go = *abort_flag == 0 && wait_bar(tfull_bar(acc), acc_phase, abort_flag, a.err, kErrEpilogue);
+        go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) break;
+        tc_fence_after();
+        const uint32_t at = t_lane + uint32_t(acc) * kAccumulator;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          float v[32], w[32];
+          tmem_load32x2(at + c, at + kTile + c, v, w);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[c + j] += v[j] + w[j];
+        }
+        tc_fence_before();
+        mbar_arrive_local(tempty_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!go) {  // the tiles that are left have no result
+        if (!last) break;
+        poison = true;
+      }
+      const int64_t x_blocks = padded_to(t.n, kTile) / kBlockK, g_blocks = padded_to(t.m, kTile) / kBlockK;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = x[c + j];
+        if (kProduct == kApply && last) {
+          write_params(a, t, u.tensor, int64_t(u.i) * kTile + r, int64_t(u.j) * kTile + c, v, poison);
+          continue;
+        }
+        // this thread's row in the output's block
+        const int64_t cols = kProduct == kApply ? x_blocks : g_blocks;
+        const int64_t block = block_at(u.i, 2 * u.j + c / kBlockK, cols);
+        unsigned char* out = a.workspace + (kProduct == kGram ? t.g : kProduct == kPoly ? t.p : t.x[from ^ 1]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t in = chunk_at(r, (c % kBlockK) / 8 + q);
+          float e[8];
+          if (kProduct == kPoly) {
+            const unsigned char* g = a.workspace + t.g + block + in;
+            const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(g)), lo = __ldcg(reinterpret_cast<const uint4*>(g + kHalf));
+            const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
+              e[2 * i] = __fmaf_rn(kC * kUnscale, v[8 * q + 2 * i], kB * (x.x + y.x));
+              e[2 * i + 1] = __fmaf_rn(kC * kUnscale, v[8 * q + 2 * i + 1], kB * (x.y + y.y));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (u.i == u.j && r == c + 8 * q + i) e[i] += kA * kScale;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = v[8 * q + i] * kUnscale;
+          }
+          uint4 hi, lo;
+          split8(e, hi, lo);
+          if (LP_CHECK(block >= 0, kChkOutBox)) {
+            *reinterpret_cast<uint4*>(out + block + in) = hi;
+            *reinterpret_cast<uint4*>(out + block + kHalf + in) = lo;
+          }
+          if (kProduct == kApply || u.i == u.j) continue;
+          // the same on the other side of the diagonal: row c + 8 q + i, column r
+          unsigned char* other = out + block_at(u.j, 2 * u.i + r / kBlockK, cols);
+          const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t to = chunk_at(c + 8 * q + i, (r % kBlockK) / 8) + (r & 7) * 2;
+            *reinterpret_cast<uint16_t*>(other + to) = uint16_t(h[i / 2] >> (16 * (i & 1)));
+            *reinterpret_cast<uint16_t*>(other + kHalf + to) = uint16_t(l[i / 2] >> (16 * (i & 1)));
+          }
+        }
+      }
+    }
+    // what the next launch's bulk copies read
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * kAccumulator)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------- host
+
+template <class... Params, class... Args>
+bool launch_next(void (*kernel)(Params...), int64_t blocks, int threads, int smem, bool dependent,
+                 cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+// Elements of the X of a batch's matrices: enough to fill the GPU many times over.
+constexpr int64_t kBatchElements = int64_t(1) << 26;
+
+// The plan as it grows.
+struct Building {
+  std::vector<MuonBatch> batches;
+  std::vector<MuonRecord> records;
+  std::vector<MuonUnit> parts, blocks, gram, apply;
+  size_t workspace = 0;
+};
+
+int k_of(const Building& b, const MuonUnit& u, bool gram) {
+  const MuonRecord& t = b.records[size_t(u.tensor)];
+  return int(gram ? t.n : t.m);
+}
+
+Building build_plan(const lp_muon_tensor* tensors, int64_t n_tensors) {
+  Building b;
+  int64_t i = 0;
+  while (i < n_tensors) {
+    MuonBatch batch{};
+    batch.first_part = int64_t(b.parts.size());
+    batch.first_block = int64_t(b.blocks.size());
+    batch.first_gram = int64_t(b.gram.size());
+    batch.first_apply = int64_t(b.apply.size());
+    int64_t elements = 0;
+    std::vector<int32_t> in;
+    for (; i < n_tensors; ++i) {
+      const lp_muon_tensor& t = tensors[i];
+      MuonRecord r{};
+      r.param = t.param;
+      r.copy = static_cast<__nv_bfloat16*>(t.copy);
+      r.grad = t.grad;
+      r.momentum = t.momentum;
+      r.rows = t.rows;
+      r.cols = t.cols;
+      r.tall = t.rows > t.cols;
+      r.m = std::min(t.rows, t.cols);
+      r.n = std::max(t.rows, t.cols);
+      r.lr_scale = t.lr_scale;
+      r.weight_decay = t.weight_decay;
+      r.update_scale = t.update_scale;
+      r.grad_bf16 = t.grad_dtype == LP_BFLOAT16;
+      const auto at = [](const void* p, uintptr_t by) { return reinterpret_cast<uintptr_t>(p) % by == 0; };
+      r.wide = at(t.grad, r.grad_bf16 ? 8 : 16) && at(t.momentum, 16) && at(t.param, 16) && t.cols % 4 == 0;
+      const int64_t padded = padded_to(r.m, kTile) * padded_to(r.n, kTile);
+      if (r.m > 0 && !in.empty() && elements + padded > kBatchElements) break;
+      b.records.push_back(r);
+      if (r.m == 0) continue;
+      elements += padded;
+      in.push_back(int32_t(i));
+    }
+    if (in.empty()) break;  // only matrices without elements are left
+    int64_t parts = 0;
+    for (int32_t k : in) {
+      MuonRecord& r = b.records[size_t(k)];
+      r.first_part = parts;
+      r.parts = (r.rows * r.cols + kMuonPart - 1) / kMuonPart;
+      parts += r.parts;
+      for (int64_t p = 0; p < r.parts; ++p) b.parts.push_back({k, int32_t(p), 0, 0});
+      const int64_t mb = padded_to(r.m, kTile) / kTile, nb = padded_to(r.n, kTile) / kTile;
+      for (int64_t x = 0; x < mb; ++x)
+        for (int64_t y = 0; y < 2 * nb; ++y) b.blocks.push_back({k, 0, int16_t(x), int16_t(y)});
+      for (int64_t x = 0; x < mb; ++x)
+        for (int64_t y = 0; y <= x; ++y) b.gram.push_back({k, 0, int16_t(x), int16_t(y)});
+      for (int64_t y = 0; y < nb; ++y)
+        for (int64_t x = 0; x < mb; ++x) b.apply.push_back({k, 0, int16_t(x), int16_t(y)});
+    }
+    // the longest products first, so that the last ones to start are short
+    std::stable_sort(b.gram.begin() + batch.first_gram, b.gram.end(),
+                     [&](const MuonUnit& x, const MuonUnit& y) { return k_of(b, x, true) > k_of(b, y, true); });
+    std::stable_sort(b.apply.begin() + batch.first_apply, b.apply.end(),
+                     [&](const MuonUnit& x, const MuonUnit& y) { return k_of(b, x, false) > k_of(b, y, false); });
+    batch.parts = int64_t(b.parts.size()) - batch.first_part;
+    batch.blocks = int64_t(b.blocks.size()) - batch.first_block;
+    batch.grams = int64_t(b.gram.size()) - batch.first_gram;
+    batch.applies = int64_t(b.apply.size()) - batch.first_apply;
+    // the workspace: header, the matrices' flags, partial sums, then each matrix's buffers
+    const auto up = [](size_t v) { return (v + 1023) / 1024 * 1024; };
+    size_t at = up(kWorkspaceHeader + size_t(n_tensors) * 4);
+    batch.partials_at = int64_t(at);
+    at += up(size_t(parts) * sizeof(double));
+    for (int32_t k : in) {
+      MuonRecord& r = b.records[size_t(k)];
+      const int64_t mp = padded_to(r.m, kTile), np = padded_to(r.n, kTile);
+      for (int64_t* p : {&r.x[0], &r.x[1]}) *p = int64_t(at), at += size_t(mp * np) * 4;
+      for (int64_t* p : {&r.g, &r.p}) *p = int64_t(at), at += size_t(mp * mp) * 4;
+    }
+    b.workspace = std::max(b.workspace, at);
+    b.batches.push_back(batch);
+  }
+  return b;
+}
+
+MuonHeader header_of(const Building& b) {
+  MuonHeader h{};
+  const auto up = [](size_t v) { return int64_t((v + 255) / 256 * 256); };
+  h.magic = kMuonMagic;
+  h.n_tensors = int64_t(b.records.size());
+  h.n_batches = int64_t(b.batches.size());
+  h.workspace = int64_t(b.workspace);
+  h.batches_at = up(sizeof(MuonHeader));
+  h.records_at = h.batches_at + up(b.batches.size() * sizeof(MuonBatch));
+  h.parts_at = h.records_at + up(b.records.size() * sizeof(MuonRecord));
+  h.blocks_at = h.parts_at + up(b.parts.size() * sizeof(MuonUnit));
+  h.gram_at = h.blocks_at + up(b.blocks.size() * sizeof(MuonUnit));
+  h.apply_at = h.gram_at + up(b.gram.size() * sizeof(MuonUnit));
+  h.bytes = h.apply_at + up(b.apply.size() * sizeof(MuonUnit));
+  return h;
+}
+
+template <class T>
+void put_all(char* to, const std::vector<T>& v) {
+  if (!v.empty()) std::copy_n(reinterpret_cast<const char*>(v.data()), v.size() * sizeof(T), to);
+}
+
+}  // namespace
+
+size_t muon_plan_bytes(const lp_muon_tensor* tensors, int64_t n_tensors) {
+  return size_t(header_of(build_plan(tensors, n_tensors)).bytes);
+}
+
+void write_muon_plan(const lp_muon_tensor* tensors, int64_t n_tensors, void* plan, size_t bytes) {
+  const Building b = build_plan(tensors, n_tensors);
+  const MuonHeader h = header_of(b);
+  if (bytes < size_t(h.bytes)) return;
+  char* p = static_cast<char*>(plan);
+  std::fill_n(p, h.bytes, char(0));
+  std::copy_n(reinterpret_cast<const char*>(&h), sizeof(h), p);
+  put_all(p + h.batches_at, b.batches);
+  put_all(p + h.records_at, b.records);
+  put_all(p + h.parts_at, b.parts);
+  put_all(p + h.blocks_at, b.blocks);
+  put_all(p + h.gram_at, b.gram);
+  put_all(p + h.apply_at, b.apply);
+}
+
+lp_status launch_muon_step(const Device& dev, const void* plan_host, const void* plan, const MuonArgs& args,
+                           int steps, cudaStream_t stream) {
+  static PerContextOnce once;
+  if (once.run(dev.ctx_id, [] {
+        for (const void* k : {reinterpret_cast<const void*>(lp_muon_product_kernel<kGram>),
+                              reinterpret_cast<const void*>(lp_muon_product_kernel<kPoly>),
+                              reinterpret_cast<const void*>(lp_muon_product_kernel<kApply>)}) {
+          const cudaError_t e = set_smem_limit(k, kSmem);
+          if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+      }) != cudaSuccess)
+    return LP_ERR_CUDA;
+  const char* host = static_cast<const char*>(plan_host);
+  const char* device = static_cast<const char*>(plan);
+  const MuonHeader& h = *reinterpret_cast<const MuonHeader*>(host);
+  MuonArgs a = args;
+  a.records = reinterpret_cast<const MuonRecord*>(device + h.records_at);
+  a.n_tensors = h.n_tensors;
+  a.err = reinterpret_cast<uint32_t*>(a.workspace);
+  a.fine = reinterpret_cast<int32_t*>(a.workspace + kWorkspaceHeader);
+  const auto units_at = [&](int64_t at, int64_t first) {
+    return reinterpret_cast<const MuonUnit*>(device + at) + first;
+  };
+  for (int64_t k = 0; k < h.n_batches; ++k) {
+    const MuonBatch& b = reinterpret_cast<const MuonBatch*>(host + h.batches_at)[k];
+    double* partials = reinterpret_cast<double*>(a.workspace + b.partials_at);
+    if (!launch_next(lp_muon_norm_kernel, b.parts, kNormThreads, 0, false, stream, a,
+                     units_at(h.parts_at, b.first_part), partials, int(k == 0)) ||
+        !launch_next(lp_muon_split_kernel, b.blocks, kSplitThreads, 0, true, stream, a,
+                     units_at(h.blocks_at, b.first_block), static_cast<const double*>(partials)))
+      return LP_ERR_CUDA;
+    const MuonUnit *gram = units_at(h.gram_at, b.first_gram), *apply = units_at(h.apply_at, b.first_apply);
+    const int gram_grid = single_grid(dev.sm_count, b.grams), apply_grid = single_grid(dev.sm_count, b.applies);
+    for (int s = 0; s < steps; ++s) {
+      const int from = s & 1, last = s == steps - 1;
+      if (!launch_next(lp_muon_product_kernel<kGram>, gram_grid, kThreads, kSmem, true, stream, a, gram,
+                       int(b.grams), from, 0, int(s == 0 && k == 0 && fault_injection() == 1)) ||
+          !launch_next(lp_muon_product_kernel<kPoly>, gram_grid, kThreads, kSmem, true, stream, a, gram,
+                       int(b.grams), from, 0, 0) ||
+          !launch_next(lp_muon_product_kernel<kApply>, apply_grid, kThreads, kSmem, true, stream, a, apply,
+                       int(b.applies), from, last, 0))
+        return LP_ERR_CUDA;
+    }
+  }
+  return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+}
+
+cudaError_t take_check_word_muon(uint32_t* out) { return take_check_word(out); }
+
+}  // namespace lp

@@ -214,4 +214,95 @@ lp_status lp_preference_loss(const float* logp, const float* ref_logp, const uin
   return launch_preference_loss(a, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+bool bad_matrices(const lp_muon_tensor* tensors, int64_t n_tensors) {
+  using namespace lp;
+  if (n_tensors < 0 || n_tensors > kMaxRows || (tensors == nullptr && n_tensors > 0)) return true;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const lp_muon_tensor& t = tensors[i];
+    if (t.rows < 0 || t.rows > kMuonMaxDim || t.cols < 0 || t.cols > kMuonMaxDim) return true;
+  }
+  return false;
+}
+const lp::MuonHeader* muon_header(const void* plan_host) {
+  if (plan_host == nullptr || !lp::aligned(plan_host, 8)) return nullptr;
+  const auto* h = static_cast<const lp::MuonHeader*>(plan_host);
+  return h->magic == lp::kMuonMagic ? h : nullptr;
+}
+}  // namespace
+
+size_t lp_muon_plan_size(const lp_muon_tensor* tensors, int64_t n_tensors) {
+  if (bad_matrices(tensors, n_tensors)) return 0;
+  try {
+    return lp::muon_plan_bytes(tensors, n_tensors);
+  } catch (...) {  // out of host memory
+    return 0;
+  }
+}
+
+lp_status lp_muon_plan(const lp_muon_tensor* tensors, int64_t n_tensors, void* plan_host,
+                       size_t plan_bytes) {
+  using namespace lp;
+  if (bad_matrices(tensors, n_tensors) || plan_host == nullptr) return LP_ERR_INVALID_ARGUMENT;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const lp_muon_tensor& t = tensors[i];
+    if (!is_dtype(t.grad_dtype)) return LP_ERR_INVALID_ARGUMENT;
+    for (float f : {t.lr_scale, t.weight_decay, t.update_scale})
+      if (!(f >= 0.0f) || !std::isfinite(f)) return LP_ERR_INVALID_ARGUMENT;
+    const int64_t n = t.rows * t.cols;
+    if (n > 0 && (t.param == nullptr || t.grad == nullptr || t.momentum == nullptr))
+      return LP_ERR_INVALID_ARGUMENT;
+    const Extent e[4] = {extent(t.param, n, 1, 1, 4), extent(t.copy, n, 1, 1, 2),
+                         extent(t.momentum, n, 1, 1, 4),
+                         extent(t.grad, n, 1, 1, size_of(t.grad_dtype == LP_BFLOAT16))};
+    for (int j = 0; j < 4; ++j)
+      for (int k = 0; k < j; ++k)
+        if (overlap(e[j], e[k])) return LP_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(plan_host, 8)) return LP_ERR_MISALIGNED;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const lp_muon_tensor& t = tensors[i];
+    if (!aligned(t.param, 4) || !aligned(t.copy, 2) || !aligned(t.momentum, 4) ||
+        !aligned(t.grad, size_of(t.grad_dtype == LP_BFLOAT16)))
+      return LP_ERR_MISALIGNED;
+  }
+  try {
+    if (plan_bytes < muon_plan_bytes(tensors, n_tensors)) return LP_ERR_WORKSPACE_TOO_SMALL;
+    write_muon_plan(tensors, n_tensors, plan_host, plan_bytes);
+  } catch (...) {  // out of host memory
+    return LP_ERR_WORKSPACE_TOO_SMALL;
+  }
+  return LP_OK;
+}
+
+size_t lp_muon_workspace_size(const void* plan_host) {
+  const lp::MuonHeader* h = muon_header(plan_host);
+  return h == nullptr ? 0 : static_cast<size_t>(h->workspace);
+}
+
+lp_status lp_muon_step(const void* plan_host, const void* plan, double lr, double momentum,
+                       int nesterov, int steps, double eps, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  using namespace lp;
+  if (!(lr >= 0.0) || !std::isfinite(lr) || !(momentum >= 0.0 && momentum < 1.0) ||
+      !(eps >= 1e-16) || !std::isfinite(static_cast<float>(eps)) || steps < 1 || steps > 32)
+    return LP_ERR_INVALID_ARGUMENT;
+  const MuonHeader* h = muon_header(plan_host);
+  if (h == nullptr) return LP_ERR_INVALID_ARGUMENT;
+  if (h->n_batches == 0) return LP_OK;
+  if (plan == nullptr || workspace == nullptr) return LP_ERR_INVALID_ARGUMENT;
+  if (!aligned(plan, 256) || !aligned(workspace, 256)) return LP_ERR_MISALIGNED;
+  if (workspace_bytes < static_cast<size_t>(h->workspace)) return LP_ERR_WORKSPACE_TOO_SMALL;
+  Device dev;
+  const lp_status st = current_device(&dev);
+  if (st != LP_OK) return st;
+  MuonArgs a{};
+  a.workspace = static_cast<unsigned char*>(workspace);
+  a.lr = lr;
+  a.momentum = static_cast<float>(momentum);
+  a.eps = static_cast<float>(eps);
+  a.nesterov = nesterov != 0;
+  return launch_muon_step(dev, plan_host, plan, a, steps, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

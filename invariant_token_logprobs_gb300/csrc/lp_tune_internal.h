@@ -54,9 +54,58 @@ struct PreferenceArgs {
 size_t preference_loss_workspace(int64_t T, int64_t n_sequences);
 lp_status launch_preference_loss(const PreferenceArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------------------------------- Muon
+
+constexpr int64_t kMuonMagic = 0x6e6f756d2d706cll;  // of a plan's header
+constexpr int64_t kMuonMaxDim = 65536;
+constexpr int64_t kMuonPart = 16384;  // elements of a partial sum of the norm
+
+// One matrix's record in the plan.  x, g, p: byte offsets of its buffers in the workspace.
+struct MuonRecord {
+  float* param;
+  __nv_bfloat16* copy;
+  const void* grad;
+  float* momentum;
+  int64_t rows, cols, m, n;  // m <= n: the X that is orthogonalised, transposed when tall
+  int64_t x[2], g, p;
+  int64_t first_part, parts;
+  float lr_scale, weight_decay, update_scale;
+  int32_t grad_bf16, tall, wide;
+};
+// A CTA's work: a partial sum, or a block or tile (i, j) of a matrix.
+struct MuonUnit {
+  int32_t tensor, part;
+  int16_t i, j;
+};
+// Matrices that go through the launches together; where their units begin, and how many.
+struct MuonBatch {
+  int64_t first_part, parts, first_block, blocks, first_gram, grams, first_apply, applies;
+  int64_t partials_at;  // in the workspace
+};
+struct MuonHeader {
+  int64_t magic, bytes, n_tensors, n_batches, workspace;
+  int64_t batches_at, records_at, parts_at, blocks_at, gram_at, apply_at;
+};
+struct MuonArgs {
+  const MuonRecord* records;  // set by the launcher, as n_tensors, err and fine
+  int64_t n_tensors;
+  unsigned char* workspace;
+  uint32_t* err;
+  int32_t* fine;              // whether a matrix's norm is finite
+  double lr;
+  float momentum, eps;
+  int nesterov;
+};
+// Both allocate on the host: std::bad_alloc is the caller's to catch.
+size_t muon_plan_bytes(const lp_muon_tensor* tensors, int64_t n_tensors);
+void write_muon_plan(const lp_muon_tensor* tensors, int64_t n_tensors, void* plan, size_t bytes);
+lp_status launch_muon_step(const Device& dev, const void* plan_host, const void* plan, const MuonArgs& a,
+                           int steps, cudaStream_t stream);
+
 // Read and clear the check words of these translation units (lp_check.cuh).
 cudaError_t take_check_word_layer_norm(uint32_t* out);
 cudaError_t take_check_word_layer_norm_backward(uint32_t* out);
 cudaError_t take_check_word_preference(uint32_t* out);
+cudaError_t take_check_word_muon(uint32_t* out);
 
 }  // namespace lp

@@ -13,6 +13,8 @@ struct EntryPoints {
   decltype(&lp_layer_norm_backward) layer_norm_backward;
   decltype(&lp_preference_loss_workspace_size) preference_workspace;
   decltype(&lp_preference_loss) preference_loss;
+  decltype(&lp_muon_workspace_size) muon_workspace;
+  decltype(&lp_muon_step) muon_step;
 } lp;
 
 // The dtype of weight and bias, which is one.
@@ -177,6 +179,32 @@ PyObject* preference_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// plan_host, plan, momenta, lr, momentum, nesterov, steps, eps, written, grads, streams, captured
+PyObject* muon_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const at::Tensor &plan_host = required(v[0], "plan_host"), &plan = required(v[1], "plan"),
+                     &momenta = required(v[2], "momenta");
+    if (plan_host.is_cuda()) value_error("plan_host must be in host memory");
+    const double lr = number(v[3]), momentum = number(v[4]), eps = number(v[7]);
+    const bool nesterov = truth(v[5]);
+    const int64_t steps = integer(v[6]);
+    const c10::Device device = device_of(plan, {&momenta});
+    const c10::cuda::CUDAGuard guard(device);
+    const c10::cuda::CUDAStream on = c10::cuda::getCurrentCUDAStream(device.index());
+    keep_for_step(on, v[1], {&momenta}, v[8], v[9], v[10], v[11]);
+    const size_t bytes = lp.muon_workspace(data(plan_host));
+    const at::Tensor workspace = empty({std::max<int64_t>(int64_t(bytes), 256)}, at::kByte, device);
+    check_status("lp_muon_step",
+                 lp.muon_step(data(plan_host), data(plan), lr, momentum, nesterov,
+                              int(std::max<int64_t>(std::min<int64_t>(steps, 1000), 0)), eps,
+                              data(workspace), bytes, on.stream()));
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(v[8]); ++i)
+      written_in_place(&required(PyTuple_GET_ITEM(v[8], i), "a tensor of the step"));
+    written_in_place(&momenta);
+    return THPVariable_Wrap(workspace);
+  });
+}
+
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return bind_table(reinterpret_cast<void**>(&lp), sizeof(lp) / sizeof(void*), v, n);
 }
@@ -184,6 +212,7 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<layer_norm>("layer_norm"),
                          method<layer_norm_backward>("layer_norm_backward"),
                          method<preference_loss>("preference_loss"),
+                         method<muon_step>("muon_step"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tune_calls", nullptr, -1, methods};
 

@@ -4,6 +4,7 @@ declared in include/lp_tune.h.
     out  = layer_norm(residual, branch, weight=..., bias=...)
     grad = layer_norm_backward(grad_normed, grad_residual, out.residual, out.mean, out.rstd, ...)
     loss = preference_loss(logp, cu_seqlens, ref_logp=..., mask=...)
+    optimizer = Muon(params, grads, copies=...); optimizer.step()
 
 As in train.py this is argument marshalling only: every step of the computation runs in liblp's
 kernels on the current stream, there is no fallback, the calls' checks and allocations are compiled
@@ -17,19 +18,22 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 import re
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
 from . import _build_lib, lp
 from .lp import LpError
-from .train import _on_stream
+from .train import _disjoint, _dtype_code, _on_one_device, _on_stream, _per_tensor
 
 __all__ = [
     "LayerNorm",
     "LayerNormGrad",
+    "MUON_ALIGN",
+    "Muon",
     "PreferenceLoss",
     "declared_symbols",
     "layer_norm",
@@ -43,12 +47,23 @@ __all__ = [
 
 HEADER = os.path.join(os.path.dirname(lp.HEADER), "lp_tune.h")
 
+MUON_ALIGN = 64  # elements that the flat momentum of each matrix is a multiple of
+
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
 _f64 = ctypes.c_double
+
+
+class _MuonTensor(ctypes.Structure):
+    _fields_ = [("param", _vp), ("copy", _vp), ("grad", _vp), ("momentum", _vp), ("rows", _i64),
+                ("cols", _i64), ("lr_scale", _f32), ("weight_decay", _f32), ("update_scale", _f32),
+                ("grad_dtype", _int)]
+
+
+_tensors = ctypes.POINTER(_MuonTensor)
 
 _SIGNATURES = {
     "lp_layer_norm": (
@@ -69,7 +84,8 @@ _calls = None
 
 # what tune_calls.cpp calls, in the order of its table
 _BOUND = ("lp_layer_norm", "lp_layer_norm_backward_workspace_size", "lp_layer_norm_backward",
-          "lp_preference_loss_workspace_size", "lp_preference_loss")
+          "lp_preference_loss_workspace_size", "lp_preference_loss", "lp_muon_workspace_size",
+          "lp_muon_step")
 
 
 def declared_symbols() -> list[str]:
@@ -200,3 +216,155 @@ def preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
     return PreferenceLoss._make((_calls or load_calls()).preference_loss(
         logp, cu_seqlens, ref_logp, mask, _KINDS[kind], average, halves, beta, margin, label_smoothing,
         nll_coef, workspace))
+
+
+# ------------------------------------------------------------------------- Muon
+
+def _update_scale(scaling: Union[str, float], rows: int, cols: int) -> float:
+    """The factor of the learning rate that a matrix's shape gives."""
+    if scaling == "spectral":
+        return math.sqrt(max(1.0, rows / max(cols, 1)))
+    if scaling == "rms":
+        return 0.2 * math.sqrt(max(rows, cols))
+    if isinstance(scaling, str):
+        raise ValueError("scaling must be 'spectral', 'rms' or a number")
+    return float(scaling)
+
+
+class Muon:
+    """Muon over a list of matrices: the momentum of each is orthogonalised by Newton-Schulz products
+    before it is taken off the parameters, for the matrices of a model's blocks (embeddings, heads and
+    vectors go to train.AdamW).
+
+        M = momentum M + g;  u = g + momentum M (nesterov) or M;  X = u / (|u| + eps)
+        steps times X = a X + b (X X^T) X + c (X X^T)^2 X;  p = p (1 - lr weight_decay) - lr s X
+
+    params are contiguous float32 matrices, updated in place; grads their gradients (float32 or
+    bfloat16), read at every step from the same memory; copies, where given, bfloat16 matrices (or None)
+    that receive the updated params.  s is by `scaling` "spectral" sqrt(max(1, rows / cols)), "rms" 0.2
+    sqrt(max(rows, cols)), which moves elements as far as AdamW does, or a number.  weight_decay and
+    lr_scale, which multiplies lr, are numbers or one for each matrix.  The products are as exact as
+    float32's.
+
+    `state`, as state_dict() gives it, continues from it with its buffer.  set_grads() names other
+    gradient tensors.  A step on any stream keeps its tensors' memory until it is done.  A matrix whose
+    update's norm is not finite is left as it was, its momentum too."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], *,
+                 copies: Optional[Sequence[Optional[torch.Tensor]]] = None, lr: float = 0.02,
+                 momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: Union[float, Sequence[float]] = 0.0,
+                 lr_scale: Union[float, Sequence[float]] = 1.0, scaling: Union[str, float] = "spectral",
+                 steps: int = 5, eps: float = 1e-7, state: Optional[dict] = None):
+        self.params = list(params)
+        n = len(self.params)
+        if n == 0:
+            raise ValueError("no tensors")
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(self.copies) != n:
+            raise ValueError("copies must have one tensor or None for each param")
+        for p, c in zip(self.params, self.copies):
+            if p.dtype != torch.float32 or not p.is_contiguous() or p.dim() != 2:
+                raise TypeError("params must be contiguous float32 matrices")
+            if c is not None and (c.dtype != torch.bfloat16 or c.shape != p.shape or
+                                  not c.is_contiguous()):
+                raise TypeError("copies must be contiguous bfloat16 tensors of the params' shapes")
+        self.lr, self.momentum, self.nesterov = float(lr), float(momentum), bool(nesterov)
+        self.steps, self.eps = int(steps), float(eps)
+        if not 1 <= self.steps <= 32:
+            raise ValueError("steps must be 1 to 32")
+        self._scales = tuple(_update_scale(scaling, *p.shape) for p in self.params)
+        weight_decay = _per_tensor(weight_decay, n, "weight_decay")
+        lr_scale = _per_tensor(lr_scale, n, "lr_scale")
+        _on_one_device(self.params + [c for c in self.copies if c is not None])
+        size = sum(-(-p.numel() // MUON_ALIGN) * MUON_ALIGN for p in self.params)
+        if state is None:
+            self.momentum_buffer = torch.zeros(size, device=self.params[0].device)
+        else:
+            flat = state["momentum"]
+            if flat.dtype != torch.float32 or flat.shape != (size,) or not flat.is_contiguous():
+                raise ValueError(f"momentum must be a contiguous float32 vector of {size}")
+            if flat.data_ptr() % 16 != 0:
+                raise ValueError("momentum must be 16-byte aligned")
+            _on_one_device([self.params[0], flat])
+            self.momentum_buffer = flat
+        self._captured: list = []  # plans and gradients of steps that are parts of graphs
+        self._lay_out(list(grads), weight_decay, lr_scale)
+
+    def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
+        """Lays the plan of the step out for these gradient tensors.  When they are refused the
+        optimizer stays as it was.  A step that was captured before goes on reading the gradients
+        that it was captured with, which the optimizer keeps."""
+        self._lay_out(list(grads), self._weight_decay, self._lr_scale)
+
+    @property
+    def weight_decay(self) -> tuple[float, ...]:
+        """Each matrix's weight decay; assigned as a number or one for each matrix, it holds from the
+        next step on."""
+        return self._weight_decay
+
+    @weight_decay.setter
+    def weight_decay(self, value: Union[float, Sequence[float]]) -> None:
+        self._lay_out(self.grads, _per_tensor(value, len(self.params), "weight_decay"), self._lr_scale)
+
+    @property
+    def lr_scale(self) -> tuple[float, ...]:
+        """Each matrix's factor of the learning rate, assigned like weight_decay."""
+        return self._lr_scale
+
+    @lr_scale.setter
+    def lr_scale(self, value: Union[float, Sequence[float]]) -> None:
+        self._lay_out(self.grads, self._weight_decay, _per_tensor(value, len(self.params), "lr_scale"))
+
+    def momenta(self) -> list[torch.Tensor]:
+        """The momentum of each matrix, in its shape: parts of momentum_buffer."""
+        out, at = [], 0
+        for p in self.params:
+            out.append(self.momentum_buffer[at:at + p.numel()].view(p.shape))
+            at += -(-p.numel() // MUON_ALIGN) * MUON_ALIGN
+        return out
+
+    def _lay_out(self, grads: list[torch.Tensor], weight_decay: tuple[float, ...],
+                 lr_scale: tuple[float, ...]) -> None:
+        """Checks these and lays the plan out; nothing is kept of what is refused."""
+        if len(grads) != len(self.params):
+            raise ValueError("grads must have one tensor for each param")
+        copies = [c for c in self.copies if c is not None]
+        written = self.params + copies + [self.momentum_buffer]
+        _on_one_device(written + grads)
+        for p, g in zip(self.params, grads):
+            _dtype_code(g, "gradients")
+            if g.shape != p.shape or not g.is_contiguous():
+                raise ValueError("gradients must be contiguous and of the params' shapes")
+        if not _disjoint(written):
+            raise ValueError("params, copies and momenta must not share memory")
+        if not _disjoint(written, grads):
+            raise ValueError("gradients must not share memory with params, copies or momenta")
+        lib = load()
+        n = len(self.params)
+        records = (_MuonTensor * n)(*[
+            _MuonTensor(p.data_ptr(), None if c is None else c.data_ptr(), g.data_ptr(), m.data_ptr(),
+                        p.shape[0], p.shape[1], s, w, u, _dtype_code(g, "gradients"))
+            for p, c, g, m, s, w, u in zip(self.params, self.copies, grads, self.momenta(), lr_scale,
+                                           weight_decay, self._scales)])
+        size = int(lib.lp_muon_plan_size(records, n))
+        host = torch.empty(max(size, 8), dtype=torch.uint8)
+        lp._check("lp_muon_plan", lib.lp_muon_plan(records, n, host.data_ptr(), size))
+        plan = host.to(self.params[0].device)
+        home = torch.cuda.current_stream(plan.device).cuda_stream if plan.is_cuda else 0
+        self.grads, self._plan_host, self._plan, self._streams = grads, host, plan, [home]
+        self._weight_decay, self._lr_scale = weight_decay, lr_scale
+        self._given = (tuple(self.params + copies), tuple(grads))
+
+    def state_dict(self) -> dict:
+        """The momenta's buffer (not copied)."""
+        return {"momentum": self.momentum_buffer}
+
+    def step(self, lr: Optional[float] = None, stream=None) -> None:
+        """One step.  Captured in a graph it is a step at every replay, with the learning rate that it
+        was captured with; the optimizer has to outlive the graph."""
+        if stream is not None:
+            return _on_stream(stream, self.params[0], self.step, lr)
+        (_calls or load_calls()).muon_step(
+            self._plan_host, self._plan, self.momentum_buffer, self.lr if lr is None else lr, self.momentum,
+            self.nesterov, self.steps, self.eps, *self._given, self._streams, self._captured)
