@@ -43,15 +43,17 @@ constexpr int kTile = 128;                  // rows and columns of a tile, rows 
 constexpr int kBlockK = 64;                 // columns of a block, K of a stage
 constexpr uint32_t kHalf = kTile * kBlockK * 2;  // bytes of a block's hi (or lo) part
 constexpr uint32_t kBlock = 2 * kHalf;
-constexpr int kStages = 3;
 // K blocks that are summed in tensor memory before the sum is added to the tile's in registers.  The
 // tensor core cuts sums off where an addition would round: over K of 1000 the singular values came
 // out 8e-6 off, five times what float32 products give; in chunks it is what 16 of its steps cut off.
-constexpr int kChunk = 4;
-constexpr uint32_t kStage = 2 * kBlock;
-constexpr int kBars = 2 * kStages + 5;
-constexpr int kSmem = 1024 + kStages * int(kStage) + kBars * 8 + 16;
+constexpr int kChunk = 8;
 constexpr uint32_t kAccumulator = 2 * kTile;     // tensor-memory columns
+constexpr int kOutThreads = 256;                 // of the epilogue: two a row of the tile
+constexpr int kOutWarps = kOutThreads / 32;
+constexpr int kProductThreads = 128 + kOutThreads;
+// Registers of a thread: what the launch gives, and how the epilogue's two warpgroups, which hold the
+// tile's sums, take from the other: 40 + 2 * 232 = 3 * 168.
+constexpr int kFewRegisters = 40, kManyRegisters = 232;
 constexpr int kNormThreads = 256;
 constexpr int kSplitThreads = 256;
 
@@ -77,7 +79,7 @@ __device__ __forceinline__ float update_of(const MuonArgs& a, float g, float m) 
   return a.nesterov ? __fmaf_rn(a.momentum, m, g) : m;
 }
 
-// The squares' sum of kMuonPart elements of a matrix.
+// The squares' sum of a part of a matrix.
 __global__ void __launch_bounds__(kNormThreads)
     lp_muon_norm_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, double* partials, int first) {
   __shared__ double slots[kNormThreads / 32];
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kNormThreads)
   const MuonUnit u = units[blockIdx.x];
   if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
   const MuonRecord& t = a.records[u.tensor];
-  const int64_t n = t.rows * t.cols, from = int64_t(u.part) * kMuonPart, to = min(from + kMuonPart, n);
+  const int64_t n = t.rows * t.cols, from = int64_t(u.part) * t.part, to = min(from + t.part, n);
   if (!LP_CHECK(from >= 0 && from < n, kChkCopyIndex)) return;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   for (int64_t i = from + 4 * threadIdx.x; i < to; i += 4 * kNormThreads) {
@@ -224,95 +226,209 @@ __global__ void __launch_bounds__(kSplitThreads)
 
 // ------------------------------------------------------------------------- products
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+// A stage of the ring: 64 of K of A's and of B's tile.
+constexpr int kStages = 3;
+constexpr uint32_t kStage = 2 * kBlock;
+constexpr int kBars = 2 * kStages + 5;
+constexpr uint32_t kOut = kStages * kStage;  // the epilogue's 32 KB
+constexpr int kSmem = 1024 + int(kOut + kBlock) + kBars * 8 + 16;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+// kind::f16 with float16 operands and float32 accumulators, M = 128; bits 15 and 16 say that A and B are M-
+// and N-major.
+__host__ __device__ constexpr uint32_t idesc_half(int n) {
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+}
+
+// 32 consecutive columns of this thread's tensor-memory lane; tmem_wait before they are used.
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// kind::f16 with float16 operands and float32 accumulators, M = 128.
-__host__ __device__ constexpr uint32_t idesc_half(bool b_mn, int n) {
-  return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
-}
-
-// 32 consecutive columns of this thread's tensor-memory lane, from two places.
-__device__ __forceinline__ void tmem_load32x2(uint32_t at0, uint32_t at1, float (&v)[32], float (&w)[32]) {
-  uint32_t r[32], q[32];
-#define LP_LOAD32(R, AT)                                                                              \
-  asm volatile(                                                                                       \
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "    \
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "    \
-      "%30, %31}, [%32];"                                                                             \
-      : "=r"(R[0]), "=r"(R[1]), "=r"(R[2]), "=r"(R[3]), "=r"(R[4]), "=r"(R[5]), "=r"(R[6]),           \
-        "=r"(R[7]), "=r"(R[8]), "=r"(R[9]), "=r"(R[10]), "=r"(R[11]), "=r"(R[12]), "=r"(R[13]),       \
-        "=r"(R[14]), "=r"(R[15]), "=r"(R[16]), "=r"(R[17]), "=r"(R[18]), "=r"(R[19]), "=r"(R[20]),    \
-        "=r"(R[21]), "=r"(R[22]), "=r"(R[23]), "=r"(R[24]), "=r"(R[25]), "=r"(R[26]), "=r"(R[27]),    \
-        "=r"(R[28]), "=r"(R[29]), "=r"(R[30]), "=r"(R[31])                                            \
-      : "r"(AT)                                                                                       \
-      : "memory")
-  LP_LOAD32(r, at0);
-  LP_LOAD32(q, at1);
-#undef LP_LOAD32
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]), w[i] = __uint_as_float(q[i]);
-}
-
-// What a tile needs to know of its matrix.
+// Where a unit's operands lie, in rows of 128 bytes of the workspace.
+constexpr int kRow = 128;
+constexpr int kBlockRows = int(kBlock) / kRow;
 struct Operands {
-  const unsigned char *a, *b;  // row blocks of A and of B (K-major), or B itself (N-major)
-  int64_t a_blocks, b_blocks;  // blocks of a row
+  int a, b;                // A and B (of X X^T and G G, the same)
+  int a_blocks, b_blocks;  // blocks of a row of blocks
   int k_blocks;
-  bool same;                   // B's tile is A's
 };
 template <int kProduct>
-__device__ __forceinline__ Operands operands_of(const MuonArgs& a, const MuonRecord& t, const MuonUnit& u, int from) {
-  const int64_t x_blocks = padded_to(t.n, kTile) / kBlockK, g_blocks = padded_to(t.m, kTile) / kBlockK;
-  Operands o;
-  if (kProduct == kApply) {
-    o.a = a.workspace + t.p;
-    o.b = a.workspace + t.x[from];
-    o.a_blocks = g_blocks;
-    o.b_blocks = x_blocks;
-    o.k_blocks = int((t.m + kBlockK - 1) / kBlockK);
-    o.same = false;
-  } else {
-    o.a = o.b = a.workspace + (kProduct == kGram ? t.x[from] : t.g);
-    o.a_blocks = o.b_blocks = kProduct == kGram ? x_blocks : g_blocks;
-    o.k_blocks = int(((kProduct == kGram ? t.n : t.m) + kBlockK - 1) / kBlockK);
-    o.same = u.i == u.j;
-  }
-  return o;
+__device__ __forceinline__ Operands operands_of(const MuonRecord& t, int from) {
+  const int x_blocks = int(padded_to(t.n, kTile)) / kBlockK, g_blocks = int(padded_to(t.m, kTile)) / kBlockK;
+  const int x = int(t.x[from] / kRow), g = int(t.g / kRow), p = int(t.p / kRow);
+  const int k = int(((kProduct == kGram ? t.n : t.m) + kBlockK - 1) / kBlockK);
+  if (kProduct == kGram) return {x, x, x_blocks, x_blocks, k};
+  if (kProduct == kPoly) return {g, g, g_blocks, g_blocks, k};
+  return {p, x, g_blocks, x_blocks, k};
+}
+// G and P are symmetric, and only the blocks of their tiles on and below the diagonal are written.  Whether
+// columns 64 kb on of row block i lie above it: they are then read where they mirror to, as an operand that is
+// contiguous along M or N.
+__device__ __forceinline__ bool mirrored(int i, int kb) { return kb / 2 > i; }
+
+// Whether `go` holds for all of the epilogue's warps.
+__device__ __forceinline__ bool epilogue_all(int go) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(go)
+      : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes)
+               : "memory");
 }
 
-// The step's last product: the parameters' rows and columns of a thread's 32 results.
-__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, int tensor, int64_t row,
-                                             int64_t col, const float (&x)[32], bool poison) {
-  if (row >= t.m || !a.fine[tensor]) return;
-  const double l = a.lr * double(t.lr_scale);
-  const float keep = float(1.0 - l * double(t.weight_decay)), rate = float(l * double(t.update_scale));
+__device__ __forceinline__ uint32_t half2_of(float x, float y) {
+  const __half2 two = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&two);
+}
+// hi of two values, or lo: what hi leaves.
+__device__ __forceinline__ uint32_t part_of(float x, float y, bool lo) {
+  const uint32_t h = half2_of(x, y);
+  if (!lo) return h;
+  const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return half2_of(x - back.x, y - back.y);
+}
+
+// The tile, of which x holds 64 columns from column 64 half on of the thread's row r, into its two blocks:
+// first the hi parts of both, then the lo parts, through shared memory.
+__device__ __forceinline__ void write_tile(const float (&x)[kTile / 2], int r, int half, unsigned char* to,
+                                           uint8_t* out, bool first_thread) {
+  const uint32_t out_at = smem_u32(out);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (col + j >= t.n) continue;
-    const int64_t at = t.tall ? (col + j) * t.cols + row : row * t.cols + col + j;
-    if (!LP_CHECK(at >= 0 && at < t.rows * t.cols, kChkOutBox)) continue;
-    float p = __fmaf_rn(-rate, x[j] * (kUnscale * kUnscale), t.param[at] * keep);
-    if (poison) p = __int_as_float(0x7fc00000);
+  for (int lo = 0; lo < 2; ++lo) {
+    if (first_thread) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the buffer is free
+    epilogue_sync();
+#pragma unroll
+    for (int q = 0; q < kTile / 16; ++q) {
+      uint4 v;
+      v.x = part_of(x[8 * q], x[8 * q + 1], lo);
+      v.y = part_of(x[8 * q + 2], x[8 * q + 3], lo);
+      v.z = part_of(x[8 * q + 4], x[8 * q + 5], lo);
+      v.w = part_of(x[8 * q + 6], x[8 * q + 7], lo);
+      *reinterpret_cast<uint4*>(out + half * kHalf + chunk_at(r, q)) = v;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    epilogue_sync();
+    if (first_thread) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) bulk_store(to + q * int64_t(kBlock) + lo * kHalf, out_at + q * kHalf, kHalf);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
+}
+
+// The step's last product: the parameters from the 64 columns in x, rows `row` on and columns `col` on of X,
+// lanes along the parameters' rows.  All loads of a turn are on their way before its first store.  slots: 4 KB
+// of the warp's own.
+__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, bool fine, int64_t row,
+                                             int64_t col, int lane, const float (&x)[kTile / 2], float* slots,
+                                             bool poison) {
+  if (!fine) return;
+  const double l = a.lr * double(t.lr_scale);
+  const float keep = float(1.0 - l * double(t.weight_decay));
+  const float rate = poison ? __int_as_float(0x7fc00000)
+                            : float(l * double(t.update_scale)) * (kUnscale * kUnscale);
+  const auto put = [&](int64_t at, float p, float v) {
+    p = __fmaf_rn(-rate, v, p * keep);
     t.param[at] = p;
     if (t.copy != nullptr) t.copy[at] = __float2bfloat16_rn(p);
+  };
+  if (!LP_CHECK(row >= 0 && col >= 0, kChkOutBox)) return;
+  if (t.tall) {  // X's rows are the parameters' columns: so are the lanes
+    const int64_t at = col * t.cols + row + lane;
+    const bool mine = row + lane < t.m;
+#pragma unroll
+    for (int c = 0; c < 64; c += 16) {
+      float p[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        p[j] = mine && col + c + j < t.n ? t.param[at + (c + j) * t.cols] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (mine && col + c + j < t.n) put(at + (c + j) * t.cols, p[j], x[c + j]);
+    }
+    return;
   }
+  // a warp's 32 rows, 32 columns at a time, through shared memory
+#pragma unroll
+  for (int c = 0; c < 64; c += 32) {
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *reinterpret_cast<float4*>(slots + lane * 32 + ((q ^ (lane & 7)) << 2)) =
+          make_float4(x[c + 4 * q], x[c + 4 * q + 1], x[c + 4 * q + 2], x[c + 4 * q + 3]);
+    __syncwarp();
+    const int64_t column = col + c + lane;
+    float* const out = t.param + row * t.cols + column;
+#pragma unroll 1
+    for (int from = 0; from < 32; from += 16) {
+      float p[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        p[r] = row + from + r < t.m && column < t.n ? out[(from + r) * t.cols] : 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (row + from + r < t.m && column < t.n)
+          put((row + from + r) * t.cols + column, p[r],
+              slots[(from + r) * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]);
+    }
+  }
+}
+
+// Bounded wait for the phase of `bar` with parity `parity`, as wait_bar but by clock64: the epilogue waits
+// once a chunk, and reading %globaltimer would be most of it.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                              uint32_t role) {
+  constexpr long long kLimit = 2000000000;  // a second
+  const long long t0 = clock64();
+  while (true) {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kLimit) {
+      *abort_flag = 1;
+      atomicOr(err, role);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                         uint32_t role) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_long(bar, parity, abort_flag, err, role);
 }
 
 // One product over `units` tiles.  from: which X is read; last: P X goes into the parameters instead of
-// the other X.  withhold (tests of the bounded waits only): the first copy is announced and not made.
+// the other X.  map_a, map_b: the workspace as rows of 128 bytes, in boxes of 256 and of 64.  withhold
+// (tests of the bounded waits only): the first copy is announced and not made.
 template <int kProduct>
-__global__ void __launch_bounds__(kThreads)
-    lp_muon_product_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, int n_units, int from,
+__global__ void __launch_bounds__(kProductThreads, 1)
+    lp_muon_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                           const __grid_constant__ MuonArgs a, const MuonUnit* units, int n_units, int from,
                            int last, int withhold) {
-  constexpr bool kBMn = kProduct == kApply;
+  constexpr int kMine = kTile / 2;  // columns of an epilogue thread
   uint8_t* smem = pipeline_smem_base();
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOut + kBlock);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t bar0 = smem_u32(bars);
@@ -321,14 +437,16 @@ __global__ void __launch_bounds__(kThreads)
   const auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, step = gridDim.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full_bar(s), 1), mbar_init(empty_bar(s), 1);
-    for (int b = 0; b < 2; ++b) mbar_init(tfull_bar(b), 1), mbar_init(tempty_bar(b), kEpilogueThreads);
+    for (int b = 0; b < 2; ++b) mbar_init(tfull_bar(b), 1), mbar_init(tempty_bar(b), kOutWarps);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -336,43 +454,57 @@ __global__ void __launch_bounds__(kThreads)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // the plan does not depend on the launch before: its first entries come on chip meanwhile
+  if (first < n_units && lane == 0) {
+    const int tensor = *reinterpret_cast<const volatile int*>(&units[first].tensor);
+    if (LP_CHECK(tensor >= 0 && tensor < a.n_tensors, kChkPlan))
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.records + tensor) : "memory");
+  }
   tc_fence_before();
   __syncthreads();
-  __syncwarp();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the operands are written
 
-  if (warp == 0) {
-    // -------------------------------------------------------------- loader
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegisters));
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ loader
       int stage = 0;
       uint32_t phase = 0, pending = 0, pending_parity = 0;
       bool ok = true;
-      for (int n = blockIdx.x; ok && n < n_units; n += gridDim.x) {
+      for (int n = first; ok && n < n_units; n += step) {
         const MuonUnit u = units[n];
         if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
-        const Operands o = operands_of<kProduct>(a, a.records[u.tensor], u, from);
+        const Operands o = operands_of<kProduct>(a.records[u.tensor], from);
+        const bool same = kProduct != kApply && u.i == u.j;
         for (int kb = 0; kb < o.k_blocks; ++kb) {
-          if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, a.err, kErrLoader)) {
+          if (!wait_for(empty_bar(stage), phase ^ 1u, abort_flag, a.err, kErrLoader)) {
             ok = false;
             break;
           }
-          const uint32_t sa = smem_u32(smem + stage * kStage), sb = sa + kBlock, bar = full_bar(stage);
-          mbar_arrive_expect_tx(bar, o.same ? kBlock : kStage);
+          const uint32_t sa = smem_u32(smem + stage * kStage), bar = full_bar(stage);
+          mbar_arrive_expect_tx(bar, same ? kBlock : kStage);
           pending |= 1u << stage;
           pending_parity = (pending_parity & ~(1u << stage)) | (phase << stage);
-          if (!(withhold != 0 && n == 0 && kb == 0) && LP_CHECK(kb < o.a_blocks, kChkTmaCoord)) {
-            bulk_load(sa, o.a + block_at(u.i, kb, o.a_blocks), kBlock, bar);
-            if (kBMn) {
-              // 64 rows of two neighbouring blocks: the hi parts, then the lo parts
-              const unsigned char* b = o.b + block_at(kb / 2, 2 * u.j, o.b_blocks) + (kb & 1) * (kHalf / 2);
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                bulk_load(sb + q * (kHalf / 2), b + (q & 1) * int64_t(kBlock) + (q / 2) * kHalf, kHalf / 2, bar);
-            } else if (!o.same) {
-              bulk_load(sb, o.b + block_at(u.j, kb, o.b_blocks), kBlock, bar);
+          // 64 columns of row block i, or where they mirror to: 64 rows of two neighbouring blocks, the hi parts,
+          // then the lo parts
+          const auto load = [&](uint32_t to, int base, int blocks, int i, bool mirror) {
+            const int row = base + (mirror ? (kb / 2 * blocks + 2 * i) * kBlockRows + (kb & 1) * 64
+                                           : (i * blocks + kb) * kBlockRows);
+            if (!LP_CHECK(row >= 0, kChkTmaCoord)) return;
+            if (!mirror) {
+              tma_load_2d_local(to, &map_a, 0, row, bar);
+              return;
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              tma_load_2d_local(to + q * (kHalf / 2), &map_b, 0, row + (q & 1) * kBlockRows + (q / 2) * kTile, bar);
+          };
+          if (!(withhold != 0 && n == 0 && kb == 0)) {
+            load(sa, o.a, o.a_blocks, u.i, kProduct != kGram && mirrored(u.i, kb));
+            if (!same)
+              load(sa + kBlock, o.b, o.b_blocks, u.j, kProduct == kApply || (kProduct == kPoly && mirrored(u.j, kb)));
           }
           if (++stage == kStages) stage = 0, phase ^= 1u;
         }
@@ -380,38 +512,42 @@ __global__ void __launch_bounds__(kThreads)
       if (!ok)  // let every issued copy land before the CTA can exit
         for (int s = 0; s < kStages; ++s)
           if (pending & (1u << s)) drain_wait(full_bar(s), (pending_parity >> s) & 1u);
-    }
-  } else if (warp == 1) {
-    // -------------------------------------------------------------- products
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ products
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int n = blockIdx.x; ok && n < n_units; n += gridDim.x) {
+      for (int n = first; ok && n < n_units; n += step) {
         const MuonUnit u = units[n];
         if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
-        const Operands o = operands_of<kProduct>(a, a.records[u.tensor], u, from);
-        for (int kb = 0; kb < o.k_blocks; ++kb) {
+        const int k_blocks = operands_of<kProduct>(a.records[u.tensor], from).k_blocks;
+        const bool same = kProduct != kApply && u.i == u.j;
+        for (int kb = 0; kb < k_blocks; ++kb) {
           const uint32_t d = tmem_base + uint32_t(acc) * kAccumulator;
           const bool begins = kb % kChunk == 0;
-          if ((begins && !wait_bar(tempty_bar(acc), acc_phase ^ 1u, abort_flag, a.err, kErrMma)) ||
-              !wait_bar(full_bar(stage), phase, abort_flag, a.err, kErrMma)) {
+          if ((begins && !wait_for(tempty_bar(acc), acc_phase ^ 1u, abort_flag, a.err, kErrMma)) ||
+              !wait_for(full_bar(stage), phase, abort_flag, a.err, kErrMma)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * kStage), sb = o.same ? sa : sa + kBlock;
-          const uint64_t hi = sw128_desc(sa), lo = sw128_desc(sa + kHalf);
-          const uint64_t b = kBMn ? sw128_mn_desc(sb, kHalf / 2) : sw128_desc(sb);
+          const uint32_t sa = smem_u32(smem + stage * kStage), sb = same ? sa : sa + kBlock;
+          const bool a_mn = kProduct != kGram && mirrored(u.i, kb);
+          const bool b_mn = kProduct == kApply || (kProduct == kPoly && mirrored(u.j, kb));
+          const uint64_t hi = a_mn ? sw128_mn_desc(sa, kHalf / 2) : sw128_desc(sa), lo = hi + (kHalf >> 4);
+          const uint64_t b = b_mn ? sw128_mn_desc(sb, kHalf / 2) : sw128_desc(sb);
+          // of a step of 16 of K, in the descriptors' units: 8 rows of 128 bytes twice, or 32 bytes of a row
+          const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+          const uint32_t major = uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16;
 #pragma unroll
           for (int k = 0; k < kBlockK / kUmmaK; ++k) {
-            const uint32_t ka = k * kUmmaK * 2, kbytes = kBMn ? k * 2048 : ka;
-            tc_mma_single(d, hi + (ka >> 4), b + (kbytes >> 4), !begins || k != 0, idesc_half(kBMn, 2 * kTile));
-            tc_mma_single(d + kTile, lo + (ka >> 4), b + (kbytes >> 4), 1u, idesc_half(kBMn, kTile));
+            // hi x [hi; lo] as one of N = 256, and lo x hi onto its second half
+            tc_mma_single(d, hi + k * a_step, b + k * b_step, !begins || k != 0, idesc_half(2 * kTile) | major);
+            tc_mma_single(d + kTile, lo + k * a_step, b + k * b_step, 1u, idesc_half(kTile) | major);
           }
           tc_commit_local(empty_bar(stage));
           if (++stage == kStages) stage = 0, phase ^= 1u;
-          if (kb % kChunk == kChunk - 1 || kb == o.k_blocks - 1) {
+          if (kb % kChunk == kChunk - 1 || kb == k_blocks - 1) {
             tc_commit_local(tfull_bar(acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -423,105 +559,92 @@ __global__ void __launch_bounds__(kThreads)
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    const int group = warp & 3, r = group * 32 + lane;  // the thread's row of the tile
-    const uint32_t t_lane = tmem_base + (uint32_t(group * 32) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegisters));
+    // the thread's row of the tile, and which half of its columns
+    const int group = warp & 3, half = warp / 4 - 1, r = group * 32 + lane;
+    const uint32_t t_lane = tmem_base + (uint32_t(group * 32) << 16) + half * kMine;
+    const bool first_thread = threadIdx.x == 128;
+    uint8_t* out = smem + kOut;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool poison = last && *reinterpret_cast<volatile uint32_t*>(a.err) != 0u;
-    for (int n = blockIdx.x; n < n_units; n += gridDim.x) {
+    for (int n = first; n < n_units; n += step) {
       const MuonUnit u = units[n];
       if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
       const MuonRecord& t = a.records[u.tensor];
-      const int k_blocks = operands_of<kProduct>(a, t, u, from).k_blocks;
-      float x[kTile];  // the tile's row: the chunks' sums, rounded to nearest
+      const int k_blocks = operands_of<kProduct>(t, from).k_blocks;
+      const int64_t cols = padded_to(kProduct == kApply ? t.n : t.m, kTile) / kBlockK;
+      const int64_t block = block_at(u.i, 2 * int64_t(u.j), cols);
+      float x[kMine];  // the chunks' sums, rounded to nearest
+      if (kProduct == kPoly) {
+        // c (G G + b / c G): what G adds comes in while the first products run
+        const unsigned char* g = a.workspace + t.g + block + half * int64_t(kBlock);
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) x[j] = 0.f;
+        for (int q = 0; q < kMine / 8; ++q) {
+          const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(g + chunk_at(r, q)));
+          const uint4 lo = __ldcg(reinterpret_cast<const uint4*>(g + kHalf + chunk_at(r, q)));
+          const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
+            x[8 * q + 2 * i] = (v.x + w.x) * (kB / kC * kScale);
+            x[8 * q + 2 * i + 1] = (v.y + w.y) * (kB / kC * kScale);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) x[j] = 0.f;
+      }
       int go = 1;
-      for (int kb = 0; kb < k_blocks && go; kb += kChunk) {
-        if (lane == 0) go = *abort_flag == 0 && wait_bar(tfull_bar(acc), acc_phase, abort_flag, a.err, kErrEpilogue);
+      for (int kb = 0; kb < k_blocks; kb += kChunk) {
+        if (lane == 0) go = *abort_flag == 0 && wait_for(tfull_bar(acc), acc_phase, abort_flag, a.err, kErrEpilogue);
         go = __shfl_sync(0xffffffffu, go, 0);
         if (!go) break;
         tc_fence_after();
         const uint32_t at = t_lane + uint32_t(acc) * kAccumulator;
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float v[32], w[32];
-          tmem_load32x2(at + c, at + kTile + c, v, w);
+        for (int c = 0; c < kMine; c += 32) {
+          uint32_t v[32], w[32];  // hi hi, and the rest
+          tmem_load32(at + c, v);
+          tmem_load32(at + kTile + c, w);
+          tmem_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[c + j] += v[j] + w[j];
+          for (int j = 0; j < 32; ++j) x[c + j] += __uint_as_float(v[j]) + __uint_as_float(w[j]);
         }
         tc_fence_before();
-        mbar_arrive_local(tempty_bar(acc));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(tempty_bar(acc));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!go) {  // the tiles that are left have no result
+      // every warp of the CTA goes on, or none does: they meet at the tile's way out
+      if (!epilogue_all(go)) {  // the tiles that are left have no result
         if (!last) break;
         poison = true;
       }
-      const int64_t x_blocks = padded_to(t.n, kTile) / kBlockK, g_blocks = padded_to(t.m, kTile) / kBlockK;
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = x[c + j];
-        if (kProduct == kApply && last) {
-          write_params(a, t, u.tensor, int64_t(u.i) * kTile + r, int64_t(u.j) * kTile + c, v, poison);
-          continue;
-        }
-        // this thread's row in the output's block
-        const int64_t cols = kProduct == kApply ? x_blocks : g_blocks;
-        const int64_t block = block_at(u.i, 2 * u.j + c / kBlockK, cols);
-        unsigned char* out = a.workspace + (kProduct == kGram ? t.g : kProduct == kPoly ? t.p : t.x[from ^ 1]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t in = chunk_at(r, (c % kBlockK) / 8 + q);
-          float e[8];
-          if (kProduct == kPoly) {
-            const unsigned char* g = a.workspace + t.g + block + in;
-            const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(g)), lo = __ldcg(reinterpret_cast<const uint4*>(g + kHalf));
-            const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
-              e[2 * i] = __fmaf_rn(kC * kUnscale, v[8 * q + 2 * i], kB * (x.x + y.x));
-              e[2 * i + 1] = __fmaf_rn(kC * kUnscale, v[8 * q + 2 * i + 1], kB * (x.y + y.y));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (u.i == u.j && r == c + 8 * q + i) e[i] += kA * kScale;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = v[8 * q + i] * kUnscale;
-          }
-          uint4 hi, lo;
-          split8(e, hi, lo);
-          if (LP_CHECK(block >= 0, kChkOutBox)) {
-            *reinterpret_cast<uint4*>(out + block + in) = hi;
-            *reinterpret_cast<uint4*>(out + block + kHalf + in) = lo;
-          }
-          if (kProduct == kApply || u.i == u.j) continue;
-          // the same on the other side of the diagonal: row c + 8 q + i, column r
-          unsigned char* other = out + block_at(u.j, 2 * u.i + r / kBlockK, cols);
-          const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t to = chunk_at(c + 8 * q + i, (r % kBlockK) / 8) + (r & 7) * 2;
-            *reinterpret_cast<uint16_t*>(other + to) = uint16_t(h[i / 2] >> (16 * (i & 1)));
-            *reinterpret_cast<uint16_t*>(other + kHalf + to) = uint16_t(l[i / 2] >> (16 * (i & 1)));
-          }
-        }
+      if (kProduct == kApply && last) {
+        write_params(a, t, a.fine[u.tensor] != 0, int64_t(u.i) * kTile + group * 32,
+                     int64_t(u.j) * kTile + half * kMine, lane, x, reinterpret_cast<float*>(out) + (warp - 4) * 1024,
+                     poison);
+        continue;
       }
+      const int diagonal = (u.i - u.j) * kTile + r - half * kMine;  // where the row meets it in x
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        x[j] *= kProduct == kPoly ? kC * kUnscale : kUnscale;
+        if (kProduct == kPoly && j == diagonal) x[j] += kA * kScale;
+      }
+      unsigned char* to = a.workspace + (kProduct == kGram ? t.g : kProduct == kPoly ? t.p : t.x[from ^ 1]);
+      if (LP_CHECK(block >= 0, kChkOutBox)) write_tile(x, r, half, to + block, out, first_thread);
     }
-    // what the next launch's bulk copies read
-    asm volatile("fence.proxy.async.global;" ::: "memory");
+    if (first_thread) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // all is written
   }
 
   tc_fence_before();
   __syncthreads();
-  __syncwarp();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * kAccumulator)
                  : "memory");
@@ -531,8 +654,8 @@ __global__ void __launch_bounds__(kThreads)
 // ------------------------------------------------------------------------- host
 
 template <class... Params, class... Args>
-bool launch_next(void (*kernel)(Params...), int64_t blocks, int threads, int smem, bool dependent,
-                 cudaStream_t stream, Args... args) {
+bool launch_next(void (*kernel)(Params...), int64_t blocks, int threads, int smem, bool dependent, cudaStream_t stream,
+                 const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(blocks));
   cfg.blockDim = dim3(unsigned(threads));
@@ -603,12 +726,18 @@ Building build_plan(const lp_muon_tensor* tensors, int64_t n_tensors) {
     for (int32_t k : in) {
       MuonRecord& r = b.records[size_t(k)];
       r.first_part = parts;
-      r.parts = (r.rows * r.cols + kMuonPart - 1) / kMuonPart;
+      // at least kMuonPart elements, and no more than 1024 parts
+      r.part = padded_to(std::max(kMuonPart, (r.rows * r.cols + 1023) / 1024), 4);
+      r.parts = (r.rows * r.cols + r.part - 1) / r.part;
       parts += r.parts;
       for (int64_t p = 0; p < r.parts; ++p) b.parts.push_back({k, int32_t(p), 0, 0});
       const int64_t mb = padded_to(r.m, kTile) / kTile, nb = padded_to(r.n, kTile) / kTile;
       for (int64_t x = 0; x < mb; ++x)
         for (int64_t y = 0; y < 2 * nb; ++y) b.blocks.push_back({k, 0, int16_t(x), int16_t(y)});
+    }
+    for (int32_t k : in) {
+      const MuonRecord& r = b.records[size_t(k)];
+      const int64_t mb = padded_to(r.m, kTile) / kTile, nb = padded_to(r.n, kTile) / kTile;
       for (int64_t x = 0; x < mb; ++x)
         for (int64_t y = 0; y <= x; ++y) b.gram.push_back({k, 0, int16_t(x), int16_t(y)});
       for (int64_t y = 0; y < nb; ++y)
@@ -683,8 +812,10 @@ void write_muon_plan(const lp_muon_tensor* tensors, int64_t n_tensors, void* pla
   put_all(p + h.apply_at, b.apply);
 }
 
-lp_status launch_muon_step(const Device& dev, const void* plan_host, const void* plan, const MuonArgs& args,
-                           int steps, cudaStream_t stream) {
+// The three products of every step of a batch.
+static lp_status launch_products(const Device& dev, const CUtensorMap& map_a, const CUtensorMap& map_b,
+                                 const MuonArgs& a, const MuonBatch& b, const MuonUnit* gram, const MuonUnit* apply,
+                                 int steps, bool withhold, cudaStream_t stream) {
   static PerContextOnce once;
   if (once.run(dev.ctx_id, [] {
         for (const void* k : {reinterpret_cast<const void*>(lp_muon_product_kernel<kGram>),
@@ -696,6 +827,22 @@ lp_status launch_muon_step(const Device& dev, const void* plan_host, const void*
         return cudaSuccess;
       }) != cudaSuccess)
     return LP_ERR_CUDA;
+  for (int s = 0; s < steps; ++s) {
+    const int from = s & 1, last = s == steps - 1;
+    const auto launch = [&](auto* kernel, const MuonUnit* units, int64_t n, int is_last, int first) {
+      return launch_next(kernel, single_grid(dev.sm_count, n), kProductThreads, kSmem, true, stream, map_a, map_b, a,
+                         units, int(n), from, is_last, first);
+    };
+    if (!launch(lp_muon_product_kernel<kGram>, gram, b.grams, 0, int(s == 0 && withhold)) ||
+        !launch(lp_muon_product_kernel<kPoly>, gram, b.grams, 0, 0) ||
+        !launch(lp_muon_product_kernel<kApply>, apply, b.applies, last, 0))
+      return LP_ERR_CUDA;
+  }
+  return LP_OK;
+}
+
+lp_status launch_muon_step(const Device& dev, const void* plan_host, const void* plan, const MuonArgs& args,
+                           int steps, cudaStream_t stream) {
   const char* host = static_cast<const char*>(plan_host);
   const char* device = static_cast<const char*>(plan);
   const MuonHeader& h = *reinterpret_cast<const MuonHeader*>(host);
@@ -704,6 +851,10 @@ lp_status launch_muon_step(const Device& dev, const void* plan_host, const void*
   a.n_tensors = h.n_tensors;
   a.err = reinterpret_cast<uint32_t*>(a.workspace);
   a.fine = reinterpret_cast<int32_t*>(a.workspace + kWorkspaceHeader);
+  CUtensorMap map_a, map_b;
+  const int64_t rows = h.workspace / kRow;
+  if (!encode_rows128(&map_a, a.workspace, rows, 256) || !encode_rows128(&map_b, a.workspace, rows, 64))
+    return LP_ERR_CUDA;
   const auto units_at = [&](int64_t at, int64_t first) {
     return reinterpret_cast<const MuonUnit*>(device + at) + first;
   };
@@ -715,18 +866,10 @@ lp_status launch_muon_step(const Device& dev, const void* plan_host, const void*
         !launch_next(lp_muon_split_kernel, b.blocks, kSplitThreads, 0, true, stream, a,
                      units_at(h.blocks_at, b.first_block), static_cast<const double*>(partials)))
       return LP_ERR_CUDA;
-    const MuonUnit *gram = units_at(h.gram_at, b.first_gram), *apply = units_at(h.apply_at, b.first_apply);
-    const int gram_grid = single_grid(dev.sm_count, b.grams), apply_grid = single_grid(dev.sm_count, b.applies);
-    for (int s = 0; s < steps; ++s) {
-      const int from = s & 1, last = s == steps - 1;
-      if (!launch_next(lp_muon_product_kernel<kGram>, gram_grid, kThreads, kSmem, true, stream, a, gram,
-                       int(b.grams), from, 0, int(s == 0 && k == 0 && fault_injection() == 1)) ||
-          !launch_next(lp_muon_product_kernel<kPoly>, gram_grid, kThreads, kSmem, true, stream, a, gram,
-                       int(b.grams), from, 0, 0) ||
-          !launch_next(lp_muon_product_kernel<kApply>, apply_grid, kThreads, kSmem, true, stream, a, apply,
-                       int(b.applies), from, last, 0))
-        return LP_ERR_CUDA;
-    }
+    const lp_status st = launch_products(
+        dev, map_a, map_b, a, b, units_at(h.gram_at, b.first_gram), units_at(h.apply_at, b.first_apply), steps,
+        k == 0 && fault_injection() == 1, stream);
+    if (st != LP_OK) return st;
   }
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }

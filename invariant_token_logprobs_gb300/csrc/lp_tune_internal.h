@@ -58,7 +58,7 @@ lp_status launch_preference_loss(const PreferenceArgs& a, cudaStream_t stream);
 
 constexpr int64_t kMuonMagic = 0x6e6f756d2d706cll;  // of a plan's header
 constexpr int64_t kMuonMaxDim = 65536;
-constexpr int64_t kMuonPart = 16384;  // elements of a partial sum of the norm
+constexpr int64_t kMuonPart = 4096;  // elements of a partial sum of the norm, at least
 
 // One matrix's record in the plan.  x, g, p: byte offsets of its buffers in the workspace.
 struct MuonRecord {
@@ -68,7 +68,7 @@ struct MuonRecord {
   float* momentum;
   int64_t rows, cols, m, n;  // m <= n: the X that is orthogonalised, transposed when tall
   int64_t x[2], g, p;
-  int64_t first_part, parts;
+  int64_t first_part, parts, part;  // its partial sums: the first, how many, of how many elements
   float lr_scale, weight_decay, update_scale;
   int32_t grad_bf16, tall, wide;
 };

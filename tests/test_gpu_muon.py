@@ -114,6 +114,12 @@ def test_large():
     run([(1024, 1536), (2100, 1100)], BF16, copy=False)
 
 
+def test_several_turns_of_all_ctas():
+    """More tiles than there are SMs, of many matrices and of one."""
+    run([(300, 200), (129, 1000), (257, 140), (64, 64)] * 25, BF16, copy=False)
+    run([(2200, 2300)], lr=0.1)
+
+
 def test_an_orthogonal_update():
     """Singular values that are all equal: after the division each is 1 / sqrt(m), and X is that
     polynomial's value times the update's directions."""
