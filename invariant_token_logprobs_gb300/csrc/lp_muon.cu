@@ -79,53 +79,70 @@ __device__ __forceinline__ float update_of(const MuonArgs& a, float g, float m) 
   return a.nesterov ? __fmaf_rn(a.momentum, m, g) : m;
 }
 
-// The squares' sum of a part of a matrix.
-__global__ void __launch_bounds__(kNormThreads)
-    lp_muon_norm_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, double* partials, int first) {
-  __shared__ double slots[kNormThreads / 32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (first && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0u;
-  const MuonUnit u = units[blockIdx.x];
-  if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
-  const MuonRecord& t = a.records[u.tensor];
-  const int64_t n = t.rows * t.cols, from = int64_t(u.part) * t.part, to = min(from + t.part, n);
-  if (!LP_CHECK(from >= 0 && from < n, kChkCopyIndex)) return;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t i = from + 4 * threadIdx.x; i < to; i += 4 * kNormThreads) {
-    float g[4], m[4];
-    if (t.wide && i + 4 <= to) {
-      const float4 v = *reinterpret_cast<const float4*>(t.momentum + i);
-      m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
-      if (t.grad_bf16) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.grad) + i));
-        g[0] = __uint_as_float(w.x << 16), g[1] = __uint_as_float(w.x & 0xffff0000u);
-        g[2] = __uint_as_float(w.y << 16), g[3] = __uint_as_float(w.y & 0xffff0000u);
-      } else {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + i));
-        g[0] = w.x, g[1] = w.y, g[2] = w.z, g[3] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        g[j] = i + j < to ? grad_at(t, i + j) : 0.f;
-        m[j] = i + j < to ? t.momentum[i + j] : 0.f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x = update_of(a, g[j], momentum_of(a, g[j], m[j]));
-      sum[j] = __fmaf_rn(x, x, sum[j]);
-    }
+// Four neighbouring elements of the gradient and the momentum, 16 bytes at a time.
+__device__ __forceinline__ void load_wide(const MuonRecord& t, int64_t i, float* g, float* m) {
+  const float4 v = *reinterpret_cast<const float4*>(t.momentum + i);
+  m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
+  if (t.grad_bf16) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.grad) + i));
+    g[0] = __uint_as_float(w.x << 16), g[1] = __uint_as_float(w.x & 0xffff0000u);
+    g[2] = __uint_as_float(w.y << 16), g[3] = __uint_as_float(w.y & 0xffff0000u);
+  } else {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + i));
+    g[0] = w.x, g[1] = w.y, g[2] = w.z, g[3] = w.w;
   }
-  double s = (double(sum[0]) + double(sum[1])) + (double(sum[2]) + double(sum[3]));
+}
+// The sum of a value over the CTA's 256 threads, the same bits for all of them.
+__device__ __forceinline__ float sum256(float s, float* slots) {
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = s;
   __syncthreads();
-  if (threadIdx.x != 0) return;
+  s = slots[threadIdx.x & 7];
 #pragma unroll
-  for (int k = 1; k < kNormThreads / 32; ++k) s += slots[k];
-  partials[blockIdx.x] = s;
+  for (int o = 4; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// The squares' sum of a part of a matrix.
+__global__ void __launch_bounds__(kNormThreads)
+    lp_muon_norm_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, float* partials, int first) {
+  __shared__ float slots[kNormThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (first && blockIdx.x == 0 && threadIdx.x < 4) a.err[threadIdx.x] = 0u;  // the words that are read back
+  const MuonUnit u = units[blockIdx.x];
+  if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
+  const MuonRecord t = a.records[u.tensor];
+  const int64_t n = t.rows * t.cols, from = int64_t(u.part) * t.part;
+  if (!LP_CHECK(from >= 0 && from < n, kChkCopyIndex)) return;
+  const int count = int(min(t.part, n - from));
+  constexpr int kTurn = 4;  // groups of four elements of a thread at once
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int first_of = 4 * int(threadIdx.x); first_of < count; first_of += kTurn * 4 * kNormThreads) {
+    float g[kTurn][4], m[kTurn][4];
+#pragma unroll
+    for (int k = 0; k < kTurn; ++k) {
+      const int at = first_of + k * 4 * kNormThreads;
+      if (t.wide && at + 4 <= count) {
+        load_wide(t, from + at, g[k], m[k]);
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[k][j] = at + j < count ? grad_at(t, from + at + j) : 0.f;
+        m[k][j] = at + j < count ? t.momentum[from + at + j] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTurn; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = update_of(a, g[k][j], momentum_of(a, g[k][j], m[k][j]));
+        sum[j] = __fmaf_rn(x, x, sum[j]);
+      }
+  }
+  const float s = sum256((sum[0] + sum[1]) + (sum[2] + sum[3]), slots);
+  if (threadIdx.x == 0) partials[blockIdx.x] = s;
 }
 
 // hi and lo of eight scaled values, as a block holds them.
@@ -147,80 +164,81 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int chunk) {
   return uint32_t(r) * 128u + (uint32_t(chunk ^ (r & 7)) << 4);
 }
 
-// A block of the first X, and the new momentum of its elements.
-__global__ void __launch_bounds__(kSplitThreads)
-    lp_muon_split_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, const double* partials) {
-  __shared__ double slots[kSplitThreads / 32];
+// A block of the first X, and the new momentum of its elements.  A thread has four groups of eight columns;
+// their loads are all on their way before the norm is there.  (float64 for the norm's last steps, 1/64 of the
+// rate, took longer than the block.)
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    lp_muon_split_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, const float* partials) {
+  constexpr int kGroups = kTile * kBlockK / 8 / kSplitThreads;
+  __shared__ float slots[kSplitThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const MuonUnit u = units[blockIdx.x];
   if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
-  const MuonRecord& t = a.records[u.tensor];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  double s = 0.0;
-  for (int64_t k = threadIdx.x; k < t.parts; k += kSplitThreads) s += __ldcg(partials + t.first_part + k);
+  const MuonRecord t = a.records[u.tensor];
+  // Neighbouring threads go along the matrix's rows, which are X's columns where it is tall.  A thread's next
+  // group is 32 rows on, or 16 columns.
+  const int tid = int(threadIdx.x);
+  const int r = t.tall ? tid % kTile : tid / 8, chunk = t.tall ? tid / kTile : tid % 8;
+  const int next_r = t.tall ? 0 : kSplitThreads / 8, next_chunk = t.tall ? kSplitThreads / kTile : 0;
+  const int rows_left = int(t.m - int64_t(u.i) * kTile) - r, cols_left = int(t.n - int64_t(u.j) * kBlockK) - 8 * chunk;
+  const int64_t row = int64_t(u.i) * kTile + r, col = int64_t(u.j) * kBlockK + 8 * chunk;
+  const int64_t at = t.tall ? col * t.cols + row : row * t.cols + col, step = t.tall ? t.cols : 1;
+  const int64_t next = (t.tall ? 8 * next_chunk : next_r) * t.cols;
+  const auto left_of = [&](int k) {  // columns of group k
+    return k * next_r < rows_left ? min(max(cols_left - 8 * k * next_chunk, 0), 8) : 0;
+  };
+  const bool wide = !t.tall && t.wide;
+  float g[kGroups][8], m[kGroups][8];
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = s;
-  __syncthreads();
-  s = 0.0;
+  for (int k = 0; k < kGroups; ++k) {
+    const int left = left_of(k);
+    const int64_t i = at + k * next;
 #pragma unroll
-  for (int k = 0; k < kSplitThreads / 32; ++k) s += slots[k];
-  const float norm = float(sqrt(s));
+    for (int j = 0; j < 8; ++j) g[k][j] = m[k][j] = 0.f;
+    if (!LP_CHECK(left == 0 || (i >= 0 && i + (left - 1) * step < t.rows * t.cols), kChkCopyIndex)) continue;
+    if (wide && left == 8) {
+      load_wide(t, i, g[k], m[k]);
+      load_wide(t, i + 4, g[k] + 4, m[k] + 4);
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) g[k][j] = grad_at(t, i + j * step), m[k][j] = t.momentum[i + j * step];
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are written
+  float s = 0.f;
+  for (int k = tid; k < int(t.parts); k += kSplitThreads) s += __ldcg(partials + t.first_part + k);
+  const float norm = sqrtf(sum256(s, slots));
   const bool fine = norm <= 0x1.fffffep127f;
-  if (u.i == 0 && u.j == 0 && threadIdx.x == 0) a.fine[u.tensor] = fine;
+  if (u.i == 0 && u.j == 0 && tid == 0) a.fine[u.tensor] = fine;
   const float scale = kScale / (norm + a.eps);
   unsigned char* block = a.workspace + t.x[0] + block_at(u.i, u.j, padded_to(t.n, kTile) / kBlockK);
-  const int64_t r0 = int64_t(u.i) * kTile, c0 = int64_t(u.j) * kBlockK;
-  for (int k = threadIdx.x; k < kTile * (kBlockK / 8); k += kSplitThreads) {
-    // neighbouring threads go along the matrix's rows, which are X's columns where it is tall
-    const int r = t.tall ? k % kTile : k / (kBlockK / 8), chunk = t.tall ? k / kTile : k % (kBlockK / 8);
-    const int64_t row = r0 + r, col = c0 + 8 * chunk;
-    const int left = row < t.m ? int(min(max(t.n - col, int64_t(0)), int64_t(8))) : 0;
-    const int64_t at = t.tall ? col * t.cols + row : row * t.cols + col, step = t.tall ? t.cols : 1;
-    if (!LP_CHECK(left == 0 || (at >= 0 && at + (left - 1) * step < t.rows * t.cols), kChkCopyIndex)) continue;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const int left = left_of(k);
+    const int64_t i = at + k * next;
     float v[8];
-    if (!t.tall && t.wide && left == 8) {
-      float m[8];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 x = *reinterpret_cast<const float4*>(t.momentum + at + 4 * q);
-        m[4 * q] = x.x, m[4 * q + 1] = x.y, m[4 * q + 2] = x.z, m[4 * q + 3] = x.w;
-        if (t.grad_bf16) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.grad) + at + 4 * q));
-          v[4 * q] = __uint_as_float(w.x << 16), v[4 * q + 1] = __uint_as_float(w.x & 0xffff0000u);
-          v[4 * q + 2] = __uint_as_float(w.y << 16), v[4 * q + 3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + at + 4 * q));
-          v[4 * q] = w.x, v[4 * q + 1] = w.y, v[4 * q + 2] = w.z, v[4 * q + 3] = w.w;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = momentum_of(a, v[j], m[j]);
-        v[j] = update_of(a, v[j], m[j]) * scale;
-      }
-      if (fine)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          *reinterpret_cast<float4*>(t.momentum + at + 4 * q) =
-              make_float4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = 0.f;
-        if (j >= left) continue;
-        const float g = grad_at(t, at + j * step), m = momentum_of(a, g, t.momentum[at + j * step]);
-        if (fine) t.momentum[at + j * step] = m;
-        v[j] = update_of(a, g, m) * scale;
-      }
+    for (int j = 0; j < 8; ++j) {
+      m[k][j] = momentum_of(a, g[k][j], m[k][j]);
+      v[j] = fine ? update_of(a, g[k][j], m[k][j]) * scale : 0.f;
     }
-    if (!fine)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
     uint4 hi, lo;
     split8(v, hi, lo);
-    *reinterpret_cast<uint4*>(block + chunk_at(r, chunk)) = hi;
-    *reinterpret_cast<uint4*>(block + kHalf + chunk_at(r, chunk)) = lo;
+    const uint32_t in = chunk_at(r + k * next_r, chunk + k * next_chunk);
+    *reinterpret_cast<uint4*>(block + in) = hi;
+    *reinterpret_cast<uint4*>(block + kHalf + in) = lo;
+    if (!fine || !LP_CHECK(left == 0 || (i >= 0 && i + (left - 1) * step < t.rows * t.cols), kChkCopyIndex)) continue;
+    if (wide && left == 8) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float4*>(t.momentum + i + 4 * q) =
+            make_float4(m[k][4 * q], m[k][4 * q + 1], m[k][4 * q + 2], m[k][4 * q + 3]);
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) t.momentum[i + j * step] = m[k][j];
   }
 }
 
@@ -229,10 +247,17 @@ __global__ void __launch_bounds__(kSplitThreads)
 // A stage of the ring: 64 of K of A's and of B's tile.
 constexpr int kStages = 3;
 constexpr uint32_t kStage = 2 * kBlock;
-constexpr int kBars = 2 * kStages + 5;
+constexpr int kBars = 2 * kStages + 6;
 constexpr uint32_t kOut = kStages * kStage;  // the epilogue's 32 KB
 constexpr int kSmem = 1024 + int(kOut + kBlock) + kBars * 8 + 16;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 
 // kind::f16 with float16 operands and float32 accumulators, M = 128; bits 15 and 16 say that A and B are M-
 // and N-major.
@@ -338,59 +363,68 @@ __device__ __forceinline__ void write_tile(const float (&x)[kTile / 2], int r, i
 }
 
 // The step's last product: the parameters from the 64 columns in x, rows `row` on and columns `col` on of X,
-// lanes along the parameters' rows.  All loads of a turn are on their way before its first store.  slots: 4 KB
-// of the warp's own.
-__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, bool fine, int64_t row,
-                                             int64_t col, int lane, const float (&x)[kTile / 2], float* slots,
-                                             bool poison) {
+// lanes along the parameters' rows.  The record's entries are read before the first store, which might be to
+// them as far as the compiler knows, and all loads of a turn are on their way before its first store: with
+// both left to the compiler a tile took 35 us.  slots: 4 KB of the warp's own.
+__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, bool fine, int row, int col,
+                                             int lane, const float (&x)[kTile / 2], float* slots, bool poison) {
   if (!fine) return;
   const double l = a.lr * double(t.lr_scale);
   const float keep = float(1.0 - l * double(t.weight_decay));
   const float rate = poison ? __int_as_float(0x7fc00000)
                             : float(l * double(t.update_scale)) * (kUnscale * kUnscale);
-  const auto put = [&](int64_t at, float p, float v) {
-    p = __fmaf_rn(-rate, v, p * keep);
-    t.param[at] = p;
-    if (t.copy != nullptr) t.copy[at] = __float2bfloat16_rn(p);
+  const bool tall = t.tall != 0;
+  const int64_t cols = t.cols;
+  // X's rows and columns from here on; lanes go along `across`
+  const int rows_left = int(t.m) - row, cols_left = int(t.n) - col;
+  if (!LP_CHECK(row >= 0 && col >= 0 && rows_left <= t.m, kChkOutBox)) return;
+  float* const param = t.param + (tall ? int64_t(col) * cols + row : int64_t(row) * cols + col) + lane;
+  __nv_bfloat16* copy = t.copy;
+  if (copy != nullptr) copy += param - t.param;
+  constexpr int kTurn = 16;
+  // `n` rows of the parameters, a lane's element of each: their loads, then their stores
+  const auto turn = [&](float* p, __nv_bfloat16* c, int n, const float (&v)[kTurn]) {
+    float old[kTurn];
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) old[j] = j < n ? p[j * cols] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) old[j] = __fmaf_rn(-rate, v[j], old[j] * keep);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j)
+      if (j < n) p[j * cols] = old[j];
+    if (c == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j)
+      if (j < n) c[j * cols] = __float2bfloat16_rn(old[j]);
   };
-  if (!LP_CHECK(row >= 0 && col >= 0, kChkOutBox)) return;
-  if (t.tall) {  // X's rows are the parameters' columns: so are the lanes
-    const int64_t at = col * t.cols + row + lane;
-    const bool mine = row + lane < t.m;
+  if (tall) {  // X's rows are the parameters' columns: so are the lanes
+    const bool mine = lane < rows_left;
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
-      float p[16];
+    for (int c = 0; c < kTile / 2; c += kTurn) {
+      float v[kTurn];
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        p[j] = mine && col + c + j < t.n ? t.param[at + (c + j) * t.cols] : 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (mine && col + c + j < t.n) put(at + (c + j) * t.cols, p[j], x[c + j]);
+      for (int j = 0; j < kTurn; ++j) v[j] = x[c + j];
+      turn(param + c * cols, copy != nullptr ? copy + c * cols : nullptr, mine ? cols_left - c : 0, v);
     }
     return;
   }
   // a warp's 32 rows, 32 columns at a time, through shared memory
 #pragma unroll
-  for (int c = 0; c < 64; c += 32) {
+  for (int c = 0; c < kTile / 2; c += 32) {
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       *reinterpret_cast<float4*>(slots + lane * 32 + ((q ^ (lane & 7)) << 2)) =
           make_float4(x[c + 4 * q], x[c + 4 * q + 1], x[c + 4 * q + 2], x[c + 4 * q + 3]);
     __syncwarp();
-    const int64_t column = col + c + lane;
-    float* const out = t.param + row * t.cols + column;
-#pragma unroll 1
-    for (int from = 0; from < 32; from += 16) {
-      float p[16];
+    const bool mine = c + lane < cols_left;
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        p[r] = row + from + r < t.m && column < t.n ? out[(from + r) * t.cols] : 0.f;
+    for (int from = 0; from < 32; from += kTurn) {
+      float v[kTurn];
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (row + from + r < t.m && column < t.n)
-          put((row + from + r) * t.cols + column, p[r],
-              slots[(from + r) * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]);
+      for (int j = 0; j < kTurn; ++j)
+        v[j] = slots[(from + j) * 32 + (((lane >> 2) ^ (j & 7)) << 2) + (lane & 3)];
+      turn(param + from * cols + c, copy != nullptr ? copy + from * cols + c : nullptr, mine ? rows_left - from : 0, v);
     }
   }
 }
@@ -436,13 +470,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
   const auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4);
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4), tile_bar = drain_bar + 8u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, step = gridDim.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full_bar(s), 1), mbar_init(empty_bar(s), 1);
     for (int b = 0; b < 2; ++b) mbar_init(tfull_bar(b), 1), mbar_init(tempty_bar(b), kOutWarps);
     mbar_init(drain_bar, 1);
+    mbar_init(tile_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
@@ -576,27 +611,46 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int64_t cols = padded_to(kProduct == kApply ? t.n : t.m, kTile) / kBlockK;
       const int64_t block = block_at(u.i, 2 * int64_t(u.j), cols);
       float x[kMine];  // the chunks' sums, rounded to nearest
+      int go = 1;
       if (kProduct == kPoly) {
-        // c (G G + b / c G): what G adds comes in while the first products run
-        const unsigned char* g = a.workspace + t.g + block + half * int64_t(kBlock);
+        // c (G G + b / c G): what G adds comes in while the first products run, the hi parts of both blocks, then
+        // the lo parts, through the tile's way out.  (Read from global memory, 16 bytes a lane of 32 rows, it took
+        // 4 us of a launch's 13.)
 #pragma unroll
-        for (int q = 0; q < kMine / 8; ++q) {
-          const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(g + chunk_at(r, q)));
-          const uint4 lo = __ldcg(reinterpret_cast<const uint4*>(g + kHalf + chunk_at(r, q)));
-          const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+        for (int lo = 0; lo < 2; ++lo) {
+          if (first_thread) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the buffer is free
+            mbar_arrive_expect_tx(tile_bar, kBlock);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
-            x[8 * q + 2 * i] = (v.x + w.x) * (kB / kC * kScale);
-            x[8 * q + 2 * i + 1] = (v.y + w.y) * (kB / kC * kScale);
+            for (int q = 0; q < 2; ++q)
+              bulk_load(smem_u32(out) + q * kHalf, a.workspace + t.g + block + q * int64_t(kBlock) + lo * kHalf, kHalf,
+                        tile_bar);
           }
+          // every lane waits itself: what it reads has come by the barrier alone
+          go = __all_sync(0xffffffffu, go && wait_for(tile_bar, lo, abort_flag, a.err, kErrEpilogue));
+#pragma unroll
+          for (int q = 0; q < kMine / 8; ++q) {
+            uint32_t h[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                         : "r"(smem_u32(out) + half * kHalf + chunk_at(r, q))
+                         : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+              if (lo == 0) x[8 * q + 2 * i] = f.x, x[8 * q + 2 * i + 1] = f.y;
+              else {
+                x[8 * q + 2 * i] = (x[8 * q + 2 * i] + f.x) * (kB / kC * kScale);
+                x[8 * q + 2 * i + 1] = (x[8 * q + 2 * i + 1] + f.y) * (kB / kC * kScale);
+              }
+            }
+          }
+          epilogue_sync();  // the buffer has been read
         }
       } else {
 #pragma unroll
         for (int j = 0; j < kMine; ++j) x[j] = 0.f;
       }
-      int go = 1;
       for (int kb = 0; kb < k_blocks; kb += kChunk) {
         if (lane == 0) go = *abort_flag == 0 && wait_for(tfull_bar(acc), acc_phase, abort_flag, a.err, kErrEpilogue);
         go = __shfl_sync(0xffffffffu, go, 0);
@@ -624,9 +678,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         poison = true;
       }
       if (kProduct == kApply && last) {
-        write_params(a, t, a.fine[u.tensor] != 0, int64_t(u.i) * kTile + group * 32,
-                     int64_t(u.j) * kTile + half * kMine, lane, x, reinterpret_cast<float*>(out) + (warp - 4) * 1024,
-                     poison);
+        write_params(a, t, a.fine[u.tensor] != 0, u.i * kTile + group * 32, u.j * kTile + half * kMine, lane, x,
+                     reinterpret_cast<float*>(out) + (warp - 4) * 1024, poison);
         continue;
       }
       const int diagonal = (u.i - u.j) * kTile + r - half * kMine;  // where the row meets it in x
@@ -756,7 +809,7 @@ Building build_plan(const lp_muon_tensor* tensors, int64_t n_tensors) {
     const auto up = [](size_t v) { return (v + 1023) / 1024 * 1024; };
     size_t at = up(kWorkspaceHeader + size_t(n_tensors) * 4);
     batch.partials_at = int64_t(at);
-    at += up(size_t(parts) * sizeof(double));
+    at += up(size_t(parts) * sizeof(float));
     for (int32_t k : in) {
       MuonRecord& r = b.records[size_t(k)];
       const int64_t mp = padded_to(r.m, kTile), np = padded_to(r.n, kTile);
@@ -860,11 +913,11 @@ lp_status launch_muon_step(const Device& dev, const void* plan_host, const void*
   };
   for (int64_t k = 0; k < h.n_batches; ++k) {
     const MuonBatch& b = reinterpret_cast<const MuonBatch*>(host + h.batches_at)[k];
-    double* partials = reinterpret_cast<double*>(a.workspace + b.partials_at);
+    float* partials = reinterpret_cast<float*>(a.workspace + b.partials_at);
     if (!launch_next(lp_muon_norm_kernel, b.parts, kNormThreads, 0, false, stream, a,
                      units_at(h.parts_at, b.first_part), partials, int(k == 0)) ||
         !launch_next(lp_muon_split_kernel, b.blocks, kSplitThreads, 0, true, stream, a,
-                     units_at(h.blocks_at, b.first_block), static_cast<const double*>(partials)))
+                     units_at(h.blocks_at, b.first_block), static_cast<const float*>(partials)))
       return LP_ERR_CUDA;
     const lp_status st = launch_products(
         dev, map_a, map_b, a, b, units_at(h.gram_at, b.first_gram), units_at(h.apply_at, b.first_apply), steps,
