@@ -47,13 +47,14 @@ constexpr uint32_t kBlock = 2 * kHalf;
 // tensor core cuts sums off where an addition would round: over K of 1000 the singular values came
 // out 8e-6 off, five times what float32 products give; in chunks it is what 16 of its steps cut off.
 constexpr int kChunk = 8;
+constexpr int kSplitBlocks = 16;  // K blocks from which on a tile's K is in segments
 constexpr uint32_t kAccumulator = 2 * kTile;     // tensor-memory columns
 constexpr int kOutThreads = 256;                 // of the epilogue: two a row of the tile
 constexpr int kOutWarps = kOutThreads / 32;
 constexpr int kProductThreads = 128 + kOutThreads;
 // Registers of a thread: what the launch gives, and how the epilogue's two warpgroups, which hold the
-// tile's sums, take from the other: 40 + 2 * 232 = 3 * 168.
-constexpr int kFewRegisters = 40, kManyRegisters = 232;
+// tile's sums, take from the other: 56 + 2 * 224 = 3 * 168.
+constexpr int kFewRegisters = 56, kManyRegisters = 224;
 constexpr int kNormThreads = 256;
 constexpr int kSplitThreads = 256;
 
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     for (int j = 0; j < 8; ++j)
       if (j < left) t.momentum[i + j * step] = m[k][j];
   }
+  asm volatile("fence.proxy.async.global;" ::: "memory");  // the next launch reads X by bulk copies
 }
 
 // ------------------------------------------------------------------------- products
@@ -298,6 +300,21 @@ __device__ __forceinline__ Operands operands_of(const MuonRecord& t, int from) {
   if (kProduct == kPoly) return {g, g, g_blocks, g_blocks, k};
   return {p, x, g_blocks, x_blocks, k};
 }
+// K in segments, by its length alone, whose sums are added in order: a tile's bits are the same whether one CTA
+// goes through them or each is another CTA's.
+constexpr int kSplits = 4;
+struct Segments {
+  int blocks, shift;
+  __device__ __forceinline__ explicit Segments(int k_blocks) : blocks(k_blocks), shift(k_blocks >= kSplitBlocks ? 2 : 0) {}
+  __device__ __forceinline__ int count() const { return 1 << shift; }
+  __device__ __forceinline__ int begin(int s) const { return s * blocks >> shift; }
+  // those of a CTA: all, or of a cluster each CTA one
+  template <bool kSplit>
+  __device__ __forceinline__ int first(uint32_t rank) const { return kSplit ? min(int(rank), count()) : 0; }
+  template <bool kSplit>
+  __device__ __forceinline__ int last(uint32_t rank) const { return kSplit ? min(int(rank) + 1, count()) : count(); }
+};
+static_assert(kSplits == 1 << 2, "the shift");
 // G and P are symmetric, and only the blocks of their tiles on and below the diagonal are written.  Whether
 // columns 64 kb on of row block i lie above it: they are then read where they mirror to, as an operand that is
 // contiguous along M or N.
@@ -452,10 +469,76 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   return wait_long(bar, parity, abort_flag, err, role);
 }
 
+// A cluster's way out.  CTA q takes columns 16 q .. 16 q + 15 of each half of the tile: every CTA writes its
+// segment's sums of them into that one's ring, which nothing reads any more, and each adds up what it has got,
+// in the segments' order, to its own x.
+template <int kProduct>
+__device__ __forceinline__ void write_split(const MuonArgs& a, const MuonRecord& t, const MuonUnit& u,
+                                            const Segments& segments, uint32_t rank, const float (&x)[kTile / 2],
+                                            const float (&y)[kTile / 2], int r, int half, uint8_t* ring, int64_t block) {
+  constexpr int kSlice = kTile / 2 / kSplits;
+  const int thread = half * kTile + r;
+  cluster_sync();  // every CTA's products are done
+  const uint32_t mine = smem_u32(ring) + thread * 16;
+  // [segment][four columns][thread]
+  constexpr uint32_t kGroup = kOutThreads * 16, kPart = kSlice / 4 * kGroup;
+  if (int(rank) < segments.count())
+#pragma unroll
+    for (int q = 0; q < kSplits; ++q) {
+      const uint32_t to = cluster_addr(mine + rank * kPart, q);
+#pragma unroll
+      for (int k = 0; k < kSlice / 4; ++k)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + k * kGroup),
+                     "f"(y[q * kSlice + 4 * k]), "f"(y[q * kSlice + 4 * k + 1]), "f"(y[q * kSlice + 4 * k + 2]),
+                     "f"(y[q * kSlice + 4 * k + 3])
+                     : "memory");
+    }
+  cluster_sync();
+  float e[kSlice];
+#pragma unroll
+  for (int q = 0; q < kSplits; ++q)
+    if (q == int(rank))
+#pragma unroll
+      for (int j = 0; j < kSlice; ++j) e[j] = x[q * kSlice + j];
+  for (int s = 0; s < segments.count(); ++s)
+#pragma unroll
+    for (int k = 0; k < kSlice / 4; ++k) {
+      float v[4];
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                   : "r"(mine + s * kPart + k * kGroup)
+                   : "memory");
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[4 * k + j] += v[j];
+    }
+  const int column = half * (kTile / 2) + int(rank) * kSlice, diagonal = (u.i - u.j) * kTile + r - column;
+#pragma unroll
+  for (int j = 0; j < kSlice; ++j) {
+    e[j] *= kProduct == kPoly ? kC * kUnscale : kUnscale;
+    if (kProduct == kPoly && j == diagonal) e[j] += kA * kScale;
+  }
+  unsigned char* to = a.workspace + (kProduct == kGram ? t.g : t.p) + block + half * int64_t(kBlock);
+  if (!LP_CHECK(block >= 0, kChkOutBox)) return;
+#pragma unroll
+  for (int q = 0; q < kSlice / 8; ++q) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = e[8 * q + j];
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    const uint32_t in = chunk_at(r, int(rank) * (kSlice / 8) + q);
+    *reinterpret_cast<uint4*>(to + in) = hi;
+    *reinterpret_cast<uint4*>(to + kHalf + in) = lo;
+  }
+  asm volatile("fence.proxy.async.global;" ::: "memory");  // the next launch reads it by bulk copies
+}
+
 // One product over `units` tiles.  from: which X is read; last: P X goes into the parameters instead of
 // the other X.  map_a, map_b: the workspace as rows of 128 bytes, in boxes of 256 and of 64.  withhold
 // (tests of the bounded waits only): the first copy is announced and not made.
-template <int kProduct>
+// kSplit: a cluster of kSplits CTAs a tile, each with a segment of K; they trade sums, so that each writes 16 of
+// each 64 columns.  (The grid has a cluster for every unit.)
+template <int kProduct, bool kSplit>
 __global__ void __launch_bounds__(kProductThreads, 1)
     lp_muon_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                            const __grid_constant__ MuonArgs a, const MuonUnit* units, int n_units, int from,
@@ -471,7 +554,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   const auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4), tile_bar = drain_bar + 8u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, step = gridDim.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = kSplit ? blockIdx.x / kSplits : blockIdx.x, step = kSplit ? gridDim.x / kSplits : gridDim.x;
+  const uint32_t rank = kSplit ? cluster_rank() : 0u;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full_bar(s), 1), mbar_init(empty_bar(s), 1);
@@ -497,6 +582,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kSplit) cluster_sync();  // the cluster's CTAs are there
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the operands are written
@@ -513,7 +599,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
         const Operands o = operands_of<kProduct>(a.records[u.tensor], from);
         const bool same = kProduct != kApply && u.i == u.j;
-        for (int kb = 0; kb < o.k_blocks; ++kb) {
+        const Segments segments(o.k_blocks);
+        const int kb_end = segments.begin(segments.template last<kSplit>(rank));
+        for (int kb = segments.begin(segments.template first<kSplit>(rank)); kb < kb_end; ++kb) {
           if (!wait_for(empty_bar(stage), phase ^ 1u, abort_flag, a.err, kErrLoader)) {
             ok = false;
             break;
@@ -557,32 +645,41 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
         const int k_blocks = operands_of<kProduct>(a.records[u.tensor], from).k_blocks;
         const bool same = kProduct != kApply && u.i == u.j;
-        for (int kb = 0; kb < k_blocks; ++kb) {
-          const uint32_t d = tmem_base + uint32_t(acc) * kAccumulator;
-          const bool begins = kb % kChunk == 0;
-          if ((begins && !wait_for(tempty_bar(acc), acc_phase ^ 1u, abort_flag, a.err, kErrMma)) ||
-              !wait_for(full_bar(stage), phase, abort_flag, a.err, kErrMma)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * kStage), sb = same ? sa : sa + kBlock;
-          const bool a_mn = kProduct != kGram && mirrored(u.i, kb);
-          const bool b_mn = kProduct == kApply || (kProduct == kPoly && mirrored(u.j, kb));
-          const uint64_t hi = a_mn ? sw128_mn_desc(sa, kHalf / 2) : sw128_desc(sa), lo = hi + (kHalf >> 4);
-          const uint64_t b = b_mn ? sw128_mn_desc(sb, kHalf / 2) : sw128_desc(sb);
-          // of a step of 16 of K, in the descriptors' units: 8 rows of 128 bytes twice, or 32 bytes of a row
-          const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-          const uint32_t major = uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16;
+        const Segments segments(k_blocks);
+        const int to = segments.template last<kSplit>(rank);
+        for (int segment = segments.template first<kSplit>(rank); ok && segment < to; ++segment) {
+          const int end = segments.begin(segment + 1);
+          int kb = segments.begin(segment);
+          while (ok && kb < end) {  // a chunk
+            const int chunk_end = min(kb + kChunk, end);
+            const uint32_t d = tmem_base + uint32_t(acc) * kAccumulator;
+            uint32_t adds = 0;
+            if (!wait_for(tempty_bar(acc), acc_phase ^ 1u, abort_flag, a.err, kErrMma)) ok = false;
+            for (; ok && kb < chunk_end; ++kb) {
+              if (!wait_for(full_bar(stage), phase, abort_flag, a.err, kErrMma)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(smem + stage * kStage), sb = same ? sa : sa + kBlock;
+              const bool a_mn = kProduct != kGram && mirrored(u.i, kb);
+              const bool b_mn = kProduct == kApply || (kProduct == kPoly && mirrored(u.j, kb));
+              const uint64_t hi = a_mn ? sw128_mn_desc(sa, kHalf / 2) : sw128_desc(sa), lo = hi + (kHalf >> 4);
+              const uint64_t b = b_mn ? sw128_mn_desc(sb, kHalf / 2) : sw128_desc(sb);
+              // of a step of 16 of K, in the descriptors' units: 8 rows of 128 bytes twice, or 32 bytes of a row
+              const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+              const uint32_t major = uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16;
 #pragma unroll
-          for (int k = 0; k < kBlockK / kUmmaK; ++k) {
-            // hi x [hi; lo] as one of N = 256, and lo x hi onto its second half
-            tc_mma_single(d, hi + k * a_step, b + k * b_step, !begins || k != 0, idesc_half(2 * kTile) | major);
-            tc_mma_single(d + kTile, lo + k * a_step, b + k * b_step, 1u, idesc_half(kTile) | major);
-          }
-          tc_commit_local(empty_bar(stage));
-          if (++stage == kStages) stage = 0, phase ^= 1u;
-          if (kb % kChunk == kChunk - 1 || kb == k_blocks - 1) {
+              for (int k = 0; k < kBlockK / kUmmaK; ++k) {
+                // hi x [hi; lo] as one of N = 256, and lo x hi onto its second half
+                tc_mma_single(d, hi + k * a_step, b + k * b_step, adds, idesc_half(2 * kTile) | major);
+                tc_mma_single(d + kTile, lo + k * a_step, b + k * b_step, 1u, idesc_half(kTile) | major);
+                adds = 1;
+              }
+              tc_commit_local(empty_bar(stage));
+              if (++stage == kStages) stage = 0, phase ^= 1u;
+            }
+            if (!ok) break;
             tc_commit_local(tfull_bar(acc));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -591,6 +688,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       tc_commit_local(drain_bar);
       drain_wait(drain_bar, 0);
+    }
+    if constexpr (kSplit) {  // the epilogues' meetings
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -605,7 +707,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     bool poison = last && *reinterpret_cast<volatile uint32_t*>(a.err) != 0u;
     for (int n = first; n < n_units; n += step) {
       const MuonUnit u = units[n];
-      if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) break;
+      if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) {
+        if constexpr (kSplit) cluster_sync(), cluster_sync();  // the cluster's other warps wait there
+        break;
+      }
       const MuonRecord& t = a.records[u.tensor];
       const int k_blocks = operands_of<kProduct>(t, from).k_blocks;
       const int64_t cols = padded_to(kProduct == kApply ? t.n : t.m, kTile) / kBlockK;
@@ -651,26 +756,41 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
         for (int j = 0; j < kMine; ++j) x[j] = 0.f;
       }
-      for (int kb = 0; kb < k_blocks; kb += kChunk) {
-        if (lane == 0) go = *abort_flag == 0 && wait_for(tfull_bar(acc), acc_phase, abort_flag, a.err, kErrEpilogue);
-        go = __shfl_sync(0xffffffffu, go, 0);
-        if (!go) break;
-        tc_fence_after();
-        const uint32_t at = t_lane + uint32_t(acc) * kAccumulator;
+      const Segments segments(k_blocks);
+      float y[kMine];  // a segment's
+      for (int segment = segments.template first<kSplit>(rank); segment < segments.template last<kSplit>(rank) && go;
+           ++segment) {
 #pragma unroll
-        for (int c = 0; c < kMine; c += 32) {
-          uint32_t v[32], w[32];  // hi hi, and the rest
-          tmem_load32(at + c, v);
-          tmem_load32(at + kTile + c, w);
-          tmem_wait();
+        for (int j = 0; j < kMine; ++j) y[j] = 0.f;
+        for (int kb = segments.begin(segment); kb < segments.begin(segment + 1); kb += kChunk) {
+          if (lane == 0) go = *abort_flag == 0 && wait_for(tfull_bar(acc), acc_phase, abort_flag, a.err, kErrEpilogue);
+          go = __shfl_sync(0xffffffffu, go, 0);
+          if (!go) break;
+          tc_fence_after();
+          const uint32_t at = t_lane + uint32_t(acc) * kAccumulator;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[c + j] += __uint_as_float(v[j]) + __uint_as_float(w[j]);
+          for (int c = 0; c < kMine; c += 32) {
+            uint32_t v[32], w[32];  // hi hi, and the rest
+            tmem_load32(at + c, v);
+            tmem_load32(at + kTile + c, w);
+            tmem_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[c + j] += __uint_as_float(v[j]) + __uint_as_float(w[j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(tempty_bar(acc));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(tempty_bar(acc));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        if constexpr (!kSplit) {
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) x[j] += y[j];
+        }
+      }
+      if constexpr (kSplit) {
+        write_split<kProduct>(a, t, u, segments, rank, x, y, r, half, smem, block);
+        continue;  // the grid's clusters have a unit each
       }
       // every warp of the CTA goes on, or none does: they meet at the tile's way out
       if (!epilogue_all(go)) {  // the tiles that are left have no result
@@ -707,18 +827,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 // ------------------------------------------------------------------------- host
 
 template <class... Params, class... Args>
-bool launch_next(void (*kernel)(Params...), int64_t blocks, int threads, int smem, bool dependent, cudaStream_t stream,
+bool launch_next(void (*kernel)(Params...), int64_t blocks, int threads, int smem, bool dependent, int cluster,
+                 cudaStream_t stream,
                  const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(blocks));
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cudaLaunchAttribute attrs[2];
+  cfg.attrs = attrs;
+  if (dependent) {
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attrs[cfg.numAttrs].val.clusterDim.x = unsigned(cluster);
+    attrs[cfg.numAttrs].val.clusterDim.y = attrs[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
@@ -783,6 +911,8 @@ Building build_plan(const lp_muon_tensor* tensors, int64_t n_tensors) {
       r.part = padded_to(std::max(kMuonPart, (r.rows * r.cols + 1023) / 1024), 4);
       r.parts = (r.rows * r.cols + r.part - 1) / r.part;
       parts += r.parts;
+      batch.most_m = std::max(batch.most_m, r.m);
+      batch.most_n = std::max(batch.most_n, r.n);
       for (int64_t p = 0; p < r.parts; ++p) b.parts.push_back({k, int32_t(p), 0, 0});
       const int64_t mb = padded_to(r.m, kTile) / kTile, nb = padded_to(r.n, kTile) / kTile;
       for (int64_t x = 0; x < mb; ++x)
@@ -871,9 +1001,11 @@ static lp_status launch_products(const Device& dev, const CUtensorMap& map_a, co
                                  int steps, bool withhold, cudaStream_t stream) {
   static PerContextOnce once;
   if (once.run(dev.ctx_id, [] {
-        for (const void* k : {reinterpret_cast<const void*>(lp_muon_product_kernel<kGram>),
-                              reinterpret_cast<const void*>(lp_muon_product_kernel<kPoly>),
-                              reinterpret_cast<const void*>(lp_muon_product_kernel<kApply>)}) {
+        for (const void* k : {reinterpret_cast<const void*>(lp_muon_product_kernel<kGram, false>),
+                              reinterpret_cast<const void*>(lp_muon_product_kernel<kPoly, false>),
+                              reinterpret_cast<const void*>(lp_muon_product_kernel<kApply, false>),
+                              reinterpret_cast<const void*>(lp_muon_product_kernel<kGram, true>),
+                              reinterpret_cast<const void*>(lp_muon_product_kernel<kPoly, true>)}) {
           const cudaError_t e = set_smem_limit(k, kSmem);
           if (e != cudaSuccess) return e;
         }
@@ -882,13 +1014,23 @@ static lp_status launch_products(const Device& dev, const CUtensorMap& map_a, co
     return LP_ERR_CUDA;
   for (int s = 0; s < steps; ++s) {
     const int from = s & 1, last = s == steps - 1;
-    const auto launch = [&](auto* kernel, const MuonUnit* units, int64_t n, int is_last, int first) {
-      return launch_next(kernel, single_grid(dev.sm_count, n), kProductThreads, kSmem, true, stream, map_a, map_b, a,
-                         units, int(n), from, is_last, first);
+    const auto launch = [&](auto* kernel, int64_t grid, int cluster, const MuonUnit* units, int64_t n, int is_last,
+                            int first) {
+      return launch_next(kernel, grid, kProductThreads, kSmem, true, cluster, stream, map_a, map_b, a, units, int(n),
+                         from, is_last, first);
     };
-    if (!launch(lp_muon_product_kernel<kGram>, gram, b.grams, 0, int(s == 0 && withhold)) ||
-        !launch(lp_muon_product_kernel<kPoly>, gram, b.grams, 0, 0) ||
-        !launch(lp_muon_product_kernel<kApply>, apply, b.applies, last, 0))
+    const int withheld = s == 0 && withhold;
+    const int64_t few = single_grid(dev.sm_count, b.grams), many = single_grid(dev.sm_count, b.applies);
+    // A cluster a tile while all clusters fit, where there is a K to split: 2047 x 1021 (36 tiles of K 2048 and
+    // 1024) takes 208 us a step so, 268 with a CTA a tile.
+    const bool split = b.grams * kSplits <= dev.sm_count && few == b.grams;
+    const bool split_gram = split && b.most_n > (kSplitBlocks - 1) * kBlockK,
+               split_poly = split && b.most_m > (kSplitBlocks - 1) * kBlockK;
+    if (!(split_gram ? launch(lp_muon_product_kernel<kGram, true>, b.grams * kSplits, kSplits, gram, b.grams, 0, withheld)
+                     : launch(lp_muon_product_kernel<kGram, false>, few, 1, gram, b.grams, 0, withheld)) ||
+        !(split_poly ? launch(lp_muon_product_kernel<kPoly, true>, b.grams * kSplits, kSplits, gram, b.grams, 0, 0)
+                     : launch(lp_muon_product_kernel<kPoly, false>, few, 1, gram, b.grams, 0, 0)) ||
+        !launch(lp_muon_product_kernel<kApply, false>, many, 1, apply, b.applies, last, 0))
       return LP_ERR_CUDA;
   }
   return LP_OK;
@@ -914,9 +1056,9 @@ lp_status launch_muon_step(const Device& dev, const void* plan_host, const void*
   for (int64_t k = 0; k < h.n_batches; ++k) {
     const MuonBatch& b = reinterpret_cast<const MuonBatch*>(host + h.batches_at)[k];
     float* partials = reinterpret_cast<float*>(a.workspace + b.partials_at);
-    if (!launch_next(lp_muon_norm_kernel, b.parts, kNormThreads, 0, false, stream, a,
+    if (!launch_next(lp_muon_norm_kernel, b.parts, kNormThreads, 0, false, 1, stream, a,
                      units_at(h.parts_at, b.first_part), partials, int(k == 0)) ||
-        !launch_next(lp_muon_split_kernel, b.blocks, kSplitThreads, 0, true, stream, a,
+        !launch_next(lp_muon_split_kernel, b.blocks, kSplitThreads, 0, true, 1, stream, a,
                      units_at(h.blocks_at, b.first_block), static_cast<const float*>(partials)))
       return LP_ERR_CUDA;
     const lp_status st = launch_products(

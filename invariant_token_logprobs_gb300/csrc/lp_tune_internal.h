@@ -80,7 +80,8 @@ struct MuonUnit {
 // Matrices that go through the launches together; where their units begin, and how many.
 struct MuonBatch {
   int64_t first_part, parts, first_block, blocks, first_gram, grams, first_apply, applies;
-  int64_t partials_at;  // in the workspace
+  int64_t partials_at;       // in the workspace
+  int64_t most_m, most_n;    // of its matrices
 };
 struct MuonHeader {
   int64_t magic, bytes, n_tensors, n_batches, workspace;

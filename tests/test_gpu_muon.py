@@ -114,6 +114,13 @@ def test_large():
     run([(1024, 1536), (2100, 1100)], BF16, copy=False)
 
 
+@pytest.mark.parametrize("shape", [(1024, 1024), (1100, 1000), (130, 4100), (2500, 60), (1023, 1025), (257, 8000)])
+def test_split_over_clusters(shape):
+    """Few tiles of a long K: a cluster a tile.  K that is no multiple of the segments, and one that only the first
+    product has."""
+    run([shape], BF16)
+
+
 def test_several_turns_of_all_ctas():
     """More tiles than there are SMs, of many matrices and of one."""
     run([(300, 200), (129, 1000), (257, 140), (64, 64)] * 25, BF16, copy=False)
@@ -152,7 +159,8 @@ def test_steps_go_on_and_a_state_continues():
 
 
 def test_a_matrix_has_the_bits_that_it_has_alone():
-    shapes = [(300, 140), (129, 500), (64, 64)]
+    """Also where K is split over a cluster's CTAs when few tiles are left to the GPU: alone, not in the batch."""
+    shapes = [(300, 140), (129, 1500), (64, 64), (900, 2100), (4000, 100)]
     params, grads, _, _ = matrices(shapes, BF16)
     alone = [p.clone() for p in params]
     tune.Muon(params, grads).step()
