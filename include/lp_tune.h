@@ -115,10 +115,8 @@ LP_API lp_status lp_layer_norm_backward(
  * not count have no gradient whatever they hold (their logp is NaN where the
  * target is padding), and neither do the rows of pairs that do not count.
  *
- * A sequence's sums are held to 48 bits or more and everything of a pair in
- * float64 (the exponential in float32), each output rounded once: differences
- * of sums of 10^5 rows keep float32's precision.  The sums are taken in a fixed
- * order.
+ * Sums, scores and z are held as pairs of float32, to 48 bits: differences of sums
+ * of 10^5 rows keep float32's precision.  The sums are taken in a fixed order.
  * ------------------------------------------------------------------------ */
 
 typedef enum lp_preference {
@@ -140,8 +138,8 @@ LP_API size_t lp_preference_loss_workspace_size(int64_t T, int64_t n_sequences);
  *   n_sequences     even.  Pair i is of the sequences 2 i (chosen) and 2 i + 1
  *                   (rejected), or with `halves` of i and i + n_sequences / 2.
  *   kind            an lp_preference.
- *   beta > 0, margin, 0 <= label_smoothing <= 1 (0 unless SIGMOID), nll_coef: finite;
- *                   with an nll_coef of 0 the term is in the stats alone, whatever it holds.
+ *   beta > 0, margin, 0 <= label_smoothing <= 1 (0 unless SIGMOID), nll_coef: finite in
+ *                   float32, beta and 1 / beta no subnormals; with an nll_coef of 0 the term is in the stats alone, whatever it holds.
  *   stats           [6] float32: the loss, and the means over the counted pairs of the
  *                   loss without the nll term, of the chosen's -logp, of s_c > s_r, and of
  *                   beta s_c and beta s_r.

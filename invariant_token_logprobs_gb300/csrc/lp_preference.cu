@@ -9,9 +9,10 @@
 //   rows   as in the first, a warp takes kChunk rows and writes their gradients.
 // Bound by HBM: 9 bytes a row in, the mask again and 4 bytes out.
 //
-// The difference of two sums of 10^5 rows is what counts, to a few units of float32: a lane's sums
-// are float pairs (Knuth's two-sum), everything past the lane is float64.  Every sum is taken in a
-// fixed order: a lane's rows, the lanes' tree, the chunks of a sequence in order.
+// The difference of two sums of 10^5 rows is what counts, to a few units of float32: sums, scores and
+// z are float pairs (Knuth's two-sum and products by fma), 48 bits.  In float64, at 1/64 of the rate
+// here, the same took 53 us instead of TODO for 512 pairs.  Every sum is taken in a fixed order: a
+// lane's rows, the lanes' tree, the chunks of a sequence in order.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,18 +35,8 @@ constexpr int kGroups = 4;                // of 4 rows, a lane
 constexpr int kChunk = kGroups * 4 * 32;  // rows of a warp
 constexpr int kPairThreads = 64;
 
-// A sequence's sums over its counted rows, whole or of one chunk.
-struct Sums {
-  double logp, ref;
-  int64_t count;
-};
-// What a CTA of the pairs' kernel adds to the call's sums.
-struct Part {
-  double loss, nll, right, chosen, rejected;
-  int64_t count;
-};
-
-// s + e is the sum of float32 values to about 48 bits; once s is no number or infinite, e is nothing.
+// s + e is a value to about 48 bits, |e| at most some units in the last place of s.  Once s is no number or
+// infinite, e is nothing.
 struct Two {
   float s = 0.f, e = 0.f;
   __device__ __forceinline__ void add(float x) {
@@ -53,25 +44,75 @@ struct Two {
     e += (s - (t - b)) + (x - b);
     s = t;
   }
-  __device__ __forceinline__ double value() const {
-    return fabsf(s) <= 0x1.fffffep127f ? double(s) + double(e) : double(s);
+  __device__ __forceinline__ void add(const Two& x) {
+    add(x.s);
+    e += x.e;
+  }
+  __device__ __forceinline__ bool finite() const { return fabsf(s) <= 0x1.fffffep127f; }
+  __device__ __forceinline__ float value() const { return finite() ? s + e : s; }
+  // the same value with |e| at most half a unit of s
+  __device__ __forceinline__ Two settled() const {
+    Two t;
+    t.s = value();
+    t.e = finite() && t.finite() ? e - (t.s - s) : 0.f;
+    return t;
+  }
+  __device__ __forceinline__ Two negative() const {
+    Two t;
+    t.s = -s, t.e = -e;
+    return t;
+  }
+  __device__ __forceinline__ Two times(const Two& x) const {
+    Two t;
+    t.s = s * x.s;
+    t.e = __fmaf_rn(s, x.s, -t.s) + __fmaf_rn(s, x.e, e * x.s);
+    return t.settled();
+  }
+  __device__ __forceinline__ Two over(float n) const {
+    Two t;
+    t.s = s / n;
+    t.e = (__fmaf_rn(-t.s, n, s) + e) / n;
+    return t.settled();
+  }
+  __device__ __forceinline__ Two from_lane(int distance) const {
+    Two t;
+    t.s = __shfl_xor_sync(0xffffffffu, s, distance);
+    t.e = __shfl_xor_sync(0xffffffffu, e, distance);
+    return t;
   }
 };
-
-template <int kLanes>
-__device__ __forceinline__ double lane_sum(double v) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ Two two_of(const Pair32& v) {
+  Two t;
+  t.s = v.high, t.e = v.low;
+  return t;
 }
-__device__ __forceinline__ double sum_over(double v, int lanes) {
-  for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ Two sum_over(Two v, int lanes) {
+  for (int o = lanes / 2; o > 0; o /= 2) {
+    // the same on both sides: the lower lane's first
+    const Two other = v.from_lane(o);
+    const bool upper = (threadIdx.x & o) != 0;
+    Two a = upper ? other : v;
+    a.add(upper ? v : other);
+    v = a;
+  }
   return v;
 }
 __device__ __forceinline__ int64_t sum_over(int64_t v, int lanes) {
   for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+
+// A sequence's sums over its counted rows, whole or of one chunk.
+struct __align__(16) Sums {
+  Two logp, ref;
+  int64_t count, unused;
+};
+static_assert(sizeof(Sums) == 32, "two accesses of 16 bytes");
+// What a CTA of the pairs' kernel adds to the call's sums.
+struct Part {
+  Two loss, nll, right, chosen, rejected;
+  int64_t count;
+};
 
 // The sequences of pair i.
 __device__ __forceinline__ int64_t chosen_of(const PreferenceArgs& a, int64_t i) {
@@ -88,67 +129,91 @@ __device__ __forceinline__ int64_t row_of(const PreferenceArgs& a, int64_t i) {
 
 struct Pair {
   Part part;               // the pair's, all zeros when it does not count
-  double chosen, rejected; // d loss / d logp of a counted row, times the number of pairs
+  float chosen, rejected;  // d loss / d logp of a counted row, times the number of pairs
   float reward[2];
 };
-__device__ __forceinline__ double score_of(const PreferenceArgs& a, const Sums& s) {
-  const double v = a.ref_logp != nullptr ? s.logp - s.ref : s.logp;
-  return a.average && s.count > 0 ? v / double(s.count) : v;
+__device__ __forceinline__ Two score_of(const PreferenceArgs& a, const Sums& s) {
+  Two v = s.logp;
+  if (a.ref_logp != nullptr) v.add(s.ref.negative());
+  return a.average && s.count > 0 ? v.settled().over(float(s.count)) : v.settled();
+}
+__device__ __forceinline__ Two one(float x) {
+  Two t;
+  t.s = x;
+  return t;
 }
 __device__ __forceinline__ Pair pair_of(const PreferenceArgs& a, const Sums& c, const Sums& r) {
   Pair p{};
-  const double sc = score_of(a, c), sr = score_of(a, r);
-  p.reward[0] = float(a.beta * sc);
-  p.reward[1] = float(a.beta * sr);
+  const Two sc = score_of(a, c), sr = score_of(a, r), beta = two_of(a.beta);
+  const Two rc = beta.times(sc), rr = beta.times(sr);
+  p.reward[0] = rc.value();
+  p.reward[1] = rr.value();
   if (c.count == 0 || r.count == 0) return p;
-  const double z = a.beta * (sc - sr) - a.margin;
-  double slope;
+  Two gap = sc;
+  gap.add(sr.negative());
+  gap = gap.settled();
+  Two z = beta.times(gap);
+  z.add(two_of(a.margin).negative());
+  z = z.settled();
+  float loss, slope;
   if (a.kind == LP_PREFERENCE_SIGMOID) {
-    // exp(-|z|) by float32's, of z's leading part, with the rest to first order: the float64 one
-    // takes hundreds of instructions at 1/64 of the rate
-    const double m = fabs(z);
-    const float high = float(m), low = high <= 0x1.fffffep127f ? float(m - double(high)) : 0.f;
+    // exp(-|z|) of z's leading part, and the rest to first order
+    const float high = fabsf(z.s), low = z.s < 0.f ? -z.e : z.e;
     const float e = expf(-high), small = e - e * low;
     const float log_part = log1pf(small), near = 1.f / (1.f + small), far = small * near;
     // softplus(-z), softplus(z), and their derivatives' sizes
-    const double down = z > 0 ? double(log_part) : m + double(log_part);
-    const double up = z > 0 ? m + double(log_part) : double(log_part);
-    const double to_down = z > 0 ? far : near, to_up = z > 0 ? near : far;
-    p.part.loss = (1.0 - a.smoothing) * down;
-    slope = -(1.0 - a.smoothing) * to_down;
-    if (a.smoothing != 0.0) {  // an infinite term without a weight is none
-      p.part.loss += a.smoothing * up;
+    const float down = z.s > 0.f ? log_part : high + (low + log_part);
+    const float up = z.s > 0.f ? high + (low + log_part) : log_part;
+    const float to_down = z.s > 0.f ? far : near, to_up = z.s > 0.f ? near : far;
+    const float rest = 1.f - a.smoothing;
+    loss = rest * down;
+    slope = -rest * to_down;
+    if (a.smoothing != 0.f) {  // an infinite term without a weight is none
+      loss += a.smoothing * up;
       slope += a.smoothing * to_up;
     }
-    if (z != z) p.part.loss = slope = z;
+    if (z.s != z.s) loss = slope = z.s;
   } else if (a.kind == LP_PREFERENCE_HINGE) {
-    p.part.loss = z < 1.0 ? 1.0 - z : z != z ? z : 0.0;
-    slope = z < 1.0 ? -1.0 : z != z ? z : 0.0;
+    Two left = one(1.f);
+    left.add(z.negative());
+    const float v = left.value();  // 1 - z
+    loss = v > 0.f ? v : v != v ? v : 0.f;
+    slope = v > 0.f ? -1.f : v != v ? v : 0.f;
   } else {
-    const double off = (z - 0.5) * a.inverse_beta;
-    p.part.loss = off * off;
-    slope = 2.0 * off * a.inverse_beta;
+    z.add(-0.5f);
+    const Two off = z.settled().times(two_of(a.inverse_beta));
+    loss = off.s * off.s;
+    slope = 2.f * off.s * a.inverse_beta.high;
   }
-  slope *= a.beta;
-  p.part.nll = -c.logp / double(c.count);
-  p.part.right = sc > sr ? 1.0 : 0.0;
-  p.part.chosen = a.beta * sc;
-  p.part.rejected = a.beta * sr;
+  slope *= a.beta.high;
+  const float nc = float(c.count), nr = float(r.count);
+  p.part.loss = one(loss);
+  p.part.nll = one(-(c.logp.value() / nc));
+  p.part.right = one(gap.s > 0.f ? 1.f : 0.f);
+  p.part.chosen = rc;
+  p.part.rejected = rr;
   p.part.count = 1;
-  p.chosen = a.average ? slope / double(c.count) : slope;
-  p.rejected = a.average ? -slope / double(r.count) : -slope;
-  if (a.nll_coef != 0.0) p.chosen -= a.nll_coef / double(c.count);
+  p.chosen = a.average ? slope / nc : slope;
+  p.rejected = a.average ? -slope / nr : -slope;
+  if (a.nll_coef != 0.f) p.chosen -= a.nll_coef / nc;
   return p;
 }
+__device__ __forceinline__ float weight_of(int64_t pairs) { return pairs > 0 ? 1.f / float(pairs) : 0.f; }
 __device__ __forceinline__ void write_stats(const PreferenceArgs& a, const Part& s) {
-  const double w = s.count > 0 ? 1.0 / double(s.count) : 0.0;
+  const float n = s.count > 0 ? float(s.count) : 1.f;
+  const auto mean = [&](const Two& v) { return v.settled().over(n).value(); };
+  const float loss = mean(s.loss), nll = mean(s.nll);
   // a likelihood term with a coefficient of 0 is watched only
-  a.stats[0] = float((a.nll_coef != 0.0 ? s.loss + a.nll_coef * s.nll : s.loss) * w);
-  a.stats[1] = float(s.loss * w);
-  a.stats[2] = float(s.nll * w);
-  a.stats[3] = float(s.right * w);
-  a.stats[4] = float(s.chosen * w);
-  a.stats[5] = float(s.rejected * w);
+  a.stats[0] = a.nll_coef != 0.f ? __fmaf_rn(a.nll_coef, nll, loss) : loss;
+  a.stats[1] = loss;
+  a.stats[2] = nll;
+  a.stats[3] = mean(s.right);
+  a.stats[4] = mean(s.chosen);
+  a.stats[5] = mean(s.rejected);
+}
+__device__ __forceinline__ void add_part(Part& s, const Part& o) {
+  s.loss.add(o.loss), s.nll.add(o.nll), s.right.add(o.right), s.chosen.add(o.chosen), s.rejected.add(o.rejected);
+  s.count += o.count;
 }
 __device__ __forceinline__ Part sum_parts(Part s, int lanes) {
   s.loss = sum_over(s.loss, lanes);
@@ -165,7 +230,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     lp_preference_small_kernel(const __grid_constant__ PreferenceArgs a, int team) {
   __shared__ Sums parts[kSmallThreads / 32];
   __shared__ Sums sums[kSmallSequences];
-  __shared__ double slopes[kSmallSequences];
+  __shared__ float slopes[kSmallSequences];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
   const int n = int(a.n_sequences), teams = warps / team, mine = warp / team;
   const int first = int(threadIdx.x) - mine * team * 32, stride = team * 32;
@@ -184,14 +249,18 @@ __global__ void __launch_bounds__(kSmallThreads)
         ++count;
       }
     }
-    const Sums s = {lane_sum<32>(logp.value()), lane_sum<32>(ref.value()), sum_over(count, 32)};
+    Sums s;
+    s.logp = sum_over(logp, 32);
+    s.ref = sum_over(ref, 32);
+    s.count = sum_over(count, 32);
     if (lane == 0) parts[warp] = s;
     __syncthreads();
     if (int(threadIdx.x) < teams && i0 + int(threadIdx.x) < n) {
       Sums whole = parts[threadIdx.x * team];
       for (int k = 1; k < team; ++k) {
         const Sums& p = parts[threadIdx.x * team + k];
-        whole.logp += p.logp, whole.ref += p.ref, whole.count += p.count;
+        whole.logp.add(p.logp), whole.ref.add(p.ref);
+        whole.count += p.count;
       }
       if (LP_CHECK(i0 + int(threadIdx.x) < kSmallSequences, kChkStateIndex)) sums[i0 + threadIdx.x] = whole;
     }
@@ -206,13 +275,13 @@ __global__ void __launch_bounds__(kSmallThreads)
       a.rewards[r] = p.reward[1];
     }
     const Part whole = sum_parts(p.part, 32);
-    const double w = whole.count > 0 ? 1.0 / double(whole.count) : 0.0;
+    const float w = weight_of(whole.count);
     if (2 * lane < n) slopes[c] = p.chosen * w, slopes[r] = p.rejected * w;
     if (lane == 0) write_stats(a, whole);
   }
   __syncthreads();
   for (int i = mine; mine < teams && i < n; i += teams) {
-    const float g = float(slopes[i]);
+    const float g = slopes[i];
     const int end = int(row_of(a, i + 1));
     for (int t = int(row_of(a, i)) + first; t < end; t += stride)
       if (LP_CHECK(t >= 0 && t < a.T, kChkRowIndex))
@@ -326,8 +395,8 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     Sums s;
-    s.logp = lane_sum<32>(x.value());
-    s.ref = a.ref_logp != nullptr ? lane_sum<32>(y.value()) : 0.0;
+    s.logp = sum_over(x, 32);
+    if (a.ref_logp != nullptr) s.ref = sum_over(y, 32);
     s.count = __reduce_add_sync(0xffffffffu, count);
     const int64_t at = slot_of(chunk, i);
     if (lane == 0 && LP_CHECK(at >= 0 && at < n_slots, kChkStateIndex)) slots[at] = s;
@@ -337,7 +406,7 @@ __global__ void __launch_bounds__(kThreads)
 // `lanes` lanes a pair (a power of two).
 __global__ void __launch_bounds__(kPairThreads)
     lp_preference_pairs_kernel(const __grid_constant__ PreferenceArgs a, const Sums* slots, int64_t n_slots,
-                               int lanes, double* slopes, Part* parts) {
+                               int lanes, float* slopes, Part* parts) {
   __shared__ Part of_warp[kPairThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int sub = int(threadIdx.x) % lanes;
@@ -358,11 +427,16 @@ __global__ void __launch_bounds__(kPairThreads)
       for (int64_t c = begin[k] / kChunk + sub; c <= (end[k] - 1) / kChunk; c += lanes) {
         const int64_t at = slot_of(c, both[k]);
         if (!LP_CHECK(at >= 0 && at < n_slots, kChkStateIndex)) break;
-        s.logp += __ldcg(&slots[at].logp);
-        s.ref += __ldcg(&slots[at].ref);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(slots + at));
+        Two logp, ref;
+        logp.s = v.x, logp.e = v.y, ref.s = v.z, ref.e = v.w;
+        s.logp.add(logp);
+        s.ref.add(ref);
         s.count += __ldcg(reinterpret_cast<const long long*>(&slots[at].count));
       }
-    sums[k] = {sum_over(s.logp, lanes), sum_over(s.ref, lanes), sum_over(s.count, lanes)};
+    sums[k].logp = sum_over(s.logp, lanes);
+    sums[k].ref = sum_over(s.ref, lanes);
+    sums[k].count = sum_over(s.count, lanes);
   }
   Pair p{};
   if (there && sub == 0) {
@@ -381,15 +455,13 @@ __global__ void __launch_bounds__(kPairThreads)
   Part whole = of_warp[0];
 #pragma unroll
   for (int k = 1; k < kPairThreads / 32; ++k) {
-    const Part& o = of_warp[k];
-    whole.loss += o.loss, whole.nll += o.nll, whole.right += o.right, whole.chosen += o.chosen;
-    whole.rejected += o.rejected, whole.count += o.count;
+    add_part(whole, of_warp[k]);
   }
   parts[blockIdx.x] = whole;
 }
 
 __global__ void __launch_bounds__(kThreads)
-    lp_preference_rows_kernel(const __grid_constant__ PreferenceArgs a, const double* slopes, const Part* parts,
+    lp_preference_rows_kernel(const __grid_constant__ PreferenceArgs a, const float* slopes, const Part* parts,
                               int64_t n_parts) {
   __shared__ int64_t counts[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -409,21 +481,17 @@ __global__ void __launch_bounds__(kThreads)
   for (int k = 0; k < kWarps; ++k) count += counts[k];
   if (blockIdx.x == 0 && warp == 0) {
     Part s{};
-    for (int64_t i = lane; i < n_parts; i += 32) {
-      s.loss += __ldcg(&parts[i].loss), s.nll += __ldcg(&parts[i].nll);
-      s.right += __ldcg(&parts[i].right), s.chosen += __ldcg(&parts[i].chosen);
-      s.rejected += __ldcg(&parts[i].rejected);
-    }
+    for (int64_t i = lane; i < n_parts; i += 32) add_part(s, parts[i]);
     s = sum_parts(s, 32);
     s.count = count;
     if (lane == 0) write_stats(a, s);
   }
   if (t0 >= a.T) return;
-  const double w = count > 0 ? 1.0 / double(count) : 0.0;
+  const float w = weight_of(count);
   float g[kGroups][4] = {};  // rows in no sequence have none
   for_sequences(a, t0, t1, [&](int64_t i, int lo, int hi) {
     if (!LP_CHECK(i >= 0 && i < a.n_sequences, kChkStateIndex)) return;
-    const float slope = float(__ldcg(slopes + i) * w);
+    const float slope = __ldcg(slopes + i) * w;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
       if (128 * (k + 1) <= lo || 128 * k >= hi) continue;  // the same for the warp
@@ -466,7 +534,7 @@ Layout layout_of(int64_t T, int64_t n) {
   l.parts = (n / 2 * l.lanes + kPairThreads - 1) / kPairThreads;
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   l.slopes_at = up(size_t(l.slots) * sizeof(Sums));
-  l.parts_at = l.slopes_at + up(size_t(n) * sizeof(double));
+  l.parts_at = l.slopes_at + up(size_t(n) * sizeof(float));
   l.bytes = l.parts_at + up(size_t(l.parts) * sizeof(Part));
   return l;
 }
@@ -507,7 +575,7 @@ lp_status launch_preference_loss(const PreferenceArgs& args, cudaStream_t stream
   const Layout l = layout_of(a.T, a.n_sequences);
   char* ws = static_cast<char*>(a.workspace);
   Sums* slots = reinterpret_cast<Sums*>(ws);
-  double* slopes = reinterpret_cast<double*>(ws + l.slopes_at);
+  float* slopes = reinterpret_cast<float*>(ws + l.slopes_at);
   Part* parts = reinterpret_cast<Part*>(ws + l.parts_at);
   const int64_t blocks = std::max<int64_t>(1, (l.chunks + kWarps - 1) / kWarps);
   lp_preference_sums_kernel<<<unsigned(blocks), kThreads, 0, stream>>>(a, slots, l.slots);
@@ -517,7 +585,7 @@ lp_status launch_preference_loss(const PreferenceArgs& args, cudaStream_t stream
                         static_cast<const Sums*>(slots), l.slots, l.lanes, slopes, parts))
     return LP_ERR_CUDA;
   if (!launch_dependent(lp_preference_rows_kernel, blocks, kThreads, stream, a,
-                        static_cast<const double*>(slopes), static_cast<const Part*>(parts), l.parts))
+                        static_cast<const float*>(slopes), static_cast<const Part*>(parts), l.parts))
     return LP_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
 }

@@ -4,6 +4,7 @@
 // and enqueues nothing before all checks pass.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -165,8 +166,10 @@ lp_status lp_preference_loss(const float* logp, const float* ref_logp, const uin
     return LP_ERR_INVALID_ARGUMENT;
   if (kind != LP_PREFERENCE_SIGMOID && kind != LP_PREFERENCE_HINGE && kind != LP_PREFERENCE_SQUARE)
     return LP_ERR_INVALID_ARGUMENT;
-  if (!(beta > 0.0) || !std::isfinite(beta) || !std::isfinite(1.0 / beta) ||
-      !std::isfinite(margin) || !std::isfinite(nll_coef) ||
+  // what the kernels take as float32 has to be one; beta and its reciprocal normal ones
+  const auto fits = [](double v) { return std::isfinite(static_cast<float>(v)); };
+  if (!(static_cast<float>(beta) >= FLT_MIN) || !(static_cast<float>(1.0 / beta) >= FLT_MIN) ||
+      !fits(beta) || !fits(1.0 / beta) || !fits(margin) || !fits(nll_coef) ||
       !(label_smoothing >= 0.0 && label_smoothing <= 1.0) ||
       (label_smoothing != 0.0 && kind != LP_PREFERENCE_SIGMOID))
     return LP_ERR_INVALID_ARGUMENT;
@@ -202,11 +205,11 @@ lp_status lp_preference_loss(const float* logp, const float* ref_logp, const uin
   a.kind = kind;
   a.average = average != 0;
   a.halves = halves != 0;
-  a.beta = beta;
-  a.inverse_beta = 1.0 / beta;
-  a.margin = margin;
-  a.smoothing = label_smoothing;
-  a.nll_coef = nll_coef;
+  a.beta = pair32(beta);
+  a.inverse_beta = pair32(1.0 / beta);
+  a.margin = pair32(margin);
+  a.smoothing = static_cast<float>(label_smoothing);
+  a.nll_coef = static_cast<float>(nll_coef);
   a.stats = stats;
   a.rewards = rewards;
   a.grad_logp = grad_logp;

@@ -39,6 +39,17 @@ lp_status launch_layer_norm_backward(const Device& dev, const LayerNormGradArgs&
 
 // -------------------------------------------------------------- preference loss
 
+// A float64 as the sum of two float32.
+struct Pair32 {
+  float high, low;
+};
+inline Pair32 pair32(double v) {
+  Pair32 p;
+  p.high = static_cast<float>(v);
+  p.low = static_cast<float>(v - static_cast<double>(p.high));
+  return p;
+}
+
 struct PreferenceArgs {
   const float *logp, *ref_logp;  // ref_logp may be null
   const uint8_t* mask;           // may be null
@@ -47,7 +58,8 @@ struct PreferenceArgs {
   int kind;                      // lp_preference
   bool average, halves;
   bool wide;                     // set by the launcher: rows may go 16 bytes at a time
-  double beta, inverse_beta, margin, smoothing, nll_coef;
+  Pair32 beta, inverse_beta, margin;
+  float smoothing, nll_coef;
   float *stats, *rewards, *grad_logp;
   void* workspace;
 };
