@@ -29,7 +29,7 @@ constexpr int64_t kSmallRows = 8192;
 constexpr int kSmallSequences = 64;  // a lane of one warp for each pair
 
 // ---- three launches
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = 4;                // of 4 rows, a lane
 constexpr int kChunk = kGroups * 4 * 32;  // rows of a warp
@@ -86,15 +86,9 @@ __device__ __forceinline__ Two two_of(const Pair32& v) {
   t.s = v.high, t.e = v.low;
   return t;
 }
+// Sums over `lanes` lanes, the first lane's to use: the others add in another order.
 __device__ __forceinline__ Two sum_over(Two v, int lanes) {
-  for (int o = lanes / 2; o > 0; o /= 2) {
-    // the same on both sides: the lower lane's first
-    const Two other = v.from_lane(o);
-    const bool upper = (threadIdx.x & o) != 0;
-    Two a = upper ? other : v;
-    a.add(upper ? v : other);
-    v = a;
-  }
+  for (int o = lanes / 2; o > 0; o /= 2) v.add(v.from_lane(o));
   return v;
 }
 __device__ __forceinline__ int64_t sum_over(int64_t v, int lanes) {
@@ -333,33 +327,45 @@ __device__ __forceinline__ unsigned load_mask4(const uint8_t* mask, int64_t t, i
   return kept;
 }
 
-// Calls f(i, lo, hi) for every sequence i that has rows [lo, hi) in [t0, t1), in order; all of a warp
-// together.
-template <class F>
-__device__ __forceinline__ void for_sequences(const PreferenceArgs& a, int64_t t0, int64_t t1, F&& f) {
-  const int lane = threadIdx.x & 31;
-  int64_t i = warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, t0);
-  while (i < a.n_sequences) {
-    // 32 sequences' offsets at once
-    const int64_t mine = i + lane;
-    int64_t begin = a.T, end = a.T;
-    if (mine < a.n_sequences) begin = row_of(a, mine), end = row_of(a, mine + 1);
-    const int lo = int(max(begin, t0) - t0), hi = int(min(end, t1) - t0);
-    unsigned some = __ballot_sync(0xffffffffu, mine < a.n_sequences && begin < t1 && lo < hi);
-    const bool more = __all_sync(0xffffffffu, mine < a.n_sequences && end < t1);
-    for (; some != 0; some &= some - 1) {
-      const int k = __ffs(some) - 1;
-      f(i + k, __shfl_sync(0xffffffffu, lo, k), __shfl_sync(0xffffffffu, hi, k));
-    }
-    if (!more) return;
-    i += 32;
+// The sequences that have rows in [t0, t1), in order, 32 at a time; all of a warp together.
+struct Cursor {
+  int64_t first;  // sequence of lane 0
+  int lo, hi;     // the lane's sequence's rows, counted from t0
+  unsigned some;  // the lanes whose sequence has any
+  bool more;      // whether the next 32 may have some
+  __device__ __forceinline__ Cursor(const PreferenceArgs& a, int64_t t0, int64_t t1)
+      : first(warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, t0)) {
+    look(a, t0, t1);
   }
-}
+  __device__ __forceinline__ void look(const PreferenceArgs& a, int64_t t0, int64_t t1) {
+    const int64_t mine = first + (threadIdx.x & 31);
+    const bool there = mine < a.n_sequences;
+    int64_t begin = a.T, end = a.T;
+    if (there) begin = row_of(a, mine), end = row_of(a, mine + 1);
+    lo = int(max(begin, t0) - t0);
+    hi = int(min(end, t1) - t0);
+    some = __ballot_sync(0xffffffffu, there && begin < t1 && lo < hi);
+    more = __all_sync(0xffffffffu, there && end < t1);
+  }
+  // f(i, lo, hi) for every sequence i, with its rows
+  template <class F>
+  __device__ __forceinline__ void each(const PreferenceArgs& a, int64_t t0, int64_t t1, F&& f) {
+    while (true) {
+      for (; some != 0; some &= some - 1) {
+        const int k = __ffs(some) - 1;
+        f(first + k, __shfl_sync(0xffffffffu, lo, k), __shfl_sync(0xffffffffu, hi, k));
+      }
+      if (!more) return;
+      first += 32;
+      look(a, t0, t1);
+    }
+  }
+};
 
 // The place of a sequence's sums over a chunk: both go up along the rows, so no two meet.
 __device__ __forceinline__ int64_t slot_of(int64_t chunk, int64_t sequence) { return chunk + sequence; }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     lp_preference_sums_kernel(const __grid_constant__ PreferenceArgs a, Sums* slots, int64_t n_slots) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -376,7 +382,8 @@ __global__ void __launch_bounds__(kThreads)
     if (a.ref_logp != nullptr) load4(a.ref_logp, t, a.T, a.wide, ref[k]);
     kept[k] = load_mask4(a.mask, t, a.T, a.wide);
   }
-  for_sequences(a, t0, t1, [&](int64_t i, int lo, int hi) {
+  Cursor cursor(a, t0, t1);
+  cursor.each(a, t0, t1, [&](int64_t i, int lo, int hi) {
     Two x, y;
     int count = 0;
 #pragma unroll
@@ -418,25 +425,47 @@ __global__ void __launch_bounds__(kPairThreads)
   for (int k = 0; k < 2; ++k)
     if (there) begin[k] = row_of(a, both[k]), end[k] = row_of(a, both[k] + 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are done
-  Sums sums[2];
+  Sums sums[2] = {};
+  // both sequences' chunks side by side, two turns at once: the loads are most of the time
+  int64_t at[2], end_at[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    Sums s{};
-    if (begin[k] < end[k])
-#pragma unroll 4
-      for (int64_t c = begin[k] / kChunk + sub; c <= (end[k] - 1) / kChunk; c += lanes) {
-        const int64_t at = slot_of(c, both[k]);
-        if (!LP_CHECK(at >= 0 && at < n_slots, kChkStateIndex)) break;
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(slots + at));
-        Two logp, ref;
-        logp.s = v.x, logp.e = v.y, ref.s = v.z, ref.e = v.w;
-        s.logp.add(logp);
-        s.ref.add(ref);
-        s.count += __ldcg(reinterpret_cast<const long long*>(&slots[at].count));
+    const bool some = begin[k] < end[k];
+    at[k] = some ? slot_of(begin[k] / kChunk, both[k]) + sub : 0;
+    end_at[k] = some ? slot_of((end[k] - 1) / kChunk, both[k]) + 1 : 0;
+  }
+  while (at[0] < end_at[0] || at[1] < end_at[1]) {
+    float4 v[2][2];
+    long long count[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int64_t slot = at[k] + q * lanes;
+        v[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        count[k][q] = 0;
+        if (slot >= end_at[k] || !LP_CHECK(slot >= 0 && slot < n_slots, kChkStateIndex)) continue;
+        v[k][q] = __ldcg(reinterpret_cast<const float4*>(slots + slot));
+        count[k][q] = __ldcg(reinterpret_cast<const long long*>(&slots[slot].count));
       }
-    sums[k].logp = sum_over(s.logp, lanes);
-    sums[k].ref = sum_over(s.ref, lanes);
-    sums[k].count = sum_over(s.count, lanes);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        Two logp, ref;
+        logp.s = v[k][q].x, logp.e = v[k][q].y, ref.s = v[k][q].z, ref.e = v[k][q].w;
+        sums[k].logp.add(logp);
+        sums[k].ref.add(ref);
+        sums[k].count += count[k][q];
+      }
+      at[k] += 2 * lanes;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    sums[k].logp = sum_over(sums[k].logp, lanes);
+    sums[k].ref = sum_over(sums[k].ref, lanes);
+    sums[k].count = sum_over(sums[k].count, lanes);
   }
   Pair p{};
   if (there && sub == 0) {
@@ -460,7 +489,7 @@ __global__ void __launch_bounds__(kPairThreads)
   parts[blockIdx.x] = whole;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 12)
     lp_preference_rows_kernel(const __grid_constant__ PreferenceArgs a, const float* slopes, const Part* parts,
                               int64_t n_parts) {
   __shared__ int64_t counts[kWarps];
@@ -469,6 +498,7 @@ __global__ void __launch_bounds__(kThreads)
   unsigned kept[kGroups];
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) kept[k] = load_mask4(a.mask, t0 + 128 * k + 4 * lane, a.T, a.wide);
+  Cursor cursor(a, min(t0, a.T), t1);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pairs are done
   int64_t count = 0;
   for (int64_t i = threadIdx.x; i < n_parts; i += kThreads)
@@ -489,7 +519,7 @@ __global__ void __launch_bounds__(kThreads)
   if (t0 >= a.T) return;
   const float w = weight_of(count);
   float g[kGroups][4] = {};  // rows in no sequence have none
-  for_sequences(a, t0, t1, [&](int64_t i, int lo, int hi) {
+  cursor.each(a, t0, t1, [&](int64_t i, int lo, int hi) {
     if (!LP_CHECK(i >= 0 && i < a.n_sequences, kChkStateIndex)) return;
     const float slope = __ldcg(slopes + i) * w;
 #pragma unroll
@@ -527,10 +557,10 @@ Layout layout_of(int64_t T, int64_t n) {
   Layout l;
   l.chunks = (T + kChunk - 1) / kChunk;
   l.slots = l.chunks + n;
-  // lanes of a pair: about four chunks each of a sequence of the mean length
+  // lanes of a pair: one for each chunk of a sequence of the mean length
   const int64_t pieces = T / (kChunk * std::max<int64_t>(n, 1)) + 1;
   l.lanes = 1;
-  while (l.lanes < 32 && l.lanes * 4 < pieces) l.lanes *= 2;
+  while (l.lanes < 32 && l.lanes < pieces) l.lanes *= 2;
   l.parts = (n / 2 * l.lanes + kPairThreads - 1) / kPairThreads;
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   l.slopes_at = up(size_t(l.slots) * sizeof(Sums));
