@@ -13,14 +13,22 @@ namespace lp {
 namespace {
 
 // With one group a thread a team takes two rows a turn: their waits for the team are one, and the
-// weights are read once.
-template <int G>
-constexpr int kRowsATurn = G == 1 ? 2 : 1;
+// weights are read once (8192 x 4096 bfloat16 47 us, with one row 60).  Where both operands are float32 the
+// rows are long enough to hide the waits, and one row a turn leaves more CTAs theirs: 8192 x 4096 85 us,
+// with two 92.
+template <class R, class A, int G>
+constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) < 8 ? 2 : 1;
+// Groups of a thread: as few as 512 threads allow, but two from 1024 columns on under a stream of the other
+// type (16384 x 2048 float32 under bfloat16 67 us, with one group 75; bfloat16 alone 52 and 47).
+int groups_of(bool residual_bf16, bool act_bf16, int64_t d) {
+  const int64_t one = residual_bf16 != act_bf16 ? 1024 : kMaxTeam * 8;
+  return d <= one ? 1 : d <= kMaxTeam * 16 ? 2 : 4;
+}
 
 template <class R, class A, int G, int kAlign>
 __global__ void __launch_bounds__(kMaxTeam, 2)
     lp_layer_norm_kernel(const __grid_constant__ LayerNormArgs a, const Plan plan) {
-  constexpr int kRows = kRowsATurn<G>;
+  constexpr int kRows = kRowsATurn<R, A, G>;
   __shared__ __align__(16) float slots[2][2][kMaxWarps][padded(kRows)];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.T, a.d, plan.shape);
@@ -154,13 +162,13 @@ lp_status launch_forward(const Device& dev, const LayerNormArgs& a, uint32_t acc
       Plan plan{shape_of(a.d, G, a.T), accesses, 1, 0};
       const int threads = plan.shape.team * plan.shape.teams;
       const int columns = int(sizeof(R)) + (a.branch.p ? int(sizeof(A)) : 0);
-      const int least = stage_bytes_of(threads, G, columns, align != kAligned) * kRowsATurn<G> +
+      const int least = stage_bytes_of(threads, G, columns, align != kAligned) * kRowsATurn<R, A, G> +
                         (align == kAligned ? 0 : threads / 32 * kStretch);
       const int ctas = std::max(1, std::min(1024 / threads, kForwardBytes / least));
       const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
       const int64_t blocks = std::min<int64_t>(all, kSlots * ctas);
       const int smem = plan_ring(&plan, columns, G, align != kAligned, (all + blocks - 1) / blocks,
-                                 kRowsATurn<G>, kForwardBytes / ctas);
+                                 kRowsATurn<R, A, G>, kForwardBytes / ctas);
       kernel<<<unsigned(blocks), threads, smem, stream>>>(a, plan);
       return launched();
     };
@@ -186,10 +194,10 @@ lp_status launch_layer_norm(const Device& dev, const LayerNormArgs& a, cudaStrea
   const Align align = fast                                                            ? kAligned
                       : any_halves(accesses, {kResidual, kBranch, kOut, kNormed}) ? kByElements
                                                                                       : kByWords;
-  // as few groups a thread as its team's 512 threads allow
-  if (a.d <= kMaxTeam * 8) return launch_forward<1>(dev, a, accesses, align, stream);
-  if (a.d <= kMaxTeam * 16) return launch_forward<2>(dev, a, accesses, align, stream);
-  return launch_forward<4>(dev, a, accesses, align, stream);
+  const int groups = groups_of(a.residual_bf16, a.act_bf16, a.d);
+  return groups == 1   ? launch_forward<1>(dev, a, accesses, align, stream)
+         : groups == 2 ? launch_forward<2>(dev, a, accesses, align, stream)
+                       : launch_forward<4>(dev, a, accesses, align, stream);
 }
 
 cudaError_t take_check_word_layer_norm(uint32_t* out) { return take_check_word(out); }

@@ -18,12 +18,13 @@ __host__ __device__ __forceinline__ int64_t pitch_of(int64_t d) { return (d + 7)
 template <class R, class A, int G>
 constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) <= 6 ? 2 : 1;
 
-// With one group a thread a row's x and D stay in registers between the sums and the outputs; with
-// more they are formed again from the ring, whose registers would not hold them beside the sums.
+// With one or two groups a thread a row's x and D stay in registers between the sums and the outputs
+// (4096 x 8192 bfloat16 69 us, formed again 76); with four they are formed again from the ring, since the
+// registers do not hold them beside the sums.
 template <class R, class A, int G, int kRows, int kAlign>
 __global__ void __launch_bounds__(kMaxTeam)
     lp_layer_norm_grad_kernel(const __grid_constant__ LayerNormGradArgs a, const Plan plan) {
-  constexpr bool kHold = G == 1;
+  constexpr bool kHold = G <= 2, kKeep = G == 1;  // the row, the weight
   __shared__ __align__(16) float slots[2][kMaxWarps][padded(kRows * 2)];
   extern __shared__ __align__(32) unsigned char ring[];
   const Place p(a.T, a.d, plan.shape);
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kMaxTeam)
     for (int e = 0; e < 4; ++e) w[e] = both(1.f);
     if (a.weight != nullptr) read_weight(a.weight, a.weight_bf16, k, wide_w, p, w);
   };
-  if (kHold) weight_of(0, kept_w);
+  if (kKeep) weight_of(0, kept_w);
   // the rows' means and roots, loaded a turn ahead
   float root[kRows], mean[kRows];
   const auto load_roots = [&](int64_t first) {
@@ -122,16 +123,16 @@ __global__ void __launch_bounds__(kMaxTeam)
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       Pairs w;
-      if (!kHold) weight_of(k, w);
+      if (!kKeep) weight_of(k, w);
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         Pairs h, x1, D1;
         Pairs& xk = kHold ? x[j][kHold ? k : 0] : x1;
-        form(j, k, kHold ? kept_w : w, xk, kHold ? D[j][kHold ? k : 0] : D1, h);
+        form(j, k, kKeep ? kept_w : w, xk, kHold ? D[j][kHold ? k : 0] : D1, h);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // columns past the row have a gradient of 0
-          const float2 dx = mul(h[e], kHold ? kept_w[e] : w[e]);
+          const float2 dx = mul(h[e], kKeep ? kept_w[e] : w[e]);
           sums[j][0] = add(sums[j][0], dx);
           sums[j][1] = fma(dx, xk[e], sums[j][1]);
           sum_w[k][e] = fma(h[e], xk[e], sum_w[k][e]);
