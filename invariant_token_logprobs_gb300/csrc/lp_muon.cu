@@ -68,9 +68,15 @@ __host__ __device__ __forceinline__ int64_t padded_to(int64_t v, int64_t by) { r
 
 // ------------------------------------------------------------------ momentum, norm, X
 
-__device__ __forceinline__ float grad_at(const MuonRecord& t, int64_t i) {
-  return t.grad_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.grad)[i])
-                     : static_cast<const float*>(t.grad)[i];
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+// f(gradient's pointer of its type)
+template <class F>
+__device__ __forceinline__ void with_grad(const MuonRecord& t, F&& f) {
+  if (t.grad_bf16)
+    f(static_cast<const __nv_bfloat16*>(t.grad));
+  else
+    f(static_cast<const float*>(t.grad));
 }
 // The new momentum and what is orthogonalised.
 __device__ __forceinline__ float momentum_of(const MuonArgs& a, float g, float m) {
@@ -80,18 +86,15 @@ __device__ __forceinline__ float update_of(const MuonArgs& a, float g, float m) 
   return a.nesterov ? __fmaf_rn(a.momentum, m, g) : m;
 }
 
-// Four neighbouring elements of the gradient and the momentum, 16 bytes at a time.
-__device__ __forceinline__ void load_wide(const MuonRecord& t, int64_t i, float* g, float* m) {
-  const float4 v = *reinterpret_cast<const float4*>(t.momentum + i);
-  m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
-  if (t.grad_bf16) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.grad) + i));
-    g[0] = __uint_as_float(w.x << 16), g[1] = __uint_as_float(w.x & 0xffff0000u);
-    g[2] = __uint_as_float(w.y << 16), g[3] = __uint_as_float(w.y & 0xffff0000u);
-  } else {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + i));
-    g[0] = w.x, g[1] = w.y, g[2] = w.z, g[3] = w.w;
-  }
+// Four neighbouring elements of the gradient, and of the momentum, at once.
+__device__ __forceinline__ void load_wide(const __nv_bfloat16* p, float* v) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load_wide(const float* p, float* v) {
+  const float4 w = *reinterpret_cast<const float4*>(p);
+  v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
 }
 // The sum of a value over the CTA's 256 threads, the same bits for all of them.
 __device__ __forceinline__ float sum256(float s, float* slots) {
@@ -119,29 +122,32 @@ __global__ void __launch_bounds__(kNormThreads)
   const int count = int(min(t.part, n - from));
   constexpr int kTurn = 4;  // groups of four elements of a thread at once
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int first_of = 4 * int(threadIdx.x); first_of < count; first_of += kTurn * 4 * kNormThreads) {
-    float g[kTurn][4], m[kTurn][4];
+  with_grad(t, [&](const auto* grad) {
+    for (int first_of = 4 * int(threadIdx.x); first_of < count; first_of += kTurn * 4 * kNormThreads) {
+      float g[kTurn][4], m[kTurn][4];
 #pragma unroll
-    for (int k = 0; k < kTurn; ++k) {
-      const int at = first_of + k * 4 * kNormThreads;
-      if (t.wide && at + 4 <= count) {
-        load_wide(t, from + at, g[k], m[k]);
-        continue;
+      for (int k = 0; k < kTurn; ++k) {
+        const int at = first_of + k * 4 * kNormThreads;
+        if (t.wide && at + 4 <= count) {
+          load_wide(grad + from + at, g[k]);
+          load_wide(t.momentum + from + at, m[k]);
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g[k][j] = at + j < count ? to_float(grad[from + at + j]) : 0.f;
+          m[k][j] = at + j < count ? t.momentum[from + at + j] : 0.f;
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        g[k][j] = at + j < count ? grad_at(t, from + at + j) : 0.f;
-        m[k][j] = at + j < count ? t.momentum[from + at + j] : 0.f;
-      }
+      for (int k = 0; k < kTurn; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = update_of(a, g[k][j], momentum_of(a, g[k][j], m[k][j]));
+          sum[j] = __fmaf_rn(x, x, sum[j]);
+        }
     }
-#pragma unroll
-    for (int k = 0; k < kTurn; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = update_of(a, g[k][j], momentum_of(a, g[k][j], m[k][j]));
-        sum[j] = __fmaf_rn(x, x, sum[j]);
-      }
-  }
+  });
   const float s = sum256((sum[0] + sum[1]) + (sum[2] + sum[3]), slots);
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
 }
@@ -190,22 +196,29 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   };
   const bool wide = !t.tall && t.wide;
   float g[kGroups][8], m[kGroups][8];
+  with_grad(t, [&](const auto* grad) {
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    const int left = left_of(k);
-    const int64_t i = at + k * next;
+    for (int k = 0; k < kGroups; ++k) {
+      const int left = left_of(k);
+      const int64_t i = at + k * next;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[k][j] = m[k][j] = 0.f;
-    if (!LP_CHECK(left == 0 || (i >= 0 && i + (left - 1) * step < t.rows * t.cols), kChkCopyIndex)) continue;
-    if (wide && left == 8) {
-      load_wide(t, i, g[k], m[k]);
-      load_wide(t, i + 4, g[k] + 4, m[k] + 4);
-      continue;
+      for (int j = 0; j < 8; ++j) g[k][j] = m[k][j] = 0.f;
+      if (!LP_CHECK(left == 0 || (i >= 0 && i + (left - 1) * step < t.rows * t.cols), kChkCopyIndex)) continue;
+      if (wide) {
+        if (left == 8)
+#pragma unroll
+          for (int q = 0; q < 8; q += 4) load_wide(grad + i + q, g[k] + q), load_wide(t.momentum + i + q, m[k] + q);
+        else
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) g[k][j] = to_float(grad[i + j]), m[k][j] = t.momentum[i + j];
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) g[k][j] = to_float(grad[i + j * step]), m[k][j] = t.momentum[i + j * step];
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) g[k][j] = grad_at(t, i + j * step), m[k][j] = t.momentum[i + j * step];
-  }
+  });
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are written
   float s = 0.f;
   for (int k = tid; k < int(t.parts); k += kSplitThreads) s += __ldcg(partials + t.first_part + k);
@@ -241,7 +254,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     for (int j = 0; j < 8; ++j)
       if (j < left) t.momentum[i + j * step] = m[k][j];
   }
-  asm volatile("fence.proxy.async.global;" ::: "memory");  // the next launch reads X by bulk copies
 }
 
 // ------------------------------------------------------------------------- products
@@ -530,7 +542,6 @@ __device__ __forceinline__ void write_split(const MuonArgs& a, const MuonRecord&
     *reinterpret_cast<uint4*>(to + in) = hi;
     *reinterpret_cast<uint4*>(to + kHalf + in) = lo;
   }
-  asm volatile("fence.proxy.async.global;" ::: "memory");  // the next launch reads it by bulk copies
 }
 
 // One product over `units` tiles.  from: which X is read; last: P X goes into the parameters instead of
