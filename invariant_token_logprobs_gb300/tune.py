@@ -77,6 +77,10 @@ _SIGNATURES = {
     "lp_preference_loss": (
         _int, [_vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _f64, _f64, _f64, _f64, _vp, _vp,
                _vp, _vp, _sz, _vp]),
+    "lp_muon_plan_size": (_sz, [_tensors, _i64]),
+    "lp_muon_plan": (_int, [_tensors, _i64, _vp, _sz]),
+    "lp_muon_workspace_size": (_sz, [_vp]),
+    "lp_muon_step": (_int, [_vp, _vp, _f64, _f64, _int, _int, _f64, _vp, _sz, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
