@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       tc_commit_local(drain_bar);
       drain_wait(drain_bar, 0);
     }
-    if constexpr (kSplit) {  // the epilogues' meetings
+    if (kSplit && first < n_units) {  // the epilogues' meetings over the cluster's one unit
       __syncwarp();
       cluster_sync();
       cluster_sync();

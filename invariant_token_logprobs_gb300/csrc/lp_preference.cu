@@ -116,9 +116,9 @@ __device__ __forceinline__ int64_t rejected_of(const PreferenceArgs& a, int64_t 
   return a.halves ? i + a.n_sequences / 2 : 2 * i + 1;
 }
 // An offset, whatever it holds, as a row of the call.
-__device__ __forceinline__ int64_t row_of(const PreferenceArgs& a, int64_t i) {
+__device__ __forceinline__ int row_of(const PreferenceArgs& a, int64_t i) {
   if (!LP_CHECK(i >= 0 && i <= a.n_sequences, kChkRowIndex)) return 0;
-  return min(max(__ldg(a.cu_seqlens + i), int64_t(0)), a.T);
+  return int(min(max(__ldg(a.cu_seqlens + i), int64_t(0)), a.T));
 }
 
 struct Pair {
@@ -228,14 +228,15 @@ __global__ void __launch_bounds__(kSmallThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
   const int n = int(a.n_sequences), teams = warps / team, mine = warp / team;
   const int first = int(threadIdx.x) - mine * team * 32, stride = team * 32;
-  const int from = n > 0 ? int(row_of(a, 0)) : 0, to = n > 0 ? int(row_of(a, n)) : 0;
+  const int from = n > 0 ? row_of(a, 0) : 0, to = n > 0 ? row_of(a, n) : 0;
+  int begin = 0, end = 0;  // the team's last sequence's rows
   for (int i0 = 0; i0 < n; i0 += teams) {
     const int i = i0 + mine;
     Two logp, ref;
     int64_t count = 0;
-    if (mine < teams && i < n) {
-      const int end = int(row_of(a, i + 1));
-      for (int t = int(row_of(a, i)) + first; t < end; t += stride) {
+    if (i < n) {
+      begin = row_of(a, i), end = row_of(a, i + 1);
+      for (int t = begin + first; t < end; t += stride) {
         if (!LP_CHECK(t >= 0 && t < a.T, kChkRowIndex)) break;
         if (a.mask != nullptr && a.mask[t] == 0) continue;
         logp.add(a.logp[t]);
@@ -274,10 +275,10 @@ __global__ void __launch_bounds__(kSmallThreads)
     if (lane == 0) write_stats(a, whole);
   }
   __syncthreads();
-  for (int i = mine; mine < teams && i < n; i += teams) {
+  for (int i = mine; i < n; i += teams) {
     const float g = slopes[i];
-    const int end = int(row_of(a, i + 1));
-    for (int t = int(row_of(a, i)) + first; t < end; t += stride)
+    if (n > teams) begin = row_of(a, i), end = row_of(a, i + 1);
+    for (int t = begin + first; t < end; t += stride)
       if (LP_CHECK(t >= 0 && t < a.T, kChkRowIndex))
         a.grad_logp[t] = a.mask == nullptr || a.mask[t] != 0 ? g : 0.f;
   }
@@ -286,19 +287,18 @@ __global__ void __launch_bounds__(kSmallThreads)
 }
 
 // The first of n ascending offsets that is above t, in [0, n], by a whole warp: 32 probes a step.
-__device__ __forceinline__ int64_t warp_upper_bound(const int64_t* offsets, int64_t n, int64_t t) {
-  const int lane = threadIdx.x & 31;
-  int64_t lo = 0, hi = n;  // the answer is in [lo, hi]
+__device__ __forceinline__ int warp_upper_bound(const int64_t* offsets, int n, int t) {
+  const unsigned lane = threadIdx.x & 31;
+  unsigned lo = 0, hi = unsigned(n);  // the answer is in [lo, hi]
   while (lo < hi) {
-    const int64_t stride = (hi - lo + 31) / 32;
-    const int64_t at = lo + lane * stride;
+    const unsigned stride = (hi - lo + 31) / 32, at = lo + lane * stride;
     const bool below = at < hi && __ldg(offsets + at) <= t;
-    const int k = __popc(__ballot_sync(0xffffffffu, below));  // the probes below t come first
-    if (k == 0) return lo;
+    const unsigned k = __popc(__ballot_sync(0xffffffffu, below));  // the probes below t come first
+    if (k == 0) break;
     hi = min(hi, lo + k * stride);
     lo += (k - 1) * stride + 1;
   }
-  return lo;
+  return int(lo);
 }
 
 // Four values of an operand; rows from T on read as zero.
@@ -329,27 +329,27 @@ __device__ __forceinline__ unsigned load_mask4(const uint8_t* mask, int64_t t, i
 
 // The sequences that have rows in [t0, t1), in order, 32 at a time; all of a warp together.
 struct Cursor {
-  int64_t first;  // sequence of lane 0
+  int first;      // sequence of lane 0
   int lo, hi;     // the lane's sequence's rows, counted from t0
   unsigned some;  // the lanes whose sequence has any
   bool more;      // whether the next 32 may have some
-  __device__ __forceinline__ Cursor(const PreferenceArgs& a, int64_t t0, int64_t t1)
-      : first(warp_upper_bound(a.cu_seqlens + 1, a.n_sequences, t0)) {
+  __device__ __forceinline__ Cursor(const PreferenceArgs& a, int t0, int t1)
+      : first(warp_upper_bound(a.cu_seqlens + 1, int(a.n_sequences), t0)) {
     look(a, t0, t1);
   }
-  __device__ __forceinline__ void look(const PreferenceArgs& a, int64_t t0, int64_t t1) {
-    const int64_t mine = first + (threadIdx.x & 31);
-    const bool there = mine < a.n_sequences;
-    int64_t begin = a.T, end = a.T;
-    if (there) begin = row_of(a, mine), end = row_of(a, mine + 1);
-    lo = int(max(begin, t0) - t0);
-    hi = int(min(end, t1) - t0);
+  __device__ __forceinline__ void look(const PreferenceArgs& a, int t0, int t1) {
+    const int lane = threadIdx.x & 31;
+    const bool there = lane < int(a.n_sequences) - first;
+    int begin = t1, end = t1;
+    if (there) begin = row_of(a, first + int64_t(lane)), end = row_of(a, first + int64_t(lane) + 1);
+    lo = max(begin, t0) - t0;
+    hi = min(end, t1) - t0;
     some = __ballot_sync(0xffffffffu, there && begin < t1 && lo < hi);
     more = __all_sync(0xffffffffu, there && end < t1);
   }
   // f(i, lo, hi) for every sequence i, with its rows
   template <class F>
-  __device__ __forceinline__ void each(const PreferenceArgs& a, int64_t t0, int64_t t1, F&& f) {
+  __device__ __forceinline__ void each(const PreferenceArgs& a, int t0, int t1, F&& f) {
     while (true) {
       for (; some != 0; some &= some - 1) {
         const int k = __ffs(some) - 1;
@@ -361,6 +361,11 @@ struct Cursor {
     }
   }
 };
+// The first row of a warp's chunk, T past the last one.
+__device__ __forceinline__ int chunk_begin(const PreferenceArgs& a, int64_t chunk) {
+  return int(min(chunk * kChunk, a.T));
+}
+__device__ __forceinline__ int chunk_end(const PreferenceArgs& a, int t0) { return int(min(int64_t(t0) + kChunk, a.T)); }
 
 // The place of a sequence's sums over a chunk: both go up along the rows, so no two meet.
 __device__ __forceinline__ int64_t slot_of(int64_t chunk, int64_t sequence) { return chunk + sequence; }
@@ -370,30 +375,31 @@ __global__ void __launch_bounds__(kThreads, 8)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t chunk = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
-  const int64_t t0 = chunk * kChunk, t1 = min(t0 + kChunk, a.T);
-  if (t0 >= a.T) return;
+  const int t0 = chunk_begin(a, chunk), t1 = chunk_end(a, t0);
+  if (t0 >= t1) return;
   float logp[kGroups][4], ref[kGroups][4];
   unsigned kept[kGroups];
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) {
-    const int64_t t = t0 + 128 * k + 4 * lane;
+    const int64_t t = t0 + int64_t(128 * k + 4 * lane);
     if (!LP_CHECK(t >= 0, kChkRowIndex)) return;
     load4(a.logp, t, a.T, a.wide, logp[k]);
     if (a.ref_logp != nullptr) load4(a.ref_logp, t, a.T, a.wide, ref[k]);
     kept[k] = load_mask4(a.mask, t, a.T, a.wide);
   }
   Cursor cursor(a, t0, t1);
-  cursor.each(a, t0, t1, [&](int64_t i, int lo, int hi) {
+  cursor.each(a, t0, t1, [&](int i, int lo, int hi) {
     Two x, y;
     int count = 0;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
       if (128 * (k + 1) <= lo || 128 * k >= hi) continue;  // the same for the warp
-      const int r = 128 * k + 4 * lane;
       unsigned in = kept[k];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (r + j < lo || r + j >= hi) in &= ~(1u << j);
+      if (128 * k < lo || 128 * (k + 1) > hi) {  // some of these rows are others'
+        const int from = lo - (128 * k + 4 * lane), to = hi - (128 * k + 4 * lane);
+        if (from > 0) in &= from >= 4 ? 0u : ~0u << from;
+        if (to < 4) in &= to <= 0 ? 0u : (1u << to) - 1u;
+      }
       count += __popc(in);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kPairThreads)
   const int64_t pair = (int64_t(blockIdx.x) * kPairThreads + threadIdx.x) / lanes;
   const bool there = 2 * pair < a.n_sequences;
   const int64_t both[2] = {chosen_of(a, pair), rejected_of(a, pair)};
-  int64_t begin[2] = {0, 0}, end[2] = {0, 0};
+  int begin[2] = {0, 0}, end[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (there) begin[k] = row_of(a, both[k]), end[k] = row_of(a, both[k] + 1);
@@ -494,11 +500,12 @@ __global__ void __launch_bounds__(kThreads, 12)
                               int64_t n_parts) {
   __shared__ int64_t counts[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t t0 = (int64_t(blockIdx.x) * kWarps + warp) * kChunk, t1 = min(t0 + kChunk, a.T);
+  const int t0 = chunk_begin(a, int64_t(blockIdx.x) * kWarps + warp), t1 = chunk_end(a, t0);
   unsigned kept[kGroups];
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) kept[k] = load_mask4(a.mask, t0 + 128 * k + 4 * lane, a.T, a.wide);
-  Cursor cursor(a, min(t0, a.T), t1);
+  for (int k = 0; k < kGroups; ++k)
+    kept[k] = load_mask4(a.mask, t0 + int64_t(128 * k + 4 * lane), a.T, a.wide);
+  Cursor cursor(a, t0, t1);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pairs are done
   int64_t count = 0;
   for (int64_t i = threadIdx.x; i < n_parts; i += kThreads)
@@ -516,24 +523,25 @@ __global__ void __launch_bounds__(kThreads, 12)
     s.count = count;
     if (lane == 0) write_stats(a, s);
   }
-  if (t0 >= a.T) return;
+  if (t0 >= t1) return;
   const float w = weight_of(count);
   float g[kGroups][4] = {};  // rows in no sequence have none
-  cursor.each(a, t0, t1, [&](int64_t i, int lo, int hi) {
+  cursor.each(a, t0, t1, [&](int i, int lo, int hi) {
     if (!LP_CHECK(i >= 0 && i < a.n_sequences, kChkStateIndex)) return;
     const float slope = __ldcg(slopes + i) * w;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
       if (128 * (k + 1) <= lo || 128 * k >= hi) continue;  // the same for the warp
       const int r = 128 * k + 4 * lane;
+      const bool whole = 128 * k >= lo && 128 * (k + 1) <= hi;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (r + j >= lo && r + j < hi) g[k][j] = kept[k] >> j & 1u ? slope : 0.f;
+        if (whole || (r + j >= lo && r + j < hi)) g[k][j] = kept[k] >> j & 1u ? slope : 0.f;
     }
   });
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) {
-    const int64_t t = t0 + 128 * k + 4 * lane;
+    const int64_t t = t0 + int64_t(128 * k + 4 * lane);
     if (!LP_CHECK(t >= 0, kChkRowIndex)) return;
     if (a.wide && t + 4 <= a.T) {
       *reinterpret_cast<float4*>(a.grad_logp + t) = make_float4(g[k][0], g[k][1], g[k][2], g[k][3]);
