@@ -33,7 +33,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = 4;                // of 4 rows, a lane
 constexpr int kChunk = kGroups * 4 * 32;  // rows of a warp
-constexpr int kPairThreads = 64;
+constexpr int kPairThreads = 128;
 
 // s + e is a value to about 48 bits, |e| at most some units in the last place of s.  Once s is no number or
 // infinite, e is nothing.
