@@ -31,7 +31,7 @@ SOURCES = ["lp_api.cu", "lp_logits.cu", "lp_linear.cu", "lp_backward.cu", "lp_tr
            "lp_muon.cu"]
 HEADERS = [os.path.join(ROOT, "include", f) for f in ("lp.h", "lp_train.h", "lp_tune.h")] + [
     os.path.join(CSRC, f) for f in ("lp_device.cuh", "lp_internal.h", "lp_tcgen05.cuh",
-                                    "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh",
+                                    "lp_check.cuh", "lp_train_internal.h", "lp_norm.cuh", "lp_layer_norm.cuh",
                                     "lp_args.h", "lp_tune_internal.h")
 ]
 # the Python calls of train.py and tune.py: host code against torch's headers, no part of liblp

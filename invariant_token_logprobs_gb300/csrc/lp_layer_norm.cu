@@ -6,7 +6,7 @@
 // over threads and come on chip.
 #include <type_traits>
 
-#include "lp_norm.cuh"
+#include "lp_layer_norm.cuh"
 #include "lp_tune_internal.h"
 
 namespace lp {

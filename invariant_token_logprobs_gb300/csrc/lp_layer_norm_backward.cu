@@ -5,7 +5,7 @@
 // fixed order.  lp_norm.cuh says how rows lie over threads and come on chip.
 #include <type_traits>
 
-#include "lp_norm.cuh"
+#include "lp_layer_norm.cuh"
 #include "lp_tune_internal.h"
 
 namespace lp {

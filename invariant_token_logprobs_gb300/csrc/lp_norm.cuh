@@ -111,12 +111,6 @@ __device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
   return as_pair(r);
 }
 
-__device__ __forceinline__ float2 add(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_bits(a)), "l"(as_bits(b)));
-  return as_pair(r);
-}
-
 // How an operand's rows can be reached: by whole groups, by words, or by words that some rows begin
 // in the middle of (bfloat16).  2 bits an operand.
 enum Access : uint32_t { kHalves = 0, kWords = 1, kWide = 2 };

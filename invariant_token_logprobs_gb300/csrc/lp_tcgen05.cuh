@@ -686,10 +686,6 @@ __device__ __forceinline__ void run_pair_pipeline(const CUtensorMap* tmA, const 
 bool encode_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld,
                     int box_rows);
 
-// Memory as `rows` rows of 128 bytes, in boxes of box_rows whole rows, without a swizzle.
-// Returns false if the CUDA driver rejects it.
-bool encode_rows128(CUtensorMap* map, const void* base, int64_t rows, int box_rows);
-
 // 3-D fp32 tensor map over [S, rows, cols] (cols contiguous, row stride ld
 // elements, S matrices split_stride elements apart) with 32 x 32 x 1 boxes and
 // 128-byte swizzle, for bulk stores of output tiles; elements outside the

@@ -3,11 +3,17 @@
 // reaching these functions have already been validated.
 #pragma once
 
+#include <cuda.h>
+
 #include "../../include/lp_tune.h"
 
 #include "lp_train_internal.h"
 
 namespace lp {
+
+// The workspace as `rows` rows of 128 bytes, in boxes of box_rows whole rows, without a swizzle.  Returns
+// false if the CUDA driver rejects it.
+bool encode_rows128(CUtensorMap* map, const void* base, int64_t rows, int box_rows);
 
 // ------------------------------------------------------------------- layer norm
 
