@@ -139,7 +139,8 @@ LP_API size_t lp_preference_loss_workspace_size(int64_t T, int64_t n_sequences);
  *                   (rejected), or with `halves` of i and i + n_sequences / 2.
  *   kind            an lp_preference.
  *   beta > 0, margin, 0 <= label_smoothing <= 1 (0 unless SIGMOID), nll_coef: finite in
- *                   float32, beta and 1 / beta no subnormals; with an nll_coef of 0 the term is in the stats alone, whatever it holds.
+ *                   float32, beta and 1 / beta no subnormals; with an nll_coef of 0 the
+ *                   term is in the stats alone, whatever it holds.
  *   stats           [6] float32: the loss, and the means over the counted pairs of the
  *                   loss without the nll term, of the chosen's -logp, of s_c > s_r, and of
  *                   beta s_c and beta s_r.

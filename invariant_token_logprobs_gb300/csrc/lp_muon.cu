@@ -13,12 +13,24 @@
 // singular directions, five times over.  (tests/test_gpu_muon.py derives what is left.)
 //
 // The pairs lie in memory as the tensor core reads them from shared memory: blocks of 128 x 64
-// with 128-byte swizzled rows, 16 KB of hi and 16 KB of lo side by side, so a tile is fetched by
-// plain bulk copies, and the same block serves as a K-major operand (G) and as an N-major one (P X).
+// with 128-byte swizzled rows, 16 KB of hi and 16 KB of lo side by side, so a tile is fetched as
+// plain rows of 128 bytes, and the same block serves as a K-major operand (G) and as an N-major one
+// (P X).  Of G and P the blocks above the diagonal are never written: they are read where they mirror
+// to, as M- or N-major operands.
 //
 // A CTA takes tiles of 128 x 128 in turn: one warp fetches stages of 64 of K (64 KB), one issues the
-// products, hi x [hi; lo] as one of N = 256, then lo x hi onto its second half; four warps take
-// finished accumulators out of tensor memory, two of which alternate.
+// products, hi x [hi; lo] as one of N = 256, then lo x hi onto its second half, and eight warps, half
+// a row of the tile a thread, take finished chunks of K out of tensor memory, two of which alternate,
+// and add them up in registers.
+//
+// Bound by the tensor cores and their power: 4096 x 4096 takes 2.8 to 3.0 ms a step, of which the
+// three products of each float16 pair cannot do without 2.14 ms at the measured bfloat16 rate; the
+// last of 528 tiles' turns on 152 SMs costs a tenth of it.  The tensor pipe is active for 56 to 58% of
+// the products' time at 2048 x 2048 (442 us a step), where the symmetric products have 136 tiles for
+// 152 SMs; the fetches alone take 2.2 ms at 4096 x 4096, the products alone 2.6 to 2.8.  Small
+// matrices are bound by their 17 dependent launches, 6 to 7 us each: four of 256 x 256 118 us.
+// Pairs of CTAs with tiles of 256 x 128 were no faster, tiles of 256 x 256 had no room in tensor memory
+// for two accumulators of every term; orders of the tiles by groups gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -47,7 +59,9 @@ constexpr uint32_t kBlock = 2 * kHalf;
 // tensor core cuts sums off where an addition would round: over K of 1000 the singular values came
 // out 8e-6 off, five times what float32 products give; in chunks it is what 16 of its steps cut off.
 constexpr int kChunk = 8;
-constexpr int kSplitBlocks = 16;  // K blocks from which on a tile's K is in segments
+// K blocks from which on a tile's K is in segments: 1024 x 1024 takes 183 us with four, 201 with one; 64
+// such matrices, which need no split, 3.7 ms and 3.5.  (The bits are not to depend on the company.)
+constexpr int kSplitBlocks = 16;
 constexpr uint32_t kAccumulator = 2 * kTile;     // tensor-memory columns
 constexpr int kOutThreads = 256;                 // of the epilogue: two a row of the tile
 constexpr int kOutWarps = kOutThreads / 32;

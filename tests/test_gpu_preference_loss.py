@@ -1,13 +1,14 @@
 """The preference loss and its gradient on a GB300 against the fp64 oracle.
 
-Tolerances, with u = 2^-24.  A lane sums up to 16 rows (up to T / 32 in the one-CTA form) as a float
-pair: each two-sum is exact and the low part's own sum is rounded, n u of terms u of the running sum:
-2^-46 n of the magnitudes, n <= 256 here, past the lane everything is float64: 2^-37 of the sums of
-magnitudes S.  A score is rounded once to float32 for rewards: u.  z is beta times that, so its error is
-ez = beta 2^-37 S, far below u |z|.  In the sigmoid kind exp(-|z|) is expf's 2 units and 2 roundings and
-is within 8 u relatively, as are log1p, the reciprocal and the product after it: the slope is within 16 u
-of the terms' sizes and what ez changes (a slope of at most 1/4 of them).  A gradient is a slope times
-factors in float64, rounded once."""
+Tolerances, with u = 2^-24.  A sum is a float pair: each two-sum is exact, its error of at most u S (S: the
+sum of the magnitudes) goes into the low part, and what n of them make, n u S, is rounded at each of n
+additions: n^2 u^2 S at most.  n is the longest chain: a lane's rows (16; with one CTA a sequence's rows over
+its warps' lanes, at most 10 here), the lanes' tree (5), then chunks over a pair's lanes and their tree, or the
+warps of a team (at most 16): n <= 45, 2^11 u^2 = 2^-37.  A score is rounded once to float32 for rewards: u.
+z is beta times that, held as a pair, so its error is ez = beta 2^-37 S, far below u |z|.  In the sigmoid kind exp(-|z|)
+is expf's 2 units and 2 roundings and is within 8 u relatively, as are log1p, the reciprocal and the product
+after it: the slope is within 16 u of the terms' sizes and what ez changes (a slope of at most 1/4 of them).  A gradient is a slope times
+factors held as pairs, rounded once."""
 
 import numpy as np
 import pytest
