@@ -14,7 +14,8 @@ The first four return the selected-token log-probabilities and entropies of
 z = H W^T / tau (lp_linear_logprob_lse) and back-propagate into H and W through
 lp_linear_logprob_backward with the forward's log Z and entropy kept, so the
 backward does not recompute them.  The next two are train.residual_norm and
-train.policy_loss, on either side of them in a training step, and the last two tune's.  This is argument marshalling only: the
+train.policy_loss, on either side of them in a training step, and the last two
+tune.layer_norm and tune.preference_loss.  This is argument marshalling only: the
 computation runs in liblp's kernels, on the current stream; torch casts
 gradients, and scales those that a loss has written by its own.
 
@@ -32,6 +33,9 @@ bfloat16 (the float32 result rounded to nearest even, the same bits as
 rounding it afterwards) and in float32 otherwise.  An output the loss does not
 use contributes nothing (its upstream gradient is passed as absent).  A
 gradient of a gradient is refused: the backward kernels have no derivative.
+A forward and backward pass can be captured in a CUDA graph as torch's own can:
+after a warm-up on a side stream, with no earlier eager graph of the same leaves
+still alive (torch ends the process where one is).
 """
 
 from __future__ import annotations

@@ -119,3 +119,43 @@ def test_a_step_in_a_graph(example):
     for k in eager.master:
         assert torch.equal(eager.master[k], captured.master[k]), k
     assert torch.equal(eager.muon.momentum_buffer, captured.muon.momentum_buffer)
+
+
+def test_the_bindings_in_a_graph(example):
+    """Forward and backward through autograd captured together; replays see the inputs of the time."""
+    batch = example.pairs_of(example.Model(192, 4096, DEV, seed=3), 16, seed=7)
+    model = example.Model(192, 4096, DEV)
+    leaves = {k: v.clone().requires_grad_() for k, v in model.weight.items() if k != "projection"}
+    hidden = batch["hidden"].clone().requires_grad_()
+    leaves["hidden"] = hidden
+
+    def loss_of():
+        h, _ = autograd.layer_norm(hidden, weight=leaves["norm"], bias=leaves["norm_bias"])
+        logp, _ = autograd.linear_logprob(h, leaves["head"], batch["tokens"])
+        loss, stats, rewards = autograd.preference_loss(logp, batch["cu_seqlens"], ref_logp=batch["ref_logp"],
+                                                        mask=batch["mask"], beta=0.1)
+        loss.backward()
+        return stats, rewards
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        loss_of()
+    torch.cuda.current_stream().wait_stream(side)
+    for v in leaves.values():
+        v.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        stats, rewards = loss_of()
+    with torch.no_grad():
+        hidden.copy_(batch["hidden"].flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = {k: v.grad.clone() for k, v in leaves.items()}
+    kept = stats.clone(), rewards.clone()
+    for v in leaves.values():
+        v.grad = None
+    again = loss_of()
+    assert torch.equal(kept[0], again[0]) and torch.equal(kept[1], again[1])
+    for k, v in leaves.items():
+        assert torch.equal(got[k], v.grad), k
