@@ -6,8 +6,7 @@
 // over threads and come on chip.
 //
 // Bound by HBM where rows are whole groups: 16384 x 2048, float32 stream under bfloat16, 67 us (0.89 of the
-// measured copy rate), 8192 x 4096 bfloat16 47 (0.84); without a branch 41 (0.48: one read and one write a
-// row, beside which the two waits for the team are long).  Rows off 8 elements are bound by instructions
+// measured copy rate), 8192 x 4096 bfloat16 47 (0.85), without a branch 29 (0.68).  Rows off 8 elements are bound by instructions
 // (4-byte copies, outputs through shared memory): 16384 x 2047 bfloat16 98 us, 0.40.  One token is bound by
 // the call: 7 us, of which the kernel is 6.
 #include <type_traits>
@@ -19,14 +18,24 @@ namespace lp {
 namespace {
 
 // With one group a thread a team takes two rows a turn: their waits for the team are one, and the
-// weights are read once (8192 x 4096 bfloat16 47 us, with one row 60).  Where both operands are float32 the
+// weights are read once (aligned rows of 8192 x 4096 bfloat16 took 47 us so, with one row 60).  Where both operands are float32 the
 // rows are long enough to hide the waits, and one row a turn leaves more CTAs theirs: 8192 x 4096 85 us,
 // with two 92.
 template <class R, class A, int G>
 constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) < 8 ? 2 : 1;
-// Groups of a thread: as few as 512 threads allow, but two from 1024 columns on under a stream of the other
-// type (16384 x 2048 float32 under bfloat16 67 us, with one group 75; bfloat16 alone 52 and 47).
-int groups_of(bool residual_bf16, bool act_bf16, int64_t d) {
+// Which rows the wide kernel takes where they are aligned: those of few bytes a column, which are bound by
+// instructions and by the waits for the sums, and fit eight warps.  Under a branch a float32 stream's rows gain
+// more from the ring's deeper copies (16384 x 2048 with a bfloat16 branch 67 us, by the wide kernel 71; 8192 x 4096
+// float32 85 and 93).
+bool few_bytes(bool branch, bool residual_bf16, bool act_bf16, int64_t d) {
+  return d % 8 == 0 && d <= 8192 && (!branch || (residual_bf16 && act_bf16));
+}
+// Groups of a thread.  Of the wide kernel's rows two from 257 columns on and four from 4097 (8192 x 4096 bfloat16
+// without a branch takes 29 us with two, 27 with four, but a single row 4.6 and 6.3); rows that are not aligned
+// have as many, and so the same sums.  Otherwise as few as 512 threads allow, but two from 1024 columns on under a
+// stream of the other type (16384 x 2048 float32 under bfloat16 67 us, with one group 75).
+int groups_of(bool branch, bool residual_bf16, bool act_bf16, int64_t d) {
+  if (few_bytes(branch, residual_bf16, act_bf16, d)) return d <= 256 ? 1 : d <= 4096 ? 2 : 4;
   const int64_t one = residual_bf16 != act_bf16 ? 1024 : kMaxTeam * 8;
   return d <= one ? 1 : d <= kMaxTeam * 16 ? 2 : 4;
 }
@@ -153,6 +162,154 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   }
 }
 
+// ---- few bytes a column, aligned
+//
+// A thread has two or four groups of its row, fetched into registers a turn ahead, so that what a row costs beside
+// its columns (sums, addresses) is spread over 16 or 32 of them; a team has a barrier of its own, so that rows wait for
+// themselves alone; and one CTA an SM keeps weight and bias in shared memory, as float32 in the order of the
+// reads.  (Read from L1 by every row, in 16-byte loads 32 bytes apart, they took 12 us of 8192 x 4096's 37.)
+
+template <class T>
+__device__ __forceinline__ void load_group(const T* p, Group<T>& g) {
+  if constexpr (sizeof(T) == 2)
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(g.w[0]), "=r"(g.w[1]), "=r"(g.w[2]), "=r"(g.w[3])
+                 : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(g.w[0]), "=r"(g.w[1]), "=r"(g.w[2]), "=r"(g.w[3]), "=r"(g.w[4]), "=r"(g.w[5]), "=r"(g.w[6]),
+                   "=r"(g.w[7])
+                 : "l"(p));
+}
+template <class T, int G>
+struct Ahead {
+  Group<T> g[G] = {};
+  __device__ __forceinline__ void fetch(const Rows& r, int64_t t, const Place& p) {
+    if (t >= p.rows) return;
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const int c = 8 * (p.i + k * p.team);
+      if (c < p.d && LP_CHECK(p.has(t, c, 8), kChkCopyIndex)) load_group(row_at<const T, kAligned>(r, t, c), g[k]);
+    }
+  }
+};
+
+// A sum over a team of at most eight warps, as team_sum takes it and in its order, with a barrier of the team's own.
+// slots: eight of the team, zeros where it has no warp; written again only after another barrier.
+__device__ __forceinline__ float own_sum(float v, float (*slots)[8], const Place& p) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (p.team == 32) return v;
+  if (p.lane == 0) (*slots)[p.warp - p.first_warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(p.in_cta + 1), "r"(p.team) : "memory");
+  const float4 x = *reinterpret_cast<const float4*>(&(*slots)[0]), y = *reinterpret_cast<const float4*>(&(*slots)[4]);
+  return ((x.x + y.x) + (x.z + y.z)) + ((x.y + y.y) + (x.w + y.w));
+}
+
+// 80 registers a thread, with four groups 128.
+template <int G>
+constexpr int kWideThreads = G <= 2 ? 768 : 512;
+constexpr int kWideTeams = 15;  // named barriers
+
+template <class R, class A, int G, bool kBranch>
+__global__ void __launch_bounds__(kWideThreads<G>, 1)
+    lp_layer_norm_wide_kernel(const __grid_constant__ LayerNormArgs a, const Plan plan) {
+  __shared__ __align__(16) float slots[kWideTeams][2][2][8];
+  extern __shared__ __align__(32) unsigned char ring[];
+  const Place p(a.T, a.d, plan.shape);
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  const int64_t step = int64_t(gridDim.x) * plan.shape.teams;
+  int64_t t = int64_t(blockIdx.x) * plan.shape.teams + p.in_cta;
+  if (!LP_CHECK(a.d <= a.residual.ld && t - p.in_cta < a.T, kChkRowIndex)) return;
+  Ahead<R, G> residual;
+  Ahead<A, kBranch ? G : 1> y;
+  residual.fetch(a.residual, t, p);
+  if constexpr (kBranch) y.fetch(a.branch, t, p);
+  // weight and bias as a thread reads them: the first four columns of each group's weight, the others, the
+  // bias's, so that a warp's accesses are of neighbours
+  float4* const affine = reinterpret_cast<float4*>(ring);
+  const int groups = G * p.team;
+  for (int n = threadIdx.x; n < groups; n += blockDim.x) {
+    Place q = p;
+    q.i = n;
+    Pairs w, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = both(1.f), b[e] = both(0.f);
+    if (a.weight != nullptr) read_weight(a.weight, a.weight_bf16, 0, access_of(plan.accesses, kWeight) == kWide, q, w);
+    if (a.bias != nullptr) read_weight(a.bias, a.weight_bf16, 0, access_of(plan.accesses, kBranchWeight) == kWide, q, b);
+    affine[n] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+    affine[n + groups] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+    affine[n + 2 * groups] = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
+    affine[n + 3 * groups] = make_float4(b[2].x, b[2].y, b[3].x, b[3].y);
+  }
+  if (p.team > 32)
+    for (int n = threadIdx.x; n < int(sizeof(slots) / sizeof(float)); n += blockDim.x) (&slots[0][0][0][0])[n] = 0.f;
+  __syncthreads();
+  const int own = p.team > 32 ? p.in_cta : 0;
+  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+    Pairs v[G];
+    float2 s = both(0.f);
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      unpack(residual.g[k], v[k]);
+      if constexpr (kBranch) {
+        Pairs n;
+        unpack(y.g[k], n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = add(v[k][e], n[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = add(s, v[k][e]);
+    }
+    residual.fetch(a.residual, t + step, p);
+    if constexpr (kBranch) y.fetch(a.branch, t + step, p);
+    const float mean = own_sum(s.x + s.y, &slots[own][turn][0], p) * inv_d;
+    s = both(0.f);
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      if constexpr (kBranch)
+        put<R, kAligned>(a.residual_out, t, k, true, access_of(plan.accesses, kOut), p, nullptr, v[k]);
+      if (8 * (p.i + k * p.team) < p.d)  // columns past the row are no part of its spread
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[k][e] = add(v[k][e], both(-mean));
+          s = fma(v[k][e], v[k][e], s);
+        }
+    }
+    const float root = 1.f / sqrtf(__fmaf_rn(own_sum(s.x + s.y, &slots[own][turn][1], p), inv_d, a.eps));
+    if (p.i == 0 && LP_CHECK(p.has(t), kChkRowIndex)) {
+      if (a.mean != nullptr) a.mean[t] = mean;
+      if (a.rstd != nullptr) a.rstd[t] = root;
+    }
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const float4* at = affine + p.i + k * p.team;
+      const float4 w0 = at[0], w1 = at[groups], b0 = at[2 * groups], b1 = at[3 * groups];
+      const Pairs w = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w}};
+      const Pairs b = {{b0.x, b0.y}, {b0.z, b0.w}, {b1.x, b1.y}, {b1.z, b1.w}};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k][e] = fma(mul(v[k][e], both(root)), w[e], b[e]);
+      put<A, kAligned>(a.normed, t, k, true, access_of(plan.accesses, kNormed), p, nullptr, v[k]);
+    }
+  }
+}
+
+// One CTA an SM, of as many teams as take its rows in the fewest turns.
+template <class R, class A, int G, bool kBranch>
+lp_status launch_wide(const Device& dev, const LayerNormArgs& a, uint32_t accesses, cudaStream_t stream) {
+  static PerContextOnce once;
+  void (*const kernel)(LayerNormArgs, Plan) = lp_layer_norm_wide_kernel<R, A, G, kBranch>;
+  if (!allow_ring(kernel, dev, &once)) return LP_ERR_CUDA;
+  Plan plan{shape_of(a.d, G, a.T), accesses, 0, 0};
+  const int team = plan.shape.team, fit = kWideThreads<G> / team;
+  const int64_t most = team > 32 ? std::min(fit, kWideTeams) : fit, rows = (a.T + kSlots - 1) / kSlots;
+  const int64_t turns = (rows + most - 1) / most;
+  plan.shape.teams = int((rows + turns - 1) / turns);
+  const int64_t all = (a.T + plan.shape.teams - 1) / plan.shape.teams;
+  kernel<<<unsigned(std::min<int64_t>(all, kSlots)), team * plan.shape.teams, G * team * 64, stream>>>(a, plan);
+  return launched();
+}
+
 // The CTAs of an SM have up to 1024 threads between them, each CTA with rows in flight of its own,
 // and this much shared memory for them.
 constexpr int kForwardBytes = 216 << 10;
@@ -186,6 +343,14 @@ lp_status launch_forward(const Device& dev, const LayerNormArgs& a, uint32_t acc
   });
 }
 
+template <int G>
+lp_status launch_few_bytes(const Device& dev, const LayerNormArgs& a, uint32_t accesses, cudaStream_t stream) {
+  if (a.branch.p != nullptr) return launch_wide<__nv_bfloat16, __nv_bfloat16, G, true>(dev, a, accesses, stream);
+  return with_types(a.residual_bf16, a.act_bf16, [&](auto r, auto x) {
+    return launch_wide<decltype(r), decltype(x), G, false>(dev, a, accesses, stream);
+  });
+}
+
 }  // namespace
 
 lp_status launch_layer_norm(const Device& dev, const LayerNormArgs& a, cudaStream_t stream) {
@@ -200,7 +365,11 @@ lp_status launch_layer_norm(const Device& dev, const LayerNormArgs& a, cudaStrea
   const Align align = fast                                                            ? kAligned
                       : any_halves(accesses, {kResidual, kBranch, kOut, kNormed}) ? kByElements
                                                                                       : kByWords;
-  const int groups = groups_of(a.residual_bf16, a.act_bf16, a.d);
+  const int groups = groups_of(a.branch.p != nullptr, a.residual_bf16, a.act_bf16, a.d);
+  if (fast && few_bytes(a.branch.p != nullptr, a.residual_bf16, a.act_bf16, a.d))
+    return groups == 1   ? launch_few_bytes<1>(dev, a, accesses, stream)
+           : groups == 2 ? launch_few_bytes<2>(dev, a, accesses, stream)
+                         : launch_few_bytes<4>(dev, a, accesses, stream);
   return groups == 1   ? launch_forward<1>(dev, a, accesses, align, stream)
          : groups == 2 ? launch_forward<2>(dev, a, accesses, align, stream)
                        : launch_forward<4>(dev, a, accesses, align, stream);

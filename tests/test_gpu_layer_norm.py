@@ -327,3 +327,30 @@ def test_autograd_dtypes_and_second_order():
     g, = torch.autograd.grad(autograd.layer_norm(leaves["residual"])[0].sum(), leaves["residual"], create_graph=True)
     with pytest.raises(RuntimeError, match="gradient of a gradient"):
         g.sum().backward()
+
+
+@pytest.mark.parametrize("branch", [False, True])
+@pytest.mark.parametrize("residual,act", [(BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("T,d", [(3, 8), (700, 248), (5, 512), (333, 520), (2500, 1024), (411, 4096), (401, 5000),
+                                 (200, 8192), (160, 8200)])
+def test_alignment_does_not_show(T, d, residual, act, branch):
+    """Rows of whole groups and the same rows at an odd pitch, one column on: the same bits, whichever kernel."""
+    if not branch and residual != act:
+        return
+    g = torch.Generator(device=DEV).manual_seed(T + d)
+    r = torch.randn(T, d, generator=g, device=DEV).to(residual)
+    y = torch.randn(T, d, generator=g, device=DEV).to(act) if branch else None
+    w, b = torch.randn(2, d, generator=g, device=DEV)
+
+    def odd(t):
+        if t is None:
+            return None
+        wide = torch.zeros(T, d + 3, device=DEV, dtype=t.dtype)
+        wide[:, 1:d + 1] = t
+        return wide[:, 1:d + 1]
+
+    for affine in (dict(weight=w, bias=b), dict(weight=w.to(BF16)), dict(bias=b), dict()):
+        want = tune.layer_norm(r, y, **affine)
+        got = tune.layer_norm(odd(r), odd(y), **{k: torch.cat([v[:1], v])[1:] for k, v in affine.items()})
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
