@@ -18,9 +18,9 @@ namespace lp {
 namespace {
 
 // With one group a thread a team takes two rows a turn: their waits for the team are one, and the
-// weights are read once (aligned rows of 8192 x 4096 bfloat16 took 47 us so, with one row 60).  Where both operands are float32 the
-// rows are long enough to hide the waits, and one row a turn leaves more CTAs theirs: 8192 x 4096 85 us,
-// with two 92.
+// weights are read once (aligned rows of 8192 x 4096 bfloat16 took 47 us so, with one row 60).  Where
+// both operands are float32 the rows are long enough to hide the waits, and one row a turn leaves more
+// CTAs theirs: 8192 x 4096 85 us, with two 92.
 template <class R, class A, int G>
 constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) < 8 ? 2 : 1;
 // Which rows the wide kernel takes where they are aligned: those of few bytes a column, which are bound by

@@ -8,7 +8,7 @@ from invariant_token_logprobs_gb300 import _build_lib
 from test_train_checks import KERNEL, bodies
 
 
-@pytest.mark.parametrize("source,kernels", [("lp_layer_norm.cu", 1), ("lp_layer_norm_backward.cu", 2),
+@pytest.mark.parametrize("source,kernels", [("lp_layer_norm.cu", 2), ("lp_layer_norm_backward.cu", 2),
                                             ("lp_preference.cu", 4), ("lp_muon.cu", 3)])
 def test_every_kernel_tests_its_indexes(source, kernels):
     with open(os.path.join(_build_lib.CSRC, source)) as f:
