@@ -179,6 +179,19 @@ PyObject* preference_loss(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// The momenta that a plan's addresses point into: float32, each matrix's rounded up to whole lines of
+// MUON_ALIGN elements.  `written` has the params, and bfloat16 copies.
+void momenta_of(const at::Tensor& momenta, PyObject* written) {
+  constexpr int64_t kAlign = 64;
+  if (!PyTuple_Check(written)) type_error("expected a tuple of tensors");
+  int64_t elements = 0;
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(written); ++i) {
+    const at::Tensor& t = required(PyTuple_GET_ITEM(written, i), "a tensor of the step");
+    if (t.scalar_type() == at::kFloat) elements += (t.numel() + kAlign - 1) / kAlign * kAlign;
+  }
+  vector(&momenta, elements, "momenta");
+}
+
 // plan_host, plan, momenta, lr, momentum, nesterov, steps, eps, written, grads, streams, captured
 PyObject* muon_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 12, [&] {
@@ -189,6 +202,7 @@ PyObject* muon_step(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const bool nesterov = truth(v[5]);
     const int64_t steps = integer(v[6]);
     const c10::Device device = device_of(plan, {&momenta});
+    momenta_of(momenta, v[8]);
     const c10::cuda::CUDAGuard guard(device);
     const c10::cuda::CUDAStream on = c10::cuda::getCurrentCUDAStream(device.index());
     keep_for_step(on, v[1], {&momenta}, v[8], v[9], v[10], v[11]);

@@ -283,7 +283,7 @@ class Muon:
         _on_one_device(self.params + [c for c in self.copies if c is not None])
         size = sum(-(-p.numel() // MUON_ALIGN) * MUON_ALIGN for p in self.params)
         if state is None:
-            self.momentum_buffer = torch.zeros(size, device=self.params[0].device)
+            self.momentum_buffer = torch.zeros(size, dtype=torch.float32, device=self.params[0].device)
         else:
             flat = state["momentum"]
             if flat.dtype != torch.float32 or flat.shape != (size,) or not flat.is_contiguous():
