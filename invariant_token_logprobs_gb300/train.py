@@ -396,7 +396,7 @@ class AdamW:
             for p, c, g, s, w in zip(self.params, self.copies, grads, lr_scale, weight_decay)])
         elements = int(lib.lp_adamw_state_elements(records, n))
         size = int(lib.lp_adamw_plan_size(records, n))
-        host = torch.empty(max(size, 1), dtype=torch.uint8)
+        host = torch.empty(max(size, 1), dtype=torch.uint8, device="cpu")
         lp._check("lp_adamw_plan", lib.lp_adamw_plan(records, n, host.data_ptr(), size))
         if not _disjoint(written, grads):
             raise ValueError("gradients must not share memory with params, copies or moments")

@@ -352,7 +352,7 @@ class Muon:
             for p, c, g, m, s, w, u in zip(self.params, self.copies, grads, self.momenta(), lr_scale,
                                            weight_decay, self._scales)])
         size = int(lib.lp_muon_plan_size(records, n))
-        host = torch.empty(max(size, 8), dtype=torch.uint8)
+        host = torch.empty(max(size, 8), dtype=torch.uint8, device="cpu")
         lp._check("lp_muon_plan", lib.lp_muon_plan(records, n, host.data_ptr(), size))
         plan = host.to(self.params[0].device)
         home = torch.cuda.current_stream(plan.device).cuda_stream if plan.is_cuda else 0

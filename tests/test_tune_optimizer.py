@@ -4,7 +4,7 @@ device taken out these tests run on CPU tensors, and no step is taken."""
 import pytest
 import torch
 
-from invariant_token_logprobs_gb300 import tune
+from invariant_token_logprobs_gb300 import train, tune
 
 F32, BF16 = torch.float32, torch.bfloat16
 
@@ -35,3 +35,19 @@ def test_momenta_are_float32_under_any_default_dtype(on_cpu, default):
     assert [v.shape for v in views] == [p.shape for p in params] and all(v.dtype == F32 for v in views)
     again = tune.Muon(params, grads, copies=copies, state=opt.state_dict())
     assert again.momentum_buffer is opt.momentum_buffer
+
+
+@pytest.mark.parametrize("optimizer", [tune.Muon, train.AdamW])
+def test_a_plan_is_laid_out_in_host_memory_under_any_default_device(monkeypatch, optimizer):
+    """The library writes the plan on the host, wherever torch makes tensors.  (Tensors of "meta" have no memory: a
+    plan there is refused, where one on a GPU would be written to from the host.)"""
+    for module in (tune, train):
+        monkeypatch.setattr(module, "_on_one_device", lambda tensors: None)
+    params, grads = matrices([(30, 20)]), matrices([(30, 20)])
+    want = optimizer(params, grads)
+    torch.set_default_device("meta")
+    try:
+        opt = optimizer(params, grads, state=want.state_dict())
+    finally:
+        torch.set_default_device(None)
+    assert torch.equal(opt._plan, want._plan)
