@@ -50,4 +50,5 @@ def test_a_plan_is_laid_out_in_host_memory_under_any_default_device(monkeypatch,
         opt = optimizer(params, grads, state=want.state_dict())
     finally:
         torch.set_default_device(None)
-    assert torch.equal(opt._plan, want._plan)
+    assert opt._plan.device.type == "cpu" and opt._plan.shape == want._plan.shape
+    assert torch.equal(opt._plan[:56], want._plan[:56])  # AdamW's record of the tensor (what pads it is not set)
