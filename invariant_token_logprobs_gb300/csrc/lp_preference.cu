@@ -166,9 +166,12 @@ __device__ __forceinline__ Pair pair_of(const PreferenceArgs& a, const Sums& c, 
     const float up = z.s > 0.f ? high + (low + log_part) : log_part;
     const float to_down = z.s > 0.f ? far : near, to_up = z.s > 0.f ? near : far;
     const float rest = 1.f - a.smoothing;
-    loss = rest * down;
-    slope = -rest * to_down;
-    if (a.smoothing != 0.f) {  // an infinite term without a weight is none
+    loss = slope = 0.f;  // an infinite term without a weight is none
+    if (rest != 0.f) {
+      loss = rest * down;
+      slope = -rest * to_down;
+    }
+    if (a.smoothing != 0.f) {
       loss += a.smoothing * up;
       slope += a.smoothing * to_up;
     }

@@ -63,10 +63,14 @@ def preference_loss(logp, cu_seqlens, *, ref_logp=None, mask=None, kind="sigmoid
             w = 1.0 / len(pairs)
             z = beta * (score[c] - score[r]) - margin
             if kind == "sigmoid":
-                loss = (1 - label_smoothing) * _log1pexp(-z)
-                slope = -(1 - label_smoothing) * _sigmoid(-z)
+                loss = slope = 0.0  # a term without a weight is none, however large
+                if label_smoothing != 1:
+                    loss = (1 - label_smoothing) * _log1pexp(-z)
+                    slope = -(1 - label_smoothing) * _sigmoid(-z)
                 if label_smoothing:
                     loss, slope = loss + label_smoothing * _log1pexp(z), slope + label_smoothing * _sigmoid(z)
+                if z != z:
+                    loss = slope = z
             elif kind == "hinge":
                 loss, slope = max(0.0, 1.0 - z) if z == z else z, -1.0 if z < 1 else (0.0 if z == z else z)
             else:

@@ -1,0 +1,44 @@
+"""The preference loss at the ends of its arguments and of its sequences' lengths, on a GB300.
+
+u = 2^-24.  Where a tolerance is named it is derived in the test."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from invariant_token_logprobs_gb300 import tune
+from oracle import tune as ot
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+@pytest.mark.parametrize("scale", [1, 400])  # one CTA, and three launches
+@pytest.mark.parametrize("smoothing", [0.0, 0.1, 1.0])
+@pytest.mark.parametrize("side", [0, 1])
+def test_a_term_without_a_weight_is_none(side, smoothing, scale):
+    """z of both infinities: the term that is infinite counts by its weight, and not at all where that is 0.  Every
+    finite value here is exact: weights of 1 / 2 of two pairs, and a slope of 0 or of a weight.
+
+    The other pair's loss has 20 u of the terms' sizes, which are below 8 (|z| is)."""
+    lengths = [8 * scale, 6 * scale, 5 * scale, 9 * scale]
+    cu = torch.tensor([0, *lengths], device=DEV).cumsum(0)
+    c = host(cu)
+    logp = torch.full((int(c[-1]),), -2.0 ** -12, device=DEV)
+    logp[c[side]] = -math.inf
+    out = tune.preference_loss(logp, cu, beta=0.25, label_smoothing=smoothing)
+    stats, rewards, grad = ot.preference_loss(host(logp), c, beta=0.25, label_smoothing=smoothing)
+    weight = (1 - smoothing, smoothing)[side]
+    assert math.isinf(stats[0]) == (weight != 0)
+    assert float(out.stats[0]) == stats[0] or abs(float(out.stats[0]) - stats[0]) <= 20 * U * 8
+    assert out.rewards[side] == -math.inf and rewards[side] == -math.inf
+    got = host(out.grad_logp).astype(np.float64)
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - grad) <= 16 * U * 0.25)
+    assert np.all(got[:c[1]] == got[0]) and abs(got[0]) == np.float32(0.125 * np.float32(weight))
