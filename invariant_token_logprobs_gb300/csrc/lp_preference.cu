@@ -186,9 +186,9 @@ __device__ __forceinline__ Pair pair_of(const PreferenceArgs& a, const Sums& c, 
     z.add(-0.5f);
     const Two off = z.settled().times(two_of(a.inverse_beta));
     loss = off.s * off.s;
-    slope = 2.f * off.s * a.inverse_beta.high;
+    slope = 2.f * off.s;  // dz is beta times a score's, and off is z over beta
   }
-  slope *= a.beta.high;
+  if (a.kind != LP_PREFERENCE_SQUARE) slope *= a.beta.high;
   const float nc = float(c.count), nr = float(r.count);
   p.part.loss = one(loss);
   p.part.nll = one(-(c.logp.value() / nc));

@@ -42,3 +42,21 @@ def test_a_term_without_a_weight_is_none(side, smoothing, scale):
     got = host(out.grad_logp).astype(np.float64)
     assert np.all(np.isfinite(got)) and np.all(np.abs(got - grad) <= 16 * U * 0.25)
     assert np.all(got[:c[1]] == got[0]) and abs(got[0]) == np.float32(0.125 * np.float32(weight))
+
+
+@pytest.mark.parametrize("scale", [1, 1200])  # one CTA, and three launches
+@pytest.mark.parametrize("beta", [1e-37, 1e-25, 1e-3, 1.0, 1e25, 1e37])
+def test_the_square_kinds_gradient_over_the_range_of_beta(beta, scale):
+    """The loss is (gap - 1 / (2 beta))^2 with margin 0, and its gradient twice the base over the pairs' number, which is
+    finite wherever the base is.  The base is a pair's product, settled (2 u), the rest 2 more; the gap is exact."""
+    lengths = [2 * scale, 3 * scale, 4 * scale, scale]
+    cu = torch.tensor([0, *lengths], device=DEV).cumsum(0)
+    c = host(cu)
+    logp = torch.zeros(int(c[-1]), device=DEV)
+    logp[c[1]], logp[c[2]] = -2.0 ** -40, -3.0
+    out = tune.preference_loss(logp, cu, kind="square", beta=beta)
+    half = 0.5 / beta
+    for i, base in enumerate((2.0 ** -40 - half, -3.0 - half)):
+        for j, sign in ((2 * i, 1.0), (2 * i + 1, -1.0)):
+            got = host(out.grad_logp[c[j]:c[j + 1]]).astype(np.float64)
+            assert np.all(np.abs(got - sign * base) <= 4 * U * abs(base)), (beta, got[0], base)
