@@ -74,10 +74,12 @@ struct Two {
     t.e = __fmaf_rn(s, x.s, -t.s) + __fmaf_rn(s, x.e, e * x.s);
     return t.settled();
   }
-  __device__ __forceinline__ Two over(float n) const {
+  // n as a pair too: from 2^24 on float32 does not hold it
+  __device__ __forceinline__ Two over(int64_t n) const {
+    const float high = float(n), low = float(n - int64_t(high));
     Two t;
-    t.s = s / n;
-    t.e = (__fmaf_rn(-t.s, n, s) + e) / n;
+    t.s = s / high;
+    t.e = (__fmaf_rn(-t.s, high, s) + __fmaf_rn(-t.s, low, e)) / high;
     return t.settled();
   }
   __device__ __forceinline__ Two from_lane(int distance) const {
@@ -135,7 +137,7 @@ struct Pair {
 __device__ __forceinline__ Two score_of(const PreferenceArgs& a, const Sums& s) {
   Two v = s.logp;
   if (a.ref_logp != nullptr) v.add(s.ref.negative());
-  return a.average && s.count > 0 ? v.settled().over(float(s.count)) : v.settled();
+  return a.average && s.count > 0 ? v.settled().over(s.count) : v.settled();
 }
 __device__ __forceinline__ Two one(float x) {
   Two t;
@@ -203,7 +205,7 @@ __device__ __forceinline__ Pair pair_of(const PreferenceArgs& a, const Sums& c, 
 }
 __device__ __forceinline__ float weight_of(int64_t pairs) { return pairs > 0 ? 1.f / float(pairs) : 0.f; }
 __device__ __forceinline__ void write_stats(const PreferenceArgs& a, const Part& s) {
-  const float n = s.count > 0 ? float(s.count) : 1.f;
+  const int64_t n = s.count > 0 ? s.count : 1;
   const auto mean = [&](const Two& v) { return v.settled().over(n).value(); };
   const float loss = mean(s.loss), nll = mean(s.nll);
   // a likelihood term with a coefficient of 0 is watched only

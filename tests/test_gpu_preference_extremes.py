@@ -60,3 +60,20 @@ def test_the_square_kinds_gradient_over_the_range_of_beta(beta, scale):
         for j, sign in ((2 * i, 1.0), (2 * i + 1, -1.0)):
             got = host(out.grad_logp[c[j]:c[j + 1]]).astype(np.float64)
             assert np.all(np.abs(got - sign * base) <= 4 * U * abs(base)), (beta, got[0], base)
+
+
+def test_means_of_more_rows_than_float32_counts():
+    """Sequences of 2^24 + 1 and 2^24 + 3 rows of -1, whose means are -1 both: every sum is of integers that a pair holds,
+    and the quotient's rest is 0, so that z is 0 without an error.  (A divisor in float32 made it -1/8.)"""
+    lengths = [2 ** 24 + 1, 2 ** 24 + 3]
+    cu = torch.tensor([0, *lengths], device=DEV).cumsum(0)
+    logp = torch.full((sum(lengths),), -1.0, device=DEV)
+    beta = 2.0 ** 20
+    out = tune.preference_loss(logp, cu, beta=beta, average=True)
+    stats = out.stats.tolist()
+    assert abs(stats[0] - math.log(2.0)) <= 20 * U
+    assert stats[3:] == [0.0, -beta, -beta] and out.rewards.tolist() == [-beta, -beta]
+    for rows, n, sign in ((out.grad_logp[:lengths[0]], lengths[0], -1.0), (out.grad_logp[lengths[0]:], lengths[1], 1.0)):
+        low, high = torch.aminmax(rows)
+        want = sign * 0.5 * beta / n
+        assert float(low) == float(high) and abs(float(low) - want) <= 16 * U * abs(want)
