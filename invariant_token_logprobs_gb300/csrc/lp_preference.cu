@@ -5,7 +5,8 @@
 // are three launches, each a programmatic dependent of the one before:
 //   sums   a warp takes kChunk neighbouring rows, however they lie in sequences, and writes a sum for
 //          each sequence that it meets: long sequences are split over many warps, short ones share one;
-//   pairs  a few lanes a pair add its sequences' sums and write its loss and both gradients;
+//   pairs  a few lanes a pair, or its warp where it is far longer than the mean, add its sequences' sums and
+//          write its loss and both gradients;
 //   rows   as in the first, a warp takes kChunk rows and writes their gradients.
 // 9 bytes a row in, the mask again and 4 bytes out.  512 pairs of up to 8192 tokens (4.1 M rows) take 27
 // to 29 us, where the bytes need 8: sums 16 us, pairs 9 and rows 15 when each runs alone.  What bounds them
@@ -427,31 +428,15 @@ __global__ void __launch_bounds__(kThreads, 8)
   });
 }
 
-// `lanes` lanes a pair (a power of two).
-__global__ void __launch_bounds__(kPairThreads)
-    lp_preference_pairs_kernel(const __grid_constant__ PreferenceArgs a, const Sums* slots, int64_t n_slots,
-                               int lanes, float* slopes, Part* parts) {
-  __shared__ Part of_warp[kPairThreads / 32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int sub = int(threadIdx.x) % lanes;
-  const int64_t pair = (int64_t(blockIdx.x) * kPairThreads + threadIdx.x) / lanes;
-  const bool there = 2 * pair < a.n_sequences;
-  const int64_t both[2] = {chosen_of(a, pair), rejected_of(a, pair)};
-  int begin[2] = {0, 0}, end[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (there) begin[k] = row_of(a, both[k]), end[k] = row_of(a, both[k] + 1);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are done
-  Sums sums[2] = {};
-  // both sequences' chunks side by side, two turns at once: the loads are most of the time
-  int64_t at[2], end_at[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const bool some = begin[k] < end[k];
-    at[k] = some ? slot_of(begin[k] / kChunk, both[k]) + sub : 0;
-    end_at[k] = some ? slot_of((end[k] - 1) / kChunk, both[k]) + 1 : 0;
-  }
-  while (at[0] < end_at[0] || at[1] < end_at[1]) {
+// Chunks of a lane from which on a pair is its whole warp's: what four turns of fold take.
+constexpr int kFewChunks = 8;
+
+// Adds up, over `lanes` lanes, the chunks of a pair's sequences, in the slots from `at` to `end`, a lane's share of
+// each: both sequences side by side, two turns at once, since the loads are most of the time.
+__device__ __forceinline__ void fold(const Sums* slots, int64_t n_slots, const int64_t (&first)[2],
+                                     const int64_t (&end)[2], int lane, int lanes, Sums (&sums)[2]) {
+  int64_t at[2] = {first[0] + lane, first[1] + lane};
+  while (at[0] < end[0] || at[1] < end[1]) {
     float4 v[2][2];
     long long count[2][2];
 #pragma unroll
@@ -461,7 +446,7 @@ __global__ void __launch_bounds__(kPairThreads)
         const int64_t slot = at[k] + q * lanes;
         v[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
         count[k][q] = 0;
-        if (slot >= end_at[k] || !LP_CHECK(slot >= 0 && slot < n_slots, kChkStateIndex)) continue;
+        if (slot >= end[k] || !LP_CHECK(slot >= 0 && slot < n_slots, kChkStateIndex)) continue;
         v[k][q] = __ldcg(reinterpret_cast<const float4*>(slots + slot));
         count[k][q] = __ldcg(reinterpret_cast<const long long*>(&slots[slot].count));
       }
@@ -478,11 +463,67 @@ __global__ void __launch_bounds__(kPairThreads)
       at[k] += 2 * lanes;
     }
   }
+}
+__device__ __forceinline__ Sums sum_over(const Sums& v, int lanes) {
+  Sums s;
+  s.logp = sum_over(v.logp, lanes);
+  s.ref = sum_over(v.ref, lanes);
+  s.count = sum_over(v.count, lanes);
+  return s;
+}
+__device__ __forceinline__ Two from_first_lane(const Two& v) {
+  Two t;
+  t.s = __shfl_sync(0xffffffffu, v.s, 0);
+  t.e = __shfl_sync(0xffffffffu, v.e, 0);
+  return t;
+}
+
+// `lanes` lanes a pair (a power of two), as many as sequences of the mean length have chunks.  Pairs of sequences far
+// longer than that are left to the whole warp, one after the other: one answer of 131072 among 20000 pairs of up to 100
+// took 112 us by one lane, 41 so, 38 without it; one of 2^20 among 2000 pairs of 16 564 us and 60.
+__global__ void __launch_bounds__(kPairThreads)
+    lp_preference_pairs_kernel(const __grid_constant__ PreferenceArgs a, const Sums* slots, int64_t n_slots,
+                               int lanes, float* slopes, Part* parts) {
+  __shared__ Part of_warp[kPairThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = int(threadIdx.x) & 31, sub = lane % lanes;
+  const int64_t pair = (int64_t(blockIdx.x) * kPairThreads + threadIdx.x) / lanes;
+  const bool there = 2 * pair < a.n_sequences;
+  const int64_t both[2] = {chosen_of(a, pair), rejected_of(a, pair)};
+  int64_t first[2] = {0, 0}, end[2] = {0, 0};  // slots
+  bool is_long = false;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    sums[k].logp = sum_over(sums[k].logp, lanes);
-    sums[k].ref = sum_over(sums[k].ref, lanes);
-    sums[k].count = sum_over(sums[k].count, lanes);
+    if (!there) continue;
+    const int begin_row = row_of(a, both[k]), end_row = row_of(a, both[k] + 1);
+    if (begin_row >= end_row) continue;
+    first[k] = slot_of(begin_row / kChunk, both[k]);
+    end[k] = slot_of((end_row - 1) / kChunk, both[k]) + 1;
+    is_long = is_long || end[k] - first[k] > kFewChunks * lanes;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are done
+  Sums sums[2] = {};
+  is_long = is_long && lanes < 32;
+  if (!is_long) fold(slots, n_slots, first, end, sub, lanes, sums);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) sums[k] = sum_over(sums[k], lanes);
+  for (unsigned left = __ballot_sync(0xffffffffu, is_long && sub == 0); left != 0; left &= left - 1) {
+    const int of = __ffs(left) - 1;
+    int64_t from[2], to[2];
+    Sums whole[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      from[k] = __shfl_sync(0xffffffffu, first[k], of), to[k] = __shfl_sync(0xffffffffu, end[k], of);
+    fold(slots, n_slots, from, to, lane, 32, whole);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      whole[k] = sum_over(whole[k], 32);
+      whole[k].logp = from_first_lane(whole[k].logp);
+      whole[k].ref = from_first_lane(whole[k].ref);
+      if (lane == of) sums[k] = whole[k];
+    }
   }
   Pair p{};
   if (there && sub == 0) {

@@ -77,3 +77,72 @@ def test_means_of_more_rows_than_float32_counts():
         low, high = torch.aminmax(rows)
         want = sign * 0.5 * beta / n
         assert float(low) == float(high) and abs(float(low) - want) <= 16 * U * abs(want)
+
+
+def rows(lengths, seed=0):
+    """logp, offsets and a reference of sequences of these lengths."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    cu = torch.tensor([0, *lengths], device=DEV).cumsum(0)
+    logp = -torch.empty(int(cu[-1]), device=DEV).exponential_(1.0, generator=g)
+    return logp, cu, logp + 0.1 * torch.randn(logp.shape, generator=g, device=DEV)
+
+
+LONG = {"one": [16] * 1001 + [1 << 20] + [16] * 2998, "side by side": [20] * 1002 + [70000, 131072, 5, 90001] + [3] * 1994,
+        "at the end": [40] * 4999 + [300000], "a few chunks": [1] * 3000 + [512 * 8, 512 * 8 + 1, 512 * 9, 7] + [1] * 3000}
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("average", [False, True])
+@pytest.mark.parametrize("lengths", LONG.values(), ids=LONG.keys())
+def test_long_sequences_among_many_short_ones(lengths, average, halves):
+    """The longest chain of additions is a lane's 16 rows and 5 steps of its warp, then 2048 / 32 chunks a lane and 5
+    more: n = 90, so that a sum is within n^2 u^2 < 2^-35 of its terms' size S (each of n two-sums leaves at most n u S in
+    the low part, rounded n times).  A mean divides both.  The stats' sums add no chain that shows: 2 u of the largest reward and
+    what the scores' errors make; a sigmoid's slope is 16 u and a quarter of z's error."""
+    logp, cu, ref = rows(lengths)
+    out = tune.preference_loss(logp, cu, ref_logp=ref, beta=0.05, average=average, halves=halves)
+    stats, rewards, grad = ot.preference_loss(host(logp), host(cu), ref_logp=host(ref), beta=0.05, average=average,
+                                              halves=halves)
+    size = np.abs(host(logp).astype(np.float64)) + np.abs(host(ref).astype(np.float64))
+    run = np.concatenate([[0.0], np.cumsum(size)])
+    S = run[host(cu)[1:]] - run[host(cu)[:-1]]
+    if average:
+        S = S / np.array(lengths)
+    got = [host(t).astype(np.float64) for t in out]
+    each = 0.05 * 2.0 ** -35 * S
+    assert np.all(np.abs(got[1] - rewards) <= 1.01 * U * np.abs(rewards) + each)
+    ez = 2 * each.max()
+    assert np.all(np.abs(got[0][:3] - stats[:3]) <= 20 * U * (np.abs(stats[:3]).max() + 1) + ez)
+    assert abs(got[0][3] - stats[3]) <= U
+    assert np.all(np.abs(got[0][4:] - stats[4:]) <= 2 * U * np.abs(rewards).max() + ez)
+    assert np.all(np.abs(got[2] - grad) <= 16 * U * np.abs(grad) + 0.05 * 0.25 * ez)
+    again = tune.preference_loss(logp, cu, ref_logp=ref, beta=0.05, average=average, halves=halves)
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+def microseconds(call):
+    best = math.inf
+    for _ in range(5):
+        start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        call()
+        start.record()
+        for _ in range(10):
+            call()
+        stop.record()
+        stop.synchronize()
+        best = min(best, start.elapsed_time(stop) * 100)
+    return best
+
+
+def test_a_long_sequence_costs_what_it_costs_alone():
+    """Among many short ones it is no chain of a single lane: the call takes 60 us, the long pair's and the short ones' own
+    66 together, and a lane's chain took 564.  The bound is three times the calls apart."""
+    short, long = [16] * 3998, [16, 1 << 20]
+
+    def time_of(lengths):
+        logp, cu, ref = rows(lengths)
+        return microseconds(lambda: tune.preference_loss(logp, cu, ref_logp=ref))
+
+    apart, together = time_of(short) + time_of(long), time_of(short[:2000] + long + short[2000:])
+    print(f"apart {apart:.1f} us, together {together:.1f} us")
+    assert together <= 3 * apart
