@@ -339,7 +339,8 @@ __device__ __forceinline__ unsigned load_mask4(const uint8_t* mask, int64_t t, i
   return kept;
 }
 
-// The sequences that have rows in [t0, t1), in order, 32 at a time; all of a warp together.
+// The sequences that have rows in [t0, t1), in order, 32 at a time; all of a warp together.  Runs of empty ones are
+// passed by a search (100000 of them between two answers took 1536 us 32 at a time, 19 so).
 struct Cursor {
   int first;      // sequence of lane 0
   int lo, hi;     // the lane's sequence's rows, counted from t0
@@ -363,12 +364,16 @@ struct Cursor {
   template <class F>
   __device__ __forceinline__ void each(const PreferenceArgs& a, int t0, int t1, F&& f) {
     while (true) {
+      // where the rows passed so far end, if all 32 are empty: behind them the next one with rows is searched for
+      const bool none = some == 0;
       for (; some != 0; some &= some - 1) {
         const int k = __ffs(some) - 1;
         f(first + k, __shfl_sync(0xffffffffu, lo, k), __shfl_sync(0xffffffffu, hi, k));
       }
       if (!more) return;
-      first += 32;
+      const int passed = t0 + max(__shfl_sync(0xffffffffu, hi, 31), 0);
+      first += 32;  // whatever the offsets hold, the search goes on
+      if (none) first = max(first, warp_upper_bound(a.cu_seqlens + 1, int(a.n_sequences), passed));
       look(a, t0, t1);
     }
   }
