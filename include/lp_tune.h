@@ -216,8 +216,10 @@ LP_API size_t lp_muon_workspace_size(const void* plan_host);
  *   workspace      256-byte aligned, lp_muon_workspace_size(plan_host) bytes; its
  *                  contents on entry do not matter.
  * lr and momentum are arguments of the launch: a captured call keeps them at every
- * replay.  If a device-side wait gives up, the params that depend on it are NaN and
- * lp_get_device_error on the workspace says so.
+ * replay.  The matrices go through the workspace in batches, in their order, of up to 2^26
+ * elements (each side rounded up to 128) or of one matrix.  If a device-side wait gives up,
+ * the params of its batch are NaN, whichever matrix it was for, those of the other batches
+ * are not, and lp_get_device_error on the workspace says so.
  */
 LP_API lp_status lp_muon_step(const void* plan_host, const void* plan, double lr, double momentum,
                               int nesterov, int steps, double eps, void* workspace,

@@ -74,6 +74,10 @@ constexpr int kSplitThreads = 256;
 
 enum Product { kGram, kPoly, kApply };
 
+// The word of the workspace's header that says, behind the four that are read back, whether a wait of the batch
+// has given up.
+constexpr int kBatchError = 4;
+
 // A record's buffers in the workspace.
 __device__ __forceinline__ int64_t block_at(int64_t row_block, int64_t col_block, int64_t col_blocks) {
   return (row_block * col_blocks + col_block) * int64_t(kBlock);
@@ -127,7 +131,8 @@ __global__ void __launch_bounds__(kNormThreads)
     lp_muon_norm_kernel(const __grid_constant__ MuonArgs a, const MuonUnit* units, float* partials, int first) {
   __shared__ float slots[kNormThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (first && blockIdx.x == 0 && threadIdx.x < 4) a.err[threadIdx.x] = 0u;  // the words that are read back
+  // the words that are read back, of all batches, and the batch's own
+  if (blockIdx.x == 0 && threadIdx.x <= kBatchError && (first || threadIdx.x == kBatchError)) a.err[threadIdx.x] = 0u;
   const MuonUnit u = units[blockIdx.x];
   if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) return;
   const MuonRecord t = a.records[u.tensor];
@@ -485,6 +490,7 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatil
     if (clock64() - t0 > kLimit) {
       *abort_flag = 1;
       atomicOr(err, role);
+      atomicOr(err + kBatchError, role);
       return false;
     }
   }
@@ -729,7 +735,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint8_t* out = smem + kOut;
     int acc = 0;
     uint32_t acc_phase = 0;
-    bool poison = last && *reinterpret_cast<volatile uint32_t*>(a.err) != 0u;
+    bool poison = last && *reinterpret_cast<volatile uint32_t*>(a.err + kBatchError) != 0u;
     for (int n = first; n < n_units; n += step) {
       const MuonUnit u = units[n];
       if (!LP_CHECK(u.tensor >= 0 && u.tensor < a.n_tensors, kChkPlan)) {
