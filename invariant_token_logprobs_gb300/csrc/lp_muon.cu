@@ -7,10 +7,11 @@
 //     X = P X
 // Operands are pairs of float16, x = hi + lo (22 bits), scaled by 2^14, which holds them inside
 // float16's range: after the division by the Frobenius norm no singular value passes 1.21 (the
-// polynomial's largest value on [0, 1]), so no element of X, G or P passes 3.45.  A product is
-// hi hi + hi lo + lo hi with float32 accumulators (lo lo is 2^-22 of it): three tensor-core
-// products where one of float16 would lose what a step multiplies by 3.4 in the small
-// singular directions, five times over.  (tests/test_gpu_muon.py derives what is left.)
+// polynomial's largest value on [0, 1]), so no element of X, G or P passes 3.45.  (Where eps leaves X
+// small, a power of two more keeps its bits; an element below 2^-16 of the norm has fewer than 22, to 2^-39
+// of the norm.)  A product is hi hi + hi lo + lo hi with float32 accumulators (lo lo is 2^-22 of it):
+// three tensor-core products where one of float16 would lose what a step multiplies by 3.4 in the
+// small singular directions, five times over.  (tests/test_gpu_muon.py derives what is left.)
 //
 // The pairs lie in memory as the tensor core reads them from shared memory: blocks of 128 x 64
 // with 128-byte swizzled rows, 16 KB of hi and 16 KB of lo side by side, so a tile is fetched as
@@ -50,6 +51,18 @@ using namespace tc;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScale = 16384.f;           // of the operands
 constexpr float kUnscale = 1.f / kScale;
+// X is held times 2^e besides, which takes its norm |u| / (|u| + eps) to 1/2 and above: an eps far above |u|
+// would leave its elements among float16's subnormals, and five steps multiply what they lose by 485.  No step
+// grows X by more than kA < 2^1.7844, so that e comes down with the steps and X stays below what it has without.
+constexpr int kMaxExponent = 60;
+__device__ __forceinline__ int exponent_of(float norm, float eps) {
+  const float share = norm / (norm + eps);
+  return share > 0.f ? min(max(-1 - ilogbf(share), 0), kMaxExponent) : 0;
+}
+__device__ __forceinline__ int exponent_at(int first, int step) { return max(first - (17844 * step + 9999) / 10000, 0); }
+__device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }  // |e| <= 126
+// From this exponent on b G and c G G are below 2^-28 of a I, and P is a I.
+constexpr int kLinear = 15;
 
 constexpr int kTile = 128;                  // rows and columns of a tile, rows of a block
 constexpr int kBlockK = 64;                 // columns of a block, K of a stage
@@ -243,8 +256,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
   for (int k = tid; k < int(t.parts); k += kSplitThreads) s += __ldcg(partials + t.first_part + k);
   const float norm = sqrtf(sum256(s, slots));
   const bool fine = norm <= 0x1.fffffep127f;
-  if (u.i == 0 && u.j == 0 && tid == 0) a.fine[u.tensor] = fine;
-  const float scale = kScale / (norm + a.eps);
+  const int exponent = fine ? exponent_of(norm, a.eps) : 0;
+  if (u.i == 0 && u.j == 0 && tid == 0) a.levels[u.tensor] = fine ? 1 + exponent : 0;
+  const float scale = kScale * power_of_2(exponent) / (norm + a.eps);
   unsigned char* block = a.workspace + t.x[0] + block_at(u.i, u.j, padded_to(t.n, kTile) / kBlockK);
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) {
@@ -414,13 +428,13 @@ __device__ __forceinline__ void write_tile(const float (&x)[kTile / 2], int r, i
 // lanes along the parameters' rows.  The record's entries are read before the first store, which might be to
 // them as far as the compiler knows, and all loads of a turn are on their way before its first store: with
 // both left to the compiler a tile took 35 us.  slots: 4 KB of the warp's own.
-__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, bool fine, int row, int col,
-                                             int lane, const float (&x)[kTile / 2], float* slots, bool poison) {
+__device__ __forceinline__ void write_params(const MuonArgs& a, const MuonRecord& t, bool fine, float unscale, int row,
+                                             int col, int lane, const float (&x)[kTile / 2], float* slots, bool poison) {
   if (!fine) return;
   const double l = a.lr * double(t.lr_scale);
   const float keep = float(1.0 - l * double(t.weight_decay));
   const float rate = poison ? __int_as_float(0x7fc00000)
-                            : float(l * double(t.update_scale)) * (kUnscale * kUnscale);
+                            : float(l * double(t.update_scale)) * unscale;
   const bool tall = t.tall != 0;
   const int64_t cols = t.cols;
   // X's rows and columns from here on; lanes go along `across`
@@ -506,7 +520,7 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 // in the segments' order, to its own x.
 template <int kProduct>
 __device__ __forceinline__ void write_split(const MuonArgs& a, const MuonRecord& t, const MuonUnit& u,
-                                            const Segments& segments, uint32_t rank, const float (&x)[kTile / 2],
+                                            const Segments& segments, uint32_t rank, float unscale, const float (&x)[kTile / 2],
                                             const float (&y)[kTile / 2], int r, int half, uint8_t* ring, int64_t block) {
   constexpr int kSlice = kTile / 2 / kSplits;
   const int thread = half * kTile + r;
@@ -546,7 +560,7 @@ __device__ __forceinline__ void write_split(const MuonArgs& a, const MuonRecord&
   const int column = half * (kTile / 2) + int(rank) * kSlice, diagonal = (u.i - u.j) * kTile + r - column;
 #pragma unroll
   for (int j = 0; j < kSlice; ++j) {
-    e[j] *= kProduct == kPoly ? kC * kUnscale : kUnscale;
+    e[j] *= unscale;
     if (kProduct == kPoly && j == diagonal) e[j] += kA * kScale;
   }
   unsigned char* to = a.workspace + (kProduct == kGram ? t.g : t.p) + block + half * int64_t(kBlock);
@@ -564,17 +578,18 @@ __device__ __forceinline__ void write_split(const MuonArgs& a, const MuonRecord&
   }
 }
 
-// One product over `units` tiles.  from: which X is read; last: P X goes into the parameters instead of
-// the other X.  map_a, map_b: the workspace as rows of 128 bytes, in boxes of 256 and of 64.  withhold
+// One product over `units` tiles.  iteration: of the steps, the even ones read the first X, the odd ones the other;
+// last: P X goes into the parameters instead of the other X.  map_a, map_b: the workspace as rows of 128 bytes, in boxes of 256 and of 64.  withhold
 // (tests of the bounded waits only): the first copy is announced and not made.
 // kSplit: a cluster of kSplits CTAs a tile, each with a segment of K; they trade sums, so that each writes 16 of
 // each 64 columns.  (The grid has a cluster for every unit.)
 template <int kProduct, bool kSplit>
 __global__ void __launch_bounds__(kProductThreads, 1)
     lp_muon_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                           const __grid_constant__ MuonArgs a, const MuonUnit* units, int n_units, int from,
-                           int last, int withhold) {
+                           const __grid_constant__ MuonArgs a, const MuonUnit* units, int n_units,
+                           int iteration, int last, int withhold) {
   constexpr int kMine = kTile / 2;  // columns of an epilogue thread
+  const int from = iteration & 1;
   uint8_t* smem = pipeline_smem_base();
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOut + kBlock);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -746,12 +761,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int k_blocks = operands_of<kProduct>(t, from).k_blocks;
       const int64_t cols = padded_to(kProduct == kApply ? t.n : t.m, kTile) / kBlockK;
       const int64_t block = block_at(u.i, 2 * int64_t(u.j), cols);
+      // the matrix's exponent here, and what takes the sums to what is written
+      int level = 1;
+      if (kProduct != kGram) level = __ldcg(a.levels + u.tensor);
+      const int exponent = exponent_at(max(level - 1, 0), iteration);
+      const float unscale =
+          kProduct == kGram   ? kUnscale
+          : kProduct == kPoly ? (exponent < kLinear ? kC * kUnscale * power_of_2(-4 * exponent) : 0.f)
+          : last              ? kUnscale * kUnscale * power_of_2(-exponent)
+                              : kUnscale * power_of_2(exponent_at(max(level - 1, 0), iteration + 1) - exponent);
       float x[kMine];  // the chunks' sums, rounded to nearest
       int go = 1;
       if (kProduct == kPoly) {
-        // c (G G + b / c G): what G adds comes in while the first products run, the hi parts of both blocks, then
+        // c (G G + b / c G), of G times 4^e c 16^-e (G G + 4^e b / c G): what G adds comes in while the first products run, the hi parts of both blocks, then
         // the lo parts, through the tile's way out.  (Read from global memory, 16 bytes a lane of 32 rows, it took
         // 4 us of a launch's 13.)
+        const float linear = kB / kC * kScale * power_of_2(2 * min(exponent, kLinear));
 #pragma unroll
         for (int lo = 0; lo < 2; ++lo) {
           if (first_thread) {
@@ -776,8 +801,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
               if (lo == 0) x[8 * q + 2 * i] = f.x, x[8 * q + 2 * i + 1] = f.y;
               else {
-                x[8 * q + 2 * i] = (x[8 * q + 2 * i] + f.x) * (kB / kC * kScale);
-                x[8 * q + 2 * i + 1] = (x[8 * q + 2 * i + 1] + f.y) * (kB / kC * kScale);
+                x[8 * q + 2 * i] = (x[8 * q + 2 * i] + f.x) * linear;
+                x[8 * q + 2 * i + 1] = (x[8 * q + 2 * i + 1] + f.y) * linear;
               }
             }
           }
@@ -820,7 +845,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
       if constexpr (kSplit) {
-        write_split<kProduct>(a, t, u, segments, rank, x, y, r, half, smem, block);
+        write_split<kProduct>(a, t, u, segments, rank, unscale, x, y, r, half, smem, block);
         continue;  // the grid's clusters have a unit each
       }
       // every warp of the CTA goes on, or none does: they meet at the tile's way out
@@ -829,14 +854,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         poison = true;
       }
       if (kProduct == kApply && last) {
-        write_params(a, t, a.fine[u.tensor] != 0, u.i * kTile + group * 32, u.j * kTile + half * kMine, lane, x,
+        write_params(a, t, level != 0, unscale, u.i * kTile + group * 32, u.j * kTile + half * kMine, lane, x,
                      reinterpret_cast<float*>(out) + (warp - 4) * 1024, poison);
         continue;
       }
       const int diagonal = (u.i - u.j) * kTile + r - half * kMine;  // where the row meets it in x
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
-        x[j] *= kProduct == kPoly ? kC * kUnscale : kUnscale;
+        x[j] *= unscale;
         if (kProduct == kPoly && j == diagonal) x[j] += kA * kScale;
       }
       unsigned char* to = a.workspace + (kProduct == kGram ? t.g : kProduct == kPoly ? t.p : t.x[from ^ 1]);
@@ -1044,11 +1069,11 @@ static lp_status launch_products(const Device& dev, const CUtensorMap& map_a, co
       }) != cudaSuccess)
     return LP_ERR_CUDA;
   for (int s = 0; s < steps; ++s) {
-    const int from = s & 1, last = s == steps - 1;
+    const int last = s == steps - 1;
     const auto launch = [&](auto* kernel, int64_t grid, int cluster, const MuonUnit* units, int64_t n, int is_last,
                             int first) {
       return launch_next(kernel, grid, kProductThreads, kSmem, true, cluster, stream, map_a, map_b, a, units, int(n),
-                         from, is_last, first);
+                         s, is_last, first);
     };
     const int withheld = s == 0 && withhold;
     const int64_t few = single_grid(dev.sm_count, b.grams), many = single_grid(dev.sm_count, b.applies);
@@ -1076,7 +1101,7 @@ lp_status launch_muon_step(const Device& dev, const void* plan_host, const void*
   a.records = reinterpret_cast<const MuonRecord*>(device + h.records_at);
   a.n_tensors = h.n_tensors;
   a.err = reinterpret_cast<uint32_t*>(a.workspace);
-  a.fine = reinterpret_cast<int32_t*>(a.workspace + kWorkspaceHeader);
+  a.levels = reinterpret_cast<int32_t*>(a.workspace + kWorkspaceHeader);
   CUtensorMap map_a, map_b;
   const int64_t rows = h.workspace / kRow;
   if (!encode_rows128(&map_a, a.workspace, rows, 256) || !encode_rows128(&map_b, a.workspace, rows, 64))

@@ -106,11 +106,11 @@ struct MuonHeader {
   int64_t batches_at, records_at, parts_at, blocks_at, gram_at, apply_at;
 };
 struct MuonArgs {
-  const MuonRecord* records;  // set by the launcher, as n_tensors, err and fine
+  const MuonRecord* records;  // set by the launcher, as n_tensors, err and levels
   int64_t n_tensors;
   unsigned char* workspace;
   uint32_t* err;
-  int32_t* fine;              // whether a matrix's norm is finite
+  int32_t* levels;            // of a matrix: 0 where its norm is not finite, else 1 + its X's exponent
   double lr;
   float momentum, eps;
   int nesterov;
