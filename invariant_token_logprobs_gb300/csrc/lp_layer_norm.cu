@@ -18,9 +18,9 @@ namespace lp {
 namespace {
 
 // With one group a thread a team takes two rows a turn: their waits for the team are one, and the
-// weights are read once (aligned rows of 8192 x 4096 bfloat16 took 47 us so, with one row 60).  Where
-// both operands are float32 the rows are long enough to hide the waits, and one row a turn leaves more
-// CTAs theirs: 8192 x 4096 85 us, with two 92.
+// weights are read once (16384 x 1024 float32 under bfloat16 takes 36.8 us so, with one row 38.9; rows off 8
+// elements, 16384 x 2047 bfloat16, 102 and 124).  Where both operands are float32 the rows are long enough to
+// hide the waits, and one row a turn leaves more CTAs theirs: 8192 x 4096 85 us, with two 92.
 template <class R, class A, int G>
 constexpr int kRowsATurn = G == 1 && sizeof(R) + sizeof(A) < 8 ? 2 : 1;
 // Which rows the wide kernel takes where they are aligned: those of few bytes a column, which are bound by
@@ -337,9 +337,11 @@ lp_status launch_forward(const Device& dev, const LayerNormArgs& a, uint32_t acc
     };
     static PerContextOnce once[3];
     constexpr Align kLeast = sizeof(R) + sizeof(A) < 8 ? kByElements : kByWords;
-    return align == kAligned   ? launch(lp_layer_norm_kernel<R, A, G, kAligned>, once)
-           : align == kByWords ? launch(lp_layer_norm_kernel<R, A, G, kByWords>, once + 1)
-                               : launch(lp_layer_norm_kernel<R, A, G, kLeast>, once + 2);
+    // aligned rows of bfloat16 of one or two groups are the wide kernel's
+    if constexpr (sizeof(R) + sizeof(A) > 4 || G > 2)
+      if (align == kAligned) return launch(lp_layer_norm_kernel<R, A, G, kAligned>, once);
+    return align == kByWords ? launch(lp_layer_norm_kernel<R, A, G, kByWords>, once + 1)
+                             : launch(lp_layer_norm_kernel<R, A, G, kLeast>, once + 2);
   });
 }
 
