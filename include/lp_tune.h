@@ -115,8 +115,9 @@ LP_API lp_status lp_layer_norm_backward(
  * not count have no gradient whatever they hold (their logp is NaN where the
  * target is padding), and neither do the rows of pairs that do not count.
  *
- * Sums, scores and z are held as pairs of float32, to 48 bits: differences of sums
- * of 10^5 rows keep float32's precision.  The sums are taken in a fixed order.
+ * Sums, scores, means and z are held as pairs of float32, 48 bits less what a sum's chain of
+ * additions loses: 2^-37 of the terms' size for 10^5 rows, 2^-35 for 10^6.  So differences
+ * of such sums keep float32's precision.  The sums are taken in a fixed order.
  * ------------------------------------------------------------------------ */
 
 typedef enum lp_preference {
@@ -168,7 +169,11 @@ LP_API lp_status lp_preference_loss(const float* logp, const float* ref_logp, co
  * which takes the singular values of X towards 1 and leaves its directions.  p and
  * M are float32; a bfloat16 copy of p is written in the same pass when asked.  The
  * products are taken on the tensor cores with operands of 22 bits (pairs of
- * float16) and float32 sums, on the smaller side of the matrix.
+ * float16) and float32 sums, on the smaller side of the matrix.  The 22 bits are those of
+ * elements of X above 2^-16 of its norm; smaller ones keep an absolute 2^-39 of it.  (X is
+ * held by a power of two that an eps above |u| does not take from it.)  The tensor core cuts sums off
+ * where float32 rounds, for 512 of K at a time.  |u| is a float32 sum of squares: elements
+ * below 2^-63 lose theirs, which shows beside an eps of less than 1e-14.
  *
  * A matrix whose |u| is not finite in float32 (a NaN or an infinity, or squares
  * past its range) keeps its p, its copy and its M; the others are not touched by it.

@@ -6,9 +6,9 @@
 // over threads and come on chip.
 //
 // Bound by HBM where rows are whole groups: 16384 x 2048, float32 stream under bfloat16, 67 us (0.89 of the
-// measured copy rate), 8192 x 4096 bfloat16 47 (0.85), without a branch 29 (0.68).  Rows off 8 elements are bound by instructions
-// (4-byte copies, outputs through shared memory): 16384 x 2047 bfloat16 98 us, 0.40.  One token is bound by
-// the call: 7 us, of which the kernel is 4.
+// measured copy rate), 8192 x 4096 bfloat16 47 (0.85), without a branch 29 (0.68).  Rows off 8 elements are
+// bound by instructions (4-byte copies, outputs through shared memory): 16384 x 2047 bfloat16 98 to 102 us, 0.40.
+// One token is bound by the call: 7 us, of which the kernel is 4.
 #include <type_traits>
 
 #include "lp_layer_norm.cuh"

@@ -24,7 +24,7 @@
 // a row of the tile a thread, take finished chunks of K out of tensor memory, two of which alternate,
 // and add them up in registers.
 //
-// Bound by the tensor cores and their power: 4096 x 4096 takes 2.8 to 3.0 ms a step, of which the
+// Bound by the tensor cores and their power: 4096 x 4096 takes 2.8 to 3.1 ms a step, of which the
 // three products of each float16 pair cannot do without 2.14 ms at the measured bfloat16 rate; the
 // last of 528 tiles' turns on 152 SMs costs a tenth of it.  The tensor pipe is active for 56 to 58% of
 // the products' time at 2048 x 2048 (442 us a step), where the symmetric products have 136 tiles for
@@ -70,7 +70,8 @@ constexpr uint32_t kHalf = kTile * kBlockK * 2;  // bytes of a block's hi (or lo
 constexpr uint32_t kBlock = 2 * kHalf;
 // K blocks that are summed in tensor memory before the sum is added to the tile's in registers.  The
 // tensor core cuts sums off where an addition would round: over K of 1000 the singular values came
-// out 8e-6 off, five times what float32 products give; in chunks it is what 16 of its steps cut off.
+// out 8e-6 off, five times what float32 products give; in chunks it is what 32 of its steps cut off.  That is
+// always downwards: where a gradient's rows are of one sign, it adds up to 1e-5 of X (float32 products 2e-6).
 constexpr int kChunk = 8;
 // K blocks from which on a tile's K is in segments: 1024 x 1024 takes 183 us with four, 201 with one; 64
 // such matrices, which need no split, 3.7 ms and 3.5.  (The bits are not to depend on the company.)
@@ -578,9 +579,10 @@ __device__ __forceinline__ void write_split(const MuonArgs& a, const MuonRecord&
   }
 }
 
-// One product over `units` tiles.  iteration: of the steps, the even ones read the first X, the odd ones the other;
-// last: P X goes into the parameters instead of the other X.  map_a, map_b: the workspace as rows of 128 bytes, in boxes of 256 and of 64.  withhold
-// (tests of the bounded waits only): the first copy is announced and not made.
+// One product over `units` tiles.  iteration: of the steps, the even ones read the first X, the odd ones the
+// other; last: P X goes into the parameters instead of the other X.  map_a, map_b: the workspace as rows of 128
+// bytes, in boxes of 256 and of 64.  withhold (tests of the bounded waits only): the first copy is announced and
+// not made.
 // kSplit: a cluster of kSplits CTAs a tile, each with a segment of K; they trade sums, so that each writes 16 of
 // each 64 columns.  (The grid has a cluster for every unit.)
 template <int kProduct, bool kSplit>
@@ -773,9 +775,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       float x[kMine];  // the chunks' sums, rounded to nearest
       int go = 1;
       if (kProduct == kPoly) {
-        // c (G G + b / c G), of G times 4^e c 16^-e (G G + 4^e b / c G): what G adds comes in while the first products run, the hi parts of both blocks, then
-        // the lo parts, through the tile's way out.  (Read from global memory, 16 bytes a lane of 32 rows, it took
-        // 4 us of a launch's 13.)
+        // c (G G + b / c G), and of a G that is held times 4^e c 16^-e (G G + 4^e b / c G): what G adds comes in while
+        // the first products run, the hi parts of both blocks, then the lo parts, through the tile's way out.  (Read
+        // from global memory, 16 bytes a lane of 32 rows, it took 4 us of a launch's 13.)
         const float linear = kB / kC * kScale * power_of_2(2 * min(exponent, kLinear));
 #pragma unroll
         for (int lo = 0; lo < 2; ++lo) {

@@ -247,8 +247,12 @@ class Muon:
     bfloat16), read at every step from the same memory; copies, where given, bfloat16 matrices (or None)
     that receive the updated params.  s is by `scaling` "spectral" sqrt(max(1, rows / cols)), "rms" 0.2
     sqrt(max(rows, cols)), which moves elements as far as AdamW does, or a number.  weight_decay and
-    lr_scale, which multiplies lr, are numbers or one for each matrix.  The products are as exact as
-    float32's.
+    lr_scale, which multiplies lr, are numbers or one for each matrix.  eps is 1e-16 at least.
+
+    The products are of operands of 22 bits, and sums that the tensor core cuts off where float32 rounds:
+    X is within 1e-6 of its norm where an update's signs are mixed, as float32 products leave it, and
+    within 1e-5 where rows are of one sign (float32 products 2e-6).  An element below 2^-16 of the norm keeps
+    an absolute 2^-39 of it.
 
     `state`, as state_dict() gives it, continues from it with its buffer.  set_grads() names other
     gradient tensors.  A step on any stream keeps its tensors' memory until it is done.  A matrix whose
