@@ -9,7 +9,7 @@
 //          write its loss and both gradients;
 //   rows   as in the first, a warp takes kChunk rows and writes their gradients.
 // 9 bytes a row in, the mask again and 4 bytes out.  512 pairs of up to 8192 tokens (4.1 M rows) take 27
-// to 29 us, where the bytes need 8: sums 16 us, pairs 9 and rows 15 when each runs alone.  What bounds them
+// to 29 us, where the bytes need 8: sums 13 to 16 us, pairs 7 to 9 and rows 13 to 15 when each runs alone.  What bounds them
 // is each launch's chain of dependent loads (offsets, rows, the chunk's sums), and in sums the two-sums'
 // instructions (issue slots 51%).  Larger batches come closer: 2048 pairs 80 us, 32 of them bytes.  Up
 // to kSmallRows a call is its launch and the chain of loads and barriers: 4 pairs 6 us.
